@@ -13,17 +13,18 @@ import torch
 
 own = False
 
-OPS = ("logprobs", "logprobs_backward", "distill", "distill_step", "distill_backward",
-       "xent_backward")
+OPS = ("logprobs", "logprobs_backward", "distill", "distill_backward", "xent_backward")
 IGNORE = -100
 
 
-def _case(name, op, rows, cols, dtype="bf16", ld=0, pad=0, top=0, temperature=1.0, entropy=True):
+def _case(name, op, rows, cols, dtype="bf16", ld=0, pad=0, top=0, temperature=1.0, entropy=True,
+          loss=True):
     """ld: distance between row starts (0: cols); pad: trailing columns masked
     to -inf (a vocabulary padded to a round size); top: alternatives or teacher
-    entries per row; entropy: logprobs_backward with the entropy's gradient."""
+    entries per row; entropy: logprobs_backward with the entropy's gradient;
+    loss: a backward pass that also gives the loss of its rows."""
     c = dict(op=op, rows=rows, cols=cols, dtype=dtype, ld=max(ld, cols), pad=pad, top=top,
-             temperature=temperature, entropy=entropy)
+             temperature=temperature, entropy=entropy, loss=loss)
     if name:
         c["name"] = name
     return c
@@ -44,14 +45,16 @@ def listed():
         # supervised log-likelihood training in fp32 on an odd vocabulary
         _case("logprobs_bwd_511_f32", "logprobs_backward", 511, 32001, "f32", entropy=False),
         # a distillation training step: loss and gradient, the logits a view of a padded matrix
-        _case("distill_step_4096", "distill_step", 4096, 50257, ld=50304, top=64, temperature=2.0),
+        _case("distill_step_4096", "distill_backward", 4096, 50257, ld=50304, top=64,
+              temperature=2.0),
         # the same for a small micro-batch in fp32
-        _case("distill_step_96_f32", "distill_step", 96, 32000, "f32", top=20),
+        _case("distill_step_96_f32", "distill_backward", 96, 32000, "f32", top=20),
         # evaluation of the distillation loss alone
         _case("distill_eval_1024", "distill", 1024, 50257, top=32, temperature=2.0),
-        # the backward pass of an autograd step that kept the forward's statistics
-        _case("distill_bwd_1022", "distill_backward", 1022, 65537, top=100, temperature=3.0),
-        # gradient of a cross-entropy training step
+        # the backward pass of an autograd step whose forward pass gave the loss
+        _case("distill_bwd_1022", "distill_backward", 1022, 65537, top=100, temperature=3.0,
+              loss=False),
+        # a cross-entropy training step: loss and gradient
         _case("xent_bwd_4096", "xent_backward", 4096, 50257),
         # a fine-tuning head over a small label set
         _case("xent_bwd_33_f32", "xent_backward", 33, 1000, "f32"),
@@ -74,7 +77,7 @@ def draw(rng):
     top = min(top, (cols - pad) // 2)
     return _case("", op, rows, cols, dtype, ld, pad, top,
                  rng.choice((1.0, 1.5, 2.0, 4.0)) if op.startswith("distill") else 1.0,
-                 rng.random() < 0.5)
+                 rng.random() < 0.5, rng.random() < 0.5)
 
 
 def prepare(case, seed):
@@ -109,17 +112,10 @@ def prepare(case, seed):
     if op == "logprobs_backward":
         st["dlogprob"] = torch.randn(rows, generator=g, device="cuda") / rows
         st["dentropy"] = -0.01 * rand(rows) / rows if case["entropy"] else None
-    if op in ("distill_step", "distill_backward"):
+    if op == "distill_backward":
         st["dloss"] = rand(rows) / rows
     if op == "xent_backward":
         st["dloss"] = (1.0 / (st["token"] != IGNORE).sum().clamp(min=1)).float().reshape(1)
-    if op in ("logprobs_backward", "distill_backward"):  # what the forward call left
-        z = x.float() / case["temperature"]
-        m = z.amax(1, keepdim=True)
-        e = torch.exp(z - m)
-        s = e.sum(1)
-        st["lse"] = m[:, 0] + torch.log(s)
-        st["entropy_value"] = torch.log(s) - (e * (z - m).clamp(min=-1e30)).sum(1) / s
     return st
 
 
@@ -131,21 +127,18 @@ def _own(st):
         r = fr.fr_logprobs(x, st["token"], top=st["top"], ignore_index=IGNORE)
         return {n: r[n] for n in _logprobs_names(st)}
     if op == "logprobs_backward":
-        return {"dlogits": fr.fr_logprobs_backward(
-            x, st["token"], st["lse"], dlogprob=st["dlogprob"], dentropy=st["dentropy"],
-            entropy=st["entropy_value"] if st["entropy"] else None, ignore_index=IGNORE)}
+        return {"dlogits": fr.fr_logprobs_backward(x, st["token"], dlogprob=st["dlogprob"],
+                                                   dentropy=st["dentropy"], ignore_index=IGNORE)}
     if op == "distill":
-        r = fr.fr_distill(x, st["t_index"], st["t_logit"], temperature=st["temperature"])
-        return {"loss": r["loss"], "lse": r["lse"]}
-    if op == "distill_step":
-        r = fr.fr_distill(x, st["t_index"], st["t_logit"], temperature=st["temperature"],
-                          dloss=st["dloss"])
-        return {"loss": r["loss"], "lse": r["lse"], "dlogits": r["dlogits"]}
+        return {"loss": fr.fr_distill(x, st["t_index"], st["t_logit"],
+                                      temperature=st["temperature"])}
     if op == "distill_backward":
-        return {"dlogits": fr.fr_distill_backward(x, st["t_index"], st["t_logit"], st["lse"],
-                                                  st["dloss"], temperature=st["temperature"])}
-    r = fr.fr_xent_backward(x, st["token"], st["dloss"], ignore_index=IGNORE)
-    return {"loss": r["loss"], "dlogits": r["dlogits"]}
+        r = fr.fr_distill_backward(x, st["t_index"], st["t_logit"], st["dloss"],
+                                   temperature=st["temperature"], want_loss=st["loss"])
+    else:
+        r = fr.fr_xent_backward(x, st["token"], st["dloss"], ignore_index=IGNORE,
+                                want_loss=st["loss"])
+    return {n: r[n] for n in (["loss"] if st["loss"] else []) + ["dlogits"]}
 
 
 def _logprobs_names(st):
@@ -168,60 +161,52 @@ def _teacher(st):
     return e / s, torch.where(live, d - torch.log(s), 0.0), st["t_index"].clamp(min=0)
 
 
-def _distill_grad(st, p, q, at):
-    """dloss T (p - q), from probabilities p that it overwrites."""
-    p.scatter_add_(1, at, -q)
-    return (p * (st["dloss"][:, None] * st["temperature"])).to(st["x"].dtype)
-
-
 def run(st):
     if own:
         return _own(st)
     op, dt = st["op"], st["x"].dtype
     x = st["x"].float()
-    if op == "logprobs_backward":
-        g = torch.where(st["token"] == IGNORE, 0.0, st["dlogprob"])[:, None]
-        d = x - st["lse"][:, None]
-        p = torch.exp(d)
-        grad = p * -g
-        if st["entropy"]:
-            grad -= st["dentropy"][:, None] * p * (d + st["entropy_value"][:, None]).clamp(min=-1e30)
-        grad.scatter_add_(1, st["token"].clamp(min=0)[:, None], g)
-        return {"dlogits": grad.to(dt)}
-    if op == "distill_backward":
-        q, _, at = _teacher(st)
-        p = torch.exp(x / st["temperature"] - st["lse"][:, None])
-        return {"dlogits": _distill_grad(st, p, q, at)}
-    z = x / st["temperature"] if op.startswith("distill") else x
-    m, d, e, s = _softmax_parts(z)
-    lse = (m + torch.log(s))[:, 0]
-    if op == "logprobs":
+    m, d, e, s = _softmax_parts(x / st["temperature"] if op.startswith("distill") else x)
+    out = {}
+    if op.startswith("logprobs"):
+        gone = st["token"] == IGNORE
         at = st["token"].clamp(min=0)[:, None]
-        lp = (d.gather(1, at) - torch.log(s))[:, 0]
-        out = {"logprob": torch.where(st["token"] == IGNORE, 0.0, lp),
-               "entropy": (torch.log(s) - (e * d.clamp(min=-1e30)).sum(1, keepdim=True) / s)[:, 0],
-               "lse": lse}
+        entropy = torch.log(s) - (e * d.clamp(min=-1e30)).sum(1, keepdim=True) / s
+    if op == "logprobs":
+        out["logprob"] = torch.where(gone, 0.0, (d.gather(1, at) - torch.log(s))[:, 0])
+        out["entropy"] = entropy[:, 0]
+        out["lse"] = (m + torch.log(s))[:, 0]
         if st["top"]:
             v, i = torch.sort(x, dim=1, descending=True, stable=True)
             out["top_logprob"] = (v[:, :st["top"]] - m) - torch.log(s)
             out["top_index"] = i[:, :st["top"]].contiguous()
-        return out
-    if op.startswith("distill"):
+    elif op == "logprobs_backward":
+        g = torch.where(gone, 0.0, st["dlogprob"])[:, None]
+        p = e / s
+        grad = p * -g
+        if st["entropy"]:
+            logp = d.clamp(min=-1e30) - torch.log(s)
+            grad -= st["dentropy"][:, None] * p * (logp + entropy)
+        grad.scatter_add_(1, at, g)
+        out["dlogits"] = grad.to(dt)
+    elif op.startswith("distill"):
         q, logq, at = _teacher(st)
-        logp = d.gather(1, at) - torch.log(s)
-        loss = st["temperature"] ** 2 * torch.where(q > 0, q * (logq - logp), 0.0).sum(1)
-        out = {"loss": loss, "lse": lse}
-        if op == "distill_step":
-            out["dlogits"] = _distill_grad(st, e / s, q, at)
-        return out
-    t = st["token"]
-    gone = t == IGNORE
-    at = t.clamp(min=0)[:, None]
-    loss = torch.log(s) - d.gather(1, at)
-    grad = e / s
-    grad.scatter_add_(1, at, -torch.ones_like(loss))
-    grad *= torch.where(gone, 0.0, st["dloss"])[:, None]
-    return {"loss": torch.where(gone, 0.0, loss[:, 0]), "dlogits": grad.to(dt)}
+        if op == "distill" or st["loss"]:
+            logp = d.gather(1, at) - torch.log(s)
+            out["loss"] = st["temperature"] ** 2 * torch.where(q > 0, q * (logq - logp), 0.0).sum(1)
+        if op == "distill_backward":
+            p = (e / s).scatter_add_(1, at, -q)
+            out["dlogits"] = (p * (st["dloss"][:, None] * st["temperature"])).to(dt)
+    else:
+        gone = st["token"] == IGNORE
+        at = st["token"].clamp(min=0)[:, None]
+        loss = torch.log(s) - d.gather(1, at)
+        grad = (e / s).scatter_add_(1, at, -torch.ones_like(loss))
+        grad *= torch.where(gone, 0.0, st["dloss"])[:, None]
+        if st["loss"]:
+            out["loss"] = torch.where(gone, 0.0, loss[:, 0])
+        out["dlogits"] = grad.to(dt)
+    return out
 
 
 def exact(case, seed):
@@ -236,8 +221,6 @@ def exact(case, seed):
         r = torch.arange(z.shape[0], device="cuda")
         hit = t != IGNORE
         lse = torch.logsumexp(z, 1)
-        if op in ("logprobs_backward", "distill_backward"):
-            lse = st["lse"][sl].double()
         logp = z - lse[:, None]
         p = logp.exp()
         o = {}
@@ -254,21 +237,23 @@ def exact(case, seed):
             g = (st["dlogprob"][sl].double() * hit)[:, None]
             dx = g * (onehot - p)
             if case["entropy"]:
-                h, ent = st["dentropy"][sl].double(), st["entropy_value"][sl].double()
-                dx -= h[:, None] * (torch.nan_to_num(p * logp, nan=0.0) + p * ent[:, None])
+                plogp = torch.nan_to_num(p * logp, nan=0.0)
+                ent = -plogp.sum(1, keepdim=True)
+                dx -= st["dentropy"][sl].double()[:, None] * (plogp + p * ent)
             o["dlogits"] = dx
         elif op == "xent_backward":
-            o["loss"] = torch.where(hit, -logp[r, t.clamp(min=0)], 0.0)
+            if case["loss"]:
+                o["loss"] = torch.where(hit, -logp[r, t.clamp(min=0)], 0.0)
             p[r[hit], t[hit]] -= 1.0
             o["dlogits"] = p * (st["dloss"].double() * hit)[:, None]
         else:
             live = st["t_index"][sl] >= 0
             q = torch.softmax(torch.where(live, st["t_logit"][sl].double() / temp, -math.inf), 1)
             at = st["t_index"][sl].clamp(min=0)
-            if op != "distill_backward":
+            if op == "distill" or case["loss"]:
                 term = torch.xlogy(q, q) - q * torch.where(live, logp.gather(1, at), 0.0)
-                o["loss"], o["lse"] = temp * temp * term.sum(1), lse
-            if op != "distill":
+                o["loss"] = temp * temp * term.sum(1)
+            if op == "distill_backward":
                 dense = torch.zeros_like(p).scatter_add_(1, at, q)
                 o["dlogits"] = temp * st["dloss"][sl].double()[:, None] * (p - dense)
         parts.append(o)
@@ -284,12 +269,11 @@ def work(case):
     if op == "logprobs":  # logits and tokens in; three floats and the alternatives out
         return {"bytes": n * es + rows * (8 + 12 + 12 * k), "flops": 6 * n}
     if op == "logprobs_backward":
-        return {"bytes": 2 * n * es + rows * (16 + (8 if case["entropy"] else 0)),
-                "flops": (7 if case["entropy"] else 4) * n}
+        return {"bytes": 2 * n * es + rows * (16 if case["entropy"] else 12),
+                "flops": (11 if case["entropy"] else 8) * n}
     if op == "distill":
-        return {"bytes": n * es + rows * (12 * k + 8), "flops": 4 * n}
-    if op == "distill_step":
-        return {"bytes": 2 * n * es + rows * (12 * k + 12), "flops": 8 * n}
+        return {"bytes": n * es + rows * (12 * k + 4), "flops": 4 * n}
+    loss = 4 if case["loss"] else 0
     if op == "distill_backward":
-        return {"bytes": 2 * n * es + rows * (12 * k + 8), "flops": 4 * n}
-    return {"bytes": 2 * n * es + rows * 12 + 4, "flops": 8 * n}
+        return {"bytes": 2 * n * es + rows * (12 * k + 4 + loss), "flops": 8 * n}
+    return {"bytes": 2 * n * es + rows * (8 + loss) + 4, "flops": 8 * n}
