@@ -72,6 +72,9 @@ typedef enum {
   FR_OP_SUMSQ = 4
 } fr_op;
 
+/* Most alternatives fr_logprobs returns, and teacher entries fr_distill takes, per row. */
+#define FR_TOP_MAX 128
+
 /* Epilogue applied to a row sum after the reduction. */
 typedef enum {
   FR_EPI_SUM = 0, /* the sum itself */
@@ -80,7 +83,8 @@ typedef enum {
 
 /* Device error codes written by kernels (read by fr_check_device_error). */
 #define FR_DEVERR_NONE 0
-#define FR_DEVERR_BAD_TARGET 1 /* a target outside [0, cols) and != ignore_index */
+#define FR_DEVERR_BAD_TARGET 1 /* a target (token) outside [0, cols) and != ignore_index,
+                                  or a teacher index >= cols */
 #define FR_DEVERR_TIMEOUT 2    /* an asynchronous copy did not complete within its
                                   time budget; the kernel gave up and returned */
 #define FR_DEVERR_BAD_WORKSPACE 3 /* fr_xent's workspace was not prepared by
@@ -325,6 +329,115 @@ fr_status fr_xent_workspace_init(void *workspace, size_t workspace_bytes, fr_str
  */
 #define FR_XENT_PARTS_OFFSET 16
 fr_status fr_xent_mean_from_parts(const void *workspace, float *loss_mean, fr_stream_t stream);
+
+/* ---- rows of logits: scoring, distillation, gradients ----------------------
+ *
+ * Not on the pages: the calls that a program which trains on, or answers with,
+ * the logits of fr_xent and fr_softmax makes around them.  Shared by all five:
+ *
+ *   logits       bf16 or fp32 (`dtype`) [rows, ld] device input, any ld >= cols
+ *                and any element-aligned address.  -inf masks an element (its
+ *                probability, its share of the entropy and its gradient are
+ *                0); the type's lowest value masks too.  A NaN, a +inf, or a
+ *                row whose every logit is -inf makes the row's results NaN (the
+ *                latter's lse is -inf).
+ *   dlogits      of `dtype` [rows, ldd] device output, the gradient, rounded
+ *                once (nearest even).  It may be the logits' own buffer (ldd ==
+ *                ld); any other overlap is not allowed.
+ *   dloss, dlogprob, dentropy
+ *                fp32 upstream gradients, row r's at [r * stride]; stride 0
+ *                gives every row the same one (the gradient of a sum or mean).
+ *   ignore_index rows whose token (target) is this have no log probability and
+ *                no loss: 0, and no gradient from them.
+ * Statistics are those of each call's own pass (max, sum of exponentials, fp32
+ * sums over short runs); x - max is taken before it is scaled, so neither a
+ * common offset of a row nor a lowest-value mask costs digits.  Results do not
+ * depend on other rows and are the same from run to run.  No workspace is
+ * needed.  A token outside [0, cols) other than ignore_index, or a teacher
+ * index >= cols, makes that row's log probability, loss and gradient NaN and
+ * sets FR_DEVERR_BAD_TARGET; nothing outside the row is read.
+ */
+
+/*
+ * Per row x, with LSE = log sum_j exp(x_j) and p_j = exp(x_j - LSE):
+ *   logprob = x[token] - LSE      (0 for token == ignore_index)
+ *   entropy = -sum_j p_j log p_j
+ *   lse     = LSE
+ *   top_index, top_logprob: the `top` largest logits' indices and x - LSE, the
+ *           largest first, equal logits by lower index, NaN as the largest
+ *           (fr_xent's argmax is the first of them)
+ * entropy, lse and the alternatives are given for ignored rows too.
+ *
+ *   token       int64 [rows] device input; may be NULL when logprob is
+ *   logprob, entropy, lse   fp32 [rows] device outputs; each may be NULL
+ *   top         0 .. min(cols, FR_TOP_MAX); 0: top_logprob and top_index NULL
+ *   top_logprob fp32, top_index int64 [rows, top] device outputs
+ * At least one output is requested.
+ */
+fr_status fr_logprobs(const void *logits, const int64_t *token, float *logprob, float *entropy,
+                      float *lse, float *top_logprob, int64_t *top_index, int32_t top,
+                      int64_t rows, int64_t cols, int64_t ld, int64_t ignore_index,
+                      fr_dtype dtype, fr_form form, fr_stream_t stream);
+
+/*
+ * The gradient of fr_logprobs' logprob and entropy with respect to the logits:
+ *   dlogits_j = g (delta_{j,token} - p_j) - h p_j (log p_j + entropy)
+ * with g = dlogprob (0 for an ignored row) and h = dentropy.  Either of dlogprob and dentropy
+ * may be NULL (no gradient from that output), not both; token may be NULL when
+ * dlogprob is.
+ */
+fr_status fr_logprobs_backward(const void *logits, const int64_t *token, const float *dlogprob,
+                               int64_t dlogprob_stride, const float *dentropy,
+                               int64_t dentropy_stride, void *dlogits, int64_t rows,
+                               int64_t cols, int64_t ld, int64_t ldd, int64_t ignore_index,
+                               fr_dtype dtype, fr_form form, fr_stream_t stream);
+
+/*
+ * Distillation from a teacher's top logits.  With q the softmax of the row's
+ * teacher_logit / temperature over its live entries and p that of the whole
+ * row of logits / temperature:
+ *   loss = temperature^2 sum_i q_i (log q_i - log p[teacher_index_i])
+ * A softmax does not see a common offset, so a teacher's log probabilities
+ * (fr_logprobs' top_logprob and top_index) serve as its logits.  An entry with
+ * a negative index is padding and is not looked at; an entry of -inf has no
+ * weight; the same index twice counts twice.  A row without weight (all
+ * padding or -inf) has loss 0 and no gradient.  An entry with weight whose
+ * logit is -inf makes the loss +inf.
+ *
+ *   teacher_index int64, teacher_logit fp32: [rows, ldt] device inputs, the first
+ *                `top` of each row's ldt >= top elements
+ *   top          1 .. FR_TOP_MAX
+ *   temperature  > 0, finite, with a finite log2(e) / temperature
+ *   loss         fp32 [rows] device output
+ */
+fr_status fr_distill(const void *logits, const int64_t *teacher_index,
+                     const float *teacher_logit, float *loss, int32_t top, int64_t rows,
+                     int64_t cols, int64_t ld, int64_t ldt, float temperature, fr_dtype dtype,
+                     fr_form form, fr_stream_t stream);
+
+/*
+ * The gradient of fr_distill's loss, and, when `loss` is not NULL, the loss of
+ * the same pass over the rows (a training step in one call):
+ *   dlogits_j = dloss temperature (p_j - sum of q_i over the entries naming j)
+ */
+fr_status fr_distill_backward(const void *logits, const int64_t *teacher_index,
+                              const float *teacher_logit, const float *dloss,
+                              int64_t dloss_stride, float *loss, void *dlogits, int32_t top,
+                              int64_t rows, int64_t cols, int64_t ld, int64_t ldd, int64_t ldt,
+                              float temperature, fr_dtype dtype, fr_form form,
+                              fr_stream_t stream);
+
+/*
+ * The gradient of fr_xent's loss, and, when `loss` is not NULL, that loss from
+ * the same pass over the rows:
+ *   dlogits_j = dloss (p_j - delta_{j,target})      (0 for an ignored row)
+ * For the mean over counted rows give one dloss of 1 / their count with
+ * stride 0.
+ */
+fr_status fr_xent_backward(const void *logits, const int64_t *target, const float *dloss,
+                           int64_t dloss_stride, float *loss, void *dlogits, int64_t rows,
+                           int64_t cols, int64_t ld, int64_t ldd, int64_t ignore_index,
+                           fr_dtype dtype, fr_form form, fr_stream_t stream);
 
 /* ---- launch configurations ----------------------------------------------
  *

@@ -12,6 +12,11 @@ Functions carry the C names:
     fr_softmax(x, form="auto")                                -> y fp32
     fr_layernorm(x, gamma, beta, eps=1e-5, form="auto")       -> (y bf16, mean, rstd)
     fr_xent(logits, target, ignore_index=-100, ...)           -> dict of outputs
+    fr_xent_backward(logits, target, dloss, ...)              -> dict: dlogits, loss
+    fr_logprobs(logits, token, top=0, ...)                    -> dict of outputs
+    fr_logprobs_backward(logits, token, dlogprob, dentropy)   -> dlogits
+    fr_distill(logits, teacher_index, teacher_logit, ...)     -> loss [rows] fp32
+    fr_distill_backward(logits, ..., dloss, ...)              -> dict: dlogits, loss
     fr_workspace_size(op, rows, cols, dtype, form)
     fr_check_device_error()
 """
@@ -28,7 +33,8 @@ __all__ = [
     "fr_xent", "fr_xent_workspace", "fr_xent_mean_from_parts", "xent_mean_parts",
     "allreduce_mean_parts", "XENT_PARTS_OFFSET",
     "fr_reduce_relu_add_sum_split_static", "fr_check_device_error", "FORMS", "OPS",
-    "EPILOGUES", "fr_coordinate_descent", "fr_xent_get_config", "fr_xent_set_config",
+    "EPILOGUES", "FR_TOP_MAX", "fr_logprobs", "fr_logprobs_backward", "fr_distill",
+    "fr_distill_backward", "fr_xent_backward", "fr_coordinate_descent", "fr_xent_get_config", "fr_xent_set_config",
     "fr_xent_tune",
 ]
 
@@ -41,11 +47,13 @@ FORMS = {"auto": 0, "persistent": 1, "looped": 2, "split": 3}
 FORM_NAMES = {v: k for k, v in FORMS.items()}
 OPS = {"relu_add_sum": 0, "softmax": 1, "layernorm": 2, "xent": 3, "sumsq": 4}
 EPILOGUES = {"sum": 0, "sqrt": 1}
+FR_TOP_MAX = 128  # most alternatives (fr_logprobs) or teacher entries (fr_distill) per row
 DTYPES = {"f32": 0, "bf16": 1}
 
 # name -> (restype, argtypes) of every symbol include/fr.h declares
 _i64, _f32, _vp, _sz, _int = ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t, \
     ctypes.c_int
+_i32 = ctypes.c_int32
 SIGNATURES = {
     "fr_version": (_int, []),
     "fr_status_string": (ctypes.c_char_p, [_int]),
@@ -64,6 +72,16 @@ SIGNATURES = {
                        _sz, _vp]),
     "fr_xent_mean_from_parts": (_int, [_vp, _vp, _vp]),
     "fr_xent_workspace_init": (_int, [_vp, _sz, _vp]),
+    "fr_logprobs": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _int,
+                           _int, _vp]),
+    "fr_logprobs_backward": (_int, [_vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64,
+                                    _i64, _int, _int, _vp]),
+    "fr_distill": (_int, [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _f32, _int, _int,
+                          _vp]),
+    "fr_distill_backward": (_int, [_vp, _vp, _vp, _vp, _i64, _vp, _vp, _i32, _i64, _i64, _i64,
+                                   _i64, _i64, _f32, _int, _int, _vp]),
+    "fr_xent_backward": (_int, [_vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _int,
+                                _int, _vp]),
     "fr_check_device_error": (_int, [_vp, ctypes.POINTER(ctypes.c_int32)]),
     "fr_coordinate_descent": (_int, [ctypes.c_int32, _vp, _vp, _vp, ctypes.c_double, _vp, _vp,
                                      _vp, _vp]),
@@ -428,6 +446,203 @@ def fr_reduce_relu_add_sum_split_static(a, b, scale: float = 2.0, out=None, stre
                                                      _stream(stream)),
            "fr_reduce_relu_add_sum_split_static")
     return out
+
+
+# ---- rows of logits: scoring, distillation, gradients ---------------------------
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _logits_arg(x, name: str = "logits"):
+    """(rows, cols, ld, dtype code) of a matrix of logits; refuses anything else."""
+    torch = _torch()
+    _need(x.is_cuda, f"{name} must be a CUDA tensor")
+    _need(x.dtype in (torch.bfloat16, torch.float32), f"{name} must be bf16 or fp32")
+    _need(x.dim() == 2, f"{name} must have two dimensions")
+    rows, cols = x.shape
+    _need(rows > 0 and cols > 0, f"{name} must have at least one row and one column")
+    _need(cols == 1 or x.stride(1) == 1, f"rows of {name} must be contiguous")
+    # a single row has no distance to the next one (torch may report any)
+    ld = x.stride(0) if rows > 1 else cols
+    _need(ld >= cols, f"rows of {name} overlap")
+    return rows, cols, ld, DTYPES["f32" if x.dtype == torch.float32 else "bf16"]
+
+
+def _row_vector(t, name: str, rows: int, dtype):
+    _need(t.is_cuda and t.dtype == dtype, f"{name} must be a CUDA tensor of {dtype}")
+    _need(t.dim() == 1 and t.shape[0] == rows and (rows == 1 or t.stride(0) == 1),
+          f"{name} must be contiguous with one element per row")
+    return t
+
+
+def _upstream(t, name: str, rows: int) -> int:
+    """The stride of an upstream gradient: fp32, one value per row or one in all."""
+    torch = _torch()
+    _need(t.is_cuda and t.dtype == torch.float32, f"{name} must be a CUDA tensor of torch.float32")
+    if t.numel() == 1:
+        return 0
+    _need(t.dim() == 1 and t.shape[0] == rows, f"{name} must hold one value, or one per row")
+    return t.stride(0)
+
+
+def _teacher_args(index, logit, rows: int):
+    """(top, ldt) of a row's teacher entries."""
+    torch = _torch()
+    _need(index.is_cuda and index.dtype == torch.int64, "teacher_index must be int64 on CUDA")
+    _need(logit.is_cuda and logit.dtype == torch.float32, "teacher_logit must be fp32 on CUDA")
+    _need(index.dim() == 2 and index.shape == logit.shape and index.shape[0] == rows,
+          "teacher_index and teacher_logit must be [rows, top]")
+    top = index.shape[1]
+    _need(1 <= top <= FR_TOP_MAX, f"1 to {FR_TOP_MAX} teacher entries per row")
+    for t in (index, logit):
+        _need(top == 1 or t.stride(1) == 1, "a row's teacher entries must be contiguous")
+    ldt = index.stride(0) if rows > 1 else top
+    _need(rows == 1 or logit.stride(0) == ldt,
+          "teacher_index and teacher_logit must have the same row stride")
+    _need(ldt >= top, "teacher rows overlap")
+    return top, ldt
+
+
+def _on_stream(stream):
+    """Outputs made for a call belong to the stream it runs on."""
+    return _nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
+def _gradient_out(x, ld: int, given):
+    """`given` after its checks, or a new matrix whose rows share the logits'
+    offset within 32 bytes (a compact matrix when theirs are compact)."""
+    torch = _torch()
+    if given is not None:
+        _need(given.shape == x.shape and given.dtype == x.dtype,
+              "dlogits must have the logits' shape and dtype")
+        return given, _logits_arg(given, "dlogits")[2]
+    rows, cols = x.shape
+    per = 32 // x.element_size()
+    ldd = cols + (ld - cols) % per
+    return torch.empty(rows, ldd, dtype=x.dtype, device=x.device)[:, :cols], ldd
+
+
+def fr_logprobs(logits, token=None, top: int = 0, ignore_index: int = -100,
+                want_entropy: bool = True, want_lse: bool = True, form: str = "auto",
+                stream=None):
+    """Log probabilities of given tokens, the entropy and the top alternatives of
+    each row of bf16 or fp32 logits, in one pass.
+
+    Returns a dict: ``logprob`` [rows] (with ``token`` int64 [rows]; 0 where it
+    is ``ignore_index``), ``entropy`` [rows], ``lse`` [rows], and with ``top``
+    (at most min(cols, FR_TOP_MAX)) ``top_logprob`` and ``top_index`` [rows,
+    top], the largest first, ties by the lower index.  All fp32 but the int64
+    ``top_index``."""
+    torch = _torch()
+    rows, cols, ld, dt = _logits_arg(logits)
+    _need(0 <= top <= min(cols, FR_TOP_MAX), f"top must be 0 to min(cols, {FR_TOP_MAX})")
+    _need(token is not None or want_entropy or want_lse or top > 0, "no output requested")
+    if token is not None:
+        _row_vector(token, "token", rows, torch.int64)
+    _on_current_device(logits, token)
+    dev = logits.device
+    res = {}
+    with _on_stream(stream):
+        def out(name, want, *shape, dtype=torch.float32):
+            if want:
+                res[name] = torch.empty(*shape, dtype=dtype, device=dev)
+            return _ptr(res.get(name))
+        p = (out("logprob", token is not None, rows), out("entropy", want_entropy, rows),
+             out("lse", want_lse, rows), out("top_logprob", top > 0, rows, top),
+             out("top_index", top > 0, rows, top, dtype=torch.int64))
+    _check(lib().fr_logprobs(_ptr(logits), _ptr(token), *p, top, rows, cols, ld, ignore_index, dt,
+                             FORMS[form], _stream(stream)), "fr_logprobs")
+    return res
+
+
+def fr_logprobs_backward(logits, token=None, dlogprob=None, dentropy=None,
+                         ignore_index: int = -100, dlogits=None, form: str = "auto",
+                         stream=None):
+    """The gradient of fr_logprobs' ``logprob`` and ``entropy`` with respect to the
+    logits, from fp32 upstream gradients with one value per row or one in all
+    (either may be None).  ``dlogits`` may be ``logits`` (in place)."""
+    rows, cols, ld, dt = _logits_arg(logits)
+    _need(dlogprob is not None or dentropy is not None, "no upstream gradient given")
+    _need(dlogprob is None or token is not None, "dlogprob needs the tokens")
+    if token is not None:
+        _row_vector(token, "token", rows, _torch().int64)
+    gs = 0 if dlogprob is None else _upstream(dlogprob, "dlogprob", rows)
+    hs = 0 if dentropy is None else _upstream(dentropy, "dentropy", rows)
+    with _on_stream(stream):
+        dlogits, ldd = _gradient_out(logits, ld, dlogits)
+    _on_current_device(logits, token, dlogprob, dentropy, dlogits)
+    _check(lib().fr_logprobs_backward(_ptr(logits), _ptr(token), _ptr(dlogprob), gs,
+                                      _ptr(dentropy), hs, _ptr(dlogits), rows, cols, ld, ldd,
+                                      ignore_index, dt, FORMS[form], _stream(stream)),
+           "fr_logprobs_backward")
+    return dlogits
+
+
+def fr_distill(logits, teacher_index, teacher_logit, temperature: float = 1.0,
+               form: str = "auto", stream=None):
+    """The distillation loss [rows] (fp32) of bf16 or fp32 logits against a teacher's
+    top logits: temperature^2 KL(softmax(teacher_logit / T) || softmax(logits /
+    T)) over the entries of ``teacher_index`` (int64 [rows, top], negative:
+    padding) and ``teacher_logit`` (fp32 [rows, top]; log probabilities serve)."""
+    torch = _torch()
+    rows, cols, ld, dt = _logits_arg(logits)
+    top, ldt = _teacher_args(teacher_index, teacher_logit, rows)
+    _on_current_device(logits, teacher_index, teacher_logit)
+    with _on_stream(stream):
+        loss = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    _check(lib().fr_distill(_ptr(logits), _ptr(teacher_index), _ptr(teacher_logit), _ptr(loss),
+                            top, rows, cols, ld, ldt, temperature, dt, FORMS[form],
+                            _stream(stream)), "fr_distill")
+    return loss
+
+
+def fr_distill_backward(logits, teacher_index, teacher_logit, dloss, temperature: float = 1.0,
+                        want_loss: bool = True, dlogits=None, form: str = "auto", stream=None):
+    """The gradient of fr_distill's loss and, with ``want_loss``, the loss of the
+    same pass: a training step in one call.  Returns a dict: ``dlogits`` and
+    ``loss``.  ``dloss`` holds one fp32 value per row or one in all; ``dlogits``
+    may be ``logits`` (in place)."""
+    torch = _torch()
+    rows, cols, ld, dt = _logits_arg(logits)
+    top, ldt = _teacher_args(teacher_index, teacher_logit, rows)
+    gs = _upstream(dloss, "dloss", rows)
+    res = {}
+    with _on_stream(stream):
+        res["dlogits"], ldd = _gradient_out(logits, ld, dlogits)
+        if want_loss:
+            res["loss"] = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    _on_current_device(logits, teacher_index, teacher_logit, dloss, res["dlogits"])
+    _check(lib().fr_distill_backward(_ptr(logits), _ptr(teacher_index), _ptr(teacher_logit),
+                                     _ptr(dloss), gs, _ptr(res.get("loss")),
+                                     _ptr(res["dlogits"]), top, rows, cols, ld, ldd, ldt,
+                                     temperature, dt, FORMS[form], _stream(stream)),
+           "fr_distill_backward")
+    return res
+
+
+def fr_xent_backward(logits, target, dloss, ignore_index: int = -100, want_loss: bool = True,
+                     dlogits=None, form: str = "auto", stream=None):
+    """The gradient of fr_xent's per-row loss and, with ``want_loss``, that loss from
+    the same pass.  Returns a dict: ``dlogits`` and ``loss``.  ``dloss`` holds one
+    fp32 value per row or one in all (1 / counted rows gives the mean's
+    gradient); ``dlogits`` may be ``logits`` (in place)."""
+    torch = _torch()
+    rows, cols, ld, dt = _logits_arg(logits)
+    _row_vector(target, "target", rows, torch.int64)
+    gs = _upstream(dloss, "dloss", rows)
+    res = {}
+    with _on_stream(stream):
+        res["dlogits"], ldd = _gradient_out(logits, ld, dlogits)
+        if want_loss:
+            res["loss"] = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    _on_current_device(logits, target, dloss, res["dlogits"])
+    _check(lib().fr_xent_backward(_ptr(logits), _ptr(target), _ptr(dloss), gs,
+                                  _ptr(res.get("loss")), _ptr(res["dlogits"]), rows, cols, ld,
+                                  ldd, ignore_index, dt, FORMS[form], _stream(stream)),
+           "fr_xent_backward")
+    return res
 
 
 # ---- launch configurations ----------------------------------------------------

@@ -607,6 +607,210 @@ fr_status fr_xent_mean_from_parts(const void *workspace, float *loss_mean, fr_st
 
 namespace {
 
+// Checks that the calls over rows of logits share; on FR_OK the device is
+// usable and `err` is its error word.
+fr_status logits_args_ok(const void *logits, int64_t rows, int64_t cols, int64_t ld,
+                         fr_dtype dtype) {
+  if (dtype != FR_BF16 && dtype != FR_F32) return FR_ERR_UNSUPPORTED_DTYPE;
+  const int64_t es = dtype == FR_F32 ? 4 : 2;
+  if (!logits || !shape_ok(rows, cols, ld, es)) return FR_ERR_INVALID_ARG;
+  if (!aligned(logits, es)) return FR_ERR_MISALIGNED;
+  return FR_OK;
+}
+
+fr_status gradient_args_ok(const void *logits, const void *dlogits, int64_t rows, int64_t cols,
+                           int64_t ld, int64_t ldd, fr_dtype dtype) {
+  if (fr_status st = logits_args_ok(logits, rows, cols, ld, dtype)) return st;
+  if (fr_status st = logits_args_ok(dlogits, rows, cols, ldd, dtype)) return st;
+  if (logits == dlogits && ld != ldd) return FR_ERR_INVALID_ARG;
+  return FR_OK;
+}
+
+fr_status teacher_args_ok(const int64_t *index, const float *logit, int32_t top, int64_t rows,
+                          int64_t ldt, float temperature) {
+  if (!index || !logit || top < 1 || top > FR_TOP_MAX || !shape_ok(rows, top, ldt, 8))
+    return FR_ERR_INVALID_ARG;
+  if (!(temperature > 0.0f) || !std::isfinite(temperature) ||
+      !std::isfinite(1.4426950408889634f / temperature))
+    return FR_ERR_INVALID_ARG;
+  if (!aligned(index, 8) || !aligned(logit, 4)) return FR_ERR_MISALIGNED;
+  return FR_OK;
+}
+
+fr_status logits_device_ok(int64_t cols, fr_form form, fr::DevInfo *info, int **err) {
+  if (form != FR_FORM_AUTO && form != FR_FORM_LOOPED) return FR_ERR_UNSUPPORTED_FORM;
+  if (cols >= (INT64_C(1) << 31)) return FR_ERR_UNSUPPORTED_FORM;  // 32-bit in-row indices
+  if (fr_status st = device_ok(info)) return st;
+  return fr::device_error_word(err) == cudaSuccess ? FR_OK : FR_ERR_CUDA;
+}
+
+// An upstream gradient's stride: not negative, and no row's offset overflows.
+bool stride_ok(int64_t stride, int64_t rows) {
+  return stride >= 0 && stride <= (INT64_C(1) << 60) / rows;
+}
+
+bool aligned_or_null(const void *p, size_t a) { return p == nullptr || aligned(p, a); }
+
+fr_status run_backward(fr::LogitsBackward &a, fr_dtype dtype, bool distill, fr_form form,
+                       fr_stream_t stream) {
+  fr::DevInfo info;
+  if (fr_status st = logits_device_ok(a.cols, form, &info, &a.err)) return st;
+  const bool f32 = dtype == FR_F32;
+  const bool vec = same_phase(a.logits, a.ld, a.dlogits, a.ldd, f32 ? 4 : 2);
+  return launched(fr::launch_logits_backward(a, f32, distill, vec,
+                                             reinterpret_cast<cudaStream_t>(stream)),
+                  FR_FORM_LOOPED);
+}
+
+}  // namespace
+
+fr_status fr_logprobs(const void *logits, const int64_t *token, float *logprob, float *entropy,
+                      float *lse, float *top_logprob, int64_t *top_index, int32_t top,
+                      int64_t rows, int64_t cols, int64_t ld, int64_t ignore_index,
+                      fr_dtype dtype, fr_form form, fr_stream_t stream) {
+  if (fr_status st = logits_args_ok(logits, rows, cols, ld, dtype)) return st;
+  if (top < 0 || top > FR_TOP_MAX || top > cols) return FR_ERR_INVALID_ARG;
+  if ((top > 0) != (top_logprob != nullptr) || (top > 0) != (top_index != nullptr))
+    return FR_ERR_INVALID_ARG;
+  if (logprob && !token) return FR_ERR_INVALID_ARG;
+  if (!logprob && !entropy && !lse && top == 0) return FR_ERR_INVALID_ARG;
+  if (!aligned_or_null(token, 8) || !aligned_or_null(logprob, 4) || !aligned_or_null(entropy, 4) ||
+      !aligned_or_null(lse, 4) || !aligned_or_null(top_logprob, 4) ||
+      !aligned_or_null(top_index, 8))
+    return FR_ERR_MISALIGNED;
+  fr::LogitsForward a{};
+  fr::DevInfo info;
+  if (fr_status st = logits_device_ok(cols, form, &info, &a.err)) return st;
+  a.logits = logits;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld = ld;
+  a.token = token;
+  a.ignore_index = ignore_index;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.lse = lse;
+  a.top_logprob = top_logprob;
+  a.top_index = top_index;
+  a.top = top;
+  a.temperature = 1.0f;
+  return launched(fr::launch_logits_forward(a, dtype == FR_F32, false,
+                                            reinterpret_cast<cudaStream_t>(stream)),
+                  FR_FORM_LOOPED);
+}
+
+fr_status fr_logprobs_backward(const void *logits, const int64_t *token, const float *dlogprob,
+                               int64_t dlogprob_stride, const float *dentropy,
+                               int64_t dentropy_stride, void *dlogits, int64_t rows,
+                               int64_t cols, int64_t ld, int64_t ldd, int64_t ignore_index,
+                               fr_dtype dtype, fr_form form, fr_stream_t stream) {
+  if (fr_status st = gradient_args_ok(logits, dlogits, rows, cols, ld, ldd, dtype)) return st;
+  if ((!dlogprob && !dentropy) || (dlogprob && !token)) return FR_ERR_INVALID_ARG;
+  if (!stride_ok(dlogprob_stride, rows) || !stride_ok(dentropy_stride, rows))
+    return FR_ERR_INVALID_ARG;
+  if (!aligned_or_null(token, 8) || !aligned_or_null(dlogprob, 4) || !aligned_or_null(dentropy, 4))
+    return FR_ERR_MISALIGNED;
+  fr::LogitsBackward a{};
+  a.logits = logits;
+  a.dlogits = dlogits;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld = ld;
+  a.ldd = ldd;
+  a.dloss = dlogprob;
+  a.dloss_stride = dlogprob_stride;
+  a.token = dlogprob ? token : nullptr;
+  a.ignore_index = ignore_index;
+  a.dloss_sign = 1.0f;
+  a.dentropy = dentropy;
+  a.dentropy_stride = dentropy_stride;
+  a.temperature = 1.0f;
+  return run_backward(a, dtype, false, form, stream);
+}
+
+fr_status fr_distill(const void *logits, const int64_t *teacher_index,
+                     const float *teacher_logit, float *loss, int32_t top, int64_t rows,
+                     int64_t cols, int64_t ld, int64_t ldt, float temperature, fr_dtype dtype,
+                     fr_form form, fr_stream_t stream) {
+  if (fr_status st = logits_args_ok(logits, rows, cols, ld, dtype)) return st;
+  if (fr_status st = teacher_args_ok(teacher_index, teacher_logit, top, rows, ldt, temperature))
+    return st;
+  if (!loss) return FR_ERR_INVALID_ARG;
+  if (!aligned(loss, 4)) return FR_ERR_MISALIGNED;
+  fr::LogitsForward a{};
+  fr::DevInfo info;
+  if (fr_status st = logits_device_ok(cols, form, &info, &a.err)) return st;
+  a.logits = logits;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld = ld;
+  a.index = teacher_index;
+  a.teacher = teacher_logit;
+  a.ldt = ldt;
+  a.top = top;
+  a.temperature = temperature;
+  a.loss = loss;
+  return launched(fr::launch_logits_forward(a, dtype == FR_F32, true,
+                                            reinterpret_cast<cudaStream_t>(stream)),
+                  FR_FORM_LOOPED);
+}
+
+fr_status fr_distill_backward(const void *logits, const int64_t *teacher_index,
+                              const float *teacher_logit, const float *dloss,
+                              int64_t dloss_stride, float *loss, void *dlogits, int32_t top,
+                              int64_t rows, int64_t cols, int64_t ld, int64_t ldd, int64_t ldt,
+                              float temperature, fr_dtype dtype, fr_form form,
+                              fr_stream_t stream) {
+  if (fr_status st = gradient_args_ok(logits, dlogits, rows, cols, ld, ldd, dtype)) return st;
+  if (fr_status st = teacher_args_ok(teacher_index, teacher_logit, top, rows, ldt, temperature))
+    return st;
+  if (!dloss || !stride_ok(dloss_stride, rows)) return FR_ERR_INVALID_ARG;
+  if (!aligned(dloss, 4) || !aligned_or_null(loss, 4)) return FR_ERR_MISALIGNED;
+  fr::LogitsBackward a{};
+  a.logits = logits;
+  a.dlogits = dlogits;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld = ld;
+  a.ldd = ldd;
+  a.dloss = dloss;
+  a.dloss_stride = dloss_stride;
+  a.loss = loss;
+  a.index = teacher_index;
+  a.teacher = teacher_logit;
+  a.ldt = ldt;
+  a.top = top;
+  a.temperature = temperature;
+  return run_backward(a, dtype, true, form, stream);
+}
+
+fr_status fr_xent_backward(const void *logits, const int64_t *target, const float *dloss,
+                           int64_t dloss_stride, float *loss, void *dlogits, int64_t rows,
+                           int64_t cols, int64_t ld, int64_t ldd, int64_t ignore_index,
+                           fr_dtype dtype, fr_form form, fr_stream_t stream) {
+  if (fr_status st = gradient_args_ok(logits, dlogits, rows, cols, ld, ldd, dtype)) return st;
+  if (!target || !dloss || !stride_ok(dloss_stride, rows)) return FR_ERR_INVALID_ARG;
+  if (!aligned(target, 8) || !aligned(dloss, 4) || !aligned_or_null(loss, 4))
+    return FR_ERR_MISALIGNED;
+  fr::LogitsBackward a{};
+  a.logits = logits;
+  a.dlogits = dlogits;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld = ld;
+  a.ldd = ldd;
+  a.dloss = dloss;
+  a.dloss_stride = dloss_stride;
+  a.loss = loss;
+  a.token = target;
+  a.ignore_index = ignore_index;
+  a.dloss_sign = -1.0f;
+  a.temperature = 1.0f;
+  return run_backward(a, dtype, false, form, stream);
+}
+
+namespace {
+
 fr::XentConfig from_c(const fr_xent_config &c) {
   return fr::XentConfig{c.threads, c.vectors, c.stages, c.ctas_per_sm};
 }

@@ -212,6 +212,55 @@ cudaError_t launch_xent(const void *logits, bool f32, const int64_t *target, flo
                         float *loss_mean, float *target_logit, int64_t *argmax, int64_t rows,
                         int64_t cols, int64_t ld, int64_t ignore_index, void *workspace,
                         int sm_count, int max_smem_optin, cudaStream_t s);
+
+// ---- rows of logits: log probabilities, distillation and their gradients ------
+
+struct LogitsForward {
+  const void *logits;
+  int64_t rows, cols, ld;
+  // log probabilities
+  const int64_t *token;  // NULL: no log probability wanted
+  int64_t ignore_index;
+  float *logprob, *entropy, *lse;  // each NULL when not wanted
+  float *top_logprob;              // [rows, top]
+  int64_t *top_index;
+  int32_t top;  // alternatives, or teacher entries, per row
+  // distillation
+  const int64_t *index;  // [rows, ldt]
+  const float *teacher;
+  int64_t ldt;
+  float temperature;
+  float *loss;
+  int *err;  // the device error word
+};
+cudaError_t launch_logits_forward(const LogitsForward &a, bool f32, bool distill,
+                                  cudaStream_t s);
+
+struct LogitsBackward {
+  const void *logits;
+  void *dlogits;  // may be logits (ldd == ld)
+  int64_t rows, cols, ld, ldd;
+  const float *dloss;  // the upstream gradient of row r at r * dloss_stride
+  int64_t dloss_stride;
+  float *loss;  // NULL when not wanted
+  // given tokens: dloss * dloss_sign is the log probability's gradient
+  const int64_t *token;  // NULL: only the entropy's gradient
+  int64_t ignore_index;
+  float dloss_sign;
+  const float *dentropy;  // NULL: no gradient of the entropy
+  int64_t dentropy_stride;
+  // distillation
+  const int64_t *index;  // [rows, ldt]
+  const float *teacher;
+  int64_t ldt;
+  int32_t top;
+  float temperature;
+  int *err;
+};
+// vec: logits and dlogits rows share their offset modulo 32 bytes
+cudaError_t launch_logits_backward(const LogitsBackward &a, bool f32, bool distill, bool vec,
+                                   cudaStream_t s);
+
 // Device address of the current device's error word (kernels record
 // FR_DEVERR_* codes there with atomicCAS; the first code wins).
 cudaError_t device_error_word(int **out);
