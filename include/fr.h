@@ -69,7 +69,12 @@ typedef enum {
   FR_OP_SOFTMAX = 1,
   FR_OP_LAYERNORM = 2,
   FR_OP_XENT = 3,
-  FR_OP_SUMSQ = 4
+  FR_OP_SUMSQ = 4,
+  FR_OP_LOGPROBS = 5,
+  FR_OP_LOGPROBS_BACKWARD = 6,
+  FR_OP_DISTILL = 7,
+  FR_OP_DISTILL_BACKWARD = 8,
+  FR_OP_XENT_BACKWARD = 9
 } fr_op;
 
 /* Most alternatives fr_logprobs returns, and teacher entries fr_distill takes, per row. */
@@ -352,8 +357,7 @@ fr_status fr_xent_mean_from_parts(const void *workspace, float *loss_mean, fr_st
  * Statistics are those of each call's own pass (max, sum of exponentials, fp32
  * sums over short runs); x - max is taken before it is scaled, so neither a
  * common offset of a row nor a lowest-value mask costs digits.  Results do not
- * depend on other rows and are the same from run to run.  No workspace is
- * needed.  A token outside [0, cols) other than ignore_index, or a teacher
+ * depend on other rows and are the same from run to run.  A token outside [0, cols) other than ignore_index, or a teacher
  * index >= cols, makes that row's log probability, loss and gradient NaN and
  * sets FR_DEVERR_BAD_TARGET; nothing outside the row is read.
  */
@@ -372,12 +376,18 @@ fr_status fr_xent_mean_from_parts(const void *workspace, float *loss_mean, fr_st
  *   logprob, entropy, lse   fp32 [rows] device outputs; each may be NULL
  *   top         0 .. min(cols, FR_TOP_MAX); 0: top_logprob and top_index NULL
  *   top_logprob fp32, top_index int64 [rows, top] device outputs
- * At least one output is requested.
+ *   workspace   device scratch of fr_workspace_size(FR_OP_LOGPROBS, ...) bytes,
+ *               16-byte aligned; only the looped form with top > 0 uses it (1/64
+ *               of a bf16 matrix, 1/128 of an fp32 one); may be NULL otherwise.
+ *               One call at a time may use a workspace.
+ * At least one output is requested.  Forms: looped (a warp per row) and split (a
+ * cluster of up to 8 CTAs per row, for few rows).
  */
 fr_status fr_logprobs(const void *logits, const int64_t *token, float *logprob, float *entropy,
                       float *lse, float *top_logprob, int64_t *top_index, int32_t top,
                       int64_t rows, int64_t cols, int64_t ld, int64_t ignore_index,
-                      fr_dtype dtype, fr_form form, fr_stream_t stream);
+                      fr_dtype dtype, fr_form form, void *workspace, size_t workspace_bytes,
+                      fr_stream_t stream);
 
 /*
  * The gradient of fr_logprobs' logprob and entropy with respect to the logits:

@@ -45,10 +45,12 @@ STATUS = {0: "FR_OK", 1: "FR_ERR_INVALID_ARG", 2: "FR_ERR_UNSUPPORTED_DTYPE",
           8: "FR_ERR_NO_DEVICE"}
 FORMS = {"auto": 0, "persistent": 1, "looped": 2, "split": 3}
 FORM_NAMES = {v: k for k, v in FORMS.items()}
-OPS = {"relu_add_sum": 0, "softmax": 1, "layernorm": 2, "xent": 3, "sumsq": 4}
+OPS = {"relu_add_sum": 0, "softmax": 1, "layernorm": 2, "xent": 3, "sumsq": 4, "logprobs": 5,
+       "logprobs_backward": 6, "distill": 7, "distill_backward": 8, "xent_backward": 9}
 EPILOGUES = {"sum": 0, "sqrt": 1}
 FR_TOP_MAX = 128  # most alternatives (fr_logprobs) or teacher entries (fr_distill) per row
 DTYPES = {"f32": 0, "bf16": 1}
+_DTYPE_NAMES = {v: k for k, v in DTYPES.items()}
 
 # name -> (restype, argtypes) of every symbol include/fr.h declares
 _i64, _f32, _vp, _sz, _int = ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t, \
@@ -73,7 +75,7 @@ SIGNATURES = {
     "fr_xent_mean_from_parts": (_int, [_vp, _vp, _vp]),
     "fr_xent_workspace_init": (_int, [_vp, _sz, _vp]),
     "fr_logprobs": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _int,
-                           _int, _vp]),
+                           _int, _vp, _sz, _vp]),
     "fr_logprobs_backward": (_int, [_vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64,
                                     _i64, _int, _int, _vp]),
     "fr_distill": (_int, [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _f32, _int, _int,
@@ -505,9 +507,12 @@ def _teacher_args(index, logit, rows: int):
     return top, ldt
 
 
+_NO_CONTEXT = _nullcontext()
+
+
 def _on_stream(stream):
     """Outputs made for a call belong to the stream it runs on."""
-    return _nullcontext() if stream is None else _torch().cuda.stream(stream)
+    return _NO_CONTEXT if stream is None else _torch().cuda.stream(stream)
 
 
 def _gradient_out(x, ld: int, given):
@@ -521,12 +526,12 @@ def _gradient_out(x, ld: int, given):
     rows, cols = x.shape
     per = 32 // x.element_size()
     ldd = cols + (ld - cols) % per
-    return torch.empty(rows, ldd, dtype=x.dtype, device=x.device)[:, :cols], ldd
+    return torch.empty_strided((rows, cols), (ldd, 1), dtype=x.dtype, device=x.device), ldd
 
 
 def fr_logprobs(logits, token=None, top: int = 0, ignore_index: int = -100,
                 want_entropy: bool = True, want_lse: bool = True, form: str = "auto",
-                stream=None):
+                workspace=None, stream=None):
     """Log probabilities of given tokens, the entropy and the top alternatives of
     each row of bf16 or fp32 logits, in one pass.
 
@@ -534,7 +539,8 @@ def fr_logprobs(logits, token=None, top: int = 0, ignore_index: int = -100,
     is ``ignore_index``), ``entropy`` [rows], ``lse`` [rows], and with ``top``
     (at most min(cols, FR_TOP_MAX)) ``top_logprob`` and ``top_index`` [rows,
     top], the largest first, ties by the lower index.  All fp32 but the int64
-    ``top_index``."""
+    ``top_index``.  ``workspace``: fr_workspace_size("logprobs", ...) bytes, by
+    default allocated for the call."""
     torch = _torch()
     rows, cols, ld, dt = _logits_arg(logits)
     _need(0 <= top <= min(cols, FR_TOP_MAX), f"top must be 0 to min(cols, {FR_TOP_MAX})")
@@ -552,8 +558,11 @@ def fr_logprobs(logits, token=None, top: int = 0, ignore_index: int = -100,
         p = (out("logprob", token is not None, rows), out("entropy", want_entropy, rows),
              out("lse", want_lse, rows), out("top_logprob", top > 0, rows, top),
              out("top_index", top > 0, rows, top, dtype=torch.int64))
+        ws, nws = (None, 0)
+        if top > 0:
+            ws, nws = _workspace("logprobs", rows, cols, _DTYPE_NAMES[dt], form, dev, workspace)
     _check(lib().fr_logprobs(_ptr(logits), _ptr(token), *p, top, rows, cols, ld, ignore_index, dt,
-                             FORMS[form], _stream(stream)), "fr_logprobs")
+                             FORMS[form], _ptr(ws), nws, _stream(stream)), "fr_logprobs")
     return res
 
 

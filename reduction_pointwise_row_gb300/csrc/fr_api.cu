@@ -220,6 +220,21 @@ fr_form pick_layernorm(int64_t, int64_t cols, bool vec, bool aligned16, bool row
   return fr::layernorm_persistent_ok(cols, vec) ? FR_FORM_PERSISTENT : FR_FORM_LOOPED;
 }
 
+// ---- rows of logits
+
+// CTAs per row of the forward calls' split form: the fewest whose grid fills the
+// SMs twice, while each thread still gets a 32-byte vector (past the row's head).
+int forward_split(int64_t rows, int64_t cols, int es, int sm_count) {
+  int split = 1;
+  while (split < 8 && rows * split < 2 * sm_count && cols * es >= 2 * split * 256 * 32 + 64)
+    split *= 2;
+  return split;
+}
+
+fr_form pick_forward(int64_t rows, int64_t, int sm_count) {
+  return rows >= 8 * static_cast<int64_t>(sm_count) ? FR_FORM_LOOPED : FR_FORM_SPLIT;
+}
+
 }  // namespace
 
 extern "C" {
@@ -257,6 +272,11 @@ fr_form fr_auto_form(fr_op op, fr_dtype dtype, int64_t rows, int64_t cols, int32
                  ? pick_layernorm(rows, cols, cols % 16 == 0, true, cols % 8 == 0, kSm103SmemOptin)
                  : FR_FORM_AUTO;
     case FR_OP_XENT: return FR_FORM_LOOPED;
+    case FR_OP_LOGPROBS:
+    case FR_OP_DISTILL: return pick_forward(rows, cols, sm_count);
+    case FR_OP_LOGPROBS_BACKWARD:
+    case FR_OP_DISTILL_BACKWARD:
+    case FR_OP_XENT_BACKWARD: return FR_FORM_LOOPED;
   }
   return FR_FORM_AUTO;
 }
@@ -276,6 +296,12 @@ size_t fr_workspace_size(fr_op op, int64_t rows, int64_t cols, fr_dtype dtype, f
       return f == FR_FORM_SPLIT ? fr::ras_split_workspace(rows, cols, info.sm_count) : 0;
     }
     case FR_OP_XENT: return fr::xent_workspace(rows, info.sm_count);
+    case FR_OP_LOGPROBS: {
+      const int es = dtype == FR_F32 ? 4 : 2;
+      if (!shape_ok(rows, cols, cols, es)) return 0;
+      const fr_form f = form == FR_FORM_AUTO ? pick_forward(rows, cols, info.sm_count) : form;
+      return f == FR_FORM_LOOPED ? fr::logprobs_workspace(rows, cols, es) : 0;
+    }
     default: return 0;
   }
 }
@@ -637,8 +663,7 @@ fr_status teacher_args_ok(const int64_t *index, const float *logit, int32_t top,
   return FR_OK;
 }
 
-fr_status logits_device_ok(int64_t cols, fr_form form, fr::DevInfo *info, int **err) {
-  if (form != FR_FORM_AUTO && form != FR_FORM_LOOPED) return FR_ERR_UNSUPPORTED_FORM;
+fr_status logits_device_ok(int64_t cols, fr::DevInfo *info, int **err) {
   if (cols >= (INT64_C(1) << 31)) return FR_ERR_UNSUPPORTED_FORM;  // 32-bit in-row indices
   if (fr_status st = device_ok(info)) return st;
   return fr::device_error_word(err) == cudaSuccess ? FR_OK : FR_ERR_CUDA;
@@ -651,10 +676,29 @@ bool stride_ok(int64_t stride, int64_t rows) {
 
 bool aligned_or_null(const void *p, size_t a) { return p == nullptr || aligned(p, a); }
 
+fr_status run_forward(fr::LogitsForward &a, fr_dtype dtype, bool distill, fr_form form,
+                      size_t workspace_bytes, fr_stream_t stream) {
+  if (form != FR_FORM_AUTO && form != FR_FORM_LOOPED && form != FR_FORM_SPLIT)
+    return FR_ERR_UNSUPPORTED_FORM;
+  fr::DevInfo info;
+  if (fr_status st = logits_device_ok(a.cols, &info, &a.err)) return st;
+  const bool f32 = dtype == FR_F32;
+  const fr_form f = form == FR_FORM_AUTO ? pick_forward(a.rows, a.cols, info.sm_count) : form;
+  if (!distill && a.top > 0 && f == FR_FORM_LOOPED) {
+    if (!a.workspace || workspace_bytes < fr::logprobs_workspace(a.rows, a.cols, f32 ? 4 : 2))
+      return FR_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned(a.workspace, 16)) return FR_ERR_MISALIGNED;
+  }
+  const int split = f == FR_FORM_LOOPED ? 0 : forward_split(a.rows, a.cols, f32 ? 4 : 2, info.sm_count);
+  return launched(fr::launch_logits_forward(a, f32, distill, split, info.sm_count,
+                                            reinterpret_cast<cudaStream_t>(stream)), f);
+}
+
 fr_status run_backward(fr::LogitsBackward &a, fr_dtype dtype, bool distill, fr_form form,
                        fr_stream_t stream) {
+  if (form != FR_FORM_AUTO && form != FR_FORM_LOOPED) return FR_ERR_UNSUPPORTED_FORM;
   fr::DevInfo info;
-  if (fr_status st = logits_device_ok(a.cols, form, &info, &a.err)) return st;
+  if (fr_status st = logits_device_ok(a.cols, &info, &a.err)) return st;
   const bool f32 = dtype == FR_F32;
   const bool vec = same_phase(a.logits, a.ld, a.dlogits, a.ldd, f32 ? 4 : 2);
   return launched(fr::launch_logits_backward(a, f32, distill, vec,
@@ -667,7 +711,8 @@ fr_status run_backward(fr::LogitsBackward &a, fr_dtype dtype, bool distill, fr_f
 fr_status fr_logprobs(const void *logits, const int64_t *token, float *logprob, float *entropy,
                       float *lse, float *top_logprob, int64_t *top_index, int32_t top,
                       int64_t rows, int64_t cols, int64_t ld, int64_t ignore_index,
-                      fr_dtype dtype, fr_form form, fr_stream_t stream) {
+                      fr_dtype dtype, fr_form form, void *workspace, size_t workspace_bytes,
+                      fr_stream_t stream) {
   if (fr_status st = logits_args_ok(logits, rows, cols, ld, dtype)) return st;
   if (top < 0 || top > FR_TOP_MAX || top > cols) return FR_ERR_INVALID_ARG;
   if ((top > 0) != (top_logprob != nullptr) || (top > 0) != (top_index != nullptr))
@@ -679,8 +724,6 @@ fr_status fr_logprobs(const void *logits, const int64_t *token, float *logprob, 
       !aligned_or_null(top_index, 8))
     return FR_ERR_MISALIGNED;
   fr::LogitsForward a{};
-  fr::DevInfo info;
-  if (fr_status st = logits_device_ok(cols, form, &info, &a.err)) return st;
   a.logits = logits;
   a.rows = rows;
   a.cols = cols;
@@ -694,9 +737,8 @@ fr_status fr_logprobs(const void *logits, const int64_t *token, float *logprob, 
   a.top_index = top_index;
   a.top = top;
   a.temperature = 1.0f;
-  return launched(fr::launch_logits_forward(a, dtype == FR_F32, false,
-                                            reinterpret_cast<cudaStream_t>(stream)),
-                  FR_FORM_LOOPED);
+  a.workspace = workspace;
+  return run_forward(a, dtype, false, form, workspace_bytes, stream);
 }
 
 fr_status fr_logprobs_backward(const void *logits, const int64_t *token, const float *dlogprob,
@@ -738,8 +780,6 @@ fr_status fr_distill(const void *logits, const int64_t *teacher_index,
   if (!loss) return FR_ERR_INVALID_ARG;
   if (!aligned(loss, 4)) return FR_ERR_MISALIGNED;
   fr::LogitsForward a{};
-  fr::DevInfo info;
-  if (fr_status st = logits_device_ok(cols, form, &info, &a.err)) return st;
   a.logits = logits;
   a.rows = rows;
   a.cols = cols;
@@ -750,9 +790,7 @@ fr_status fr_distill(const void *logits, const int64_t *teacher_index,
   a.top = top;
   a.temperature = temperature;
   a.loss = loss;
-  return launched(fr::launch_logits_forward(a, dtype == FR_F32, true,
-                                            reinterpret_cast<cudaStream_t>(stream)),
-                  FR_FORM_LOOPED);
+  return run_forward(a, dtype, true, form, 0, stream);
 }
 
 fr_status fr_distill_backward(const void *logits, const int64_t *teacher_index,

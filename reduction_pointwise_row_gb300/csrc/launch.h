@@ -231,10 +231,13 @@ struct LogitsForward {
   int64_t ldt;
   float temperature;
   float *loss;
-  int *err;  // the device error word
+  void *workspace;  // with alternatives, a warp per row: logprobs_workspace bytes
+  int *err;         // the device error word
 };
-cudaError_t launch_logits_forward(const LogitsForward &a, bool f32, bool distill,
-                                  cudaStream_t s);
+size_t logprobs_workspace(int64_t rows, int64_t cols, int es);
+// split: 0, a warp per row; else a cluster of that many CTAs (1, 2, 4 or 8) per row
+cudaError_t launch_logits_forward(const LogitsForward &a, bool f32, bool distill, int split,
+                                  int sm_count, cudaStream_t s);
 
 struct LogitsBackward {
   const void *logits;

@@ -152,10 +152,7 @@ __global__ void __launch_bounds__(kT) logit_grad_looped(LogitsBackward a) {
 #pragma unroll
       for (int k = 0; k < kNV; ++k)
         v[k] = b + k * kT < sp.nvec ? ld_v8(pr + vo + (b + k * kT) * kVecBytes) : L::filler();
-      float cm = L::max(v[0]);
-#pragma unroll
-      for (int k = 1; k < kNV; ++k) cm = max_nan(cm, L::max(v[k]));
-      stat_fold<F32, HAS_B, kNV>(st, v, cm, c);
+      stat_fold<F32, HAS_B, kNV>(st, v, L::max(v), c);
     }
     st = block_stat<kT>(st, c, red);
 

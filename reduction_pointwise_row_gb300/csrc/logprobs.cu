@@ -4,61 +4,464 @@
 //
 // Each thread keeps the statistics (m, l, s) of logits.cuh over its vectors,
 // folding every group of vectors in with the online-softmax merge of "Stax
-// (4): GPU Codegen and Dynamic Shapes", section 9.5; the CTA merges them
-// (Proposition 9.1).  Then, at T = 1,
+// (4): GPU Codegen and Dynamic Shapes", section 9.5; lanes, warps and CTAs merge
+// theirs the same way (Proposition 9.1).  Then, at T = 1,
 //   log p_t = (x_t - m) - log l,   H = log l - s / l,   LSE = m + log l,
 // the differences from m taken first, so that a large common offset of a row's
 // logits costs no digits.
 //
-// Top alternatives.  The pass keeps the largest logit of every group of
-// vectors (a chunk) in shared memory.  The k-th largest of the chunk maxima is
-// a lower bound of the row's k-th largest logit (k chunks hold one each that
-// large), so only chunks whose maximum reaches a threshold at or below it are
-// read again -- about k of them -- and their logits at or above the threshold
-// are the candidates.  Each candidate's place in the order (larger first, equal
-// ones by index, every NaN largest) is the number of candidates before it.
-// A row whose candidates do not fit (many equal logits, or a row of fewer
-// chunks than k) takes its exact k-th largest logit by bisection over the
-// keys, counting in the row itself.
+// Top alternatives.  A logit's place in the output is the number of candidates
+// that precede it (larger first, equal ones by index, every NaN largest); what
+// matters is to have few candidates.  Both forms find a floor that at least k
+// logits reach: the k-th largest of the maxima of at least k disjoint groups of
+// the row's logits.  With g groups about g log(g / (g - k)) logits reach it, some
+// more than k.  Only vectors that reach it are read again, for their logits.
+//   looped  the pass over the row writes the maximum of every four vectors of a
+//           lane (128 bytes of logits) to the workspace, 1/64 of a bf16 row, and a
+//           second kernel, a warp per row with little state and so many warps an
+//           SM, does the rest: the groups are every eighth of a lane's maxima; the
+//           vectors under the maxima that reach the floor are read again.  (In
+//           one kernel the list's 7 us a row of dependent steps held up the loads:
+//           bf16 [8192, 50257] top 20 took 200-220 us.)  A list that still grows
+//           (equal logits, an order that puts the largest together)
+//           is cut to its k largest, whose least is the next floor.
+//   split   the groups are the threads' vectors, floors of a cluster's CTAs for
+//           k / CTAs each, the least of them the row's; candidates that do not
+//           fit are replaced by an exact bisection over the keys of the row.
+// Candidates are compared with their indexes, so no result depends on the order
+// in which they were found.
 #include "launch.h"
 #include "logits.cuh"
 
 namespace fr {
 namespace {
 
-constexpr int kT = 256;           // threads per CTA
-constexpr int kNV = 4;            // 32-byte vectors a thread loads at once
-constexpr int kChunkSlots = 8;    // chunk maxima a thread keeps
-constexpr int kCandidates = 1024; // candidates a CTA holds
+constexpr int kWarps = 8;  // warps per CTA
+constexpr int kT = 32 * kWarps;
 
-struct TopShared {
-  uint32_t chunk[kChunkSlots * kT];  // keys of the chunk maxima (0: no such chunk)
+// The row's results from its statistics, its token and the token's logit.
+__device__ __forceinline__ void write_stats(const LogitsForward &a, int64_t row, int64_t token,
+                                            float xt, const RowStat &st, float logl) {
+  if (a.logprob) {
+    float lp = (xt - st.m) - logl;
+    if (token == a.ignore_index) {
+      lp = 0.0f;
+    } else if (token < 0 || token >= a.cols) {
+      lp = __int_as_float(0x7fc00000);
+      atomicCAS(a.err, 0, FR_DEVERR_BAD_TARGET);
+    }
+    a.logprob[row] = lp;
+  }
+  if (a.entropy) a.entropy[row] = logl - st.s / st.l;
+  if (a.lse) a.lse[row] = st.m + logl;
+}
+
+// Candidates list[0, n) to their places among the first k: thread `tid` of
+// `threads` takes every threads-th of them.
+__device__ __forceinline__ void write_top(const LogitsForward &a, int64_t row,
+                                          const uint64_t *list, int n, int tid, int threads,
+                                          const RowStat &st, float logl) {
+  const int k = a.top;
+  for (int i = tid; i < n; i += threads) {
+    const uint64_t mine = list[i];
+    int before = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) before += list[j] > mine;
+    if (before >= k) continue;
+    a.top_index[row * k + before] = place_index(mine);
+    a.top_logprob[row * k + before] =
+        (key_logit(static_cast<uint32_t>(mine >> 32)) - st.m) - logl;
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ void write_distill(const LogitsForward &a, int64_t row,
+                                              const unsigned char *pr, const RowStat &st) {
+  const Teacher t = teacher_load<F32>(a.index + row * a.ldt, a.teacher + row * a.ldt, a.top, pr,
+                                      a.cols, a.temperature);
+  const float loss = teacher_loss(t, st, a.temperature);
+  if ((threadIdx.x & 31) != 0) return;
+  a.loss[row] = loss;
+  if (t.bad) atomicCAS(a.err, 0, FR_DEVERR_BAD_TARGET);
+}
+
+// ---- looped: a warp per row ----------------------------------------------------
+
+constexpr int kNV = 8;           // 32-byte vectors a lane loads at once
+constexpr int kStep = 32 * kNV;  // vectors a warp loads at once
+static_assert(kNV == 8, "two maxima of four vectors a step");
+
+// Workspace of a call with alternatives: (m, log l) of each row, then the maxima
+// of its steps, [rows][steps][32 lanes] pairs of bf16 rounded down.
+__host__ __device__ constexpr int64_t maxima_steps(int64_t cols, int es) {
+  return (cols * es / kVecBytes + kStep - 1) / kStep;
+}
+
+constexpr int kSegment = 16;        // steps that the second kernel takes together
+constexpr int kCutAt = FR_TOP_MAX;  // a longer list is cut before more is listed
+
+// A warp's workspace in the second kernel: 5.1 KiB.
+struct WarpTop {
+  uint16_t hot[kSegment * 64];     // first vectors of the maxima that reach the floor
+  uint16_t vec[64];                // vectors (in the segment) that do
+  uint64_t list[kCutAt + 32 * 8];  // room for half the logits of 32 bf16 vectors
+};
+
+// Cuts list[0, n), n > k, to its k largest entries (in any order); returns a
+// bound that those reach and the others do not.  Entries differ (each has its
+// index).  One warp.
+__device__ __noinline__ uint64_t cut_list(uint64_t *list, int n, int k) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  uint32_t kmin = 0xFFFFFFFFu, kmax = 0;
+  for (int i = lane; i < n; i += 32) {
+    const uint32_t key = static_cast<uint32_t>(list[i] >> 32);
+    kmin = min(kmin, key);
+    kmax = max(kmax, key);
+  }
+  uint32_t lo = __reduce_min_sync(0xffffffffu, kmin);  // count(>= lo) >= k
+  uint32_t hi = __reduce_max_sync(0xffffffffu, kmax);  // count(> hi) < k
+  int reach = n;
+  while (lo < hi && reach != k) {
+    const uint32_t mid = hi - (hi - lo) / 2;  // lo < mid <= hi
+    int c = 0;
+    for (int i = lane; i < n; i += 32) c += static_cast<uint32_t>(list[i] >> 32) >= mid;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (c >= k) {
+      lo = mid;
+      reach = c;
+    } else {
+      hi = mid - 1;
+    }
+  }
+  uint64_t least = static_cast<uint64_t>(lo) << 32;
+  if (reach != k) {  // equal logits: the same bisection over their indexes
+    uint32_t a = 0, b = 0xFFFFFFFFu;
+    while (a < b) {
+      const uint32_t mid = b - (b - a) / 2;
+      int c = 0;
+      for (int i = lane; i < n; i += 32) c += list[i] >= (least | mid);
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (c >= k) a = mid;
+      else b = mid - 1;
+      if (c == k) break;
+    }
+    least |= a;
+  }
+  int out = 0;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const uint64_t e = i0 + lane < n ? list[i0 + lane] : 0;
+    const bool keep = i0 + lane < n && e >= least;
+    const uint32_t kept = __ballot_sync(0xffffffffu, keep);
+    if (keep) list[out + __popc(kept & ((1u << lane) - 1))] = e;  // at or before i0 + lane
+    out += __popc(kept);
+    __syncwarp();
+  }
+  return least;
+}
+
+// The key of a floor that at least k of the G * 32 keys in a warp's lanes reach,
+// and not many more: a bisection that stops early.
+template <int G>
+__device__ __forceinline__ uint32_t group_floor(const uint32_t (&key)[G], int k) {
+  uint32_t lo = key[0], hi = key[0];
+#pragma unroll
+  for (int g = 1; g < G; ++g) {
+    lo = min(lo, key[g]);
+    hi = max(hi, key[g]);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  int reach = 32 * G;
+  while (lo < hi && reach > k + k / 4 + 4) {
+    const uint32_t mid = hi - (hi - lo) / 2;  // lo < mid <= hi
+    int c = 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) c += key[g] >= mid;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (c >= k) {
+      lo = mid;
+      reach = c;
+    } else {
+      hi = mid - 1;
+    }
+  }
+  return lo;
+}
+
+// What a logit has to pass to be listed: `v` (a NaN passes any v), and after a
+// cut also to precede `bound` among the place keys.
+struct Floor {
+  float v;
+  uint64_t bound;  // 0: no cut yet
+  __device__ __forceinline__ bool passed(float x) const { return !(x < v); }
+  __device__ __forceinline__ void raise(uint32_t key) {
+    const float f = key_logit(key);
+    v = f != f ? INFINITY : f;  // all NaN: the bound decides
+  }
+};
+
+// The sum of n over the lanes before this one; `total` over all.
+__device__ __forceinline__ int lanes_before(int n, int &total) {
+  int s = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) >= o) s += t;
+  }
+  total = __shfl_sync(0xffffffffu, s, 31);
+  return s - n;
+}
+
+__device__ __forceinline__ void cut_if_long(WarpTop &w, int k, int most, int &n, Floor &floor) {
+  if (n <= most) return;
+  floor.bound = cut_list(w.list, n, k);
+  floor.raise(static_cast<uint32_t>(floor.bound >> 32));
+  n = k;
+}
+
+// Lists the logits that pass of vectors b0 + vec[0, count), count <= 32.
+template <bool F32>
+__device__ __forceinline__ void list_vectors(const unsigned char *pv, int head, WarpTop &w, int b0,
+                                             int count, int k, int &n, Floor &floor) {
+  using L = Logits<F32>;
+  const int lane = threadIdx.x & 31;
+  const bool have = lane < count;
+  const int vi = b0 + (have ? w.vec[lane] : 0);
+  const V8 v = have ? ld_keep_v8(pv + static_cast<int64_t>(vi) * kVecBytes) : L::filler();
+  const uint32_t index = static_cast<uint32_t>(head + vi * L::EPV);
+#pragma unroll
+  for (int j0 = 0; j0 < L::EPV; j0 += 8) {
+    cut_if_long(w, k, kCutAt, n, floor);
+    uint32_t pass = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) pass |= have && floor.passed(L::at(v, j0 + j)) ? 1u << j : 0;
+    if (floor.bound != 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (place_key(logit_key(L::at(v, j0 + j)), index + j0 + j) < floor.bound)
+          pass &= ~(1u << j);
+    }
+    if (!__any_sync(0xffffffffu, pass != 0)) continue;
+    int more;
+    int to = n + lanes_before(__popc(pass), more);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if ((pass >> j) & 1) w.list[to++] = place_key(logit_key(L::at(v, j0 + j)), index + j0 + j);
+    n += more;
+    __syncwarp();
+  }
+}
+
+// Lists one logit a lane (`take`), if it passes.
+__device__ __forceinline__ void list_scalars(WarpTop &w, bool take, float x, int index, int &n,
+                                             const Floor &floor) {
+  const uint64_t place = place_key(logit_key(x), static_cast<uint32_t>(index));
+  const bool hit = take && floor.passed(x) && place >= floor.bound;
+  const uint32_t hits = __ballot_sync(0xffffffffu, hit);
+  if (hit) w.list[n + __popc(hits & ((1u << (threadIdx.x & 31)) - 1))] = place;
+  n += __popc(hits);
+  __syncwarp();
+}
+
+// The largest bf16 that is not above v (v itself where it is one), NaN for NaN.
+__device__ __forceinline__ uint32_t bf16_below(float v) {
+  const uint32_t u = __float_as_uint(v);
+  if (v != v) return 0x7FFFu;
+  return (u >> 16) + ((u & 0x80000000u) && (u & 0xFFFFu) ? 1 : 0);  // towards -inf
+}
+
+template <bool F32, bool DISTILL, bool TOP>
+__global__ void __launch_bounds__(kT, 2) logit_rows_warp(LogitsForward a) {
+  pdl_enter();
+  using L = Logits<F32>;
+  const int lane = threadIdx.x & 31;
+  const float c = DISTILL ? kLog2e / a.temperature : kLog2e;
+  const int64_t nw = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); row < a.rows;
+       row += nw) {
+    const unsigned char *pr = static_cast<const unsigned char *>(a.logits) + row * a.ld * L::ES;
+    const RowSplit sp = row_split(pr, a.cols, L::ES);
+    const unsigned char *pv = pr + static_cast<int64_t>(sp.head) * L::ES;
+    const int nvec = static_cast<int>(sp.nvec);  // cols < 2^31, so at most 2^28
+    uint32_t *maxima = nullptr;
+    if constexpr (TOP)
+      maxima = reinterpret_cast<uint32_t *>(static_cast<float2 *>(a.workspace) + a.rows) +
+               row * maxima_steps(a.cols, L::ES) * 32 + lane;
+    RowStat st = stat_empty();
+    for (int b = 0; b < nvec; b += kStep) {
+      V8 v[kNV];
+#pragma unroll
+      for (int u = 0; u < kNV; ++u) {
+        const int vi = b + lane + 32 * u;
+        v[u] = vi < nvec ? ld_stream_v8(pv + static_cast<int64_t>(vi) * kVecBytes) : L::filler();
+      }
+      float cm;
+      if constexpr (TOP) {
+        const V8 v0[4] = {v[0], v[1], v[2], v[3]}, v1[4] = {v[4], v[5], v[6], v[7]};
+        const float m0 = L::max(v0), m1 = L::max(v1);
+        *maxima = bf16_below(m0) | bf16_below(m1) << 16;
+        maxima += 32;
+        cm = max_nan(m0, m1);
+      } else {
+        cm = L::max(v);
+      }
+      stat_fold<F32, !DISTILL, kNV>(st, v, cm, c);
+    }
+    if (lane < sp.head) {
+      const float x = L::load(pr, lane);
+      if (x != -INFINITY) st = stat_merge(st, RowStat{x, 1.0f, 0.0f}, c);
+    }
+    if (lane < sp.tail) {
+      const float x = L::load(pr, a.cols - sp.tail + lane);
+      if (x != -INFINITY) st = stat_merge(st, RowStat{x, 1.0f, 0.0f}, c);
+    }
+    st = warp_stat(st, c);
+    if constexpr (DISTILL) {
+      write_distill<F32>(a, row, pr, st);
+    } else if (lane == 0) {
+      const float logl = logf(st.l);
+      const int64_t token = a.logprob ? a.token[row] : -1;
+      const float xt = token >= 0 && token < a.cols ? L::load(pr, token) : 0.0f;
+      write_stats(a, row, token, xt, st, logl);
+      if constexpr (TOP) static_cast<float2 *>(a.workspace)[row] = make_float2(st.m, logl);
+    }
+    __syncwarp();
+  }
+}
+
+// The alternatives of the rows whose maxima the kernel above wrote: a warp per row.
+template <bool F32>
+__global__ void __launch_bounds__(kT, 4) logit_top_rows(LogitsForward a) {
+  pdl_enter();
+  using L = Logits<F32>;
+  __shared__ WarpTop tops[kWarps];
+  WarpTop &w = tops[threadIdx.x >> 5];
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (row >= a.rows) return;
+  const unsigned char *pr = static_cast<const unsigned char *>(a.logits) + row * a.ld * L::ES;
+  const RowSplit sp = row_split(pr, a.cols, L::ES);
+  const unsigned char *pv = pr + static_cast<int64_t>(sp.head) * L::ES;
+  const int nvec = static_cast<int>(sp.nvec), steps = (nvec + kStep - 1) / kStep;
+  const float2 stat = static_cast<const float2 *>(a.workspace)[row];
+  const uint32_t *maxima =
+      reinterpret_cast<const uint32_t *>(static_cast<const float2 *>(a.workspace) + a.rows) +
+      row * maxima_steps(a.cols, L::ES) * 32 + lane;
+  const float head = lane < sp.head ? L::load(pr, lane) : -INFINITY;
+  const float tail = lane < sp.tail ? L::load(pr, a.cols - sp.tail + lane) : -INFINITY;
+  const int k = a.top;
+
+  uint32_t sub[4] = {0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u};  // 8 groups a lane
+  for (int step = 0; step < steps; step += 4)
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (step + g < steps) sub[g] = max_nan_bf16x2(sub[g], maxima[(step + g) * 32]);
+  uint32_t key[8];  // of bf16 values: 16 bits order them
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    key[2 * g] = logit_key(bf16_lo(sub[g])) >> 16;
+    key[2 * g + 1] = logit_key(bf16_hi(sub[g])) >> 16;
+  }
+  Floor floor{-INFINITY, 0};
+  const uint32_t fkey = group_floor(key, k);
+  floor.raise(fkey << 16 | (fkey & 0x8000u ? 0 : 0xFFFFu));
+
+  int n = 0, pending = 0;
+  list_scalars(w, lane < sp.head, head, lane, n, floor);
+  list_scalars(w, lane < sp.tail, tail, static_cast<int>(a.cols) - sp.tail + lane, n, floor);
+  for (int s0 = 0; s0 < steps; s0 += kSegment) {
+    const int b0 = s0 * kStep;  // the segment's first vector
+    // the maxima are rounded down, so the floor is too: max >= v makes both >= v's
+    const float low = bf16_lo(bf16_below(floor.v));
+    uint32_t mask = 0;  // bit 2 s + h: four vectors of step s0 + s pass
+#pragma unroll 4
+    for (int s = 0; s < min(kSegment, steps - s0); ++s) {
+      const uint32_t m = maxima[(s0 + s) * 32];
+      mask |= (bf16_lo(m) < low ? 0 : 1u) << (2 * s) | (bf16_hi(m) < low ? 0 : 2u) << (2 * s);
+    }
+    int total;
+    int at = lanes_before(__popc(mask), total);
+    while (mask != 0) {
+      const int bit = __ffs(static_cast<int>(mask)) - 1;
+      mask &= mask - 1;
+      w.hot[at++] = static_cast<uint16_t>((bit >> 1) * kStep + (bit & 1) * 128 + lane);
+    }
+    __syncwarp();
+    // a lane reads one vector, four lanes a listed maximum
+    for (int i0 = 0; i0 < 4 * total; i0 += 32) {
+      const int i = i0 + lane;
+      const int vec = i < 4 * total ? w.hot[i / 4] + 32 * (i % 4) : nvec;
+      const bool have = b0 + vec < nvec;
+      const V8 v =
+          have ? ld_keep_v8(pv + static_cast<int64_t>(b0 + vec) * kVecBytes) : L::filler();
+      const bool hit = have && floor.passed(L::max(v));
+      const uint32_t hits = __ballot_sync(0xffffffffu, hit);
+      if (hit) w.vec[pending + __popc(hits & ((1u << lane) - 1))] = static_cast<uint16_t>(vec);
+      pending += __popc(hits);
+      __syncwarp();
+      if (pending >= 32) {
+        list_vectors<F32>(pv, sp.head, w, b0, 32, k, n, floor);
+        pending -= 32;
+        const uint16_t rest = w.vec[32 + lane];
+        __syncwarp();
+        w.vec[lane] = rest;
+        __syncwarp();
+      }
+    }
+    list_vectors<F32>(pv, sp.head, w, b0, pending, k, n, floor);
+    pending = 0;
+    if (s0 + kSegment < steps) cut_if_long(w, k, k, n, floor);  // the k-th largest so far
+  }
+  cut_if_long(w, k, kCutAt, n, floor);
+  write_top(a, row, w.list, n, lane, 32, RowStat{stat.x, 0.0f, 0.0f}, stat.y);
+}
+
+// ---- split: a cluster of CTAs per row ---------------------------------------------
+
+constexpr int kSplitNV = 4;        // 32-byte vectors a thread loads at once
+constexpr int kCandidates = 1024;  // candidates of a row that its first CTA holds
+
+// 8 bytes from the shared memory of CTA `rank` of this cluster, at the offset
+// that `local` has here.
+__device__ __forceinline__ uint64_t ld_dsmem_u64(const void *local, uint32_t rank) {
+  uint32_t remote;
+  uint64_t v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote) : "memory");
+  return v;
+}
+
+struct SplitShared {
+  float4 part;  // this CTA's m, l, s and (as bits) the key of its floor
+  RowStat red[kWarps];
+  uint32_t key[kT];  // the threads' maxima
+  int warp_n[2][kWarps];
+  uint64_t count;  // candidates found (may pass kCandidates)
   uint64_t cand[kCandidates];
-  int count;                         // candidates found (may pass kCandidates)
-  int warp_n[2][kT / 32];
 };
 
 // The sum of n over the CTA, in every thread.  `buf` alternates between the
 // two sets so that one barrier a call is enough.
-__device__ __forceinline__ int block_count(TopShared &sh, int n, int &buf) {
+__device__ __forceinline__ int block_count(SplitShared &sh, int n, int &buf) {
   n = __reduce_add_sync(0xffffffffu, n);
   if ((threadIdx.x & 31) == 0) sh.warp_n[buf][threadIdx.x >> 5] = n;
   __syncthreads();
   int sum = 0;
 #pragma unroll
-  for (int i = 0; i < kT / 32; ++i) sum += sh.warp_n[buf][i];
+  for (int i = 0; i < kWarps; ++i) sum += sh.warp_n[buf][i];
   buf ^= 1;
   return sum;
 }
 
-__device__ __forceinline__ void add_candidate(TopShared &sh, uint32_t key, int64_t index) {
-  const int at = atomicAdd(&sh.count, 1);
-  if (at < kCandidates) sh.cand[at] = place_key(key, static_cast<uint32_t>(index));
+__device__ __forceinline__ void add_candidate(SplitShared &sh, float x, int64_t index) {
+  const uint32_t at = atomicAdd(reinterpret_cast<uint32_t *>(&sh.count), 1u);  // its low half
+  if (at < kCandidates) sh.cand[at] = place_key(logit_key(x), static_cast<uint32_t>(index));
 }
 
 // Keys of the row's logits at or above `key`, counted over the CTA.
 template <bool F32>
-__device__ int count_from(TopShared &sh, const unsigned char *pr, int64_t cols, uint32_t key,
+__device__ int count_from(SplitShared &sh, const unsigned char *pr, int64_t cols, uint32_t key,
                           int &buf) {
   int n = 0;
   for (int64_t i = threadIdx.x; i < cols; i += kT) n += logit_key(Logits<F32>::load(pr, i)) >= key;
@@ -66,10 +469,11 @@ __device__ int count_from(TopShared &sh, const unsigned char *pr, int64_t cols, 
 }
 
 // The row's k candidates by its exact k-th largest key, given a key that at
-// least k logits reach.  Leaves exactly k of them in sh.cand.
+// least k logits reach: leaves exactly k of them in sh.cand.  One CTA.
 template <bool F32>
-__device__ void exact_candidates(TopShared &sh, const unsigned char *pr, int64_t cols, int k,
-                                 uint32_t reached, int &buf) {
+__device__ __noinline__ void exact_candidates(SplitShared &sh, const unsigned char *pr,
+                                              int64_t cols, int k, uint32_t reached) {
+  int buf = 0;
   uint32_t lo = reached;
   if (lo != 0xFFFFFFFFu && count_from<F32>(sh, pr, cols, lo + 1, buf) >= k) {
     uint64_t a = lo + 1ull, b = 1ull << 32;  // count(>= a) >= k > count(>= b) = 0
@@ -85,12 +489,11 @@ __device__ void exact_candidates(TopShared &sh, const unsigned char *pr, int64_t
   if (threadIdx.x == 0) sh.count = 0;
   __syncthreads();
   for (int64_t i = threadIdx.x; i < cols; i += kT) {
-    const uint32_t key = logit_key(Logits<F32>::load(pr, i));
-    if (key > lo) add_candidate(sh, key, i);
+    const float x = Logits<F32>::load(pr, i);
+    if (logit_key(x) > lo) add_candidate(sh, x, i);
   }
   __syncthreads();
-  int have = sh.count;
-  __syncthreads();
+  int have = static_cast<int>(sh.count);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int64_t i0 = 0; i0 < cols && have < k; i0 += kT) {
     const int64_t i = i0 + threadIdx.x;
@@ -103,161 +506,177 @@ __device__ void exact_candidates(TopShared &sh, const unsigned char *pr, int64_t
     have += total;
   }
   __syncthreads();
-  if (threadIdx.x == 0) sh.count = k;
-  __syncthreads();
 }
 
-template <bool F32, bool DISTILL>
-__global__ void __launch_bounds__(kT) logit_rows(LogitsForward a) {
+template <bool F32, bool DISTILL, bool TOP>
+__global__ void __launch_bounds__(kT, TOP ? 3 : 4) logit_rows_split(LogitsForward a) {
   pdl_enter();
   using L = Logits<F32>;
-  __shared__ RowStat red[kT / 32];
-  __shared__ TopShared sh;
-  const int tid = threadIdx.x;
+  __shared__ SplitShared sh;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int C = static_cast<int>(cluster_nctarank()), q = static_cast<int>(cluster_ctarank());
   const float c = DISTILL ? kLog2e / a.temperature : kLog2e;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const unsigned char *pr =
-        static_cast<const unsigned char *>(a.logits) + row * a.ld * L::ES;
+  for (int64_t row = cluster_id_x(); row < a.rows; row += ncluster_x()) {
+    const unsigned char *pr = static_cast<const unsigned char *>(a.logits) + row * a.ld * L::ES;
     const RowSplit sp = row_split(pr, a.cols, L::ES);
     const unsigned char *pv = pr + static_cast<int64_t>(sp.head) * L::ES;
-    const int64_t steps = (sp.nvec + kT * kNV - 1) / (kT * kNV);
-    const int64_t per_slot = (steps + kChunkSlots - 1) / kChunkSlots;  // steps of one chunk
-    // the scalar this thread takes, if any
-    int64_t si = -1;
-    if (tid < sp.head) si = tid;
-    else if (tid < sp.head + sp.tail) si = sp.head + sp.nvec * L::EPV + (tid - sp.head);
-    const float sv = si >= 0 ? L::load(pr, si) : -INFINITY;
-    RowStat st{sv, si >= 0 ? 1.0f : 0.0f, 0.0f};
-    if (sv == -INFINITY) st = stat_empty();
-
-    float chunk = -INFINITY;
-    int slot = 0;
-    bool chunk_any = false;
-    for (int64_t step = 0; step < steps; ++step) {
-      V8 v[kNV];
-      const int64_t b = step * (kT * kNV) + tid;
-#pragma unroll
-      for (int k = 0; k < kNV; ++k)
-        v[k] = b + k * kT < sp.nvec ? ld_stream_v8(pv + (b + k * kT) * kVecBytes) : L::filler();
-      float cm = L::max(v[0]);
-#pragma unroll
-      for (int k = 1; k < kNV; ++k) cm = max_nan(cm, L::max(v[k]));
-      stat_fold<F32, !DISTILL, kNV>(st, v, cm, c);
-      if (!DISTILL && a.top > 0) {
-        chunk = max_nan(chunk, cm);
-        chunk_any |= b < sp.nvec;
-        if ((step + 1) % per_slot == 0 || step + 1 == steps) {
-          sh.chunk[slot * kT + tid] = chunk_any ? logit_key(chunk) : 0;
-          ++slot;
-          chunk = -INFINITY;
-          chunk_any = false;
-        }
-      }
+    // a row of fewer vectors than threads goes logit by logit, so that every
+    // thread has some: at least k groups for any k
+    const bool scalar = sp.nvec < kT && C == 1;
+    const int v0 = scalar ? 0 : static_cast<int>(sp.nvec * q / C);
+    const int v1 = scalar ? 0 : static_cast<int>(sp.nvec * (q + 1) / C);
+    // this thread's scalars: i0, i0 + kT, ... below i1
+    int i0 = tid, i1 = 0;
+    if (scalar) i1 = static_cast<int>(a.cols);
+    else if (q == 0 && tid < sp.head) i1 = sp.head;
+    const int tail0 = static_cast<int>(a.cols) - sp.tail;
+    if (!scalar && q == C - 1 && tid >= 32 && tid < 32 + sp.tail) {
+      i0 = tail0 + tid - 32;
+      i1 = i0 + 1;
     }
-    st = block_stat<kT>(st, c, red);
-
+    const int64_t token = !DISTILL && a.logprob ? a.token[row] : -1;
+    const float xt = token >= 0 && token < a.cols ? L::load(pr, token) : 0.0f;
+    RowStat st = stat_empty();
+    for (int i = i0; i < i1; i += kT) {
+      const float x = L::load(pr, i);
+      if (x != -INFINITY) st = stat_merge(st, RowStat{x, 1.0f, 0.0f}, c);
+    }
+    for (int b = v0 + tid; b < v1; b += kT * kSplitNV) {
+      V8 v[kSplitNV];
+#pragma unroll
+      for (int u = 0; u < kSplitNV; ++u)
+        v[u] = b + u * kT < v1 ? ld_keep_v8(pv + static_cast<int64_t>(b + u * kT) * kVecBytes)
+                               : L::filler();
+      stat_fold<F32, !DISTILL, kSplitNV>(st, v, L::max(v), c);
+    }
+    const float mine = st.m;  // the largest of this thread's logits
+    const uint32_t mykey = i0 < i1 || v0 + tid < v1 ? logit_key(mine) : 0;
+    if constexpr (TOP) {
+      sh.key[tid] = mykey;
+      if (tid == 0) sh.count = 0;
+    }
+    st = block_stat<kT>(st, c, sh.red);
+    uint32_t fkey = 0;
+    if constexpr (TOP) {
+      // this CTA's floor, for its share of k (every warp computes it)
+      uint32_t key[kWarps];
+#pragma unroll
+      for (int g = 0; g < kWarps; ++g) key[g] = sh.key[g * 32 + lane];
+      fkey = group_floor(key, (a.top + C - 1) / C);
+      if (tid == 0) sh.part.w = __uint_as_float(fkey);
+    }
+    if (tid == 0) {
+      sh.part.x = st.m;
+      sh.part.y = st.l;
+      sh.part.z = st.s;
+    }
+    if (C > 1) {
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+      const float4 o = lane < C ? ld_dsmem_f4(&sh.part, lane)
+                                : make_float4(-INFINITY, 0, 0, __uint_as_float(0xFFFFFFFFu));
+      st = warp_stat(RowStat{o.x, o.y, o.z}, c);
+      if constexpr (TOP) fkey = __reduce_min_sync(0xffffffffu, __float_as_uint(o.w));
+    }
     if constexpr (DISTILL) {
-      if (tid < 32) {
-        const Teacher t = teacher_load<F32>(a.index + row * a.ldt, a.teacher + row * a.ldt, a.top,
-                                            pr, a.cols, a.temperature);
-        const float loss = teacher_loss(t, st, a.temperature);
-        if (tid == 0) {
-          a.loss[row] = loss;
-          if (t.bad) atomicCAS(a.err, 0, FR_DEVERR_BAD_TARGET);
-        }
-      }
+      if (q == 0 && tid < 32) write_distill<F32>(a, row, pr, st);
     } else {
       const float logl = logf(st.l);
-      if (tid == 0) {
-        if (a.logprob) {
-          const int64_t t = a.token[row];
-          float lp = 0.0f;
-          if (t != a.ignore_index) {
-            if (t < 0 || t >= a.cols) {
-              lp = __int_as_float(0x7fc00000);
-              atomicCAS(a.err, 0, FR_DEVERR_BAD_TARGET);
-            } else {
-              lp = (L::load(pr, t) - st.m) - logl;
+      if (q == 0 && tid == 0) write_stats(a, row, token, xt, st, logl);
+      if constexpr (TOP) {
+        if (mykey != 0 && mykey >= fkey) {
+          for (int i = i0; i < i1; i += kT) {
+            const float x = L::load(pr, i);
+            if (logit_key(x) >= fkey) add_candidate(sh, x, i);
+          }
+          for (int b = v0 + tid; b < v1; b += kT) {
+            const V8 v = ld_keep_v8(pv + static_cast<int64_t>(b) * kVecBytes);
+            if (logit_key(L::max(v)) < fkey) continue;
+            const int64_t index = sp.head + int64_t{b} * L::EPV;
+#pragma unroll 1
+            for (int j = 0; j < L::EPV; ++j) {
+              const float x = L::load(pr, index + j);  // from L1
+              if (logit_key(x) >= fkey) add_candidate(sh, x, index + j);
             }
           }
-          a.logprob[row] = lp;
         }
-        if (a.entropy) a.entropy[row] = logl - st.s / st.l;
-        if (a.lse) a.lse[row] = st.m + logl;
-      }
-      if (a.top > 0) {
-        const int k = a.top;
-        int buf = 0;
-        if (tid == 0) sh.count = 0;
-        // A threshold that at least k chunks reach and not many more: bisection
-        // over the keys, down from the row's maximum.  With fewer chunks than k
-        // (the head's and tail's scalars count as one each) every logit passes.
-        const uint32_t skey = si >= 0 ? logit_key(sv) : 0;
-        auto reaching = [&](uint32_t key) {
-          int n = skey >= key;
-          for (int i = 0; i < slot; ++i) n += sh.chunk[i * kT + tid] >= key;
-          return block_count(sh, n, buf);
-        };
-        uint32_t lo = 0;
-        if (reaching(1) >= k) {
-          uint64_t x0 = 1, x1 = static_cast<uint64_t>(logit_key(st.m)) + 1;
-          while (x1 - x0 > 1) {
-            const uint64_t mid = (x0 + x1) / 2;
-            const int n = reaching(static_cast<uint32_t>(mid));
-            if (n >= k) x0 = mid;
-            else x1 = mid;
-            if (n >= k && n <= k + k / 2 + 8) break;
+        if (C > 1) {
+          __syncwarp();
+          cluster_arrive();
+          cluster_wait();
+        } else {
+          __syncthreads();
+        }
+        if (q == 0) {
+          int n = static_cast<int>(sh.count);
+          if (C > 1) {  // warp r takes CTA r's candidates (C is at most kWarps)
+            const int r = tid >> 5;
+            const int mine = lane < C ? static_cast<int>(ld_dsmem_u64(&sh.count, lane)) : 0;
+            const int at = __shfl_sync(0xffffffffu, lanes_before(mine, n), r);
+            const int count = __shfl_sync(0xffffffffu, mine, r);
+            if (n <= kCandidates && r > 0)
+              for (int i = lane; i < count; i += 32) sh.cand[at + i] = ld_dsmem_u64(&sh.cand[i], r);
+            __syncthreads();
           }
-          lo = static_cast<uint32_t>(x0);
-        }
-        __syncthreads();
-        if (skey != 0 && skey >= lo) add_candidate(sh, skey, si);
-        for (int i = 0; i < slot; ++i) {
-          if (sh.chunk[i * kT + tid] == 0 || sh.chunk[i * kT + tid] < lo) continue;
-          const int64_t s1 = (i + 1) * per_slot < steps ? (i + 1) * per_slot : steps;
-          for (int64_t step = i * per_slot; step < s1; ++step)
-            for (int q = 0; q < kNV; ++q) {
-              const int64_t vi = step * (kT * kNV) + q * kT + tid;
-              if (vi >= sp.nvec) break;
-              const V8 v = ld_stream_v8(pv + vi * kVecBytes);
-              if (logit_key(L::max(v)) < lo) continue;
-#pragma unroll
-              for (int j = 0; j < L::EPV; ++j) {
-                const uint32_t key = logit_key(L::at(v, j));
-                if (key >= lo) add_candidate(sh, key, sp.head + vi * L::EPV + j);
-              }
-            }
-        }
-        __syncthreads();
-        if (sh.count > kCandidates) exact_candidates<F32>(sh, pr, a.cols, k, lo, buf);
-        const int n = sh.count;
-        for (int i = tid; i < n; i += kT) {
-          const uint64_t mine = sh.cand[i];
-          int before = 0;
-          for (int j = 0; j < n; ++j) before += sh.cand[j] > mine;
-          if (before < k) {
-            const int64_t o = row * k + before;
-            a.top_index[o] = place_index(mine);
-            a.top_logprob[o] = (key_logit(static_cast<uint32_t>(mine >> 32)) - st.m) - logl;
+          if (n > kCandidates) {
+            exact_candidates<F32>(sh, pr, a.cols, a.top, fkey);
+            n = a.top;
           }
+          write_top(a, row, sh.cand, n, tid, kT, st, logl);
         }
       }
     }
-    __syncthreads();
+    if (C > 1) {  // no CTA's shared memory is written again, or given up, while it is read
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
   }
+}
+
+template <bool F32, bool DISTILL, bool TOP>
+cudaError_t launch_forward(const LogitsForward &a, int split, int sm_count, cudaStream_t s) {
+  const dim3 block(kT);
+  if (split == 0) {
+    // a persistent grid of two CTAs an SM, shrunk so that every warp takes the
+    // same number of rows
+    const int64_t warps = static_cast<int64_t>(sm_count) * 2 * kWarps;
+    const int64_t per_warp = (a.rows + warps - 1) / warps;
+    const int64_t grid = (a.rows + per_warp * kWarps - 1) / (per_warp * kWarps);
+    cudaError_t e = launch_k(logit_rows_warp<F32, DISTILL, TOP>,
+                             dim3(static_cast<unsigned>(grid)), block, 0, s, 0, a);
+    if constexpr (TOP) {
+      if (e != cudaSuccess) return e;
+      e = launch_k(logit_top_rows<F32>, dim3(static_cast<unsigned>((a.rows + kWarps - 1) / kWarps)),
+                   block, 0, s, 0, a);
+    }
+    return e;
+  }
+  const int64_t most = (INT64_C(1) << 30) / split;
+  const int64_t clusters = a.rows < most ? a.rows : most;
+  return launch_k(logit_rows_split<F32, DISTILL, TOP>,
+                  dim3(static_cast<unsigned>(clusters * split)), block, 0, s, split, a);
 }
 
 }  // namespace
 
-cudaError_t launch_logits_forward(const LogitsForward &a, bool f32, bool distill,
-                                  cudaStream_t s) {
-  const int64_t grid = a.rows < (INT64_C(1) << 30) ? a.rows : (INT64_C(1) << 30);
-  const dim3 g(static_cast<unsigned>(grid)), b(kT);
+size_t logprobs_workspace(int64_t rows, int64_t cols, int es) {
+  return static_cast<size_t>(rows) * (8 + 128 * static_cast<size_t>(maxima_steps(cols, es)));
+}
+
+cudaError_t launch_logits_forward(const LogitsForward &a, bool f32, bool distill, int split,
+                                  int sm_count, cudaStream_t s) {
   if (distill)
-    return f32 ? launch_k(logit_rows<true, true>, g, b, 0, s, 0, a)
-               : launch_k(logit_rows<false, true>, g, b, 0, s, 0, a);
-  return f32 ? launch_k(logit_rows<true, false>, g, b, 0, s, 0, a)
-             : launch_k(logit_rows<false, false>, g, b, 0, s, 0, a);
+    return f32 ? launch_forward<true, true, false>(a, split, sm_count, s)
+               : launch_forward<false, true, false>(a, split, sm_count, s);
+  if (a.top > 0)
+    return f32 ? launch_forward<true, false, true>(a, split, sm_count, s)
+               : launch_forward<false, false, true>(a, split, sm_count, s);
+  return f32 ? launch_forward<true, false, false>(a, split, sm_count, s)
+             : launch_forward<false, false, false>(a, split, sm_count, s);
 }
 
 }  // namespace fr

@@ -6,7 +6,7 @@ Bounds.  With u = 2^-24 (half a step of fp32), t = (x - m) log2(e) / T:
     roundings and c = log2(e) / T two more, 4 u |t| of relative error, and where
     the exponential is below 2^-126 it is 0;
   * l and s are sums whose longest chain of additions is 64 + cols / 4096 long
-    (16 per group of vectors, one per group, the merges of 32 lanes and of at most
+    (up to 32 per group of vectors, one per group, the merges of 32 lanes and of at most
     32 warps and 16 CTAs, each of three roundings and one ex2): chain(cols) u + 14 *
     2^-22 relative of the sum of magnitudes.
 So log l is within EPS = (64 + cols / 4096 + 64) u + 2^-18 absolute, which also

@@ -20,7 +20,7 @@ OK_SO_FAR = 8  # every argument accepted: without a device, FR_ERR_NO_DEVICE
 def logprobs(logits=GOOD, token=GOOD, logprob=GOOD, entropy=GOOD, lse=GOOD, tl=GOOD, ti=GOOD,
              top=4, rows=4, cols=8, ld=8, dtype=1, form=0):
     return fr.lib().fr_logprobs(logits, token, logprob, entropy, lse, tl, ti, top, rows, cols, ld,
-                                -100, dtype, form, None)
+                                -100, dtype, form, None, 0, None)
 
 
 def logprobs_backward(logits=GOOD, token=GOOD, dlp=GOOD, dlps=1, dent=GOOD, dents=1,

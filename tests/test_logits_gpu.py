@@ -67,27 +67,29 @@ def entries(rows, cols, top, seed, padding=0.3):
 
 
 def check_logprobs(x, got, t, top, what):
+    """Each output in `got` against its formula."""
     cols = x.shape[1]
     r = ref.logprobs(x, t, top)
     e = ref.eps(cols)
-    m, d, logp, _ = ref.parts(x)
-    size = torch.nan_to_num(m[:, 0].abs(), posinf=0.0)
-    if t is not None:
-        b = e + 4 * ref.U * torch.nan_to_num(r["logprob"].abs(), posinf=0.0)
-        ref.assert_near(got["logprob"], r["logprob"], b, f"{what} logprob")
-    ref.assert_near(got["entropy"], r["entropy"], e * (2 + 2 * math.log(cols)), f"{what} entropy")
-    ref.assert_near(got["lse"], r["lse"], e + 2 * ref.U * (size + math.log(cols)), f"{what} lse")
-    if top:
-        assert torch.equal(got["top_index"].cpu(), r["top_index"]), f"{what} top_index"
-        b = e + 4 * ref.U * torch.nan_to_num(r["top_logprob"].abs(), posinf=0.0)
-        ref.assert_near(got["top_logprob"], r["top_logprob"], b, f"{what} top_logprob")
+    size = torch.nan_to_num(x.double().amax(1).abs(), posinf=0.0)
+    bounds = {
+        "logprob": lambda v: e + 4 * ref.U * torch.nan_to_num(v.abs(), posinf=0.0),
+        "entropy": lambda v: e * (2 + 2 * math.log(cols)),
+        "lse": lambda v: e + 2 * ref.U * (size + math.log(cols)),
+        "top_logprob": lambda v: e + 4 * ref.U * torch.nan_to_num(v.abs(), posinf=0.0),
+    }
+    for k, o in got.items():
+        if k == "top_index":
+            assert torch.equal(o.cpu(), r[k]), f"{what} top_index"
+        else:
+            ref.assert_near(o, r[k], bounds[k](r[k]), f"{what} {k}")
 
 
 def forms(*names):
     return pytest.mark.parametrize("form", names)
 
 
-FORWARD_FORMS = forms("auto")
+FORWARD_FORMS = forms("looped", "split")
 BACKWARD_FORMS = forms("auto")
 
 
@@ -160,17 +162,17 @@ def test_logprobs_special_rows(cols, dtype, form):
 def test_logprobs_outputs_are_optional(form):
     x = logits(9, 3000, "bf16", 5)
     v, t = x.cuda(), tokens(9, 3000, 5)
-    full = fr.fr_logprobs(v, t.cuda(), top=7, form=form)
     only = [dict(token=t.cuda(), want_entropy=False, want_lse=False), dict(want_lse=False),
             dict(want_entropy=False), dict(want_entropy=False, want_lse=False, top=7)]
-    for kw in only:
+    names = [["logprob"], ["entropy"], ["lse"], ["top_index", "top_logprob"]]
+    for kw, name in zip(only, names):
         got = fr.fr_logprobs(v, form=form, **kw)
-        for k, o in got.items():
-            assert torch.equal(o, full[k]), k
+        assert sorted(got) == name
+        check_logprobs(x, got, t, kw.get("top", 0), str(name))
     assert sorted(fr.fr_logprobs(v, top=3)) == ["entropy", "lse", "top_index", "top_logprob"]
 
 
-@FORWARD_FORMS
+@forms("auto", "looped")
 def test_bad_tokens_and_indexes_are_recorded(form):
     x = logits(6, 500, "bf16", 8).cuda()
     t = torch.tensor([0, 500, -1, 499, -100, 1 << 40])
@@ -427,8 +429,9 @@ def test_a_teacher_scores_and_a_student_learns():
     ref.assert_near(step["loss"], rl, loss_bound(sx, rl, i, z, 2.0) + 60 * ref.eps(cols), "loss")
     ref.assert_near(step["dlogits"], rd, ref.gradient_bound(sx, rd, 2 * g, temperature=2.0)
                     + 4 * ref.eps(cols) / rows, "dlogits")
-    assert torch.equal(fr.fr_distill(v, scored["top_index"], scored["top_logprob"], 2.0),
-                       step["loss"])
+    # the forward call sums in another order: each is within its bound of the formula
+    ref.assert_near(fr.fr_distill(v, scored["top_index"], scored["top_logprob"], 2.0), rl,
+                    loss_bound(sx, rl, i, z, 2.0) + 60 * ref.eps(cols), "loss alone")
     # beside fr_xent: its loss, its argmax and its gradient
     x1 = fr.fr_xent(v, t.cuda(), -100, want_argmax=True)
     x2 = fr.fr_xent_backward(v, t.cuda(), torch.ones(1, device="cuda"))
