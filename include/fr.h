@@ -377,8 +377,8 @@ fr_status fr_xent_mean_from_parts(const void *workspace, float *loss_mean, fr_st
  *   top         0 .. min(cols, FR_TOP_MAX); 0: top_logprob and top_index NULL
  *   top_logprob fp32, top_index int64 [rows, top] device outputs
  *   workspace   device scratch of fr_workspace_size(FR_OP_LOGPROBS, ...) bytes,
- *               16-byte aligned; only the looped form with top > 0 uses it (1/64
- *               of a bf16 matrix, 1/128 of an fp32 one); may be NULL otherwise.
+ *               16-byte aligned; only the looped form with top > 0 uses it (about
+ *               1/64 of the logits' bytes); may be NULL otherwise.
  *               One call at a time may use a workspace.
  * At least one output is requested.  Forms: looped (a warp per row) and split (a
  * cluster of up to 8 CTAs per row, for few rows).

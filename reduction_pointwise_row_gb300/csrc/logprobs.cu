@@ -16,8 +16,8 @@
 // logits reach: the k-th largest of the maxima of at least k disjoint groups of
 // the row's logits.  With g groups about g log(g / (g - k)) logits reach it, some
 // more than k.  Only vectors that reach it are read again, for their logits.
-//   looped  the pass over the row writes the maximum of every four vectors of a
-//           lane (128 bytes of logits) to the workspace, 1/64 of a bf16 row, and a
+//   looped  the pass over the row writes the maximum of every 128 bytes of logits
+//           to the workspace, 1/64 of a row, and a
 //           second kernel, a warp per row with little state and so many warps an
 //           SM, does the rest: the groups are every eighth of a lane's maxima; the
 //           vectors under the maxima that reach the floor are read again.  (In
@@ -97,13 +97,14 @@ __host__ __device__ constexpr int64_t maxima_steps(int64_t cols, int es) {
   return (cols * es / kVecBytes + kStep - 1) / kStep;
 }
 
-constexpr int kSegment = 16;        // steps that the second kernel takes together
-constexpr int kCutAt = FR_TOP_MAX;  // a longer list is cut before more is listed
+constexpr int kTopWarps = 4;            // warps per CTA of the second kernel
+constexpr int kSegment = 16;            // steps that it takes together
+constexpr int kCutAt = 2 * FR_TOP_MAX;  // a longer list is cut before more is listed
 
-// A warp's workspace in the second kernel: 5.1 KiB.
+// A warp's workspace in the second kernel: 6.1 KiB.
 struct WarpTop {
   uint16_t hot[kSegment * 64];     // first vectors of the maxima that reach the floor
-  uint16_t vec[64];                // vectors (in the segment) that do
+  uint16_t vec[128];               // vectors (in the segment) that do
   uint64_t list[kCutAt + 32 * 8];  // room for half the logits of 32 bf16 vectors
 };
 
@@ -220,14 +221,15 @@ __device__ __forceinline__ void cut_if_long(WarpTop &w, int k, int most, int &n,
   n = k;
 }
 
-// Lists the logits that pass of vectors b0 + vec[0, count), count <= 32.
+// Lists the logits that pass of the row's vectors b0 + vec[0, count), count <= 32.
 template <bool F32>
 __device__ __forceinline__ void list_vectors(const unsigned char *pv, int head, WarpTop &w, int b0,
-                                             int count, int k, int &n, Floor &floor) {
+                                             const uint16_t *vec, int count, int k, int &n,
+                                             Floor &floor) {
   using L = Logits<F32>;
   const int lane = threadIdx.x & 31;
   const bool have = lane < count;
-  const int vi = b0 + (have ? w.vec[lane] : 0);
+  const int vi = b0 + (have ? vec[lane] : 0);
   const V8 v = have ? ld_keep_v8(pv + static_cast<int64_t>(vi) * kVecBytes) : L::filler();
   const uint32_t index = static_cast<uint32_t>(head + vi * L::EPV);
 #pragma unroll
@@ -271,6 +273,56 @@ __device__ __forceinline__ uint32_t bf16_below(float v) {
   return (u >> 16) + ((u & 0x80000000u) && (u & 0xFFFFu) ? 1 : 0);  // towards -inf
 }
 
+// Writes the maxima of a step's lines (128 bytes of logits: one vector of each of
+// four lanes), rounded down to bf16, as lane 4 g + w's word for vectors 2 w and
+// 2 w + 1 of lanes 4 g .. 4 g + 3; returns the lane's own maximum.  The four lanes
+// exchange in two halving steps, each keeping the half it will write.
+template <bool F32>
+__device__ __forceinline__ float step_maxima(const V8 (&v)[kNV], uint32_t *out) {
+  using L = Logits<F32>;
+  const bool hi2 = threadIdx.x & 2, hi1 = threadIdx.x & 1;
+  if constexpr (F32) {
+    float m[kNV];
+#pragma unroll
+    for (int u = 0; u < kNV; ++u) m[u] = L::max(v[u]);
+    float own = m[0], h[4];
+#pragma unroll
+    for (int u = 1; u < kNV; ++u) own = max_nan(own, m[u]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      h[i] = max_nan(hi2 ? m[4 + i] : m[i],
+                     __shfl_xor_sync(0xffffffffu, hi2 ? m[i] : m[4 + i], 2));
+    float q[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      q[i] = max_nan(hi1 ? h[2 + i] : h[i],
+                     __shfl_xor_sync(0xffffffffu, hi1 ? h[i] : h[2 + i], 1));
+    *out = bf16_below(q[0]) | bf16_below(q[1]) << 16;
+    return own;
+  } else {
+    uint32_t m[4];  // (vector 2 w, vector 2 w + 1), exact: they are bf16
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      uint32_t a = v[2 * w].w[0], b = v[2 * w + 1].w[0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) {
+        a = max_nan_bf16x2(a, v[2 * w].w[j]);
+        b = max_nan_bf16x2(b, v[2 * w + 1].w[j]);
+      }
+      m[w] = max_nan_bf16x2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+    }
+    const uint32_t own = max_nan_bf16x2(max_nan_bf16x2(m[0], m[1]), max_nan_bf16x2(m[2], m[3]));
+    uint32_t h[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      h[i] = max_nan_bf16x2(hi2 ? m[2 + i] : m[i],
+                            __shfl_xor_sync(0xffffffffu, hi2 ? m[i] : m[2 + i], 2));
+    *out = max_nan_bf16x2(hi1 ? h[1] : h[0],
+                          __shfl_xor_sync(0xffffffffu, hi1 ? h[0] : h[1], 1));
+    return max_nan(bf16_lo(own), bf16_hi(own));
+  }
+}
+
 template <bool F32, bool DISTILL, bool TOP>
 __global__ void __launch_bounds__(kT, 2) logit_rows_warp(LogitsForward a) {
   pdl_enter();
@@ -297,15 +349,8 @@ __global__ void __launch_bounds__(kT, 2) logit_rows_warp(LogitsForward a) {
         v[u] = vi < nvec ? ld_stream_v8(pv + static_cast<int64_t>(vi) * kVecBytes) : L::filler();
       }
       float cm;
-      if constexpr (TOP) {
-        const V8 v0[4] = {v[0], v[1], v[2], v[3]}, v1[4] = {v[4], v[5], v[6], v[7]};
-        const float m0 = L::max(v0), m1 = L::max(v1);
-        *maxima = bf16_below(m0) | bf16_below(m1) << 16;
-        maxima += 32;
-        cm = max_nan(m0, m1);
-      } else {
-        cm = L::max(v);
-      }
+      if constexpr (TOP) cm = step_maxima<F32>(v, maxima), maxima += 32;
+      else cm = L::max(v);
       stat_fold<F32, !DISTILL, kNV>(st, v, cm, c);
     }
     if (lane < sp.head) {
@@ -332,13 +377,13 @@ __global__ void __launch_bounds__(kT, 2) logit_rows_warp(LogitsForward a) {
 
 // The alternatives of the rows whose maxima the kernel above wrote: a warp per row.
 template <bool F32>
-__global__ void __launch_bounds__(kT, 4) logit_top_rows(LogitsForward a) {
+__global__ void __launch_bounds__(32 * kTopWarps, 8) logit_top_rows(LogitsForward a) {
   pdl_enter();
   using L = Logits<F32>;
-  __shared__ WarpTop tops[kWarps];
+  __shared__ WarpTop tops[kTopWarps];
   WarpTop &w = tops[threadIdx.x >> 5];
   const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kTopWarps + (threadIdx.x >> 5);
   if (row >= a.rows) return;
   const unsigned char *pr = static_cast<const unsigned char *>(a.logits) + row * a.ld * L::ES;
   const RowSplit sp = row_split(pr, a.cols, L::ES);
@@ -374,7 +419,7 @@ __global__ void __launch_bounds__(kT, 4) logit_top_rows(LogitsForward a) {
     const int b0 = s0 * kStep;  // the segment's first vector
     // the maxima are rounded down, so the floor is too: max >= v makes both >= v's
     const float low = bf16_lo(bf16_below(floor.v));
-    uint32_t mask = 0;  // bit 2 s + h: four vectors of step s0 + s pass
+    uint32_t mask = 0;  // bit 2 s + h: half h of this lane's word of step s0 + s passes
 #pragma unroll 4
     for (int s = 0; s < min(kSegment, steps - s0); ++s) {
       const uint32_t m = maxima[(s0 + s) * 32];
@@ -385,35 +430,42 @@ __global__ void __launch_bounds__(kT, 4) logit_top_rows(LogitsForward a) {
     while (mask != 0) {
       const int bit = __ffs(static_cast<int>(mask)) - 1;
       mask &= mask - 1;
-      w.hot[at++] = static_cast<uint16_t>((bit >> 1) * kStep + (bit & 1) * 128 + lane);
+      // vector 2 (lane % 4) + h of lanes 4 (lane / 4) .. + 3 of the step
+      w.hot[at++] = static_cast<uint16_t>((bit >> 1) * kStep + 32 * (2 * (lane & 3) + (bit & 1)) +
+                                          (lane & ~3));
     }
     __syncwarp();
-    // a lane reads one vector, four lanes a listed maximum
-    for (int i0 = 0; i0 < 4 * total; i0 += 32) {
-      const int i = i0 + lane;
-      const int vec = i < 4 * total ? w.hot[i / 4] + 32 * (i % 4) : nvec;
-      const bool have = b0 + vec < nvec;
-      const V8 v =
-          have ? ld_keep_v8(pv + static_cast<int64_t>(b0 + vec) * kVecBytes) : L::filler();
-      const bool hit = have && floor.passed(L::max(v));
-      const uint32_t hits = __ballot_sync(0xffffffffu, hit);
-      if (hit) w.vec[pending + __popc(hits & ((1u << lane) - 1))] = static_cast<uint16_t>(vec);
-      pending += __popc(hits);
-      __syncwarp();
-      if (pending >= 32) {
-        list_vectors<F32>(pv, sp.head, w, b0, 32, k, n, floor);
-        pending -= 32;
-        const uint16_t rest = w.vec[32 + lane];
-        __syncwarp();
-        w.vec[lane] = rest;
+    // a lane reads one vector, four lanes a listed line; kAhead loads at once
+    constexpr int kAhead = 4;
+    for (int i0 = 0; i0 < 4 * total; i0 += 32 * kAhead) {
+      V8 v[kAhead];
+      int vec[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + 32 * u + lane;
+        vec[u] = i < 4 * total ? w.hot[i / 4] + i % 4 : nvec;
+        v[u] = b0 + vec[u] < nvec
+                   ? ld_keep_v8(pv + static_cast<int64_t>(b0 + vec[u]) * kVecBytes)
+                   : L::filler();
+      }
+      uint32_t hits[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        hits[u] = __ballot_sync(0xffffffffu, b0 + vec[u] < nvec && floor.passed(L::max(v[u])));
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (hits[u] == 0) continue;
+        if ((hits[u] >> lane) & 1)
+          w.vec[pending + __popc(hits[u] & ((1u << lane) - 1))] = static_cast<uint16_t>(vec[u]);
+        pending += __popc(hits[u]);
         __syncwarp();
       }
+      for (int done = 0; done < pending; done += 32)
+        list_vectors<F32>(pv, sp.head, w, b0, w.vec + done, min(32, pending - done), k, n, floor);
+      pending = 0;
     }
-    list_vectors<F32>(pv, sp.head, w, b0, pending, k, n, floor);
-    pending = 0;
-    if (s0 + kSegment < steps) cut_if_long(w, k, k, n, floor);  // the k-th largest so far
   }
-  cut_if_long(w, k, kCutAt, n, floor);
+  cut_if_long(w, k, max(k, 64), n, floor);  // n^2 / 32 comparisons follow
   write_top(a, row, w.list, n, lane, 32, RowStat{stat.x, 0.0f, 0.0f}, stat.y);
 }
 
@@ -646,15 +698,22 @@ cudaError_t launch_forward(const LogitsForward &a, int split, int sm_count, cuda
     const int64_t warps = static_cast<int64_t>(sm_count) * 2 * kWarps;
     const int64_t per_warp = (a.rows + warps - 1) / warps;
     const int64_t grid = (a.rows + per_warp * kWarps - 1) / (per_warp * kWarps);
-    cudaError_t e = launch_k(logit_rows_warp<F32, DISTILL, TOP>,
-                             dim3(static_cast<unsigned>(grid)), block, 0, s, 0, a);
-    if constexpr (TOP) {
+    const dim3 g(static_cast<unsigned>(grid));
+    if constexpr (!TOP) {
+      return launch_k(logit_rows_warp<F32, DISTILL, TOP>, g, block, 0, s, 0, a);
+    } else {
+      // An ordinary launch: placed while the second kernel of the call before is
+      // ending, its CTAs fill the SMs that free up first (bf16 [8192, 50257]: 173
+      // us a call with one alternative, 144 so).
+      logit_rows_warp<F32, DISTILL, TOP><<<g, block, 0, s>>>(a);
+      cudaError_t e = cudaGetLastError();
       if (e != cudaSuccess) return e;
-      e = launch_k(logit_top_rows<F32>, dim3(static_cast<unsigned>((a.rows + kWarps - 1) / kWarps)),
-                   block, 0, s, 0, a);
+      return launch_k(logit_top_rows<F32>,
+                      dim3(static_cast<unsigned>((a.rows + kTopWarps - 1) / kTopWarps)),
+                      dim3(32 * kTopWarps), 0, s, 0, a);
     }
-    return e;
   }
+
   const int64_t most = (INT64_C(1) << 30) / split;
   const int64_t clusters = a.rows < most ? a.rows : most;
   return launch_k(logit_rows_split<F32, DISTILL, TOP>,
