@@ -10,9 +10,8 @@
 // the differences from m taken first, so that a large common offset of a row's
 // logits costs no digits.
 //
-// Top alternatives.  A logit's place in the output is the number of candidates
-// that precede it (larger first, equal ones by index, every NaN largest); what
-// matters is to have few candidates.  Both forms find a floor that at least k
+// Top alternatives.  The order is larger logits first, equal ones by index, every
+// NaN largest; what matters is to sort few candidates.  Both forms find a floor that at least k
 // logits reach: the k-th largest of the maxima of at least k disjoint groups of
 // the row's logits.  With g groups about g log(g / (g - k)) logits reach it, some
 // more than k.  Only vectors that reach it are read again, for their logits.
@@ -56,22 +55,50 @@ __device__ __forceinline__ void write_stats(const LogitsForward &a, int64_t row,
   if (a.lse) a.lse[row] = st.m + logl;
 }
 
-// Candidates list[0, n) to their places among the first k: thread `tid` of
-// `threads` takes every threads-th of them.
-__device__ __forceinline__ void write_top(const LogitsForward &a, int64_t row,
-                                          const uint64_t *list, int n, int tid, int threads,
-                                          const RowStat &st, float logl) {
-  const int k = a.top;
-  for (int i = tid; i < n; i += threads) {
-    const uint64_t mine = list[i];
-    int before = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) before += list[j] > mine;
-    if (before >= k) continue;
-    a.top_index[row * k + before] = place_index(mine);
-    a.top_logprob[row * k + before] =
-        (key_logit(static_cast<uint32_t>(mine >> 32)) - st.m) - logl;
+__device__ __forceinline__ void write_alternative(const LogitsForward &a, int64_t row, int place,
+                                                  uint64_t e, const RowStat &st, float logl) {
+  a.top_index[row * a.top + place] = place_index(e);
+  a.top_logprob[row * a.top + place] =
+      (key_logit(static_cast<uint32_t>(e >> 32)) - st.m) - logl;
+}
+
+// Candidates list[0, n), n <= 32 R, to their places among the first k by one
+// warp: a bitonic sort, entry R lane + i in a lane's register i.
+template <int R>
+__device__ __forceinline__ void sort_top(const LogitsForward &a, int64_t row, const uint64_t *list,
+                                         int n, const RowStat &st, float logl) {
+  const int lane = threadIdx.x & 31;
+  uint64_t e[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) e[i] = R * lane + i < n ? list[R * lane + i] : 0;
+#pragma unroll
+  for (int size = 2; size <= 32 * R; size *= 2) {
+#pragma unroll
+    for (int stride = size / 2; stride > 0; stride /= 2) {
+      if (stride >= R) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const uint64_t o = __shfl_xor_sync(0xffffffffu, e[i], stride / R);
+          const bool down = ((R * lane + i) & size) == 0;  // larger ones to the front
+          const bool low = (lane & (stride / R)) == 0;
+          e[i] = (low == down) == (e[i] > o) ? e[i] : o;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if ((i & stride) == 0) {
+            const bool down = ((R * lane + i) & size) == 0;
+            const uint64_t x = e[i], y = e[i | stride];
+            const bool swap = (x < y) == down;
+            e[i] = swap ? y : x;
+            e[i | stride] = swap ? x : y;
+          }
+      }
+    }
   }
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (R * lane + i < a.top) write_alternative(a, row, R * lane + i, e[i], st, logl);
 }
 
 template <bool F32>
@@ -340,6 +367,11 @@ __global__ void __launch_bounds__(kT, 2) logit_rows_warp(LogitsForward a) {
     if constexpr (TOP)
       maxima = reinterpret_cast<uint32_t *>(static_cast<float2 *>(a.workspace) + a.rows) +
                row * maxima_steps(a.cols, L::ES) * 32 + lane;
+    // loads that nothing waits for before the row's end
+    const float head = lane < sp.head ? L::load(pr, lane) : -INFINITY;
+    const float tail = lane < sp.tail ? L::load(pr, a.cols - sp.tail + lane) : -INFINITY;
+    const int64_t token = !DISTILL && a.logprob ? a.token[row] : -1;
+    float xt = 0.0f;
     RowStat st = stat_empty();
     for (int b = 0; b < nvec; b += kStep) {
       V8 v[kNV];
@@ -353,21 +385,14 @@ __global__ void __launch_bounds__(kT, 2) logit_rows_warp(LogitsForward a) {
       else cm = L::max(v);
       stat_fold<F32, !DISTILL, kNV>(st, v, cm, c);
     }
-    if (lane < sp.head) {
-      const float x = L::load(pr, lane);
-      if (x != -INFINITY) st = stat_merge(st, RowStat{x, 1.0f, 0.0f}, c);
-    }
-    if (lane < sp.tail) {
-      const float x = L::load(pr, a.cols - sp.tail + lane);
-      if (x != -INFINITY) st = stat_merge(st, RowStat{x, 1.0f, 0.0f}, c);
-    }
+    if (!DISTILL && token >= 0 && token < a.cols) xt = L::load(pr, token);
+    if (head != -INFINITY) st = stat_merge(st, RowStat{head, 1.0f, 0.0f}, c);
+    if (tail != -INFINITY) st = stat_merge(st, RowStat{tail, 1.0f, 0.0f}, c);
     st = warp_stat(st, c);
     if constexpr (DISTILL) {
       write_distill<F32>(a, row, pr, st);
     } else if (lane == 0) {
       const float logl = logf(st.l);
-      const int64_t token = a.logprob ? a.token[row] : -1;
-      const float xt = token >= 0 && token < a.cols ? L::load(pr, token) : 0.0f;
       write_stats(a, row, token, xt, st, logl);
       if constexpr (TOP) static_cast<float2 *>(a.workspace)[row] = make_float2(st.m, logl);
     }
@@ -465,8 +490,14 @@ __global__ void __launch_bounds__(32 * kTopWarps, 8) logit_top_rows(LogitsForwar
       pending = 0;
     }
   }
-  cut_if_long(w, k, max(k, 64), n, floor);  // n^2 / 32 comparisons follow
-  write_top(a, row, w.list, n, lane, 32, RowStat{stat.x, 0.0f, 0.0f}, stat.y);
+  const RowStat st{stat.x, 0.0f, 0.0f};
+  if (n <= 32) sort_top<1>(a, row, w.list, n, st, stat.y);
+  else if (n <= 64) sort_top<2>(a, row, w.list, n, st, stat.y);
+  else if (n <= 128) sort_top<4>(a, row, w.list, n, st, stat.y);
+  else {
+    cut_if_long(w, k, kCutAt, n, floor);
+    sort_top<8>(a, row, w.list, n, st, stat.y);
+  }
 }
 
 // ---- split: a cluster of CTAs per row ---------------------------------------------
@@ -491,6 +522,7 @@ struct SplitShared {
   int warp_n[2][kWarps];
   uint64_t count;  // candidates found (may pass kCandidates)
   uint64_t cand[kCandidates];
+  V8 vec[kT];  // a vector of each thread
 };
 
 // The sum of n over the CTA, in every thread.  `buf` alternates between the
@@ -587,7 +619,6 @@ __global__ void __launch_bounds__(kT, TOP ? 3 : 4) logit_rows_split(LogitsForwar
       i1 = i0 + 1;
     }
     const int64_t token = !DISTILL && a.logprob ? a.token[row] : -1;
-    const float xt = token >= 0 && token < a.cols ? L::load(pr, token) : 0.0f;
     RowStat st = stat_empty();
     for (int i = i0; i < i1; i += kT) {
       const float x = L::load(pr, i);
@@ -601,6 +632,7 @@ __global__ void __launch_bounds__(kT, TOP ? 3 : 4) logit_rows_split(LogitsForwar
                                : L::filler();
       stat_fold<F32, !DISTILL, kSplitNV>(st, v, L::max(v), c);
     }
+    const float xt = token >= 0 && token < a.cols ? L::load(pr, token) : 0.0f;
     const float mine = st.m;  // the largest of this thread's logits
     const uint32_t mykey = i0 < i1 || v0 + tid < v1 ? logit_key(mine) : 0;
     if constexpr (TOP) {
@@ -642,14 +674,26 @@ __global__ void __launch_bounds__(kT, TOP ? 3 : 4) logit_rows_split(LogitsForwar
             const float x = L::load(pr, i);
             if (logit_key(x) >= fkey) add_candidate(sh, x, i);
           }
-          for (int b = v0 + tid; b < v1; b += kT) {
-            const V8 v = ld_keep_v8(pv + static_cast<int64_t>(b) * kVecBytes);
-            if (logit_key(L::max(v)) < fkey) continue;
-            const int64_t index = sp.head + int64_t{b} * L::EPV;
-#pragma unroll 1
-            for (int j = 0; j < L::EPV; ++j) {
-              const float x = L::load(pr, index + j);  // from L1
-              if (logit_key(x) >= fkey) add_candidate(sh, x, index + j);
+          // a NaN passes any floor; a floor of NaN is left to the candidates' keys
+          const float fl = fkey == 0 ? -INFINITY : key_logit(fkey);
+          const float floor = fl != fl ? INFINITY : fl;
+          for (int b = v0 + tid; b < v1; b += kT * kSplitNV) {
+            V8 v[kSplitNV];
+#pragma unroll
+            for (int u = 0; u < kSplitNV; ++u)
+              v[u] = b + u * kT < v1 ? ld_keep_v8(pv + static_cast<int64_t>(b + u * kT) * kVecBytes)
+                                     : L::filler();
+#pragma unroll
+            for (int u = 0; u < kSplitNV; ++u) {
+              if (b + u * kT >= v1 || L::max(v[u]) < floor) continue;
+              // the vector by its elements, which a loop cannot pick from registers
+              sh.vec[tid] = v[u];
+              const int64_t index = sp.head + int64_t{b + u * kT} * L::EPV;
+#pragma unroll 4
+              for (int j = 0; j < L::EPV; ++j) {
+                const float x = L::load(&sh.vec[tid], j);
+                if (!(x < floor)) add_candidate(sh, x, index + j);
+              }
             }
           }
         }
@@ -675,7 +719,14 @@ __global__ void __launch_bounds__(kT, TOP ? 3 : 4) logit_rows_split(LogitsForwar
             exact_candidates<F32>(sh, pr, a.cols, a.top, fkey);
             n = a.top;
           }
-          write_top(a, row, sh.cand, n, tid, kT, st, logl);
+          // a candidate's place: the number of candidates before it
+          for (int i = tid; i < n; i += kT) {
+            const uint64_t mine = sh.cand[i];
+            int before = 0;
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) before += sh.cand[j] > mine;
+            if (before < a.top) write_alternative(a, row, before, mine, st, logl);
+          }
         }
       }
     }
