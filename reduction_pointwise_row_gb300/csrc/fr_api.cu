@@ -72,11 +72,12 @@ bool shape_ok(int64_t rows, int64_t cols, int64_t ld, int64_t esize) {
 }
 
 // Rows of p and q (element size esize, leading dimensions lp, lq) share their
-// offset modulo 32 bytes on every row.
-bool same_phase(const void *p, int64_t lp, const void *q, int64_t lq, int64_t esize) {
+// offset modulo 32 (or `modulo`) bytes on every row.
+bool same_phase(const void *p, int64_t lp, const void *q, int64_t lq, int64_t esize,
+                int64_t modulo = 32) {
   const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(p)) -
                     static_cast<int64_t>(reinterpret_cast<uintptr_t>(q));
-  return (d % 32 == 0) && (((lp - lq) * esize) % 32 == 0);
+  return (d % modulo == 0) && (((lp - lq) * esize) % modulo == 0);
 }
 
 fr_status device_ok(fr::DevInfo *info) {
@@ -235,6 +236,22 @@ fr_form pick_forward(int64_t rows, int64_t, int sm_count) {
   return rows >= 8 * static_cast<int64_t>(sm_count) ? FR_FORM_LOOPED : FR_FORM_SPLIT;
 }
 
+// CTAs per row of the gradients' staged form, `least` or more: enough for two
+// buffers of a CTA's run of the row in shared memory (one, where 8 CTAs do not
+// reach that), and for few rows as many as fill the SMs.  0: the row is too long.
+int backward_cluster(int64_t rows, int64_t cols, int es, bool distill, int sm_count, int smem,
+                     int least) {
+  int cluster = least;
+  while (cluster < 8 && !fr::logit_grad_staged_ok(cols, es, cluster, distill, smem / 2)) cluster *= 2;
+  while (cluster < 8 && rows * cluster * 2 <= sm_count && cols * es >= 2 * cluster * 8192) cluster *= 2;
+  return fr::logit_grad_staged_ok(cols, es, cluster, distill, smem) ? cluster : 0;
+}
+
+fr_form pick_backward(int64_t rows, int64_t cols, int es, bool distill, int sm_count, int smem) {
+  const int cluster = backward_cluster(rows, cols, es, distill, sm_count, smem, 1);
+  return cluster == 0 ? FR_FORM_LOOPED : cluster == 1 ? FR_FORM_PERSISTENT : FR_FORM_SPLIT;
+}
+
 }  // namespace
 
 extern "C" {
@@ -276,7 +293,9 @@ fr_form fr_auto_form(fr_op op, fr_dtype dtype, int64_t rows, int64_t cols, int32
     case FR_OP_DISTILL: return pick_forward(rows, cols, sm_count);
     case FR_OP_LOGPROBS_BACKWARD:
     case FR_OP_DISTILL_BACKWARD:
-    case FR_OP_XENT_BACKWARD: return FR_FORM_LOOPED;
+    case FR_OP_XENT_BACKWARD:
+      return pick_backward(rows, cols, dtype == FR_F32 ? 4 : 2, op == FR_OP_DISTILL_BACKWARD,
+                           sm_count, kSm103SmemOptin);
   }
   return FR_FORM_AUTO;
 }
@@ -696,14 +715,25 @@ fr_status run_forward(fr::LogitsForward &a, fr_dtype dtype, bool distill, fr_for
 
 fr_status run_backward(fr::LogitsBackward &a, fr_dtype dtype, bool distill, fr_form form,
                        fr_stream_t stream) {
-  if (form != FR_FORM_AUTO && form != FR_FORM_LOOPED) return FR_ERR_UNSUPPORTED_FORM;
   fr::DevInfo info;
   if (fr_status st = logits_device_ok(a.cols, &info, &a.err)) return st;
   const bool f32 = dtype == FR_F32;
-  const bool vec = same_phase(a.logits, a.ld, a.dlogits, a.ldd, f32 ? 4 : 2);
-  return launched(fr::launch_logits_backward(a, f32, distill, vec,
-                                             reinterpret_cast<cudaStream_t>(stream)),
-                  FR_FORM_LOOPED);
+  const int es = f32 ? 4 : 2;
+  const fr_form f = form == FR_FORM_AUTO
+                        ? pick_backward(a.rows, a.cols, es, distill, info.sm_count,
+                                        info.max_smem_optin)
+                        : form;
+  int cluster = 0;
+  if (f == FR_FORM_PERSISTENT) cluster = 1;
+  else if (f == FR_FORM_SPLIT) cluster = backward_cluster(a.rows, a.cols, es, distill, info.sm_count, info.max_smem_optin, 2);
+  if (f != FR_FORM_LOOPED &&
+      (cluster < 1 || !fr::logit_grad_staged_ok(a.cols, es, cluster, distill, info.max_smem_optin)))
+    return FR_ERR_UNSUPPORTED_FORM;
+  return launched(fr::launch_logits_backward(
+                      a, f32, distill, cluster, same_phase(a.logits, a.ld, a.dlogits, a.ldd, es),
+                      same_phase(a.logits, a.ld, a.dlogits, a.ldd, es, 16), info,
+                      reinterpret_cast<cudaStream_t>(stream)),
+                  f);
 }
 
 }  // namespace

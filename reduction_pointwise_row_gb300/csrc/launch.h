@@ -260,9 +260,12 @@ struct LogitsBackward {
   float temperature;
   int *err;
 };
-// vec: logits and dlogits rows share their offset modulo 32 bytes
-cudaError_t launch_logits_backward(const LogitsBackward &a, bool f32, bool distill, bool vec,
-                                   cudaStream_t s);
+// True when a CTA of a cluster of that many holds its run of a row in shared memory.
+bool logit_grad_staged_ok(int64_t cols, int es, int cluster, bool distill, int max_smem_optin);
+// cluster: 0, the looped form; else CTAs per row of the staged form (1: a row a
+// CTA).  vec32, vec16: logits and dlogits rows share their offset modulo 32, 16 bytes.
+cudaError_t launch_logits_backward(const LogitsBackward &a, bool f32, bool distill, int cluster,
+                                   bool vec32, bool vec16, const DevInfo &info, cudaStream_t s);
 
 // Device address of the current device's error word (kernels record
 // FR_DEVERR_* codes there with atomicCAS; the first code wins).

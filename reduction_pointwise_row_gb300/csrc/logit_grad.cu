@@ -13,14 +13,21 @@
 // the teacher's entries) differ: the row is written without them first, and
 // after a barrier those elements are written again with their term, each from
 // the logit read before the row was written (dlogits may be the logits).
+//
+// What bounds these kernels is the row's bytes, read once and written once.  The
+// staged form keeps the row in shared memory between the two passes (the ring
+// of bulk copies of "Stax (4)", section 9.8, with whole rows as its stages); the
+// looped form streams it twice and relies on L2 for the second time, which
+// misses for about half of it (bf16 [2048, 50257]: 411 MB of DRAM traffic, with
+// 60 MB of the output still in L2, for 412 algorithmic).
 #include "launch.h"
 #include "logits.cuh"
 
 namespace fr {
 namespace {
 
-constexpr int kT = 512;  // threads per CTA
-constexpr int kNV = 2;   // 32-byte vectors a thread loads at once
+constexpr int kT = 512;  // threads per CTA of the looped form
+constexpr int kNV = 2;   // 32-byte vectors a thread folds at once
 
 // An ordinary (coherent) 32-byte load: the row may be written by this kernel.
 __device__ __forceinline__ V8 ld_v8(const void *p) {
@@ -33,31 +40,57 @@ __device__ __forceinline__ V8 ld_v8(const void *p) {
   return v;
 }
 
-// What the row's elements are computed from: dx = e (a + b (x - m)).
+// What the elements of a row are computed from: with t = (x - m) c,
+//   dx = 2^t (a + b max(t, kFar)).
+// 2^t is 0 from kFar down, and the bound keeps b t finite where x is -inf.  Where
+// m c is in range, t is one fused multiply-add, x c - mc, larger than (x - m) c by
+// rest = m c - mc (see stat_fold), which a and b take in.
+constexpr float kFar = -200.0f;
+
 struct RowCoef {
-  float m, a, b;
+  float m, c, mc, a, b;
+  bool fused;
 };
 
-struct GradShared {
-  int64_t idx[FR_TOP_MAX];  // elements written again (-1: none)
-  float val[FR_TOP_MAX];    // what they get
-  float q[FR_TOP_MAX];
-};
+// From the row's statistics: dx = e (a + b (x - m) c) before the correction.
+__device__ __forceinline__ RowCoef row_coef(const RowStat &st, float c, float a, float b) {
+  RowCoef r{st.m, c, st.m * c, a, b, false};
+  r.fused = fabsf(r.mc) <= 1e30f;
+  if (r.fused) {
+    const float rest = fmaf(st.m, c, -r.mc), f = ex2(-rest);
+    r.a = fmaf(-b, rest, a) * f;
+    r.b = b * f;
+  }
+  return r;
+}
+
+// The coefficients of a row with the token's gradient g and the entropy's h.
+__device__ __forceinline__ RowCoef token_coef(const RowStat &st, float c, float g, float h,
+                                              bool has_h) {
+  if (!has_h) return row_coef(st, c, -g / st.l, 0.0f);
+  return row_coef(st, c, (h * (st.s / st.l) - g) / st.l, -h / st.l / c);
+}
+
+template <bool HAS_B>
+__device__ __forceinline__ float grad_scalar(float x, const RowCoef &r) {
+  const float t = r.fused ? fmaf(x, r.c, -r.mc) : (x - r.m) * r.c;
+  return ex2(t) * (HAS_B ? fmaf(r.b, fmaxf(t, kFar), r.a) : r.a);
+}
 
 template <bool F32, bool HAS_B>
-__device__ __forceinline__ V8 grad_vector(const V8 &x, const RowCoef &r, float c) {
+__device__ __forceinline__ V8 grad_vector(const V8 &x, const RowCoef &r) {
   using L = Logits<F32>;
-  const uint64_t m2 = pack_f32x2(r.m, r.m), c2 = pack_f32x2(c, c), a2 = pack_f32x2(r.a, r.a);
+  const uint64_t c2 = pack_f32x2(r.c, r.c), a2 = pack_f32x2(r.a, r.a), b2 = pack_f32x2(r.b, r.b);
+  const uint64_t nmc2 = pack_f32x2(-r.mc, -r.mc), m2 = pack_f32x2(r.m, r.m);
   V8 o;
 #pragma unroll
   for (int j = 0; j < L::EPV / 2; ++j) {
-    const uint64_t d = sub_f32x2(pack_f32x2(L::at(x, 2 * j), L::at(x, 2 * j + 1)), m2);
-    const uint64_t t = mul_f32x2(d, c2);
+    const uint64_t v = pack_f32x2(L::at(x, 2 * j), L::at(x, 2 * j + 1));
+    const uint64_t t = r.fused ? fma_f32x2(v, c2, nmc2) : mul_f32x2(sub_f32x2(v, m2), c2);
     const uint64_t e = pack_f32x2(ex2(f32x2_lo(t)), ex2(f32x2_hi(t)));
     uint64_t f = a2;
     if constexpr (HAS_B)
-      f = fma_f32x2(pack_f32x2(r.b, r.b), pack_f32x2(fmaxf(f32x2_lo(d), kFarBelow),
-                                                     fmaxf(f32x2_hi(d), kFarBelow)), a2);
+      f = fma_f32x2(b2, pack_f32x2(fmaxf(f32x2_lo(t), kFar), fmaxf(f32x2_hi(t), kFar)), a2);
     const uint64_t y = mul_f32x2(e, f);
     if constexpr (F32) {
       o.w[2 * j] = __float_as_uint(f32x2_lo(y));
@@ -69,22 +102,70 @@ __device__ __forceinline__ V8 grad_vector(const V8 &x, const RowCoef &r, float c
   return o;
 }
 
-template <bool HAS_B>
-__device__ __forceinline__ float grad_scalar(float x, const RowCoef &r, float c) {
-  const float d = x - r.m;
-  return ex2(d * c) * (HAS_B ? fmaf(r.b, fmaxf(d, kFarBelow), r.a) : r.a);
-}
-
 // A row's gradient is all zeros (an ignored row, a row without teacher) or all
 // NaN (a target past the row) before anything is read of it.
 enum RowKind { kRowGrad = 0, kRowZero = 1, kRowNan = 2 };
 
+// What a token makes of its row.  LOGITS only: an entropy's gradient is left.
+template <bool HAS_B>
+__device__ __forceinline__ int token_kind(const LogitsBackward &a, int64_t token) {
+  if (!a.token) return kRowGrad;
+  if (token == a.ignore_index) return HAS_B ? kRowGrad : kRowZero;
+  return token < 0 || token >= a.cols ? kRowNan : kRowGrad;
+}
+
+// A row's teacher entries in shared memory, by one warp.
+struct TeacherShared {
+  int32_t idx[FR_TOP_MAX];  // -1: no weight
+  float q[FR_TOP_MAX], logq[FR_TOP_MAX], x[FR_TOP_MAX];
+  float sum[FR_TOP_MAX];  // the weights of all entries that name idx
+};
+
+__device__ __forceinline__ void teacher_share(const Teacher &t, int top, TeacherShared &sh) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < kTopPerLane; ++i) {
+    const int e = lane + 32 * i;
+    sh.idx[e] = t.q[i] != 0.0f ? static_cast<int32_t>(t.idx[i]) : -1;
+    sh.q[e] = t.q[i];
+    sh.logq[e] = t.logq[i];
+    sh.x[e] = t.x[i];
+  }
+  __syncwarp();
+  for (int e = lane; e < top; e += 32) {
+    const int32_t j = sh.idx[e];
+    float sum = 0.0f;  // in the entries' order
+    for (int n = 0; n < top; ++n) sum += sh.idx[n] == j ? sh.q[n] : 0.0f;
+    sh.sum[e] = sum;
+  }
+  __syncwarp();
+}
+
+// The row's loss from its shared entries, in every lane of one warp.
+__device__ __forceinline__ float teacher_loss(const TeacherShared &sh, int top, const RowStat &st,
+                                              float temperature) {
+  const float logl = logf(st.l);
+  float sum = 0.0f;
+  for (int e = threadIdx.x & 31; e < top; e += 32)
+    if (sh.idx[e] >= 0)
+      sum += sh.q[e] * (sh.logq[e] - ((sh.x[e] - st.m) / temperature - logl));
+  return temperature * temperature * warp_sum(sum);
+}
+
+// Entry e's element: g (p - sum of its weights).
+__device__ __forceinline__ float teacher_element(const TeacherShared &sh, int e, const RowStat &st,
+                                                 float c, float g) {
+  return g * (ex2((sh.x[e] - st.m) * c) / st.l - sh.sum[e]);
+}
+
+// ---- looped: a CTA per row, the row streamed twice ---------------------------------
+
 template <bool F32, bool DISTILL, bool HAS_B, bool VEC>
-__global__ void __launch_bounds__(kT) logit_grad_looped(LogitsBackward a) {
+__global__ void __launch_bounds__(kT, 2) logit_grad_looped(LogitsBackward a) {
   pdl_enter();
   using L = Logits<F32>;
   __shared__ RowStat red[kT / 32];
-  __shared__ GradShared sh;
+  __shared__ TeacherShared sh[1];
   __shared__ int kind_s;
   const int tid = threadIdx.x;
   const float c = DISTILL ? kLog2e / a.temperature : kLog2e;
@@ -95,41 +176,34 @@ __global__ void __launch_bounds__(kT) logit_grad_looped(LogitsBackward a) {
     const RowSplit sp = row_split(pr, a.cols, L::ES);
     const int64_t vo = static_cast<int64_t>(sp.head) * L::ES;
 
-    Teacher t;
     int64_t token = -1;
     float xt = 0.0f, g = 0.0f, h = 0.0f;
-    bool ignored = false;
     if constexpr (DISTILL) {
       if (tid < 32) {
-        t = teacher_load<F32>(a.index + row * a.ldt, a.teacher + row * a.ldt, a.top, pr, a.cols,
-                              a.temperature);
+        const Teacher t = teacher_load<F32>(a.index + row * a.ldt, a.teacher + row * a.ldt, a.top,
+                                            pr, a.cols, a.temperature);
+        teacher_share(t, a.top, sh[0]);
         if (tid == 0) {
           kind_s = t.bad ? kRowNan : t.any ? kRowGrad : kRowZero;
           if (t.bad) atomicCAS(a.err, 0, FR_DEVERR_BAD_TARGET);
         }
       }
       g = a.dloss[row * a.dloss_stride] * a.temperature;
+      __syncthreads();
     } else {
-      if (a.token) {
-        token = a.token[row];
-        ignored = token == a.ignore_index;
-        const bool bad = !ignored && (token < 0 || token >= a.cols);
-        if (tid == 0) {
-          kind_s = bad ? kRowNan : ignored && !HAS_B ? kRowZero : kRowGrad;
-          if (bad) atomicCAS(a.err, 0, FR_DEVERR_BAD_TARGET);
-        }
-        if (!ignored && !bad) {
-          xt = L::load(pr, token);
-          g = a.dloss[row * a.dloss_stride] * a.dloss_sign;
-        } else {
-          token = -1;
-        }
-      } else if (tid == 0) {
-        kind_s = kRowGrad;
+      if (a.token) token = a.token[row];
+      if (tid == 0) kind_s = token_kind<HAS_B>(a, token);
+      __syncthreads();
+      if (a.token && (kind_s != kRowGrad || token == a.ignore_index)) {
+        if (kind_s == kRowNan && tid == 0) atomicCAS(a.err, 0, FR_DEVERR_BAD_TARGET);
+        token = -1;
+      }
+      if (token >= 0) {
+        xt = L::load(pr, token);
+        g = a.dloss[row * a.dloss_stride] * a.dloss_sign;
       }
       if constexpr (HAS_B) h = a.dentropy[row * a.dentropy_stride];
     }
-    __syncthreads();
     const int kind = kind_s;
 
     if (kind != kRowGrad) {
@@ -156,77 +230,394 @@ __global__ void __launch_bounds__(kT) logit_grad_looped(LogitsBackward a) {
     }
     st = block_stat<kT>(st, c, red);
 
-    RowCoef r;
-    r.m = st.m;
-    r.b = HAS_B ? -h / st.l : 0.0f;
-    if constexpr (DISTILL) r.a = g / st.l;
-    else r.a = HAS_B ? (h * (st.s / st.l) - g) / st.l : -g / st.l;
-
-    // the elements with a term of their own, before the row is overwritten
+    const RowCoef r = DISTILL ? row_coef(st, c, g / st.l, 0.0f) : token_coef(st, c, g, h, HAS_B);
     if constexpr (DISTILL) {
-      if (tid < 32) {
-#pragma unroll
-        for (int i = 0; i < kTopPerLane; ++i) {
-          sh.idx[tid + 32 * i] = t.q[i] != 0.0f ? t.idx[i] : -1;
-          sh.q[tid + 32 * i] = t.q[i];
-        }
-        __syncwarp();
-        const float loss = teacher_loss(t, st, a.temperature);
-        if (a.loss && tid == 0) a.loss[row] = loss;
-#pragma unroll
-        for (int i = 0; i < kTopPerLane; ++i) {
-          const int64_t j = sh.idx[tid + 32 * i];
-          if (j < 0) continue;
-          float q = 0.0f;  // entries that name j, in their order
-          for (int n = 0; n < a.top; ++n)
-            if (sh.idx[n] == j) q += sh.q[n];
-          sh.val[tid + 32 * i] = g * (ex2((t.x[i] - st.m) * c) / st.l - q);
-        }
+      if (a.loss && tid < 32) {
+        const float loss = teacher_loss(sh[0], a.top, st, a.temperature);
+        if (tid == 0) a.loss[row] = loss;
       }
     } else if (a.loss && tid == 0) {
       a.loss[row] = logf(st.l) - (xt - st.m);
     }
     // in place, every element is read by the thread that writes it
     if constexpr (VEC) {
-      if (si >= 0) L::store(po, si, grad_scalar<HAS_B>(L::load(pr, si), r, c));
+      if (si >= 0) L::store(po, si, grad_scalar<HAS_B>(L::load(pr, si), r));
       for (int64_t b = tid; b < sp.nvec; b += kT) {
         const V8 x = ld_v8(pr + vo + b * kVecBytes);
-        st_stream_v8(po + vo + b * kVecBytes, grad_vector<F32, HAS_B>(x, r, c));
+        st_stream_v8(po + vo + b * kVecBytes, grad_vector<F32, HAS_B>(x, r));
       }
     } else {
       for (int64_t j = tid; j < a.cols; j += kT)
-        L::store(po, j, grad_scalar<HAS_B>(L::load(pr, j), r, c));
+        L::store(po, j, grad_scalar<HAS_B>(L::load(pr, j), r));
     }
     __syncthreads();
     if constexpr (DISTILL) {
-      if (tid < a.top && sh.idx[tid] >= 0) L::store(po, sh.idx[tid], sh.val[tid]);
+      if (tid < a.top && sh[0].idx[tid] >= 0)
+        L::store(po, sh[0].idx[tid], teacher_element(sh[0], tid, st, c, g));
     } else if (tid == 0 && token >= 0) {
-      L::store(po, token, grad_scalar<HAS_B>(xt, r, c) + g);
+      L::store(po, token, grad_scalar<HAS_B>(xt, r) + g);
     }
     __syncthreads();
   }
 }
 
+// ---- staged: rows (or a cluster's runs of them) in a ring of bulk copies --------------
+//
+// A persistent grid of clusters of C CTAs; a cluster takes rows c, c + clusters, ...
+// CTA q of C holds the row's 16-byte units [n q / C, n (q + 1) / C) in one of the
+// `nbuf` buffers of its ring.  All warps but the last fold the run's units into the
+// statistics and, after the CTA's (and the cluster's) merge, write the gradient
+// from shared memory while the next rows' copies are in flight.  The last warp
+// keeps them supplied: it issues the copies, reads the next row's token, upstream
+// gradients, ragged ends and teacher entries a row ahead, writes the loss, and
+// after the row's last barrier the elements with a term of their own.
+
+constexpr int kMaxBufs = 4;
+constexpr int kMaxThreads = 832;  // 72 registers a thread
+constexpr long long kWaitBudget = 1LL << 31;  // SM clocks, about one second
+
+struct RowParams {
+  int kind;
+  float g, h;
+};
+
+template <bool DISTILL>
+struct StagedShared {
+  uint64_t full[kMaxBufs];
+  RowStat red[2][kMaxThreads / 32];
+  float4 part[2];  // this CTA's statistics, for the cluster
+  RowParams par[2];
+  TeacherShared teacher[DISTILL ? 2 : 1];
+  int dead;  // a wait ran out: nothing more is copied or waited for
+};
+
+struct UnitGeom {
+  int head, tail;   // scalars before and after the units
+  int u0, u1;       // this CTA's 16-byte units
+  int64_t first;    // the first unit's byte offset in the row
+};
+
+template <int ES>
+__device__ __forceinline__ UnitGeom unit_geom(const unsigned char *pr, int64_t cols, int q,
+                                              int C) {
+  const uint64_t s0 = reinterpret_cast<uint64_t>(pr), s1 = s0 + cols * ES;
+  const uint64_t a0 = (s0 + 15) & ~uint64_t{15}, a1 = s1 & ~uint64_t{15};
+  UnitGeom g;
+  if (a1 <= a0) {  // fewer than 32 bytes: all scalars
+    g.head = static_cast<int>(cols);
+    g.tail = g.u0 = g.u1 = 0;
+    g.first = 0;
+    return g;
+  }
+  const int64_t n = static_cast<int64_t>((a1 - a0) / 16);
+  g.head = static_cast<int>((a0 - s0) / ES);
+  g.tail = static_cast<int>((s1 - a1) / ES);
+  g.first = static_cast<int64_t>(a0 - s0);
+  g.u0 = static_cast<int>(n * q / C);
+  g.u1 = static_cast<int>(n * (q + 1) / C);
+  return g;
+}
+
+// Units i and i + step of the n at `buf` as one vector; -inf past the end.
+template <bool F32>
+__device__ __forceinline__ V8 lds_units(const unsigned char *buf, int i, int step, int n) {
+  V8 v = Logits<F32>::filler();
+  if (i < n) {
+    const uint4 x = lds_u4(buf + 16 * i);
+    v.w[0] = x.x, v.w[1] = x.y, v.w[2] = x.z, v.w[3] = x.w;
+  }
+  if (i + step < n) {
+    const uint4 x = lds_u4(buf + 16 * (i + step));
+    v.w[4] = x.x, v.w[5] = x.y, v.w[6] = x.z, v.w[7] = x.w;
+  }
+  return v;
+}
+
+template <bool F32, bool DISTILL, bool HAS_B, bool VEC>
+__global__ void __launch_bounds__(kMaxThreads, 1)
+logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf) {
+  pdl_enter();
+  using L = Logits<F32>;
+  constexpr int EPU = 16 / L::ES;  // logits per unit
+  extern __shared__ __align__(128) unsigned char bufs[];  // [nbuf][buf_bytes]
+  __shared__ StagedShared<DISTILL> sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int workers = static_cast<int>(blockDim.x) - 32, helper = workers >> 5;  // the last warp
+  const int C = static_cast<int>(cluster_nctarank()), q = static_cast<int>(cluster_ctarank());
+  const int64_t row0 = cluster_id_x(), stride = ncluster_x();
+  const float c = DISTILL ? kLog2e / a.temperature : kLog2e;
+  const float nan = __int_as_float(0x7fc00000);
+  const unsigned char *logits = static_cast<const unsigned char *>(a.logits);
+  if (tid == 0) {
+    for (int b = 0; b < nbuf; ++b) mbar_init(&sh.full[b], 1);
+    mbar_init_fence();
+    sh.dead = 0;
+  }
+  __syncthreads();
+
+  // ---- the helper's parts
+  uint64_t policy = 0;
+  uint32_t issued = 0;  // bit b: parity of buffer b's last copy, set + 1
+  uint32_t ever = 0;
+  auto issue = [&](int64_t row, int b) {  // one lane
+    const unsigned char *pr = logits + row * a.ld * L::ES;
+    const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, C);
+    const uint32_t bytes = 16u * static_cast<uint32_t>(g.u1 - g.u0);
+    if (bytes == 0) return;
+    fence_proxy_async_smem();
+    mbar_arrive_expect_tx(&sh.full[b], bytes);
+    bulk_copy_g2s(bufs + static_cast<size_t>(b) * buf_bytes,
+                  pr + g.first + 16 * static_cast<int64_t>(g.u0), bytes, &sh.full[b], policy);
+    issued ^= 1u << b;
+    ever |= 1u << b;
+  };
+  auto token_of = [&](int64_t row) -> int64_t {
+    return !DISTILL && a.token && row < a.rows ? a.token[row] : -1;
+  };
+  auto wanted = [&](int64_t token) { return DISTILL || token_kind<HAS_B>(a, token) == kRowGrad; };
+  // the next row's parameters, in the helper's registers until it is its turn
+  int64_t tok = -1;
+  float xt = 0.0f, head = -INFINITY, tail = -INFINITY;
+  auto prepare = [&](int64_t row, int64_t token, int slot) {  // the whole warp
+    const unsigned char *pr = logits + row * a.ld * L::ES;
+    const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, C);
+    RowParams p{kRowGrad, 0.0f, 0.0f};
+    head = q == 0 && lane < g.head ? L::load(pr, lane) : -INFINITY;
+    tail = q == C - 1 && lane < g.tail ? L::load(pr, a.cols - g.tail + lane) : -INFINITY;
+    if constexpr (DISTILL) {
+      p.g = a.dloss[row * a.dloss_stride] * a.temperature;
+      const Teacher t = teacher_load<F32>(a.index + row * a.ldt, a.teacher + row * a.ldt, a.top,
+                                          pr, a.cols, a.temperature);
+      p.kind = t.bad ? kRowNan : t.any ? kRowGrad : kRowZero;
+      teacher_share(t, a.top, sh.teacher[slot]);
+    } else {
+      p.kind = token_kind<HAS_B>(a, token);
+      tok = p.kind == kRowGrad && a.token && token != a.ignore_index ? token : -1;
+      if (tok >= 0) {
+        xt = L::load(pr, tok);
+        p.g = a.dloss[row * a.dloss_stride] * a.dloss_sign;
+      }
+      if constexpr (HAS_B) p.h = a.dentropy[row * a.dentropy_stride];
+    }
+    if (lane == 0) {
+      sh.par[slot] = p;
+      if (p.kind == kRowNan) atomicCAS(a.err, 0, FR_DEVERR_BAD_TARGET);
+    }
+  };
+  if (warp == helper) {
+    policy = l2_evict_first_policy();
+    for (int b = 0; b < nbuf; ++b) {
+      const int64_t row = row0 + b * stride;
+      if (row < a.rows && wanted(token_of(row)) && lane == 0) issue(row, b);
+    }
+    if (row0 < a.rows) prepare(row0, token_of(row0), 0);
+  }
+  __syncthreads();
+
+  uint32_t phases = 0;  // bit b: parity that the next wait on buffer b takes
+  bool ok = true;
+  int b = 0;
+  for (int64_t row = row0, k = 0; row < a.rows; row += stride, ++k, b = b + 1 == nbuf ? 0 : b + 1) {
+    const int slot = static_cast<int>(k & 1);
+    const unsigned char *pr = logits + row * a.ld * L::ES;
+    unsigned char *po = static_cast<unsigned char *>(a.dlogits) + row * a.ldd * L::ES;
+    const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, C);
+    const int n = g.u1 - g.u0;
+    const unsigned char *buf = bufs + static_cast<size_t>(b) * buf_bytes;
+    const RowParams par = sh.par[slot];
+    const bool copied = n > 0 && (DISTILL || par.kind == kRowGrad);
+    const int64_t next_token = warp == helper ? token_of(row + stride) : -1;
+    const int64_t refill_token = warp == helper ? token_of(row + nbuf * stride) : -1;
+
+    RowStat st = stat_empty();
+    if (warp != helper) {
+      if (copied) {
+        if (ok && !mbar_wait_bounded(&sh.full[b], (phases >> b) & 1, kWaitBudget)) {
+          ok = false;
+          sh.dead = 1;
+          atomicCAS(a.err, 0, FR_DEVERR_TIMEOUT);
+        }
+        phases ^= 1u << b;
+      }
+      if (par.kind == kRowGrad) {
+        for (int i = tid; i < n; i += 4 * workers) {
+          const V8 v[2] = {lds_units<F32>(buf, i, workers, n),
+                           lds_units<F32>(buf, i + 2 * workers, workers, n)};
+          stat_fold<F32, HAS_B, 2>(st, v, L::max(v), c);
+        }
+      }
+    } else {
+      if (head != -INFINITY) st = stat_merge(st, RowStat{head, 1.0f, 0.0f}, c);
+      if (tail != -INFINITY) st = stat_merge(st, RowStat{tail, 1.0f, 0.0f}, c);
+    }
+    st = warp_stat(st, c);
+    if (lane == 0) sh.red[slot][warp] = st;
+    __syncthreads();
+    if (par.kind == kRowGrad) {
+      st = warp_stat(lane <= helper ? sh.red[slot][lane] : stat_empty(), c);
+      if (C > 1) {
+        if (tid == 0) sh.part[slot] = make_float4(st.m, st.l, st.s, 0.0f);
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        const float4 o = lane < C ? ld_dsmem_f4(&sh.part[slot], lane)
+                                  : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+        st = warp_stat(RowStat{o.x, o.y, o.z}, c);
+      }
+    }
+    const RowCoef r = DISTILL ? row_coef(st, c, par.g / st.l, 0.0f)
+                              : token_coef(st, c, par.g, par.h, HAS_B);
+    const int64_t out0 = g.first + 16 * static_cast<int64_t>(g.u0);  // bytes into the row
+    if (warp != helper) {
+      if (par.kind == kRowGrad && VEC) {
+        for (int i = tid; i < n; i += 2 * workers) {
+          const V8 y = grad_vector<F32, HAS_B>(lds_units<F32>(buf, i, workers, n), r);
+          st_stream_u4(po + out0 + 16 * static_cast<int64_t>(i),
+                       make_uint4(y.w[0], y.w[1], y.w[2], y.w[3]));
+          if (i + workers < n)
+            st_stream_u4(po + out0 + 16 * static_cast<int64_t>(i + workers),
+                         make_uint4(y.w[4], y.w[5], y.w[6], y.w[7]));
+        }
+      } else if (VEC) {
+        const uint32_t w = par.kind == kRowNan ? (F32 ? 0x7FC00000u : 0x7FC07FC0u) : 0;
+        for (int i = tid; i < n; i += workers)
+          st_stream_u4(po + out0 + 16 * static_cast<int64_t>(i), make_uint4(w, w, w, w));
+      } else {
+        const int64_t e0 = out0 / L::ES;
+        for (int j = tid; j < n * EPU; j += workers)
+          L::store(po, e0 + j,
+                   par.kind == kRowGrad ? grad_scalar<HAS_B>(L::load(buf, j), r)
+                                        : par.kind == kRowNan ? nan : 0.0f);
+      }
+    } else {
+      if (q == 0 && lane < g.head)
+        L::store(po, lane, par.kind == kRowGrad ? grad_scalar<HAS_B>(head, r)
+                                                : par.kind == kRowNan ? nan : 0.0f);
+      if (q == C - 1 && lane < g.tail)
+        L::store(po, a.cols - g.tail + lane, par.kind == kRowGrad ? grad_scalar<HAS_B>(tail, r)
+                                                                  : par.kind == kRowNan ? nan : 0.0f);
+      if (a.loss && q == 0) {
+        float loss = par.kind == kRowNan ? nan : 0.0f;
+        if (par.kind == kRowGrad) {
+          if constexpr (DISTILL) loss = teacher_loss(sh.teacher[slot], a.top, st, a.temperature);
+          else if (tok >= 0) loss = logf(st.l) - (xt - st.m);
+        }
+        if (lane == 0) a.loss[row] = loss;
+      }
+    }
+    // this row's elements with a term of their own, and the next row's parameters
+    const int64_t own_tok = tok;
+    const float own_value = !DISTILL && tok >= 0 ? grad_scalar<HAS_B>(xt, r) + par.g : 0.0f;
+    if (warp == helper && row + stride < a.rows) prepare(row + stride, next_token, slot ^ 1);
+    __syncthreads();
+    if (warp == helper) {
+      // element j is written here if this CTA wrote it above
+      const int64_t lo = q == 0 ? 0 : out0 / L::ES;
+      const int64_t hi = q == C - 1 ? a.cols : (g.first + 16 * static_cast<int64_t>(g.u1)) / L::ES;
+      if constexpr (DISTILL) {
+        const TeacherShared &t = sh.teacher[slot];
+        if (par.kind == kRowGrad)
+          for (int e = lane; e < a.top; e += 32)
+            if (t.idx[e] >= lo && t.idx[e] < hi)
+              L::store(po, t.idx[e], teacher_element(t, e, st, c, par.g));
+      } else if (lane == 0 && own_tok >= lo && own_tok < hi) {
+        L::store(po, own_tok, own_value);
+      }
+      const int64_t refill = row + nbuf * stride;
+      if (refill < a.rows && wanted(refill_token) && lane == 0 &&
+          *reinterpret_cast<volatile int *>(&sh.dead) == 0)
+        issue(refill, b);
+      __syncwarp();
+    }
+  }
+  if (warp == helper && lane == 0 && *reinterpret_cast<volatile int *>(&sh.dead) != 0)
+    for (int i = 0; i < nbuf; ++i)  // copies in flight may not outlive the CTA
+      if ((ever >> i) & 1) mbar_wait_bounded(&sh.full[i], ((issued >> i) & 1) ^ 1, kWaitBudget);
+  if (C > 1) {  // no CTA's statistics are given up while a peer reads them
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  }
+}
+
+// Bytes of a CTA's run of a row, for any offset of the row.
+int64_t staged_buf_bytes(int64_t cols, int es, int cluster) {
+  const int64_t units = cols * es / 16;
+  return ((units + cluster - 1) / cluster * 16 + 127) / 128 * 128;
+}
+
+// Shared memory left for the ring of one CTA.
+int64_t staged_smem(bool distill, int max_smem_optin) {
+  return max_smem_optin -
+         static_cast<int64_t>(distill ? sizeof(StagedShared<true>) : sizeof(StagedShared<false>));
+}
+
+struct StagedShape {
+  int threads, nbuf;
+  uint32_t buf_bytes;
+};
+
+// Threads for about 8 units (64 bf16 logits) each, in whole fours of units; as
+// many CTAs an SM as their registers and two buffers each leave room for, and up to four buffers where the room is there.
+StagedShape staged_shape(int64_t cols, int es, int cluster, bool distill, const DevInfo &info) {
+  StagedShape sh;
+  sh.buf_bytes = static_cast<uint32_t>(staged_buf_bytes(cols, es, cluster));
+  const int64_t units = sh.buf_bytes / 16;
+  int64_t workers = (units / 8 + 31) / 32 * 32;
+  workers = workers < 64 ? 64 : workers > kMaxThreads - 32 ? kMaxThreads - 32 : workers;
+  sh.threads = static_cast<int>(workers) + 32;
+  const int64_t room = staged_smem(distill, info.max_smem_optin);
+  int64_t ctas = (kMaxThreads + 64) / sh.threads;
+  const int64_t other = info.max_smem_optin - room + 1024;
+  while (ctas > 1 && ctas * (2 * sh.buf_bytes + other) > info.max_smem_optin) --ctas;
+  int64_t nbuf = ((info.max_smem_optin + 1024) / ctas - other) / (sh.buf_bytes > 0 ? sh.buf_bytes : 1);
+  sh.nbuf = static_cast<int>(nbuf < 1 ? 1 : nbuf > kMaxBufs ? kMaxBufs : nbuf);
+  return sh;
+}
+
 template <bool F32, bool DISTILL, bool HAS_B>
-cudaError_t launch_looped(const LogitsBackward &a, bool vec, cudaStream_t s) {
-  const int64_t grid = a.rows < (INT64_C(1) << 30) ? a.rows : (INT64_C(1) << 30);
-  const dim3 g(static_cast<unsigned>(grid)), b(kT);
-  return vec ? launch_k(logit_grad_looped<F32, DISTILL, HAS_B, true>, g, b, 0, s, 0, a)
-             : launch_k(logit_grad_looped<F32, DISTILL, HAS_B, false>, g, b, 0, s, 0, a);
+cudaError_t launch_form(const LogitsBackward &a, int cluster, bool vec32, bool vec16,
+                        const DevInfo &info, cudaStream_t s) {
+  if (cluster == 0) {
+    const int64_t grid = a.rows < (INT64_C(1) << 30) ? a.rows : (INT64_C(1) << 30);
+    const dim3 g(static_cast<unsigned>(grid)), b(kT);
+    return vec32 ? launch_k(logit_grad_looped<F32, DISTILL, HAS_B, true>, g, b, 0, s, 0, a)
+                 : launch_k(logit_grad_looped<F32, DISTILL, HAS_B, false>, g, b, 0, s, 0, a);
+  }
+  auto *kern = vec16 ? &logit_grad_staged<F32, DISTILL, HAS_B, true>
+                     : &logit_grad_staged<F32, DISTILL, HAS_B, false>;
+  const StagedShape sh = staged_shape(a.cols, F32 ? 4 : 2, cluster, DISTILL, info);
+  const size_t smem = static_cast<size_t>(sh.buf_bytes) * sh.nbuf;
+  cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kern), smem);
+  if (e != cudaSuccess) return e;
+  int per_sm = 0;
+  if ((e = blocks_per_sm(&per_sm, reinterpret_cast<const void *>(kern), sh.threads, smem)) !=
+      cudaSuccess)
+    return e;
+  if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  int64_t clusters = static_cast<int64_t>(per_sm) * info.sm_count / cluster;
+  if (clusters < 1) clusters = 1;
+  if (clusters > a.rows) clusters = a.rows;
+  return launch_k(kern, dim3(static_cast<unsigned>(clusters * cluster)), dim3(sh.threads), smem,
+                  s, cluster, a, sh.buf_bytes, sh.nbuf);
 }
 
 }  // namespace
 
-cudaError_t launch_logits_backward(const LogitsBackward &a, bool f32, bool distill, bool vec,
-                                   cudaStream_t s) {
+bool logit_grad_staged_ok(int64_t cols, int es, int cluster, bool distill, int max_smem_optin) {
+  return staged_buf_bytes(cols, es, cluster) <= staged_smem(distill, max_smem_optin);
+}
+
+cudaError_t launch_logits_backward(const LogitsBackward &a, bool f32, bool distill, int cluster,
+                                   bool vec32, bool vec16, const DevInfo &info, cudaStream_t s) {
   if (distill)
-    return f32 ? launch_looped<true, true, false>(a, vec, s)
-               : launch_looped<false, true, false>(a, vec, s);
+    return f32 ? launch_form<true, true, false>(a, cluster, vec32, vec16, info, s)
+               : launch_form<false, true, false>(a, cluster, vec32, vec16, info, s);
   if (a.dentropy)
-    return f32 ? launch_looped<true, false, true>(a, vec, s)
-               : launch_looped<false, false, true>(a, vec, s);
-  return f32 ? launch_looped<true, false, false>(a, vec, s)
-             : launch_looped<false, false, false>(a, vec, s);
+    return f32 ? launch_form<true, false, true>(a, cluster, vec32, vec16, info, s)
+               : launch_form<false, false, true>(a, cluster, vec32, vec16, info, s);
+  return f32 ? launch_form<true, false, false>(a, cluster, vec32, vec16, info, s)
+             : launch_form<false, false, false>(a, cluster, vec32, vec16, info, s);
 }
 
 }  // namespace fr

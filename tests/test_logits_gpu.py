@@ -90,7 +90,7 @@ def forms(*names):
 
 
 FORWARD_FORMS = forms("looped", "split")
-BACKWARD_FORMS = forms("auto")
+BACKWARD_FORMS = forms("looped", "persistent", "split")
 
 
 @FORWARD_FORMS
@@ -237,6 +237,8 @@ def out_of_phase(x, n):
 def run_backward(op, x, layout, dlayout, form, **kw):
     """(gradient, loss or None) of the call on a copy of x at `layout`, the
     gradient written at `dlayout` (None: over the logits)."""
+    if form == "persistent" and x.shape[1] * x.element_size() > 200000:
+        pytest.skip("a row longer than shared memory")
     buf, v = placed(x, *layout)
     if dlayout is None:
         dbuf, out, dlayout = buf, v, layout
@@ -353,6 +355,7 @@ def test_teacher_rows(form):
     """Rows without weight, entries of -inf, the same index twice, one entry, a row
     stride past the entries."""
     cols = 3000
+    fwd = "looped" if form == "looped" else "split"
     ninf = -math.inf
     i = torch.tensor([[-1, -1, -1, -1], [5, 6, 7, 8], [5, 6, 7, 8], [9, 9, 9, 9], [-1, -1, 4, -1],
                       [2999, 0, 2999, 0]])
@@ -369,15 +372,15 @@ def test_teacher_rows(form):
     ref.assert_near(r["dlogits"], rd, ref.gradient_bound(x, rd, 2 * g, temperature=2.0)
                     + g.double().abs()[:, None] * 320 * ref.U, "dlogits")
     ref.assert_near(r["loss"], rl, loss_bound(x, rl, i, z, 2.0), "loss")
-    ref.assert_near(fr.fr_distill(x.cuda(), vi, vz, 2.0, form=form), rl,
+    ref.assert_near(fr.fr_distill(x.cuda(), vi, vz, 2.0, form=fwd), rl,
                     loss_bound(x, rl, i, z, 2.0), "loss alone")
     assert (r["dlogits"][:2] == 0).all() and (r["loss"][:2] == 0).all()
     # a weighted entry at a masked logit: +inf; an entry without weight there: nothing
     x[:, 6] = ninf
-    loss = fr.fr_distill(x.cuda(), vi, vz, 2.0, form=form)
+    loss = fr.fr_distill(x.cuda(), vi, vz, 2.0, form=fwd)
     assert torch.isfinite(loss).all()
     z[1] = torch.tensor([0.0, 0.0, 0.0, 0.0])
-    assert fr.fr_distill(x.cuda(), i.cuda(), z.cuda(), 2.0, form=form)[1] == math.inf
+    assert fr.fr_distill(x.cuda(), i.cuda(), z.cuda(), 2.0, form=fwd)[1] == math.inf
     assert fr.fr_check_device_error() == 0
 
 
