@@ -47,6 +47,11 @@ __device__ __forceinline__ V8 ld_v8(const void *p) {
 // rest = m c - mc (see stat_fold), which a and b take in.
 constexpr float kFar = -200.0f;
 
+template <bool B>
+struct Flag {
+  static constexpr bool value = B;
+};
+
 struct RowCoef {
   float m, c, mc, a, b;
   bool fused;
@@ -77,7 +82,8 @@ __device__ __forceinline__ float grad_scalar(float x, const RowCoef &r) {
   return ex2(t) * (HAS_B ? fmaf(r.b, fmaxf(t, kFar), r.a) : r.a);
 }
 
-template <bool F32, bool HAS_B>
+// FUSED is r.fused, a branch around the caller's loop.
+template <bool F32, bool HAS_B, bool FUSED>
 __device__ __forceinline__ V8 grad_vector(const V8 &x, const RowCoef &r) {
   using L = Logits<F32>;
   const uint64_t c2 = pack_f32x2(r.c, r.c), a2 = pack_f32x2(r.a, r.a), b2 = pack_f32x2(r.b, r.b);
@@ -86,7 +92,7 @@ __device__ __forceinline__ V8 grad_vector(const V8 &x, const RowCoef &r) {
 #pragma unroll
   for (int j = 0; j < L::EPV / 2; ++j) {
     const uint64_t v = pack_f32x2(L::at(x, 2 * j), L::at(x, 2 * j + 1));
-    const uint64_t t = r.fused ? fma_f32x2(v, c2, nmc2) : mul_f32x2(sub_f32x2(v, m2), c2);
+    const uint64_t t = FUSED ? fma_f32x2(v, c2, nmc2) : mul_f32x2(sub_f32x2(v, m2), c2);
     const uint64_t e = pack_f32x2(ex2(f32x2_lo(t)), ex2(f32x2_hi(t)));
     uint64_t f = a2;
     if constexpr (HAS_B)
@@ -242,10 +248,14 @@ __global__ void __launch_bounds__(kT, 2) logit_grad_looped(LogitsBackward a) {
     // in place, every element is read by the thread that writes it
     if constexpr (VEC) {
       if (si >= 0) L::store(po, si, grad_scalar<HAS_B>(L::load(pr, si), r));
-      for (int64_t b = tid; b < sp.nvec; b += kT) {
-        const V8 x = ld_v8(pr + vo + b * kVecBytes);
-        st_stream_v8(po + vo + b * kVecBytes, grad_vector<F32, HAS_B>(x, r));
-      }
+      auto write = [&](auto fused) {
+        for (int64_t b = tid; b < sp.nvec; b += kT) {
+          const V8 x = ld_v8(pr + vo + b * kVecBytes);
+          st_stream_v8(po + vo + b * kVecBytes, grad_vector<F32, HAS_B, fused.value>(x, r));
+        }
+      };
+      if (r.fused) write(Flag<true>());
+      else write(Flag<false>());
     } else {
       for (int64_t j = tid; j < a.cols; j += kT)
         L::store(po, j, grad_scalar<HAS_B>(L::load(pr, j), r));
@@ -265,41 +275,53 @@ __global__ void __launch_bounds__(kT, 2) logit_grad_looped(LogitsBackward a) {
 //
 // A persistent grid of clusters of C CTAs; a cluster takes rows c, c + clusters, ...
 // CTA q of C holds the row's 16-byte units [n q / C, n (q + 1) / C) in one of the
-// `nbuf` buffers of its ring.  All warps but the last fold the run's units into the
-// statistics and, after the CTA's (and the cluster's) merge, write the gradient
-// from shared memory while the next rows' copies are in flight.  The last warp
-// keeps them supplied: it issues the copies, reads the next row's token, upstream
-// gradients, ragged ends and teacher entries a row ahead, writes the loss, and
-// after the row's last barrier the elements with a term of their own.
+// `nbuf` buffers of its ring.  All warps but the last (the workers) fold the run's
+// units into the statistics and, after the CTA's and the cluster's merge, write
+// the gradient from shared memory; a worker goes on to the next row when its own
+// part of a row is written, so one row's writing overlaps the next one's folding.
+// The last warp keeps them supplied, two rows ahead: it reads a row's token,
+// upstream gradients, ragged ends and teacher entries, and when a row's workers
+// are done it refills their buffer and writes the loss and the elements with a term of
+// their own.  (With the helper's work between two barriers of the row all waited
+// for it: bf16 [4096, 50257] with 64 entries 237 us.)  Every wait is on an mbarrier
+// and bounded; the cluster's statistics travel by st.async, which does not wait for
+// the row's stores as a cluster barrier's release does.
 
 constexpr int kMaxBufs = 4;
 constexpr int kMaxThreads = 832;  // 72 registers a thread
+constexpr int kMaxCluster = 8;
 constexpr long long kWaitBudget = 1LL << 31;  // SM clocks, about one second
 
 struct RowParams {
   int kind;
-  float g, h;
+  int token;         // of which the gradient has a term, or -1
+  float g, h, xt;    // upstream gradients, the token's logit
+  float ends[32];    // the head's and then the tail's logits
 };
 
 template <bool DISTILL>
 struct StagedShared {
-  uint64_t full[kMaxBufs];
+  uint64_t full[kMaxBufs];  // a buffer's copy has landed
+  uint64_t ready[2];        // a row's parameters are there
+  uint64_t done[2];         // a row's workers have written it
+  uint64_t merged[2];       // the cluster's statistics are there
   RowStat red[2][kMaxThreads / 32];
-  float4 part[2];  // this CTA's statistics, for the cluster
+  float4 part[2][kMaxCluster];
+  RowStat stat[2];  // the row's, for the helper
   RowParams par[2];
   TeacherShared teacher[DISTILL ? 2 : 1];
-  int dead;  // a wait ran out: nothing more is copied or waited for
 };
 
 struct UnitGeom {
-  int head, tail;   // scalars before and after the units
-  int u0, u1;       // this CTA's 16-byte units
-  int64_t first;    // the first unit's byte offset in the row
+  int head, tail;  // scalars before and after the units
+  int u0, u1;      // this CTA's 16-byte units
+  int64_t first;   // the first unit's byte offset in the row
 };
 
+// C = 1 << lg CTAs.
 template <int ES>
-__device__ __forceinline__ UnitGeom unit_geom(const unsigned char *pr, int64_t cols, int q,
-                                              int C) {
+__device__ __forceinline__ UnitGeom unit_geom(const unsigned char *pr, int64_t cols, uint32_t q,
+                                              int lg) {
   const uint64_t s0 = reinterpret_cast<uint64_t>(pr), s1 = s0 + cols * ES;
   const uint64_t a0 = (s0 + 15) & ~uint64_t{15}, a1 = s1 & ~uint64_t{15};
   UnitGeom g;
@@ -309,33 +331,48 @@ __device__ __forceinline__ UnitGeom unit_geom(const unsigned char *pr, int64_t c
     g.first = 0;
     return g;
   }
-  const int64_t n = static_cast<int64_t>((a1 - a0) / 16);
+  const uint64_t n = (a1 - a0) / 16;
   g.head = static_cast<int>((a0 - s0) / ES);
   g.tail = static_cast<int>((s1 - a1) / ES);
   g.first = static_cast<int64_t>(a0 - s0);
-  g.u0 = static_cast<int>(n * q / C);
-  g.u1 = static_cast<int>(n * (q + 1) / C);
+  g.u0 = static_cast<int>((n * q) >> lg);
+  g.u1 = static_cast<int>((n * (q + 1)) >> lg);
   return g;
 }
 
-// Units i and i + step of the n at `buf` as one vector; -inf past the end.
-template <bool F32>
+// Units i and i + step of the n at `buf` as one vector; CHECKED: -inf past the end.
+template <bool F32, bool CHECKED>
 __device__ __forceinline__ V8 lds_units(const unsigned char *buf, int i, int step, int n) {
   V8 v = Logits<F32>::filler();
-  if (i < n) {
+  if (!CHECKED || i < n) {
     const uint4 x = lds_u4(buf + 16 * i);
     v.w[0] = x.x, v.w[1] = x.y, v.w[2] = x.z, v.w[3] = x.w;
   }
-  if (i + step < n) {
+  if (!CHECKED || i + step < n) {
     const uint4 x = lds_u4(buf + 16 * (i + step));
     v.w[4] = x.x, v.w[5] = x.y, v.w[6] = x.z, v.w[7] = x.w;
   }
   return v;
 }
 
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ void worker_barrier(int workers) {
+  asm volatile("bar.sync 1, %0;" ::"r"(workers) : "memory");
+}
+
+// A bounded wait; after one that ran out, nothing is waited for any more.
+__device__ __forceinline__ void wait_for(uint64_t *bar, uint32_t parity, bool &ok, int *err) {
+  if (!ok || mbar_wait_bounded(bar, parity, kWaitBudget)) return;
+  ok = false;
+  atomicCAS(err, 0, FR_DEVERR_TIMEOUT);
+}
+
 template <bool F32, bool DISTILL, bool HAS_B, bool VEC>
 __global__ void __launch_bounds__(kMaxThreads, 1)
-logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf) {
+logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
   pdl_enter();
   using L = Logits<F32>;
   constexpr int EPU = 16 / L::ES;  // logits per unit
@@ -343,197 +380,227 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf) {
   __shared__ StagedShared<DISTILL> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int workers = static_cast<int>(blockDim.x) - 32, helper = workers >> 5;  // the last warp
-  const int C = static_cast<int>(cluster_nctarank()), q = static_cast<int>(cluster_ctarank());
+  const uint32_t C = 1u << lg;
+  const uint32_t q = cluster_ctarank();
   const int64_t row0 = cluster_id_x(), stride = ncluster_x();
   const float c = DISTILL ? kLog2e / a.temperature : kLog2e;
   const float nan = __int_as_float(0x7fc00000);
   const unsigned char *logits = static_cast<const unsigned char *>(a.logits);
   if (tid == 0) {
     for (int b = 0; b < nbuf; ++b) mbar_init(&sh.full[b], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.ready[i], 1);
+      mbar_init(&sh.done[i], helper);
+      mbar_init(&sh.merged[i], 1);
+    }
     mbar_init_fence();
-    sh.dead = 0;
   }
-  __syncthreads();
+  if (C > 1) {  // the peers' barriers are initialised before anything is sent
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  bool ok = true;
 
-  // ---- the helper's parts
-  uint64_t policy = 0;
-  uint32_t issued = 0;  // bit b: parity of buffer b's last copy, set + 1
-  uint32_t ever = 0;
-  auto issue = [&](int64_t row, int b) {  // one lane
-    const unsigned char *pr = logits + row * a.ld * L::ES;
-    const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, C);
-    const uint32_t bytes = 16u * static_cast<uint32_t>(g.u1 - g.u0);
-    if (bytes == 0) return;
-    fence_proxy_async_smem();
-    mbar_arrive_expect_tx(&sh.full[b], bytes);
-    bulk_copy_g2s(bufs + static_cast<size_t>(b) * buf_bytes,
-                  pr + g.first + 16 * static_cast<int64_t>(g.u0), bytes, &sh.full[b], policy);
-    issued ^= 1u << b;
-    ever |= 1u << b;
-  };
-  auto token_of = [&](int64_t row) -> int64_t {
-    return !DISTILL && a.token && row < a.rows ? a.token[row] : -1;
-  };
-  auto wanted = [&](int64_t token) { return DISTILL || token_kind<HAS_B>(a, token) == kRowGrad; };
-  // the next row's parameters, in the helper's registers until it is its turn
-  int64_t tok = -1;
-  float xt = 0.0f, head = -INFINITY, tail = -INFINITY;
-  auto prepare = [&](int64_t row, int64_t token, int slot) {  // the whole warp
-    const unsigned char *pr = logits + row * a.ld * L::ES;
-    const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, C);
-    RowParams p{kRowGrad, 0.0f, 0.0f};
-    head = q == 0 && lane < g.head ? L::load(pr, lane) : -INFINITY;
-    tail = q == C - 1 && lane < g.tail ? L::load(pr, a.cols - g.tail + lane) : -INFINITY;
-    if constexpr (DISTILL) {
-      p.g = a.dloss[row * a.dloss_stride] * a.temperature;
-      const Teacher t = teacher_load<F32>(a.index + row * a.ldt, a.teacher + row * a.ldt, a.top,
-                                          pr, a.cols, a.temperature);
-      p.kind = t.bad ? kRowNan : t.any ? kRowGrad : kRowZero;
-      teacher_share(t, a.top, sh.teacher[slot]);
-    } else {
-      p.kind = token_kind<HAS_B>(a, token);
-      tok = p.kind == kRowGrad && a.token && token != a.ignore_index ? token : -1;
-      if (tok >= 0) {
-        xt = L::load(pr, tok);
-        p.g = a.dloss[row * a.dloss_stride] * a.dloss_sign;
-      }
-      if constexpr (HAS_B) p.h = a.dentropy[row * a.dentropy_stride];
-    }
-    if (lane == 0) {
-      sh.par[slot] = p;
-      if (p.kind == kRowNan) atomicCAS(a.err, 0, FR_DEVERR_BAD_TARGET);
-    }
-  };
   if (warp == helper) {
-    policy = l2_evict_first_policy();
+    const uint64_t policy = l2_evict_first_policy();
+    uint32_t issued = 0, ever = 0;  // per buffer: copies issued mod 2; any
+    auto issue = [&](int64_t row, int b) {
+      const unsigned char *pr = logits + row * a.ld * L::ES;
+      const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, lg);
+      const uint32_t bytes = 16u * static_cast<uint32_t>(g.u1 - g.u0);
+      if (bytes == 0 || lane != 0) return;
+      fence_proxy_async_smem();
+      mbar_arrive_expect_tx(&sh.full[b], bytes);
+      bulk_copy_g2s(bufs + static_cast<size_t>(b) * buf_bytes,
+                    pr + g.first + 16 * static_cast<int64_t>(g.u0), bytes, &sh.full[b], policy);
+      issued ^= 1u << b;
+      ever |= 1u << b;
+    };
+    auto token_of = [&](int64_t row) -> int64_t {
+      return !DISTILL && a.token && row < a.rows ? a.token[row] : -1;
+    };
+    auto wanted = [&](int64_t token) {
+      return DISTILL || token_kind<HAS_B>(a, token) == kRowGrad;
+    };
+    auto prepare = [&](int64_t row, int64_t token, int slot) {
+      const unsigned char *pr = logits + row * a.ld * L::ES;
+      const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, lg);
+      RowParams &p = sh.par[slot];
+      int kind, t = -1;
+      float gr = 0.0f, h = 0.0f, xt = 0.0f;
+      float end = 0.0f;
+      if (lane < g.head) end = L::load(pr, lane);
+      else if (lane < g.head + g.tail) end = L::load(pr, a.cols - g.tail + lane - g.head);
+      if constexpr (DISTILL) {
+        gr = a.dloss[row * a.dloss_stride] * a.temperature;
+        const Teacher te = teacher_load<F32>(a.index + row * a.ldt, a.teacher + row * a.ldt, a.top,
+                                             pr, a.cols, a.temperature);
+        kind = te.bad ? kRowNan : te.any ? kRowGrad : kRowZero;
+        teacher_share(te, a.top, sh.teacher[slot]);
+      } else {
+        kind = token_kind<HAS_B>(a, token);
+        if (kind == kRowGrad && a.token && token != a.ignore_index) {
+          t = static_cast<int>(token);
+          xt = L::load(pr, t);
+          gr = a.dloss[row * a.dloss_stride] * a.dloss_sign;
+        }
+        if constexpr (HAS_B) h = a.dentropy[row * a.dentropy_stride];
+      }
+      p.ends[lane] = end;
+      if (lane == 0) {
+        p.kind = kind;
+        p.token = t;
+        p.g = gr;
+        p.h = h;
+        p.xt = xt;
+        if (kind == kRowNan) atomicCAS(a.err, 0, FR_DEVERR_BAD_TARGET);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.ready[slot]);
+    };
     for (int b = 0; b < nbuf; ++b) {
       const int64_t row = row0 + b * stride;
-      if (row < a.rows && wanted(token_of(row)) && lane == 0) issue(row, b);
+      if (row < a.rows && wanted(token_of(row))) issue(row, b);
     }
     if (row0 < a.rows) prepare(row0, token_of(row0), 0);
-  }
-  __syncthreads();
-
-  uint32_t phases = 0;  // bit b: parity that the next wait on buffer b takes
-  bool ok = true;
-  int b = 0;
-  for (int64_t row = row0, k = 0; row < a.rows; row += stride, ++k, b = b + 1 == nbuf ? 0 : b + 1) {
-    const int slot = static_cast<int>(k & 1);
-    const unsigned char *pr = logits + row * a.ld * L::ES;
-    unsigned char *po = static_cast<unsigned char *>(a.dlogits) + row * a.ldd * L::ES;
-    const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, C);
-    const int n = g.u1 - g.u0;
-    const unsigned char *buf = bufs + static_cast<size_t>(b) * buf_bytes;
-    const RowParams par = sh.par[slot];
-    const bool copied = n > 0 && (DISTILL || par.kind == kRowGrad);
-    const int64_t next_token = warp == helper ? token_of(row + stride) : -1;
-    const int64_t refill_token = warp == helper ? token_of(row + nbuf * stride) : -1;
-
-    RowStat st = stat_empty();
-    if (warp != helper) {
-      if (copied) {
-        if (ok && !mbar_wait_bounded(&sh.full[b], (phases >> b) & 1, kWaitBudget)) {
-          ok = false;
-          sh.dead = 1;
-          atomicCAS(a.err, 0, FR_DEVERR_TIMEOUT);
-        }
-        phases ^= 1u << b;
-      }
-      if (par.kind == kRowGrad) {
-        for (int i = tid; i < n; i += 4 * workers) {
-          const V8 v[2] = {lds_units<F32>(buf, i, workers, n),
-                           lds_units<F32>(buf, i + 2 * workers, workers, n)};
-          stat_fold<F32, HAS_B, 2>(st, v, L::max(v), c);
-        }
-      }
-    } else {
-      if (head != -INFINITY) st = stat_merge(st, RowStat{head, 1.0f, 0.0f}, c);
-      if (tail != -INFINITY) st = stat_merge(st, RowStat{tail, 1.0f, 0.0f}, c);
-    }
-    st = warp_stat(st, c);
-    if (lane == 0) sh.red[slot][warp] = st;
-    __syncthreads();
-    if (par.kind == kRowGrad) {
-      st = warp_stat(lane <= helper ? sh.red[slot][lane] : stat_empty(), c);
-      if (C > 1) {
-        if (tid == 0) sh.part[slot] = make_float4(st.m, st.l, st.s, 0.0f);
-        __syncwarp();
-        cluster_arrive();
-        cluster_wait();
-        const float4 o = lane < C ? ld_dsmem_f4(&sh.part[slot], lane)
-                                  : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-        st = warp_stat(RowStat{o.x, o.y, o.z}, c);
-      }
-    }
-    const RowCoef r = DISTILL ? row_coef(st, c, par.g / st.l, 0.0f)
-                              : token_coef(st, c, par.g, par.h, HAS_B);
-    const int64_t out0 = g.first + 16 * static_cast<int64_t>(g.u0);  // bytes into the row
-    if (warp != helper) {
-      if (par.kind == kRowGrad && VEC) {
-        for (int i = tid; i < n; i += 2 * workers) {
-          const V8 y = grad_vector<F32, HAS_B>(lds_units<F32>(buf, i, workers, n), r);
-          st_stream_u4(po + out0 + 16 * static_cast<int64_t>(i),
-                       make_uint4(y.w[0], y.w[1], y.w[2], y.w[3]));
-          if (i + workers < n)
-            st_stream_u4(po + out0 + 16 * static_cast<int64_t>(i + workers),
-                         make_uint4(y.w[4], y.w[5], y.w[6], y.w[7]));
-        }
-      } else if (VEC) {
-        const uint32_t w = par.kind == kRowNan ? (F32 ? 0x7FC00000u : 0x7FC07FC0u) : 0;
-        for (int i = tid; i < n; i += workers)
-          st_stream_u4(po + out0 + 16 * static_cast<int64_t>(i), make_uint4(w, w, w, w));
-      } else {
-        const int64_t e0 = out0 / L::ES;
-        for (int j = tid; j < n * EPU; j += workers)
-          L::store(po, e0 + j,
-                   par.kind == kRowGrad ? grad_scalar<HAS_B>(L::load(buf, j), r)
-                                        : par.kind == kRowNan ? nan : 0.0f);
-      }
-    } else {
-      if (q == 0 && lane < g.head)
-        L::store(po, lane, par.kind == kRowGrad ? grad_scalar<HAS_B>(head, r)
-                                                : par.kind == kRowNan ? nan : 0.0f);
-      if (q == C - 1 && lane < g.tail)
-        L::store(po, a.cols - g.tail + lane, par.kind == kRowGrad ? grad_scalar<HAS_B>(tail, r)
-                                                                  : par.kind == kRowNan ? nan : 0.0f);
-      if (a.loss && q == 0) {
-        float loss = par.kind == kRowNan ? nan : 0.0f;
-        if (par.kind == kRowGrad) {
-          if constexpr (DISTILL) loss = teacher_loss(sh.teacher[slot], a.top, st, a.temperature);
-          else if (tok >= 0) loss = logf(st.l) - (xt - st.m);
-        }
-        if (lane == 0) a.loss[row] = loss;
-      }
-    }
-    // this row's elements with a term of their own, and the next row's parameters
-    const int64_t own_tok = tok;
-    const float own_value = !DISTILL && tok >= 0 ? grad_scalar<HAS_B>(xt, r) + par.g : 0.0f;
-    if (warp == helper && row + stride < a.rows) prepare(row + stride, next_token, slot ^ 1);
-    __syncthreads();
-    if (warp == helper) {
-      // element j is written here if this CTA wrote it above
-      const int64_t lo = q == 0 ? 0 : out0 / L::ES;
-      const int64_t hi = q == C - 1 ? a.cols : (g.first + 16 * static_cast<int64_t>(g.u1)) / L::ES;
-      if constexpr (DISTILL) {
-        const TeacherShared &t = sh.teacher[slot];
-        if (par.kind == kRowGrad)
+    if (row0 + stride < a.rows) prepare(row0 + stride, token_of(row0 + stride), 1);
+    int b = 0;
+    uint32_t k = 0;
+    for (int64_t row = row0; row < a.rows; row += stride, ++k, b = b + 1 == nbuf ? 0 : b + 1) {
+      const int slot = k & 1;
+      const int64_t refill = row + nbuf * stride, ahead = row + 2 * stride;
+      const int64_t refill_token = token_of(refill), ahead_token = token_of(ahead);
+      wait_for(&sh.done[slot], (k >> 1) & 1, ok, a.err);
+      if (ok && refill < a.rows && wanted(refill_token)) issue(refill, b);
+      const RowParams &p = sh.par[slot];
+      const RowStat st = sh.stat[slot];
+      const unsigned char *pr = logits + row * a.ld * L::ES;
+      unsigned char *po = static_cast<unsigned char *>(a.dlogits) + row * a.ldd * L::ES;
+      const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, lg);
+      // element j is written here if this CTA wrote it
+      const int64_t lo = q == 0 ? 0 : (g.first + 16 * static_cast<int64_t>(g.u0)) / L::ES;
+      const int64_t hi =
+          q + 1 == C ? a.cols : (g.first + 16 * static_cast<int64_t>(g.u1)) / L::ES;
+      float loss = p.kind == kRowNan ? nan : 0.0f;
+      if (p.kind == kRowGrad) {
+        if constexpr (DISTILL) {
+          const TeacherShared &t = sh.teacher[slot];
           for (int e = lane; e < a.top; e += 32)
             if (t.idx[e] >= lo && t.idx[e] < hi)
-              L::store(po, t.idx[e], teacher_element(t, e, st, c, par.g));
-      } else if (lane == 0 && own_tok >= lo && own_tok < hi) {
-        L::store(po, own_tok, own_value);
+              L::store(po, t.idx[e], teacher_element(t, e, st, c, p.g));
+          if (a.loss && q == 0) loss = teacher_loss(t, a.top, st, a.temperature);
+        } else if (p.token >= 0) {
+          if (lane == 0 && p.token >= lo && p.token < hi)
+            L::store(po, p.token,
+                     grad_scalar<HAS_B>(p.xt, token_coef(st, c, p.g, p.h, HAS_B)) + p.g);
+          loss = logf(st.l) - (p.xt - st.m);
+        }
       }
-      const int64_t refill = row + nbuf * stride;
-      if (refill < a.rows && wanted(refill_token) && lane == 0 &&
-          *reinterpret_cast<volatile int *>(&sh.dead) == 0)
-        issue(refill, b);
+      if (a.loss && q == 0 && lane == 0) a.loss[row] = loss;
       __syncwarp();
+      if (ahead < a.rows) prepare(ahead, ahead_token, slot);
+    }
+    if (lane == 0)  // done with, unless a worker gave up: no copy may outlive the CTA
+      for (int i = 0; i < nbuf; ++i)
+        if ((ever >> i) & 1) mbar_wait_bounded(&sh.full[i], ((issued >> i) & 1) ^ 1, kWaitBudget);
+  } else {
+    uint32_t phases = 0;  // bit b: parity that the next wait on buffer b takes
+    uint32_t merges = 0;  // bit slot: the same for the cluster's statistics
+    int b = 0;
+    uint32_t k = 0;
+    for (int64_t row = row0; row < a.rows; row += stride, ++k, b = b + 1 == nbuf ? 0 : b + 1) {
+      const int slot = k & 1;
+      const unsigned char *pr = logits + row * a.ld * L::ES;
+      unsigned char *po = static_cast<unsigned char *>(a.dlogits) + row * a.ldd * L::ES;
+      const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, lg);
+      const int n = g.u1 - g.u0;
+      const unsigned char *buf = bufs + static_cast<size_t>(b) * buf_bytes;
+      wait_for(&sh.ready[slot], (k >> 1) & 1, ok, a.err);
+      const int kind = sh.par[slot].kind;
+      if (n > 0 && (DISTILL || kind == kRowGrad)) {
+        wait_for(&sh.full[b], (phases >> b) & 1, ok, a.err);
+        phases ^= 1u << b;
+      }
+      RowCoef r{};
+      const bool end = lane < g.head ? q == 0 : lane < g.head + g.tail && q + 1 == C;
+      RowStat st = stat_empty();
+      if (kind == kRowGrad) {
+        if (warp == 0 && end) {
+          const float x = sh.par[slot].ends[lane];
+          if (x != -INFINITY) st = RowStat{x, 1.0f, 0.0f};
+        }
+        int i = tid;
+        for (; i + 3 * workers < n; i += 4 * workers) {
+          const V8 v[2] = {lds_units<F32, false>(buf, i, workers, n),
+                           lds_units<F32, false>(buf, i + 2 * workers, workers, n)};
+          stat_fold<F32, HAS_B, 2>(st, v, L::max(v), c);
+        }
+        for (; i < n; i += 2 * workers) {
+          const V8 v[1] = {lds_units<F32, true>(buf, i, workers, n)};
+          stat_fold<F32, HAS_B, 1>(st, v, L::max(v), c);
+        }
+        st = warp_stat(st, c);
+        if (lane == 0) sh.red[slot][warp] = st;
+      }
+      worker_barrier(workers);  // for every row: a wait that ran out leaves no one behind
+      if (kind == kRowGrad) {
+        st = warp_stat(lane < helper ? sh.red[slot][lane] : stat_empty(), c);
+        if (C > 1) {
+          if (warp == 0) {
+            if (lane == 0) mbar_arrive_expect_tx(&sh.merged[slot], 16u * C);
+            __syncwarp();
+            if (lane < C)
+              st_async_f4(&sh.part[slot][q], &sh.merged[slot], lane,
+                          make_float4(st.m, st.l, st.s, 0.0f));
+          }
+          wait_for(&sh.merged[slot], (merges >> slot) & 1, ok, a.err);
+          merges ^= 1u << slot;
+          const float4 o = lane < C ? sh.part[slot][lane]
+                                    : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+          st = warp_stat(RowStat{o.x, o.y, o.z}, c);
+        }
+        if (tid == 0) sh.stat[slot] = st;
+        const float gr = sh.par[slot].g;
+        r = DISTILL ? row_coef(st, c, gr / st.l, 0.0f)
+                    : token_coef(st, c, gr, sh.par[slot].h, HAS_B);
+      }
+      unsigned char *out = po + g.first + 16 * static_cast<int64_t>(g.u0);
+      if (kind == kRowGrad && VEC) {
+        auto write = [&](auto fused) {
+          int i = tid;
+          for (; i + workers < n; i += 2 * workers) {
+            const V8 y = grad_vector<F32, HAS_B, fused.value>(
+                lds_units<F32, false>(buf, i, workers, n), r);
+            st_stream_u4(out + 16 * i, make_uint4(y.w[0], y.w[1], y.w[2], y.w[3]));
+            st_stream_u4(out + 16 * (i + workers), make_uint4(y.w[4], y.w[5], y.w[6], y.w[7]));
+          }
+          if (i < n) {
+            const V8 y = grad_vector<F32, HAS_B, fused.value>(
+                lds_units<F32, true>(buf, i, workers, n), r);
+            st_stream_u4(out + 16 * i, make_uint4(y.w[0], y.w[1], y.w[2], y.w[3]));
+          }
+        };
+        if (r.fused) write(Flag<true>());
+        else write(Flag<false>());
+      } else if (VEC) {
+        const uint32_t w = kind == kRowNan ? (F32 ? 0x7FC00000u : 0x7FC07FC0u) : 0;
+        for (int i = tid; i < n; i += workers) st_stream_u4(out + 16 * i, make_uint4(w, w, w, w));
+      } else {
+        for (int j = tid; j < n * EPU; j += workers)
+          L::store(out, j, kind == kRowGrad ? grad_scalar<HAS_B>(L::load(buf, j), r)
+                                            : kind == kRowNan ? nan : 0.0f);
+      }
+      if (warp == 0 && end)
+        L::store(po, lane < g.head ? lane : a.cols - g.tail + lane - g.head,
+                 kind == kRowGrad ? grad_scalar<HAS_B>(sh.par[slot].ends[lane], r)
+                                  : kind == kRowNan ? nan : 0.0f);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.done[slot]);
     }
   }
-  if (warp == helper && lane == 0 && *reinterpret_cast<volatile int *>(&sh.dead) != 0)
-    for (int i = 0; i < nbuf; ++i)  // copies in flight may not outlive the CTA
-      if ((ever >> i) & 1) mbar_wait_bounded(&sh.full[i], ((issued >> i) & 1) ^ 1, kWaitBudget);
-  if (C > 1) {  // no CTA's statistics are given up while a peer reads them
+  if (C > 1) {  // no CTA goes while a peer may still send to it
     __syncwarp();
     cluster_arrive();
     cluster_wait();
@@ -599,7 +666,7 @@ cudaError_t launch_form(const LogitsBackward &a, int cluster, bool vec32, bool v
   if (clusters < 1) clusters = 1;
   if (clusters > a.rows) clusters = a.rows;
   return launch_k(kern, dim3(static_cast<unsigned>(clusters * cluster)), dim3(sh.threads), smem,
-                  s, cluster, a, sh.buf_bytes, sh.nbuf);
+                  s, cluster, a, sh.buf_bytes, sh.nbuf, __builtin_ctz(cluster));
 }
 
 }  // namespace
