@@ -72,8 +72,9 @@ __device__ __forceinline__ RowCoef row_coef(const RowStat &st, float c, float a,
 // The coefficients of a row with the token's gradient g and the entropy's h.
 __device__ __forceinline__ RowCoef token_coef(const RowStat &st, float c, float g, float h,
                                               bool has_h) {
-  if (!has_h) return row_coef(st, c, -g / st.l, 0.0f);
-  return row_coef(st, c, (h * (st.s / st.l) - g) / st.l, -h / st.l / c);
+  const float inv = 1.0f / st.l;
+  if (!has_h) return row_coef(st, c, -g * inv, 0.0f);
+  return row_coef(st, c, (h * (st.s * inv) - g) * inv, -h * inv * kLn2);  // c = log2(e) here
 }
 
 template <bool HAS_B>
@@ -126,24 +127,62 @@ struct TeacherShared {
   float q[FR_TOP_MAX], logq[FR_TOP_MAX], x[FR_TOP_MAX];
   float sum[FR_TOP_MAX];  // the weights of all entries that name idx
 };
+using EntryTable = uint16_t[256];
 
-__device__ __forceinline__ void teacher_share(const Teacher &t, int top, TeacherShared &sh) {
+// Whether two of the warp's entries name the same element.  Each puts its number
+// in the table at a hash of its index and looks who is there: an entry with the
+// same index, or another index with the same hash, which is met by another
+// round of those that lost.
+__device__ __forceinline__ bool teacher_repeats(const TeacherShared &sh, int top,
+                                                EntryTable &table) {
+  const int lane = threadIdx.x & 31;
+  uint32_t open = 0;
+  bool repeats = false;
+#pragma unroll
+  for (int i = 0; i < kTopPerLane; ++i)
+    if (lane + 32 * i < top && sh.idx[lane + 32 * i] >= 0) open |= 1u << i;
+  while (__any_sync(0xffffffffu, open != 0)) {
+#pragma unroll
+    for (int i = 0; i < kTopPerLane; ++i)
+      if ((open >> i) & 1) {
+        const int32_t j = sh.idx[lane + 32 * i];
+        table[(j ^ (j >> 8)) & 255] = static_cast<uint16_t>(lane + 32 * i);
+      }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kTopPerLane; ++i)
+      if ((open >> i) & 1) {
+        const int32_t j = sh.idx[lane + 32 * i];
+        const int e = table[(j ^ (j >> 8)) & 255];
+        if (sh.idx[e] == j) {
+          open &= ~(1u << i);
+          repeats |= e != lane + 32 * i;
+        }
+      }
+    __syncwarp();
+  }
+  return __any_sync(0xffffffffu, repeats);
+}
+
+__device__ __forceinline__ void teacher_share(const Teacher &t, int top, TeacherShared &sh,
+                                              EntryTable &table) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < kTopPerLane; ++i) {
     const int e = lane + 32 * i;
     sh.idx[e] = t.q[i] != 0.0f ? static_cast<int32_t>(t.idx[i]) : -1;
-    sh.q[e] = t.q[i];
+    sh.q[e] = sh.sum[e] = t.q[i];
     sh.logq[e] = t.logq[i];
     sh.x[e] = t.x[i];
   }
   __syncwarp();
-  for (int e = lane; e < top; e += 32) {
-    const int32_t j = sh.idx[e];
-    float sum = 0.0f;  // in the entries' order
-    for (int n = 0; n < top; ++n) sum += sh.idx[n] == j ? sh.q[n] : 0.0f;
-    sh.sum[e] = sum;
-  }
+  if (teacher_repeats(sh, top, table))
+    for (int e = lane; e < top; e += 32) {
+      const int32_t j = sh.idx[e];
+      float sum = 0.0f;  // in the entries' order
+      for (int n = 0; n < top; ++n) sum += sh.idx[n] == j ? sh.q[n] : 0.0f;
+      sh.sum[e] = sum;
+    }
   __syncwarp();
 }
 
@@ -161,7 +200,7 @@ __device__ __forceinline__ float teacher_loss(const TeacherShared &sh, int top, 
 // Entry e's element: g (p - sum of its weights).
 __device__ __forceinline__ float teacher_element(const TeacherShared &sh, int e, const RowStat &st,
                                                  float c, float g) {
-  return g * (ex2((sh.x[e] - st.m) * c) / st.l - sh.sum[e]);
+  return g * (ex2((sh.x[e] - st.m) * c) * (1.0f / st.l) - sh.sum[e]);
 }
 
 // ---- looped: a CTA per row, the row streamed twice ---------------------------------
@@ -172,6 +211,7 @@ __global__ void __launch_bounds__(kT, 2) logit_grad_looped(LogitsBackward a) {
   using L = Logits<F32>;
   __shared__ RowStat red[kT / 32];
   __shared__ TeacherShared sh[1];
+  __shared__ EntryTable table;
   __shared__ int kind_s;
   const int tid = threadIdx.x;
   const float c = DISTILL ? kLog2e / a.temperature : kLog2e;
@@ -188,7 +228,7 @@ __global__ void __launch_bounds__(kT, 2) logit_grad_looped(LogitsBackward a) {
       if (tid < 32) {
         const Teacher t = teacher_load<F32>(a.index + row * a.ldt, a.teacher + row * a.ldt, a.top,
                                             pr, a.cols, a.temperature);
-        teacher_share(t, a.top, sh[0]);
+        teacher_share(t, a.top, sh[0], table);
         if (tid == 0) {
           kind_s = t.bad ? kRowNan : t.any ? kRowGrad : kRowZero;
           if (t.bad) atomicCAS(a.err, 0, FR_DEVERR_BAD_TARGET);
@@ -236,7 +276,8 @@ __global__ void __launch_bounds__(kT, 2) logit_grad_looped(LogitsBackward a) {
     }
     st = block_stat<kT>(st, c, red);
 
-    const RowCoef r = DISTILL ? row_coef(st, c, g / st.l, 0.0f) : token_coef(st, c, g, h, HAS_B);
+    const RowCoef r =
+        DISTILL ? row_coef(st, c, g * (1.0f / st.l), 0.0f) : token_coef(st, c, g, h, HAS_B);
     if constexpr (DISTILL) {
       if (a.loss && tid < 32) {
         const float loss = teacher_loss(sh[0], a.top, st, a.temperature);
@@ -294,9 +335,12 @@ constexpr long long kWaitBudget = 1LL << 31;  // SM clocks, about one second
 
 struct RowParams {
   int kind;
-  int token;         // of which the gradient has a term, or -1
-  float g, h, xt;    // upstream gradients, the token's logit
-  float ends[32];    // the head's and then the tail's logits
+  int n;               // this CTA's units
+  unsigned char *out;  // where the gradient of the first one goes
+  int ends;            // this CTA's scalars of the row's head and tail: bits
+  int token;           // of which the gradient has a term here, or -1
+  float g, h, xt;      // upstream gradients, the token's logit
+  float end[32];       // the head's and then the tail's logits
 };
 
 template <bool DISTILL>
@@ -310,6 +354,7 @@ struct StagedShared {
   RowStat stat[2];  // the row's, for the helper
   RowParams par[2];
   TeacherShared teacher[DISTILL ? 2 : 1];
+  EntryTable table;
 };
 
 struct UnitGeom {
@@ -424,37 +469,63 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
     auto wanted = [&](int64_t token) {
       return DISTILL || token_kind<HAS_B>(a, token) == kRowGrad;
     };
-    auto prepare = [&](int64_t row, int64_t token, int slot) {
+    // A row's parameters are fetched (loads in flight) and, later, published.
+    struct Fetched {
+      TeacherRaw teacher;  // its entries are fetched a row earlier still
+      int64_t token;
+      float g, h, xt, end;
+    } f;
+    auto fetch_entries = [&](int64_t row) {
+      if (DISTILL && row < a.rows)
+        teacher_fetch(f.teacher, a.index + row * a.ldt, a.teacher + row * a.ldt, a.top);
+    };
+    auto fetch = [&](int64_t row, int64_t token) {
+      if (row >= a.rows) return;
+      const unsigned char *pr = logits + row * a.ld * L::ES;
+      const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, lg);
+      f.token = token;
+      f.g = f.h = f.xt = f.end = 0.0f;
+      if (lane < g.head) f.end = L::load(pr, lane);
+      else if (lane < g.head + g.tail) f.end = L::load(pr, a.cols - g.tail + lane - g.head);
+      if constexpr (DISTILL) {
+        f.g = a.dloss[row * a.dloss_stride];
+        teacher_gather<F32>(f.teacher, pr, a.cols);
+      } else {
+        if (token >= 0 && token < a.cols && token != a.ignore_index) {
+          f.xt = L::load(pr, token);
+          f.g = a.dloss[row * a.dloss_stride];
+        }
+        if constexpr (HAS_B) f.h = a.dentropy[row * a.dentropy_stride];
+      }
+    };
+    auto publish = [&](int64_t row, int slot) {
+      if (row >= a.rows) return;
       const unsigned char *pr = logits + row * a.ld * L::ES;
       const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, lg);
       RowParams &p = sh.par[slot];
-      int kind, t = -1;
-      float gr = 0.0f, h = 0.0f, xt = 0.0f;
-      float end = 0.0f;
-      if (lane < g.head) end = L::load(pr, lane);
-      else if (lane < g.head + g.tail) end = L::load(pr, a.cols - g.tail + lane - g.head);
+      int kind, token = -1;
       if constexpr (DISTILL) {
-        gr = a.dloss[row * a.dloss_stride] * a.temperature;
-        const Teacher te = teacher_load<F32>(a.index + row * a.ldt, a.teacher + row * a.ldt, a.top,
-                                             pr, a.cols, a.temperature);
-        kind = te.bad ? kRowNan : te.any ? kRowGrad : kRowZero;
-        teacher_share(te, a.top, sh.teacher[slot]);
+        const Teacher t = teacher_finish(f.teacher, a.cols, a.temperature);
+        kind = t.bad ? kRowNan : t.any ? kRowGrad : kRowZero;
+        teacher_share(t, a.top, sh.teacher[slot], sh.table);
       } else {
-        kind = token_kind<HAS_B>(a, token);
-        if (kind == kRowGrad && a.token && token != a.ignore_index) {
-          t = static_cast<int>(token);
-          xt = L::load(pr, t);
-          gr = a.dloss[row * a.dloss_stride] * a.dloss_sign;
-        }
-        if constexpr (HAS_B) h = a.dentropy[row * a.dentropy_stride];
+        kind = token_kind<HAS_B>(a, f.token);
+        if (kind == kRowGrad && a.token && f.token != a.ignore_index)
+          token = static_cast<int>(f.token);
       }
-      p.ends[lane] = end;
+      p.end[lane] = f.end;
+      const bool end = lane < g.head ? q == 0 : lane < g.head + g.tail && q + 1 == C;
+      const uint32_t ends = __ballot_sync(0xffffffffu, end);
       if (lane == 0) {
         p.kind = kind;
-        p.token = t;
-        p.g = gr;
-        p.h = h;
-        p.xt = xt;
+        p.n = g.u1 - g.u0;
+        p.out = static_cast<unsigned char *>(a.dlogits) + row * a.ldd * L::ES + g.first +
+                16 * static_cast<int64_t>(g.u0);
+        p.ends = static_cast<int>(ends);
+        p.token = token;
+        p.g = f.g * (DISTILL ? a.temperature : a.dloss_sign);
+        p.h = f.h;
+        p.xt = f.xt;
         if (kind == kRowNan) atomicCAS(a.err, 0, FR_DEVERR_BAD_TARGET);
       }
       __syncwarp();
@@ -464,27 +535,45 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
       const int64_t row = row0 + b * stride;
       if (row < a.rows && wanted(token_of(row))) issue(row, b);
     }
-    if (row0 < a.rows) prepare(row0, token_of(row0), 0);
-    if (row0 + stride < a.rows) prepare(row0 + stride, token_of(row0 + stride), 1);
+    for (int i = 0; i < 2; ++i) {
+      fetch_entries(row0 + i * stride);
+      fetch(row0 + i * stride, token_of(row0 + i * stride));
+      publish(row0 + i * stride, i);
+    }
+    fetch_entries(row0 + 2 * stride);
+    int64_t ahead_token = token_of(row0 + 2 * stride);
+    int64_t refill_token = token_of(row0 + nbuf * stride);
     int b = 0;
     uint32_t k = 0;
     for (int64_t row = row0; row < a.rows; row += stride, ++k, b = b + 1 == nbuf ? 0 : b + 1) {
       const int slot = k & 1;
       const int64_t refill = row + nbuf * stride, ahead = row + 2 * stride;
-      const int64_t refill_token = token_of(refill), ahead_token = token_of(ahead);
+      const bool refill_wanted = refill < a.rows && wanted(refill_token);
+      fetch(ahead, ahead_token);
+      ahead_token = token_of(ahead + stride);
+      refill_token = token_of(refill + stride);
       wait_for(&sh.done[slot], (k >> 1) & 1, ok, a.err);
-      if (ok && refill < a.rows && wanted(refill_token)) issue(refill, b);
+      if (ok && refill_wanted) issue(refill, b);
       const RowParams &p = sh.par[slot];
       const RowStat st = sh.stat[slot];
       const unsigned char *pr = logits + row * a.ld * L::ES;
       unsigned char *po = static_cast<unsigned char *>(a.dlogits) + row * a.ldd * L::ES;
       const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, lg);
-      // element j is written here if this CTA wrote it
+      // element j is written here if it is this CTA's
       const int64_t lo = q == 0 ? 0 : (g.first + 16 * static_cast<int64_t>(g.u0)) / L::ES;
       const int64_t hi =
           q + 1 == C ? a.cols : (g.first + 16 * static_cast<int64_t>(g.u1)) / L::ES;
+      const bool grad = p.kind == kRowGrad;
       float loss = p.kind == kRowNan ? nan : 0.0f;
-      if (p.kind == kRowGrad) {
+      RowCoef r{};
+      if (grad)
+        r = DISTILL ? row_coef(st, c, p.g * (1.0f / st.l), 0.0f)
+                    : token_coef(st, c, p.g, p.h, HAS_B);
+      if ((p.ends >> lane) & 1)
+        L::store(po, lane < g.head ? lane : a.cols - g.tail + lane - g.head,
+                 grad ? grad_scalar<HAS_B>(p.end[lane], r) : p.kind == kRowNan ? nan : 0.0f);
+      __syncwarp();  // an end may be written again below
+      if (grad) {
         if constexpr (DISTILL) {
           const TeacherShared &t = sh.teacher[slot];
           for (int e = lane; e < a.top; e += 32)
@@ -493,14 +582,14 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
           if (a.loss && q == 0) loss = teacher_loss(t, a.top, st, a.temperature);
         } else if (p.token >= 0) {
           if (lane == 0 && p.token >= lo && p.token < hi)
-            L::store(po, p.token,
-                     grad_scalar<HAS_B>(p.xt, token_coef(st, c, p.g, p.h, HAS_B)) + p.g);
+            L::store(po, p.token, grad_scalar<HAS_B>(p.xt, r) + p.g);
           loss = logf(st.l) - (p.xt - st.m);
         }
       }
       if (a.loss && q == 0 && lane == 0) a.loss[row] = loss;
       __syncwarp();
-      if (ahead < a.rows) prepare(ahead, ahead_token, slot);
+      publish(ahead, slot);
+      fetch_entries(ahead + stride);
     }
     if (lane == 0)  // done with, unless a worker gave up: no copy may outlive the CTA
       for (int i = 0; i < nbuf; ++i)
@@ -512,23 +601,19 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
     uint32_t k = 0;
     for (int64_t row = row0; row < a.rows; row += stride, ++k, b = b + 1 == nbuf ? 0 : b + 1) {
       const int slot = k & 1;
-      const unsigned char *pr = logits + row * a.ld * L::ES;
-      unsigned char *po = static_cast<unsigned char *>(a.dlogits) + row * a.ldd * L::ES;
-      const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, lg);
-      const int n = g.u1 - g.u0;
       const unsigned char *buf = bufs + static_cast<size_t>(b) * buf_bytes;
       wait_for(&sh.ready[slot], (k >> 1) & 1, ok, a.err);
-      const int kind = sh.par[slot].kind;
+      const RowParams &par = sh.par[slot];
+      const int kind = par.kind, n = par.n;
       if (n > 0 && (DISTILL || kind == kRowGrad)) {
         wait_for(&sh.full[b], (phases >> b) & 1, ok, a.err);
         phases ^= 1u << b;
       }
       RowCoef r{};
-      const bool end = lane < g.head ? q == 0 : lane < g.head + g.tail && q + 1 == C;
       RowStat st = stat_empty();
       if (kind == kRowGrad) {
-        if (warp == 0 && end) {
-          const float x = sh.par[slot].ends[lane];
+        if (warp == 0 && ((par.ends >> lane) & 1)) {
+          const float x = par.end[lane];
           if (x != -INFINITY) st = RowStat{x, 1.0f, 0.0f};
         }
         int i = tid;
@@ -562,11 +647,10 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
           st = warp_stat(RowStat{o.x, o.y, o.z}, c);
         }
         if (tid == 0) sh.stat[slot] = st;
-        const float gr = sh.par[slot].g;
-        r = DISTILL ? row_coef(st, c, gr / st.l, 0.0f)
-                    : token_coef(st, c, gr, sh.par[slot].h, HAS_B);
+        r = DISTILL ? row_coef(st, c, par.g * (1.0f / st.l), 0.0f)
+                    : token_coef(st, c, par.g, par.h, HAS_B);
       }
-      unsigned char *out = po + g.first + 16 * static_cast<int64_t>(g.u0);
+      unsigned char *out = par.out;
       if (kind == kRowGrad && VEC) {
         auto write = [&](auto fused) {
           int i = tid;
@@ -592,10 +676,6 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
           L::store(out, j, kind == kRowGrad ? grad_scalar<HAS_B>(L::load(buf, j), r)
                                             : kind == kRowNan ? nan : 0.0f);
       }
-      if (warp == 0 && end)
-        L::store(po, lane < g.head ? lane : a.cols - g.tail + lane - g.head,
-                 kind == kRowGrad ? grad_scalar<HAS_B>(sh.par[slot].ends[lane], r)
-                                  : kind == kRowNan ? nan : 0.0f);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.done[slot]);
     }
@@ -624,13 +704,16 @@ struct StagedShape {
   uint32_t buf_bytes;
 };
 
-// Threads for about 8 units (64 bf16 logits) each, in whole fours of units; as
+// Workers for about 10 units (80 bf16 logits) each: fewer units leave more of the
+// time to what every thread does once a row, more of them too few warps to cover
+// the latencies (bf16 [4096, 50257], 6283 units: 320 workers 128.8 us, 512 126.1, 640
+// 126.0, 800 131.0).  As
 // many CTAs an SM as their registers and two buffers each leave room for, and up to four buffers where the room is there.
 StagedShape staged_shape(int64_t cols, int es, int cluster, bool distill, const DevInfo &info) {
   StagedShape sh;
   sh.buf_bytes = static_cast<uint32_t>(staged_buf_bytes(cols, es, cluster));
   const int64_t units = sh.buf_bytes / 16;
-  int64_t workers = (units / 8 + 31) / 32 * 32;
+  int64_t workers = (units / 10 + 31) / 32 * 32;
   workers = workers < 64 ? 64 : workers > kMaxThreads - 32 ? kMaxThreads - 32 : workers;
   sh.threads = static_cast<int>(workers) + 32;
   const int64_t room = staged_smem(distill, info.max_smem_optin);

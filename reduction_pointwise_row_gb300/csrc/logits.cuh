@@ -218,23 +218,44 @@ struct Teacher {
   bool bad;  // some index is past the row; the same in every lane
 };
 
+// The entries of a row as they are in memory, and the student's logits at them:
+// two steps of loads, so that a caller can have others in flight between.
+struct TeacherRaw {
+  int64_t idx[kTopPerLane];
+  float z[kTopPerLane], x[kTopPerLane];
+};
+
+__device__ __forceinline__ void teacher_fetch(TeacherRaw &t, const int64_t *index, const float *z,
+                                              int k) {
+#pragma unroll
+  for (int i = 0; i < kTopPerLane; ++i) {
+    const int e = (threadIdx.x & 31) + 32 * i;
+    t.idx[i] = e < k ? index[e] : -1;
+    t.z[i] = e < k ? z[e] : 0.0f;
+  }
+}
+
 template <bool F32>
-__device__ __forceinline__ Teacher teacher_load(const int64_t *index, const float *z, int k,
-                                                const void *row, int64_t cols, float temperature) {
+__device__ __forceinline__ void teacher_gather(TeacherRaw &t, const void *row, int64_t cols) {
+#pragma unroll
+  for (int i = 0; i < kTopPerLane; ++i)
+    t.x[i] = t.idx[i] >= 0 && t.idx[i] < cols ? Logits<F32>::load(row, t.idx[i]) : 0.0f;
+}
+
+__device__ __forceinline__ Teacher teacher_finish(const TeacherRaw &raw, int64_t cols,
+                                                  float temperature) {
   Teacher t;
-  const int lane = threadIdx.x & 31;
   float zv[kTopPerLane], zm = -INFINITY;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < kTopPerLane; ++i) {
-    const int e = lane + 32 * i;
-    t.idx[i] = e < k ? index[e] : -1;
-    zv[i] = t.idx[i] >= 0 ? z[e] : -INFINITY;
+    t.idx[i] = raw.idx[i];
+    t.x[i] = raw.x[i];
+    zv[i] = t.idx[i] >= 0 ? raw.z[i] : -INFINITY;
     bad |= t.idx[i] >= cols;
-    t.x[i] = t.idx[i] >= 0 && t.idx[i] < cols ? Logits<F32>::load(row, t.idx[i]) : 0.0f;
     zm = max_nan(zm, zv[i]);
   }
-  zm = warp_max_nan(zm);
+  zm = warp_max(zm);
   t.bad = __any_sync(0xffffffffu, bad);
   t.any = zm != -INFINITY;
   float sum = 0.0f;
@@ -254,6 +275,15 @@ __device__ __forceinline__ Teacher teacher_load(const int64_t *index, const floa
       t.logq[i] -= logsum;
     }
   return t;
+}
+
+template <bool F32>
+__device__ __forceinline__ Teacher teacher_load(const int64_t *index, const float *z, int k,
+                                                const void *row, int64_t cols, float temperature) {
+  TeacherRaw raw;
+  teacher_fetch(raw, index, z, k);
+  teacher_gather<F32>(raw, row, cols);
+  return teacher_finish(raw, cols, temperature);
 }
 
 // T^2 sum q (log q - log p) with log p = (x - m) / T - log l; entries without
