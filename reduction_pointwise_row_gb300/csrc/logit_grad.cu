@@ -316,17 +316,19 @@ __global__ void __launch_bounds__(kT, 2) logit_grad_looped(LogitsBackward a) {
 //
 // A persistent grid of clusters of C CTAs; a cluster takes rows c, c + clusters, ...
 // CTA q of C holds the row's 16-byte units [n q / C, n (q + 1) / C) in one of the
-// `nbuf` buffers of its ring.  All warps but the last (the workers) fold the run's
-// units into the statistics and, after the CTA's and the cluster's merge, write
-// the gradient from shared memory; a worker goes on to the next row when its own
-// part of a row is written, so one row's writing overlaps the next one's folding.
-// The last warp keeps them supplied, two rows ahead: it reads a row's token,
-// upstream gradients, ragged ends and teacher entries, and when a row's workers
-// are done it refills their buffer and writes the loss and the elements with a term of
-// their own.  (With the helper's work between two barriers of the row all waited
-// for it: bf16 [4096, 50257] with 64 entries 237 us.)  Every wait is on an mbarrier
-// and bounded; the cluster's statistics travel by st.async, which does not wait for
-// the row's stores as a cluster barrier's release does.
+// `nbuf` buffers of its ring.  All warps but the last few (the workers) fold the
+// run's units into the statistics and, after the CTA's and the cluster's merge,
+// write the gradient from shared memory; a worker goes on to the next row when its
+// own part of a row is written, so one row's writing overlaps the next one's
+// folding.  The last warps (the helpers) keep them supplied, each with every H-th
+// row: a helper reads a row's token, upstream gradients, ragged ends and teacher
+// entries H rows ahead, and when a row's workers are done it refills their buffer
+// and writes the loss and the elements with a term of their own.  A helper's
+// row takes 6-7 us with teacher entries (dependent loads and one warp's
+// arithmetic), so one of them would be the bound: bf16 [4096, 50257] with 64
+// entries, H = 1: 187 us.  Every wait is on an mbarrier and bounded; the cluster's
+// statistics travel by st.async, which does not wait for the row's stores as a
+// cluster barrier's release does.
 
 constexpr int kMaxBufs = 4;
 constexpr int kMaxThreads = 832;  // 72 registers a thread
@@ -343,18 +345,24 @@ struct RowParams {
   float end[32];       // the head's and then the tail's logits
 };
 
+// Helper warps, and rows that they prepare ahead.
+template <bool DISTILL>
+constexpr int kHelpers = DISTILL ? 4 : 2;
+
 template <bool DISTILL>
 struct StagedShared {
-  uint64_t full[kMaxBufs];  // a buffer's copy has landed
-  uint64_t ready[2];        // a row's parameters are there
-  uint64_t done[2];         // a row's workers have written it
+  static constexpr int H = kHelpers<DISTILL>;
+  uint64_t full[kMaxBufs];  // a buffer's copy has landed (or none was needed)
+  uint64_t ready[H];        // a row's parameters are there
+  uint64_t done[H];         // a row's workers have written it
   uint64_t merged[2];       // the cluster's statistics are there
   RowStat red[2][kMaxThreads / 32];
   float4 part[2][kMaxCluster];
-  RowStat stat[2];  // the row's, for the helper
-  RowParams par[2];
-  TeacherShared teacher[DISTILL ? 2 : 1];
-  EntryTable table;
+  RowStat stat[H];  // the row's, for its helper
+  RowParams par[H];
+  TeacherShared teacher[DISTILL ? H : 1];
+  EntryTable table[DISTILL ? H : 1];
+  int gave_up;  // a wait ran out
 };
 
 struct UnitGeom {
@@ -408,10 +416,13 @@ __device__ __forceinline__ void worker_barrier(int workers) {
   asm volatile("bar.sync 1, %0;" ::"r"(workers) : "memory");
 }
 
-// A bounded wait; after one that ran out, nothing is waited for any more.
-__device__ __forceinline__ void wait_for(uint64_t *bar, uint32_t parity, bool &ok, int *err) {
+// A bounded wait; after one that ran out, its thread waits for nothing any more
+// and the CTA's helpers copy nothing more.
+__device__ __forceinline__ void wait_for(uint64_t *bar, uint32_t parity, bool &ok, int *gave_up,
+                                         int *err) {
   if (!ok || mbar_wait_bounded(bar, parity, kWaitBudget)) return;
   ok = false;
+  *reinterpret_cast<volatile int *>(gave_up) = 1;
   atomicCAS(err, 0, FR_DEVERR_TIMEOUT);
 }
 
@@ -424,7 +435,8 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
   extern __shared__ __align__(128) unsigned char bufs[];  // [nbuf][buf_bytes]
   __shared__ StagedShared<DISTILL> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int workers = static_cast<int>(blockDim.x) - 32, helper = workers >> 5;  // the last warp
+  constexpr int H = kHelpers<DISTILL>;
+  const int workers = static_cast<int>(blockDim.x) - 32 * H, worker_warps = workers >> 5;
   const uint32_t C = 1u << lg;
   const uint32_t q = cluster_ctarank();
   const int64_t row0 = cluster_id_x(), stride = ncluster_x();
@@ -433,11 +445,12 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
   const unsigned char *logits = static_cast<const unsigned char *>(a.logits);
   if (tid == 0) {
     for (int b = 0; b < nbuf; ++b) mbar_init(&sh.full[b], 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < H; ++i) {
       mbar_init(&sh.ready[i], 1);
-      mbar_init(&sh.done[i], helper);
-      mbar_init(&sh.merged[i], 1);
+      mbar_init(&sh.done[i], worker_warps);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.merged[i], 1);
+    sh.gave_up = 0;
     mbar_init_fence();
   }
   if (C > 1) {  // the peers' barriers are initialised before anything is sent
@@ -448,20 +461,27 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
   }
   bool ok = true;
 
-  if (warp == helper) {
+  if (warp >= worker_warps) {
+    const int slot = warp - worker_warps;  // of the rows k = slot, slot + H, ... of the cluster
     const uint64_t policy = l2_evict_first_policy();
-    uint32_t issued = 0, ever = 0;  // per buffer: copies issued mod 2; any
-    auto issue = [&](int64_t row, int b) {
+    int64_t last_k = -1;  // the last row that this helper's lane 0 copied
+    // Row k of the cluster into its buffer, or the word that nothing is needed.
+    auto issue = [&](int64_t k, bool wanted) {
+      const int64_t row = row0 + k * stride;
+      const int b = static_cast<int>(k % nbuf);
       const unsigned char *pr = logits + row * a.ld * L::ES;
       const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, lg);
-      const uint32_t bytes = 16u * static_cast<uint32_t>(g.u1 - g.u0);
-      if (bytes == 0 || lane != 0) return;
+      const uint32_t bytes = wanted ? 16u * static_cast<uint32_t>(g.u1 - g.u0) : 0;
+      if (lane != 0) return;
+      if (bytes == 0) {
+        mbar_arrive(&sh.full[b]);
+        return;
+      }
       fence_proxy_async_smem();
       mbar_arrive_expect_tx(&sh.full[b], bytes);
       bulk_copy_g2s(bufs + static_cast<size_t>(b) * buf_bytes,
                     pr + g.first + 16 * static_cast<int64_t>(g.u0), bytes, &sh.full[b], policy);
-      issued ^= 1u << b;
-      ever |= 1u << b;
+      last_k = k;
     };
     auto token_of = [&](int64_t row) -> int64_t {
       return !DISTILL && a.token && row < a.rows ? a.token[row] : -1;
@@ -498,7 +518,7 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
         if constexpr (HAS_B) f.h = a.dentropy[row * a.dentropy_stride];
       }
     };
-    auto publish = [&](int64_t row, int slot) {
+    auto publish = [&](int64_t row) {
       if (row >= a.rows) return;
       const unsigned char *pr = logits + row * a.ld * L::ES;
       const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, lg);
@@ -507,7 +527,7 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
       if constexpr (DISTILL) {
         const Teacher t = teacher_finish(f.teacher, a.cols, a.temperature);
         kind = t.bad ? kRowNan : t.any ? kRowGrad : kRowZero;
-        teacher_share(t, a.top, sh.teacher[slot], sh.table);
+        teacher_share(t, a.top, sh.teacher[slot], sh.table[slot]);
       } else {
         kind = token_kind<HAS_B>(a, f.token);
         if (kind == kRowGrad && a.token && f.token != a.ignore_index)
@@ -531,29 +551,27 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.ready[slot]);
     };
-    for (int b = 0; b < nbuf; ++b) {
-      const int64_t row = row0 + b * stride;
-      if (row < a.rows && wanted(token_of(row))) issue(row, b);
+    const int64_t mine = row0 + slot * stride, step = H * stride;  // this helper's rows
+    for (int64_t k = slot; k < nbuf; k += H) {
+      const int64_t row = row0 + k * stride;
+      if (row < a.rows) issue(k, wanted(token_of(row)));
     }
-    for (int i = 0; i < 2; ++i) {
-      fetch_entries(row0 + i * stride);
-      fetch(row0 + i * stride, token_of(row0 + i * stride));
-      publish(row0 + i * stride, i);
-    }
-    fetch_entries(row0 + 2 * stride);
-    int64_t ahead_token = token_of(row0 + 2 * stride);
-    int64_t refill_token = token_of(row0 + nbuf * stride);
-    int b = 0;
-    uint32_t k = 0;
-    for (int64_t row = row0; row < a.rows; row += stride, ++k, b = b + 1 == nbuf ? 0 : b + 1) {
-      const int slot = k & 1;
-      const int64_t refill = row + nbuf * stride, ahead = row + 2 * stride;
-      const bool refill_wanted = refill < a.rows && wanted(refill_token);
+    fetch_entries(mine);
+    fetch(mine, token_of(mine));
+    publish(mine);
+    fetch_entries(mine + step);
+    int64_t ahead_token = token_of(mine + step);
+    int64_t refill_token = token_of(mine + nbuf * stride);
+    uint32_t turn = 0;
+    for (int64_t row = mine, k = slot; row < a.rows; row += step, k += H, ++turn) {
+      const int64_t refill = row + nbuf * stride, ahead = row + step;
+      const bool refill_wanted = wanted(refill_token);
       fetch(ahead, ahead_token);
-      ahead_token = token_of(ahead + stride);
-      refill_token = token_of(refill + stride);
-      wait_for(&sh.done[slot], (k >> 1) & 1, ok, a.err);
-      if (ok && refill_wanted) issue(refill, b);
+      ahead_token = token_of(ahead + step);
+      refill_token = token_of(refill + step);
+      wait_for(&sh.done[slot], turn & 1, ok, &sh.gave_up, a.err);
+      const bool up = *reinterpret_cast<volatile int *>(&sh.gave_up) == 0;
+      if (refill < a.rows) issue(k + nbuf, up && refill_wanted);
       const RowParams &p = sh.par[slot];
       const RowStat st = sh.stat[slot];
       const unsigned char *pr = logits + row * a.ld * L::ES;
@@ -588,27 +606,24 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
       }
       if (a.loss && q == 0 && lane == 0) a.loss[row] = loss;
       __syncwarp();
-      publish(ahead, slot);
-      fetch_entries(ahead + stride);
+      publish(ahead);
+      fetch_entries(ahead + step);
     }
-    if (lane == 0)  // done with, unless a worker gave up: no copy may outlive the CTA
-      for (int i = 0; i < nbuf; ++i)
-        if ((ever >> i) & 1) mbar_wait_bounded(&sh.full[i], ((issued >> i) & 1) ^ 1, kWaitBudget);
+    // Every copy was waited for by the workers, unless one gave up: then this
+    // helper waits (bounded) for those it issued last, as none may outlive the CTA.
+    if (*reinterpret_cast<volatile int *>(&sh.gave_up) != 0)
+      for (int64_t k = last_k, i = 0; k >= 0 && i < kMaxBufs; k -= H, ++i)
+        mbar_wait_bounded(&sh.full[k % nbuf], static_cast<uint32_t>(k / nbuf) & 1, kWaitBudget);
   } else {
-    uint32_t phases = 0;  // bit b: parity that the next wait on buffer b takes
-    uint32_t merges = 0;  // bit slot: the same for the cluster's statistics
-    int b = 0;
-    uint32_t k = 0;
-    for (int64_t row = row0; row < a.rows; row += stride, ++k, b = b + 1 == nbuf ? 0 : b + 1) {
-      const int slot = k & 1;
+    uint32_t merges = 0;  // bit i: parity that the next wait on merged[i] takes
+    int b = 0, slot = 0;
+    uint32_t lap = 0, turn = 0, k = 0;  // times through the buffers, the slots
+    for (int64_t row = row0; row < a.rows; row += stride, ++k) {
       const unsigned char *buf = bufs + static_cast<size_t>(b) * buf_bytes;
-      wait_for(&sh.ready[slot], (k >> 1) & 1, ok, a.err);
+      wait_for(&sh.ready[slot], turn & 1, ok, &sh.gave_up, a.err);
       const RowParams &par = sh.par[slot];
       const int kind = par.kind, n = par.n;
-      if (n > 0 && (DISTILL || kind == kRowGrad)) {
-        wait_for(&sh.full[b], (phases >> b) & 1, ok, a.err);
-        phases ^= 1u << b;
-      }
+      wait_for(&sh.full[b], lap & 1, ok, &sh.gave_up, a.err);
       RowCoef r{};
       RowStat st = stat_empty();
       if (kind == kRowGrad) {
@@ -627,23 +642,24 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
           stat_fold<F32, HAS_B, 1>(st, v, L::max(v), c);
         }
         st = warp_stat(st, c);
-        if (lane == 0) sh.red[slot][warp] = st;
+        if (lane == 0) sh.red[k & 1][warp] = st;
       }
       worker_barrier(workers);  // for every row: a wait that ran out leaves no one behind
       if (kind == kRowGrad) {
-        st = warp_stat(lane < helper ? sh.red[slot][lane] : stat_empty(), c);
+        st = warp_stat(lane < worker_warps ? sh.red[k & 1][lane] : stat_empty(), c);
         if (C > 1) {
+          const int i = k & 1;
           if (warp == 0) {
-            if (lane == 0) mbar_arrive_expect_tx(&sh.merged[slot], 16u * C);
+            if (lane == 0) mbar_arrive_expect_tx(&sh.merged[i], 16u * C);
             __syncwarp();
             if (lane < C)
-              st_async_f4(&sh.part[slot][q], &sh.merged[slot], lane,
+              st_async_f4(&sh.part[i][q], &sh.merged[i], lane,
                           make_float4(st.m, st.l, st.s, 0.0f));
           }
-          wait_for(&sh.merged[slot], (merges >> slot) & 1, ok, a.err);
-          merges ^= 1u << slot;
-          const float4 o = lane < C ? sh.part[slot][lane]
-                                    : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+          wait_for(&sh.merged[i], (merges >> i) & 1, ok, &sh.gave_up, a.err);
+          merges ^= 1u << i;
+          const float4 o =
+              lane < C ? sh.part[i][lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
           st = warp_stat(RowStat{o.x, o.y, o.z}, c);
         }
         if (tid == 0) sh.stat[slot] = st;
@@ -678,6 +694,8 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.done[slot]);
+      if (++b == nbuf) b = 0, ++lap;
+      if (++slot == H) slot = 0, ++turn;
     }
   }
   if (C > 1) {  // no CTA goes while a peer may still send to it
@@ -714,8 +732,9 @@ StagedShape staged_shape(int64_t cols, int es, int cluster, bool distill, const 
   sh.buf_bytes = static_cast<uint32_t>(staged_buf_bytes(cols, es, cluster));
   const int64_t units = sh.buf_bytes / 16;
   int64_t workers = (units / 10 + 31) / 32 * 32;
-  workers = workers < 64 ? 64 : workers > kMaxThreads - 32 ? kMaxThreads - 32 : workers;
-  sh.threads = static_cast<int>(workers) + 32;
+  const int helpers = 32 * (distill ? kHelpers<true> : kHelpers<false>);
+  workers = workers < 64 ? 64 : workers > kMaxThreads - helpers ? kMaxThreads - helpers : workers;
+  sh.threads = static_cast<int>(workers) + helpers;
   const int64_t room = staged_smem(distill, info.max_smem_optin);
   int64_t ctas = (kMaxThreads + 64) / sh.threads;
   const int64_t other = info.max_smem_optin - room + 1024;
