@@ -244,6 +244,7 @@ int backward_cluster(int64_t rows, int64_t cols, int es, bool distill, int sm_co
   int cluster = least;
   while (cluster < 8 && !fr::logit_grad_staged_ok(cols, es, cluster, distill, smem / 2)) cluster *= 2;
   while (cluster < 8 && rows * cluster * 2 <= sm_count && cols * es >= 2 * cluster * 8192) cluster *= 2;
+  if (rows > INT32_MAX) return 0;  // a CTA for every row
   return fr::logit_grad_staged_ok(cols, es, cluster, distill, smem) ? cluster : 0;
 }
 
@@ -724,7 +725,7 @@ fr_status run_backward(fr::LogitsBackward &a, fr_dtype dtype, bool distill, fr_f
                                         info.max_smem_optin)
                         : form;
   int cluster = 0;
-  if (f == FR_FORM_PERSISTENT) cluster = 1;
+  if (f == FR_FORM_PERSISTENT) cluster = a.rows <= INT32_MAX ? 1 : 0;
   else if (f == FR_FORM_SPLIT) cluster = backward_cluster(a.rows, a.cols, es, distill, info.sm_count, info.max_smem_optin, 2);
   if (f != FR_FORM_LOOPED &&
       (cluster < 1 || !fr::logit_grad_staged_ok(a.cols, es, cluster, distill, info.max_smem_optin)))

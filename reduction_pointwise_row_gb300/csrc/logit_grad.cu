@@ -111,7 +111,7 @@ __device__ __forceinline__ V8 grad_vector(const V8 &x, const RowCoef &r) {
 
 // A row's gradient is all zeros (an ignored row, a row without teacher) or all
 // NaN (a target past the row) before anything is read of it.
-enum RowKind { kRowGrad = 0, kRowZero = 1, kRowNan = 2 };
+enum RowKind { kRowGrad = 0, kRowZero = 1, kRowNan = 2, kNoRow = 3 };
 
 // What a token makes of its row.  LOGITS only: an entropy's gradient is left.
 template <bool HAS_B>
@@ -314,8 +314,11 @@ __global__ void __launch_bounds__(kT, 2) logit_grad_looped(LogitsBackward a) {
 
 // ---- staged: rows (or a cluster's runs of them) in a ring of bulk copies --------------
 //
-// A persistent grid of clusters of C CTAs; a cluster takes rows c, c + clusters, ...
-// CTA q of C holds the row's 16-byte units [n q / C, n (q + 1) / C) in one of the
+// One CTA a row (C = 1): the grid has a CTA for every row, and those that run take
+// the rows of those not yet launched, one at a time, by cluster launch control.
+// With rows dealt out in advance the SMs that the memory system serves better were
+// done 20-30 us before the last (xent_backward bf16 [4096, 50257]: 132-140 us).
+// Clusters: a persistent grid, a cluster taking rows c, c + clusters, ...  CTA q of C holds the row's 16-byte units [n q / C, n (q + 1) / C) in one of the
 // `nbuf` buffers of its ring.  All warps but the last few (the workers) fold the
 // run's units into the statistics and, after the CTA's and the cluster's merge,
 // write the gradient from shared memory; a worker goes on to the next row when its
@@ -345,9 +348,10 @@ struct RowParams {
   float end[32];       // the head's and then the tail's logits
 };
 
-// Helper warps, and rows that they prepare ahead.
+// Helper warps, and rows that they prepare ahead; a last warp finds the rows.
 template <bool DISTILL>
 constexpr int kHelpers = DISTILL ? 4 : 2;
+constexpr int kRowRing = 32;  // rows whose numbers are kept
 
 template <bool DISTILL>
 struct StagedShared {
@@ -362,6 +366,11 @@ struct StagedShared {
   RowParams par[H];
   TeacherShared teacher[DISTILL ? H : 1];
   EntryTable table[DISTILL ? H : 1];
+  // the CTA's (cluster's) rows in turn, -1 past the last
+  uint64_t named[kRowRing];  // row k's number is there
+  int64_t row[kRowRing];
+  uint4 answer;  // of the request for another row
+  uint64_t answered;
   int gave_up;  // a wait ran out
 };
 
@@ -412,8 +421,16 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-__device__ __forceinline__ void worker_barrier(int workers) {
-  asm volatile("bar.sync 1, %0;" ::"r"(workers) : "memory");
+// A barrier of the workers; whether `any` holds in one of them, in all of them.
+__device__ __forceinline__ bool worker_barrier(int workers, bool any) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n bar.red.or.pred q, 1, %1, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(workers), "r"(static_cast<uint32_t>(any))
+      : "memory");
+  return r != 0;
 }
 
 // A bounded wait; after one that ran out, its thread waits for nothing any more
@@ -426,6 +443,37 @@ __device__ __forceinline__ void wait_for(uint64_t *bar, uint32_t parity, bool &o
   atomicCAS(err, 0, FR_DEVERR_TIMEOUT);
 }
 
+// The same by a whole warp, whose lanes keep one `ok`.
+__device__ __forceinline__ void warp_wait(uint64_t *bar, uint32_t parity, bool &ok, int *gave_up,
+                                          int *err) {
+  wait_for(bar, parity, ok, gave_up, err);
+  ok = __all_sync(0xffffffffu, ok);
+}
+
+// Asks for a cluster of this grid that has not been launched, to be taken over by
+// this one; the answer arrives in shared memory, counted on `bar`.  Not to be
+// asked again once the answer was no.
+__device__ __forceinline__ void request_cluster(uint4 *answer, uint64_t *bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_addr(answer)),
+      "r"(smem_addr(bar))
+      : "memory");
+}
+// The first CTA's x index of the cluster that was taken over, -1: none was left.
+__device__ __forceinline__ int64_t requested_cluster(const uint4 *answer) {
+  uint32_t taken, x;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 a;\n ld.shared.b128 a, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n selp.u32 %0, 1, 0, p;\n"
+      " mov.u32 %1, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n}"
+      : "=r"(taken), "=r"(x)
+      : "r"(smem_addr(answer))
+      : "memory");
+  return taken ? static_cast<int64_t>(x) : -1;
+}
+
 template <bool F32, bool DISTILL, bool HAS_B, bool VEC>
 __global__ void __launch_bounds__(kMaxThreads, 1)
 logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
@@ -436,10 +484,10 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
   __shared__ StagedShared<DISTILL> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int H = kHelpers<DISTILL>;
-  const int workers = static_cast<int>(blockDim.x) - 32 * H, worker_warps = workers >> 5;
+  static_assert(2 * (H + kMaxBufs + 2) <= kRowRing, "no number is needed when its place is reused");
+  const int workers = static_cast<int>(blockDim.x) - 32 * (H + 1), worker_warps = workers >> 5;
   const uint32_t C = 1u << lg;
   const uint32_t q = cluster_ctarank();
-  const int64_t row0 = cluster_id_x(), stride = ncluster_x();
   const float c = DISTILL ? kLog2e / a.temperature : kLog2e;
   const float nan = __int_as_float(0x7fc00000);
   const unsigned char *logits = static_cast<const unsigned char *>(a.logits);
@@ -450,6 +498,8 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
       mbar_init(&sh.done[i], worker_warps);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&sh.merged[i], 1);
+    for (int i = 0; i < kRowRing; ++i) mbar_init(&sh.named[i], 1);
+    mbar_init(&sh.answered, 1);
     sh.gave_up = 0;
     mbar_init_fence();
   }
@@ -461,50 +511,91 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
   }
   bool ok = true;
 
-  if (warp >= worker_warps) {
+  if (warp == worker_warps + H) {
+    if (lane == 0) {
+      // names the rows: each when the row two before has landed, so that no CTA
+      // takes many at the start (the row before, with one buffer: the row named
+      // last must not land in the same one before this looks)
+      const int back = nbuf > 1 ? 2 : 1;
+      int64_t row = cluster_id_x();
+      auto name = [&](int k) {
+        sh.row[k % kRowRing] = row;
+        mbar_arrive(&sh.named[k % kRowRing]);
+      };
+      int k = 0;
+      if (row >= a.rows) row = -1;
+      while (row >= 0) {
+        name(k++);
+        if (k >= back)
+          wait_for(&sh.full[(k - back) % nbuf], ((k - back) / nbuf) & 1, ok, &sh.gave_up, a.err);
+        if (!ok) {
+          row = -1;
+        } else if (C > 1) {
+          row += ncluster_x();
+          if (row >= a.rows) row = -1;
+        } else {
+          fence_proxy_async_smem();  // the last answer was read
+          mbar_arrive_expect_tx(&sh.answered, 16);
+          request_cluster(&sh.answer, &sh.answered);
+          wait_for(&sh.answered, (k - 1) & 1, ok, &sh.gave_up, a.err);
+          row = ok ? requested_cluster(&sh.answer) : -1;
+        }
+      }
+      for (int i = 0; i < H + kMaxBufs + 1; ++i) name(k++);
+    }
+  } else if (warp >= worker_warps) {
     const int slot = warp - worker_warps;  // of the rows k = slot, slot + H, ... of the cluster
     const uint64_t policy = l2_evict_first_policy();
-    int64_t last_k = -1;  // the last row that this helper's lane 0 copied
-    // Row k of the cluster into its buffer, or the word that nothing is needed.
-    auto issue = [&](int64_t k, bool wanted) {
-      const int64_t row = row0 + k * stride;
-      const int b = static_cast<int>(k % nbuf);
+    int last_k = -1;  // the last row that this helper copied
+    auto row_of = [&](int k) -> int64_t {
+      warp_wait(&sh.named[k % kRowRing], (k / kRowRing) & 1, ok, &sh.gave_up, a.err);
+      return ok ? sh.row[k % kRowRing] : -1;
+    };
+    // A copy of row k of the cluster into its buffer; no bytes: nothing is needed.
+    struct Copy {
+      const unsigned char *src;
+      uint32_t bytes;
+      int b;
+    };
+    auto copy_of = [&](int64_t row, int k, bool wanted) {
+      if (row < 0) return Copy{nullptr, 0, k % nbuf};
       const unsigned char *pr = logits + row * a.ld * L::ES;
       const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, lg);
-      const uint32_t bytes = wanted ? 16u * static_cast<uint32_t>(g.u1 - g.u0) : 0;
+      return Copy{pr + g.first + 16 * static_cast<int64_t>(g.u0),
+                  wanted ? 16u * static_cast<uint32_t>(g.u1 - g.u0) : 0, k % nbuf};
+    };
+    auto issue = [&](const Copy &c, int k) {
       if (lane != 0) return;
-      if (bytes == 0) {
-        mbar_arrive(&sh.full[b]);
+      if (c.bytes == 0) {
+        mbar_arrive(&sh.full[c.b]);
         return;
       }
       fence_proxy_async_smem();
-      mbar_arrive_expect_tx(&sh.full[b], bytes);
-      bulk_copy_g2s(bufs + static_cast<size_t>(b) * buf_bytes,
-                    pr + g.first + 16 * static_cast<int64_t>(g.u0), bytes, &sh.full[b], policy);
+      mbar_arrive_expect_tx(&sh.full[c.b], c.bytes);
+      bulk_copy_g2s(bufs + static_cast<size_t>(c.b) * buf_bytes, c.src, c.bytes, &sh.full[c.b],
+                    policy);
       last_k = k;
     };
     auto token_of = [&](int64_t row) -> int64_t {
-      return !DISTILL && a.token && row < a.rows ? a.token[row] : -1;
+      return !DISTILL && a.token && row >= 0 ? a.token[row] : -1;
     };
     auto wanted = [&](int64_t token) {
       return DISTILL || token_kind<HAS_B>(a, token) == kRowGrad;
     };
     // A row's parameters are fetched (loads in flight) and, later, published.
     struct Fetched {
-      TeacherRaw teacher;  // its entries are fetched a row earlier still
+      TeacherRaw teacher;
       int64_t token;
       float g, h, xt, end;
     } f;
-    auto fetch_entries = [&](int64_t row) {
-      if (DISTILL && row < a.rows)
-        teacher_fetch(f.teacher, a.index + row * a.ldt, a.teacher + row * a.ldt, a.top);
-    };
     auto fetch = [&](int64_t row, int64_t token) {
-      if (row >= a.rows) return;
+      if (row < 0) return;
       const unsigned char *pr = logits + row * a.ld * L::ES;
       const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, lg);
       f.token = token;
       f.g = f.h = f.xt = f.end = 0.0f;
+      if constexpr (DISTILL)
+        teacher_fetch(f.teacher, a.index + row * a.ldt, a.teacher + row * a.ldt, a.top);
       if (lane < g.head) f.end = L::load(pr, lane);
       else if (lane < g.head + g.tail) f.end = L::load(pr, a.cols - g.tail + lane - g.head);
       if constexpr (DISTILL) {
@@ -519,10 +610,16 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
       }
     };
     auto publish = [&](int64_t row) {
-      if (row >= a.rows) return;
+      RowParams &p = sh.par[slot];
+      if (row < 0) {
+        if (lane == 0) {
+          p.kind = kNoRow;
+          mbar_arrive(&sh.ready[slot]);
+        }
+        return;
+      }
       const unsigned char *pr = logits + row * a.ld * L::ES;
       const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, lg);
-      RowParams &p = sh.par[slot];
       int kind, token = -1;
       if constexpr (DISTILL) {
         const Teacher t = teacher_finish(f.teacher, a.cols, a.temperature);
@@ -551,27 +648,22 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.ready[slot]);
     };
-    const int64_t mine = row0 + slot * stride, step = H * stride;  // this helper's rows
-    for (int64_t k = slot; k < nbuf; k += H) {
-      const int64_t row = row0 + k * stride;
-      if (row < a.rows) issue(k, wanted(token_of(row)));
-    }
-    fetch_entries(mine);
-    fetch(mine, token_of(mine));
-    publish(mine);
-    fetch_entries(mine + step);
-    int64_t ahead_token = token_of(mine + step);
-    int64_t refill_token = token_of(mine + nbuf * stride);
-    uint32_t turn = 0;
-    for (int64_t row = mine, k = slot; row < a.rows; row += step, k += H, ++turn) {
-      const int64_t refill = row + nbuf * stride, ahead = row + step;
-      const bool refill_wanted = wanted(refill_token);
-      fetch(ahead, ahead_token);
-      ahead_token = token_of(ahead + step);
-      refill_token = token_of(refill + step);
-      wait_for(&sh.done[slot], turn & 1, ok, &sh.gave_up, a.err);
-      const bool up = *reinterpret_cast<volatile int *>(&sh.gave_up) == 0;
-      if (refill < a.rows) issue(k + nbuf, up && refill_wanted);
+    auto first_copy = [&](int64_t row, int k) {
+      if (row >= 0) issue(copy_of(row, k, wanted(token_of(row))), k);
+    };
+    int k = slot;  // of this helper's rows in turn
+    int64_t row = row_of(k);
+    if (k < nbuf) first_copy(row, k);
+    fetch(row, token_of(row));
+    publish(row);
+    for (int i = k + H; i < nbuf; i += H) first_copy(row_of(i), i);
+    for (uint32_t turn = 0; row >= 0; ++turn) {
+      const int64_t refill = row_of(k + nbuf);
+      const Copy next = copy_of(refill, k + nbuf, wanted(token_of(refill)));
+      warp_wait(&sh.done[slot], turn & 1, ok, &sh.gave_up, a.err);
+      if (refill >= 0)
+        issue(*reinterpret_cast<volatile int *>(&sh.gave_up) == 0 ? next : Copy{nullptr, 0, next.b},
+              k + nbuf);
       const RowParams &p = sh.par[slot];
       const RowStat st = sh.stat[slot];
       const unsigned char *pr = logits + row * a.ld * L::ES;
@@ -605,25 +697,29 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
         }
       }
       if (a.loss && q == 0 && lane == 0) a.loss[row] = loss;
+      k += H;
+      row = row_of(k);
+      fetch(row, token_of(row));
       __syncwarp();
-      publish(ahead);
-      fetch_entries(ahead + step);
+      publish(row);
     }
     // Every copy was waited for by the workers, unless one gave up: then this
     // helper waits (bounded) for those it issued last, as none may outlive the CTA.
     if (*reinterpret_cast<volatile int *>(&sh.gave_up) != 0)
-      for (int64_t k = last_k, i = 0; k >= 0 && i < kMaxBufs; k -= H, ++i)
-        mbar_wait_bounded(&sh.full[k % nbuf], static_cast<uint32_t>(k / nbuf) & 1, kWaitBudget);
+      for (int i = 0; last_k >= 0 && i < kMaxBufs; last_k -= H, ++i)
+        mbar_wait_bounded(&sh.full[last_k % nbuf], (last_k / nbuf) & 1, kWaitBudget);
   } else {
     uint32_t merges = 0;  // bit i: parity that the next wait on merged[i] takes
     int b = 0, slot = 0;
     uint32_t lap = 0, turn = 0, k = 0;  // times through the buffers, the slots
-    for (int64_t row = row0; row < a.rows; row += stride, ++k) {
+    for (;; ++k) {
       const unsigned char *buf = bufs + static_cast<size_t>(b) * buf_bytes;
-      wait_for(&sh.ready[slot], turn & 1, ok, &sh.gave_up, a.err);
+      warp_wait(&sh.ready[slot], turn & 1, ok, &sh.gave_up, a.err);
       const RowParams &par = sh.par[slot];
-      const int kind = par.kind, n = par.n;
-      wait_for(&sh.full[b], lap & 1, ok, &sh.gave_up, a.err);
+      int kind = ok ? par.kind : kNoRow;
+      if (kind != kNoRow) warp_wait(&sh.full[b], lap & 1, ok, &sh.gave_up, a.err);
+      if (!ok) kind = kNoRow;
+      const int n = kind != kNoRow ? par.n : 0;
       RowCoef r{};
       RowStat st = stat_empty();
       if (kind == kRowGrad) {
@@ -644,7 +740,8 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
         st = warp_stat(st, c);
         if (lane == 0) sh.red[k & 1][warp] = st;
       }
-      worker_barrier(workers);  // for every row: a wait that ran out leaves no one behind
+      // every worker comes here whatever it saw, and all of them stop together
+      if (worker_barrier(workers, !ok) || kind == kNoRow) break;
       if (kind == kRowGrad) {
         st = warp_stat(lane < worker_warps ? sh.red[k & 1][lane] : stat_empty(), c);
         if (C > 1) {
@@ -656,7 +753,7 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
               st_async_f4(&sh.part[i][q], &sh.merged[i], lane,
                           make_float4(st.m, st.l, st.s, 0.0f));
           }
-          wait_for(&sh.merged[i], (merges >> i) & 1, ok, &sh.gave_up, a.err);
+          warp_wait(&sh.merged[i], (merges >> i) & 1, ok, &sh.gave_up, a.err);
           merges ^= 1u << i;
           const float4 o =
               lane < C ? sh.part[i][lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
@@ -732,7 +829,7 @@ StagedShape staged_shape(int64_t cols, int es, int cluster, bool distill, const 
   sh.buf_bytes = static_cast<uint32_t>(staged_buf_bytes(cols, es, cluster));
   const int64_t units = sh.buf_bytes / 16;
   int64_t workers = (units / 10 + 31) / 32 * 32;
-  const int helpers = 32 * (distill ? kHelpers<true> : kHelpers<false>);
+  const int helpers = 32 * ((distill ? kHelpers<true> : kHelpers<false>) + 1);
   workers = workers < 64 ? 64 : workers > kMaxThreads - helpers ? kMaxThreads - helpers : workers;
   sh.threads = static_cast<int>(workers) + helpers;
   const int64_t room = staged_smem(distill, info.max_smem_optin);
@@ -764,9 +861,13 @@ cudaError_t launch_form(const LogitsBackward &a, int cluster, bool vec32, bool v
       cudaSuccess)
     return e;
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
-  int64_t clusters = static_cast<int64_t>(per_sm) * info.sm_count / cluster;
-  if (clusters < 1) clusters = 1;
-  if (clusters > a.rows) clusters = a.rows;
+  // a CTA for every row, or as many clusters as the device holds
+  int64_t clusters = a.rows;
+  if (cluster > 1) {
+    clusters = static_cast<int64_t>(per_sm) * info.sm_count / cluster;
+    if (clusters < 1) clusters = 1;
+    if (clusters > a.rows) clusters = a.rows;
+  }
   return launch_k(kern, dim3(static_cast<unsigned>(clusters * cluster)), dim3(sh.threads), smem,
                   s, cluster, a, sh.buf_bytes, sh.nbuf, __builtin_ctz(cluster));
 }
