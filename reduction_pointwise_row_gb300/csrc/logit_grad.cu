@@ -864,9 +864,23 @@ cudaError_t launch_form(const LogitsBackward &a, int cluster, bool vec32, bool v
   // a CTA for every row, or as many clusters as the device holds
   int64_t clusters = a.rows;
   if (cluster > 1) {
-    clusters = static_cast<int64_t>(per_sm) * info.sm_count / cluster;
-    if (clusters < 1) clusters = 1;
-    if (clusters > a.rows) clusters = a.rows;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+    cfg.blockDim = dim3(sh.threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int held = 0;
+    if ((e = resident_clusters(&held, reinterpret_cast<const void *>(kern), cfg,
+                               static_cast<unsigned>(cluster))) != cudaSuccess)
+      return e;
+    if (held < 1) return cudaErrorInvalidConfiguration;
+    clusters = held < a.rows ? held : a.rows;
   }
   return launch_k(kern, dim3(static_cast<unsigned>(clusters * cluster)), dim3(sh.threads), smem,
                   s, cluster, a, sh.buf_bytes, sh.nbuf, __builtin_ctz(cluster));
