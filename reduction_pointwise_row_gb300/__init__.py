@@ -376,9 +376,17 @@ def fr_xent_mean_from_parts(workspace, mean=None, stream=None):
     return mean
 
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported with the first call that needs it."""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+        _LOGIT_DTYPES.update({torch.float32: DTYPES["f32"], torch.bfloat16: DTYPES["bf16"]})
+    return _TORCH
 
 
 def _nullcontext():
@@ -452,6 +460,9 @@ def fr_reduce_relu_add_sum_split_static(a, b, scale: float = 2.0, out=None, stre
 
 # ---- rows of logits: scoring, distillation, gradients ---------------------------
 
+_LOGIT_DTYPES = {}  # torch dtype -> dtype code (filled when torch is imported)
+
+
 def _need(ok: bool, what: str):
     if not ok:
         raise ValueError(what)
@@ -459,52 +470,56 @@ def _need(ok: bool, what: str):
 
 def _logits_arg(x, name: str = "logits"):
     """(rows, cols, ld, dtype code) of a matrix of logits; refuses anything else."""
-    torch = _torch()
-    _need(x.is_cuda, f"{name} must be a CUDA tensor")
-    _need(x.dtype in (torch.bfloat16, torch.float32), f"{name} must be bf16 or fp32")
-    _need(x.dim() == 2, f"{name} must have two dimensions")
+    dt = _LOGIT_DTYPES.get(x.dtype)
+    if dt is None or not x.is_cuda or x.dim() != 2:
+        raise ValueError(f"{name} must be a CUDA matrix of bf16 or fp32")
     rows, cols = x.shape
-    _need(rows > 0 and cols > 0, f"{name} must have at least one row and one column")
-    _need(cols == 1 or x.stride(1) == 1, f"rows of {name} must be contiguous")
-    # a single row has no distance to the next one (torch may report any)
-    ld = x.stride(0) if rows > 1 else cols
-    _need(ld >= cols, f"rows of {name} overlap")
-    return rows, cols, ld, DTYPES["f32" if x.dtype == torch.float32 else "bf16"]
+    ld, inner = x.stride()
+    if rows < 1 or cols < 1:
+        raise ValueError(f"{name} must have at least one row and one column")
+    if inner != 1 and cols != 1:
+        raise ValueError(f"rows of {name} must be contiguous")
+    if rows == 1:  # a single row has no distance to the next one (torch may report any)
+        ld = cols
+    elif ld < cols:
+        raise ValueError(f"rows of {name} overlap")
+    return rows, cols, ld, dt
 
 
-def _row_vector(t, name: str, rows: int, dtype):
-    _need(t.is_cuda and t.dtype == dtype, f"{name} must be a CUDA tensor of {dtype}")
-    _need(t.dim() == 1 and t.shape[0] == rows and (rows == 1 or t.stride(0) == 1),
-          f"{name} must be contiguous with one element per row")
-    return t
+def _tokens_ptr(t, name: str, rows: int):
+    """The address of int64 tokens, one per row."""
+    if not t.is_cuda or t.dtype is not _TORCH.int64 or t.shape != (rows,) or \
+            (rows > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of int64, one per row")
+    return t.data_ptr()
 
 
 def _upstream(t, name: str, rows: int) -> int:
     """The stride of an upstream gradient: fp32, one value per row or one in all."""
-    torch = _torch()
-    _need(t.is_cuda and t.dtype == torch.float32, f"{name} must be a CUDA tensor of torch.float32")
+    if not t.is_cuda or t.dtype is not _TORCH.float32:
+        raise ValueError(f"{name} must be a CUDA tensor of fp32")
     if t.numel() == 1:
         return 0
-    _need(t.dim() == 1 and t.shape[0] == rows, f"{name} must hold one value, or one per row")
+    if t.shape != (rows,):
+        raise ValueError(f"{name} must hold one value, or one per row")
     return t.stride(0)
 
 
 def _teacher_args(index, logit, rows: int):
     """(top, ldt) of a row's teacher entries."""
-    torch = _torch()
-    _need(index.is_cuda and index.dtype == torch.int64, "teacher_index must be int64 on CUDA")
-    _need(logit.is_cuda and logit.dtype == torch.float32, "teacher_logit must be fp32 on CUDA")
+    _need(index.is_cuda and index.dtype is _TORCH.int64, "teacher_index must be int64 on CUDA")
+    _need(logit.is_cuda and logit.dtype is _TORCH.float32, "teacher_logit must be fp32 on CUDA")
     _need(index.dim() == 2 and index.shape == logit.shape and index.shape[0] == rows,
           "teacher_index and teacher_logit must be [rows, top]")
     top = index.shape[1]
     _need(1 <= top <= FR_TOP_MAX, f"1 to {FR_TOP_MAX} teacher entries per row")
-    for t in (index, logit):
-        _need(top == 1 or t.stride(1) == 1, "a row's teacher entries must be contiguous")
-    ldt = index.stride(0) if rows > 1 else top
-    _need(rows == 1 or logit.stride(0) == ldt,
-          "teacher_index and teacher_logit must have the same row stride")
-    _need(ldt >= top, "teacher rows overlap")
-    return top, ldt
+    (li, si), (lz, sz) = index.stride(), logit.stride()
+    _need(top == 1 or si == sz == 1, "a row's teacher entries must be contiguous")
+    if rows == 1:
+        return top, top
+    _need(li == lz, "teacher_index and teacher_logit must have the same row stride")
+    _need(li >= top, "teacher rows overlap")
+    return top, li
 
 
 _NO_CONTEXT = _nullcontext()
@@ -512,21 +527,20 @@ _NO_CONTEXT = _nullcontext()
 
 def _on_stream(stream):
     """Outputs made for a call belong to the stream it runs on."""
-    return _NO_CONTEXT if stream is None else _torch().cuda.stream(stream)
+    return _NO_CONTEXT if stream is None else _TORCH.cuda.stream(stream)
 
 
-def _gradient_out(x, ld: int, given):
-    """`given` after its checks, or a new matrix whose rows share the logits'
-    offset within 32 bytes (a compact matrix when theirs are compact)."""
-    torch = _torch()
+def _gradient_out(x, rows: int, cols: int, ld: int, given):
+    """(dlogits, ldd): `given` after its checks, or a new matrix whose rows share
+    the logits' offset within 32 bytes (a compact matrix when theirs are)."""
     if given is not None:
-        _need(given.shape == x.shape and given.dtype == x.dtype,
+        _need(given.shape == x.shape and given.dtype is x.dtype,
               "dlogits must have the logits' shape and dtype")
         return given, _logits_arg(given, "dlogits")[2]
-    rows, cols = x.shape
-    per = 32 // x.element_size()
-    ldd = cols + (ld - cols) % per
-    return torch.empty_strided((rows, cols), (ldd, 1), dtype=x.dtype, device=x.device), ldd
+    if ld == cols:
+        return _TORCH.empty((rows, cols), dtype=x.dtype, device=x.device), cols
+    ldd = cols + (ld - cols) % (32 // x.element_size())
+    return _TORCH.empty_strided((rows, cols), (ldd, 1), dtype=x.dtype, device=x.device), ldd
 
 
 def fr_logprobs(logits, token=None, top: int = 0, ignore_index: int = -100,
@@ -541,28 +555,38 @@ def fr_logprobs(logits, token=None, top: int = 0, ignore_index: int = -100,
     top], the largest first, ties by the lower index.  All fp32 but the int64
     ``top_index``.  ``workspace``: fr_workspace_size("logprobs", ...) bytes, by
     default allocated for the call."""
-    torch = _torch()
+    torch = _TORCH or _torch()
     rows, cols, ld, dt = _logits_arg(logits)
-    _need(0 <= top <= min(cols, FR_TOP_MAX), f"top must be 0 to min(cols, {FR_TOP_MAX})")
-    _need(token is not None or want_entropy or want_lse or top > 0, "no output requested")
-    if token is not None:
-        _row_vector(token, "token", rows, torch.int64)
-    _on_current_device(logits, token)
-    dev = logits.device
+    if not 0 <= top <= min(cols, FR_TOP_MAX):
+        raise ValueError(f"top must be 0 to min(cols, {FR_TOP_MAX})")
+    _on_current_device(logits, token, workspace)
+    dev, f32 = logits.device, torch.float32
     res = {}
+    p_token = p_lp = p_ent = p_lse = p_tl = p_ti = p_ws = None
+    nws = 0
     with _on_stream(stream):
-        def out(name, want, *shape, dtype=torch.float32):
-            if want:
-                res[name] = torch.empty(*shape, dtype=dtype, device=dev)
-            return _ptr(res.get(name))
-        p = (out("logprob", token is not None, rows), out("entropy", want_entropy, rows),
-             out("lse", want_lse, rows), out("top_logprob", top > 0, rows, top),
-             out("top_index", top > 0, rows, top, dtype=torch.int64))
-        ws, nws = (None, 0)
+        if token is not None:
+            p_token = _tokens_ptr(token, "token", rows)
+            t = res["logprob"] = torch.empty(rows, dtype=f32, device=dev)
+            p_lp = t.data_ptr()
+        if want_entropy:
+            t = res["entropy"] = torch.empty(rows, dtype=f32, device=dev)
+            p_ent = t.data_ptr()
+        if want_lse:
+            t = res["lse"] = torch.empty(rows, dtype=f32, device=dev)
+            p_lse = t.data_ptr()
         if top > 0:
+            t = res["top_logprob"] = torch.empty((rows, top), dtype=f32, device=dev)
+            p_tl = t.data_ptr()
+            t = res["top_index"] = torch.empty((rows, top), dtype=torch.int64, device=dev)
+            p_ti = t.data_ptr()
             ws, nws = _workspace("logprobs", rows, cols, _DTYPE_NAMES[dt], form, dev, workspace)
-    _check(lib().fr_logprobs(_ptr(logits), _ptr(token), *p, top, rows, cols, ld, ignore_index, dt,
-                             FORMS[form], _ptr(ws), nws, _stream(stream)), "fr_logprobs")
+            p_ws = _ptr(ws)
+        _need(bool(res), "no output requested")
+    status = lib().fr_logprobs(logits.data_ptr(), p_token, p_lp, p_ent, p_lse, p_tl, p_ti, top,
+                               rows, cols, ld, ignore_index, dt, FORMS[form], p_ws, nws,
+                               _stream(stream))
+    _check(status, "fr_logprobs")
     return res
 
 
@@ -572,18 +596,18 @@ def fr_logprobs_backward(logits, token=None, dlogprob=None, dentropy=None,
     """The gradient of fr_logprobs' ``logprob`` and ``entropy`` with respect to the
     logits, from fp32 upstream gradients with one value per row or one in all
     (either may be None).  ``dlogits`` may be ``logits`` (in place)."""
+    _TORCH or _torch()
     rows, cols, ld, dt = _logits_arg(logits)
     _need(dlogprob is not None or dentropy is not None, "no upstream gradient given")
     _need(dlogprob is None or token is not None, "dlogprob needs the tokens")
-    if token is not None:
-        _row_vector(token, "token", rows, _torch().int64)
+    p_token = None if token is None else _tokens_ptr(token, "token", rows)
     gs = 0 if dlogprob is None else _upstream(dlogprob, "dlogprob", rows)
     hs = 0 if dentropy is None else _upstream(dentropy, "dentropy", rows)
     with _on_stream(stream):
-        dlogits, ldd = _gradient_out(logits, ld, dlogits)
+        dlogits, ldd = _gradient_out(logits, rows, cols, ld, dlogits)
     _on_current_device(logits, token, dlogprob, dentropy, dlogits)
-    _check(lib().fr_logprobs_backward(_ptr(logits), _ptr(token), _ptr(dlogprob), gs,
-                                      _ptr(dentropy), hs, _ptr(dlogits), rows, cols, ld, ldd,
+    _check(lib().fr_logprobs_backward(logits.data_ptr(), p_token, _ptr(dlogprob), gs,
+                                      _ptr(dentropy), hs, dlogits.data_ptr(), rows, cols, ld, ldd,
                                       ignore_index, dt, FORMS[form], _stream(stream)),
            "fr_logprobs_backward")
     return dlogits
@@ -595,15 +619,15 @@ def fr_distill(logits, teacher_index, teacher_logit, temperature: float = 1.0,
     top logits: temperature^2 KL(softmax(teacher_logit / T) || softmax(logits /
     T)) over the entries of ``teacher_index`` (int64 [rows, top], negative:
     padding) and ``teacher_logit`` (fp32 [rows, top]; log probabilities serve)."""
-    torch = _torch()
+    torch = _TORCH or _torch()
     rows, cols, ld, dt = _logits_arg(logits)
     top, ldt = _teacher_args(teacher_index, teacher_logit, rows)
     _on_current_device(logits, teacher_index, teacher_logit)
     with _on_stream(stream):
         loss = torch.empty(rows, dtype=torch.float32, device=logits.device)
-    _check(lib().fr_distill(_ptr(logits), _ptr(teacher_index), _ptr(teacher_logit), _ptr(loss),
-                            top, rows, cols, ld, ldt, temperature, dt, FORMS[form],
-                            _stream(stream)), "fr_distill")
+    _check(lib().fr_distill(logits.data_ptr(), teacher_index.data_ptr(), teacher_logit.data_ptr(),
+                            loss.data_ptr(), top, rows, cols, ld, ldt, temperature, dt,
+                            FORMS[form], _stream(stream)), "fr_distill")
     return loss
 
 
@@ -613,19 +637,21 @@ def fr_distill_backward(logits, teacher_index, teacher_logit, dloss, temperature
     same pass: a training step in one call.  Returns a dict: ``dlogits`` and
     ``loss``.  ``dloss`` holds one fp32 value per row or one in all; ``dlogits``
     may be ``logits`` (in place)."""
-    torch = _torch()
+    torch = _TORCH or _torch()
     rows, cols, ld, dt = _logits_arg(logits)
     top, ldt = _teacher_args(teacher_index, teacher_logit, rows)
     gs = _upstream(dloss, "dloss", rows)
-    res = {}
+    p_loss = None
     with _on_stream(stream):
-        res["dlogits"], ldd = _gradient_out(logits, ld, dlogits)
+        dlogits, ldd = _gradient_out(logits, rows, cols, ld, dlogits)
+        res = {"dlogits": dlogits}
         if want_loss:
-            res["loss"] = torch.empty(rows, dtype=torch.float32, device=logits.device)
-    _on_current_device(logits, teacher_index, teacher_logit, dloss, res["dlogits"])
-    _check(lib().fr_distill_backward(_ptr(logits), _ptr(teacher_index), _ptr(teacher_logit),
-                                     _ptr(dloss), gs, _ptr(res.get("loss")),
-                                     _ptr(res["dlogits"]), top, rows, cols, ld, ldd, ldt,
+            t = res["loss"] = torch.empty(rows, dtype=torch.float32, device=logits.device)
+            p_loss = t.data_ptr()
+    _on_current_device(logits, teacher_index, teacher_logit, dloss, dlogits)
+    _check(lib().fr_distill_backward(logits.data_ptr(), teacher_index.data_ptr(),
+                                     teacher_logit.data_ptr(), dloss.data_ptr(), gs, p_loss,
+                                     dlogits.data_ptr(), top, rows, cols, ld, ldd, ldt,
                                      temperature, dt, FORMS[form], _stream(stream)),
            "fr_distill_backward")
     return res
@@ -637,20 +663,21 @@ def fr_xent_backward(logits, target, dloss, ignore_index: int = -100, want_loss:
     the same pass.  Returns a dict: ``dlogits`` and ``loss``.  ``dloss`` holds one
     fp32 value per row or one in all (1 / counted rows gives the mean's
     gradient); ``dlogits`` may be ``logits`` (in place)."""
-    torch = _torch()
+    torch = _TORCH or _torch()
     rows, cols, ld, dt = _logits_arg(logits)
-    _row_vector(target, "target", rows, torch.int64)
+    p_target = _tokens_ptr(target, "target", rows)
     gs = _upstream(dloss, "dloss", rows)
-    res = {}
+    p_loss = None
     with _on_stream(stream):
-        res["dlogits"], ldd = _gradient_out(logits, ld, dlogits)
+        dlogits, ldd = _gradient_out(logits, rows, cols, ld, dlogits)
+        res = {"dlogits": dlogits}
         if want_loss:
-            res["loss"] = torch.empty(rows, dtype=torch.float32, device=logits.device)
-    _on_current_device(logits, target, dloss, res["dlogits"])
-    _check(lib().fr_xent_backward(_ptr(logits), _ptr(target), _ptr(dloss), gs,
-                                  _ptr(res.get("loss")), _ptr(res["dlogits"]), rows, cols, ld,
-                                  ldd, ignore_index, dt, FORMS[form], _stream(stream)),
-           "fr_xent_backward")
+            t = res["loss"] = torch.empty(rows, dtype=torch.float32, device=logits.device)
+            p_loss = t.data_ptr()
+    _on_current_device(logits, target, dloss, dlogits)
+    _check(lib().fr_xent_backward(logits.data_ptr(), p_target, dloss.data_ptr(), gs, p_loss,
+                                  dlogits.data_ptr(), rows, cols, ld, ldd, ignore_index, dt,
+                                  FORMS[form], _stream(stream)), "fr_xent_backward")
     return res
 
 

@@ -716,6 +716,7 @@ fr_status run_forward(fr::LogitsForward &a, fr_dtype dtype, bool distill, fr_for
 
 fr_status run_backward(fr::LogitsBackward &a, fr_dtype dtype, bool distill, fr_form form,
                        fr_stream_t stream) {
+  if (form < FR_FORM_AUTO || form > FR_FORM_SPLIT) return FR_ERR_UNSUPPORTED_FORM;
   fr::DevInfo info;
   if (fr_status st = logits_device_ok(a.cols, &info, &a.err)) return st;
   const bool f32 = dtype == FR_F32;
