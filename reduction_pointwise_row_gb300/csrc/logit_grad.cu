@@ -203,6 +203,116 @@ __device__ __forceinline__ float teacher_element(const TeacherShared &sh, int e,
   return g * (ex2((sh.x[e] - st.m) * c) * (1.0f / st.l) - sh.sum[e]);
 }
 
+// ---- held: a warp per row, the row in registers ----------------------------------------
+//
+// Rows of at most 8 KiB, 1 to 8 32-byte vectors a lane.  The staged form has a few
+// us to do once a row, which such a row's bytes do not cover (us held / staged, bf16:
+// 30000 x 1000 22.1 / 62.0; 30000 x 2048 38.9 / 80; 16000 x 4096 41.9 / 53.1, with 20
+// teacher entries 58.8 / 72.5).  For longer rows a CTA holding the row in its registers
+// was no faster than the staged form (8192 x 8192 47.4 / 45.2, 4096 x 30000 107 / 83).
+
+constexpr int kRowWarps = 4;  // rows per CTA
+constexpr int64_t kHeldVectors = 256;
+
+template <bool F32, bool DISTILL, bool HAS_B, int NV, bool VEC>
+__global__ void __launch_bounds__(32 * kRowWarps, NV > 4 ? 4 : NV > 2 ? 5 : NV > 1 ? 7 : 8)
+logit_grad_held(LogitsBackward a) {
+  pdl_enter();
+  using L = Logits<F32>;
+  __shared__ TeacherShared teachers[DISTILL ? kRowWarps : 1];
+  __shared__ EntryTable tables[DISTILL ? kRowWarps : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp;
+  if (row >= a.rows) return;
+  const float c = DISTILL ? kLog2e / a.temperature : kLog2e;
+  const float nan = __int_as_float(0x7fc00000);
+  const unsigned char *pr = static_cast<const unsigned char *>(a.logits) + row * a.ld * L::ES;
+  unsigned char *po = static_cast<unsigned char *>(a.dlogits) + row * a.ldd * L::ES;
+  const RowSplit sp = row_split(pr, a.cols, L::ES);
+  const int nvec = static_cast<int>(sp.nvec), v0 = sp.head * L::ES;
+  // everything that the row is computed from, before any of it is overwritten
+  const int64_t token = !DISTILL && a.token ? a.token[row] : -1;
+  V8 v[NV];
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+    v[u] = lane + 32 * u < nvec ? ld_v8(pr + v0 + (lane + 32 * u) * kVecBytes) : L::filler();
+  int si = -1;
+  if (lane < sp.head) si = lane;
+  else if (lane < sp.head + sp.tail) si = sp.head + nvec * L::EPV + (lane - sp.head);
+  const float sx = si >= 0 ? L::load(pr, si) : -INFINITY;
+  float g = 0.0f, h = 0.0f, xt = 0.0f;
+  int kind = kRowGrad, own = -1;
+  if constexpr (DISTILL) {
+    g = a.dloss[row * a.dloss_stride] * a.temperature;
+    const Teacher t = teacher_load<F32>(a.index + row * a.ldt, a.teacher + row * a.ldt, a.top, pr,
+                                        a.cols, a.temperature);
+    kind = t.bad ? kRowNan : t.any ? kRowGrad : kRowZero;
+    teacher_share(t, a.top, teachers[warp], tables[warp]);
+  } else {
+    kind = token_kind<HAS_B>(a, token);
+    if (kind == kRowGrad && a.token && token != a.ignore_index) {
+      own = static_cast<int>(token);
+      xt = L::load(pr, own);
+      g = a.dloss[row * a.dloss_stride] * a.dloss_sign;
+    }
+    if constexpr (HAS_B) h = a.dentropy[row * a.dentropy_stride];
+  }
+
+  RowStat st = stat_empty();
+  stat_fold<F32, HAS_B, NV>(st, v, L::max(v), c);
+  if (sx != -INFINITY) st = stat_merge(st, RowStat{sx, 1.0f, 0.0f}, c);
+  st = warp_stat(st, c);  // every lane has read its part of the row
+  if (kind == kRowNan && lane == 0) atomicCAS(a.err, 0, FR_DEVERR_BAD_TARGET);
+  const RowCoef r =
+      DISTILL ? row_coef(st, c, g * (1.0f / st.l), 0.0f) : token_coef(st, c, g, h, HAS_B);
+  const float fill = kind == kRowNan ? nan : 0.0f;
+  const uint32_t fill_w = kind == kRowNan ? (F32 ? 0x7FC00000u : 0x7FC07FC0u) : 0;
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    if (lane + 32 * u >= nvec) continue;
+    V8 y;
+    if (kind != kRowGrad) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y.w[j] = fill_w;
+    } else if (r.fused) {
+      y = grad_vector<F32, HAS_B, true>(v[u], r);
+    } else {
+      y = grad_vector<F32, HAS_B, false>(v[u], r);
+    }
+    if constexpr (VEC) {
+      st_stream_v8(po + v0 + (lane + 32 * u) * kVecBytes, y);
+    } else {
+#pragma unroll
+      for (int j = 0; j < L::EPV; ++j)
+        L::store(po, sp.head + (lane + 32 * u) * L::EPV + j, L::at(y, j));
+    }
+  }
+  if (si >= 0) L::store(po, si, kind == kRowGrad ? grad_scalar<HAS_B>(sx, r) : fill);
+  // the elements with a term of their own come after the rest
+  __syncwarp();
+  float loss = fill;
+  if (kind == kRowGrad) {
+    if constexpr (DISTILL) {
+      const TeacherShared &t = teachers[warp];
+      for (int e = lane; e < a.top; e += 32)
+        if (t.idx[e] >= 0) L::store(po, t.idx[e], teacher_element(t, e, st, c, g));
+      if (a.loss) loss = teacher_loss(t, a.top, st, a.temperature);
+    } else if (own >= 0) {
+      if (lane == 0) L::store(po, own, grad_scalar<HAS_B>(xt, r) + g);
+      loss = logf(st.l) - (xt - st.m);
+    }
+  }
+  if (a.loss && lane == 0) a.loss[row] = loss;
+}
+
+template <bool F32, bool DISTILL, bool HAS_B, int NV>
+cudaError_t launch_held(const LogitsBackward &a, bool vec, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((a.rows + kRowWarps - 1) / kRowWarps));
+  const dim3 block(32 * kRowWarps);
+  return vec ? launch_k(logit_grad_held<F32, DISTILL, HAS_B, NV, true>, grid, block, 0, s, 0, a)
+             : launch_k(logit_grad_held<F32, DISTILL, HAS_B, NV, false>, grid, block, 0, s, 0, a);
+}
+
 // ---- looped: a CTA per row, the row streamed twice ---------------------------------
 
 template <bool F32, bool DISTILL, bool HAS_B, bool VEC>
@@ -849,6 +959,13 @@ cudaError_t launch_form(const LogitsBackward &a, int cluster, bool vec32, bool v
     const dim3 g(static_cast<unsigned>(grid)), b(kT);
     return vec32 ? launch_k(logit_grad_looped<F32, DISTILL, HAS_B, true>, g, b, 0, s, 0, a)
                  : launch_k(logit_grad_looped<F32, DISTILL, HAS_B, false>, g, b, 0, s, 0, a);
+  }
+  const int64_t vectors = a.cols * (F32 ? 4 : 2) / kVecBytes;
+  if (cluster == 1 && vectors <= kHeldVectors) {
+    if (vectors <= 32) return launch_held<F32, DISTILL, HAS_B, 1>(a, vec32, s);
+    if (vectors <= 64) return launch_held<F32, DISTILL, HAS_B, 2>(a, vec32, s);
+    if (vectors <= 128) return launch_held<F32, DISTILL, HAS_B, 4>(a, vec32, s);
+    return launch_held<F32, DISTILL, HAS_B, 8>(a, vec32, s);
   }
   auto *kern = vec16 ? &logit_grad_staged<F32, DISTILL, HAS_B, true>
                      : &logit_grad_staged<F32, DISTILL, HAS_B, false>;
