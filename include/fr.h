@@ -380,8 +380,10 @@ fr_status fr_xent_mean_from_parts(const void *workspace, float *loss_mean, fr_st
  *               16-byte aligned; only the looped form with top > 0 uses it (about
  *               1/64 of the logits' bytes); may be NULL otherwise.
  *               One call at a time may use a workspace.
- * At least one output is requested.  Forms: looped (a warp per row) and split (a
- * cluster of up to 8 CTAs per row, for few rows).
+ * At least one output is requested.  Forms: persistent (a warp per row of at most
+ * 4 KiB, in registers), looped (a warp per row) and split (a cluster of up to 8
+ * CTAs per row, for few rows).  AUTO takes the looped form from 4 x SMs rows with
+ * alternatives (what fr_auto_form and fr_workspace_size assume), 8 x SMs without.
  */
 fr_status fr_logprobs(const void *logits, const int64_t *token, float *logprob, float *entropy,
                       float *lse, float *top_logprob, int64_t *top_index, int32_t top,

@@ -223,17 +223,26 @@ fr_form pick_layernorm(int64_t, int64_t cols, bool vec, bool aligned16, bool row
 
 // ---- rows of logits
 
-// CTAs per row of the forward calls' split form: the fewest whose grid fills the
-// SMs twice, while each thread still gets a 32-byte vector (past the row's head).
+// CTAs per row of the forward calls' split form: as many as leave the grid under two
+// CTAs an SM, while each thread still gets a 32-byte vector (past the row's head).
+// Measured (us, bf16 x 50257 with 20 alternatives; 1, 2, 4, 8 CTAs a row): 1 row 10.8,
+// 10.1, 8.8, 8.1; 64 rows 14.3, 14.7, 12.4, 19.1; 152 rows 14.5, 16.1, 21.2, 32.0.
 int forward_split(int64_t rows, int64_t cols, int es, int sm_count) {
   int split = 1;
-  while (split < 8 && rows * split < 2 * sm_count && cols * es >= 2 * split * 256 * 32 + 64)
+  while (split < 8 && rows * 2 * split < 2 * sm_count && cols * es >= 2 * split * 256 * 32 + 64)
     split *= 2;
   return split;
 }
 
-fr_form pick_forward(int64_t rows, int64_t, int sm_count) {
-  return rows >= 8 * static_cast<int64_t>(sm_count) ? FR_FORM_LOOPED : FR_FORM_SPLIT;
+// Rows of up to 4 KiB: a warp holds a row (us held / looped / split, bf16 with 20
+// alternatives: 4000 x 1000 11.6 / 49.0 / 45.6; 30 x 1000 5.0 / 26.3 / 5.1; 4000 x 4000, 8
+// KiB, 30.2 / 22.9 / 102.9).  Longer ones: a warp per row from 4 x SMs rows with
+// alternatives (looped / split, 20 of 50257: 304 rows 26.8 / 19.4, 608 28.7 / 34.2,
+// 1216 37.1 / 53.2), without from 8 x SMs (distillation, 50257: 608 rows 21.6 / 13.9, 1024
+// 27.6 / 23.8, 2048 35.0 / 44.6).
+fr_form pick_forward(int64_t rows, int64_t cols, int es, bool top, int sm_count) {
+  if (fr::logits_held_ok(cols, es)) return FR_FORM_PERSISTENT;
+  return rows >= (top ? 4 : 8) * static_cast<int64_t>(sm_count) ? FR_FORM_LOOPED : FR_FORM_SPLIT;
 }
 
 // CTAs per row of the gradients' staged form, `least` or more: enough for two
@@ -248,9 +257,15 @@ int backward_cluster(int64_t rows, int64_t cols, int es, bool distill, int sm_co
   return fr::logit_grad_staged_ok(cols, es, cluster, distill, smem) ? cluster : 0;
 }
 
+// Few rows of up to 100 KiB are done before a ring of them is filled: a CTA a row
+// that reads it twice, the second time from L2 (us looped / persistent, bf16: 152 x
+// 30000 4.4 / 6.2; 300 x 30000 8.3 / 11.5; 300 x 50257 13.9 / 16.9; 64 x 50257 8.5 / 8.0;
+// 1000 x 8000 15.5 / 15.2).
 fr_form pick_backward(int64_t rows, int64_t cols, int es, bool distill, int sm_count, int smem) {
+  if (cols * es < 257 * 32 && rows <= INT32_MAX) return FR_FORM_PERSISTENT;
   const int cluster = backward_cluster(rows, cols, es, distill, sm_count, smem, 1);
-  return cluster == 0 ? FR_FORM_LOOPED : cluster == 1 ? FR_FORM_PERSISTENT : FR_FORM_SPLIT;
+  if (cluster == 0 || (rows <= 2 * sm_count && cols * es <= (100 << 10))) return FR_FORM_LOOPED;
+  return cluster == 1 ? FR_FORM_PERSISTENT : FR_FORM_SPLIT;
 }
 
 }  // namespace
@@ -291,7 +306,8 @@ fr_form fr_auto_form(fr_op op, fr_dtype dtype, int64_t rows, int64_t cols, int32
                  : FR_FORM_AUTO;
     case FR_OP_XENT: return FR_FORM_LOOPED;
     case FR_OP_LOGPROBS:
-    case FR_OP_DISTILL: return pick_forward(rows, cols, sm_count);
+    case FR_OP_DISTILL:
+      return pick_forward(rows, cols, dtype == FR_F32 ? 4 : 2, op == FR_OP_LOGPROBS, sm_count);
     case FR_OP_LOGPROBS_BACKWARD:
     case FR_OP_DISTILL_BACKWARD:
     case FR_OP_XENT_BACKWARD:
@@ -319,7 +335,7 @@ size_t fr_workspace_size(fr_op op, int64_t rows, int64_t cols, fr_dtype dtype, f
     case FR_OP_LOGPROBS: {
       const int es = dtype == FR_F32 ? 4 : 2;
       if (!shape_ok(rows, cols, cols, es)) return 0;
-      const fr_form f = form == FR_FORM_AUTO ? pick_forward(rows, cols, info.sm_count) : form;
+      const fr_form f = form == FR_FORM_AUTO ? pick_forward(rows, cols, es, true, info.sm_count) : form;
       return f == FR_FORM_LOOPED ? fr::logprobs_workspace(rows, cols, es) : 0;
     }
     default: return 0;
@@ -698,18 +714,21 @@ bool aligned_or_null(const void *p, size_t a) { return p == nullptr || aligned(p
 
 fr_status run_forward(fr::LogitsForward &a, fr_dtype dtype, bool distill, fr_form form,
                       size_t workspace_bytes, fr_stream_t stream) {
-  if (form != FR_FORM_AUTO && form != FR_FORM_LOOPED && form != FR_FORM_SPLIT)
-    return FR_ERR_UNSUPPORTED_FORM;
+  if (form < FR_FORM_AUTO || form > FR_FORM_SPLIT) return FR_ERR_UNSUPPORTED_FORM;
   fr::DevInfo info;
   if (fr_status st = logits_device_ok(a.cols, &info, &a.err)) return st;
   const bool f32 = dtype == FR_F32;
-  const fr_form f = form == FR_FORM_AUTO ? pick_forward(a.rows, a.cols, info.sm_count) : form;
+  const int es = f32 ? 4 : 2;
+  const fr_form f = form == FR_FORM_AUTO ? pick_forward(a.rows, a.cols, es, !distill && a.top > 0, info.sm_count) : form;
+  if (f == FR_FORM_PERSISTENT && !fr::logits_held_ok(a.cols, es)) return FR_ERR_UNSUPPORTED_FORM;
   if (!distill && a.top > 0 && f == FR_FORM_LOOPED) {
     if (!a.workspace || workspace_bytes < fr::logprobs_workspace(a.rows, a.cols, f32 ? 4 : 2))
       return FR_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned(a.workspace, 16)) return FR_ERR_MISALIGNED;
   }
-  const int split = f == FR_FORM_LOOPED ? 0 : forward_split(a.rows, a.cols, f32 ? 4 : 2, info.sm_count);
+  const int split = f == FR_FORM_PERSISTENT ? -1
+                    : f == FR_FORM_LOOPED   ? 0
+                                            : forward_split(a.rows, a.cols, es, info.sm_count);
   return launched(fr::launch_logits_forward(a, f32, distill, split, info.sm_count,
                                             reinterpret_cast<cudaStream_t>(stream)), f);
 }

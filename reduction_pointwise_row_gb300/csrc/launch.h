@@ -235,7 +235,9 @@ struct LogitsForward {
   int *err;         // the device error word
 };
 size_t logprobs_workspace(int64_t rows, int64_t cols, int es);
-// split: 0, a warp per row; else a cluster of that many CTAs (1, 2, 4 or 8) per row
+// True when a warp holds a row in its registers.
+bool logits_held_ok(int64_t cols, int es);
+// split: -1, a warp per row that holds it; 0, a warp per row that streams it; else a cluster of that many CTAs (1, 2, 4 or 8) per row
 cudaError_t launch_logits_forward(const LogitsForward &a, bool f32, bool distill, int split,
                                   int sm_count, cudaStream_t s);
 

@@ -11,7 +11,7 @@
 // logits costs no digits.
 //
 // Top alternatives.  The order is larger logits first, equal ones by index, every
-// NaN largest; what matters is to sort few candidates.  Both forms find a floor that at least k
+// NaN largest; what matters is to sort few candidates.  Every form finds a floor that at least k
 // logits reach: the k-th largest of the maxima of at least k disjoint groups of
 // the row's logits.  With g groups about g log(g / (g - k)) logits reach it, some
 // more than k.  Only vectors that reach it are read again, for their logits.
@@ -24,6 +24,8 @@
 //           bf16 [8192, 50257] top 20 took 200-220 us.)  A list that still grows
 //           (equal logits, an order that puts the largest together)
 //           is cut to its k largest, whose least is the next floor.
+//   held    (rows in registers) the groups are places of the lanes' vectors; the
+//           candidates are listed as in the looped form.
 //   split   the groups are the threads' vectors, floors of a cluster's CTAs for
 //           k / CTAs each, the least of them the row's; candidates that do not
 //           fit are replaced by an exact bisection over the keys of the row.
@@ -248,17 +250,12 @@ __device__ __forceinline__ void cut_if_long(WarpTop &w, int k, int most, int &n,
   n = k;
 }
 
-// Lists the logits that pass of the row's vectors b0 + vec[0, count), count <= 32.
+// Lists the logits of each lane's vector (where it has one) that pass; `index` is
+// the first one's place in the row.
 template <bool F32>
-__device__ __forceinline__ void list_vectors(const unsigned char *pv, int head, WarpTop &w, int b0,
-                                             const uint16_t *vec, int count, int k, int &n,
-                                             Floor &floor) {
+__device__ __forceinline__ void list_vector(WarpTop &w, const V8 &v, bool have, uint32_t index,
+                                            int k, int &n, Floor &floor) {
   using L = Logits<F32>;
-  const int lane = threadIdx.x & 31;
-  const bool have = lane < count;
-  const int vi = b0 + (have ? vec[lane] : 0);
-  const V8 v = have ? ld_keep_v8(pv + static_cast<int64_t>(vi) * kVecBytes) : L::filler();
-  const uint32_t index = static_cast<uint32_t>(head + vi * L::EPV);
 #pragma unroll
   for (int j0 = 0; j0 < L::EPV; j0 += 8) {
     cut_if_long(w, k, kCutAt, n, floor);
@@ -279,6 +276,31 @@ __device__ __forceinline__ void list_vectors(const unsigned char *pv, int head, 
       if ((pass >> j) & 1) w.list[to++] = place_key(logit_key(L::at(v, j0 + j)), index + j0 + j);
     n += more;
     __syncwarp();
+  }
+}
+
+// The same of the row's vectors b0 + vec[0, count), count <= 32.
+template <bool F32>
+__device__ __forceinline__ void list_vectors(const unsigned char *pv, int head, WarpTop &w, int b0,
+                                             const uint16_t *vec, int count, int k, int &n,
+                                             Floor &floor) {
+  const int lane = threadIdx.x & 31;
+  const bool have = lane < count;
+  const int vi = b0 + (have ? vec[lane] : 0);
+  const V8 v =
+      have ? ld_keep_v8(pv + static_cast<int64_t>(vi) * kVecBytes) : Logits<F32>::filler();
+  list_vector<F32>(w, v, have, static_cast<uint32_t>(head + vi * Logits<F32>::EPV), k, n, floor);
+}
+
+// The listed candidates to their places (one warp).
+__device__ __forceinline__ void sort_list(const LogitsForward &a, int64_t row, WarpTop &w, int n,
+                                          Floor &floor, const RowStat &st, float logl) {
+  if (n <= 32) sort_top<1>(a, row, w.list, n, st, logl);
+  else if (n <= 64) sort_top<2>(a, row, w.list, n, st, logl);
+  else if (n <= 128) sort_top<4>(a, row, w.list, n, st, logl);
+  else {
+    cut_if_long(w, a.top, kCutAt, n, floor);
+    sort_top<8>(a, row, w.list, n, st, logl);
   }
 }
 
@@ -490,19 +512,85 @@ __global__ void __launch_bounds__(32 * kTopWarps, 8) logit_top_rows(LogitsForwar
       pending = 0;
     }
   }
-  const RowStat st{stat.x, 0.0f, 0.0f};
-  if (n <= 32) sort_top<1>(a, row, w.list, n, st, stat.y);
-  else if (n <= 64) sort_top<2>(a, row, w.list, n, st, stat.y);
-  else if (n <= 128) sort_top<4>(a, row, w.list, n, st, stat.y);
-  else {
-    cut_if_long(w, k, kCutAt, n, floor);
-    sort_top<8>(a, row, w.list, n, st, stat.y);
+  sort_list(a, row, w, n, floor, RowStat{stat.x, 0.0f, 0.0f}, stat.y);
+}
+
+// ---- held: a warp per row, the row in registers ------------------------------------
+//
+// Rows of at most 4 KiB, NV vectors a lane.  The groups of the alternatives' floor
+// are the lanes' 32-bit words at one place of their vectors, 8 a lane.
+
+constexpr int64_t kHeldVectors = 128;
+
+template <bool F32, bool DISTILL, bool TOP, int NV>
+__global__ void __launch_bounds__(32 * kTopWarps, 5)
+logit_rows_held(LogitsForward a) {
+  pdl_enter();
+  using L = Logits<F32>;
+  __shared__ WarpTop tops[TOP ? kTopWarps : 1];
+  WarpTop &w = tops[TOP ? threadIdx.x >> 5 : 0];
+  const int lane = threadIdx.x & 31;
+  const float c = DISTILL ? kLog2e / a.temperature : kLog2e;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kTopWarps + (threadIdx.x >> 5);
+  if (row >= a.rows) return;
+  const unsigned char *pr = static_cast<const unsigned char *>(a.logits) + row * a.ld * L::ES;
+  const RowSplit sp = row_split(pr, a.cols, L::ES);
+  const unsigned char *pv = pr + static_cast<int64_t>(sp.head) * L::ES;
+  const int nvec = static_cast<int>(sp.nvec), tail0 = static_cast<int>(a.cols) - sp.tail;
+  const int64_t token = !DISTILL && a.logprob ? a.token[row] : -1;
+  V8 v[NV];
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+    v[u] = lane + 32 * u < nvec ? ld_stream_v8(pv + (lane + 32 * u) * kVecBytes) : L::filler();
+  const float head = lane < sp.head ? L::load(pr, lane) : -INFINITY;
+  const float tail = lane < sp.tail ? L::load(pr, tail0 + lane) : -INFINITY;
+  const float xt = token >= 0 && token < a.cols ? L::load(pr, token) : 0.0f;
+  RowStat st = stat_empty();
+  stat_fold<F32, !DISTILL, NV>(st, v, L::max(v), c);
+  if (head != -INFINITY) st = stat_merge(st, RowStat{head, 1.0f, 0.0f}, c);
+  if (tail != -INFINITY) st = stat_merge(st, RowStat{tail, 1.0f, 0.0f}, c);
+  st = warp_stat(st, c);
+  if constexpr (DISTILL) {
+    write_distill<F32>(a, row, pr, st);
+  } else {
+    const float logl = logf(st.l);
+    if (lane == 0) write_stats(a, row, token, xt, st, logl);
+    if constexpr (TOP) {
+      uint32_t key[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t m = v[0].w[j];
+        if constexpr (F32) {
+#pragma unroll
+          for (int u = 1; u < NV; ++u)
+            m = __float_as_uint(max_nan(__uint_as_float(m), __uint_as_float(v[u].w[j])));
+          key[j] = logit_key(__uint_as_float(m));
+        } else {
+#pragma unroll
+          for (int u = 1; u < NV; ++u) m = max_nan_bf16x2(m, v[u].w[j]);
+          key[j] = logit_key(max_nan(bf16_lo(m), bf16_hi(m)));
+        }
+      }
+      Floor floor{-INFINITY, 0};
+      floor.raise(group_floor(key, a.top));
+      int n = 0;
+      list_scalars(w, lane < sp.head, head, lane, n, floor);
+      list_scalars(w, lane < sp.tail, tail, tail0 + lane, n, floor);
+#pragma unroll
+      for (int u = 0; u < NV; ++u)
+        if (32 * u < nvec)
+          list_vector<F32>(w, v[u], lane + 32 * u < nvec,
+                           static_cast<uint32_t>(sp.head + (lane + 32 * u) * L::EPV), a.top, n,
+                           floor);
+      sort_list(a, row, w, n, floor, st, logl);
+    }
   }
 }
 
 // ---- split: a cluster of CTAs per row ---------------------------------------------
 
 constexpr int kSplitNV = 4;        // 32-byte vectors a thread loads at once
+constexpr int kStepMaxima = 16;
 constexpr int kCandidates = 1024;  // candidates of a row that its first CTA holds
 
 // 8 bytes from the shared memory of CTA `rank` of this cluster, at the offset
@@ -523,6 +611,7 @@ struct SplitShared {
   uint64_t count;  // candidates found (may pass kCandidates)
   uint64_t cand[kCandidates];
   V8 vec[kT];  // a vector of each thread
+  float step_max[kStepMaxima][kT];  // the maxima of the threads' steps (the last: of the rest)
 };
 
 // The sum of n over the CTA, in every thread.  `buf` alternates between the
@@ -624,13 +713,18 @@ __global__ void __launch_bounds__(kT, TOP ? 3 : 4) logit_rows_split(LogitsForwar
       const float x = L::load(pr, i);
       if (x != -INFINITY) st = stat_merge(st, RowStat{x, 1.0f, 0.0f}, c);
     }
-    for (int b = v0 + tid; b < v1; b += kT * kSplitNV) {
+    for (int b = v0 + tid, step = 0; b < v1; b += kT * kSplitNV, ++step) {
       V8 v[kSplitNV];
 #pragma unroll
       for (int u = 0; u < kSplitNV; ++u)
         v[u] = b + u * kT < v1 ? ld_keep_v8(pv + static_cast<int64_t>(b + u * kT) * kVecBytes)
                                : L::filler();
-      stat_fold<F32, !DISTILL, kSplitNV>(st, v, L::max(v), c);
+      const float cm = L::max(v);
+      if constexpr (TOP) {
+        float &m = sh.step_max[step < kStepMaxima ? step : kStepMaxima - 1][tid];
+        m = step < kStepMaxima ? cm : max_nan(m, cm);
+      }
+      stat_fold<F32, !DISTILL, kSplitNV>(st, v, cm, c);
     }
     const float xt = token >= 0 && token < a.cols ? L::load(pr, token) : 0.0f;
     const float mine = st.m;  // the largest of this thread's logits
@@ -677,7 +771,8 @@ __global__ void __launch_bounds__(kT, TOP ? 3 : 4) logit_rows_split(LogitsForwar
           // a NaN passes any floor; a floor of NaN is left to the candidates' keys
           const float fl = fkey == 0 ? -INFINITY : key_logit(fkey);
           const float floor = fl != fl ? INFINITY : fl;
-          for (int b = v0 + tid; b < v1; b += kT * kSplitNV) {
+          for (int b = v0 + tid, step = 0; b < v1; b += kT * kSplitNV, ++step) {
+            if (sh.step_max[step < kStepMaxima ? step : kStepMaxima - 1][tid] < floor) continue;
             V8 v[kSplitNV];
 #pragma unroll
             for (int u = 0; u < kSplitNV; ++u)
@@ -741,7 +836,19 @@ __global__ void __launch_bounds__(kT, TOP ? 3 : 4) logit_rows_split(LogitsForwar
 }
 
 template <bool F32, bool DISTILL, bool TOP>
+cudaError_t launch_held(const LogitsForward &a, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((a.rows + kTopWarps - 1) / kTopWarps));
+  const dim3 block(32 * kTopWarps);
+  const int64_t vectors = a.cols * (F32 ? 4 : 2) / kVecBytes;
+  return vectors <= 32 ? launch_k(logit_rows_held<F32, DISTILL, TOP, 1>, grid, block, 0, s, 0, a)
+         : vectors <= 64
+             ? launch_k(logit_rows_held<F32, DISTILL, TOP, 2>, grid, block, 0, s, 0, a)
+             : launch_k(logit_rows_held<F32, DISTILL, TOP, 4>, grid, block, 0, s, 0, a);
+}
+
+template <bool F32, bool DISTILL, bool TOP>
 cudaError_t launch_forward(const LogitsForward &a, int split, int sm_count, cudaStream_t s) {
+  if (split < 0) return launch_held<F32, DISTILL, TOP>(a, s);
   const dim3 block(kT);
   if (split == 0) {
     // a persistent grid of two CTAs an SM, shrunk so that every warp takes the
@@ -772,6 +879,8 @@ cudaError_t launch_forward(const LogitsForward &a, int split, int sm_count, cuda
 }
 
 }  // namespace
+
+bool logits_held_ok(int64_t cols, int es) { return cols * es / kVecBytes <= kHeldVectors; }
 
 size_t logprobs_workspace(int64_t rows, int64_t cols, int es) {
   return static_cast<size_t>(rows) * (8 + 128 * static_cast<size_t>(maxima_steps(cols, es)));
