@@ -779,10 +779,14 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
       const unsigned char *pr = logits + row * a.ld * L::ES;
       unsigned char *po = static_cast<unsigned char *>(a.dlogits) + row * a.ldd * L::ES;
       const UnitGeom g = unit_geom<L::ES>(pr, a.cols, q, lg);
-      // element j is written here if it is this CTA's
-      const int64_t lo = q == 0 ? 0 : (g.first + 16 * static_cast<int64_t>(g.u0)) / L::ES;
-      const int64_t hi =
-          q + 1 == C ? a.cols : (g.first + 16 * static_cast<int64_t>(g.u1)) / L::ES;
+      // element j is written here if it is this CTA's: the first has the head (all of
+      // a row without units), the last the tail
+      int64_t lo = q == 0 ? 0 : (g.first + 16 * static_cast<int64_t>(g.u0)) / L::ES;
+      int64_t hi = q + 1 == C ? a.cols : (g.first + 16 * static_cast<int64_t>(g.u1)) / L::ES;
+      if (g.head == a.cols) {
+        lo = q == 0 ? 0 : a.cols;
+        hi = a.cols;
+      }
       const bool grad = p.kind == kRowGrad;
       float loss = p.kind == kRowNan ? nan : 0.0f;
       RowCoef r{};
