@@ -253,7 +253,7 @@ int backward_cluster(int64_t rows, int64_t cols, int es, bool distill, int sm_co
   int cluster = least;
   while (cluster < 8 && !fr::logit_grad_staged_ok(cols, es, cluster, distill, smem / 2)) cluster *= 2;
   while (cluster < 8 && rows * cluster * 2 <= sm_count && cols * es >= 2 * cluster * 8192) cluster *= 2;
-  if (rows > INT32_MAX) return 0;  // a CTA for every row
+  if (rows > INT32_MAX / 8) return 0;  // the grid has a cluster for every row
   return fr::logit_grad_staged_ok(cols, es, cluster, distill, smem) ? cluster : 0;
 }
 
@@ -262,7 +262,7 @@ int backward_cluster(int64_t rows, int64_t cols, int es, bool distill, int sm_co
 // 30000 4.4 / 6.2; 300 x 30000 8.3 / 11.5; 300 x 50257 13.9 / 16.9; 64 x 50257 8.5 / 8.0;
 // 1000 x 8000 15.5 / 15.2).
 fr_form pick_backward(int64_t rows, int64_t cols, int es, bool distill, int sm_count, int smem) {
-  if (cols * es < 257 * 32 && rows <= INT32_MAX) return FR_FORM_PERSISTENT;
+  if (cols * es < 257 * 32 && rows <= INT32_MAX / 8) return FR_FORM_PERSISTENT;
   const int cluster = backward_cluster(rows, cols, es, distill, sm_count, smem, 1);
   if (cluster == 0 || (rows <= 2 * sm_count && cols * es <= (100 << 10))) return FR_FORM_LOOPED;
   return cluster == 1 ? FR_FORM_PERSISTENT : FR_FORM_SPLIT;
@@ -745,7 +745,7 @@ fr_status run_backward(fr::LogitsBackward &a, fr_dtype dtype, bool distill, fr_f
                                         info.max_smem_optin)
                         : form;
   int cluster = 0;
-  if (f == FR_FORM_PERSISTENT) cluster = a.rows <= INT32_MAX ? 1 : 0;
+  if (f == FR_FORM_PERSISTENT) cluster = a.rows <= INT32_MAX / 8 ? 1 : 0;
   else if (f == FR_FORM_SPLIT) cluster = backward_cluster(a.rows, a.cols, es, distill, info.sm_count, info.max_smem_optin, 2);
   if (f != FR_FORM_LOOPED &&
       (cluster < 1 || !fr::logit_grad_staged_ok(a.cols, es, cluster, distill, info.max_smem_optin)))

@@ -424,11 +424,11 @@ __global__ void __launch_bounds__(kT, 2) logit_grad_looped(LogitsBackward a) {
 
 // ---- staged: rows (or a cluster's runs of them) in a ring of bulk copies --------------
 //
-// One CTA a row (C = 1): the grid has a CTA for every row, and those that run take
-// the rows of those not yet launched, one at a time, by cluster launch control.
-// With rows dealt out in advance the SMs that the memory system serves better were
-// done 20-30 us before the last (xent_backward bf16 [4096, 50257]: 132-140 us).
-// Clusters: a persistent grid, a cluster taking rows c, c + clusters, ...  CTA q of C holds the row's 16-byte units [n q / C, n (q + 1) / C) in one of the
+// The grid has a cluster of C CTAs for every row, and those that run take the rows of
+// those not yet launched, one at a time, by cluster launch control.  With rows
+// dealt out in advance the SMs that the memory system serves better were done 20-30 us
+// before the last (xent_backward bf16 [4096, 50257]: 132-140 us).  CTA q of C holds the
+// row's 16-byte units [n q / C, n (q + 1) / C) in one of the
 // `nbuf` buffers of its ring.  All warps but the last few (the workers) fold the
 // run's units into the statistics and, after the CTA's and the cluster's merge,
 // write the gradient from shared memory; a worker goes on to the next row when its
@@ -462,6 +462,11 @@ struct RowParams {
 template <bool DISTILL>
 constexpr int kHelpers = DISTILL ? 4 : 2;
 constexpr int kRowRing = 32;  // rows whose numbers are kept
+// Answers that are kept: a CTA asks for row j when its row j - 2 has landed, so its row
+// j - 2 - nbuf is written and its peers sent their statistics of that one, which
+// they had named: they have read all answers but the last nbuf + 2.
+constexpr int kAnswers = 8;
+static_assert(kMaxBufs + 2 < kAnswers, "no answer is overwritten before it is read");
 
 template <bool DISTILL>
 struct StagedShared {
@@ -479,8 +484,9 @@ struct StagedShared {
   // the CTA's (cluster's) rows in turn, -1 past the last
   uint64_t named[kRowRing];  // row k's number is there
   int64_t row[kRowRing];
-  uint4 answer;  // of the request for another row
-  uint64_t answered;
+  // answers to the requests for another row, to all CTAs of the cluster
+  uint4 answer[kAnswers];
+  uint64_t answered[kAnswers];
   int gave_up;  // a wait ran out
 };
 
@@ -561,14 +567,21 @@ __device__ __forceinline__ void warp_wait(uint64_t *bar, uint32_t parity, bool &
 }
 
 // Asks for a cluster of this grid that has not been launched, to be taken over by
-// this one; the answer arrives in shared memory, counted on `bar`.  Not to be
-// asked again once the answer was no.
-__device__ __forceinline__ void request_cluster(uint4 *answer, uint64_t *bar) {
-  asm volatile(
-      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-          smem_addr(answer)),
-      "r"(smem_addr(bar))
-      : "memory");
+// this one; the answer arrives in the shared memory of all its CTAs (at the same
+// place), counted on their `bar`.  Not to be asked again once the answer was no.
+__device__ __forceinline__ void request_cluster(uint4 *answer, uint64_t *bar, bool peers) {
+  if (peers)
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+        ".multicast::cluster::all.b128 [%0], [%1];" ::"r"(smem_addr(answer)),
+        "r"(smem_addr(bar))
+        : "memory");
+  else
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+        ".b128 [%0], [%1];" ::"r"(smem_addr(answer)),
+        "r"(smem_addr(bar))
+        : "memory");
 }
 // The first CTA's x index of the cluster that was taken over, -1: none was left.
 __device__ __forceinline__ int64_t requested_cluster(const uint4 *answer) {
@@ -609,7 +622,7 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
     }
     for (int i = 0; i < 2; ++i) mbar_init(&sh.merged[i], 1);
     for (int i = 0; i < kRowRing; ++i) mbar_init(&sh.named[i], 1);
-    mbar_init(&sh.answered, 1);
+    for (int i = 0; i < kAnswers; ++i) mbar_init(&sh.answered[i], 1);
     sh.gave_up = 0;
     mbar_init_fence();
   }
@@ -633,22 +646,20 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
         mbar_arrive(&sh.named[k % kRowRing]);
       };
       int k = 0;
-      if (row >= a.rows) row = -1;
       while (row >= 0) {
         name(k++);
         if (k >= back)
           wait_for(&sh.full[(k - back) % nbuf], ((k - back) / nbuf) & 1, ok, &sh.gave_up, a.err);
         if (!ok) {
           row = -1;
-        } else if (C > 1) {
-          row += ncluster_x();
-          if (row >= a.rows) row = -1;
         } else {
-          fence_proxy_async_smem();  // the last answer was read
-          mbar_arrive_expect_tx(&sh.answered, 16);
-          request_cluster(&sh.answer, &sh.answered);
-          wait_for(&sh.answered, (k - 1) & 1, ok, &sh.gave_up, a.err);
-          row = ok ? requested_cluster(&sh.answer) : -1;
+          const int i = (k - 1) % kAnswers;
+          fence_proxy_async_smem();  // the answer that was here before is read
+          mbar_arrive_expect_tx(&sh.answered[i], 16);
+          if (q == 0) request_cluster(&sh.answer[i], &sh.answered[i], C > 1);
+          wait_for(&sh.answered[i], ((k - 1) / kAnswers) & 1, ok, &sh.gave_up, a.err);
+          row = ok ? requested_cluster(&sh.answer[i]) : -1;
+          if (row > 0) row >>= lg;
         }
       }
       for (int i = 0; i < H + kMaxBufs + 1; ++i) name(k++);
@@ -823,7 +834,6 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
       for (int i = 0; last_k >= 0 && i < kMaxBufs; last_k -= H, ++i)
         mbar_wait_bounded(&sh.full[last_k % nbuf], (last_k / nbuf) & 1, kWaitBudget);
   } else {
-    uint32_t merges = 0;  // bit i: parity that the next wait on merged[i] takes
     int b = 0, slot = 0;
     uint32_t lap = 0, turn = 0, k = 0;  // times through the buffers, the slots
     for (;; ++k) {
@@ -856,23 +866,22 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
       }
       // every worker comes here whatever it saw, and all of them stop together
       if (worker_barrier(workers, !ok) || kind == kNoRow) break;
-      if (kind == kRowGrad) {
+      if (kind == kRowGrad)
         st = warp_stat(lane < worker_warps ? sh.red[k & 1][lane] : stat_empty(), c);
-        if (C > 1) {
-          const int i = k & 1;
-          if (warp == 0) {
-            if (lane == 0) mbar_arrive_expect_tx(&sh.merged[i], 16u * C);
-            __syncwarp();
-            if (lane < C)
-              st_async_f4(&sh.part[i][q], &sh.merged[i], lane,
-                          make_float4(st.m, st.l, st.s, 0.0f));
-          }
-          warp_wait(&sh.merged[i], (merges >> i) & 1, ok, &sh.gave_up, a.err);
-          merges ^= 1u << i;
-          const float4 o =
-              lane < C ? sh.part[i][lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-          st = warp_stat(RowStat{o.x, o.y, o.z}, c);
+      if (C > 1) {  // for every row, so that no CTA gets far ahead of its peers
+        const int i = k & 1;
+        if (warp == 0) {
+          if (lane == 0) mbar_arrive_expect_tx(&sh.merged[i], 16u * C);
+          __syncwarp();
+          if (lane < C)
+            st_async_f4(&sh.part[i][q], &sh.merged[i], lane,
+                        make_float4(st.m, st.l, st.s, 0.0f));
         }
+        warp_wait(&sh.merged[i], (k >> 1) & 1, ok, &sh.gave_up, a.err);
+        const float4 o = lane < C ? sh.part[i][lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+        if (kind == kRowGrad) st = warp_stat(RowStat{o.x, o.y, o.z}, c);
+      }
+      if (kind == kRowGrad) {
         if (tid == 0) sh.stat[slot] = st;
         r = DISTILL ? row_coef(st, c, par.g * (1.0f / st.l), 0.0f)
                     : token_coef(st, c, par.g, par.h, HAS_B);
@@ -977,33 +986,7 @@ cudaError_t launch_form(const LogitsBackward &a, int cluster, bool vec32, bool v
   const size_t smem = static_cast<size_t>(sh.buf_bytes) * sh.nbuf;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kern), smem);
   if (e != cudaSuccess) return e;
-  int per_sm = 0;
-  if ((e = blocks_per_sm(&per_sm, reinterpret_cast<const void *>(kern), sh.threads, smem)) !=
-      cudaSuccess)
-    return e;
-  if (per_sm < 1) return cudaErrorInvalidConfiguration;
-  // a CTA for every row, or as many clusters as the device holds
-  int64_t clusters = a.rows;
-  if (cluster > 1) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(cluster));
-    cfg.blockDim = dim3(sh.threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int held = 0;
-    if ((e = resident_clusters(&held, reinterpret_cast<const void *>(kern), cfg,
-                               static_cast<unsigned>(cluster))) != cudaSuccess)
-      return e;
-    if (held < 1) return cudaErrorInvalidConfiguration;
-    clusters = held < a.rows ? held : a.rows;
-  }
-  return launch_k(kern, dim3(static_cast<unsigned>(clusters * cluster)), dim3(sh.threads), smem,
+  return launch_k(kern, dim3(static_cast<unsigned>(a.rows * cluster)), dim3(sh.threads), smem,
                   s, cluster, a, sh.buf_bytes, sh.nbuf, __builtin_ctz(cluster));
 }
 
