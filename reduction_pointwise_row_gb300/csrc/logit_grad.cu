@@ -942,16 +942,18 @@ struct StagedShape {
   uint32_t buf_bytes;
 };
 
-// Workers for about 10 units (80 bf16 logits) each: fewer units leave more of the
-// time to what every thread does once a row, more of them too few warps to cover
-// the latencies (bf16 [4096, 50257], 6283 units: 320 workers 128.8 us, 512 126.1, 640
-// 126.0, 800 131.0).  As
-// many CTAs an SM as their registers and two buffers each leave room for, and up to four buffers where the room is there.
+// Workers for 8 units (64 bf16 logits) each, or 10 where that is over 576 of them:
+// fewer units leave more of the time to what every thread does once a row, more of
+// them too few warps to cover the latencies (us; 6283 units, bf16 [4096, 50257]: 320
+// workers 128.8, 512 126.1, 640 126.0, 800 131.0; 4096 units, bf16 [1022, 65537] in
+// clusters of two: 416 54.9, 512 53.3, 576 57.8).  As many CTAs an SM as their registers
+// and two buffers each leave room for, and up to four buffers where the room is there.
 StagedShape staged_shape(int64_t cols, int es, int cluster, bool distill, const DevInfo &info) {
   StagedShape sh;
   sh.buf_bytes = static_cast<uint32_t>(staged_buf_bytes(cols, es, cluster));
   const int64_t units = sh.buf_bytes / 16;
-  int64_t workers = (units / 10 + 31) / 32 * 32;
+  int64_t workers = (units / 8 + 31) / 32 * 32;
+  if (workers > 576) workers = (units / 10 + 31) / 32 * 32;
   const int helpers = 32 * ((distill ? kHelpers<true> : kHelpers<false>) + 1);
   workers = workers < 64 ? 64 : workers > kMaxThreads - helpers ? kMaxThreads - helpers : workers;
   sh.threads = static_cast<int>(workers) + helpers;

@@ -445,10 +445,14 @@ __global__ void __launch_bounds__(32 * kTopWarps, 8) logit_top_rows(LogitsForwar
   const int k = a.top;
 
   uint32_t sub[4] = {0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u};  // 8 groups a lane
-  for (int step = 0; step < steps; step += 4)
+  for (int step = 0; step < steps; step += kSegment) {
+    uint32_t m[kSegment];  // a segment's loads at once
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
-      if (step + g < steps) sub[g] = max_nan_bf16x2(sub[g], maxima[(step + g) * 32]);
+    for (int i = 0; i < kSegment; ++i)
+      m[i] = step + i < steps ? maxima[(step + i) * 32] : 0xFF80FF80u;
+#pragma unroll
+    for (int i = 0; i < kSegment; ++i) sub[i % 4] = max_nan_bf16x2(sub[i % 4], m[i]);
+  }
   uint32_t key[8];  // of bf16 values: 16 bits order them
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
@@ -460,18 +464,20 @@ __global__ void __launch_bounds__(32 * kTopWarps, 8) logit_top_rows(LogitsForwar
   floor.raise(fkey << 16 | (fkey & 0x8000u ? 0 : 0xFFFFu));
 
   int n = 0, pending = 0;
-  list_scalars(w, lane < sp.head, head, lane, n, floor);
-  list_scalars(w, lane < sp.tail, tail, static_cast<int>(a.cols) - sp.tail + lane, n, floor);
+  if (sp.head > 0) list_scalars(w, lane < sp.head, head, lane, n, floor);
+  if (sp.tail > 0)
+    list_scalars(w, lane < sp.tail, tail, static_cast<int>(a.cols) - sp.tail + lane, n, floor);
   for (int s0 = 0; s0 < steps; s0 += kSegment) {
     const int b0 = s0 * kStep;  // the segment's first vector
     // the maxima are rounded down, so the floor is too: max >= v makes both >= v's
     const float low = bf16_lo(bf16_below(floor.v));
     uint32_t mask = 0;  // bit 2 s + h: half h of this lane's word of step s0 + s passes
-#pragma unroll 4
-    for (int s = 0; s < min(kSegment, steps - s0); ++s) {
-      const uint32_t m = maxima[(s0 + s) * 32];
+#pragma unroll
+    for (int s = 0; s < kSegment; ++s) {
+      const uint32_t m = s0 + s < steps ? maxima[(s0 + s) * 32] : 0xFF80FF80u;
       mask |= (bf16_lo(m) < low ? 0 : 1u) << (2 * s) | (bf16_hi(m) < low ? 0 : 2u) << (2 * s);
     }
+    if (s0 + kSegment > steps) mask &= (1u << (2 * (steps - s0))) - 1;
     int total;
     int at = lanes_before(__popc(mask), total);
     while (mask != 0) {
