@@ -447,6 +447,13 @@ constexpr int kMaxBufs = 4;
 constexpr int kMaxThreads = 832;  // 72 registers a thread
 constexpr int kMaxCluster = 8;
 constexpr long long kWaitBudget = 1LL << 31;  // SM clocks, about one second
+// A test-only build (-DFR_TEST_GRAD_WAIT_RUNS_OUT) gives the wait for a CTA's first row
+// no budget: it runs out whether or not the copy has landed.
+#ifdef FR_TEST_GRAD_WAIT_RUNS_OUT
+constexpr long long kFirstBudget = 0;
+#else
+constexpr long long kFirstBudget = kWaitBudget;
+#endif
 
 struct RowParams {
   int kind;
@@ -549,20 +556,28 @@ __device__ __forceinline__ bool worker_barrier(int workers, bool any) {
   return r != 0;
 }
 
-// A bounded wait; after one that ran out, its thread waits for nothing any more
-// and the CTA's helpers copy nothing more.
+// A wait of at most `budget` SM clocks (0: it runs out at once), shorter where another
+// of the CTA's waits ran out.  After that its thread waits for nothing any more, the CTA's helpers copy
+// nothing more, and its workers stop.
 __device__ __forceinline__ void wait_for(uint64_t *bar, uint32_t parity, bool &ok, int *gave_up,
-                                         int *err) {
-  if (!ok || mbar_wait_bounded(bar, parity, kWaitBudget)) return;
-  ok = false;
-  *reinterpret_cast<volatile int *>(gave_up) = 1;
-  atomicCAS(err, 0, FR_DEVERR_TIMEOUT);
+                                         int *err, long long budget = kWaitBudget) {
+  if (!ok) return;
+  const long long t0 = clock64();
+  while (budget == 0 || !mbar_try_wait(bar, parity)) {
+    if (*reinterpret_cast<volatile int *>(gave_up) == 0) {
+      if (budget > 0 && clock64() - t0 <= budget) continue;
+      *reinterpret_cast<volatile int *>(gave_up) = 1;
+      atomicCAS(err, 0, FR_DEVERR_TIMEOUT);
+    }
+    ok = false;
+    return;
+  }
 }
 
 // The same by a whole warp, whose lanes keep one `ok`.
 __device__ __forceinline__ void warp_wait(uint64_t *bar, uint32_t parity, bool &ok, int *gave_up,
-                                          int *err) {
-  wait_for(bar, parity, ok, gave_up, err);
+                                          int *err, long long budget = kWaitBudget) {
+  wait_for(bar, parity, ok, gave_up, err, budget);
   ok = __all_sync(0xffffffffu, ok);
 }
 
@@ -657,7 +672,9 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
           fence_proxy_async_smem();  // the answer that was here before is read
           mbar_arrive_expect_tx(&sh.answered[i], 16);
           if (q == 0) request_cluster(&sh.answer[i], &sh.answered[i], C > 1);
-          wait_for(&sh.answered[i], ((k - 1) / kAnswers) & 1, ok, &sh.gave_up, a.err);
+          // to the end of its own budget, whoever else gave up: the answer is on its way
+          ok = mbar_wait_bounded(&sh.answered[i], ((k - 1) / kAnswers) & 1, kWaitBudget);
+          if (!ok) atomicCAS(a.err, 0, FR_DEVERR_TIMEOUT);
           row = ok ? requested_cluster(&sh.answer[i]) : -1;
           if (row > 0) row >>= lg;
         }
@@ -841,7 +858,8 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
       warp_wait(&sh.ready[slot], turn & 1, ok, &sh.gave_up, a.err);
       const RowParams &par = sh.par[slot];
       int kind = ok ? par.kind : kNoRow;
-      if (kind != kNoRow) warp_wait(&sh.full[b], lap & 1, ok, &sh.gave_up, a.err);
+      if (kind != kNoRow)
+        warp_wait(&sh.full[b], lap & 1, ok, &sh.gave_up, a.err, k == 0 ? kFirstBudget : kWaitBudget);
       if (!ok) kind = kNoRow;
       const int n = kind != kNoRow ? par.n : 0;
       RowCoef r{};

@@ -170,3 +170,20 @@ def test_the_comparison_notices_mistakes():
     tied[0, 4] = math.nan
     tied[0, 6] = math.inf
     assert ref.logprobs(tied, None, 3)["top_index"].tolist() == [[4, 6, 0]]
+
+
+def test_the_forms_that_auto_takes():
+    """Host-side rules: a warp per short row, a cluster per long one, a CTA per row for
+    few rows, and never a form past its limits."""
+    def form(op, rows, cols, dtype="bf16"):
+        return fr.fr_auto_form(op, rows, cols, dtype, 152)
+
+    for op in ("logprobs", "distill"):
+        assert form(op, 4000, 1000) == "persistent" and form(op, 1, 50257) == "split"
+        assert form(op, 8192, 50257) == "looped"
+    assert form("logprobs", 700, 50257) == "looped" and form("distill", 700, 50257) == "split"
+    for op in ("logprobs_backward", "distill_backward", "xent_backward"):
+        assert form(op, 30000, 1000) == "persistent" and form(op, 4096, 50257) == "persistent"
+        assert form(op, 8, 50257) == "looped" and form(op, 1024, 65537) == "split"
+        assert form(op, 1024, 900000) in ("split", "looped")
+        assert form(op, 4, 1 << 30) == "looped" and form(op, (1 << 31), 60000) == "looped"

@@ -612,3 +612,137 @@ def test_gradients_of_a_view_keep_its_phase():
     far = wide.view(2, 3, 1088)[:, -1, :1001]
     d = fr.fr_xent_backward(far, t[:2], torch.ones(1, device="cuda"))["dlogits"]
     assert d.stride(0) < 1017
+
+
+def test_a_workspace_of_the_callers_own():
+    """The looped form's alternatives in a workspace of the caller's: used again, too
+    small, misaligned, and not needed where another form runs."""
+    rows, cols = 700, 4099
+    x, t = logits(rows, cols, "bf16", 1), tokens(rows, cols, 1)
+    v, tc = x.cuda(), t.cuda()
+    n = fr.fr_workspace_size("logprobs", rows, cols, "bf16")
+    assert n > 0 and fr.fr_auto_form("logprobs", rows, cols, "bf16", fr.sm_count()) == "looped"
+    ws = torch.empty(n + 16, dtype=torch.uint8, device="cuda")
+    for seed in (1, 2):
+        x = logits(rows, cols, "bf16", seed)
+        v.copy_(x)
+        check_logprobs(x, fr.fr_logprobs(v, tc, top=9, workspace=ws), t, 9, f"seed {seed}")
+    for bad in (ws[:n - 1], ws[8:n + 8]):
+        with pytest.raises(fr.FRError):
+            fr.fr_logprobs(v, tc, top=9, workspace=bad)
+    assert fr.fr_workspace_size("logprobs", 5, cols, "bf16") == 0
+    check_logprobs(x[:5], fr.fr_logprobs(v[:5], tc[:5], top=9), t[:5], 9, "few rows")
+
+
+def test_calls_on_two_streams_at_once():
+    """Eager calls of every kind interleaved on two streams, each with its own data."""
+    data = []
+    for seed in (1, 2):
+        rows, cols = 650 + seed, 9001
+        x = logits(rows, cols, "bf16", seed)
+        i, z = entries(rows, cols, 30, seed)
+        data.append((x, tokens(rows, cols, seed), i, z, upstream(rows, seed)))
+    held = [[v.cuda() for v in d] for d in data]
+    scratch = [torch.empty_like(h[0]) for h in held]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [None, None]
+    for _ in range(4):
+        for n, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[n] = step_of_all(*held[n], scratch[n])
+    torch.cuda.synchronize()
+    for n in range(2):
+        for o, e in zip(outs[n], step_of_all(*held[n], scratch[n])):
+            assert torch.equal(o.nan_to_num(7.0), e.nan_to_num(7.0))
+    assert fr.fr_check_device_error() == 0
+
+
+@pytest.mark.parametrize("rows", [1, 150, 153, 457, 1200])
+def test_row_counts_around_the_device(rows):
+    """Fewer rows than SMs, a few more, several a CTA: every row is written once, by
+    the staged form whose CTAs take rows from one another and by the rule's choice."""
+    cols = 9000
+    x, t, g = logits(rows, cols, "bf16", 3), tokens(rows, cols, 3), upstream(rows, 3)
+    r = ref.xent_backward(x, t, g)
+    b = ref.gradient_bound(x, r, g)
+    for form in ("persistent", "split", "auto"):
+        for _ in range(3):
+            d, _ = run_backward(fr.fr_xent_backward, x, (0, 0), (0, 0), form, target=t.cuda(),
+                                dloss=g.cuda())
+            ref.assert_near(d, r, b, f"{rows} rows {form}")
+
+
+def test_all_rows_ignored_and_all_rows_bad():
+    x = logits(400, 12000, "f32", 2).cuda()
+    g = torch.ones(1, device="cuda")
+    for form in ("looped", "persistent", "split"):
+        r = fr.fr_xent_backward(x, torch.full((400,), -100, device="cuda"), g, form=form)
+        assert (r["dlogits"] == 0).all() and (r["loss"] == 0).all()
+        assert fr.fr_check_device_error() == 0
+        r = fr.fr_xent_backward(x, torch.full((400,), 12000, device="cuda"), g, form=form)
+        assert torch.isnan(r["dlogits"]).all() and torch.isnan(r["loss"]).all()
+        assert fr.fr_check_device_error() == 1
+
+
+@pytest.mark.parametrize("cols", [600, 20000, 90001])
+def test_teacher_entries_that_repeat(cols):
+    """The same index in many entries, in different lanes and registers; indexes that
+    share a hash; all entries at one element."""
+    top, rows = 128, 5
+    i = torch.arange(top).repeat(rows, 1) * (cols // top)
+    i[1, ::2] = i[1, 1]
+    i[2, 64:] = i[2, :64]
+    i[3] = 7
+    i[4] = (torch.arange(top) % 2) * 256 + 3  # two indexes of one hash, 64 times each
+    x, g = logits(rows, cols, "f32", 8), upstream(rows, 8)
+    z = torch.from_numpy(rng(8, cols).normal(0, 2, (rows, top)).astype(np.float32))
+    r = ref.distill_backward(x, i, z, g)
+    q, _, _ = ref.teacher(i, z, 1.0)
+    dense = torch.zeros_like(r).scatter_add_(1, i, q)
+    b = ref.gradient_bound(x, r, g) + g.double().abs()[:, None] * dense * 320 * ref.U
+    for form in ("looped", "split", "auto"):
+        d, _ = run_backward(fr.fr_distill_backward, x, (0, 0), (0, 0), form,
+                            teacher_index=i.cuda(), teacher_logit=z.cuda(), dloss=g.cuda())
+        ref.assert_near(d, r, b, f"{cols} {form}")
+
+
+def test_upstream_gradients_that_are_not_finite():
+    """An infinite or NaN upstream gradient reaches its own row alone."""
+    x, t = logits(4, 9000, "f32", 4), torch.tensor([0, 5, 7, -100])
+    g = torch.tensor([1.0, math.inf, math.nan, math.inf])
+    for form in ("looped", "persistent", "split"):
+        d = fr.fr_xent_backward(x.cuda(), t.cuda(), g.cuda(), form=form)["dlogits"].cpu()
+        r = ref.xent_backward(x[:1], t[:1], g[:1])
+        ref.assert_near(d[:1], r, ref.gradient_bound(x[:1], r, g[:1]), form)
+        assert not torch.isfinite(d[1, 5]) and torch.isnan(d[2]).all() and (d[3] == 0).all()
+
+
+FIRST_CALL = """
+import torch, reduction_pointwise_row_gb300 as fr
+x = torch.randn(300, 40000, device="cuda").bfloat16()
+t, g = torch.zeros(300, dtype=torch.int64, device="cuda"), torch.ones(1, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    a = fr.fr_logprobs(x, t, top=5, form="looped")
+    b = fr.fr_xent_backward(x, t, g, form="persistent")
+    c = fr.fr_logprobs(x, t, top=5, form="split")
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(a["top_index"], c["top_index"])
+assert torch.equal(a["top_index"], x.float().topk(5).indices) or (x.float().gather(
+    1, a["top_index"]) == x.float().topk(5).values).all()
+assert torch.allclose(b["loss"], -a["logprob"], atol=1e-4)
+assert fr.fr_check_device_error() == 0
+"""
+
+
+def test_the_first_call_of_a_process_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True,
+                       timeout=300, cwd=root)
+    assert r.returncode == 0, r.stdout + r.stderr
