@@ -238,8 +238,8 @@ int forward_split(int64_t rows, int64_t cols, int es, int sm_count) {
 // alternatives: 4000 x 1000 11.6 / 49.0 / 45.6; 30 x 1000 5.0 / 26.3 / 5.1; 4000 x 4000, 8
 // KiB, 30.2 / 22.9 / 102.9).  Longer ones: a warp per row from 4 x SMs rows with
 // alternatives (looped / split, 20 of 50257: 304 rows 26.8 / 19.4, 608 28.7 / 34.2,
-// 1216 37.1 / 53.2), without from 8 x SMs (distillation, 50257: 608 rows 21.6 / 13.9, 1024
-// 27.6 / 23.8, 2048 35.0 / 44.6).
+// 1216 37.1 / 53.2), without from 8 x SMs (distillation, 50257: 608 rows 21.9 / 13.4, 1024
+// 27.9 / 22.3, 1216 24.7 / 24.3, 2048 34.7 / 40.1).
 fr_form pick_forward(int64_t rows, int64_t cols, int es, bool top, int sm_count) {
   if (fr::logits_held_ok(cols, es)) return FR_FORM_PERSISTENT;
   return rows >= (top ? 4 : 8) * static_cast<int64_t>(sm_count) ? FR_FORM_LOOPED : FR_FORM_SPLIT;
