@@ -187,3 +187,16 @@ def test_the_forms_that_auto_takes():
         assert form(op, 8, 50257) == "looped" and form(op, 1024, 65537) == "split"
         assert form(op, 1024, 900000) in ("split", "looped")
         assert form(op, 4, 1 << 30) == "looped" and form(op, (1 << 31), 60000) == "looped"
+
+
+def test_algorithmic_bytes_of_the_logits_calls():
+    """Logits read once (and their gradient written once), plus the rows' vectors."""
+    from reduction_pointwise_row_gb300 import traffic as t
+    R, C = 7, 1001
+    assert t.algorithmic_bytes("logprobs", R, C) == R * (2 * C + 20)
+    assert t.algorithmic_bytes("logprobs", R, C, dtype="f32", top=5) == R * (4 * C + 20 + 60)
+    assert t.algorithmic_bytes("logprobs_backward", R, C) == R * (4 * C + 16)
+    assert t.algorithmic_bytes("distill", R, C, top=64) == R * (2 * C + 768 + 4)
+    assert t.algorithmic_bytes("distill_backward", R, C, top=64) == R * (4 * C + 768 + 8)
+    assert t.algorithmic_bytes("distill_backward", R, C, top=64, loss=False) == R * (4 * C + 772)
+    assert t.algorithmic_bytes("xent_backward", R, C, dtype="f32") == R * (8 * C + 16)
