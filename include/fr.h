@@ -357,9 +357,18 @@ fr_status fr_xent_mean_from_parts(const void *workspace, float *loss_mean, fr_st
  * Statistics are those of each call's own pass (max, sum of exponentials, fp32
  * sums over short runs); x - max is taken before it is scaled, so neither a
  * common offset of a row nor a lowest-value mask costs digits.  Results do not
- * depend on other rows and are the same from run to run.  A token outside [0, cols) other than ignore_index, or a teacher
- * index >= cols, makes that row's log probability, loss and gradient NaN and
- * sets FR_DEVERR_BAD_TARGET; nothing outside the row is read.
+ * depend on other rows and are the same from run to run.  A token outside [0,
+ * cols) other than ignore_index, or a teacher index >= cols, makes that row's
+ * log probability, loss and gradient NaN and sets FR_DEVERR_BAD_TARGET; nothing
+ * outside the row is read.  dlogits beyond column cols of a row are not written.
+ *
+ * Forms of the gradients: persistent (rows on chip: a warp holds a row of at most
+ * 8 KiB in registers, a CTA a longer one in shared memory, about 200 KiB), split
+ * (a cluster of 2 to 8 CTAs holds a row in shared memory) and looped (a CTA reads
+ * a row twice; any length).  The first two need rows <= INT32_MAX / 8; a form that
+ * does not fit is FR_ERR_UNSUPPORTED_FORM.  AUTO takes the persistent form where a
+ * warp holds a row or two rows fit in shared memory, else the split one; the looped
+ * one for at most 2 x SMs rows of 8 to 100 KiB and for what nothing else holds.
  */
 
 /*
@@ -421,6 +430,7 @@ fr_status fr_logprobs_backward(const void *logits, const int64_t *token, const f
  *   top          1 .. FR_TOP_MAX
  *   temperature  > 0, finite, with a finite log2(e) / temperature
  *   loss         fp32 [rows] device output
+ * Forms as for fr_logprobs without alternatives.
  */
 fr_status fr_distill(const void *logits, const int64_t *teacher_index,
                      const float *teacher_logit, float *loss, int32_t top, int64_t rows,
