@@ -43,7 +43,7 @@ __device__ __forceinline__ V8 ld_v8(const void *p) {
 // What the elements of a row are computed from: with t = (x - m) c,
 //   dx = 2^t (a + b max(t, kFar)).
 // 2^t is 0 from kFar down, and the bound keeps b t finite where x is -inf.  Where
-// m c is in range, t is one fused multiply-add, x c - mc, larger than (x - m) c by
+// |m c| <= kFusedRange, t is one fused multiply-add, x c - mc, larger than (x - m) c by
 // rest = m c - mc (see stat_fold), which a and b take in.
 constexpr float kFar = -200.0f;
 
@@ -60,7 +60,7 @@ struct RowCoef {
 // From the row's statistics: dx = e (a + b (x - m) c) before the correction.
 __device__ __forceinline__ RowCoef row_coef(const RowStat &st, float c, float a, float b) {
   RowCoef r{st.m, c, st.m * c, a, b, false};
-  r.fused = fabsf(r.mc) <= 1e30f;
+  r.fused = fabsf(r.mc) <= kFusedRange;
   if (r.fused) {
     const float rest = fmaf(st.m, c, -r.mc), f = ex2(-rest);
     r.a = fmaf(-b, rest, a) * f;

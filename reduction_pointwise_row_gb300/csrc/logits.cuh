@@ -107,6 +107,10 @@ struct Logits {
   }
 };
 
+// Where |m c| is at most this, |m c rounded - m c| is at most 1/2: 2^rest stays close to
+// 1 (from |m c| = 2^31 on it may leave the range of fp32) and costs s no digits.
+constexpr float kFusedRange = 16777216.0f;
+
 // Folds NV vectors with largest element cm into a thread's statistics; the
 // entropy's sum (at T = 1) only with ENT.  Two partial sums of pairs per call are
 // added to the running fp32 sums once, so a thread's chains of additions stay
@@ -116,7 +120,7 @@ struct Logits {
 // rounded product and rest = m c - mc exactly (one more fused multiply-add),
 // x c - mc is rounded once, at its own size, and every exponential is too large
 // by the same 2^rest, which is taken out of the sums.  Where that does not
-// serve -- m c past the range, or an element at t = -inf, whose exp * t = 0 * -inf
+// serve -- m c past kFusedRange, or an element at t = -inf, whose exp * t = 0 * -inf
 // -- the sums are taken again from x - m with the far differences cut off.
 // (Measured with the alternatives of a row off, bf16 [2432, 50257]: 7.0
 // instructions a logit with x - m and the cut for every logit.)
@@ -136,7 +140,7 @@ __device__ __forceinline__ void stat_fold(RowStat &st, const V8 (&v)[NV], float 
   }
   const uint64_t c2 = pack_f32x2(c, c);
   const float mc = st.m * c;
-  if (fabsf(mc) <= 1e30f) {
+  if (fabsf(mc) <= kFusedRange) {
     const uint64_t nmc2 = pack_f32x2(-mc, -mc);
     uint64_t al[2] = {0, 0}, as[2] = {0, 0};
 #pragma unroll

@@ -746,3 +746,66 @@ def test_the_first_call_of_a_process_inside_a_capture():
     r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True,
                        timeout=300, cwd=root)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+OFFSETS = [s * o for o in (1e6, 3e7, 1e9, 5e9, 1e12, 1e20, 1e29, 6e29, 1e38) for s in (1, -1)]
+
+
+def offset_rows(cols, dtype):
+    """Rows far from zero: all at one value (what a finite mask leaves of a row), spread
+    around it as far as the type has values there, and partly masked by -inf."""
+    base = torch.from_numpy(rng(cols, 9).normal(0.0, 3.0, cols))
+    rows = []
+    for o in OFFSETS:
+        rows += [torch.full((cols,), o, dtype=torch.float64), base + o,
+                 torch.where(torch.arange(cols) % 3 == 1, -math.inf, base + o)]
+    return torch.stack(rows).float().to(DTYPES[dtype])
+
+
+@FORWARD_FORMS
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cols", [40, 1000, 9001])
+def test_rows_far_from_zero(cols, dtype, form):
+    skip_long(form, cols, dtype)
+    x = offset_rows(cols, dtype)
+    t = torch.zeros(x.shape[0], dtype=torch.int64)
+    i = torch.tensor([[0, 2, 3]]).repeat(x.shape[0], 1)
+    z = torch.tensor([[0.5, 1.0, -1.0]]).repeat(x.shape[0], 1)
+    got = fr.fr_logprobs(x.cuda(), t.cuda(), top=9, form=form)
+    loss, r = fr.fr_distill(x.cuda(), i.cuda(), z.cuda(), form=form), ref.distill(x, i, z)
+    bound = loss_bound(x, r, i, z, 1.0)
+    for n in range(x.shape[0]):
+        s = slice(n, n + 1)
+        what = f"{OFFSETS[n // 3]:g}, kind {n % 3}, {cols} {dtype}"
+        check_logprobs(x[s], {k: o[s] for k, o in got.items()}, t[s], 9, what)
+        ref.assert_near(loss[s], r[s], bound[s], f"{what} distill")
+
+
+@BACKWARD_FORMS
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cols", [40, 1000, 9001])
+def test_gradients_of_rows_far_from_zero(cols, dtype, form):
+    x = offset_rows(cols, dtype)
+    rows = x.shape[0]
+    t = torch.zeros(rows, dtype=torch.int64)
+    g, h = upstream(rows, 1), upstream(rows, 2)
+    i = torch.tensor([[0, 2, 3]]).repeat(rows, 1)
+    z = torch.tensor([[0.5, 1.0, -1.0]]).repeat(rows, 1)
+    d, _ = run_backward(fr.fr_logprobs_backward, x, (0, 0), (0, 0), form, token=t.cuda(),
+                        dlogprob=g.cuda(), dentropy=h.cuda())
+    e, loss = run_backward(fr.fr_xent_backward, x, (0, 0), (0, 0), form, target=t.cuda(),
+                           dloss=g.cuda())
+    k, _ = run_backward(fr.fr_distill_backward, x, (0, 0), (0, 0), form, teacher_index=i.cuda(),
+                        teacher_logit=z.cuda(), dloss=g.cuda())
+    rd, re, rk = (ref.logprobs_backward(x, t, g, h), ref.xent_backward(x, t, g),
+                  ref.distill_backward(x, i, z, g))
+    bd, be = ref.gradient_bound(x, rd, g, h), ref.gradient_bound(x, re, g)
+    bk = ref.gradient_bound(x, rk, g) + g.double().abs()[:, None] * 160 * ref.U
+    rl = ref.xent(x, t)
+    for n in range(rows):
+        s = slice(n, n + 1)
+        what = f"{OFFSETS[n // 3]:g}, kind {n % 3}, {cols} {dtype}"
+        ref.assert_near(d[s], rd[s], bd[s], f"{what} logprobs")
+        ref.assert_near(e[s], re[s], be[s], f"{what} xent")
+        ref.assert_near(k[s], rk[s], bk[s], f"{what} distill")
+        ref.assert_near(loss[s], rl[s], ref.eps(cols) + 4 * ref.U * rl[s].abs(), f"{what} loss")
