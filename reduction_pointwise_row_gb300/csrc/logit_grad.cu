@@ -186,15 +186,16 @@ __device__ __forceinline__ void teacher_share(const Teacher &t, int top, Teacher
   __syncwarp();
 }
 
-// The row's loss from its shared entries, in every lane of one warp.
+// The row's loss from its shared entries, in every lane of one warp (as the other
+// teacher_loss, for its range).
 __device__ __forceinline__ float teacher_loss(const TeacherShared &sh, int top, const RowStat &st,
                                               float temperature) {
   const float logl = logf(st.l);
   float sum = 0.0f;
   for (int e = threadIdx.x & 31; e < top; e += 32)
     if (sh.idx[e] >= 0)
-      sum += sh.q[e] * (sh.logq[e] - ((sh.x[e] - st.m) / temperature - logl));
-  return temperature * temperature * warp_sum(sum);
+      sum += sh.q[e] * (temperature * (sh.logq[e] + logl) - (sh.x[e] - st.m));
+  return temperature * warp_sum(sum);
 }
 
 // Entry e's element: g (p - sum of its weights).

@@ -809,3 +809,23 @@ def test_gradients_of_rows_far_from_zero(cols, dtype, form):
         ref.assert_near(e[s], re[s], be[s], f"{what} xent")
         ref.assert_near(k[s], rk[s], bk[s], f"{what} distill")
         ref.assert_near(loss[s], rl[s], ref.eps(cols) + 4 * ref.U * rl[s].abs(), f"{what} loss")
+
+
+@pytest.mark.parametrize("temperature", [0.25, 0.5, 1.0])
+def test_teacher_entries_at_the_lowest_value(temperature):
+    """A masked element that the teacher gives weight costs its distance, which divided
+    by a temperature below 1 is past fp32: the loss is not."""
+    x = logits(6, 9000, "f32", 5)
+    x[:, ::2] = torch.finfo(torch.float32).min
+    i = torch.tensor([[0, 1, 3]]).repeat(6, 1)
+    z = torch.tensor([[0.0, 1.0, 2.0]]).repeat(6, 1)
+    r = ref.distill(x, i, z, temperature)
+    # T q_0 3.4e38 with q_0 = exp(-2 / T) / sum: 2.8e34 at T = 1/4, 3.1e37 at 1
+    assert (r > 1e34).all() and (r < 3e38).all()
+    b = loss_bound(x, r, i, z, temperature)
+    for form in ("looped", "split"):
+        ref.assert_near(fr.fr_distill(x.cuda(), i.cuda(), z.cuda(), temperature, form=form), r, b)
+    for form in ("looped", "persistent", "split"):
+        got = fr.fr_distill_backward(x.cuda(), i.cuda(), z.cuda(), torch.ones(1, device="cuda"),
+                                     temperature, form=form)
+        ref.assert_near(got["loss"], r, b, form)
