@@ -348,7 +348,8 @@ fr_status fr_xent_mean_from_parts(const void *workspace, float *loss_mean, fr_st
  *                latter's lse is -inf).
  *   dlogits      of `dtype` [rows, ldd] device output, the gradient, rounded
  *                once (nearest even).  It may be the logits' own buffer (ldd ==
- *                ld); any other overlap is not allowed.
+ *                ld) or, with ldd == ld, lie between its rows; any other overlap of
+ *                the two is FR_ERR_INVALID_ARG.
  *   dloss, dlogprob, dentropy
  *                fp32 upstream gradients, row r's at [r * stride]; stride 0
  *                gives every row the same one (the gradient of a sum or mean).

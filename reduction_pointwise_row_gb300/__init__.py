@@ -560,6 +560,7 @@ def fr_logprobs(logits, token=None, top: int = 0, ignore_index: int = -100,
     if not 0 <= top <= min(cols, FR_TOP_MAX):
         raise ValueError(f"top must be 0 to min(cols, {FR_TOP_MAX})")
     _on_current_device(logits, token, workspace)
+    _need(workspace is None or workspace.is_contiguous(), "workspace must be contiguous")
     dev, f32 = logits.device, torch.float32
     res = {}
     p_token = p_lp = p_ent = p_lse = p_tl = p_ti = p_ws = None

@@ -680,11 +680,27 @@ fr_status logits_args_ok(const void *logits, int64_t rows, int64_t cols, int64_t
   return FR_OK;
 }
 
+// Whether no row of p lies over one of q: they are the same rows, or apart, or (with
+// the same ld) in the gaps of one another.
+bool rows_apart(const void *p, const void *q, int64_t rows, int64_t cols, int64_t lp, int64_t lq,
+                int64_t es) {
+  const uint64_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  if (a == b) return lp == lq || rows == 1;
+  const uint64_t a1 = a + static_cast<uint64_t>(((rows - 1) * lp + cols) * es);
+  const uint64_t b1 = b + static_cast<uint64_t>(((rows - 1) * lq + cols) * es);
+  if (a1 <= b || b1 <= a) return true;
+  if (lp != lq) return false;
+  const uint64_t row = static_cast<uint64_t>(lp * es), used = static_cast<uint64_t>(cols * es);
+  const uint64_t shift = a < b ? (b - a) % row : row - (a - b) % row;  // of q's rows in p's
+  return shift >= used && shift + used <= row;
+}
+
 fr_status gradient_args_ok(const void *logits, const void *dlogits, int64_t rows, int64_t cols,
                            int64_t ld, int64_t ldd, fr_dtype dtype) {
   if (fr_status st = logits_args_ok(logits, rows, cols, ld, dtype)) return st;
   if (fr_status st = logits_args_ok(dlogits, rows, cols, ldd, dtype)) return st;
-  if (logits == dlogits && ld != ldd) return FR_ERR_INVALID_ARG;
+  if (!rows_apart(logits, dlogits, rows, cols, ld, ldd, dtype == FR_F32 ? 4 : 2))
+    return FR_ERR_INVALID_ARG;
   return FR_OK;
 }
 

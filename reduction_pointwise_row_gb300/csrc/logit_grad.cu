@@ -666,9 +666,9 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
         name(k++);
         if (k >= back)
           wait_for(&sh.full[(k - back) % nbuf], ((k - back) / nbuf) & 1, ok, &sh.gave_up, a.err);
-        if (!ok) {
-          row = -1;
-        } else {
+        if (!ok && q == 0) {
+          row = -1;  // no more requests
+        } else {     // the others wait for what the first may still have asked for
           const int i = (k - 1) % kAnswers;
           fence_proxy_async_smem();  // the answer that was here before is read
           mbar_arrive_expect_tx(&sh.answered[i], 16);

@@ -200,3 +200,28 @@ def test_algorithmic_bytes_of_the_logits_calls():
     assert t.algorithmic_bytes("distill_backward", R, C, top=64) == R * (4 * C + 768 + 8)
     assert t.algorithmic_bytes("distill_backward", R, C, top=64, loss=False) == R * (4 * C + 772)
     assert t.algorithmic_bytes("xent_backward", R, C, dtype="f32") == R * (8 * C + 16)
+
+
+OVERLAPS = [  # (dlogits - logits in bytes, rows, cols, ld, ldd, allowed), bf16
+    (0, 4, 8, 8, 8, True), (0, 4, 8, 16, 8, False), (0, 4, 8, 8, 16, False),
+    (0, 1, 8, 16, 8, True),
+    (64, 4, 8, 8, 8, True), (62, 4, 8, 8, 8, False), (-64, 4, 8, 8, 8, True),
+    (-62, 4, 8, 8, 8, False), (2, 4, 8, 8, 8, False), (16, 4, 8, 8, 8, False),
+    (16, 4, 8, 16, 16, True), (14, 4, 8, 16, 16, False), (18, 4, 8, 16, 16, False),
+    (-16, 4, 8, 16, 16, True), (-18, 4, 8, 16, 16, False), (48, 4, 8, 16, 16, True),
+    (-80, 4, 8, 16, 16, True), (32, 4, 8, 16, 16, False), (16, 4, 8, 32, 16, False),
+    (16, 4, 8, 20, 20, True), (24, 4, 8, 20, 20, True), (26, 4, 8, 20, 20, False),
+    (8, 1, 8, 100, 100, False), (16, 1, 8, 8, 8, True), (-16, 1, 8, 8, 8, True),
+]
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers are not device memory")
+@pytest.mark.parametrize("shift,rows,cols,ld,ldd,allowed", OVERLAPS)
+def test_gradients_over_a_part_of_the_logits_are_refused(shift, rows, cols, ld, ldd, allowed):
+    used = {(r * ld + j) * 2 for r in range(rows) for j in range(cols)}
+    own = {shift + (r * ldd + j) * 2 for r in range(rows) for j in range(cols)}
+    if allowed:  # what is allowed is disjoint or the same rows
+        assert not used & own or used == own
+    for call in (logprobs_backward, distill_backward, xent_backward):
+        assert call(dlogits=P(0x10000 + shift), rows=rows, cols=cols, ld=ld, ldd=ldd) == (
+            OK_SO_FAR if allowed else 1)

@@ -829,3 +829,28 @@ def test_teacher_entries_at_the_lowest_value(temperature):
         got = fr.fr_distill_backward(x.cuda(), i.cuda(), z.cuda(), torch.ones(1, device="cuda"),
                                      temperature, form=form)
         ref.assert_near(got["loss"], r, b, form)
+
+
+def test_a_workspace_with_gaps_is_refused():
+    x = logits(700, 4099, "bf16", 1).cuda()
+    n = fr.fr_workspace_size("logprobs", 700, 4099, "bf16")
+    for ws in (torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2],
+               torch.empty(1, dtype=torch.uint8, device="cuda").expand(n)):
+        with pytest.raises(ValueError):
+            fr.fr_logprobs(x, top=3, workspace=ws)
+
+
+def test_a_gradient_between_the_logits_rows():
+    """dlogits in the padding of the logits' rows."""
+    both = torch.zeros(300, 2 * 12000, device="cuda")
+    x, t = logits(300, 12000, "f32", 6), tokens(300, 12000, 6)
+    both[:, :12000] = x.cuda()
+    g = upstream(300, 6)
+    r = ref.xent_backward(x, t, g)
+    for form in ("looped", "persistent", "split"):
+        d = fr.fr_xent_backward(both[:, :12000], t.cuda(), g.cuda(), dlogits=both[:, 12000:],
+                                form=form)["dlogits"]
+        ref.assert_near(d, r, ref.gradient_bound(x, r, g), form)
+        assert torch.equal(both[:, :12000].cpu(), x)
+    with pytest.raises(fr.FRError):
+        fr.fr_xent_backward(both[:, :12000], t.cuda(), g.cuda(), dlogits=both[:, 11999:23999])
