@@ -194,8 +194,8 @@ __device__ __forceinline__ float teacher_loss(const TeacherShared &sh, int top, 
   float sum = 0.0f;
   for (int e = threadIdx.x & 31; e < top; e += 32)
     if (sh.idx[e] >= 0)
-      sum += sh.q[e] * (temperature * (sh.logq[e] + logl) - (sh.x[e] - st.m));
-  return temperature * warp_sum(sum);
+      sum += sh.q[e] * temperature * (temperature * (sh.logq[e] + logl) - (sh.x[e] - st.m));
+  return warp_sum(sum);
 }
 
 // Entry e's element: g (p - sum of its weights).

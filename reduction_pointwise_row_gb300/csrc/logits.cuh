@@ -290,19 +290,20 @@ __device__ __forceinline__ Teacher teacher_load(const int64_t *index, const floa
   return teacher_finish(raw, cols, temperature);
 }
 
-// T^2 sum q (log q - log p) with log p = (x - m) / T - log l, as T sum q (T (log q +
-// log l) - (x - m)): x - m may be the type's lowest value, which 1 / T takes out of
-// range.  Entries without weight add nothing, whatever the student gives them.
+// T^2 sum q (log q - log p) with log p = (x - m) / T - log l, as sum q T (T (log q +
+// log l) - (x - m)): x - m may be the type's lowest value, which 1 / T, or a sum without
+// the weights or T, would take out of range.  Entries without weight add nothing, whatever the student gives them.
 __device__ __forceinline__ float teacher_loss(const Teacher &t, const RowStat &st,
                                               float temperature) {
   const float logl = logf(st.l);
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < kTopPerLane; ++i)
-    if (t.q[i] != 0.0f) sum += t.q[i] * (temperature * (t.logq[i] + logl) - (t.x[i] - st.m));
+    if (t.q[i] != 0.0f)
+      sum += t.q[i] * temperature * (temperature * (t.logq[i] + logl) - (t.x[i] - st.m));
   sum = warp_sum(sum);
   if (t.bad) return __int_as_float(0x7fc00000);
-  return t.any ? temperature * sum : 0.0f;
+  return t.any ? sum : 0.0f;
 }
 
 }  // namespace fr

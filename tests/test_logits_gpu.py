@@ -854,3 +854,20 @@ def test_a_gradient_between_the_logits_rows():
         assert torch.equal(both[:, :12000].cpu(), x)
     with pytest.raises(fr.FRError):
         fr.fr_xent_backward(both[:, :12000], t.cuda(), g.cuda(), dlogits=both[:, 11999:23999])
+
+
+@pytest.mark.parametrize("temperature", [0.5, 0.99, 2.0])
+def test_a_teacher_whose_entries_are_all_masked(temperature):
+    """T 3.4e38 and a little: in range for T < 1, +inf for 2."""
+    x = logits(3, 700, "f32", 5)
+    x[:, :60] = torch.finfo(torch.float32).min
+    i = torch.arange(50).repeat(3, 1)
+    z = torch.from_numpy(rng(50).normal(0, 3, (3, 50)).astype(np.float32))
+    r = ref.distill(x, i, z, temperature).float().double()
+    b = loss_bound(x, r, i, z, temperature)
+    assert torch.isinf(r).all() == (temperature > 1)
+    for form in ("looped", "split", "persistent"):
+        ref.assert_near(fr.fr_distill(x.cuda(), i.cuda(), z.cuda(), temperature, form=form), r, b)
+        got = fr.fr_distill_backward(x.cuda(), i.cuda(), z.cuda(), torch.ones(1, device="cuda"),
+                                     temperature, form=form)
+        ref.assert_near(got["loss"], r, b, form)
