@@ -863,7 +863,7 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
       };
       // A row with a teacher is copied whatever its entries are: the first one, whose
       // entries have been looked at no earlier than its copy landed, is folded before
-      // (bf16 [2048, 50257], 64 entries: 73.6 us, 71.5 so; every row so: 71.5, but in
+      // (bf16 [2048, 50257], 64 entries: 73.6 us, 72.7 so; every row so: 71.5, but in
       // clusters [1022, 65537] 59.8, 61.3).
       const bool early = DISTILL && k == 0;
       int kind = kRowGrad, n = 0;
@@ -982,26 +982,41 @@ struct StagedShape {
   uint32_t buf_bytes;
 };
 
-// Workers for 8 units (64 bf16 logits) each, or 10 where that is over 576 of them:
-// fewer units leave more of the time to what every thread does once a row, more of
-// them too few warps to cover the latencies (us; 6283 units, bf16 [4096, 50257]: 320
-// workers 128.8, 512 126.1, 640 126.0, 800 131.0; 4096 units, bf16 [1022, 65537] in
-// clusters of two: 416 54.9, 512 53.3, 576 57.8).  As many CTAs an SM as their registers
-// and two buffers each leave room for, and up to four buffers where the room is there.
-StagedShape staged_shape(int64_t cols, int es, int cluster, bool distill, const DevInfo &info) {
+// As many CTAs an SM as two buffers each and their registers leave room for, with 64
+// workers or more: a row is a chain of dependent steps for its CTA, so rows in flight
+// matter more than workers a row.  (us, CTAs an SM of the rule / with workers for 8
+// units each first: logprobs_backward bf16 [6000, 24001] 97.7 / 128.2, [16000, 8200]
+// 94.6 / 113.0; distill_backward with 64 entries [16000, 8200] 110.3 / 156.5, [10000,
+// 12000] 96.4 / 115.8.)  Four at most, five where that takes all rows at once
+// (logprobs_backward [16000, 8200] 94.6 with four, 100.1 with five; [700, 8200] 10.1,
+// 8.3).  Then workers for 8 units (64 bf16 logits) each, or 10 where
+// that is over 576 of them, as far as there is room: fewer units leave more of the time
+// to what every thread does once a row, more of them too few warps to cover the
+// latencies (6283 units, bf16 [4096, 50257]: 320 workers 128.8, 512 126.1, 640 126.0,
+// 800 131.0; 4096 units, bf16 [1022, 65537] in clusters of two: 416 54.9, 512 53.3, 576
+// 57.8).  Up to four buffers where the room is there.
+StagedShape staged_shape(int64_t rows, int64_t cols, int es, int cluster, bool distill,
+                         const DevInfo &info) {
   StagedShape sh;
   sh.buf_bytes = static_cast<uint32_t>(staged_buf_bytes(cols, es, cluster));
   const int64_t units = sh.buf_bytes / 16;
+  const int helpers = 32 * ((distill ? kHelpers<true> : kHelpers<false>) + 1);
+  const int64_t sm_threads = kMaxThreads + 64;  // at 72 registers a thread
+  const int64_t sm_smem = info.max_smem_optin + 1024;
+  const int64_t other = sm_smem - staged_smem(distill, info.max_smem_optin);
+  const int64_t wanted = (rows * cluster + info.sm_count - 1) / info.sm_count;
+  int64_t ctas = 1, room = kMaxThreads - helpers;
+  for (int64_t n = 2; n <= (wanted <= 5 ? wanted : 4); ++n) {
+    const int64_t left = sm_threads / n / 32 * 32 - helpers;
+    if (left < 64 || n * (2 * sh.buf_bytes + other) > sm_smem) break;
+    ctas = n;
+    room = left;
+  }
   int64_t workers = (units / 8 + 31) / 32 * 32;
   if (workers > 576) workers = (units / 10 + 31) / 32 * 32;
-  const int helpers = 32 * ((distill ? kHelpers<true> : kHelpers<false>) + 1);
-  workers = workers < 64 ? 64 : workers > kMaxThreads - helpers ? kMaxThreads - helpers : workers;
+  workers = workers < 64 ? 64 : workers > room ? room : workers;
   sh.threads = static_cast<int>(workers) + helpers;
-  const int64_t room = staged_smem(distill, info.max_smem_optin);
-  int64_t ctas = (kMaxThreads + 64) / sh.threads;
-  const int64_t other = info.max_smem_optin - room + 1024;
-  while (ctas > 1 && ctas * (2 * sh.buf_bytes + other) > info.max_smem_optin) --ctas;
-  int64_t nbuf = ((info.max_smem_optin + 1024) / ctas - other) / (sh.buf_bytes > 0 ? sh.buf_bytes : 1);
+  const int64_t nbuf = (sm_smem / ctas - other) / (sh.buf_bytes > 0 ? sh.buf_bytes : 1);
   sh.nbuf = static_cast<int>(nbuf < 1 ? 1 : nbuf > kMaxBufs ? kMaxBufs : nbuf);
   return sh;
 }
@@ -1024,7 +1039,7 @@ cudaError_t launch_form(const LogitsBackward &a, int cluster, bool vec32, bool v
   }
   auto *kern = vec16 ? &logit_grad_staged<F32, DISTILL, HAS_B, true>
                      : &logit_grad_staged<F32, DISTILL, HAS_B, false>;
-  const StagedShape sh = staged_shape(a.cols, F32 ? 4 : 2, cluster, DISTILL, info);
+  const StagedShape sh = staged_shape(a.rows, a.cols, F32 ? 4 : 2, cluster, DISTILL, info);
   const size_t smem = static_cast<size_t>(sh.buf_bytes) * sh.nbuf;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kern), smem);
   if (e != cudaSuccess) return e;
