@@ -20,8 +20,9 @@
 //           second kernel, a warp per row with little state and so many warps an
 //           SM, does the rest: the groups are every eighth of a lane's maxima; the
 //           vectors under the maxima that reach the floor are read again.  (In
-//           one kernel the list's 7 us a row of dependent steps held up the loads:
-//           bf16 [8192, 50257] top 20 took 200-220 us.)  A list that still grows
+//           one kernel the list's 5-7 us a row of dependent steps held up the loads:
+//           bf16 [8192, 50257] top 20 took 173 us by each warp after its row and 192
+//           by a helper warp, 152 so.)  A list that still grows
 //           (equal logits, an order that puts the largest together)
 //           is cut to its k largest, whose least is the next floor.
 //   held    (rows in registers) the groups are places of the lanes' vectors; the
