@@ -262,7 +262,8 @@ logit_grad_held(LogitsBackward a) {
   RowStat st = stat_empty();
   stat_fold<F32, HAS_B, NV>(st, v, L::max(v), c);
   if (sx != -INFINITY) st = stat_merge(st, RowStat{sx, 1.0f, 0.0f}, c);
-  st = warp_stat(st, c);  // every lane has read its part of the row
+  st = warp_stat(st, c);
+  __syncwarp();  // every lane has read its part of the row
   if (kind == kRowNan && lane == 0) atomicCAS(a.err, 0, FR_DEVERR_BAD_TARGET);
   const RowCoef r =
       DISTILL ? row_coef(st, c, g * (1.0f / st.l), 0.0f) : token_coef(st, c, g, h, HAS_B);
@@ -558,8 +559,8 @@ __device__ __forceinline__ bool worker_barrier(int workers, bool any) {
 }
 
 // A wait of at most `budget` SM clocks (0: it runs out at once), shorter where another
-// of the CTA's waits ran out.  After that its thread waits for nothing any more, the CTA's helpers copy
-// nothing more, and its workers stop.
+// of the CTA's waits ran out.  After that its thread waits for nothing any more, the
+// CTA's helpers copy nothing more, and its workers stop.
 __device__ __forceinline__ void wait_for(uint64_t *bar, uint32_t parity, bool &ok, int *gave_up,
                                          int *err, long long budget = kWaitBudget) {
   if (!ok) return;
@@ -876,7 +877,8 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
         if (kind != kNoRow) n = par.n;
       }
       if (kind != kNoRow)
-        warp_wait(&sh.full[b], lap & 1, ok, &sh.gave_up, a.err, k == 0 ? kFirstBudget : kWaitBudget);
+        warp_wait(&sh.full[b], lap & 1, ok, &sh.gave_up, a.err,
+                  k == 0 ? kFirstBudget : kWaitBudget);
       if (!ok) kind = kNoRow;
       RowCoef r{};
       auto end_stat = [&](int kind) {  // this lane's scalar of the row's ends
@@ -989,7 +991,8 @@ struct StagedShape {
 // 94.6 / 113.0; distill_backward with 64 entries [16000, 8200] 110.3 / 156.5, [10000,
 // 12000] 96.4 / 115.8.)  Four at most, five where that takes all rows at once
 // (logprobs_backward [16000, 8200] 94.6 with four, 100.1 with five; [700, 8200] 10.1,
-// 8.3).  Then workers for 8 units (64 bf16 logits) each, or 10 where
+// 8.3), and two buffers, not one, for each ([2048, 50257] 70.3 in one CTA with two, 75.7
+// in two with one).  Then workers for 8 units (64 bf16 logits) each, or 10 where
 // that is over 576 of them, as far as there is room: fewer units leave more of the time
 // to what every thread does once a row, more of them too few warps to cover the
 // latencies (6283 units, bf16 [4096, 50257]: 320 workers 128.8, 512 126.1, 640 126.0,

@@ -292,7 +292,8 @@ __device__ __forceinline__ Teacher teacher_load(const int64_t *index, const floa
 
 // T^2 sum q (log q - log p) with log p = (x - m) / T - log l, as sum q T (T (log q +
 // log l) - (x - m)): x - m may be the type's lowest value, which 1 / T, or a sum without
-// the weights or T, would take out of range.  Entries without weight add nothing, whatever the student gives them.
+// the weights or T, would take out of range.  Entries without weight add nothing,
+// whatever the student gives them.
 __device__ __forceinline__ float teacher_loss(const Teacher &t, const RowStat &st,
                                               float temperature) {
   const float logl = logf(st.l);
