@@ -865,7 +865,9 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
       // A row with a teacher is copied whatever its entries are: the first one, whose
       // entries have been looked at no earlier than its copy landed, is folded before
       // (bf16 [2048, 50257], 64 entries: 73.6 us, 72.7 so; every row so: 71.5, but in
-      // clusters [1022, 65537] 59.8, 61.3).
+      // clusters [1022, 65537] 59.8, 61.3).  Every row with a teacher adds its ragged
+      // ends after its units: which rows are a CTA's first differs from run to run, and
+      // the sums' order must not.
       const bool early = DISTILL && k == 0;
       int kind = kRowGrad, n = 0;
       if (early) {
@@ -886,7 +888,7 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
         const float x = has ? par.end[lane] : -INFINITY;
         return x != -INFINITY ? RowStat{x, 1.0f, 0.0f} : stat_empty();
       };
-      RowStat st = early ? stat_empty() : end_stat(kind);
+      RowStat st = DISTILL ? stat_empty() : end_stat(kind);
       if (kind == kRowGrad) {
         int i = tid;
         for (; i + 3 * workers < n; i += 4 * workers) {
@@ -898,8 +900,8 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
           const V8 v[1] = {lds_units<F32, true>(buf, i, workers, n)};
           stat_fold<F32, HAS_B, 1>(st, v, L::max(v), c);
         }
-        if (early) {
-          kind = ready();
+        if (early) kind = ready();
+        if constexpr (DISTILL) {
           const RowStat end = end_stat(kind);
           if (end.l != 0.0f) st = stat_merge(st, end, c);
         }
