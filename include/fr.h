@@ -394,6 +394,8 @@ fr_status fr_xent_mean_from_parts(const void *workspace, float *loss_mean, fr_st
  * 4 KiB, in registers), looped (a warp per row) and split (a cluster of up to 8
  * CTAs per row, for few rows).  AUTO takes the looped form from 4 x SMs rows with
  * alternatives (what fr_auto_form and fr_workspace_size assume), 8 x SMs without.
+ * The persistent form, and the looped one with alternatives, take at most
+ * 4 * INT32_MAX rows (more: FR_ERR_UNSUPPORTED_FORM, and AUTO takes another form).
  */
 fr_status fr_logprobs(const void *logits, const int64_t *token, float *logprob, float *entropy,
                       float *lse, float *top_logprob, int64_t *top_index, int32_t top,

@@ -240,8 +240,12 @@ int forward_split(int64_t rows, int64_t cols, int es, int sm_count) {
 // alternatives (looped / split, 20 of 50257: 304 rows 26.8 / 19.4, 608 28.7 / 34.2,
 // 1216 37.1 / 53.2), without from 8 x SMs (distillation, 50257: 608 rows 21.9 / 13.4, 1024
 // 27.9 / 22.3, 1216 24.7 / 24.3, 2048 34.7 / 40.1).
+//
+// More rows than one grid has warps for go to the kernels whose CTAs take several.
 fr_form pick_forward(int64_t rows, int64_t cols, int es, bool top, int sm_count) {
-  if (fr::logits_held_ok(cols, es)) return FR_FORM_PERSISTENT;
+  const bool grid = fr::logits_grid_ok(rows);
+  if (fr::logits_held_ok(cols, es) && grid) return FR_FORM_PERSISTENT;
+  if (top && !grid) return FR_FORM_SPLIT;
   return rows >= (top ? 4 : 8) * static_cast<int64_t>(sm_count) ? FR_FORM_LOOPED : FR_FORM_SPLIT;
 }
 
@@ -731,14 +735,18 @@ bool aligned_or_null(const void *p, size_t a) { return p == nullptr || aligned(p
 fr_status run_forward(fr::LogitsForward &a, fr_dtype dtype, bool distill, fr_form form,
                       size_t workspace_bytes, fr_stream_t stream) {
   if (form < FR_FORM_AUTO || form > FR_FORM_SPLIT) return FR_ERR_UNSUPPORTED_FORM;
+  const bool f32 = dtype == FR_F32, top = !distill && a.top > 0;
+  const int es = f32 ? 4 : 2;
+  if (form == FR_FORM_PERSISTENT && !fr::logits_held_ok(a.cols, es)) return FR_ERR_UNSUPPORTED_FORM;
+  if ((form == FR_FORM_PERSISTENT || (form == FR_FORM_LOOPED && top)) &&
+      !fr::logits_grid_ok(a.rows))
+    return FR_ERR_UNSUPPORTED_FORM;
   fr::DevInfo info;
   if (fr_status st = logits_device_ok(a.cols, &info, &a.err)) return st;
-  const bool f32 = dtype == FR_F32;
-  const int es = f32 ? 4 : 2;
-  const fr_form f = form == FR_FORM_AUTO ? pick_forward(a.rows, a.cols, es, !distill && a.top > 0, info.sm_count) : form;
-  if (f == FR_FORM_PERSISTENT && !fr::logits_held_ok(a.cols, es)) return FR_ERR_UNSUPPORTED_FORM;
-  if (!distill && a.top > 0 && f == FR_FORM_LOOPED) {
-    if (!a.workspace || workspace_bytes < fr::logprobs_workspace(a.rows, a.cols, f32 ? 4 : 2))
+  const fr_form f =
+      form == FR_FORM_AUTO ? pick_forward(a.rows, a.cols, es, top, info.sm_count) : form;
+  if (top && f == FR_FORM_LOOPED) {
+    if (!a.workspace || workspace_bytes < fr::logprobs_workspace(a.rows, a.cols, es))
       return FR_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned(a.workspace, 16)) return FR_ERR_MISALIGNED;
   }

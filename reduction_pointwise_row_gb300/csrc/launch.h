@@ -237,6 +237,9 @@ struct LogitsForward {
 size_t logprobs_workspace(int64_t rows, int64_t cols, int es);
 // True when a warp holds a row in its registers.
 bool logits_held_ok(int64_t cols, int es);
+// True when a grid has a warp for every row: the held rows, and the alternatives of
+// the rows that a warp streams.
+bool logits_grid_ok(int64_t rows);
 // split: -1, a warp per row that holds it; 0, a warp per row that streams it; else a cluster of that many CTAs (1, 2, 4 or 8) per row
 cudaError_t launch_logits_forward(const LogitsForward &a, bool f32, bool distill, int split,
                                   int sm_count, cudaStream_t s);

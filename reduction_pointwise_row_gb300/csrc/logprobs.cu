@@ -919,6 +919,8 @@ cudaError_t launch_forward(const LogitsForward &a, int split, int sm_count, cuda
 
 bool logits_held_ok(int64_t cols, int es) { return cols * es / kVecBytes <= kHeldVectors; }
 
+bool logits_grid_ok(int64_t rows) { return rows <= int64_t{INT32_MAX} * kTopWarps; }
+
 size_t logprobs_workspace(int64_t rows, int64_t cols, int es) {
   return static_cast<size_t>(rows) * (8 + 128 * static_cast<size_t>(maxima_steps(cols, es)));
 }
