@@ -384,8 +384,8 @@ def _torch():
     global _TORCH
     if _TORCH is None:
         import torch
-        _TORCH = torch
         _LOGIT_DTYPES.update({torch.float32: DTYPES["f32"], torch.bfloat16: DTYPES["bf16"]})
+        _TORCH = torch  # last: another thread's call that sees it finds the table filled
     return _TORCH
 
 

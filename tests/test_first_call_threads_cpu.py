@@ -1,0 +1,22 @@
+"""What the binding looks up with its first call is complete for another thread's call
+that begins meanwhile."""
+import torch
+
+import reduction_pointwise_row_gb300 as fr
+
+
+class Watched(dict):
+    """A table that notes what another thread would see just before it is filled."""
+
+    def update(self, *a, **kw):
+        self.seen = fr._TORCH
+        super().update(*a, **kw)
+
+
+def test_the_dtype_table_is_filled_before_torch_is_published(monkeypatch):
+    table = Watched()
+    monkeypatch.setattr(fr, "_TORCH", None)
+    monkeypatch.setattr(fr, "_LOGIT_DTYPES", table)
+    fr._torch()
+    assert table.seen is None, "a second thread finds torch there and the table empty"
+    assert fr._TORCH is torch and set(table) == {torch.float32, torch.bfloat16}
