@@ -148,9 +148,9 @@ def _stream(stream=None, device_index=None):
     if _current_raw_stream is None:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _current_raw_stream = raw if raw is not None else (
-            lambda i: torch.cuda.current_stream(i).cuda_stream)
         _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _current_raw_stream = raw if raw is not None else (  # last: it is what is tested
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
     return _current_raw_stream(_current_device() if device_index is None else device_index)
 
 
