@@ -32,13 +32,21 @@ struct alignas(32) V8 {
 
 // ---- global memory -------------------------------------------------------
 
+// The loads are volatile with a memory clobber, and not of the read-only kind (.nc): a
+// kernel may be placed while the one before it still runs (pdl_enter below), so none of
+// them may move before its wait, and what they read may be written until then.  (Against
+// volatile or movable .nc loads: every workload of bench.py and every call over logits
+// within 0.5 %, single calls of 7-9 us within their spread.)
+
 // 32-byte read-once load: no L1 allocation, first in line for L2 eviction.
 __device__ __forceinline__ V8 ld_stream_v8(const void *p) {
   V8 v;
-  asm("ld.global.nc.L1::no_allocate.L2::evict_first.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+  asm volatile(
+      "ld.global.L1::no_allocate.L2::evict_first.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
       : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]),
         "=r"(v.w[6]), "=r"(v.w[7])
-      : "l"(p));
+      : "l"(p)
+      : "memory");
   return v;
 }
 
@@ -46,38 +54,43 @@ __device__ __forceinline__ V8 ld_stream_v8(const void *p) {
 // createpolicy, e.g. l2_evict_first_policy()) as the L2 hint.
 __device__ __forceinline__ uint4 ld_stream_u4(const void *p, uint64_t policy) {
   uint4 v;
-  asm("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
-      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-      : "l"(p), "l"(policy));
+  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p), "l"(policy)
+               : "memory");
   return v;
 }
 
 // 32-byte load of data that many CTAs re-read (kept in L2 normally).
 __device__ __forceinline__ V8 ld_keep_v8(const void *p) {
   V8 v;
-  asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-      : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]),
-        "=r"(v.w[6]), "=r"(v.w[7])
-      : "l"(p));
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]),
+                 "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
+               : "l"(p)
+               : "memory");
   return v;
 }
 
 // 16-byte load of data that many CTAs re-read.
 __device__ __forceinline__ float4 ld_keep_f4(const float *p) {
   float4 v;
-  asm("ld.global.nc.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p)
+               : "memory");
   return v;
 }
 
 __device__ __forceinline__ float ld_stream_f32(const float *p) {
   float v;
-  asm("ld.global.nc.L1::no_allocate.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
   return v;
 }
 
 __device__ __forceinline__ uint16_t ld_stream_u16(const void *p) {
   uint16_t v;
-  asm("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
   return v;
 }
 
