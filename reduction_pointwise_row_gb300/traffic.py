@@ -46,14 +46,14 @@ def algorithmic_bytes(op: str, rows: int, cols: int, **kw) -> int:
         return rows * cols * 2 + rows * 8 + rows * 4 + 4
     if op == "xent_f32":              # the same with fp32 logits
         return rows * cols * 4 + rows * 8 + rows * 4 + 4
-    # rows of logits (kw: dtype "bf16" or "f32", top entries a row, loss wanted); tokens
-    # and teacher indices int64, everything else a row has fp32
+    # rows of logits (kw: dtype "bf16" or "f32", top entries a row, loss wanted, entropy's
+    # gradient given); tokens and teacher indices int64, everything else a row has fp32
     logits = rows * cols * (4 if kw.get("dtype", "bf16") == "f32" else 2)
     top, loss = kw.get("top", 0), 4 * rows if kw.get("loss", True) else 0
     if op == "logprobs":              # logprob, entropy, lse and the alternatives out
         return logits + rows * (8 + 3 * 4 + 12 * top)
     if op == "logprobs_backward":     # dlogprob and dentropy in
-        return 2 * logits + rows * (8 + 2 * 4)
+        return 2 * logits + rows * (8 + 4 + (4 if kw.get("entropy", True) else 0))
     if op == "distill":               # teacher entries in
         return logits + rows * 12 * top + 4 * rows
     if op == "distill_backward":      # teacher entries and dloss in

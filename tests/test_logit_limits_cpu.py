@@ -37,3 +37,12 @@ def test_rows_within_the_limits_reach_the_device_check():
         assert logprobs(rows=rows, top=1, form=3, **one) == OK_SO_FAR
         assert logprobs(rows=rows, top=1, **one) == OK_SO_FAR
         assert distill(rows=rows, form=2, **one) == OK_SO_FAR
+
+
+def test_bytes_of_a_gradient_without_the_entropys():
+    from reduction_pointwise_row_gb300 import traffic
+    count = traffic.algorithmic_bytes
+    for dtype, es in (("bf16", 2), ("f32", 4)):
+        assert count("logprobs_backward", 7, 1001, dtype=dtype) == 7 * (2 * es * 1001 + 16)
+        assert count("logprobs_backward", 7, 1001, dtype=dtype, entropy=False) == \
+            7 * (2 * es * 1001 + 12)
