@@ -341,11 +341,15 @@ fr_status fr_xent_mean_from_parts(const void *workspace, float *loss_mean, fr_st
  * the logits of fr_xent and fr_softmax makes around them.  Shared by all five:
  *
  *   logits       bf16 or fp32 (`dtype`) [rows, ld] device input, any ld >= cols
- *                and any element-aligned address.  -inf masks an element (its
- *                probability, its share of the entropy and its gradient are
- *                0); the type's lowest value masks too.  A NaN, a +inf, or a
- *                row whose every logit is -inf makes the row's results NaN (the
- *                latter's lse is -inf).
+ *                and any element-aligned address, cols < 2^31 (more:
+ *                FR_ERR_UNSUPPORTED_FORM).  -inf masks an element: its
+ *                probability, its share of the entropy and its gradient are 0,
+ *                but for the term that the row's token (g) or a teacher's
+ *                entry with weight (-dloss T q) has there.  The type's lowest
+ *                value masks too.  A NaN, a +inf, or a row whose every logit is
+ *                -inf makes the row's results NaN (the latter's lse is -inf),
+ *                but for the zeros of rows without a loss: ignored ones, and
+ *                those without weight in their teacher's entries.
  *   dlogits      of `dtype` [rows, ldd] device output, the gradient, rounded
  *                once (nearest even).  It may be the logits' own buffer (ldd ==
  *                ld) or, with ldd == ld, lie between its rows; any other overlap of
@@ -358,7 +362,7 @@ fr_status fr_xent_mean_from_parts(const void *workspace, float *loss_mean, fr_st
  * Statistics are those of each call's own pass (max, sum of exponentials, fp32
  * sums over short runs); x - max is taken before it is scaled, so neither a
  * common offset of a row nor a lowest-value mask costs digits.  Results do not
- * depend on other rows and are the same from run to run.  A token outside [0,
+ * depend on what other rows hold and are the same from run to run.  A token outside [0,
  * cols) other than ignore_index, or a teacher index >= cols, makes that row's
  * log probability, loss and gradient NaN and sets FR_DEVERR_BAD_TARGET; nothing
  * outside the row is read.  dlogits beyond column cols of a row are not written.
@@ -426,7 +430,8 @@ fr_status fr_logprobs_backward(const void *logits, const int64_t *token, const f
  * a negative index is padding and is not looked at; an entry of -inf has no
  * weight; the same index twice counts twice.  A row without weight (all
  * padding or -inf) has loss 0 and no gradient.  An entry with weight whose
- * logit is -inf makes the loss +inf.
+ * logit is -inf makes the loss +inf; at fp32's lowest value it costs temperature
+ * q 3.4e38, which entries that all lie there take past fp32 from about temperature 1 on.
  *
  *   teacher_index int64, teacher_logit fp32: [rows, ldt] device inputs, the first
  *                `top` of each row's ldt >= top elements

@@ -252,6 +252,8 @@ fr_form pick_forward(int64_t rows, int64_t cols, int es, bool top, int sm_count)
 // CTAs per row of the gradients' staged form, `least` or more: enough for two
 // buffers of a CTA's run of the row in shared memory (one, where 8 CTAs do not
 // reach that), and for few rows as many as fill the SMs.  0: the row is too long.
+// (One CTA for bf16 rows of 56-70 KiB suits distillation, 114 us against 125 in clusters
+// of two at [5000, 30000]; cross entropy would take 94 in clusters, 107 so.)
 int backward_cluster(int64_t rows, int64_t cols, int es, bool distill, int sm_count, int smem,
                      int least) {
   int cluster = least;
@@ -673,8 +675,7 @@ fr_status fr_xent_mean_from_parts(const void *workspace, float *loss_mean, fr_st
 
 namespace {
 
-// Checks that the calls over rows of logits share; on FR_OK the device is
-// usable and `err` is its error word.
+// Checks that the calls over rows of logits share.
 fr_status logits_args_ok(const void *logits, int64_t rows, int64_t cols, int64_t ld,
                          fr_dtype dtype) {
   if (dtype != FR_BF16 && dtype != FR_F32) return FR_ERR_UNSUPPORTED_DTYPE;
@@ -719,6 +720,7 @@ fr_status teacher_args_ok(const int64_t *index, const float *logit, int32_t top,
   return FR_OK;
 }
 
+// On FR_OK the device is usable and `err` is its error word.
 fr_status logits_device_ok(int64_t cols, fr::DevInfo *info, int **err) {
   if (cols >= (INT64_C(1) << 31)) return FR_ERR_UNSUPPORTED_FORM;  // 32-bit in-row indices
   if (fr_status st = device_ok(info)) return st;

@@ -113,7 +113,7 @@ __device__ __forceinline__ V8 grad_vector(const V8 &x, const RowCoef &r) {
 // NaN (a target past the row) before anything is read of it.
 enum RowKind { kRowGrad = 0, kRowZero = 1, kRowNan = 2, kNoRow = 3 };
 
-// What a token makes of its row.  LOGITS only: an entropy's gradient is left.
+// What a token makes of its row.  An ignored one leaves the entropy's gradient (HAS_B).
 template <bool HAS_B>
 __device__ __forceinline__ int token_kind(const LogitsBackward &a, int64_t token) {
   if (!a.token) return kRowGrad;
@@ -586,6 +586,8 @@ __device__ __forceinline__ void warp_wait(uint64_t *bar, uint32_t parity, bool &
 // Asks for a cluster of this grid that has not been launched, to be taken over by
 // this one; the answer arrives in the shared memory of all its CTAs (at the same
 // place), counted on their `bar`.  Not to be asked again once the answer was no.
+// (multicast::cluster here is the answer's 16 bytes to the CTAs of the cluster; nothing is
+// loaded from memory by it.)
 __device__ __forceinline__ void request_cluster(uint4 *answer, uint64_t *bar, bool peers) {
   if (peers)
     asm volatile(
