@@ -158,7 +158,7 @@ fr_form pick_ras(int64_t rows, int64_t cols, int sm_count, bool bf16 = false) {
 // (x and y at different offsets within a 32-byte sector): a CTA per row up to
 // 32768 columns (the row in registers up to 4608, staged in shared memory
 // beyond), then a cluster per row with its runs staged in shared memory (608
-// x 65537: 62.6 us, looped 96.2; 608 x 131072: 148.0 against 191.4), looped
+// x 65537: 57.9 us, looped 89.6; 608 x 131072: 127.1 against 169.6), looped
 // past its reach.
 fr_form pick_softmax(int64_t rows, int64_t cols, bool vec, int sm_count) {
   if (cols <= 1024) return FR_FORM_PERSISTENT;
@@ -176,9 +176,9 @@ fr_form pick_softmax(int64_t rows, int64_t cols, bool vec, int sm_count) {
 }
 
 // bf16 softmax.  Rows out of phase: up to 32768 columns a CTA per row, the row
-// staged in shared memory (16384 x 4097: 48.3 us, looped 87.8; 4864 x 32768:
-// 95.1 against 183.5), then a cluster per row with staged runs (608 x 65537:
-// 32.9 us, looped 67.7; 2432 x 65537: 108.3 against 206.9), looped past its
+// staged in shared memory (16384 x 4097: 48.4 us, looped 97.4; 4864 x 32768:
+// 95.8 against 183.7), then a cluster per row with staged runs (608 x 65537:
+// 32.9 us, looped 63.1; 2432 x 65537: 108.0 against 201.3), looped past its
 // reach.  Rows in phase: up to 2048 columns a warp per row, up to 8192 a CTA
 // per row; at 16384 the looped form from 4 x SMs rows (608: looped 9.4 us, CTA
 // per row 10.5), a CTA per row below, and a CTA per row again from 8 x SMs
