@@ -449,13 +449,16 @@ constexpr int kMaxBufs = 4;
 constexpr int kMaxThreads = 832;  // 72 registers a thread
 constexpr int kMaxCluster = 8;
 constexpr long long kWaitBudget = 1LL << 31;  // SM clocks, about one second
-// A test-only build (-DFR_TEST_GRAD_WAIT_RUNS_OUT) gives the wait for a CTA's first row
-// no budget: it runs out whether or not the copy has landed.
-#ifdef FR_TEST_GRAD_WAIT_RUNS_OUT
-constexpr long long kFirstBudget = 0;
-#else
-constexpr long long kFirstBudget = kWaitBudget;
+// A test-only build (-DFR_TEST_GRAD_WAIT_RUNS_OUT, =2: in the first CTA of a cluster alone)
+// gives the wait for a CTA's first row no budget: it runs out whether or not the copy has
+// landed.
+#ifndef FR_TEST_GRAD_WAIT_RUNS_OUT
+#define FR_TEST_GRAD_WAIT_RUNS_OUT 0
 #endif
+__device__ __forceinline__ long long row_budget(uint32_t k, uint32_t q) {
+  constexpr int in = FR_TEST_GRAD_WAIT_RUNS_OUT;
+  return in != 0 && k == 0 && (in == 1 || q == 0) ? 0 : kWaitBudget;
+}
 
 struct RowParams {
   int kind;
@@ -881,8 +884,7 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
         if (kind != kNoRow) n = par.n;
       }
       if (kind != kNoRow)
-        warp_wait(&sh.full[b], lap & 1, ok, &sh.gave_up, a.err,
-                  k == 0 ? kFirstBudget : kWaitBudget);
+        warp_wait(&sh.full[b], lap & 1, ok, &sh.gave_up, a.err, row_budget(k, q));
       if (!ok) kind = kNoRow;
       RowCoef r{};
       auto end_stat = [&](int kind) {  // this lane's scalar of the row's ends
@@ -923,7 +925,14 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
             st_async_f4(&sh.part[i][q], &sh.merged[i], lane,
                         make_float4(st.m, st.l, st.s, 0.0f));
         }
-        warp_wait(&sh.merged[i], (k >> 1) & 1, ok, &sh.gave_up, a.err);
+        // to the end of its own budget, whoever else gave up: a CTA comes to its end only
+        // when what it sent has long landed, in a peer that may wait for it no more
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_bounded(&sh.merged[i], (k >> 1) & 1, kWaitBudget));
+        if (!ok) {
+          *reinterpret_cast<volatile int *>(&sh.gave_up) = 1;
+          atomicCAS(a.err, 0, FR_DEVERR_TIMEOUT);
+        }
         const float4 o = lane < C ? sh.part[i][lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
         if (kind == kRowGrad) st = warp_stat(RowStat{o.x, o.y, o.z}, c);
       }
