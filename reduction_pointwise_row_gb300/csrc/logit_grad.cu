@@ -806,9 +806,9 @@ logit_grad_staged(LogitsBackward a, uint32_t buf_bytes, int nbuf, int lg) {
       const int64_t refill = row_of(k + nbuf);
       const Copy next = copy_of(refill, k + nbuf, wanted(token_of(refill)));
       warp_wait(&sh.done[slot], turn & 1, ok, &sh.gave_up, a.err);
-      if (refill >= 0)
-        issue(*reinterpret_cast<volatile int *>(&sh.gave_up) == 0 ? next : Copy{nullptr, 0, next.b},
-              k + nbuf);
+      // after a timeout nothing: the buffer's barrier may still count row k's copy, and
+      // takes no second arrival until that has landed
+      if (refill >= 0 && *reinterpret_cast<volatile int *>(&sh.gave_up) == 0) issue(next, k + nbuf);
       const RowParams &p = sh.par[slot];
       const RowStat st = sh.stat[slot];
       const unsigned char *pr = logits + row * a.ld * L::ES;
