@@ -36,9 +36,9 @@ struct alignas(32) V8 {
 // kernel may be placed while the one before it still runs (pdl_enter below), so none of
 // them may move before its wait, and what they read may be written until then.  (Against
 // volatile or movable .nc loads: every workload of bench.py, every call over logits and the
-// forms of its sweep within 1 %, single calls of 7-9 us within their spread; but a loop of
-// single loads and stores takes its loads ahead of the stores by itself, as the compiler
-// may not: fp32 softmax out of phase, looped, 608 x 131072 315 us without, 169.9 with.)
+// forms of its sweep within 1 %, single calls of 7-9 us within their spread; but the
+// compiler cannot take them ahead of stores, so a loop of single loads and stores has to:
+// fp32 softmax out of phase, looped, 608 x 131072 315 us without, 169.9 so.)
 
 // 32-byte read-once load: no L1 allocation, first in line for L2 eviction.
 __device__ __forceinline__ V8 ld_stream_v8(const void *p) {
