@@ -74,7 +74,10 @@ typedef enum {
   FR_OP_LOGPROBS_BACKWARD = 6,
   FR_OP_DISTILL = 7,
   FR_OP_DISTILL_BACKWARD = 8,
-  FR_OP_XENT_BACKWARD = 9
+  FR_OP_XENT_BACKWARD = 9,
+  FR_OP_RMSNORM = 10,
+  FR_OP_RMSNORM_QUANT = 11,
+  FR_OP_RMSNORM_BACKWARD = 12
 } fr_op;
 
 /* Most alternatives fr_logprobs returns, and teacher entries fr_distill takes, per row. */
@@ -85,6 +88,14 @@ typedef enum {
   FR_EPI_SUM = 0, /* the sum itself */
   FR_EPI_SQRT = 1 /* its square root (taken in fp64, rounded once to fp32) */
 } fr_epilogue;
+
+/* The scales of an e4m3 output (fr_rmsnorm_quant). */
+typedef enum {
+  FR_SCALE_ROW = 0,   /* one a row, written */
+  FR_SCALE_GROUP = 1, /* one per FR_SCALE_COLS columns of a row, written */
+  FR_SCALE_GIVEN = 2  /* one in all, read */
+} fr_scale;
+#define FR_SCALE_COLS 128
 
 /* Device error codes written by kernels (read by fr_check_device_error). */
 #define FR_DEVERR_NONE 0
@@ -468,6 +479,114 @@ fr_status fr_xent_backward(const void *logits, const int64_t *target, const floa
                            int64_t dloss_stride, float *loss, void *dlogits, int64_t rows,
                            int64_t cols, int64_t ld, int64_t ldd, int64_t ignore_index,
                            fr_dtype dtype, fr_form form, fr_stream_t stream);
+
+/* ---- a residual block's row operators -------------------------------------
+ *
+ * Not on the pages: what a model with pre-normed residual blocks computes per row
+ * around its matrix products.  Shared by the four calls:
+ *
+ *   matrices     of `dtype` (FR_BF16 or FR_F32), [rows, ld] with any ld >= cols and
+ *                any element-aligned address.  Rows of all of a call's matrices that
+ *                start at multiples of 8 elements (16 bytes of bf16, 32 of fp32; an
+ *                e4m3 output 8), with cols a multiple of 8 and gamma and dgamma
+ *                16-byte aligned, take the vector path; others an element an access
+ *                (same results up to the order of a row's sums).  rows <= INT32_MAX,
+ *                cols < 2^31 (more: FR_ERR_UNSUPPORTED_FORM).
+ *   overlap      an output matrix may be the very buffer of an input matrix of its
+ *                type with the same ld, or lie in the gaps of its rows (same ld); any
+ *                other overlap of an output with an input or another output is
+ *                FR_ERR_INVALID_ARG (for vectors: with any byte from a matrix's first
+ *                to its last).  Elements between rows are not written.
+ *   dropout      p in [0, 1]; 0: none, rng and site are not looked at.  Else rng is
+ *                device memory of two int64, {seed, offset}, read by the kernels (a
+ *                captured graph replays with what it holds then), and site, added to
+ *                the offset, tells apart the places of a model that share it.  Element
+ *                (r, c) is dropped where half c % 8 (16 bits, the low half of each
+ *                word first) of the Philox4x32 block of 7 rounds with counter (c / 8,
+ *                r, offset + site low, high) and key (seed low, high) is below t =
+ *                65536 p rounded (ties to even; 1 at least, 65535 at most while p < 1
+ *                rounds to it): the mask depends on nothing else, not on ld, form or
+ *                device, and is never stored; the backward pass draws it again.  What
+ *                stays is multiplied by 65536 / (65536 - t); what is dropped is 0
+ *                whatever it holds; p = 1 drops everything.
+ *   gamma        fp32 [cols], as fr_layernorm's.
+ * Arithmetic is fp32, each output rounded once (nearest even).  NaN and infinities
+ * follow the formulas: a NaN or an infinity in h makes its row's y, and the gradients
+ * of that row and dgamma, NaN (an infinity: zeros where the other elements are
+ * finite).  A row whose squares add up past fp32 (elements of about 1e19) has rstd 0.
+ * Results are the same from run to run.
+ */
+
+/*
+ * y = residual + dropout(x), rounded once; residual NULL: dropout(x).  The gradient
+ * of x is fr_dropout of y's with the same rng, site and p; that of the residual is
+ * y's.  p = 0 copies (or adds).
+ */
+fr_status fr_dropout(const void *x, const void *residual, void *y, int64_t rows, int64_t cols,
+                     int64_t ldx, int64_t ldr, int64_t ldy, float p, const int64_t *rng,
+                     int64_t site, fr_dtype dtype, fr_stream_t stream);
+
+/*
+ *   h = residual + dropout(x)           rounded to dtype; bit for bit fr_dropout's y
+ *   rstd = 1 / sqrt(sum h^2 / cols + eps)
+ *   y = h rstd gamma
+ * With neither a residual nor dropout h is x: pass h NULL.  Otherwise h is required.
+ *
+ *   eps         finite, >= 0 (with 0, a row of zeros gives NaN)
+ *   rstd        fp32 [rows] device output; may be NULL
+ * Forms: persistent (the row in registers, at most 16384 columns; 1 to 32 warps a
+ * row) and looped (a CTA goes over its row twice).  AUTO takes the persistent one as
+ * far as it reaches.
+ */
+fr_status fr_rmsnorm(const void *x, const void *residual, const float *gamma, void *h, void *y,
+                     float *rstd, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr,
+                     int64_t ldh, int64_t ldy, float eps, float p, const int64_t *rng,
+                     int64_t site, fr_dtype dtype, fr_form form, fr_stream_t stream);
+
+/*
+ * fr_rmsnorm with y in 8 bits: y8 = e4m3(v / scale) of v = h rstd gamma in fp32, to
+ * nearest even, saturating at 448 (NaN stays NaN).
+ *
+ *   y           e4m3 bytes [rows, ldy]
+ *   mode        FR_SCALE_ROW: scale = max |v| / 448 over the row, written; FR_SCALE_GROUP:
+ *               over each 128 columns (the last group may be shorter), written;
+ *               FR_SCALE_GIVEN: *scale is read (finite, > 0).  A written scale is
+ *               at least 2^-126, so zeros stay zeros, and NaN where its values hold one.
+ *   scale       fp32 device memory; row r's at [r * scale_row_stride], group g's at
+ *               [r * scale_row_stride + g * scale_col_stride].  One of the two strides
+ *               is 1 and the other at least the groups (rows) it passes; of
+ *               FR_SCALE_ROW scale_row_stride >= 1 alone counts.
+ */
+fr_status fr_rmsnorm_quant(const void *x, const void *residual, const float *gamma, void *h,
+                           void *y, float *scale, fr_scale mode, int64_t scale_row_stride,
+                           int64_t scale_col_stride, float *rstd, int64_t rows, int64_t cols,
+                           int64_t ldx, int64_t ldr, int64_t ldh, int64_t ldy, float eps,
+                           float p, const int64_t *rng, int64_t site, fr_dtype dtype,
+                           fr_form form, fr_stream_t stream);
+
+/*
+ * The gradient of fr_rmsnorm, from dy and, when it is not NULL, dh, the gradient that
+ * reaches h by the residual's path.  With u = dy gamma and n = h rstd:
+ *   dresidual = dh + rstd (u - n sum(u n) / cols)
+ *   dx        = dresidual, or with p > 0 dropout's gradient of it (before its rounding)
+ *   dgamma    = sum over the rows of dy n
+ *
+ *   h, rstd     of the forward pass (h: x where it had neither residual nor dropout)
+ *   dresidual   with p > 0 only; may be NULL
+ *   dgamma      fp32 [cols], may be NULL; the sum over the rows in a fixed order
+ *   workspace   device scratch of fr_workspace_size(FR_OP_RMSNORM_BACKWARD, ...) bytes,
+ *               16-byte aligned (partial sums of dgamma, row sums of the looped form;
+ *               contents on entry ignored).  One call at a time may use it.
+ * Forms: persistent (the row in registers, at most 16384 columns of bf16, 8192 of
+ * fp32) and looped (two passes over the rows; any length).
+ */
+fr_status fr_rmsnorm_backward(const void *dy, const void *h, const float *gamma,
+                              const float *rstd, const void *dh, void *dx, void *dresidual,
+                              float *dgamma, int64_t rows, int64_t cols, int64_t ld_dy,
+                              int64_t ld_h, int64_t ld_dh, int64_t ld_dx, int64_t ld_dresidual,
+                              float p, const int64_t *rng, int64_t site, fr_dtype dtype,
+                              fr_form form, void *workspace, size_t workspace_bytes,
+                              fr_stream_t stream);
 
 /* ---- launch configurations ----------------------------------------------
  *

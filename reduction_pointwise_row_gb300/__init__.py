@@ -17,6 +17,10 @@ Functions carry the C names:
     fr_logprobs_backward(logits, token, dlogprob, dentropy)   -> dlogits
     fr_distill(logits, teacher_index, teacher_logit, ...)     -> loss [rows] fp32
     fr_distill_backward(logits, ..., dloss, ...)              -> dict: dlogits, loss
+    fr_dropout(x, p, rng, site=0, residual=None)              -> y
+    fr_rmsnorm(x, gamma, eps=1e-5, residual=None, ...)        -> dict: y, h, rstd
+    fr_rmsnorm_quant(x, gamma, eps=1e-5, scale="row", ...)    -> dict: y (e4m3), scale, h
+    fr_rmsnorm_backward(dy, h, gamma, rstd, dh=None, ...)     -> dict: dx, dresidual, dgamma
     fr_workspace_size(op, rows, cols, dtype, form)
     fr_check_device_error()
 """
@@ -34,7 +38,8 @@ __all__ = [
     "allreduce_mean_parts", "XENT_PARTS_OFFSET",
     "fr_reduce_relu_add_sum_split_static", "fr_check_device_error", "FORMS", "OPS",
     "EPILOGUES", "FR_TOP_MAX", "fr_logprobs", "fr_logprobs_backward", "fr_distill",
-    "fr_distill_backward", "fr_xent_backward", "fr_coordinate_descent", "fr_xent_get_config", "fr_xent_set_config",
+    "fr_distill_backward", "fr_xent_backward", "fr_dropout", "fr_rmsnorm", "fr_rmsnorm_quant",
+    "fr_rmsnorm_backward", "SCALE_COLS", "fr_coordinate_descent", "fr_xent_get_config", "fr_xent_set_config",
     "fr_xent_tune",
 ]
 
@@ -46,9 +51,11 @@ STATUS = {0: "FR_OK", 1: "FR_ERR_INVALID_ARG", 2: "FR_ERR_UNSUPPORTED_DTYPE",
 FORMS = {"auto": 0, "persistent": 1, "looped": 2, "split": 3}
 FORM_NAMES = {v: k for k, v in FORMS.items()}
 OPS = {"relu_add_sum": 0, "softmax": 1, "layernorm": 2, "xent": 3, "sumsq": 4, "logprobs": 5,
-       "logprobs_backward": 6, "distill": 7, "distill_backward": 8, "xent_backward": 9}
+       "logprobs_backward": 6, "distill": 7, "distill_backward": 8, "xent_backward": 9,
+       "rmsnorm": 10, "rmsnorm_quant": 11, "rmsnorm_backward": 12}
 EPILOGUES = {"sum": 0, "sqrt": 1}
 FR_TOP_MAX = 128  # most alternatives (fr_logprobs) or teacher entries (fr_distill) per row
+SCALE_COLS = 128  # FR_SCALE_COLS: columns of a scale in groups (fr_rmsnorm_quant)
 DTYPES = {"f32": 0, "bf16": 1}
 _DTYPE_NAMES = {v: k for k, v in DTYPES.items()}
 
@@ -84,6 +91,12 @@ SIGNATURES = {
                                    _i64, _i64, _f32, _int, _int, _vp]),
     "fr_xent_backward": (_int, [_vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _int,
                                 _int, _vp]),
+    "fr_dropout": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _f32, _vp, _i64, _int, _vp]),
+    "fr_rmsnorm": (_int, [_vp] * 6 + [_i64] * 6 + [_f32, _f32, _vp, _i64, _int, _int, _vp]),
+    "fr_rmsnorm_quant": (_int, [_vp] * 6 + [_int, _i64, _i64, _vp] + [_i64] * 6 +
+                         [_f32, _f32, _vp, _i64, _int, _int, _vp]),
+    "fr_rmsnorm_backward": (_int, [_vp] * 8 + [_i64] * 7 +
+                            [_f32, _vp, _i64, _int, _int, _vp, _sz, _vp]),
     "fr_check_device_error": (_int, [_vp, ctypes.POINTER(ctypes.c_int32)]),
     "fr_coordinate_descent": (_int, [ctypes.c_int32, _vp, _vp, _vp, ctypes.c_double, _vp, _vp,
                                      _vp, _vp]),
@@ -679,6 +692,234 @@ def fr_xent_backward(logits, target, dloss, ignore_index: int = -100, want_loss:
     _check(lib().fr_xent_backward(logits.data_ptr(), p_target, dloss.data_ptr(), gs, p_loss,
                                   dlogits.data_ptr(), rows, cols, ld, ldd, ignore_index, dt,
                                   FORMS[form], _stream(stream)), "fr_xent_backward")
+    return res
+
+
+# ---- a residual block's row operators: dropout, root-mean-square norm ------------
+
+
+def _like(t, x, name: str) -> int:
+    """The row stride of a matrix that has to have x's shape, dtype and device."""
+    if t.dtype is not x.dtype or t.shape != x.shape:
+        raise ValueError(f"{name} must have the first matrix's shape and dtype")
+    return _logits_arg(t, name)[2]
+
+
+def _rng_ptr(p: float, rng, site: int):
+    """The address of a call's {seed, offset}; None without dropout."""
+    if not 0.0 <= p <= 1.0:
+        raise ValueError("p must be 0 to 1")
+    if not -2**63 <= site < 2**63:
+        raise ValueError("site must fit 64 bits")
+    if p == 0.0:
+        return None
+    if rng is None or not rng.is_cuda or rng.dtype is not _TORCH.int64 or rng.shape != (2,) or \
+            not rng.is_contiguous():
+        raise ValueError("rng must be a contiguous CUDA tensor of two int64: seed and offset")
+    return rng.data_ptr()
+
+
+def _gamma_ptr(gamma, cols: int):
+    if not gamma.is_cuda or gamma.dtype is not _TORCH.float32 or gamma.shape != (cols,) or \
+            not gamma.is_contiguous():
+        raise ValueError("gamma must be a contiguous CUDA tensor of fp32, one per column")
+    return gamma.data_ptr()
+
+
+def _rows_out(t, name: str, rows: int):
+    """The address of an fp32 output with one value per row."""
+    if not t.is_cuda or t.dtype is not _TORCH.float32 or t.shape != (rows,) or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of fp32, one per row")
+    return t.data_ptr()
+
+
+def fr_dropout(x, p: float, rng, site: int = 0, residual=None, out=None, stream=None):
+    """residual + dropout(x) (residual None: dropout(x)) of bf16 or fp32 rows.  The
+    mask is drawn from ``rng``, an int64 CUDA tensor {seed, offset}, ``site`` and the
+    element's row and column, and never stored: the gradient of x is fr_dropout of
+    y's gradient with the same rng, site and p.  ``out`` may be x or residual."""
+    torch = _TORCH or _torch()
+    rows, cols, ld, dt = _logits_arg(x, "x")
+    p_rng = _rng_ptr(p, rng, site)
+    ldr = 0 if residual is None else _like(residual, x, "residual")
+    if out is None:
+        with _on_stream(stream):
+            out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+        ldo = cols
+    else:
+        ldo = _like(out, x, "out")
+    _on_current_device(x, residual, out, rng)
+    _check(lib().fr_dropout(x.data_ptr(), _ptr(residual), out.data_ptr(), rows, cols, ld, ldr, ldo,
+                            p, p_rng, site, dt, _stream(stream)), "fr_dropout")
+    return out
+
+
+def _norm_sum(x, residual, p, h, stream, rows, cols):
+    """(h, ldh, ldr) of the norm's sum: the output `h` is made unless given."""
+    if residual is None and p == 0.0:
+        _need(h is None, "h without a residual or dropout: the norm's input is x itself")
+        return None, 0, 0
+    ldr = 0 if residual is None else _like(residual, x, "residual")
+    if h is None:
+        with _on_stream(stream):
+            return _TORCH.empty((rows, cols), dtype=x.dtype, device=x.device), cols, ldr
+    return h, _like(h, x, "h"), ldr
+
+
+def fr_rmsnorm(x, gamma, eps: float = 1e-5, residual=None, p: float = 0.0, rng=None, site: int = 0,
+               want_rstd: bool = True, form: str = "auto", out=None, h=None, rstd=None, stream=None):
+    """Root-mean-square norm of bf16 or fp32 rows after the residual's addition:
+    h = residual + dropout(x), y = h / sqrt(mean(h^2) + eps) * gamma (fp32).
+
+    Returns a dict: ``y``; ``h`` where there is a residual or dropout (else the
+    norm's input is x); ``rstd`` [rows] fp32 for the backward pass.  ``out`` and
+    ``h`` may be x or residual.  Dropout as in fr_dropout."""
+    torch = _TORCH or _torch()
+    rows, cols, ld, dt = _logits_arg(x, "x")
+    p_gamma = _gamma_ptr(gamma, cols)
+    p_rng = _rng_ptr(p, rng, site)
+    h, ldh, ldr = _norm_sum(x, residual, p, h, stream, rows, cols)
+    res = {}
+    p_rstd = p_h = None
+    with _on_stream(stream):
+        if out is None:
+            out, ldy = torch.empty((rows, cols), dtype=x.dtype, device=x.device), cols
+        else:
+            ldy = _like(out, x, "out")
+        if want_rstd or rstd is not None:
+            if rstd is None:
+                rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+            p_rstd = _rows_out(rstd, "rstd", rows)
+            res["rstd"] = rstd
+    res["y"] = out
+    if h is not None:
+        res["h"] = h
+        p_h = h.data_ptr()
+    _on_current_device(x, gamma, residual, h, out, rstd, rng)
+    _check(lib().fr_rmsnorm(x.data_ptr(), _ptr(residual), p_gamma, p_h, out.data_ptr(), p_rstd,
+                            rows, cols, ld, ldr, ldh, ldy, eps, p, p_rng, site, dt, FORMS[form],
+                            _stream(stream)), "fr_rmsnorm")
+    return res
+
+
+_SCALE_MODES = {"row": 0, "group": 1}
+
+
+def fr_rmsnorm_quant(x, gamma, eps: float = 1e-5, scale="row", residual=None, p: float = 0.0,
+                     rng=None, site: int = 0, want_rstd: bool = False, form: str = "auto", out=None,
+                     scale_out=None, h=None, rstd=None, stream=None):
+    """fr_rmsnorm with y in 8 bits (torch.float8_e4m3fn), y * scale being the norm.
+
+    ``scale``: "row" (one scale a row, max |y| / 448), "group" (one per 128 columns of
+    a row) or a CUDA tensor of one fp32 value, which is used as it is.  Returns a
+    dict: ``y``; ``scale`` ([rows], or [rows, groups], where it is not given); ``h``
+    and ``rstd`` as fr_rmsnorm.  ``scale_out`` takes the scales in a tensor of the
+    caller's, groups in either order ([rows, groups] with one stride of 1)."""
+    torch = _TORCH or _torch()
+    rows, cols, ld, dt = _logits_arg(x, "x")
+    p_gamma = _gamma_ptr(gamma, cols)
+    p_rng = _rng_ptr(p, rng, site)
+    h, ldh, ldr = _norm_sum(x, residual, p, h, stream, rows, cols)
+    res = {}
+    p_rstd = p_h = None
+    sr = sc = 1
+    with _on_stream(stream):
+        if out is None:
+            out = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=x.device)
+            ldy = cols
+        else:
+            if not out.is_cuda or out.dtype is not torch.float8_e4m3fn or out.shape != x.shape or \
+                    (out.stride(1) != 1 and cols != 1):
+                raise ValueError("out must be a CUDA matrix of float8_e4m3fn, x's shape")
+            ldy = cols if rows == 1 else out.stride(0)
+        if isinstance(scale, str):
+            mode = _SCALE_MODES.get(scale)
+            _need(mode is not None, 'scale must be "row", "group" or a tensor of one fp32 value')
+            groups = -(-cols // SCALE_COLS)
+            shape = (rows,) if mode == 0 else (rows, groups)
+            if scale_out is None:
+                scale_out = torch.empty(shape, dtype=torch.float32, device=x.device)
+            elif not scale_out.is_cuda or scale_out.dtype is not torch.float32 or \
+                    scale_out.shape != shape:
+                raise ValueError("scale_out must be a CUDA tensor of fp32, one per row (or group)")
+            sr, sc = scale_out.stride() if mode else (scale_out.stride(0), 1)
+            if rows == 1:  # a dimension of one element has no stride that counts
+                sr = groups if mode and sc == 1 else 1
+            if groups == 1 and mode:
+                sc = 1 if sr != 1 else rows
+            values = res["scale"] = scale_out
+        else:
+            mode, values = 2, scale
+            _need(scale_out is None, "scale_out with a given scale")
+            _need(scale.is_cuda and scale.dtype is torch.float32 and scale.numel() == 1,
+                  "scale must be a CUDA tensor of one fp32 value")
+        if want_rstd or rstd is not None:
+            if rstd is None:
+                rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+            p_rstd = _rows_out(rstd, "rstd", rows)
+            res["rstd"] = rstd
+    res["y"] = out
+    if h is not None:
+        res["h"] = h
+        p_h = h.data_ptr()
+    _on_current_device(x, gamma, residual, h, out, rstd, rng, values)
+    _check(lib().fr_rmsnorm_quant(x.data_ptr(), _ptr(residual), p_gamma, p_h, out.data_ptr(),
+                                  values.data_ptr(), mode, sr, sc, p_rstd, rows, cols, ld, ldr, ldh,
+                                  ldy, eps, p, p_rng, site, dt, FORMS[form], _stream(stream)),
+           "fr_rmsnorm_quant")
+    return res
+
+
+def fr_rmsnorm_backward(dy, h, gamma, rstd, dh=None, p: float = 0.0, rng=None, site: int = 0,
+                        want_dgamma: bool = True, want_dresidual: bool = True, form: str = "auto",
+                        dx=None, dresidual=None, dgamma=None, workspace=None, stream=None):
+    """The gradient of fr_rmsnorm from ``dy`` and, with ``dh``, the gradient that
+    reaches h by the residual's path.  ``h`` and ``rstd`` are the forward pass's (h: x
+    where it had neither residual nor dropout).
+
+    Returns a dict: ``dx``, the gradient of x; ``dgamma`` [cols] fp32; and with
+    dropout (p, rng and site as in the forward pass) ``dresidual``, the gradient of
+    the residual, which without dropout is dx.  ``dx`` and ``dresidual`` may be given,
+    also as dy, h or dh.  ``workspace``: fr_workspace_size("rmsnorm_backward", ...)
+    bytes, by default allocated for the call."""
+    torch = _TORCH or _torch()
+    rows, cols, ld, dt = _logits_arg(dy, "dy")
+    ldh = _like(h, dy, "h")
+    p_gamma = _gamma_ptr(gamma, cols)
+    p_rstd = _rows_out(rstd, "rstd", rows)
+    p_rng = _rng_ptr(p, rng, site)
+    lddh = 0 if dh is None else _like(dh, dy, "dh")
+    _need(workspace is None or (workspace.is_cuda and workspace.is_contiguous()),
+          "workspace must be contiguous CUDA memory")
+    res = {}
+    lddr = 0
+    with _on_stream(stream):
+        if dx is None:
+            dx, lddx = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device), cols
+        else:
+            lddx = _like(dx, dy, "dx")
+        res["dx"] = dx
+        if p_rng is None:
+            _need(dresidual is None, "dresidual without dropout is dx")
+        elif dresidual is not None:
+            lddr = _like(dresidual, dy, "dresidual")
+            res["dresidual"] = dresidual
+        elif want_dresidual:
+            dresidual, lddr = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device), cols
+            res["dresidual"] = dresidual
+        if dgamma is not None:
+            _gamma_ptr(dgamma, cols)
+            res["dgamma"] = dgamma
+        elif want_dgamma:
+            dgamma = res["dgamma"] = torch.empty(cols, dtype=torch.float32, device=dy.device)
+        ws, nws = _workspace("rmsnorm_backward", rows, cols, _DTYPE_NAMES[dt], form, dy.device,
+                             workspace)
+    _on_current_device(dy, h, gamma, rstd, dh, dx, dresidual, dgamma, ws, rng)
+    _check(lib().fr_rmsnorm_backward(dy.data_ptr(), h.data_ptr(), p_gamma, p_rstd, _ptr(dh),
+                                     dx.data_ptr(), _ptr(dresidual), _ptr(dgamma), rows, cols, ld,
+                                     ldh, lddh, lddx, lddr, p, p_rng, site, dt, FORMS[form],
+                                     _ptr(ws), nws, _stream(stream)), "fr_rmsnorm_backward")
     return res
 
 

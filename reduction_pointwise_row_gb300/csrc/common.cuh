@@ -63,6 +63,16 @@ __device__ __forceinline__ uint4 ld_stream_u4(const void *p, uint64_t policy) {
   return v;
 }
 
+// 16-byte read-once load: no L1 allocation.
+__device__ __forceinline__ uint4 ld_once_u4(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // 32-byte load of data that many CTAs re-read (kept in L2 normally).
 __device__ __forceinline__ V8 ld_keep_v8(const void *p) {
   V8 v;
@@ -81,6 +91,22 @@ __device__ __forceinline__ float4 ld_keep_f4(const float *p) {
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "l"(p)
                : "memory");
+  return v;
+}
+
+// 16 bytes that are read again soon.
+__device__ __forceinline__ uint4 ld_keep_u4(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float ld_keep_f32(const float *p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
   return v;
 }
 

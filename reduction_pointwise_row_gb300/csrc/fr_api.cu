@@ -11,6 +11,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <limits>
 #include <mutex>
 #include <vector>
@@ -274,6 +275,16 @@ fr_form pick_backward(int64_t rows, int64_t cols, int es, bool distill, int sm_c
   return cluster == 1 ? FR_FORM_PERSISTENT : FR_FORM_SPLIT;
 }
 
+// ---- a residual block's row operators: the row in registers as far as it fits
+
+fr_form pick_rmsnorm(int64_t cols) {
+  return fr::rmsnorm_held_ok(cols) ? FR_FORM_PERSISTENT : FR_FORM_LOOPED;
+}
+
+fr_form pick_rmsnorm_backward(int64_t cols, bool f32, bool vec) {
+  return fr::rmsnorm_grad_held_ok(cols, f32, vec) ? FR_FORM_PERSISTENT : FR_FORM_LOOPED;
+}
+
 }  // namespace
 
 extern "C" {
@@ -319,6 +330,9 @@ fr_form fr_auto_form(fr_op op, fr_dtype dtype, int64_t rows, int64_t cols, int32
     case FR_OP_XENT_BACKWARD:
       return pick_backward(rows, cols, dtype == FR_F32 ? 4 : 2, op == FR_OP_DISTILL_BACKWARD,
                            sm_count, kSm103SmemOptin);
+    case FR_OP_RMSNORM:
+    case FR_OP_RMSNORM_QUANT: return pick_rmsnorm(cols);
+    case FR_OP_RMSNORM_BACKWARD: return pick_rmsnorm_backward(cols, dtype == FR_F32, cols % 8 == 0);
   }
   return FR_FORM_AUTO;
 }
@@ -343,6 +357,18 @@ size_t fr_workspace_size(fr_op op, int64_t rows, int64_t cols, fr_dtype dtype, f
       if (!shape_ok(rows, cols, cols, es)) return 0;
       const fr_form f = form == FR_FORM_AUTO ? pick_forward(rows, cols, es, true, info.sm_count) : form;
       return f == FR_FORM_LOOPED ? fr::logprobs_workspace(rows, cols, es) : 0;
+    }
+    case FR_OP_RMSNORM_BACKWARD: {
+      const bool f32 = dtype == FR_F32;
+      if ((!f32 && dtype != FR_BF16) || rows > INT32_MAX || cols > INT32_MAX) return 0;
+      // AUTO may take either form, by the rows' alignment
+      const size_t held = fr::rmsnorm_grad_workspace(rows, cols, f32, true, info.sm_count);
+      const size_t looped = fr::rmsnorm_grad_workspace(rows, cols, f32, false, info.sm_count);
+      const bool h = form == FR_FORM_PERSISTENT ||
+                     (form == FR_FORM_AUTO && fr::rmsnorm_grad_held_ok(cols, f32, cols % 8 == 0));
+      const bool l = form == FR_FORM_LOOPED ||
+                     (form == FR_FORM_AUTO && !fr::rmsnorm_grad_held_ok(cols, f32, false));
+      return std::max(h ? held : 0, l ? looped : 0);
     }
     default: return 0;
   }
@@ -922,6 +948,228 @@ fr_status fr_xent_backward(const void *logits, const int64_t *target, const floa
   a.dloss_sign = -1.0f;
   a.temperature = 1.0f;
   return run_backward(a, dtype, false, form, stream);
+}
+
+// ---- a residual block's row operators ----------------------------------------
+
+namespace {
+
+// A call's matrices [rows, cols] and its vectors; p NULL: not given.
+struct Matrix {
+  const void *p;
+  int64_t ld;
+  int es;  // bytes an element
+  bool out;
+};
+struct Vector {
+  const void *p;
+  int64_t bytes;
+  int align;
+  bool out;
+};
+
+bool spans_apart(const void *p, int64_t np, const void *q, int64_t nq) {
+  const uint64_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a + static_cast<uint64_t>(np) <= b || b + static_cast<uint64_t>(nq) <= a;
+}
+
+// Shapes, alignment, limits and overlaps: no output lies over an input (but for the very
+// buffer of a matrix of its type) or another output.
+fr_status block_args_ok(int64_t rows, int64_t cols, const std::initializer_list<Matrix> &ms,
+                        const std::initializer_list<Vector> &vs) {
+  for (const Matrix &m : ms)
+    if (m.p && !shape_ok(rows, cols, m.ld, m.es)) return FR_ERR_INVALID_ARG;
+  for (const Matrix &m : ms)
+    if (m.p && !aligned(m.p, m.es)) return FR_ERR_MISALIGNED;
+  for (const Vector &v : vs)
+    if (v.p && !aligned(v.p, v.align)) return FR_ERR_MISALIGNED;
+  if (rows > INT32_MAX || cols > INT32_MAX) return FR_ERR_UNSUPPORTED_FORM;
+  const auto span = [&](const Matrix &m) { return ((rows - 1) * m.ld + cols) * m.es; };
+  for (const Matrix &o : ms) {
+    if (!o.p) continue;
+    if (o.out)
+      for (const Matrix &m : ms) {
+        if (!m.p || &m == &o) continue;
+        if (m.out && m.p == o.p) return FR_ERR_INVALID_ARG;
+        if (m.es == o.es ? !rows_apart(o.p, m.p, rows, cols, o.ld, m.ld, o.es)
+                         : !spans_apart(o.p, span(o), m.p, span(m)))
+          return FR_ERR_INVALID_ARG;
+      }
+    for (const Vector &v : vs)
+      if (v.p && (o.out || v.out) && !spans_apart(o.p, span(o), v.p, v.bytes))
+        return FR_ERR_INVALID_ARG;
+  }
+  for (const Vector &o : vs)
+    for (const Vector &v : vs)
+      if (o.p && o.out && v.p && &v != &o && !spans_apart(o.p, o.bytes, v.p, v.bytes))
+        return FR_ERR_INVALID_ARG;
+  return FR_OK;
+}
+
+// True when every row starts at a multiple of 8 elements.
+bool rows_of_8(const Matrix &m, int64_t rows) {
+  return m.p == nullptr || (aligned(m.p, 8 * m.es) && (m.ld % 8 == 0 || rows == 1));
+}
+
+fr_status drop_ok(float p, const int64_t *rng, int64_t site, fr::DropSpec *out) {
+  *out = fr::DropSpec{};
+  if (!(p >= 0.0f && p <= 1.0f)) return FR_ERR_INVALID_ARG;
+  if (p == 0.0f) return FR_OK;
+  if (!rng) return FR_ERR_INVALID_ARG;
+  if (!aligned(rng, 8)) return FR_ERR_MISALIGNED;
+  const int64_t t = p == 1.0f ? 65536
+                              : std::min<int64_t>(std::max<int64_t>(std::llrint(65536.0 * p), 1), 65535);
+  out->rng = rng;
+  out->site = site;
+  out->limit = static_cast<uint32_t>((t << 16) - 1);
+  out->factor = t == 65536 ? 0.0f : static_cast<float>(65536.0 / static_cast<double>(65536 - t));
+  return FR_OK;
+}
+
+fr_status run_rmsnorm(fr::NormForward &a, fr_dtype dtype, bool quant, float p, const int64_t *rng,
+                      int64_t site, fr_form form, fr_stream_t stream) {
+  if (dtype != FR_BF16 && dtype != FR_F32) return FR_ERR_UNSUPPORTED_DTYPE;
+  if (!a.x || !a.gamma || !a.y) return FR_ERR_INVALID_ARG;
+  if (!(a.eps >= 0.0f) || !std::isfinite(a.eps)) return FR_ERR_INVALID_ARG;
+  if (fr_status st = drop_ok(p, rng, site, &a.drop)) return st;
+  if ((a.residual != nullptr || a.drop.rng != nullptr) != (a.h != nullptr))
+    return FR_ERR_INVALID_ARG;
+  if (a.rows < 1 || a.cols < 1) return FR_ERR_INVALID_ARG;
+  const int es = dtype == FR_F32 ? 4 : 2;
+  int64_t scales = 0;  // fp32 values from the first scale to the last
+  if (quant) {
+    if (!a.scale) return FR_ERR_INVALID_ARG;
+    const int64_t groups = (a.cols - 1) / FR_SCALE_COLS + 1, lim = INT64_C(1) << 59;
+    switch (a.scale_mode) {
+      case FR_SCALE_GIVEN: scales = 1; break;
+      case FR_SCALE_ROW:
+        if (a.scale_row < 1 || a.scale_row > lim / a.rows) return FR_ERR_INVALID_ARG;
+        scales = (a.rows - 1) * a.scale_row + 1;
+        break;
+      case FR_SCALE_GROUP:
+        if (!(a.scale_col == 1 && a.scale_row >= groups) &&
+            !(a.scale_row == 1 && a.scale_col >= a.rows))
+          return FR_ERR_INVALID_ARG;
+        if (a.scale_row > lim / a.rows || a.scale_col > lim / groups) return FR_ERR_INVALID_ARG;
+        scales = (a.rows - 1) * a.scale_row + (groups - 1) * a.scale_col + 1;
+        break;
+      default: return FR_ERR_INVALID_ARG;
+    }
+  }
+  const Matrix x{a.x, a.ldx, es, false}, res{a.residual, a.ldr, es, false},
+      h{a.h, a.ldh, es, true}, y{a.y, a.ldy, quant ? 1 : es, true};
+  if (a.cols > (INT64_C(1) << 58) || a.rows > (INT64_C(1) << 58)) return FR_ERR_INVALID_ARG;
+  if (fr_status st = block_args_ok(
+          a.rows, a.cols, {x, res, h, y},
+          {{a.gamma, a.cols * 4, 4, false},
+           {a.rstd, a.rows * 4, 4, true},
+           {a.scale, scales * 4, 4, a.scale_mode != FR_SCALE_GIVEN},
+           {a.drop.rng, 16, 8, false}}))
+    return st;
+  if (form < FR_FORM_AUTO || form > FR_FORM_LOOPED) return FR_ERR_UNSUPPORTED_FORM;
+  if (form == FR_FORM_PERSISTENT && !fr::rmsnorm_held_ok(a.cols)) return FR_ERR_UNSUPPORTED_FORM;
+  fr::DevInfo info;
+  if (fr_status st = device_ok(&info)) return st;
+  const fr_form f = form == FR_FORM_AUTO ? pick_rmsnorm(a.cols) : form;
+  const bool vec = a.cols % 8 == 0 && aligned(a.gamma, 16) && rows_of_8(x, a.rows) &&
+                   rows_of_8(res, a.rows) && rows_of_8(h, a.rows) && rows_of_8(y, a.rows);
+  return launched(fr::launch_rmsnorm(a, dtype == FR_F32, vec, quant, f == FR_FORM_PERSISTENT,
+                                     info.sm_count, reinterpret_cast<cudaStream_t>(stream)),
+                  f);
+}
+
+}  // namespace
+
+fr_status fr_dropout(const void *x, const void *residual, void *y, int64_t rows, int64_t cols,
+                     int64_t ldx, int64_t ldr, int64_t ldy, float p, const int64_t *rng,
+                     int64_t site, fr_dtype dtype, fr_stream_t stream) {
+  if (dtype != FR_BF16 && dtype != FR_F32) return FR_ERR_UNSUPPORTED_DTYPE;
+  if (!x || !y) return FR_ERR_INVALID_ARG;
+  fr::NormForward a{};
+  if (fr_status st = drop_ok(p, rng, site, &a.drop)) return st;
+  const int es = dtype == FR_F32 ? 4 : 2;
+  const Matrix mx{x, ldx, es, false}, mr{residual, ldr, es, false}, my{y, ldy, es, true};
+  if (fr_status st = block_args_ok(rows, cols, {mx, mr, my}, {{a.drop.rng, 16, 8, false}}))
+    return st;
+  fr::DevInfo info;
+  if (fr_status st = device_ok(&info)) return st;
+  a.x = x;
+  a.residual = residual;
+  a.h = y;
+  a.rows = rows;
+  a.cols = cols;
+  a.ldx = ldx;
+  a.ldr = ldr;
+  a.ldh = ldy;
+  const bool vec = cols % 8 == 0 && rows_of_8(mx, rows) && rows_of_8(mr, rows) && rows_of_8(my, rows);
+  return fr::launch_dropout(a, dtype == FR_F32, vec, info.sm_count,
+                            reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FR_OK
+             : FR_ERR_CUDA;
+}
+
+fr_status fr_rmsnorm(const void *x, const void *residual, const float *gamma, void *h, void *y,
+                     float *rstd, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr,
+                     int64_t ldh, int64_t ldy, float eps, float p, const int64_t *rng,
+                     int64_t site, fr_dtype dtype, fr_form form, fr_stream_t stream) {
+  fr::NormForward a{x,    residual, gamma, h,   y,   rstd,  rows, cols,    ldx,
+                    ldr,  ldh,      ldy,   eps, {},  0,     nullptr, 0,    0};
+  return run_rmsnorm(a, dtype, false, p, rng, site, form, stream);
+}
+
+fr_status fr_rmsnorm_quant(const void *x, const void *residual, const float *gamma, void *h,
+                           void *y, float *scale, fr_scale mode, int64_t scale_row_stride,
+                           int64_t scale_col_stride, float *rstd, int64_t rows, int64_t cols,
+                           int64_t ldx, int64_t ldr, int64_t ldh, int64_t ldy, float eps,
+                           float p, const int64_t *rng, int64_t site, fr_dtype dtype,
+                           fr_form form, fr_stream_t stream) {
+  fr::NormForward a{x,    residual, gamma, h,   y,  rstd, rows,  cols,             ldx,
+                    ldr,  ldh,      ldy,   eps, {}, mode, scale, scale_row_stride, scale_col_stride};
+  return run_rmsnorm(a, dtype, true, p, rng, site, form, stream);
+}
+
+fr_status fr_rmsnorm_backward(const void *dy, const void *h, const float *gamma,
+                              const float *rstd, const void *dh, void *dx, void *dresidual,
+                              float *dgamma, int64_t rows, int64_t cols, int64_t ld_dy,
+                              int64_t ld_h, int64_t ld_dh, int64_t ld_dx, int64_t ld_dresidual,
+                              float p, const int64_t *rng, int64_t site, fr_dtype dtype,
+                              fr_form form, void *workspace, size_t workspace_bytes,
+                              fr_stream_t stream) {
+  if (dtype != FR_BF16 && dtype != FR_F32) return FR_ERR_UNSUPPORTED_DTYPE;
+  if (!dy || !h || !gamma || !rstd || !dx || rows < 1 || cols < 1) return FR_ERR_INVALID_ARG;
+  fr::NormBackward a{dy,   h,    gamma, rstd, dh,    dx,    dresidual,    dgamma, rows,
+                     cols, ld_dy, ld_h, ld_dh, ld_dx, ld_dresidual, {},    workspace};
+  if (fr_status st = drop_ok(p, rng, site, &a.drop)) return st;
+  if (dresidual && !a.drop.rng) return FR_ERR_INVALID_ARG;
+  const bool f32 = dtype == FR_F32;
+  const int es = f32 ? 4 : 2;
+  const Matrix mdy{dy, ld_dy, es, false}, mh{h, ld_h, es, false}, mdh{dh, ld_dh, es, false},
+      mdx{dx, ld_dx, es, true}, mdr{dresidual, ld_dresidual, es, true};
+  if (cols > (INT64_C(1) << 58) || rows > (INT64_C(1) << 58)) return FR_ERR_INVALID_ARG;
+  if (fr_status st = block_args_ok(rows, cols, {mdy, mh, mdh, mdx, mdr},
+                                   {{gamma, cols * 4, 4, false},
+                                    {rstd, rows * 4, 4, false},
+                                    {dgamma, cols * 4, 4, true},
+                                    {a.drop.rng, 16, 8, false}}))
+    return st;
+  if (form < FR_FORM_AUTO || form > FR_FORM_LOOPED) return FR_ERR_UNSUPPORTED_FORM;
+  const bool vec = cols % 8 == 0 && aligned(gamma, 16) && rows_of_8(mdy, rows) &&
+                   rows_of_8(mh, rows) && rows_of_8(mdh, rows) && rows_of_8(mdx, rows) &&
+                   rows_of_8(mdr, rows);
+  if (form == FR_FORM_PERSISTENT && !fr::rmsnorm_grad_held_ok(cols, f32, vec))
+    return FR_ERR_UNSUPPORTED_FORM;
+  fr::DevInfo info;
+  if (fr_status st = device_ok(&info)) return st;
+  const fr_form f = form == FR_FORM_AUTO ? pick_rmsnorm_backward(cols, f32, vec) : form;
+  const bool held = f == FR_FORM_PERSISTENT;
+  if (!held || dgamma) {
+    const size_t need = fr::rmsnorm_grad_workspace(rows, cols, f32, held, info.sm_count);
+    if (!workspace || workspace_bytes < need) return FR_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned(workspace, 16)) return FR_ERR_MISALIGNED;
+  }
+  return launched(fr::launch_rmsnorm_backward(a, f32, vec, held, info.sm_count,
+                                              reinterpret_cast<cudaStream_t>(stream)),
+                  f);
 }
 
 namespace {

@@ -272,6 +272,54 @@ bool logit_grad_staged_ok(int64_t cols, int es, int cluster, bool distill, int m
 cudaError_t launch_logits_backward(const LogitsBackward &a, bool f32, bool distill, int cluster,
                                    bool vec32, bool vec16, const DevInfo &info, cudaStream_t s);
 
+// ---- a residual block's row operators: dropout, root-mean-square norm ----------
+
+// The dropout of a call; rng NULL: none.
+struct DropSpec {
+  const int64_t *rng;  // device: seed, offset
+  int64_t site;
+  uint32_t limit;  // (t << 16) - 1, t of 65536 dropped
+  float factor;    // of what stays
+};
+
+struct NormForward {
+  const void *x, *residual;  // residual NULL: none
+  const float *gamma;
+  void *h;  // residual + dropout(x), rounded; NULL with neither (the norm is x's)
+  void *y;  // of the matrices' type, or e4m3
+  float *rstd;  // NULL: not wanted
+  int64_t rows, cols, ldx, ldr, ldh, ldy;
+  float eps;
+  DropSpec drop;
+  int32_t scale_mode;  // of an e4m3 y: an fr_scale
+  float *scale;        // written, or read where it is given
+  int64_t scale_row, scale_col;  // its strides
+};
+// True when a row fits the registers of a CTA.
+bool rmsnorm_held_ok(int64_t cols);
+// quant: y in e4m3.  vec: every matrix's rows are aligned to 8 elements (and cols a
+// multiple of 8), gamma to 16 bytes.
+cudaError_t launch_rmsnorm(const NormForward &a, bool f32, bool vec, bool quant, bool held,
+                           int sm_count, cudaStream_t s);
+// y = residual + dropout(x): x, residual, h (as y), rows, cols, lds and drop of `a`.
+cudaError_t launch_dropout(const NormForward &a, bool f32, bool vec, int sm_count, cudaStream_t s);
+
+struct NormBackward {
+  const void *dy, *h;
+  const float *gamma, *rstd;
+  const void *dh;   // gradient that reaches h by the residual's path; NULL: none
+  void *dx, *dres;  // dres NULL: not wanted (without dropout it is dx)
+  float *dgamma;    // NULL: not wanted
+  int64_t rows, cols, ld_dy, ld_h, ld_dh, ld_dx, ld_dres;
+  DropSpec drop;
+  void *workspace;
+};
+// True when a row fits the registers of a CTA (vec: the rows are aligned).
+bool rmsnorm_grad_held_ok(int64_t cols, bool f32, bool vec);
+size_t rmsnorm_grad_workspace(int64_t rows, int64_t cols, bool f32, bool held, int sm_count);
+cudaError_t launch_rmsnorm_backward(const NormBackward &a, bool f32, bool vec, bool held,
+                                    int sm_count, cudaStream_t s);
+
 // Device address of the current device's error word (kernels record
 // FR_DEVERR_* codes there with atomicCAS; the first code wins).
 cudaError_t device_error_word(int **out);

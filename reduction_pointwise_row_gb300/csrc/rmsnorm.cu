@@ -1,0 +1,359 @@
+// Dropout and the root-mean-square norm of rows, with the residual's addition
+// before it and an output of the matrices' type or in 8 bits (e4m3) with scales:
+//   h = residual + dropout(x)            rounded to the type, what the residual's path keeps
+//   rstd = 1 / sqrt(mean(h^2) + eps)     of the rounded h, so that a backward pass that
+//   y = h rstd gamma                     reads h sees the norm that was taken
+// One pass: the row is held in registers from its load to its store, so the bytes
+// are those of the inputs and outputs, and memory bounds every size but the smallest.
+#include "rmsnorm.cuh"
+
+namespace fr {
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr int kGroup = FR_SCALE_COLS;  // columns of a scale in groups
+
+// Two values to e4m3, to nearest even, past the largest to it; lo in the low byte.
+__device__ __forceinline__ uint16_t pack_e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// A lane's 8 values times inv, in 8 bits.
+template <bool VEC>
+__device__ __forceinline__ void store8_e4m3(void *row, int c, int lane, int cols,
+                                            const float (&v)[8], const float (&inv)[2]) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    w[i] = pack_e4m3x2(v[4 * i] * inv[i], v[4 * i + 1] * inv[i]) |
+           static_cast<uint32_t>(pack_e4m3x2(v[4 * i + 2] * inv[i], v[4 * i + 3] * inv[i])) << 16;
+  if constexpr (VEC) {
+    const int col = c * kChunk + lane * 8;
+    if (col < cols)
+      asm volatile("st.global.cs.v2.b32 [%0], {%1, %2};" ::"l"(static_cast<char *>(row) + col),
+                   "r"(w[0]), "r"(w[1])
+                   : "memory");
+  } else {
+    const int first = lane_col<false>(c, lane, 0), left = cols - first;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (32 * j < left)
+        asm volatile("st.global.cs.u8 [%0], %1;" ::"l"(static_cast<char *>(row) + first + 32 * j),
+                     "r"(w[j >> 2] >> (8 * (j & 3)))
+                     : "memory");
+    }
+  }
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+
+// The scale for values whose largest magnitude is `most` (NaN stays): never below
+// the smallest normal, so that its reciprocal is finite and rows of zeros give zeros.
+__device__ __forceinline__ float scale_for(float most) {
+  return max_nan(most / kE4m3Max, 1.17549435e-38f);
+}
+
+// A chunk of y in 8 bits with a scale per 128 columns: two scales a chunk.  Aligned
+// rows: the halves of the warp hold one group each; others: a lane's first and last
+// four elements belong to one each.
+template <bool VEC>
+__device__ __forceinline__ void store_groups(const NormForward &a, int64_t row, void *yrow, int c,
+                                             int lane, const float (&y)[8]) {
+  const int cols = static_cast<int>(a.cols);
+  float m[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    m[i] = max_nan(max_nan(fabsf(y[4 * i]), fabsf(y[4 * i + 1])),
+                   max_nan(fabsf(y[4 * i + 2]), fabsf(y[4 * i + 3])));
+  float inv[2];
+  if constexpr (VEC) {
+    float v = max_nan(m[0], m[1]);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+    const float s = scale_for(v);
+    inv[0] = inv[1] = 1.0f / s;
+    const int g = 2 * c + (lane >> 4);
+    if ((lane & 15) == 0 && g * kGroup < cols) a.scale[row * a.scale_row + g * a.scale_col] = s;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float s = scale_for(warp_max(m[i]));
+      inv[i] = 1.0f / s;
+      const int g = 2 * c + i;
+      if (lane == i && g * kGroup < cols) a.scale[row * a.scale_row + g * a.scale_col] = s;
+    }
+  }
+  store8_e4m3<VEC>(yrow, c, lane, cols, y, inv);
+}
+
+// h of a chunk: residual + dropout(x), rounded and stored; x itself with neither.
+template <bool F32, bool VEC>
+__device__ __forceinline__ void block_sum(const NormForward &a, const Mask &mask, uint32_t row,
+                                          int c, int lane, Lane8<F32> &x, const Lane8<F32> &res) {
+  if (a.h == nullptr) return;
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = x.at(j);
+  if (a.drop.rng != nullptr) drop8<VEC>(v, mask, row, c, lane);
+  if (a.residual != nullptr) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += res.at(j);
+  }
+  x.set(v);
+}
+
+template <bool F32>
+__device__ __forceinline__ const char *row_of(const void *p, int64_t row, int64_t ld) {
+  return static_cast<const char *>(p) + row * ld * (F32 ? 4 : 2);
+}
+template <bool F32>
+__device__ __forceinline__ char *row_of(void *p, int64_t row, int64_t ld) {
+  return static_cast<char *>(p) + row * ld * (F32 ? 4 : 2);
+}
+
+// The sum of squares of each row group of the CTA (and the largest magnitude) over
+// its W warps: every thread gets its row's.  `red` is one pass's own.
+__device__ __forceinline__ void row_reduce(float &ss, float &most, bool with_max, int W,
+                                           float (&red)[2][32]) {
+  ss = warp_sum(ss);
+  if (with_max) most = warp_max(most);
+  if (W == 1) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int first = threadIdx.y * W;  // of this row's warps
+  if (lane == 0) {
+    red[0][first + warp] = ss;
+    if (with_max) red[1][first + warp] = most;
+  }
+  __syncthreads();
+  ss = warp_sum(lane < W ? red[0][first + lane] : 0.0f);
+  if (with_max) most = warp_max(lane < W ? red[1][first + lane] : 0.0f);
+}
+
+// Persistent form: blockDim = (32 W, R), R rows a CTA, W warps a row, NU chunks a warp.
+template <bool F32, bool VEC, int NU, bool QUANT>
+__global__ void __launch_bounds__(NU == 1 ? 1024 : 512) rmsnorm_held(NormForward a) {
+  pdl_enter();
+  __shared__ float red[2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+  const int cols = static_cast<int>(a.cols);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const bool live = row < a.rows;
+  float ss = 0.0f, most = 0.0f;
+  Lane8<F32> h[NU];
+  // gamma waits in registers for the row's statistics, and the residual is all loaded
+  // ahead, where there are enough of them
+  constexpr bool HELD_G = VEC || NU <= 2;
+  float g[HELD_G ? NU : 1][8];
+  if (live) {
+    Lane8<F32> res[HELD_G ? NU : 1];
+    const char *xr = row_of<F32>(a.x, row, a.ldx);
+    const char *rr = row_of<F32>(a.residual, row, a.ldr);
+#pragma unroll
+    for (int i = 0; i < NU; ++i) h[i] = load8<F32, VEC>(xr, i * W + warp, lane, cols);
+    if (HELD_G && a.residual != nullptr) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i) res[i] = load8<F32, VEC>(rr, i * W + warp, lane, cols);
+    }
+    if constexpr (HELD_G) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i) load_cols8<VEC>(g[i], a.gamma, i * W + warp, lane, cols);
+    }
+    Mask mask{};
+    if (a.drop.rng != nullptr) mask = mask_of(a.drop);
+    char *hr = row_of<F32>(a.h, row, a.ldh);
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      if (!HELD_G && a.residual != nullptr)
+        res[0] = load8<F32, VEC>(rr, i * W + warp, lane, cols);
+      block_sum<F32, VEC>(a, mask, static_cast<uint32_t>(row), i * W + warp, lane, h[i],
+                          res[HELD_G ? i : 0]);
+      if (a.h != nullptr) store8<F32, VEC>(hr, i * W + warp, lane, cols, h[i]);
+      if constexpr (QUANT && !HELD_G) load_cols8<VEC>(g[0], a.gamma, i * W + warp, lane, cols);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {  // 0 past the row
+        const float v = h[i].at(j);
+        ss = fmaf(v, v, ss);
+        if (QUANT) most = max_nan(most, fabsf(v * g[HELD_G ? i : 0][j]));
+      }
+    }
+  }
+  row_reduce(ss, most, QUANT && a.scale_mode == FR_SCALE_ROW, W, red);
+  if (!live) return;
+  const float rstd = 1.0f / sqrtf(ss / static_cast<float>(cols) + a.eps);
+  if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
+  float inv[2] = {1.0f, 1.0f};
+  if (QUANT && a.scale_mode != FR_SCALE_GROUP) {
+    const float s = a.scale_mode == FR_SCALE_ROW ? scale_for(most * rstd) : ld_keep_f32(a.scale);
+    if (a.scale_mode == FR_SCALE_ROW && threadIdx.x == 0) a.scale[row * a.scale_row] = s;
+    inv[0] = inv[1] = 1.0f / s;
+  }
+  char *yr = QUANT ? static_cast<char *>(a.y) + row * a.ldy : row_of<F32>(a.y, row, a.ldy);
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const int c = i * W + warp;
+    if (c * kChunk >= cols) continue;
+    float v[8];
+    if constexpr (!HELD_G) load_cols8<VEC>(g[0], a.gamma, c, lane, cols);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = h[i].at(j) * rstd * g[HELD_G ? i : 0][j];
+    if constexpr (QUANT) {
+      if (a.scale_mode == FR_SCALE_GROUP) store_groups<VEC>(a, row, yr, c, lane, v);
+      else store8_e4m3<VEC>(yr, c, lane, cols, v, inv);
+    } else {
+      Lane8<F32> y;
+      y.set(v);
+      store8<F32, VEC>(yr, c, lane, cols, y);
+    }
+  }
+}
+
+// Looped form, rows of any length: a CTA goes over its row twice, the second time
+// over h, which its own threads stored (or x), from L2.
+constexpr int kLoopThreads = 512;
+template <bool F32, bool VEC, bool QUANT>
+__global__ void __launch_bounds__(kLoopThreads) rmsnorm_looped(NormForward a) {
+  pdl_enter();
+  __shared__ float red[2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int W = kLoopThreads / 32;
+  const int cols = static_cast<int>(a.cols);
+  const int chunks = static_cast<int>((a.cols + kChunk - 1) / kChunk);
+  Mask mask{};
+  if (a.drop.rng != nullptr) mask = mask_of(a.drop);
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const char *xr = row_of<F32>(a.x, row, a.ldx);
+    const char *rr = row_of<F32>(a.residual, row, a.ldr);
+    char *hr = row_of<F32>(a.h, row, a.ldh);
+    float ss = 0.0f, most = 0.0f;
+    for (int c = warp; c < chunks; c += W) {
+      Lane8<F32> x = load8<F32, VEC>(xr, c, lane, cols), res{};
+      if (a.residual != nullptr) res = load8<F32, VEC>(rr, c, lane, cols);
+      block_sum<F32, VEC>(a, mask, static_cast<uint32_t>(row), c, lane, x, res);
+      if (a.h != nullptr) store8<F32, VEC>(hr, c, lane, cols, x);
+      float part = 0.0f;  // a short run of its own: long rows add chunk sums, not elements
+#pragma unroll
+      for (int j = 0; j < 8; ++j) part = fmaf(x.at(j), x.at(j), part);
+      ss += part;
+      if (QUANT && a.scale_mode == FR_SCALE_ROW) {
+        float g[8];
+        load_cols8<VEC>(g, a.gamma, c, lane, cols);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) most = max_nan(most, fabsf(x.at(j) * g[j]));
+      }
+    }
+    row_reduce(ss, most, QUANT && a.scale_mode == FR_SCALE_ROW, W, red);
+    const float rstd = 1.0f / sqrtf(ss / static_cast<float>(cols) + a.eps);
+    if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
+    float inv[2] = {1.0f, 1.0f};
+    if (QUANT && a.scale_mode != FR_SCALE_GROUP) {
+      const float s = a.scale_mode == FR_SCALE_ROW ? scale_for(most * rstd) : ld_keep_f32(a.scale);
+      if (a.scale_mode == FR_SCALE_ROW && threadIdx.x == 0) a.scale[row * a.scale_row] = s;
+      inv[0] = inv[1] = 1.0f / s;
+    }
+    const char *again = a.h != nullptr ? hr : xr;
+    char *yr = QUANT ? static_cast<char *>(a.y) + row * a.ldy : row_of<F32>(a.y, row, a.ldy);
+    for (int c = warp; c < chunks; c += W) {
+      const Lane8<F32> x = load8<F32, VEC, true>(again, c, lane, cols);
+      float v[8], g[8];
+      load_cols8<VEC>(g, a.gamma, c, lane, cols);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = x.at(j) * rstd * g[j];
+      if constexpr (QUANT) {
+        if (a.scale_mode == FR_SCALE_GROUP) store_groups<VEC>(a, row, yr, c, lane, v);
+        else store8_e4m3<VEC>(yr, c, lane, cols, v, inv);
+      } else {
+        Lane8<F32> y;
+        y.set(v);
+        store8<F32, VEC>(yr, c, lane, cols, y);
+      }
+    }
+    __syncthreads();  // `red` is free for the next row
+  }
+}
+
+// Dropout alone: a warp takes chunks of rows in turn.
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(256) dropout_chunks(NormForward a, int64_t items, int chunks) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31;
+  const int cols = static_cast<int>(a.cols);
+  Mask mask{};
+  if (a.drop.rng != nullptr) mask = mask_of(a.drop);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items; it += step) {
+    const int64_t row = it / chunks;
+    const int c = static_cast<int>(it - row * chunks);
+    Lane8<F32> x = load8<F32, VEC>(row_of<F32>(a.x, row, a.ldx), c, lane, cols), res{};
+    if (a.residual != nullptr)
+      res = load8<F32, VEC>(row_of<F32>(a.residual, row, a.ldr), c, lane, cols);
+    block_sum<F32, VEC>(a, mask, static_cast<uint32_t>(row), c, lane, x, res);
+    store8<F32, VEC>(row_of<F32>(a.h, row, a.ldh), c, lane, cols, x);
+  }
+}
+
+constexpr int kHeldUnits = 4;   // most chunks a warp holds
+constexpr int kHeldWarps = 32;  // most warps a row has
+
+template <bool F32, bool VEC, bool QUANT>
+cudaError_t launch_held(const NormForward &a, int sm_count, cudaStream_t s) {
+  const int chunks = static_cast<int>((a.cols + kChunk - 1) / kChunk);
+  int units = chunks <= 2 ? 1 : chunks <= 32 ? 2 : 4;
+  if (a.rows < sm_count && chunks <= kHeldWarps) units = 1;  // few rows: latency
+  const int W = (chunks + units - 1) / units;
+  const int R = W >= 8 ? 1 : 8 / W;
+  const dim3 grid(static_cast<unsigned>((a.rows + R - 1) / R)), block(32 * W, R);
+  if (units == 1) return launch_k(rmsnorm_held<F32, VEC, 1, QUANT>, grid, block, 0, s, 0, a);
+  if (units == 2) return launch_k(rmsnorm_held<F32, VEC, 2, QUANT>, grid, block, 0, s, 0, a);
+  return launch_k(rmsnorm_held<F32, VEC, 4, QUANT>, grid, block, 0, s, 0, a);
+}
+
+template <bool F32, bool VEC, bool QUANT>
+cudaError_t launch_looped(const NormForward &a, int sm_count, cudaStream_t s) {
+  const int64_t most = static_cast<int64_t>(sm_count) * 4;
+  return launch_k(rmsnorm_looped<F32, VEC, QUANT>, dim3(static_cast<unsigned>(a.rows < most ? a.rows : most)),
+                  dim3(kLoopThreads), 0, s, 0, a);
+}
+
+template <bool F32, bool VEC>
+cudaError_t launch_norm(const NormForward &a, bool quant, bool held, int sm_count, cudaStream_t s) {
+  if (held)
+    return quant ? launch_held<F32, VEC, true>(a, sm_count, s)
+                 : launch_held<F32, VEC, false>(a, sm_count, s);
+  return quant ? launch_looped<F32, VEC, true>(a, sm_count, s)
+               : launch_looped<F32, VEC, false>(a, sm_count, s);
+}
+
+template <bool F32, bool VEC>
+cudaError_t launch_drop(const NormForward &a, int sm_count, cudaStream_t s) {
+  const int chunks = static_cast<int>((a.cols + kChunk - 1) / kChunk);
+  const int64_t items = a.rows * chunks;
+  const int64_t ctas = (items + 7) / 8, most = static_cast<int64_t>(sm_count) * 64;
+  return launch_k(dropout_chunks<F32, VEC>, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(256),
+                  0, s, 0, a, items, chunks);
+}
+
+}  // namespace
+
+bool rmsnorm_held_ok(int64_t cols) { return cols <= kChunk * kHeldUnits * 16; }
+
+cudaError_t launch_rmsnorm(const NormForward &a, bool f32, bool vec, bool quant, bool held,
+                           int sm_count, cudaStream_t s) {
+  if (f32)
+    return vec ? launch_norm<true, true>(a, quant, held, sm_count, s)
+               : launch_norm<true, false>(a, quant, held, sm_count, s);
+  return vec ? launch_norm<false, true>(a, quant, held, sm_count, s)
+             : launch_norm<false, false>(a, quant, held, sm_count, s);
+}
+
+cudaError_t launch_dropout(const NormForward &a, bool f32, bool vec, int sm_count, cudaStream_t s) {
+  if (f32) return vec ? launch_drop<true, true>(a, sm_count, s) : launch_drop<true, false>(a, sm_count, s);
+  return vec ? launch_drop<false, true>(a, sm_count, s) : launch_drop<false, false>(a, sm_count, s);
+}
+
+}  // namespace fr

@@ -1,0 +1,198 @@
+// Pieces shared by the kernels of a residual block's row operators (dropout, the
+// root-mean-square norm and its gradient): rows read and written in chunks of
+// 256 columns a warp, and the dropout mask.
+#pragma once
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace fr {
+
+// ---- rows in chunks of 256 columns a warp --------------------------------------
+// A lane holds 8 elements of a chunk.  Aligned rows (VEC): the 8 consecutive ones
+// from 8 lane on, one 16-byte (bf16) or 32-byte (fp32) access.  Other rows: columns
+// lane, 32 + lane, ... 224 + lane, an element an access, which needs no alignment and
+// keeps a warp's accesses adjacent.
+constexpr int kChunk = 256;
+
+template <bool F32>
+struct Lane8 {
+  static constexpr int NW = F32 ? 8 : 4;
+  uint32_t w[NW];  // fp32 values, or bf16 pairs (element 2i in the low half of w[i])
+  __device__ __forceinline__ float at(int j) const {
+    if constexpr (F32) return __uint_as_float(w[j]);
+    else return (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+  }
+  // rounds v to the type (nearest even)
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      if constexpr (F32) w[i] = __float_as_uint(v[i]);
+      else w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) w[i] = 0;
+  }
+};
+
+// Column (within the row) of a lane's element j of chunk c.
+template <bool VEC>
+__device__ __forceinline__ int lane_col(int c, int lane, int j) {
+  return c * kChunk + (VEC ? lane * 8 + j : j * 32 + lane);
+}
+
+// A lane's elements of chunk c of the row at `row`; 0 past the row's end.
+// KEEP: the row is read again soon (ordinary caching), else once.
+template <bool F32, bool VEC, bool KEEP = false>
+__device__ __forceinline__ Lane8<F32> load8(const void *row, int c, int lane, int cols) {
+  constexpr int ES = F32 ? 4 : 2;
+  Lane8<F32> v;
+  if constexpr (VEC) {
+    const int col = c * kChunk + lane * 8;
+    const char *p = static_cast<const char *>(row) + static_cast<int64_t>(col) * ES;
+    if (col >= cols) {
+      v.zero();
+    } else if constexpr (F32) {
+      const V8 u = KEEP ? ld_keep_v8(p) : ld_stream_v8(p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v.w[i] = u.w[i];
+    } else {
+      const uint4 u = KEEP ? ld_keep_u4(p) : ld_once_u4(p);
+      v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
+    }
+  } else {
+    const int first = lane_col<false>(c, lane, 0), left = cols - first;
+    const char *p = static_cast<const char *>(row) + static_cast<int64_t>(first) * ES;
+    uint32_t e[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      e[j] = 0;
+      if (32 * j < left) {
+        if constexpr (F32) e[j] = __float_as_uint(ld_stream_f32(reinterpret_cast<const float *>(p + 32 * j * ES)));
+        else e[j] = ld_stream_u16(p + 32 * j * ES);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < Lane8<F32>::NW; ++i) v.w[i] = F32 ? e[i] : (e[2 * i] | (e[2 * i + 1] << 16));
+  }
+  return v;
+}
+
+template <bool F32, bool VEC>
+__device__ __forceinline__ void store8(void *row, int c, int lane, int cols, const Lane8<F32> &v) {
+  constexpr int ES = F32 ? 4 : 2;
+  if constexpr (VEC) {
+    const int col = c * kChunk + lane * 8;
+    if (col >= cols) return;
+    char *p = static_cast<char *>(row) + static_cast<int64_t>(col) * ES;
+    if constexpr (F32) {
+      V8 u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u.w[i] = v.w[i];
+      st_stream_v8(p, u);
+    } else {
+      st_stream_u4(p, make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]));
+    }
+  } else {
+    const int first = lane_col<false>(c, lane, 0), left = cols - first;
+    char *p = static_cast<char *>(row) + static_cast<int64_t>(first) * ES;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (32 * j >= left) continue;
+      if constexpr (F32) st_stream_f32(reinterpret_cast<float *>(p + 32 * j * ES), __uint_as_float(v.w[j]));
+      else st_stream_u16(p + 32 * j * ES, static_cast<uint16_t>((j & 1) ? v.w[j >> 1] >> 16 : v.w[j >> 1]));
+    }
+  }
+}
+
+// A lane's 8 values of a vector over the columns (gamma), 0 past its end.
+template <bool VEC>
+__device__ __forceinline__ void load_cols8(float (&g)[8], const float *p, int c, int lane,
+                                           int cols) {
+  if constexpr (VEC) {
+    const int col = c * kChunk + lane * 8;
+    if (col < cols) {
+      const float4 a = ld_keep_f4(p + col), b = ld_keep_f4(p + col + 4);
+      g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
+      g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = 0.0f;
+    }
+  } else {
+    const int first = lane_col<false>(c, lane, 0), left = cols - first;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] = 32 * j < left ? ld_keep_f32(p + first + 32 * j) : 0.0f;
+  }
+}
+
+// ---- the dropout mask -----------------------------------------------------------
+// Element (r, c) has the 16-bit half c mod 8 of the Philox4x32 block (7 rounds: the
+// fewest that pass every test of BigCrush; Salmon, Moraes, Dror, Shaw, "Parallel
+// random numbers: as easy as 1, 2, 3", SC 2011) of counter (c / 8, r, offset low,
+// offset high) and key seed; it is dropped where that half is below 65536 p.  A lane
+// of an aligned chunk needs one block for its 8 elements.  16 bits and 7 rounds
+// because the rounds' wide products, not memory, bound dropout alone: bf16 [32768,
+// 4096], 86 us; with 32 bits an element 100, with 10 rounds 100, with both 121 (a
+// copy of the same size: 80).
+struct Mask {
+  uint32_t k0, k1, o0, o1;  // key and offset
+  uint32_t limit;           // (t << 16) - 1 for threshold t in 1 .. 65536
+  float factor;             // 65536 / (65536 - t) for the elements that stay
+};
+
+__device__ __forceinline__ Mask mask_of(const DropSpec &d) {
+  int64_t seed, offset;
+  asm volatile("ld.global.b64 %0, [%1];" : "=l"(seed) : "l"(d.rng) : "memory");
+  asm volatile("ld.global.b64 %0, [%1];" : "=l"(offset) : "l"(d.rng + 1) : "memory");
+  const uint64_t s = static_cast<uint64_t>(seed);
+  const uint64_t o = static_cast<uint64_t>(offset) + static_cast<uint64_t>(d.site);
+  return Mask{static_cast<uint32_t>(s), static_cast<uint32_t>(s >> 32), static_cast<uint32_t>(o),
+              static_cast<uint32_t>(o >> 32), d.limit, d.factor};
+}
+
+// The four words of a block.
+__device__ __forceinline__ uint4 philox7(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3,
+                                         uint32_t k0, uint32_t k1) {
+#pragma unroll
+  for (int i = 0; i < 7; ++i) {
+    const uint64_t a = static_cast<uint64_t>(0xD2511F53u) * c0;
+    const uint64_t b = static_cast<uint64_t>(0xCD9E8D57u) * c2;
+    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ (k0 + i * 0x9E3779B9u);
+    c1 = static_cast<uint32_t>(b);
+    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ (k1 + i * 0xBB67AE85u);
+    c3 = static_cast<uint32_t>(a);
+  }
+  return make_uint4(c0, c1, c2, c3);
+}
+
+// v[j] = kept ? v[j] * factor : 0 for a lane's elements of chunk c of a row.  Every
+// lane of the warp takes part.  A dropped element is 0 whatever it holds.
+template <bool VEC>
+__device__ __forceinline__ void drop8(float (&v)[8], const Mask &m, uint32_t row, int c, int lane) {
+  const uint4 b = philox7(static_cast<uint32_t>(c * 32 + lane), row, m.o0, m.o1, m.k0, m.k1);
+  const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // a half above the limit in the upper 16 bits: kept
+      v[2 * i] = (w[i] << 16) > m.limit ? v[2 * i] * m.factor : 0.0f;
+      v[2 * i + 1] = w[i] > m.limit ? v[2 * i + 1] * m.factor : 0.0f;
+    }
+  } else {
+    // element j is column 32 j + lane: half lane % 8 of the block of lane 4 j + lane / 8
+    uint32_t mine = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t h = (e & 1) ? w[e >> 1] : w[e >> 1] << 16;
+      const uint32_t kept = __ballot_sync(0xffffffffu, h > m.limit);
+      if ((lane & 7) == e) mine = kept;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = (mine >> (4 * j + (lane >> 3))) & 1u ? v[j] * m.factor : 0.0f;
+  }
+}
+
+}  // namespace fr
