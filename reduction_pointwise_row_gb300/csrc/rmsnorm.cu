@@ -5,6 +5,8 @@
 //   y = h rstd gamma                     reads h sees the norm that was taken
 // One pass: the row is held in registers from its load to its store, so the bytes
 // are those of the inputs and outputs, and memory bounds every size but the smallest.
+#include <algorithm>
+
 #include "rmsnorm.cuh"
 
 namespace fr {
@@ -37,13 +39,14 @@ __device__ __forceinline__ void store8_e4m3(void *row, int c, int lane, int cols
                    : "memory");
   } else {
     const int first = lane_col<false>(c, lane, 0), left = cols - first;
+    char *p = static_cast<char *>(row) + first;
+    const auto st = [&](int j) {
+      asm volatile("st.global.cs.u8 [%0], %1;" ::"l"(p + 32 * j), "r"(w[j >> 2] >> (8 * (j & 3)))
+                   : "memory");
+    };
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (32 * j < left)
-        asm volatile("st.global.cs.u8 [%0], %1;" ::"l"(static_cast<char *>(row) + first + 32 * j),
-                     "r"(w[j >> 2] >> (8 * (j & 3)))
-                     : "memory");
-    }
+    for (int j = 0; j < 8; ++j)
+      if (32 * j < left) st(j);
   }
 }
 
@@ -92,11 +95,10 @@ __device__ __forceinline__ void store_groups(const NormForward &a, int64_t row, 
   store8_e4m3<VEC>(yrow, c, lane, cols, y, inv);
 }
 
-// h of a chunk: residual + dropout(x), rounded and stored; x itself with neither.
+// h of a chunk: residual + dropout(x), rounded; x becomes it.
 template <bool F32, bool VEC>
 __device__ __forceinline__ void block_sum(const NormForward &a, const Mask &mask, uint32_t row,
                                           int c, int lane, Lane8<F32> &x, const Lane8<F32> &res) {
-  if (a.h == nullptr) return;
   float v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = x.at(j);
@@ -117,8 +119,8 @@ __device__ __forceinline__ char *row_of(void *p, int64_t row, int64_t ld) {
   return static_cast<char *>(p) + row * ld * (F32 ? 4 : 2);
 }
 
-// The sum of squares of each row group of the CTA (and the largest magnitude) over
-// its W warps: every thread gets its row's.  `red` is one pass's own.
+// The sum of a row's squares (and its largest magnitude) over the W warps that hold
+// it: every thread gets them.  `red` is one pass's own.
 __device__ __forceinline__ void row_reduce(float &ss, float &most, bool with_max, int W,
                                            float (&red)[2][32]) {
   ss = warp_sum(ss);
@@ -135,62 +137,63 @@ __device__ __forceinline__ void row_reduce(float &ss, float &most, bool with_max
   if (with_max) most = warp_max(lane < W ? red[1][first + lane] : 0.0f);
 }
 
+// Threads of a CTA that holds NU chunks a warp, at most; an SM holds 1024 of them.
+template <int NU>
+constexpr int kHeldThreads = NU <= 2 ? 1024 : NU <= 4 ? 512 : 256;
+
 // Persistent form: blockDim = (32 W, R), R rows a CTA, W warps a row, NU chunks a warp.
-template <bool F32, bool VEC, int NU, bool QUANT>
-__global__ void __launch_bounds__(NU == 1 ? 1024 : 512) rmsnorm_held(NormForward a) {
+template <bool F32, bool VEC, int NU, bool SUM, bool QUANT>
+__global__ void __launch_bounds__(kHeldThreads<NU>, 1024 / kHeldThreads<NU>)
+rmsnorm_held(NormForward a) {
   pdl_enter();
   __shared__ float red[2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
   const int cols = static_cast<int>(a.cols);
   const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const bool live = row < a.rows;
+  const bool with_max = QUANT && a.scale_mode == FR_SCALE_ROW;
   float ss = 0.0f, most = 0.0f;
   Lane8<F32> h[NU];
-  // gamma waits in registers for the row's statistics, and the residual is all loaded
-  // ahead, where there are enough of them
-  constexpr bool HELD_G = VEC || NU <= 2;
-  float g[HELD_G ? NU : 1][8];
   if (live) {
-    Lane8<F32> res[HELD_G ? NU : 1];
     const char *xr = row_of<F32>(a.x, row, a.ldx);
-    const char *rr = row_of<F32>(a.residual, row, a.ldr);
 #pragma unroll
     for (int i = 0; i < NU; ++i) h[i] = load8<F32, VEC>(xr, i * W + warp, lane, cols);
-    if (HELD_G && a.residual != nullptr) {
+    if constexpr (SUM) {
+      Lane8<F32> res[NU];
+      const char *rr = row_of<F32>(a.residual, row, a.ldr);
+      if (a.residual != nullptr) {
 #pragma unroll
-      for (int i = 0; i < NU; ++i) res[i] = load8<F32, VEC>(rr, i * W + warp, lane, cols);
-    }
-    if constexpr (HELD_G) {
+        for (int i = 0; i < NU; ++i) res[i] = load8<F32, VEC>(rr, i * W + warp, lane, cols);
+      }
+      Mask mask{};
+      if (a.drop.rng != nullptr) mask = mask_of(a.drop);
+      char *hr = row_of<F32>(a.h, row, a.ldh);
 #pragma unroll
-      for (int i = 0; i < NU; ++i) load_cols8<VEC>(g[i], a.gamma, i * W + warp, lane, cols);
+      for (int i = 0; i < NU; ++i) {
+        block_sum<F32, VEC>(a, mask, static_cast<uint32_t>(row), i * W + warp, lane, h[i], res[i]);
+        store8<F32, VEC>(hr, i * W + warp, lane, cols, h[i]);
+      }
     }
-    Mask mask{};
-    if (a.drop.rng != nullptr) mask = mask_of(a.drop);
-    char *hr = row_of<F32>(a.h, row, a.ldh);
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      if (!HELD_G && a.residual != nullptr)
-        res[0] = load8<F32, VEC>(rr, i * W + warp, lane, cols);
-      block_sum<F32, VEC>(a, mask, static_cast<uint32_t>(row), i * W + warp, lane, h[i],
-                          res[HELD_G ? i : 0]);
-      if (a.h != nullptr) store8<F32, VEC>(hr, i * W + warp, lane, cols, h[i]);
-      if constexpr (QUANT && !HELD_G) load_cols8<VEC>(g[0], a.gamma, i * W + warp, lane, cols);
+      float g[8];
+      if (with_max) load_cols8<VEC>(g, a.gamma, i * W + warp, lane, cols);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {  // 0 past the row
         const float v = h[i].at(j);
         ss = fmaf(v, v, ss);
-        if (QUANT) most = max_nan(most, fabsf(v * g[HELD_G ? i : 0][j]));
+        if (with_max) most = max_nan(most, fabsf(v * g[j]));
       }
     }
   }
-  row_reduce(ss, most, QUANT && a.scale_mode == FR_SCALE_ROW, W, red);
+  row_reduce(ss, most, with_max, W, red);
   if (!live) return;
   const float rstd = 1.0f / sqrtf(ss / static_cast<float>(cols) + a.eps);
   if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
   float inv[2] = {1.0f, 1.0f};
   if (QUANT && a.scale_mode != FR_SCALE_GROUP) {
-    const float s = a.scale_mode == FR_SCALE_ROW ? scale_for(most * rstd) : ld_keep_f32(a.scale);
-    if (a.scale_mode == FR_SCALE_ROW && threadIdx.x == 0) a.scale[row * a.scale_row] = s;
+    const float s = with_max ? scale_for(most * rstd) : ld_keep_f32(a.scale);
+    if (with_max && threadIdx.x == 0) a.scale[row * a.scale_row] = s;
     inv[0] = inv[1] = 1.0f / s;
   }
   char *yr = QUANT ? static_cast<char *>(a.y) + row * a.ldy : row_of<F32>(a.y, row, a.ldy);
@@ -198,10 +201,10 @@ __global__ void __launch_bounds__(NU == 1 ? 1024 : 512) rmsnorm_held(NormForward
   for (int i = 0; i < NU; ++i) {
     const int c = i * W + warp;
     if (c * kChunk >= cols) continue;
-    float v[8];
-    if constexpr (!HELD_G) load_cols8<VEC>(g[0], a.gamma, c, lane, cols);
+    float v[8], g[8];
+    load_cols8<VEC>(g, a.gamma, c, lane, cols);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = h[i].at(j) * rstd * g[HELD_G ? i : 0][j];
+    for (int j = 0; j < 8; ++j) v[j] = h[i].at(j) * rstd * g[j];
     if constexpr (QUANT) {
       if (a.scale_mode == FR_SCALE_GROUP) store_groups<VEC>(a, row, yr, c, lane, v);
       else store8_e4m3<VEC>(yr, c, lane, cols, v, inv);
@@ -234,8 +237,10 @@ __global__ void __launch_bounds__(kLoopThreads) rmsnorm_looped(NormForward a) {
     for (int c = warp; c < chunks; c += W) {
       Lane8<F32> x = load8<F32, VEC>(xr, c, lane, cols), res{};
       if (a.residual != nullptr) res = load8<F32, VEC>(rr, c, lane, cols);
-      block_sum<F32, VEC>(a, mask, static_cast<uint32_t>(row), c, lane, x, res);
-      if (a.h != nullptr) store8<F32, VEC>(hr, c, lane, cols, x);
+      if (a.h != nullptr) {
+        block_sum<F32, VEC>(a, mask, static_cast<uint32_t>(row), c, lane, x, res);
+        store8<F32, VEC>(hr, c, lane, cols, x);
+      }
       float part = 0.0f;  // a short run of its own: long rows add chunk sums, not elements
 #pragma unroll
       for (int j = 0; j < 8; ++j) part = fmaf(x.at(j), x.at(j), part);
@@ -277,40 +282,152 @@ __global__ void __launch_bounds__(kLoopThreads) rmsnorm_looped(NormForward a) {
   }
 }
 
-// Dropout alone: a warp takes chunks of rows in turn.
-template <bool F32, bool VEC>
-__global__ void __launch_bounds__(256) dropout_chunks(NormForward a, int64_t items, int chunks) {
+// Rows of at most a chunk, aligned: 1 << lg lanes hold a row, a warp U times 32 >> lg
+// rows at a time, with one reading of gamma; no barrier.
+template <bool F32, int U, bool SUM, bool QUANT>
+__global__ void __launch_bounds__(256) rmsnorm_short(NormForward a, int lg) {
   pdl_enter();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, at = lane & ((1 << lg) - 1), sub = lane >> lg, per = 32 >> lg;
   const int cols = static_cast<int>(a.cols);
-  Mask mask{};
-  if (a.drop.rng != nullptr) mask = mask_of(a.drop);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items; it += step) {
-    const int64_t row = it / chunks;
-    const int c = static_cast<int>(it - row * chunks);
-    Lane8<F32> x = load8<F32, VEC>(row_of<F32>(a.x, row, a.ldx), c, lane, cols), res{};
-    if (a.residual != nullptr)
-      res = load8<F32, VEC>(row_of<F32>(a.residual, row, a.ldr), c, lane, cols);
-    block_sum<F32, VEC>(a, mask, static_cast<uint32_t>(row), c, lane, x, res);
-    store8<F32, VEC>(row_of<F32>(a.h, row, a.ldh), c, lane, cols, x);
+  const int64_t first =
+      (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * (U * per) + sub;
+  Lane8<F32> h[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t row = first + u * per;
+    if (row < a.rows) h[u] = load8<F32, true>(row_of<F32>(a.x, row, a.ldx), 0, at, cols);
+    else h[u].zero();
+  }
+  if constexpr (SUM) {
+    Lane8<F32> res[U];
+    if (a.residual != nullptr) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t row = first + u * per;
+        if (row < a.rows) res[u] = load8<F32, true>(row_of<F32>(a.residual, row, a.ldr), 0, at, cols);
+      }
+    }
+    Mask mask{};
+    if (a.drop.rng != nullptr) mask = mask_of(a.drop);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = first + u * per;
+      if (row >= a.rows) continue;
+      block_sum<F32, true>(a, mask, static_cast<uint32_t>(row), 0, at, h[u], res[u]);
+      store8<F32, true>(row_of<F32>(a.h, row, a.ldh), 0, at, cols, h[u]);
+    }
+  }
+  float g[8];
+  load_cols8<true>(g, a.gamma, 0, at, cols);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t row = first + u * per;
+    const bool live = row < a.rows;
+    float v[8], ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(h[u].at(j), h[u].at(j), ss);
+    for (int o = 1 << lg >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float rstd = 1.0f / sqrtf(ss / static_cast<float>(cols) + a.eps);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = h[u].at(j) * rstd * g[j];
+    if (live && a.rstd != nullptr && at == 0) a.rstd[row] = rstd;
+    if constexpr (QUANT) {
+      char *yr = static_cast<char *>(a.y) + row * a.ldy;
+      float s;
+      if (a.scale_mode == FR_SCALE_GIVEN) {
+        s = ld_keep_f32(a.scale);
+      } else {  // groups of 128 columns are 16 lanes
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[j]));
+        const bool row_scale = a.scale_mode == FR_SCALE_ROW;
+        const int lanes = !row_scale && lg > 4 ? 16 : 1 << lg;
+        for (int o = lanes >> 1; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        s = scale_for(m);
+        const int group = row_scale ? 0 : at >> 4;
+        if (live && (at & (lanes - 1)) == 0 && group * kGroup < cols)
+          a.scale[row * a.scale_row + (row_scale ? 0 : group * a.scale_col)] = s;
+      }
+      const float inv[2] = {1.0f / s, 1.0f / s};
+      if (live) store8_e4m3<true>(yr, 0, at, cols, v, inv);
+    } else if (live) {
+      Lane8<F32> y;
+      y.set(v);
+      store8<F32, true>(row_of<F32>(a.y, row, a.ldy), 0, at, cols, y);
+    }
   }
 }
 
-constexpr int kHeldUnits = 4;   // most chunks a warp holds
-constexpr int kHeldWarps = 32;  // most warps a row has
+// Dropout alone.  A CTA's 8 warps take a run of 8 NU chunks of a row, or R = 8 / W short
+// rows of W warps; 1 << lg lanes hold a row of at most a chunk (32 of longer ones).
+template <bool F32, bool VEC, int NU>
+__global__ void __launch_bounds__(256) dropout_chunks(NormForward a, unsigned runs, int lg) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31, at = lane & ((1 << lg) - 1), W = blockDim.x >> 5;
+  const int cols = static_cast<int>(a.cols);
+  const unsigned group = blockIdx.x / runs, run = blockIdx.x - group * runs;
+  const int first = static_cast<int>(run) * (W * NU) + (threadIdx.x >> 5);
+  const int64_t row = ((static_cast<int64_t>(group) * blockDim.y + threadIdx.y) << (5 - lg)) + (lane >> lg);
+  const bool live = row < a.rows;
+  const int chunks = live ? (cols - 1) / kChunk + 1 : 0;
+  Lane8<F32> x[NU], res[NU];
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const int c = first + i * W;
+    if (c >= chunks) break;
+    x[i] = load8<F32, VEC>(row_of<F32>(a.x, row, a.ldx), c, at, cols);
+    if (a.residual != nullptr) res[i] = load8<F32, VEC>(row_of<F32>(a.residual, row, a.ldr), c, at, cols);
+  }
+  Mask mask{};
+  if (a.drop.rng != nullptr) mask = mask_of(a.drop);
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const int c = first + i * W;
+    if (c >= chunks) break;
+    block_sum<F32, VEC>(a, mask, static_cast<uint32_t>(row), c, at, x[i], res[i]);
+    store8<F32, VEC>(row_of<F32>(a.h, row, a.ldh), c, at, cols, x[i]);
+  }
+}
 
-template <bool F32, bool VEC, bool QUANT>
+constexpr int kHeldChunks = 64;  // of a row, at most: 32 warps with 2 each
+
+template <bool F32, bool SUM, bool QUANT>
+cudaError_t launch_short(const NormForward &a, cudaStream_t s) {
+  int lg = 5;
+  while (lg > 0 && (8 << lg >> 1) >= a.cols) --lg;
+  // two rows a lane: loads in flight (us with 1, 2, 4, 8: bf16 [524288, 128] 57.6, 47.2,
+  // 48.8, 51.6; 64 columns and a residual 43.4, 40.4, 41.3, 49.2; e4m3 out 72.4, 66.4,
+  // 63.8, 70.3; fp32 64 columns 40.1, 40.5, 40.9, 43.5)
+  constexpr int U = 2;
+  const int64_t per = 8 * U * static_cast<int64_t>(32 >> lg);
+  return launch_k(rmsnorm_short<F32, U, SUM, QUANT>, dim3(static_cast<unsigned>((a.rows + per - 1) / per)),
+                  dim3(256), 0, s, 0, a, lg);
+}
+
+// How many chunks a warp holds: few warps a row make the row's reduction cheap and the
+// loads in flight of each many, as long as 64 registers suffice (1024 threads an SM).
+// Measured (us with 1, 2, 3, 4, 6, 8): bf16 with residual, [16384, 4096] with dropout 90,
+// 84.8, -, 78.7, 80, -; [32768, 768] without, 3 chunks, -, 27, 14.7, 15.4, 16.2, -; [8192,
+// 16384] without -, 146, 143, 94.7, -, 80.1; fp32 [8192, 4096] with 83, 78.6, 79.1, -, -, -.
+template <bool F32, bool VEC, bool QUANT, bool SUM>
 cudaError_t launch_held(const NormForward &a, int sm_count, cudaStream_t s) {
   const int chunks = static_cast<int>((a.cols + kChunk - 1) / kChunk);
-  int units = chunks <= 2 ? 1 : chunks <= 32 ? 2 : 4;
-  if (a.rows < sm_count && chunks <= kHeldWarps) units = 1;  // few rows: latency
-  const int W = (chunks + units - 1) / units;
-  const int R = W >= 8 ? 1 : 8 / W;
+  int units = F32 ? 2 : !VEC ? 3 : SUM || chunks <= 32 ? 4 : 8;
+  if (units == 3 && chunks > 3 * kHeldThreads<3> / 32) units = 2;
+  if (chunks < units) units = chunks;
+  if (a.rows < sm_count && chunks <= 32) units = 1;  // few rows: latency
+  const int W = (chunks + units - 1) / units, R = W >= 4 ? 1 : 4 / W;
   const dim3 grid(static_cast<unsigned>((a.rows + R - 1) / R)), block(32 * W, R);
-  if (units == 1) return launch_k(rmsnorm_held<F32, VEC, 1, QUANT>, grid, block, 0, s, 0, a);
-  if (units == 2) return launch_k(rmsnorm_held<F32, VEC, 2, QUANT>, grid, block, 0, s, 0, a);
-  return launch_k(rmsnorm_held<F32, VEC, 4, QUANT>, grid, block, 0, s, 0, a);
+  if (units == 1) return launch_k(rmsnorm_held<F32, VEC, 1, SUM, QUANT>, grid, block, 0, s, 0, a);
+  if constexpr (!F32) {
+    if (units == 3) return launch_k(rmsnorm_held<F32, VEC, 3, SUM, QUANT>, grid, block, 0, s, 0, a);
+    if constexpr (VEC) {
+      if (units == 4) return launch_k(rmsnorm_held<F32, VEC, 4, SUM, QUANT>, grid, block, 0, s, 0, a);
+      if constexpr (!SUM)
+        if (units == 8) return launch_k(rmsnorm_held<F32, VEC, 8, SUM, QUANT>, grid, block, 0, s, 0, a);
+    }
+  }
+  return launch_k(rmsnorm_held<F32, VEC, 2, SUM, QUANT>, grid, block, 0, s, 0, a);
 }
 
 template <bool F32, bool VEC, bool QUANT>
@@ -320,27 +437,44 @@ cudaError_t launch_looped(const NormForward &a, int sm_count, cudaStream_t s) {
                   dim3(kLoopThreads), 0, s, 0, a);
 }
 
+template <bool F32, bool VEC, bool QUANT>
+cudaError_t launch_form(const NormForward &a, bool held, int sm_count, cudaStream_t s) {
+  if (!held) return launch_looped<F32, VEC, QUANT>(a, sm_count, s);
+  const bool sum = a.h != nullptr;
+  if constexpr (VEC)
+    if (a.cols <= kChunk)
+      return sum ? launch_short<F32, true, QUANT>(a, s) : launch_short<F32, false, QUANT>(a, s);
+  return sum ? launch_held<F32, VEC, QUANT, true>(a, sm_count, s)
+             : launch_held<F32, VEC, QUANT, false>(a, sm_count, s);
+}
+
 template <bool F32, bool VEC>
 cudaError_t launch_norm(const NormForward &a, bool quant, bool held, int sm_count, cudaStream_t s) {
-  if (held)
-    return quant ? launch_held<F32, VEC, true>(a, sm_count, s)
-                 : launch_held<F32, VEC, false>(a, sm_count, s);
-  return quant ? launch_looped<F32, VEC, true>(a, sm_count, s)
-               : launch_looped<F32, VEC, false>(a, sm_count, s);
+  return quant ? launch_form<F32, VEC, true>(a, held, sm_count, s)
+               : launch_form<F32, VEC, false>(a, held, sm_count, s);
 }
 
 template <bool F32, bool VEC>
 cudaError_t launch_drop(const NormForward &a, int sm_count, cudaStream_t s) {
-  const int chunks = static_cast<int>((a.cols + kChunk - 1) / kChunk);
-  const int64_t items = a.rows * chunks;
-  const int64_t ctas = (items + 7) / 8, most = static_cast<int64_t>(sm_count) * 64;
-  return launch_k(dropout_chunks<F32, VEC>, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(256),
-                  0, s, 0, a, items, chunks);
+  const int64_t chunks = (a.cols + kChunk - 1) / kChunk;
+  // several chunks a warp: their loads are in flight together (us with 1, 2, 4: bf16
+  // [16384, 4096] 57.0, 49.8, 47.0); few in all: a warp each
+  const int units = !F32 && a.rows * chunks >= 64 * static_cast<int64_t>(sm_count) ? 4 : 1;
+  int lg = 5;
+  if (VEC)
+    while (lg > 0 && (8 << lg >> 1) >= a.cols) --lg;
+  const int W = static_cast<int>(std::min<int64_t>(8, (chunks + units - 1) / units)), R = 8 / W;
+  const int64_t runs = (chunks + W * units - 1) / (W * units), per = static_cast<int64_t>(R) << (5 - lg);
+  const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per * runs)), block(32 * W, R);
+  if constexpr (!F32)
+    if (units == 4)
+      return launch_k(dropout_chunks<F32, VEC, 4>, grid, block, 0, s, 0, a, static_cast<unsigned>(runs), lg);
+  return launch_k(dropout_chunks<F32, VEC, 1>, grid, block, 0, s, 0, a, static_cast<unsigned>(runs), lg);
 }
 
 }  // namespace
 
-bool rmsnorm_held_ok(int64_t cols) { return cols <= kChunk * kHeldUnits * 16; }
+bool rmsnorm_held_ok(int64_t cols) { return cols <= kChunk * kHeldChunks; }
 
 cudaError_t launch_rmsnorm(const NormForward &a, bool f32, bool vec, bool quant, bool held,
                            int sm_count, cudaStream_t s) {

@@ -65,15 +65,13 @@ __device__ __forceinline__ Lane8<F32> load8(const void *row, int c, int lane, in
   } else {
     const int first = lane_col<false>(c, lane, 0), left = cols - first;
     const char *p = static_cast<const char *>(row) + static_cast<int64_t>(first) * ES;
+    const auto ld = [&](int j) -> uint32_t {
+      if constexpr (F32) return __float_as_uint(ld_stream_f32(reinterpret_cast<const float *>(p + 32 * j * ES)));
+      else return ld_stream_u16(p + 32 * j * ES);
+    };
     uint32_t e[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      e[j] = 0;
-      if (32 * j < left) {
-        if constexpr (F32) e[j] = __float_as_uint(ld_stream_f32(reinterpret_cast<const float *>(p + 32 * j * ES)));
-        else e[j] = ld_stream_u16(p + 32 * j * ES);
-      }
-    }
+    for (int j = 0; j < 8; ++j) e[j] = 32 * j < left ? ld(j) : 0;
 #pragma unroll
     for (int i = 0; i < Lane8<F32>::NW; ++i) v.w[i] = F32 ? e[i] : (e[2 * i] | (e[2 * i + 1] << 16));
   }
@@ -98,12 +96,13 @@ __device__ __forceinline__ void store8(void *row, int c, int lane, int cols, con
   } else {
     const int first = lane_col<false>(c, lane, 0), left = cols - first;
     char *p = static_cast<char *>(row) + static_cast<int64_t>(first) * ES;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (32 * j >= left) continue;
+    const auto st = [&](int j) {
       if constexpr (F32) st_stream_f32(reinterpret_cast<float *>(p + 32 * j * ES), __uint_as_float(v.w[j]));
       else st_stream_u16(p + 32 * j * ES, static_cast<uint16_t>((j & 1) ? v.w[j >> 1] >> 16 : v.w[j >> 1]));
-    }
+    };
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (32 * j < left) st(j);
   }
 }
 
