@@ -178,6 +178,11 @@ __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
   return d;
 }
+__device__ __forceinline__ uint64_t pack_u32x2(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
 __device__ __forceinline__ float f32x2_lo(uint64_t v) {
   float lo, hi;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
@@ -360,6 +365,15 @@ __device__ __forceinline__ void cp_async_16(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src)
                : "memory");
 }
+// To a shared-memory address.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The first `bytes` (0 .. 16) of them; the rest is filled with zeros.
+__device__ __forceinline__ void cp_async_16_part(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
 // The same with an L2 policy (createpolicy) as the hint.
 __device__ __forceinline__ void cp_async_16_hint(void *dst, const void *src, uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)),
@@ -385,6 +399,11 @@ __device__ __forceinline__ V8 lds_v8(const void *p) {
                : "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
                : "r"(a + 16));
   return v;
+}
+
+// A barrier (of 1 .. 15) of `threads` threads, whole warps.
+__device__ __forceinline__ void group_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // ---- thread-block clusters ------------------------------------------------
@@ -458,13 +477,14 @@ __device__ __forceinline__ void st_cluster_f2(void *local, uint32_t rank, float 
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(a), "f"(b) : "memory");
 }
 
-__device__ __forceinline__ uint4 lds_u4(const void *p) {
+__device__ __forceinline__ uint4 lds_u4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(smem_addr(p)));
+               : "r"(addr));
   return v;
 }
+__device__ __forceinline__ uint4 lds_u4(const void *p) { return lds_u4(smem_addr(p)); }
 
 // ---- row geometry --------------------------------------------------------
 

@@ -1011,6 +1011,18 @@ bool rows_of_8(const Matrix &m, int64_t rows) {
   return m.p == nullptr || (aligned(m.p, 8 * m.es) && (m.ld % 8 == 0 || rows == 1));
 }
 
+// True when the matrices start at multiples of 8 elements and any row of them starts at
+// the same place modulo 8.
+bool rows_in_phase(const std::initializer_list<Matrix> &ms, int64_t rows) {
+  int64_t ld = -1;
+  for (const Matrix &m : ms) {
+    if (!m.p) continue;
+    if (!aligned(m.p, 8 * m.es) || (ld >= 0 && rows > 1 && m.ld % 8 != ld)) return false;
+    ld = m.ld % 8;
+  }
+  return true;
+}
+
 fr_status drop_ok(float p, const int64_t *rng, int64_t site, fr::DropSpec *out) {
   *out = fr::DropSpec{};
   if (!(p >= 0.0f && p <= 1.0f)) return FR_ERR_INVALID_ARG;
@@ -1167,7 +1179,9 @@ fr_status fr_rmsnorm_backward(const void *dy, const void *h, const float *gamma,
     if (!workspace || workspace_bytes < need) return FR_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned(workspace, 16)) return FR_ERR_MISALIGNED;
   }
-  return launched(fr::launch_rmsnorm_backward(a, f32, vec, held, info.sm_count,
+  const bool phase = rows_in_phase({mdy, mh, mdh, mdx, mdr}, rows);
+  return launched(fr::launch_rmsnorm_backward(a, f32, vec, phase, held, info.sm_count,
+                                              info.max_smem_optin,
                                               reinterpret_cast<cudaStream_t>(stream)),
                   f);
 }

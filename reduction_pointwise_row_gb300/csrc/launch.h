@@ -317,8 +317,10 @@ struct NormBackward {
 // True when a row fits the registers of a CTA (vec: the rows are aligned).
 bool rmsnorm_grad_held_ok(int64_t cols, bool f32, bool vec);
 size_t rmsnorm_grad_workspace(int64_t rows, int64_t cols, bool f32, bool held, int sm_count);
-cudaError_t launch_rmsnorm_backward(const NormBackward &a, bool f32, bool vec, bool held,
-                                    int sm_count, cudaStream_t s);
+// phase: every matrix starts at a multiple of 8 elements and their row strides agree
+// modulo 8.
+cudaError_t launch_rmsnorm_backward(const NormBackward &a, bool f32, bool vec, bool phase, bool held,
+                                    int sm_count, int smem_max, cudaStream_t s);
 
 // Device address of the current device's error word (kernels record
 // FR_DEVERR_* codes there with atomicCAS; the first code wins).

@@ -31,6 +31,15 @@ struct Lane8 {
       else w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
     }
   }
+  // elements before `lo` and from `hi` on become 0
+  __device__ __forceinline__ void clip(int lo, int hi) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j >= lo && j < hi) continue;
+      if constexpr (F32) w[j] = 0;
+      else w[j >> 1] &= (j & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+    }
+  }
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < NW; ++i) w[i] = 0;
@@ -192,6 +201,67 @@ __device__ __forceinline__ void drop8(float (&v)[8], const Mask &m, uint32_t row
     for (int j = 0; j < 8; ++j)
       v[j] = (mine >> (4 * j + (lane >> 3))) & 1u ? v[j] * m.factor : 0.0f;
   }
+}
+
+// ---- rows in phase ------------------------------------------------------------------
+// Rows that start at element `phase` (0 .. 7) of an aligned 8-element unit: lane l of
+// chunk c holds the columns from 256 c + 8 l - phase on, one aligned unit; the first and
+// the last unit of a row lie partly outside it.
+
+// Writes the elements of a unit from column `col` on that are within the row.
+template <bool F32, bool PH>
+__device__ __forceinline__ void store_unit(char *row, int col, int cols, const Lane8<F32> &v) {
+  constexpr int ES = F32 ? 4 : 2;
+  if (col >= cols) return;
+  char *p = row + static_cast<int64_t>(col) * ES;
+  if (!PH || (col >= 0 && col + 8 <= cols)) {
+    if constexpr (F32) {
+      V8 u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u.w[i] = v.w[i];
+      st_stream_v8(p, u);
+    } else {
+      st_stream_u4(p, make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]));
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (col + j < 0 || col + j >= cols) continue;
+    if constexpr (F32) st_stream_f32(reinterpret_cast<float *>(p) + j, __uint_as_float(v.w[j]));
+    else st_stream_u16(p + 2 * j, static_cast<uint16_t>((j & 1) ? v.w[j >> 1] >> 16 : v.w[j >> 1]));
+  }
+}
+
+// Which elements of block `b` of a row stay: bit e of element e.
+__device__ __forceinline__ uint32_t kept_bits(const Mask &m, uint32_t row, uint32_t b) {
+  const uint4 r = philox7(b, row, m.o0, m.o1, m.k0, m.k1);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    bits |= ((w[i] << 16) > m.limit ? 1u : 0u) << (2 * i);
+    bits |= (w[i] > m.limit ? 1u : 0u) << (2 * i + 1);
+  }
+  return bits;
+}
+
+// The kept bits of the block before chunk c (chunk 0: of none).
+__device__ __forceinline__ uint32_t mask_before(const Mask &m, uint32_t row, int c) {
+  return kept_bits(m, row, static_cast<uint32_t>(c * 32 - 1));
+}
+
+// drop8 for a lane's unit of a row in phase: its first `phase` elements belong to the
+// block before its lane's.  `before`: lane i's mask_before of the warp's i-th chunk.
+__device__ __forceinline__ void drop8_phase(float (&v)[8], const Mask &m, uint32_t row, int c,
+                                            int lane, int phase, uint32_t before, int i) {
+  const uint32_t own = kept_bits(m, row, static_cast<uint32_t>(c * 32 + lane));
+  uint32_t prev = __shfl_up_sync(0xffffffffu, own, 1);
+  const uint32_t first = __shfl_sync(0xffffffffu, before, i);
+  if (lane == 0) prev = first;
+  const uint32_t bits = (prev | own << 8) >> (8 - phase);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = bits >> j & 1u ? v[j] * m.factor : 0.0f;
 }
 
 }  // namespace fr

@@ -5,6 +5,8 @@
 // A CTA goes over many rows and keeps its columns' share of dgamma in registers, so
 // the rows are read once; the CTAs' shares go to the workspace and a second small
 // kernel adds them in a fixed order.
+#include <algorithm>
+
 #include "rmsnorm.cuh"
 
 namespace fr {
@@ -156,6 +158,233 @@ __global__ void __launch_bounds__(512) rmsnorm_grad_held(NormBackward a) {
     part[col] = sums[col];
 }
 
+// bf16 rows in phase (every matrix's row starts at the same element of an 8-element unit;
+// base addresses at its first): the rows' units come through a ring of `stages` stages of
+// RP rows in shared memory by asynchronous 16-byte copies.  A thread reads only what it
+// copied, so the ring needs no barrier, and the copies of the next rows are in flight
+// while a row is reduced and written.  blockDim = (32 W, R), R groups of RP rows at a time,
+// NU units a lane; short rows (1 << lg < 32 lanes a row, W = NU = 1) several a warp.  With
+// u = dy gamma, the gradient is dh + rstd dy gamma - (rstd^2 mean) h: paired fp32
+// arithmetic, two fused steps a pair.
+//
+// EXACT: aligned rows of 256 NU W columns (or short ones).  Otherwise a row may start
+// within a unit and end within one: a CTA takes rows that start at one such place (phase),
+// so that its threads' columns stay the same.  The first and last unit of such a row
+// hold elements of its neighbours (or nothing, which the copy leaves out past the matrix's
+// end); they count as 0 and are not written.
+// Warps of a CTA, at most: 128 registers a thread, or 170 where NU units of inexact rows
+// need them.
+template <bool EXACT, int NU>
+constexpr int kRingWarps = EXACT || NU <= 2 ? 16 : 12;
+
+template <bool EXACT, int NU, int RP>
+__global__ void __launch_bounds__(kRingWarps<EXACT, NU> * 32, 1)
+rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
+  pdl_enter();
+  __shared__ float red[2][16][RP][16];  // [round & 1][row group][row][warp]
+  extern __shared__ __align__(16) unsigned char ring[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5, R = blockDim.y;
+  const int at = lane & ((1 << lg) - 1), sub = lane >> lg, per = 32 >> lg;
+  const int T = blockDim.x * R, tid = threadIdx.y * blockDim.x + threadIdx.x;
+  const int cols = static_cast<int>(a.cols);
+  const uint32_t rows = static_cast<uint32_t>(a.rows);
+  const bool up = a.dh != nullptr, drop = RP == 1 && a.drop.rng != nullptr;
+  // rows cls, cls + classes, ...: of these, runs of per R RP, every step-th run
+  const uint32_t cls = blockIdx.x % classes;
+  const uint32_t next = classes * per * R;  // from a group's row to its next of the same stage
+  const uint32_t hop = next * RP * (gridDim.x / classes);
+  const uint32_t begin = cls + classes * per * R * RP * (blockIdx.x / classes);
+  uint32_t row = begin + classes * (threadIdx.y * per + sub);
+  const int rounds = begin < rows ? static_cast<int>((rows - begin - 1) / hop + 1) : 0;
+  const int phase = EXACT ? 0 : static_cast<int>((cls * a.ld_h) & 7);
+  const int col0 = warp * kChunk + at * 8 - phase;  // of the first unit; the next is W chunks on
+
+  const int row_bytes = NU * T * 16, input_bytes = RP * row_bytes;
+  const int stage_bytes = (up ? 3 : 2) * input_bytes;
+  uint32_t ahead = row;  // the next row to copy, and where to
+  const uint32_t base = smem_addr(ring) + tid * 16, end = base + stages * stage_bytes;
+  uint32_t into = base;
+  const auto copy_row = [&](const void *m, int64_t ld, uint32_t r, uint32_t dst) {
+    const char *src = static_cast<const char *>(m) + (r * ld + col0) * 2;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int left = cols - (col0 + i * W * kChunk);
+      if (EXACT || left >= 8) {
+        if (EXACT && lg < 5 && at * 8 >= cols) continue;
+        cp_async_16(dst + i * (T * 16), src + i * W * (2 * kChunk));
+      } else if (left > 0) {
+        cp_async_16_part(dst + i * (T * 16), src + i * W * (2 * kChunk), 2 * left);
+      }
+    }
+  };
+  const auto issue = [&] {
+#pragma unroll
+    for (int p = 0; p < RP; ++p) {
+      const uint32_t r = ahead + p * next;
+      if (r >= rows) break;
+      copy_row(a.dy, a.ld_dy, r, into + p * row_bytes);
+      copy_row(a.h, a.ld_h, r, into + input_bytes + p * row_bytes);
+      if (up) copy_row(a.dh, a.ld_dh, r, into + 2 * input_bytes + p * row_bytes);
+    }
+    cp_async_commit();
+    ahead += hop;  // rows <= INT32_MAX and hops of under 2^22: no wrap
+    into += stage_bytes;
+    if (into == end) into = base;
+  };
+  uint32_t slot = base;
+  // a lane's unit i of row p of input n of the stage at `slot`
+  const auto unit = [&](int n, int p, int i) {
+    const uint4 u = lds_u4(slot + n * input_bytes + p * row_bytes + i * (T * 16));
+    Lane8<false> v;
+    v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
+    if constexpr (!EXACT) {
+      const int col = col0 + i * W * kChunk;
+      if (col < 0 || col + 8 > cols) v.clip(-col, cols - col);
+    } else if (lg < 5 && at * 8 >= cols) {
+      v.zero();
+    }
+    return v;
+  };
+  const auto pair = [](uint32_t w) { return pack_f32x2(bf16_lo(w), bf16_hi(w)); };
+
+  for (int k = 0; k < stages - 1; ++k) issue();
+  uint64_t g[NU][4], acc[NU][4];
+#pragma unroll
+  for (int i = 0; i < NU; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int col = col0 + i * W * kChunk + 2 * j;
+      g[i][j] = pack_f32x2(col >= 0 && col < cols ? ld_keep_f32(a.gamma + col) : 0.0f,
+                           col >= -1 && col + 1 < cols ? ld_keep_f32(a.gamma + col + 1) : 0.0f);
+      acc[i][j] = 0;
+    }
+  for (int i = tid; i < 2 * 16 * RP * 16; i += T) (&red[0][0][0][0])[i] = 0.0f;
+  __syncthreads();
+  const float over = 1.0f / static_cast<float>(cols);
+  Mask mask{};
+  if (drop) mask = mask_of(a.drop);
+  float scale[RP];  // rstd of the next round's rows
+#pragma unroll
+  for (int p = 0; p < RP; ++p) scale[p] = row + p * next < rows ? ld_keep_f32(a.rstd + row + p * next) : 0.0f;
+  for (int k = 0; k < rounds; ++k) {
+    issue();
+    if (stages == 4) cp_async_wait<3>();
+    else if (stages == 3) cp_async_wait<2>();
+    else cp_async_wait<1>();
+    float dot[RP], rstd[RP];
+#pragma unroll
+    for (int p = 0; p < RP; ++p) {
+      rstd[p] = scale[p];
+      const uint32_t r = row + hop + p * next;
+      if (r < rows) scale[p] = ld_keep_f32(a.rstd + r);
+      uint64_t s = 0;
+      if (row + p * next < rows) {
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+          const Lane8<false> dy = unit(0, p, i), h = unit(1, p, i);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            s = fma_f32x2(mul_f32x2(pair(dy.w[j]), g[i][j]), pair(h.w[j]), s);
+        }
+      }
+      dot[p] = f32x2_lo(s) + f32x2_hi(s);
+    }
+    if (lg < 5) {
+#pragma unroll
+      for (int p = 0; p < RP; ++p)
+        for (int o = 1 << lg >> 1; o > 0; o >>= 1) dot[p] += __shfl_xor_sync(0xffffffffu, dot[p], o);
+    } else {
+      // two rows: each half of the warp adds up one of them
+      float v = dot[0];
+      if (RP == 2) {
+        const float other = lane < 16 ? dot[RP - 1] : dot[0];
+        v = (lane < 16 ? dot[0] : dot[RP - 1]) + __shfl_xor_sync(0xffffffffu, other, 16);
+      } else {
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (W > 1) {  // the two halves of red in turn: one barrier a round
+        float *r = red[k & 1][threadIdx.y][RP == 2 ? lane >> 4 : 0];
+        if ((lane & (RP == 2 ? 15 : 31)) == 0) r[warp] = v;
+        group_barrier(1 + threadIdx.y, blockDim.x);
+        v = r[lane & 15];
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      }
+      dot[0] = v;
+      if (RP == 2) {
+        dot[0] = __shfl_sync(0xffffffffu, v, 0);
+        dot[RP - 1] = __shfl_sync(0xffffffffu, v, 16);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < RP; ++p) {
+      const uint32_t r = row + p * next;
+      if (r >= rows) break;
+      const float b = -(dot[p] * over * rstd[p]) * rstd[p] * rstd[p];
+      const uint64_t rstd2 = pack_f32x2(rstd[p], rstd[p]), b2 = pack_f32x2(b, b);
+      uint32_t edge = 0;
+      if (!EXACT && drop) edge = mask_before(mask, r, lane * W + warp);
+      char *const out_x = row_of<false>(a.dx, r, a.ld_dx), *const out_r = row_of<false>(a.dres, r, a.ld_dres);
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        const int c = i * W + warp, col = col0 + i * W * kChunk;
+        if (!EXACT && c * kChunk - phase >= cols) continue;
+        const Lane8<false> dy = unit(0, p, i), h = unit(1, p, i);
+        Lane8<false> dh{};
+        if (up) dh = unit(2, p, i);
+        float d[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t x = mul_f32x2(pair(dy.w[j]), rstd2), hj = pair(h.w[j]);
+          acc[i][j] = fma_f32x2(x, hj, acc[i][j]);
+          const uint64_t v = fma_f32x2(hj, b2, up ? fma_f32x2(x, g[i][j], pair(dh.w[j]))
+                                                  : mul_f32x2(x, g[i][j]));
+          d[2 * j] = f32x2_lo(v);
+          d[2 * j + 1] = f32x2_hi(v);
+        }
+        Lane8<false> out;
+        const int bound = EXACT && lg == 5 ? INT32_MAX : cols;
+        if (drop) {
+          if (a.dres != nullptr) {
+            out.set(d);
+            store_unit<false, !EXACT>(out_r, col, bound, out);
+          }
+          if constexpr (!EXACT) drop8_phase(d, mask, r, c, lane, phase, edge, i);
+          else drop8<true>(d, mask, r, c, at);
+        }
+        out.set(d);
+        store_unit<false, !EXACT>(out_x, col, bound, out);
+      }
+    }
+    row += hop;
+    slot += stage_bytes;
+    if (slot == end) slot = base;
+  }
+  if (a.dgamma == nullptr) return;
+  // a warp's rows, then the row groups one after the other, in the ring's memory
+  float *part = static_cast<float *>(a.workspace) + static_cast<int64_t>(blockIdx.x) * cols;
+  float *sums = reinterpret_cast<float *>(ring);
+  cp_async_wait<0>();
+  for (int y = 0; y < R; ++y) {
+    __syncthreads();
+    if (static_cast<int>(threadIdx.y) != y) continue;
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float v = j & 1 ? f32x2_hi(acc[i][j >> 1]) : f32x2_lo(acc[i][j >> 1]);
+        for (int o = 16; o >= 1 << lg; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        const int col = col0 + i * W * kChunk + j;
+        if (sub != 0 || col < 0 || col >= cols) continue;
+        if (y > 0) v += sums[col];
+        if (y + 1 < R) sums[col] = v;
+        else part[col] = v;
+      }
+  }
+}
+
 // Looped form, first kernel: sum(u h) of each row, a CTA a row.
 constexpr int kLoopThreads = 512;
 template <bool F32, bool VEC>
@@ -234,7 +463,70 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_join(const float *partial, 
   if (threadIdx.x == 0 && out < cols) dgamma[out] = s;
 }
 
-// Shapes of the launches, which the workspace follows.
+// The ring's launch; W = 0: the row does not fit.
+struct RingShape {
+  int units, W, R, rp, lg, stages, classes;
+  bool exact;
+  int64_t grid;
+  size_t smem;
+};
+
+RingShape ring_shape(const NormBackward &a, int sm_count, int smem_max) {
+  RingShape g{};
+  const int64_t rem = a.rows == 1 ? 0 : a.ld_h & 7;
+  g.classes = rem == 0 ? 1 : rem & 1 ? 8 : rem & 2 ? 4 : 2;
+  const int chunks = static_cast<int>((a.cols + (g.classes > 1 ? 7 : 0) + kChunk - 1) / kChunk);
+  g.lg = 5;
+  if (g.classes == 1 && a.cols % 8 == 0)
+    while (g.lg > 0 && (8 << g.lg >> 1) >= a.cols) --g.lg;
+  // Two rows at a time, one with dropout (with two its generator's code, twice, costs more
+  // than they gain: bf16 [16384, 4096] 121 us against 105) or where two do not fit.  Without:
+  // [8192, 8192] 66.4 us against 73, 78 with a reduction for each.
+  g.rp = a.drop.rng != nullptr || chunks > 32 ? 1 : 2;
+  g.units = chunks <= 4 ? 1 : chunks <= 32 ? 2 : 4;
+  int warps = 16;
+  const auto fit = [&](int units) {
+    g.units = units;
+    g.W = (chunks + units - 1) / units;
+    g.exact = g.classes == 1 && (g.lg < 5 || a.cols == static_cast<int64_t>(kChunk) * units * g.W);
+    warps = g.exact || units <= 2 ? 16 : 12;
+    return warps / g.W * g.W;
+  };
+  // inexact rows of 9 to 11 warps leave the others idle ([8192, 4097]: 84 us, 64 so)
+  if (fit(g.units) < 12 && g.units == 2 && !g.exact) fit(3);
+  if (g.W > warps || (g.units == 4 && !g.exact)) return RingShape{};
+  const int64_t rows = (a.rows + g.classes - 1) / g.classes, ctas = sm_count / g.classes;
+  const int64_t per = (32 >> g.lg) * g.rp, groups = (rows + per - 1) / per;
+  g.R = static_cast<int>(std::min<int64_t>(std::min(15, warps / g.W), (groups + ctas - 1) / ctas));
+  g.grid = std::min<int64_t>((groups + g.R - 1) / g.R, ctas) * g.classes;
+  const size_t stage = static_cast<size_t>(a.dh ? 3 : 2) * g.units * 32 * g.W * g.R * 16 * g.rp;
+  g.stages = static_cast<int>(std::min<size_t>(g.rp == 2 ? 2 : 3, (smem_max - 5120) / stage));
+  if (g.stages < 2) return RingShape{};
+  g.smem = g.stages * stage;
+  return g;
+}
+
+template <bool EXACT, int NU, int RP>
+cudaError_t launch_ring_of(const NormBackward &a, const RingShape &g, cudaStream_t s) {
+  const auto kern = rmsnorm_grad_ring<EXACT, NU, RP>;
+  cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kern), g.smem);
+  if (e != cudaSuccess) return e;
+  return launch_k(kern, dim3(static_cast<unsigned>(g.grid)), dim3(32 * g.W, g.R), g.smem, s, 0, a, g.stages,
+                  g.classes, g.lg);
+}
+
+cudaError_t launch_ring(const NormBackward &a, const RingShape &g, cudaStream_t s) {
+  if (g.exact) {
+    if (g.units == 1) return g.rp == 1 ? launch_ring_of<true, 1, 1>(a, g, s) : launch_ring_of<true, 1, 2>(a, g, s);
+    if (g.units == 2) return g.rp == 1 ? launch_ring_of<true, 2, 1>(a, g, s) : launch_ring_of<true, 2, 2>(a, g, s);
+    return launch_ring_of<true, 4, 1>(a, g, s);
+  }
+  if (g.units == 1) return g.rp == 1 ? launch_ring_of<false, 1, 1>(a, g, s) : launch_ring_of<false, 1, 2>(a, g, s);
+  if (g.units == 2) return g.rp == 1 ? launch_ring_of<false, 2, 1>(a, g, s) : launch_ring_of<false, 2, 2>(a, g, s);
+  return g.rp == 1 ? launch_ring_of<false, 3, 1>(a, g, s) : launch_ring_of<false, 3, 2>(a, g, s);
+}
+
+// Shapes of the other launches, which the workspace follows.
 struct GradShape {
   int units, W, R;  // persistent
   int64_t grid;     // CTAs, or the looped form's runs of rows
@@ -243,7 +535,7 @@ struct GradShape {
 GradShape held_shape(int64_t rows, int64_t cols, bool f32, int sm_count) {
   const int chunks = static_cast<int>((cols + kChunk - 1) / kChunk);
   GradShape g{};
-  g.units = chunks <= 2 ? 1 : (chunks <= 32 || f32) ? 2 : 4;
+  g.units = !f32 && chunks > 32 ? 4 : chunks <= 2 ? 1 : 2;
   g.W = (chunks + g.units - 1) / g.units;
   g.R = g.W >= 8 ? 1 : 8 / g.W;
   const int64_t per = g.W * g.R >= 16 ? 1 : 2;
@@ -263,17 +555,25 @@ GradShape looped_shape(int64_t rows, int64_t cols, int sm_count) {
 int64_t dots_bytes(int64_t rows) { return (rows * 4 + 15) / 16 * 16; }
 
 template <bool F32, bool VEC>
-cudaError_t launch_grad(const NormBackward &a, bool held, int sm_count, cudaStream_t s) {
+cudaError_t launch_grad(const NormBackward &a, bool held, bool phase, int sm_count, int smem_max, cudaStream_t s) {
   cudaError_t e;
   const float *partial = static_cast<const float *>(a.workspace);
   int64_t P;
-  if (held) {
+  RingShape rs{};
+  if (!F32 && held && phase) rs = ring_shape(a, sm_count, smem_max);
+  if (rs.W > 0) {
+    e = launch_ring(a, rs, s);
+    P = rs.grid;
+  } else if (held) {
     const GradShape g = held_shape(a.rows, a.cols, F32, sm_count);
     const dim3 grid(static_cast<unsigned>(g.grid)), block(32 * g.W, g.R);
     const size_t smem = g.R > 1 ? a.cols * 4 : 0;
-    if (g.units == 1) e = launch_k(rmsnorm_grad_held<F32, VEC, 1>, grid, block, smem, s, 0, a);
-    else if (F32 || !VEC || g.units == 2) e = launch_k(rmsnorm_grad_held<F32, VEC, 2>, grid, block, smem, s, 0, a);
-    else e = launch_k(rmsnorm_grad_held<false, true, 4>, grid, block, smem, s, 0, a);
+    if constexpr (!F32 && VEC) {  // shorter ones take the ring
+      e = launch_k(rmsnorm_grad_held<false, true, 4>, grid, block, smem, s, 0, a);
+    } else {
+      e = g.units == 1 ? launch_k(rmsnorm_grad_held<F32, VEC, 1>, grid, block, smem, s, 0, a)
+                       : launch_k(rmsnorm_grad_held<F32, VEC, 2>, grid, block, smem, s, 0, a);
+    }
     P = g.grid;
   } else {
     float *dots = static_cast<float *>(a.workspace);
@@ -301,14 +601,17 @@ bool rmsnorm_grad_held_ok(int64_t cols, bool f32, bool vec) {
 }
 
 size_t rmsnorm_grad_workspace(int64_t rows, int64_t cols, bool f32, bool held, int sm_count) {
-  if (held) return static_cast<size_t>(held_shape(rows, cols, f32, sm_count).grid * cols * 4);
+  if (held) return static_cast<size_t>(std::min<int64_t>(std::max<int64_t>(rows, 8), 2 * sm_count) * cols * 4);
   return static_cast<size_t>(dots_bytes(rows) + looped_shape(rows, cols, sm_count).grid * cols * 4);
 }
 
-cudaError_t launch_rmsnorm_backward(const NormBackward &a, bool f32, bool vec, bool held,
-                                    int sm_count, cudaStream_t s) {
-  if (f32) return vec ? launch_grad<true, true>(a, held, sm_count, s) : launch_grad<true, false>(a, held, sm_count, s);
-  return vec ? launch_grad<false, true>(a, held, sm_count, s) : launch_grad<false, false>(a, held, sm_count, s);
+cudaError_t launch_rmsnorm_backward(const NormBackward &a, bool f32, bool vec, bool phase, bool held,
+                                    int sm_count, int smem_max, cudaStream_t s) {
+  if (f32)
+    return vec ? launch_grad<true, true>(a, held, phase, sm_count, smem_max, s)
+               : launch_grad<true, false>(a, held, phase, sm_count, smem_max, s);
+  return vec ? launch_grad<false, true>(a, held, phase, sm_count, smem_max, s)
+             : launch_grad<false, false>(a, held, phase, sm_count, smem_max, s);
 }
 
 }  // namespace fr
