@@ -1085,7 +1085,8 @@ fr_status run_rmsnorm(fr::NormForward &a, fr_dtype dtype, bool quant, float p, c
   const fr_form f = form == FR_FORM_AUTO ? pick_rmsnorm(a.cols) : form;
   const bool vec = a.cols % 8 == 0 && aligned(a.gamma, 16) && rows_of_8(x, a.rows) &&
                    rows_of_8(res, a.rows) && rows_of_8(h, a.rows) && rows_of_8(y, a.rows);
-  return launched(fr::launch_rmsnorm(a, dtype == FR_F32, vec, quant, f == FR_FORM_PERSISTENT,
+  const bool phase = aligned(a.gamma, 16) && rows_in_phase({x, res, h, y}, a.rows);
+  return launched(fr::launch_rmsnorm(a, dtype == FR_F32, vec, phase, quant, f == FR_FORM_PERSISTENT,
                                      info.sm_count, reinterpret_cast<cudaStream_t>(stream)),
                   f);
 }
@@ -1114,7 +1115,7 @@ fr_status fr_dropout(const void *x, const void *residual, void *y, int64_t rows,
   a.ldr = ldr;
   a.ldh = ldy;
   const bool vec = cols % 8 == 0 && rows_of_8(mx, rows) && rows_of_8(mr, rows) && rows_of_8(my, rows);
-  return fr::launch_dropout(a, dtype == FR_F32, vec, info.sm_count,
+  return fr::launch_dropout(a, dtype == FR_F32, vec, rows_in_phase({mx, mr, my}, rows), info.sm_count,
                             reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FR_OK
              : FR_ERR_CUDA;

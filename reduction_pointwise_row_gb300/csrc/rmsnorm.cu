@@ -50,6 +50,24 @@ __device__ __forceinline__ void store8_e4m3(void *row, int c, int lane, int cols
   }
 }
 
+// The same for a unit of a row in phase, from column `col` on.
+__device__ __forceinline__ void store_unit_e4m3(char *row, int col, int cols, const float (&v)[8],
+                                                const float (&inv)[2]) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    w[i] = pack_e4m3x2(v[4 * i] * inv[i], v[4 * i + 1] * inv[i]) |
+           static_cast<uint32_t>(pack_e4m3x2(v[4 * i + 2] * inv[i], v[4 * i + 3] * inv[i])) << 16;
+  if (col >= 0 && col + 8 <= cols) {
+    asm volatile("st.global.cs.v2.b32 [%0], {%1, %2};" ::"l"(row + col), "r"(w[0]), "r"(w[1]) : "memory");
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (col + j >= 0 && col + j < cols)
+      asm volatile("st.global.cs.u8 [%0], %1;" ::"l"(row + col + j), "r"(w[j >> 2] >> (8 * (j & 3))) : "memory");
+}
+
 __device__ __forceinline__ float warp_max(float v) {
   float m;
   asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
@@ -103,6 +121,21 @@ __device__ __forceinline__ void block_sum(const NormForward &a, const Mask &mask
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = x.at(j);
   if (a.drop.rng != nullptr) drop8<VEC>(v, mask, row, c, lane);
+  if (a.residual != nullptr) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += res.at(j);
+  }
+  x.set(v);
+}
+
+// The same for the warp's i-th chunk of a row in phase.
+__device__ __forceinline__ void block_sum_phase(const NormForward &a, const Mask &mask, uint32_t row,
+                                                int c, int lane, int phase, uint32_t before, int i,
+                                                Lane8<false> &x, const Lane8<false> &res) {
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = x.at(j);
+  if (a.drop.rng != nullptr) drop8_phase(v, mask, row, c, lane, phase, before, i);
   if (a.residual != nullptr) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += res.at(j);
@@ -282,6 +315,91 @@ __global__ void __launch_bounds__(kLoopThreads) rmsnorm_looped(NormForward a) {
   }
 }
 
+// bf16 rows in phase that are not aligned (odd row lengths): a lane's units are aligned ones
+// that begin up to 7 elements before their columns.  One 16-byte access instead of 8 of an
+// element: bf16 [16384, 4097] with residual MEASURED.
+template <int NU, bool SUM, bool QUANT>
+__global__ void __launch_bounds__(kHeldThreads<NU>, 1024 / kHeldThreads<NU>)
+rmsnorm_phase(NormForward a) {
+  pdl_enter();
+  __shared__ float red[2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+  const int cols = static_cast<int>(a.cols);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const bool live = row < a.rows, last = row + 1 == a.rows;
+  const bool with_max = QUANT && a.scale_mode == FR_SCALE_ROW;
+  const int phase = static_cast<int>(row * a.ldx & 7);
+  const int col0 = warp * kChunk + lane * 8 - phase;
+  float ss = 0.0f, most = 0.0f;
+  Lane8<false> h[NU];
+  if (live) {
+    const char *xr = row_of<false>(a.x, row, a.ldx);
+#pragma unroll
+    for (int i = 0; i < NU; ++i) h[i] = load_unit(xr, col0 + i * W * kChunk, cols, last);
+    if constexpr (SUM) {
+      Lane8<false> res[NU];
+      const char *rr = row_of<false>(a.residual, row, a.ldr);
+      if (a.residual != nullptr) {
+#pragma unroll
+        for (int i = 0; i < NU; ++i) res[i] = load_unit(rr, col0 + i * W * kChunk, cols, last);
+      }
+      Mask mask{};
+      uint32_t before = 0;
+      if (a.drop.rng != nullptr) {
+        mask = mask_of(a.drop);
+        before = mask_before(mask, static_cast<uint32_t>(row), lane * W + warp);
+      }
+      char *hr = row_of<false>(a.h, row, a.ldh);
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        block_sum_phase(a, mask, static_cast<uint32_t>(row), i * W + warp, lane, phase, before, i, h[i],
+                        res[i]);
+        store_unit<false, true>(hr, col0 + i * W * kChunk, cols, h[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int col = col0 + i * W * kChunk;
+      if (col < 0 || col + 8 > cols) h[i].clip(-col, cols - col);
+      float g[8];
+      if (with_max) load_cols_unit(g, a.gamma, col, cols);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = h[i].at(j);
+        ss = fmaf(v, v, ss);
+        if (with_max) most = max_nan(most, fabsf(v * g[j]));
+      }
+    }
+  }
+  row_reduce(ss, most, with_max, W, red);
+  if (!live) return;
+  const float rstd = 1.0f / sqrtf(ss / static_cast<float>(cols) + a.eps);
+  if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
+  float inv[2] = {1.0f, 1.0f};
+  if (QUANT) {
+    const float s = with_max ? scale_for(most * rstd) : ld_keep_f32(a.scale);
+    if (with_max && threadIdx.x == 0) a.scale[row * a.scale_row] = s;
+    inv[0] = inv[1] = 1.0f / s;
+  }
+  char *yr = QUANT ? static_cast<char *>(a.y) + row * a.ldy : row_of<false>(a.y, row, a.ldy);
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const int col = col0 + i * W * kChunk;
+    if (col >= cols) continue;
+    float v[8], g[8];
+    load_cols_unit(g, a.gamma, col, cols);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = h[i].at(j) * rstd * g[j];
+    if constexpr (QUANT) {
+      store_unit_e4m3(yr, col, cols, v, inv);
+    } else {
+      Lane8<false> y;
+      y.set(v);
+      store_unit<false, true>(yr, col, cols, y);
+    }
+  }
+}
+
 // Rows of at most a chunk, aligned: 1 << lg lanes hold a row, a warp U times 32 >> lg
 // rows at a time, with one reading of gamma; no barrier.
 template <bool F32, int U, bool SUM, bool QUANT>
@@ -359,33 +477,53 @@ __global__ void __launch_bounds__(256) rmsnorm_short(NormForward a, int lg) {
 }
 
 // Dropout alone.  A CTA's 8 warps take a run of 8 NU chunks of a row, or R = 8 / W short
-// rows of W warps; 1 << lg lanes hold a row of at most a chunk (32 of longer ones).
-template <bool F32, bool VEC, int NU>
+// rows of W warps; 1 << lg lanes hold an aligned row of at most a chunk (32 of others).
+enum { kScattered, kAligned, kPhase };  // how a lane's elements lie: element by element,
+                                        // in an aligned unit, in a unit of a row in phase
+template <bool F32, int HOW, int NU>
 __global__ void __launch_bounds__(256) dropout_chunks(NormForward a, unsigned runs, int lg) {
+  constexpr bool VEC = HOW == kAligned;
   pdl_enter();
   const int lane = threadIdx.x & 31, at = lane & ((1 << lg) - 1), W = blockDim.x >> 5;
   const int cols = static_cast<int>(a.cols);
   const unsigned group = blockIdx.x / runs, run = blockIdx.x - group * runs;
   const int first = static_cast<int>(run) * (W * NU) + (threadIdx.x >> 5);
   const int64_t row = ((static_cast<int64_t>(group) * blockDim.y + threadIdx.y) << (5 - lg)) + (lane >> lg);
-  const bool live = row < a.rows;
-  const int chunks = live ? (cols - 1) / kChunk + 1 : 0;
+  const bool live = row < a.rows, last = row + 1 == a.rows;
+  const int phase = HOW == kPhase ? static_cast<int>(row * a.ldx & 7) : 0;
+  const int chunks = live ? (cols - 1 + phase) / kChunk + 1 : 0;
+  const char *xr = row_of<F32>(a.x, row, a.ldx), *rr = row_of<F32>(a.residual, row, a.ldr);
+  char *yr = row_of<F32>(a.h, row, a.ldh);
   Lane8<F32> x[NU], res[NU];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     const int c = first + i * W;
     if (c >= chunks) break;
-    x[i] = load8<F32, VEC>(row_of<F32>(a.x, row, a.ldx), c, at, cols);
-    if (a.residual != nullptr) res[i] = load8<F32, VEC>(row_of<F32>(a.residual, row, a.ldr), c, at, cols);
+    if constexpr (HOW == kPhase) {
+      x[i] = load_unit(xr, c * kChunk + lane * 8 - phase, cols, last);
+      if (a.residual != nullptr) res[i] = load_unit(rr, c * kChunk + lane * 8 - phase, cols, last);
+    } else {
+      x[i] = load8<F32, VEC>(xr, c, at, cols);
+      if (a.residual != nullptr) res[i] = load8<F32, VEC>(rr, c, at, cols);
+    }
   }
   Mask mask{};
-  if (a.drop.rng != nullptr) mask = mask_of(a.drop);
+  uint32_t before = 0;
+  if (a.drop.rng != nullptr) {
+    mask = mask_of(a.drop);
+    if (HOW == kPhase) before = mask_before(mask, static_cast<uint32_t>(row), first + lane * W);
+  }
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     const int c = first + i * W;
     if (c >= chunks) break;
-    block_sum<F32, VEC>(a, mask, static_cast<uint32_t>(row), c, at, x[i], res[i]);
-    store8<F32, VEC>(row_of<F32>(a.h, row, a.ldh), c, at, cols, x[i]);
+    if constexpr (HOW == kPhase) {
+      block_sum_phase(a, mask, static_cast<uint32_t>(row), c, lane, phase, before, i, x[i], res[i]);
+      store_unit<false, true>(yr, c * kChunk + lane * 8 - phase, cols, x[i]);
+    } else {
+      block_sum<F32, VEC>(a, mask, static_cast<uint32_t>(row), c, at, x[i], res[i]);
+      store8<F32, VEC>(yr, c, at, cols, x[i]);
+    }
   }
 }
 
@@ -430,6 +568,19 @@ cudaError_t launch_held(const NormForward &a, int sm_count, cudaStream_t s) {
   return launch_k(rmsnorm_held<F32, VEC, 2, SUM, QUANT>, grid, block, 0, s, 0, a);
 }
 
+// Chunks a warp holds (us with 1, 2, 3, 4: [16384, 4097] with residual 134, 108, 89.1, 87.7;
+// [32768, 769] without 34.8, 27.6, 31.7, 23.8; [65536, 255] 57.9, 45.6, -, 61.7).
+template <bool QUANT, bool SUM>
+cudaError_t launch_phase(const NormForward &a, int sm_count, cudaStream_t s) {
+  const int chunks = static_cast<int>((a.cols + 7 + kChunk - 1) / kChunk);
+  const int units = a.rows < sm_count && chunks <= 32 ? 1 : chunks <= 2 ? 2 : 4;  // few rows: latency
+  const int W = (chunks + units - 1) / units, R = W >= 4 ? 1 : 4 / W;
+  const dim3 grid(static_cast<unsigned>((a.rows + R - 1) / R)), block(32 * W, R);
+  if (units == 1) return launch_k(rmsnorm_phase<1, SUM, QUANT>, grid, block, 0, s, 0, a);
+  if (units == 2) return launch_k(rmsnorm_phase<2, SUM, QUANT>, grid, block, 0, s, 0, a);
+  return launch_k(rmsnorm_phase<4, SUM, QUANT>, grid, block, 0, s, 0, a);
+}
+
 template <bool F32, bool VEC, bool QUANT>
 cudaError_t launch_looped(const NormForward &a, int sm_count, cudaStream_t s) {
   const int64_t most = static_cast<int64_t>(sm_count) * 4;
@@ -438,56 +589,63 @@ cudaError_t launch_looped(const NormForward &a, int sm_count, cudaStream_t s) {
 }
 
 template <bool F32, bool VEC, bool QUANT>
-cudaError_t launch_form(const NormForward &a, bool held, int sm_count, cudaStream_t s) {
+cudaError_t launch_form(const NormForward &a, bool phase, bool held, int sm_count, cudaStream_t s) {
   if (!held) return launch_looped<F32, VEC, QUANT>(a, sm_count, s);
   const bool sum = a.h != nullptr;
   if constexpr (VEC)
     if (a.cols <= kChunk)
       return sum ? launch_short<F32, true, QUANT>(a, s) : launch_short<F32, false, QUANT>(a, s);
+  if constexpr (!F32 && !VEC)
+    if (phase && !(QUANT && a.scale_mode == FR_SCALE_GROUP) && a.cols + 7 <= kChunk * kHeldChunks)
+      return sum ? launch_phase<QUANT, true>(a, sm_count, s) : launch_phase<QUANT, false>(a, sm_count, s);
   return sum ? launch_held<F32, VEC, QUANT, true>(a, sm_count, s)
              : launch_held<F32, VEC, QUANT, false>(a, sm_count, s);
 }
 
 template <bool F32, bool VEC>
-cudaError_t launch_norm(const NormForward &a, bool quant, bool held, int sm_count, cudaStream_t s) {
-  return quant ? launch_form<F32, VEC, true>(a, held, sm_count, s)
-               : launch_form<F32, VEC, false>(a, held, sm_count, s);
+cudaError_t launch_norm(const NormForward &a, bool phase, bool quant, bool held, int sm_count,
+                        cudaStream_t s) {
+  return quant ? launch_form<F32, VEC, true>(a, phase, held, sm_count, s)
+               : launch_form<F32, VEC, false>(a, phase, held, sm_count, s);
 }
 
-template <bool F32, bool VEC>
+template <bool F32, int HOW>
 cudaError_t launch_drop(const NormForward &a, int sm_count, cudaStream_t s) {
-  const int64_t chunks = (a.cols + kChunk - 1) / kChunk;
+  const int64_t chunks = (a.cols + (HOW == kPhase ? 7 : 0) + kChunk - 1) / kChunk;
   // several chunks a warp: their loads are in flight together (us with 1, 2, 4: bf16
   // [16384, 4096] 57.0, 49.8, 47.0); few in all: a warp each
   const int units = !F32 && a.rows * chunks >= 64 * static_cast<int64_t>(sm_count) ? 4 : 1;
   int lg = 5;
-  if (VEC)
+  if (HOW == kAligned)
     while (lg > 0 && (8 << lg >> 1) >= a.cols) --lg;
   const int W = static_cast<int>(std::min<int64_t>(8, (chunks + units - 1) / units)), R = 8 / W;
   const int64_t runs = (chunks + W * units - 1) / (W * units), per = static_cast<int64_t>(R) << (5 - lg);
   const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per * runs)), block(32 * W, R);
   if constexpr (!F32)
     if (units == 4)
-      return launch_k(dropout_chunks<F32, VEC, 4>, grid, block, 0, s, 0, a, static_cast<unsigned>(runs), lg);
-  return launch_k(dropout_chunks<F32, VEC, 1>, grid, block, 0, s, 0, a, static_cast<unsigned>(runs), lg);
+      return launch_k(dropout_chunks<F32, HOW, 4>, grid, block, 0, s, 0, a, static_cast<unsigned>(runs), lg);
+  return launch_k(dropout_chunks<F32, HOW, 1>, grid, block, 0, s, 0, a, static_cast<unsigned>(runs), lg);
 }
 
 }  // namespace
 
 bool rmsnorm_held_ok(int64_t cols) { return cols <= kChunk * kHeldChunks; }
 
-cudaError_t launch_rmsnorm(const NormForward &a, bool f32, bool vec, bool quant, bool held,
+cudaError_t launch_rmsnorm(const NormForward &a, bool f32, bool vec, bool phase, bool quant, bool held,
                            int sm_count, cudaStream_t s) {
   if (f32)
-    return vec ? launch_norm<true, true>(a, quant, held, sm_count, s)
-               : launch_norm<true, false>(a, quant, held, sm_count, s);
-  return vec ? launch_norm<false, true>(a, quant, held, sm_count, s)
-             : launch_norm<false, false>(a, quant, held, sm_count, s);
+    return vec ? launch_norm<true, true>(a, phase, quant, held, sm_count, s)
+               : launch_norm<true, false>(a, phase, quant, held, sm_count, s);
+  return vec ? launch_norm<false, true>(a, phase, quant, held, sm_count, s)
+             : launch_norm<false, false>(a, phase, quant, held, sm_count, s);
 }
 
-cudaError_t launch_dropout(const NormForward &a, bool f32, bool vec, int sm_count, cudaStream_t s) {
-  if (f32) return vec ? launch_drop<true, true>(a, sm_count, s) : launch_drop<true, false>(a, sm_count, s);
-  return vec ? launch_drop<false, true>(a, sm_count, s) : launch_drop<false, false>(a, sm_count, s);
+cudaError_t launch_dropout(const NormForward &a, bool f32, bool vec, bool phase, int sm_count,
+                           cudaStream_t s) {
+  if (f32) return vec ? launch_drop<true, kAligned>(a, sm_count, s) : launch_drop<true, kScattered>(a, sm_count, s);
+  return vec     ? launch_drop<false, kAligned>(a, sm_count, s)
+         : phase ? launch_drop<false, kPhase>(a, sm_count, s)
+                 : launch_drop<false, kScattered>(a, sm_count, s);
 }
 
 }  // namespace fr

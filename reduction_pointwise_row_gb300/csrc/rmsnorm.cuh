@@ -208,6 +208,55 @@ __device__ __forceinline__ void drop8(float (&v)[8], const Mask &m, uint32_t row
 // chunk c holds the columns from 256 c + 8 l - phase on, one aligned unit; the first and
 // the last unit of a row lie partly outside it.
 
+// The unit from column `col` on of the bf16 row at `row`, as it lies in memory: elements
+// outside the row are its neighbours', to be clipped.  A matrix's first row has no head
+// (its base is aligned); what lies past its last one is not read.
+__device__ __forceinline__ Lane8<false> load_unit(const char *row, int col, int cols, bool last) {
+  Lane8<false> v;
+  v.zero();
+  const char *p = row + static_cast<int64_t>(col) * 2;
+  if (col < cols && (!last || col + 8 <= cols)) {
+    const uint4 u = ld_once_u4(p);
+    v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
+  } else if (col < cols) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + j < cols)
+        v.w[j >> 1] |= static_cast<uint32_t>(ld_stream_u16(p + 2 * j)) << (16 * (j & 1));
+  }
+  return v;
+}
+
+// The 8 values from column `col` on of a 16-byte aligned vector over the columns, 0
+// outside it: the three aligned 16-byte pieces that hold them, cut at the same place in
+// every lane (rows start at one phase), instead of 8 scattered values a lane.
+__device__ __forceinline__ void load_cols_unit(float (&g)[8], const float *p, int col, int cols) {
+  const int t = col & 3, first = col - t;
+  if (first >= 0 && first + 12 <= cols) {
+    const float4 a = ld_keep_f4(p + first), b = ld_keep_f4(p + first + 4);
+    float4 c = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (t != 0) c = ld_keep_f4(p + first + 8);
+    const float f[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+    if (t == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = f[j];
+    } else if (t == 1) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = f[j + 1];
+    } else if (t == 2) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = f[j + 2];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = f[j + 3];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      g[j] = col + j >= 0 && col + j < cols ? ld_keep_f32(p + col + j) : 0.0f;
+  }
+}
+
 // Writes the elements of a unit from column `col` on that are within the row.
 template <bool F32, bool PH>
 __device__ __forceinline__ void store_unit(char *row, int col, int cols, const Lane8<F32> &v) {

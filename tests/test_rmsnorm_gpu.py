@@ -472,8 +472,9 @@ def test_outputs_in_the_inputs_buffers(cols, form):
     # the two halves of one buffer: each in the gaps of the other
     both = torch.empty(rows, 2 * cols, dtype=x.dtype, device="cuda")
     both[:, :cols] = x
-    got = fr.fr_rmsnorm(both[:, :cols], gamma, EPS, out=both[:, cols:], form=form)["y"]
-    assert torch.equal(got, fr.fr_rmsnorm(x, gamma, EPS, form=form)["y"])
+    got = fr.fr_rmsnorm(both[:, :cols], gamma, EPS, out=both[:, cols:], form=form)
+    # (another alignment adds up a row's squares in another order: not the same bits)
+    check_norm(x.cpu(), None, 0.0, None, 0, got, gamma.cpu(), "gaps")
     assert torch.equal(both[:, :cols], x)
 
 
