@@ -128,14 +128,14 @@ __device__ __forceinline__ void block_sum(const NormForward &a, const Mask &mask
   x.set(v);
 }
 
-// The same for the warp's i-th chunk of a row in phase.
+// The same for a chunk of a row in phase.
 __device__ __forceinline__ void block_sum_phase(const NormForward &a, const Mask &mask, uint32_t row,
-                                                int c, int lane, int phase, uint32_t before, int i,
+                                                int c, int lane, int phase, uint32_t &before,
                                                 Lane8<false> &x, const Lane8<false> &res) {
   float v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = x.at(j);
-  if (a.drop.rng != nullptr) drop8_phase(v, mask, row, c, lane, phase, before, i);
+  if (a.drop.rng != nullptr) drop8_phase(v, mask, row, c, lane, phase, before);
   if (a.residual != nullptr) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += res.at(j);
@@ -329,37 +329,37 @@ rmsnorm_phase(NormForward a) {
   const bool live = row < a.rows, last = row + 1 == a.rows;
   const bool with_max = QUANT && a.scale_mode == FR_SCALE_ROW;
   const int phase = static_cast<int>(row * a.ldx & 7);
-  const int col0 = warp * kChunk + lane * 8 - phase;
+  const int col0 = warp * NU * kChunk + lane * 8 - phase;  // a warp's chunks follow one another
   float ss = 0.0f, most = 0.0f;
   Lane8<false> h[NU];
   if (live) {
     const char *xr = row_of<false>(a.x, row, a.ldx);
 #pragma unroll
-    for (int i = 0; i < NU; ++i) h[i] = load_unit(xr, col0 + i * W * kChunk, cols, last);
+    for (int i = 0; i < NU; ++i) h[i] = load_unit(xr, col0 + i * kChunk, cols, last);
     if constexpr (SUM) {
       Lane8<false> res[NU];
       const char *rr = row_of<false>(a.residual, row, a.ldr);
       if (a.residual != nullptr) {
 #pragma unroll
-        for (int i = 0; i < NU; ++i) res[i] = load_unit(rr, col0 + i * W * kChunk, cols, last);
+        for (int i = 0; i < NU; ++i) res[i] = load_unit(rr, col0 + i * kChunk, cols, last);
       }
       Mask mask{};
       uint32_t before = 0;
       if (a.drop.rng != nullptr) {
         mask = mask_of(a.drop);
-        before = mask_before(mask, static_cast<uint32_t>(row), lane * W + warp);
+        before = kept_before(mask, static_cast<uint32_t>(row), warp * NU);
       }
       char *hr = row_of<false>(a.h, row, a.ldh);
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
-        block_sum_phase(a, mask, static_cast<uint32_t>(row), i * W + warp, lane, phase, before, i, h[i],
+        block_sum_phase(a, mask, static_cast<uint32_t>(row), warp * NU + i, lane, phase, before, h[i],
                         res[i]);
-        store_unit<false, true>(hr, col0 + i * W * kChunk, cols, h[i]);
+        store_unit<false, true>(hr, col0 + i * kChunk, cols, h[i]);
       }
     }
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const int col = col0 + i * W * kChunk;
+      const int col = col0 + i * kChunk;
       if (col < 0 || col + 8 > cols) h[i].clip(-col, cols - col);
       float g[8];
       if (with_max) load_cols_unit(g, a.gamma, col, cols);
@@ -384,7 +384,7 @@ rmsnorm_phase(NormForward a) {
   char *yr = QUANT ? static_cast<char *>(a.y) + row * a.ldy : row_of<false>(a.y, row, a.ldy);
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    const int col = col0 + i * W * kChunk;
+    const int col = col0 + i * kChunk;
     if (col >= cols) continue;
     float v[8], g[8];
     load_cols_unit(g, a.gamma, col, cols);
@@ -476,54 +476,84 @@ __global__ void __launch_bounds__(256) rmsnorm_short(NormForward a, int lg) {
   }
 }
 
-// Dropout alone.  A CTA's 8 warps take a run of 8 NU chunks of a row, or R = 8 / W short
-// rows of W warps; 1 << lg lanes hold an aligned row of at most a chunk (32 of others).
+// Dropout alone.  A warp has NU chunks of a row, one after the other (a CTA's 8 warps a run
+// of 8 NU of them, or R = 8 / W rows), or for short rows (SHORT, not in phase) the same chunk
+// of NU rows; 1 << lg lanes hold an aligned row of at most a chunk (32 of others).
 enum { kScattered, kAligned, kPhase };  // how a lane's elements lie: element by element,
                                         // in an aligned unit, in a unit of a row in phase
-template <bool F32, int HOW, int NU>
-__global__ void __launch_bounds__(256) dropout_chunks(NormForward a, unsigned runs, int lg) {
+template <bool F32, int HOW, int NU, bool SHORT, bool RES>
+__global__ void __launch_bounds__(256, HOW == kAligned && RES ? 3 : 4) dropout_chunks(NormForward a, unsigned runs, int lg) {
   constexpr bool VEC = HOW == kAligned;
   pdl_enter();
   const int lane = threadIdx.x & 31, at = lane & ((1 << lg) - 1), W = blockDim.x >> 5;
   const int cols = static_cast<int>(a.cols);
-  const unsigned group = blockIdx.x / runs, run = blockIdx.x - group * runs;
-  const int first = static_cast<int>(run) * (W * NU) + (threadIdx.x >> 5);
-  const int64_t row = ((static_cast<int64_t>(group) * blockDim.y + threadIdx.y) << (5 - lg)) + (lane >> lg);
-  const bool live = row < a.rows, last = row + 1 == a.rows;
-  const int phase = HOW == kPhase ? static_cast<int>(row * a.ldx & 7) : 0;
-  const int chunks = live ? (cols - 1 + phase) / kChunk + 1 : 0;
-  const char *xr = row_of<F32>(a.x, row, a.ldx), *rr = row_of<F32>(a.residual, row, a.ldr);
-  char *yr = row_of<F32>(a.h, row, a.ldh);
-  Lane8<F32> x[NU], res[NU];
+  const unsigned group = SHORT ? blockIdx.x : blockIdx.x / runs;
+  const int first = SHORT ? threadIdx.x >> 5
+                          : (static_cast<int>(blockIdx.x - group * runs) * W + static_cast<int>(threadIdx.x >> 5)) * NU;
+  const int64_t row0 = ((static_cast<int64_t>(group) * ((SHORT ? NU : 1) * blockDim.y) + threadIdx.y) << (5 - lg)) +
+                       (lane >> lg);
+  const auto row_at = [&](int i) { return SHORT ? row0 + (static_cast<int64_t>(i * blockDim.y) << (5 - lg)) : row0; };
+  const auto chunk_at = [&](int i) { return SHORT ? first : first + i; };
+  const auto phase_at = [&](int i) { return HOW == kPhase ? static_cast<int>(row_at(i) * a.ldx & 7) : 0; };
+  const auto has = [&](int i) {  // a warp's lanes agree but for short aligned rows
+    return row_at(i) < a.rows && chunk_at(i) <= (cols - 1 + phase_at(i)) / kChunk;
+  };
+  Mask mask{};
+  if (a.drop.rng != nullptr) mask = mask_of(a.drop);
+  Lane8<F32> x[NU], res[RES ? NU : 1];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    const int c = first + i * W;
-    if (c >= chunks) break;
+    if (!has(i)) continue;
+    const int64_t row = row_at(i);
+    const char *xr = row_of<F32>(a.x, row, a.ldx), *rr = row_of<F32>(a.residual, row, a.ldr);
     if constexpr (HOW == kPhase) {
-      x[i] = load_unit(xr, c * kChunk + lane * 8 - phase, cols, last);
-      if (a.residual != nullptr) res[i] = load_unit(rr, c * kChunk + lane * 8 - phase, cols, last);
+      const int col = chunk_at(i) * kChunk + lane * 8 - phase_at(i);
+      x[i] = load_unit(xr, col, cols, row + 1 == a.rows);
+      if constexpr (RES) res[i] = load_unit(rr, col, cols, row + 1 == a.rows);
     } else {
-      x[i] = load8<F32, VEC>(xr, c, at, cols);
-      if (a.residual != nullptr) res[i] = load8<F32, VEC>(rr, c, at, cols);
+      x[i] = load8<F32, VEC>(xr, chunk_at(i), at, cols);
+      if constexpr (RES) res[i] = load8<F32, VEC>(rr, chunk_at(i), at, cols);
     }
   }
-  Mask mask{};
+  // The generator's work is done while the loads are on their way: bf16 [16384, 4096] 43.7
+  // us, 47.2 with each chunk's done when its turn comes.
+  uint4 words[NU];
   uint32_t before = 0;
   if (a.drop.rng != nullptr) {
-    mask = mask_of(a.drop);
-    if (HOW == kPhase) before = mask_before(mask, static_cast<uint32_t>(row), first + lane * W);
+    if (HOW == kPhase) before = kept_before(mask, static_cast<uint32_t>(row0), first);
+    if constexpr (HOW == kAligned) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        words[i] = block_of(mask, static_cast<uint32_t>(row_at(i)), chunk_at(i), at);
+        asm volatile("" : "+r"(words[i].x), "+r"(words[i].y), "+r"(words[i].z), "+r"(words[i].w));
+      }
+    }
   }
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    const int c = first + i * W;
-    if (c >= chunks) break;
-    if constexpr (HOW == kPhase) {
-      block_sum_phase(a, mask, static_cast<uint32_t>(row), c, lane, phase, before, i, x[i], res[i]);
-      store_unit<false, true>(yr, c * kChunk + lane * 8 - phase, cols, x[i]);
-    } else {
-      block_sum<F32, VEC>(a, mask, static_cast<uint32_t>(row), c, at, x[i], res[i]);
-      store8<F32, VEC>(yr, c, at, cols, x[i]);
+    if (!has(i)) continue;
+    const int64_t row = row_at(i);
+    const int c = chunk_at(i);
+    char *yr = row_of<F32>(a.h, row, a.ldh);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = x[i].at(j);
+    if (a.drop.rng != nullptr) {
+      if constexpr (HOW == kPhase) {
+        drop8_phase(v, mask, static_cast<uint32_t>(row), c, lane, phase_at(i), before);
+      } else if constexpr (VEC) {
+        drop8_by<true>(v, mask, words[i], at);
+      } else {
+        drop8<false>(v, mask, static_cast<uint32_t>(row), c, lane);
+      }
     }
+    if constexpr (RES) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += res[i].at(j);
+    }
+    x[i].set(v);
+    if constexpr (HOW == kPhase) store_unit<false, true>(yr, c * kChunk + lane * 8 - phase_at(i), cols, x[i]);
+    else store8<F32, VEC>(yr, c, at, cols, x[i]);
   }
 }
 
@@ -609,22 +639,37 @@ cudaError_t launch_norm(const NormForward &a, bool phase, bool quant, bool held,
                : launch_form<F32, VEC, false>(a, phase, held, sm_count, s);
 }
 
-template <bool F32, int HOW>
-cudaError_t launch_drop(const NormForward &a, int sm_count, cudaStream_t s) {
+template <bool F32, int HOW, bool RES>
+cudaError_t launch_drop_of(const NormForward &a, int sm_count, cudaStream_t s) {
   const int64_t chunks = (a.cols + (HOW == kPhase ? 7 : 0) + kChunk - 1) / kChunk;
-  // several chunks a warp: their loads are in flight together (us with 1, 2, 4: bf16
-  // [16384, 4096] 57.0, 49.8, 47.0); few in all: a warp each
-  const int units = !F32 && a.rows * chunks >= 64 * static_cast<int64_t>(sm_count) ? 4 : 1;
   int lg = 5;
   if (HOW == kAligned)
     while (lg > 0 && (8 << lg >> 1) >= a.cols) --lg;
-  const int W = static_cast<int>(std::min<int64_t>(8, (chunks + units - 1) / units)), R = 8 / W;
-  const int64_t runs = (chunks + W * units - 1) / (W * units), per = static_cast<int64_t>(R) << (5 - lg);
+  // several chunks a warp: their loads are in flight together (us with 1, 2, 4: bf16
+  // [16384, 4096] 57.0, 49.8, 47.0); few in all, or fp32 (39.8, 40.1, 40.3 at [8192, 4096]): one
+  int units = !F32 && a.rows * chunks >= 64 * static_cast<int64_t>(sm_count) ? 4 : 1;
+  const bool rows4 = HOW != kPhase && units == 4 && chunks <= 2;
+  if (HOW == kPhase && units == 4 && chunks <= 2) units = 2;
+  const int W = static_cast<int>(rows4 ? chunks : std::min<int64_t>(8, (chunks + units - 1) / units)), R = 8 / W;
+  const int64_t runs = (chunks + W * units - 1) / (W * units);
+  const int64_t per = (static_cast<int64_t>(R) << (5 - lg)) * (rows4 ? units : 1);
   const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per * runs)), block(32 * W, R);
-  if constexpr (!F32)
-    if (units == 4)
-      return launch_k(dropout_chunks<F32, HOW, 4>, grid, block, 0, s, 0, a, static_cast<unsigned>(runs), lg);
-  return launch_k(dropout_chunks<F32, HOW, 1>, grid, block, 0, s, 0, a, static_cast<unsigned>(runs), lg);
+  const unsigned n = static_cast<unsigned>(runs);
+  if constexpr (!F32) {
+    if constexpr (HOW == kPhase) {
+      if (units == 2) return launch_k(dropout_chunks<F32, HOW, 2, false, RES>, grid, block, 0, s, 0, a, n, lg);
+    } else {
+      if (rows4) return launch_k(dropout_chunks<F32, HOW, 4, true, RES>, grid, block, 0, s, 0, a, n, lg);
+    }
+    if (units == 4) return launch_k(dropout_chunks<F32, HOW, 4, false, RES>, grid, block, 0, s, 0, a, n, lg);
+  }
+  return launch_k(dropout_chunks<F32, HOW, 1, false, RES>, grid, block, 0, s, 0, a, n, lg);
+}
+
+template <bool F32, int HOW>
+cudaError_t launch_drop(const NormForward &a, int sm_count, cudaStream_t s) {
+  return a.residual != nullptr ? launch_drop_of<F32, HOW, true>(a, sm_count, s)
+                               : launch_drop_of<F32, HOW, false>(a, sm_count, s);
 }
 
 }  // namespace

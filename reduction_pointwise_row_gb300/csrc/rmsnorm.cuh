@@ -176,11 +176,15 @@ __device__ __forceinline__ uint4 philox7(uint32_t c0, uint32_t c1, uint32_t c2, 
   return make_uint4(c0, c1, c2, c3);
 }
 
-// v[j] = kept ? v[j] * factor : 0 for a lane's elements of chunk c of a row.  Every
-// lane of the warp takes part.  A dropped element is 0 whatever it holds.
+// The block of a lane's aligned chunk c of a row.
+__device__ __forceinline__ uint4 block_of(const Mask &m, uint32_t row, int c, int lane) {
+  return philox7(static_cast<uint32_t>(c * 32 + lane), row, m.o0, m.o1, m.k0, m.k1);
+}
+
+// v[j] = kept ? v[j] * factor : 0 for a lane's elements of a chunk, given its block b.
+// Every lane of the warp takes part.  A dropped element is 0 whatever it holds.
 template <bool VEC>
-__device__ __forceinline__ void drop8(float (&v)[8], const Mask &m, uint32_t row, int c, int lane) {
-  const uint4 b = philox7(static_cast<uint32_t>(c * 32 + lane), row, m.o0, m.o1, m.k0, m.k1);
+__device__ __forceinline__ void drop8_by(float (&v)[8], const Mask &m, const uint4 &b, int lane) {
   const uint32_t w[4] = {b.x, b.y, b.z, b.w};
   if constexpr (VEC) {
 #pragma unroll
@@ -201,6 +205,11 @@ __device__ __forceinline__ void drop8(float (&v)[8], const Mask &m, uint32_t row
     for (int j = 0; j < 8; ++j)
       v[j] = (mine >> (4 * j + (lane >> 3))) & 1u ? v[j] * m.factor : 0.0f;
   }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void drop8(float (&v)[8], const Mask &m, uint32_t row, int c, int lane) {
+  drop8_by<VEC>(v, m, block_of(m, row, c, lane), lane);
 }
 
 // ---- rows in phase ------------------------------------------------------------------
@@ -295,19 +304,20 @@ __device__ __forceinline__ uint32_t kept_bits(const Mask &m, uint32_t row, uint3
   return bits;
 }
 
-// The kept bits of the block before chunk c (chunk 0: of none).
-__device__ __forceinline__ uint32_t mask_before(const Mask &m, uint32_t row, int c) {
-  return kept_bits(m, row, static_cast<uint32_t>(c * 32 - 1));
+// The kept bits of the block before a row's chunk c (none before its first).
+__device__ __forceinline__ uint32_t kept_before(const Mask &m, uint32_t row, int c) {
+  return c > 0 ? kept_bits(m, row, static_cast<uint32_t>(c * 32 - 1)) : 0;
 }
 
 // drop8 for a lane's unit of a row in phase: its first `phase` elements belong to the
-// block before its lane's.  `before`: lane i's mask_before of the warp's i-th chunk.
+// block before its lane's, lane 0's to the one with the kept bits `before`, which become
+// those before the next chunk.
 __device__ __forceinline__ void drop8_phase(float (&v)[8], const Mask &m, uint32_t row, int c,
-                                            int lane, int phase, uint32_t before, int i) {
+                                            int lane, int phase, uint32_t &before) {
   const uint32_t own = kept_bits(m, row, static_cast<uint32_t>(c * 32 + lane));
   uint32_t prev = __shfl_up_sync(0xffffffffu, own, 1);
-  const uint32_t first = __shfl_sync(0xffffffffu, before, i);
-  if (lane == 0) prev = first;
+  if (lane == 0) prev = before;
+  before = __shfl_sync(0xffffffffu, own, 31);
   const uint32_t bits = (prev | own << 8) >> (8 - phase);
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = bits >> j & 1u ? v[j] * m.factor : 0.0f;

@@ -197,7 +197,10 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
   uint32_t row = begin + classes * (threadIdx.y * per + sub);
   const int rounds = begin < rows ? static_cast<int>((rows - begin - 1) / hop + 1) : 0;
   const int phase = EXACT ? 0 : static_cast<int>((cls * a.ld_h) & 7);
-  const int col0 = warp * kChunk + at * 8 - phase;  // of the first unit; the next is W chunks on
+  // a lane's first unit, and columns from one to the next (inexact rows: a warp's chunks
+  // follow one another, as their mask goes on from each to the next)
+  const int chunk0 = EXACT ? warp : warp * NU, chunk_step = EXACT ? W : 1;
+  const int col0 = chunk0 * kChunk + at * 8 - phase, unit_cols = chunk_step * kChunk;
 
   const int row_bytes = NU * T * 16, input_bytes = RP * row_bytes;
   const int stage_bytes = (up ? 3 : 2) * input_bytes;
@@ -208,12 +211,12 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
     const char *src = static_cast<const char *>(m) + (r * ld + col0) * 2;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const int left = cols - (col0 + i * W * kChunk);
+      const int left = cols - (col0 + i * unit_cols);
       if (EXACT || left >= 8) {
         if (EXACT && lg < 5 && at * 8 >= cols) continue;
-        cp_async_16(dst + i * (T * 16), src + i * W * (2 * kChunk));
+        cp_async_16(dst + i * (T * 16), src + i * 2 * unit_cols);
       } else if (left > 0) {
-        cp_async_16_part(dst + i * (T * 16), src + i * W * (2 * kChunk), 2 * left);
+        cp_async_16_part(dst + i * (T * 16), src + i * 2 * unit_cols, 2 * left);
       }
     }
   };
@@ -238,7 +241,7 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
     Lane8<false> v;
     v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
     if constexpr (!EXACT) {
-      const int col = col0 + i * W * kChunk;
+      const int col = col0 + i * unit_cols;
       if (col < 0 || col + 8 > cols) v.clip(-col, cols - col);
     } else if (lg < 5 && at * 8 >= cols) {
       v.zero();
@@ -253,7 +256,7 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
   for (int i = 0; i < NU; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int col = col0 + i * W * kChunk + 2 * j;
+      const int col = col0 + i * unit_cols + 2 * j;
       g[i][j] = pack_f32x2(col >= 0 && col < cols ? ld_keep_f32(a.gamma + col) : 0.0f,
                            col >= -1 && col + 1 < cols ? ld_keep_f32(a.gamma + col + 1) : 0.0f);
       acc[i][j] = 0;
@@ -324,12 +327,12 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
       if (r >= rows) break;
       const float b = -(dot[p] * over * rstd[p]) * rstd[p] * rstd[p];
       const uint64_t rstd2 = pack_f32x2(rstd[p], rstd[p]), b2 = pack_f32x2(b, b);
-      uint32_t edge = 0;
-      if (!EXACT && drop) edge = mask_before(mask, r, lane * W + warp);
+      uint32_t before = 0;
+      if (!EXACT && drop) before = kept_before(mask, r, chunk0);
       char *const out_x = row_of<false>(a.dx, r, a.ld_dx), *const out_r = row_of<false>(a.dres, r, a.ld_dres);
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
-        const int c = i * W + warp, col = col0 + i * W * kChunk;
+        const int c = chunk0 + i * chunk_step, col = col0 + i * unit_cols;
         if (!EXACT && c * kChunk - phase >= cols) continue;
         const Lane8<false> dy = unit(0, p, i), h = unit(1, p, i);
         Lane8<false> dh{};
@@ -351,7 +354,7 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
             out.set(d);
             store_unit<false, !EXACT>(out_r, col, bound, out);
           }
-          if constexpr (!EXACT) drop8_phase(d, mask, r, c, lane, phase, edge, i);
+          if constexpr (!EXACT) drop8_phase(d, mask, r, c, lane, phase, before);
           else drop8<true>(d, mask, r, c, at);
         }
         out.set(d);
@@ -376,7 +379,7 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
       for (int j = 0; j < 8; ++j) {
         float v = j & 1 ? f32x2_hi(acc[i][j >> 1]) : f32x2_lo(acc[i][j >> 1]);
         for (int o = 16; o >= 1 << lg; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        const int col = col0 + i * W * kChunk + j;
+        const int col = col0 + i * unit_cols + j;
         if (sub != 0 || col < 0 || col >= cols) continue;
         if (y > 0) v += sums[col];
         if (y + 1 < R) sums[col] = v;
