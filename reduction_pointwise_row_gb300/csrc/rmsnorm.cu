@@ -15,6 +15,30 @@ namespace {
 constexpr float kE4m3Max = 448.0f;
 constexpr int kGroup = FR_SCALE_COLS;  // columns of a scale in groups
 
+// v = h k gamma for a lane's 8 elements.
+template <bool F32>
+__device__ __forceinline__ void normed8(float (&v)[8], const Lane8<F32> &h, float k, const float (&g)[8]) {
+  const uint64_t k2 = pack_f32x2(k, k);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t x = mul_f32x2(mul_f32x2(pack_f32x2(h.at(2 * i), h.at(2 * i + 1)), k2),
+                                 pack_f32x2(g[2 * i], g[2 * i + 1]));
+    v[2 * i] = f32x2_lo(x);
+    v[2 * i + 1] = f32x2_hi(x);
+  }
+}
+
+// s + the squares of a lane's 8 elements, the even and the odd ones apart.
+template <bool F32>
+__device__ __forceinline__ uint64_t squares8(const Lane8<F32> &h, uint64_t s) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t x = pack_f32x2(h.at(2 * i), h.at(2 * i + 1));
+    s = fma_f32x2(x, x, s);
+  }
+  return s;
+}
+
 // Two values to e4m3, to nearest even, past the largest to it; lo in the low byte.
 __device__ __forceinline__ uint16_t pack_e4m3x2(float lo, float hi) {
   uint16_t d;
@@ -22,15 +46,24 @@ __device__ __forceinline__ uint16_t pack_e4m3x2(float lo, float hi) {
   return d;
 }
 
+// 8 values to e4m3, the first four times inv[0], the others times inv[1].
+__device__ __forceinline__ void e4m3_8(uint32_t (&w)[2], const float (&v)[8], const float (&inv)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t k = pack_f32x2(inv[i], inv[i]);
+    const uint64_t a = mul_f32x2(pack_f32x2(v[4 * i], v[4 * i + 1]), k);
+    const uint64_t b = mul_f32x2(pack_f32x2(v[4 * i + 2], v[4 * i + 3]), k);
+    w[i] = pack_e4m3x2(f32x2_lo(a), f32x2_hi(a)) |
+           static_cast<uint32_t>(pack_e4m3x2(f32x2_lo(b), f32x2_hi(b))) << 16;
+  }
+}
+
 // A lane's 8 values times inv, in 8 bits.
 template <bool VEC>
 __device__ __forceinline__ void store8_e4m3(void *row, int c, int lane, int cols,
                                             const float (&v)[8], const float (&inv)[2]) {
   uint32_t w[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    w[i] = pack_e4m3x2(v[4 * i] * inv[i], v[4 * i + 1] * inv[i]) |
-           static_cast<uint32_t>(pack_e4m3x2(v[4 * i + 2] * inv[i], v[4 * i + 3] * inv[i])) << 16;
+  e4m3_8(w, v, inv);
   if constexpr (VEC) {
     const int col = c * kChunk + lane * 8;
     if (col < cols)
@@ -54,10 +87,7 @@ __device__ __forceinline__ void store8_e4m3(void *row, int c, int lane, int cols
 __device__ __forceinline__ void store_unit_e4m3(char *row, int col, int cols, const float (&v)[8],
                                                 const float (&inv)[2]) {
   uint32_t w[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    w[i] = pack_e4m3x2(v[4 * i] * inv[i], v[4 * i + 1] * inv[i]) |
-           static_cast<uint32_t>(pack_e4m3x2(v[4 * i + 2] * inv[i], v[4 * i + 3] * inv[i])) << 16;
+  e4m3_8(w, v, inv);
   if (col >= 0 && col + 8 <= cols) {
     asm volatile("st.global.cs.v2.b32 [%0], {%1, %2};" ::"l"(row + col), "r"(w[0]), "r"(w[1]) : "memory");
     return;
@@ -77,7 +107,7 @@ __device__ __forceinline__ float warp_max(float v) {
 // The scale for values whose largest magnitude is `most` (NaN stays): never below
 // the smallest normal, so that its reciprocal is finite and rows of zeros give zeros.
 __device__ __forceinline__ float scale_for(float most) {
-  return max_nan(most / kE4m3Max, 1.17549435e-38f);
+  return max_nan(most * (1.0f / kE4m3Max), 1.17549435e-38f);
 }
 
 // A chunk of y in 8 bits with a scale per 128 columns: two scales a chunk.  Aligned
@@ -186,6 +216,7 @@ rmsnorm_held(NormForward a) {
   const bool live = row < a.rows;
   const bool with_max = QUANT && a.scale_mode == FR_SCALE_ROW;
   float ss = 0.0f, most = 0.0f;
+  uint64_t squares = 0;
   Lane8<F32> h[NU];
   if (live) {
     const char *xr = row_of<F32>(a.x, row, a.ldx);
@@ -211,14 +242,19 @@ rmsnorm_held(NormForward a) {
     for (int i = 0; i < NU; ++i) {
       float g[8];
       if (with_max) load_cols8<VEC>(g, a.gamma, i * W + warp, lane, cols);
+      if constexpr (NU < 8) {
+        squares = squares8(h[i], squares);  // 0 past the row
+      } else {  // (a register fewer: 64 suffice)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {  // 0 past the row
-        const float v = h[i].at(j);
-        ss = fmaf(v, v, ss);
-        if (with_max) most = max_nan(most, fabsf(v * g[j]));
+        for (int j = 0; j < 8; ++j) ss = fmaf(h[i].at(j), h[i].at(j), ss);
+      }
+      if (with_max) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) most = max_nan(most, fabsf(h[i].at(j) * g[j]));
       }
     }
   }
+  if constexpr (NU < 8) ss = f32x2_lo(squares) + f32x2_hi(squares);
   row_reduce(ss, most, with_max, W, red);
   if (!live) return;
   const float rstd = 1.0f / sqrtf(ss / static_cast<float>(cols) + a.eps);
@@ -236,8 +272,7 @@ rmsnorm_held(NormForward a) {
     if (c * kChunk >= cols) continue;
     float v[8], g[8];
     load_cols8<VEC>(g, a.gamma, c, lane, cols);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = h[i].at(j) * rstd * g[j];
+    normed8(v, h[i], rstd, g);
     if constexpr (QUANT) {
       if (a.scale_mode == FR_SCALE_GROUP) store_groups<VEC>(a, row, yr, c, lane, v);
       else store8_e4m3<VEC>(yr, c, lane, cols, v, inv);
@@ -274,10 +309,9 @@ __global__ void __launch_bounds__(kLoopThreads) rmsnorm_looped(NormForward a) {
         block_sum<F32, VEC>(a, mask, static_cast<uint32_t>(row), c, lane, x, res);
         store8<F32, VEC>(hr, c, lane, cols, x);
       }
-      float part = 0.0f;  // a short run of its own: long rows add chunk sums, not elements
-#pragma unroll
-      for (int j = 0; j < 8; ++j) part = fmaf(x.at(j), x.at(j), part);
-      ss += part;
+      // a short run of its own: long rows add chunk sums, not elements
+      const uint64_t part = squares8(x, 0);
+      ss += f32x2_lo(part) + f32x2_hi(part);
       if (QUANT && a.scale_mode == FR_SCALE_ROW) {
         float g[8];
         load_cols8<VEC>(g, a.gamma, c, lane, cols);
@@ -300,8 +334,7 @@ __global__ void __launch_bounds__(kLoopThreads) rmsnorm_looped(NormForward a) {
       const Lane8<F32> x = load8<F32, VEC, true>(again, c, lane, cols);
       float v[8], g[8];
       load_cols8<VEC>(g, a.gamma, c, lane, cols);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = x.at(j) * rstd * g[j];
+      normed8(v, x, rstd, g);
       if constexpr (QUANT) {
         if (a.scale_mode == FR_SCALE_GROUP) store_groups<VEC>(a, row, yr, c, lane, v);
         else store8_e4m3<VEC>(yr, c, lane, cols, v, inv);
@@ -330,7 +363,8 @@ rmsnorm_phase(NormForward a) {
   const bool with_max = QUANT && a.scale_mode == FR_SCALE_ROW;
   const int phase = static_cast<int>(row * a.ldx & 7);
   const int col0 = warp * NU * kChunk + lane * 8 - phase;  // a warp's chunks follow one another
-  float ss = 0.0f, most = 0.0f;
+  float most = 0.0f;
+  uint64_t squares = 0;
   Lane8<false> h[NU];
   if (live) {
     const char *xr = row_of<false>(a.x, row, a.ldx);
@@ -363,14 +397,14 @@ rmsnorm_phase(NormForward a) {
       if (col < 0 || col + 8 > cols) h[i].clip(-col, cols - col);
       float g[8];
       if (with_max) load_cols_unit(g, a.gamma, col, cols);
+      squares = squares8(h[i], squares);
+      if (with_max) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float v = h[i].at(j);
-        ss = fmaf(v, v, ss);
-        if (with_max) most = max_nan(most, fabsf(v * g[j]));
+        for (int j = 0; j < 8; ++j) most = max_nan(most, fabsf(h[i].at(j) * g[j]));
       }
     }
   }
+  float ss = f32x2_lo(squares) + f32x2_hi(squares);
   row_reduce(ss, most, with_max, W, red);
   if (!live) return;
   const float rstd = 1.0f / sqrtf(ss / static_cast<float>(cols) + a.eps);
@@ -388,8 +422,7 @@ rmsnorm_phase(NormForward a) {
     if (col >= cols) continue;
     float v[8], g[8];
     load_cols_unit(g, a.gamma, col, cols);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = h[i].at(j) * rstd * g[j];
+    normed8(v, h[i], rstd, g);
     if constexpr (QUANT) {
       store_unit_e4m3(yr, col, cols, v, inv);
     } else {
@@ -437,17 +470,19 @@ __global__ void __launch_bounds__(256) rmsnorm_short(NormForward a, int lg) {
   }
   float g[8];
   load_cols8<true>(g, a.gamma, 0, at, cols);
+  const float over = 1.0f / static_cast<float>(cols);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t row = first + u * per;
     const bool live = row < a.rows;
-    float v[8], ss = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(h[u].at(j), h[u].at(j), ss);
+    float v[8];
+    const uint64_t squares = squares8(h[u], 0);
+    float ss = f32x2_lo(squares) + f32x2_hi(squares);
     for (int o = 1 << lg >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float rstd = 1.0f / sqrtf(ss / static_cast<float>(cols) + a.eps);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = h[u].at(j) * rstd * g[j];
+    // (an exact root and reciprocal are a large part of a short row's work; the
+    // approximate ones, off by 2 units in the last place, cost less than its few additions)
+    const float rstd = rsqrtf(fmaf(ss, over, a.eps));
+    normed8(v, h[u], rstd, g);
     if (live && a.rstd != nullptr && at == 0) a.rstd[row] = rstd;
     if constexpr (QUANT) {
       char *yr = static_cast<char *>(a.y) + row * a.ldy;
@@ -580,7 +615,7 @@ cudaError_t launch_short(const NormForward &a, cudaStream_t s) {
 template <bool F32, bool VEC, bool QUANT, bool SUM>
 cudaError_t launch_held(const NormForward &a, int sm_count, cudaStream_t s) {
   const int chunks = static_cast<int>((a.cols + kChunk - 1) / kChunk);
-  int units = F32 ? 2 : !VEC ? 3 : SUM || chunks <= 32 ? 4 : 8;
+  int units = F32 ? 2 : !VEC ? (QUANT ? 2 : 3) : SUM || chunks <= 32 ? 4 : 8;
   if (units == 3 && chunks > 3 * kHeldThreads<3> / 32) units = 2;
   if (chunks < units) units = chunks;
   if (a.rows < sm_count && chunks <= 32) units = 1;  // few rows: latency
@@ -588,7 +623,8 @@ cudaError_t launch_held(const NormForward &a, int sm_count, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((a.rows + R - 1) / R)), block(32 * W, R);
   if (units == 1) return launch_k(rmsnorm_held<F32, VEC, 1, SUM, QUANT>, grid, block, 0, s, 0, a);
   if constexpr (!F32) {
-    if (units == 3) return launch_k(rmsnorm_held<F32, VEC, 3, SUM, QUANT>, grid, block, 0, s, 0, a);
+    if constexpr (VEC || !QUANT)
+      if (units == 3) return launch_k(rmsnorm_held<F32, VEC, 3, SUM, QUANT>, grid, block, 0, s, 0, a);
     if constexpr (VEC) {
       if (units == 4) return launch_k(rmsnorm_held<F32, VEC, 4, SUM, QUANT>, grid, block, 0, s, 0, a);
       if constexpr (!SUM)
