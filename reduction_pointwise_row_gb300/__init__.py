@@ -697,46 +697,67 @@ def fr_xent_backward(logits, target, dloss, ignore_index: int = -100, want_loss:
 
 # ---- a residual block's row operators: dropout, root-mean-square norm ------------
 #
-# Small calls are bound by the host, so a call looks at each tensor once and enters a
-# context only for a given `stream` (fr_rmsnorm of one row: 16.0 us, 18.9 before; 3.8 of
-# it the library's call, 2.4 each output's allocation).
+# Small calls are bound by the host, so a call looks at each tensor once, mostly inline,
+# and enters a context only for a given `stream` (fr_rmsnorm of one row: 15.4 us, 18.9 before; 3.7
+# of it the library's call, about 2 each output's allocation).
 
 
-def _like(t, x, ld: int, name: str) -> int:
+def _device_of(x) -> int:
+    """x's device, which has to be the current one (the library launches there)."""
+    dev = x.get_device()
+    if _current_device is None:
+        _stream()  # resolves the lookup
+    if dev != _current_device():
+        _on_current_device(x)
+    return dev
+
+
+def _like(t, x, ld: int, dev: int, name: str) -> int:
     """The row stride of a matrix that has to have x's shape, dtype and device."""
-    if t.shape == x.shape and t.dtype is x.dtype and t.is_cuda:
-        if t.stride() == x.stride():
-            return ld
-        return _logits_arg(t, name)[2]
+    if t.dtype is x.dtype and t.shape == x.shape and t.is_cuda:
+        if t.get_device() != dev:
+            _on_current_device(t)
+        return ld if t.stride() == x.stride() else _logits_arg(t, name)[2]
     raise ValueError(f"{name} must be on CUDA and have the first matrix's shape and dtype")
 
 
-def _rng_ptr(p: float, rng, site: int):
-    """The address of a call's {seed, offset}; None without dropout."""
-    if not 0.0 <= p <= 1.0:
-        raise ValueError("p must be 0 to 1")
-    if not -2**63 <= site < 2**63:
-        raise ValueError("site must fit 64 bits")
-    if p == 0.0:
-        return None
-    if rng is None or not rng.is_cuda or rng.dtype is not _TORCH.int64 or rng.shape != (2,) or \
-            not rng.is_contiguous():
-        raise ValueError("rng must be a contiguous CUDA tensor of two int64: seed and offset")
-    return rng.data_ptr()
-
-
-def _vector_ptr(t, n: int, name: str):
+def _vector_ptr(t, n: int, dev: int, name: str) -> int:
     """The address of n contiguous fp32 values."""
-    if t.is_cuda and t.dtype is _TORCH.float32 and t.shape == (n,) and t.is_contiguous():
+    if t.dtype is _TORCH.float32 and t.shape == (n,) and t.is_cuda and t.is_contiguous():
+        if t.get_device() != dev:
+            _on_current_device(t)
         return t.data_ptr()
     raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} fp32 values")
 
 
+def _rng_ptr(p: float, rng, site: int, dev: int):
+    """The address of a call's {seed, offset}; None without dropout."""
+    if not -2**63 <= site < 2**63:
+        raise ValueError("site must fit 64 bits")
+    if p == 0.0:
+        return None
+    if not 0.0 < p <= 1.0:
+        raise ValueError("p must be 0 to 1")
+    if rng is None or not rng.is_cuda or rng.dtype is not _TORCH.int64 or rng.shape != (2,) or \
+            not rng.is_contiguous():
+        raise ValueError("rng must be a contiguous CUDA tensor of two int64: seed and offset")
+    if rng.get_device() != dev:
+        _on_current_device(rng)
+    return rng.data_ptr()
+
+
 def _matrix_out(x, rows: int, cols: int, ld: int):
     """A new compact matrix of x's shape and dtype."""
-    if ld == cols and rows > 1:
+    if ld == cols and x.is_contiguous():
         return _TORCH.empty_like(x)
     return _TORCH.empty((rows, cols), dtype=x.dtype, device=x.device)
+
+
+def _with_stream(call, stream, *args):
+    """The call with `stream` as the current one: what it makes belongs to it."""
+    _torch()
+    with _TORCH.cuda.stream(stream):
+        return call(*args)
 
 
 def fr_dropout(x, p: float, rng, site: int = 0, residual=None, out=None, stream=None):
@@ -748,27 +769,19 @@ def fr_dropout(x, p: float, rng, site: int = 0, residual=None, out=None, stream=
         return _with_stream(fr_dropout, stream, x, p, rng, site, residual, out)
     _TORCH or _torch()
     rows, cols, ld, dt = _logits_arg(x, "x")
-    p_rng = _rng_ptr(p, rng, site)
-    ldr = 0 if residual is None else _like(residual, x, ld, "residual")
+    dev = _device_of(x)
+    p_rng = _rng_ptr(p, rng, site, dev)
+    ldr = 0 if residual is None else _like(residual, x, ld, dev, "residual")
     if out is None:
-        _on_current_device(x, residual, rng)
         out, ldo = _matrix_out(x, rows, cols, ld), cols
     else:
-        ldo = _like(out, x, ld, "out")
-        _on_current_device(x, residual, rng, out)
+        ldo = _like(out, x, ld, dev, "out")
     status = lib().fr_dropout(x.data_ptr(), None if residual is None else residual.data_ptr(),
                               out.data_ptr(), rows, cols, ld, ldr, ldo, p, p_rng, site, dt,
-                              _stream())
+                              _current_raw_stream(dev))
     if status != FR_OK:
         raise FRError(status, "fr_dropout")
     return out
-
-
-def _with_stream(call, stream, *args):
-    """The call with `stream` as the current one: what it makes belongs to it."""
-    _torch()
-    with _TORCH.cuda.stream(stream):
-        return call(*args)
 
 
 def fr_rmsnorm(x, gamma, eps: float = 1e-5, residual=None, p: float = 0.0, rng=None, site: int = 0,
@@ -784,47 +797,50 @@ def fr_rmsnorm(x, gamma, eps: float = 1e-5, residual=None, p: float = 0.0, rng=N
                             out, h, rstd)
     _TORCH or _torch()
     rows, cols, ld, dt = _logits_arg(x, "x")
-    p_gamma = _vector_ptr(gamma, cols, "gamma")
-    p_rng = _rng_ptr(p, rng, site)
+    dev = _device_of(x)
+    p_gamma = _vector_ptr(gamma, cols, dev, "gamma")
+    p_rng = _rng_ptr(p, rng, site, dev)
     ldr = ldh = 0
     ldy = cols
     p_res = p_h = p_rstd = None
     if residual is not None:
-        ldr = _like(residual, x, ld, "residual")
+        ldr = _like(residual, x, ld, dev, "residual")
         p_res = residual.data_ptr()
-    _on_current_device(x, gamma, residual, out, h, rstd, rng)
     if out is None:
         out = _matrix_out(x, rows, cols, ld)
     else:
-        ldy = _like(out, x, ld, "out")
+        ldy = _like(out, x, ld, dev, "out")
     res = {"y": out}
     if p_res is not None or p_rng is not None:
         if h is None:
             h, ldh = _matrix_out(x, rows, cols, ld), cols
         else:
-            ldh = _like(h, x, ld, "h")
+            ldh = _like(h, x, ld, dev, "h")
         p_h = h.data_ptr()
         res["h"] = h
     elif h is not None:
         raise ValueError("h without a residual or dropout: the norm's input is x itself")
     if rstd is not None:
-        p_rstd = _vector_ptr(rstd, rows, "rstd")
+        p_rstd = _vector_ptr(rstd, rows, dev, "rstd")
         res["rstd"] = rstd
     elif want_rstd:
         rstd = res["rstd"] = _TORCH.empty(rows, dtype=_TORCH.float32, device=x.device)
         p_rstd = rstd.data_ptr()
     status = lib().fr_rmsnorm(x.data_ptr(), p_res, p_gamma, p_h, out.data_ptr(), p_rstd, rows, cols, ld,
-                              ldr, ldh, ldy, eps, p, p_rng, site, dt, FORMS[form], _stream())
+                              ldr, ldh, ldy, eps, p, p_rng, site, dt, FORMS[form],
+                              _current_raw_stream(dev))
     if status != FR_OK:
         raise FRError(status, "fr_rmsnorm")
     return res
 
 
-def _scale_strides(t, rows: int, cols: int, groups: int, name: str):
+def _scale_strides(t, rows: int, groups: int, dev: int):
     """(row stride, group stride) of scales [rows] (groups 0) or [rows, groups]."""
     if not t.is_cuda or t.dtype is not _TORCH.float32 or \
             t.shape != ((rows, groups) if groups else (rows,)):
-        raise ValueError(f"{name} must be a CUDA tensor of fp32, one per row (or group)")
+        raise ValueError("scale_out must be a CUDA tensor of fp32, one per row (or group)")
+    if t.get_device() != dev:
+        _on_current_device(t)
     if not groups:
         return t.stride(0) if rows > 1 else 1, 1
     sr, sc = t.stride()
@@ -850,32 +866,27 @@ def fr_rmsnorm_quant(x, gamma, eps: float = 1e-5, scale="row", residual=None, p:
                             want_rstd, form, out, scale_out, h, rstd)
     torch = _TORCH or _torch()
     rows, cols, ld, dt = _logits_arg(x, "x")
-    p_gamma = _vector_ptr(gamma, cols, "gamma")
-    p_rng = _rng_ptr(p, rng, site)
+    dev = _device_of(x)
+    p_gamma = _vector_ptr(gamma, cols, dev, "gamma")
+    p_rng = _rng_ptr(p, rng, site, dev)
     ldr = ldh = 0
     ldy = cols
     p_res = p_h = p_rstd = None
     if residual is not None:
-        ldr = _like(residual, x, ld, "residual")
+        ldr = _like(residual, x, ld, dev, "residual")
         p_res = residual.data_ptr()
-    given = None if isinstance(scale, str) else scale
-    _on_current_device(x, gamma, residual, out, h, rstd, rng, given, scale_out)
     if out is None:
         out = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=x.device)
     else:
         if not out.is_cuda or out.dtype is not torch.float8_e4m3fn or out.shape != x.shape or \
                 (out.stride(1) != 1 and cols != 1):
             raise ValueError("out must be a CUDA matrix of float8_e4m3fn, x's shape")
+        if out.get_device() != dev:
+            _on_current_device(out)
         ldy = cols if rows == 1 else out.stride(0)
     res = {"y": out}
     sr = sc = 1
-    if given is not None:
-        mode = 2
-        _need(scale_out is None, "scale_out with a given scale")
-        _need(given.is_cuda and given.dtype is torch.float32 and given.numel() == 1,
-              "scale must be a CUDA tensor of one fp32 value")
-        p_scale = given.data_ptr()
-    else:
+    if isinstance(scale, str):
         if scale == "row":
             mode, groups = 0, 0
         elif scale == "group":
@@ -884,30 +895,37 @@ def fr_rmsnorm_quant(x, gamma, eps: float = 1e-5, scale="row", residual=None, p:
         else:
             raise ValueError('scale must be "row", "group" or a tensor of one fp32 value')
         if scale_out is None:
-            scale_out = torch.empty((rows, groups) if groups else rows, dtype=torch.float32,
-                                    device=x.device)
+            scale_out = torch.empty((rows, groups) if groups else rows, dtype=torch.float32, device=x.device)
         else:
-            sr, sc = _scale_strides(scale_out, rows, cols, groups, "scale_out")
+            sr, sc = _scale_strides(scale_out, rows, groups, dev)
         p_scale = scale_out.data_ptr()
         res["scale"] = scale_out
+    else:
+        mode = 2
+        _need(scale_out is None, "scale_out with a given scale")
+        _need(scale.is_cuda and scale.dtype is torch.float32 and scale.numel() == 1,
+              "scale must be a CUDA tensor of one fp32 value")
+        if scale.get_device() != dev:
+            _on_current_device(scale)
+        p_scale = scale.data_ptr()
     if p_res is not None or p_rng is not None:
         if h is None:
             h, ldh = _matrix_out(x, rows, cols, ld), cols
         else:
-            ldh = _like(h, x, ld, "h")
+            ldh = _like(h, x, ld, dev, "h")
         p_h = h.data_ptr()
         res["h"] = h
     elif h is not None:
         raise ValueError("h without a residual or dropout: the norm's input is x itself")
     if rstd is not None:
-        p_rstd = _vector_ptr(rstd, rows, "rstd")
+        p_rstd = _vector_ptr(rstd, rows, dev, "rstd")
         res["rstd"] = rstd
     elif want_rstd:
-        rstd = res["rstd"] = torch.empty(rows, dtype=torch.float32, device=x.device)
+        rstd = res["rstd"] = _TORCH.empty(rows, dtype=_TORCH.float32, device=x.device)
         p_rstd = rstd.data_ptr()
     status = lib().fr_rmsnorm_quant(x.data_ptr(), p_res, p_gamma, p_h, out.data_ptr(), p_scale, mode, sr,
                                     sc, p_rstd, rows, cols, ld, ldr, ldh, ldy, eps, p, p_rng, site, dt,
-                                    FORMS[form], _stream())
+                                    FORMS[form], _current_raw_stream(dev))
     if status != FR_OK:
         raise FRError(status, "fr_rmsnorm_quant")
     return res
@@ -930,36 +948,39 @@ def fr_rmsnorm_backward(dy, h, gamma, rstd, dh=None, p: float = 0.0, rng=None, s
                             want_dgamma, want_dresidual, form, dx, dresidual, dgamma, workspace)
     _TORCH or _torch()
     rows, cols, ld, dt = _logits_arg(dy, "dy")
-    ldh = _like(h, dy, ld, "h")
-    p_gamma = _vector_ptr(gamma, cols, "gamma")
-    p_rstd = _vector_ptr(rstd, rows, "rstd")
-    p_rng = _rng_ptr(p, rng, site)
+    dev = _device_of(dy)
+    ldh = _like(h, dy, ld, dev, "h")
+    p_gamma = _vector_ptr(gamma, cols, dev, "gamma")
+    p_rstd = _vector_ptr(rstd, rows, dev, "rstd")
+    p_rng = _rng_ptr(p, rng, site, dev)
     lddh = lddr = 0
     lddx = cols
     p_dh = p_dr = p_dg = None
     if dh is not None:
-        lddh = _like(dh, dy, ld, "dh")
+        lddh = _like(dh, dy, ld, dev, "dh")
         p_dh = dh.data_ptr()
-    if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
-        raise ValueError("workspace must be contiguous CUDA memory")
-    _on_current_device(dy, h, gamma, rstd, dh, dx, dresidual, dgamma, workspace, rng)
+    if workspace is not None:
+        if not (workspace.is_cuda and workspace.is_contiguous()):
+            raise ValueError("workspace must be contiguous CUDA memory")
+        if workspace.get_device() != dev:
+            _on_current_device(workspace)
     if dx is None:
         dx = _matrix_out(dy, rows, cols, ld)
     else:
-        lddx = _like(dx, dy, ld, "dx")
+        lddx = _like(dx, dy, ld, dev, "dx")
     res = {"dx": dx}
     if p_rng is None:
         _need(dresidual is None, "dresidual without dropout is dx")
     else:
         if dresidual is not None:
-            lddr = _like(dresidual, dy, ld, "dresidual")
+            lddr = _like(dresidual, dy, ld, dev, "dresidual")
         elif want_dresidual:
             dresidual, lddr = _matrix_out(dy, rows, cols, ld), cols
         if dresidual is not None:
             p_dr = dresidual.data_ptr()
             res["dresidual"] = dresidual
     if dgamma is not None:
-        p_dg = _vector_ptr(dgamma, cols, "dgamma")
+        p_dg = _vector_ptr(dgamma, cols, dev, "dgamma")
         res["dgamma"] = dgamma
     elif want_dgamma:
         dgamma = res["dgamma"] = _TORCH.empty(cols, dtype=_TORCH.float32, device=dy.device)
@@ -967,7 +988,7 @@ def fr_rmsnorm_backward(dy, h, gamma, rstd, dh=None, p: float = 0.0, rng=None, s
     ws, nws = _workspace("rmsnorm_backward", rows, cols, _DTYPE_NAMES[dt], form, dy.device, workspace)
     status = lib().fr_rmsnorm_backward(dy.data_ptr(), h.data_ptr(), p_gamma, p_rstd, p_dh, dx.data_ptr(),
                                        p_dr, p_dg, rows, cols, ld, ldh, lddh, lddx, lddr, p, p_rng, site,
-                                       dt, FORMS[form], _ptr(ws), nws, _stream())
+                                       dt, FORMS[form], _ptr(ws), nws, _current_raw_stream(dev))
     if status != FR_OK:
         raise FRError(status, "fr_rmsnorm_backward")
     return res

@@ -158,6 +158,10 @@ __global__ void __launch_bounds__(512) rmsnorm_grad_held(NormBackward a) {
     part[col] = sums[col];
 }
 
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
 // bf16 rows in phase (every matrix's row starts at the same element of an 8-element unit;
 // base addresses at its first): the rows' units come through a ring of `stages` stages of
 // RP rows in shared memory by asynchronous 16-byte copies.  A thread reads only what it
@@ -374,17 +378,34 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
     __syncthreads();
     if (static_cast<int>(threadIdx.y) != y) continue;
 #pragma unroll
-    for (int i = 0; i < NU; ++i)
+    for (int i = 0; i < NU; ++i) {
+      float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float v = j & 1 ? f32x2_hi(acc[i][j >> 1]) : f32x2_lo(acc[i][j >> 1]);
-        for (int o = 16; o >= 1 << lg; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        const int col = col0 + i * unit_cols + j;
-        if (sub != 0 || col < 0 || col >= cols) continue;
-        if (y > 0) v += sums[col];
-        if (y + 1 < R) sums[col] = v;
-        else part[col] = v;
+        v[j] = j & 1 ? f32x2_hi(acc[i][j >> 1]) : f32x2_lo(acc[i][j >> 1]);
+        for (int o = 16; o >= 1 << lg; o >>= 1) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
       }
+      const int col = col0 + i * unit_cols;
+      if constexpr (EXACT) {  // 16-byte pieces: a float an access cost 3 us at 8192 columns
+        if (sub != 0 || col >= cols) continue;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float4 w = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          float4 *const at_sums = reinterpret_cast<float4 *>(sums + col + 4 * q);
+          if (y > 0) w = add4(w, *at_sums);
+          if (y + 1 < R) *at_sums = w;
+          else *reinterpret_cast<float4 *>(part + col + 4 * q) = w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (col + j >= 0 && col + j < cols) sums[col + j] = y == 0 ? v[j] : sums[col + j] + v[j];
+      }
+    }
+  }
+  if constexpr (!EXACT) {
+    __syncthreads();
+    for (int col = tid; col < cols; col += T) part[col] = sums[col];
   }
 }
 
@@ -450,15 +471,22 @@ __global__ void __launch_bounds__(256) rmsnorm_grad_cols(NormBackward a, const f
     store_cols8<VEC>(partial + static_cast<int64_t>(blockIdx.y) * cols, c, lane, cols, acc);
 }
 
-// dgamma: the sum of P shares of each column.  32 columns a CTA, 32 runs of shares.
+// dgamma: the sum of P shares of each column.  32 columns a CTA, 32 runs of shares; a
+// thread's loads are in flight together (one after the other: 4 us more with 152 shares).
 __global__ void __launch_bounds__(1024) rmsnorm_grad_join(const float *partial, float *dgamma,
                                                           int P, int64_t cols) {
   pdl_enter();
   __shared__ float red[32][33];
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
   float s = 0.0f;
-  if (col < cols)
-    for (int p = threadIdx.y; p < P; p += 32) s += ld_keep_f32(partial + p * cols + col);
+  for (int p = threadIdx.y; p < P; p += 32 * 8) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = col < cols && p + 32 * i < P ? ld_keep_f32(partial + (p + 32 * i) * cols + col) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += v[i];
+  }
   red[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   s = warp_sum(red[threadIdx.x][threadIdx.y]);
