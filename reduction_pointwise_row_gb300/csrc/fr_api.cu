@@ -1011,14 +1011,14 @@ bool rows_of_8(const Matrix &m, int64_t rows) {
   return m.p == nullptr || (aligned(m.p, 8 * m.es) && (m.ld % 8 == 0 || rows == 1));
 }
 
-// True when the matrices start at multiples of 8 elements and any row of them starts at
-// the same place modulo 8.
-bool rows_in_phase(const std::initializer_list<Matrix> &ms, int64_t rows) {
+// True when the matrices start at multiples of `unit` elements and any row of them starts
+// at the same place modulo `unit`.
+bool rows_in_phase(const std::initializer_list<Matrix> &ms, int64_t rows, int unit) {
   int64_t ld = -1;
   for (const Matrix &m : ms) {
     if (!m.p) continue;
-    if (!aligned(m.p, 8 * m.es) || (ld >= 0 && rows > 1 && m.ld % 8 != ld)) return false;
-    ld = m.ld % 8;
+    if (!aligned(m.p, unit * m.es) || (ld >= 0 && rows > 1 && m.ld % unit != ld)) return false;
+    ld = m.ld % unit;
   }
   return true;
 }
@@ -1085,7 +1085,7 @@ fr_status run_rmsnorm(fr::NormForward &a, fr_dtype dtype, bool quant, float p, c
   const fr_form f = form == FR_FORM_AUTO ? pick_rmsnorm(a.cols) : form;
   const bool vec = a.cols % 8 == 0 && aligned(a.gamma, 16) && rows_of_8(x, a.rows) &&
                    rows_of_8(res, a.rows) && rows_of_8(h, a.rows) && rows_of_8(y, a.rows);
-  const bool phase = aligned(a.gamma, 16) && rows_in_phase({x, res, h, y}, a.rows);
+  const bool phase = aligned(a.gamma, 16) && rows_in_phase({x, res, h, y}, a.rows, 8);
   return launched(fr::launch_rmsnorm(a, dtype == FR_F32, vec, phase, quant, f == FR_FORM_PERSISTENT,
                                      info.sm_count, reinterpret_cast<cudaStream_t>(stream)),
                   f);
@@ -1115,7 +1115,7 @@ fr_status fr_dropout(const void *x, const void *residual, void *y, int64_t rows,
   a.ldr = ldr;
   a.ldh = ldy;
   const bool vec = cols % 8 == 0 && rows_of_8(mx, rows) && rows_of_8(mr, rows) && rows_of_8(my, rows);
-  return fr::launch_dropout(a, dtype == FR_F32, vec, rows_in_phase({mx, mr, my}, rows), info.sm_count,
+  return fr::launch_dropout(a, dtype == FR_F32, vec, rows_in_phase({mx, mr, my}, rows, 8), info.sm_count,
                             reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FR_OK
              : FR_ERR_CUDA;
@@ -1180,7 +1180,7 @@ fr_status fr_rmsnorm_backward(const void *dy, const void *h, const float *gamma,
     if (!workspace || workspace_bytes < need) return FR_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned(workspace, 16)) return FR_ERR_MISALIGNED;
   }
-  const bool phase = rows_in_phase({mdy, mh, mdh, mdx, mdr}, rows);
+  const bool phase = rows_in_phase({mdy, mh, mdh, mdx, mdr}, rows, 16 / es);
   return launched(fr::launch_rmsnorm_backward(a, f32, vec, phase, held, info.sm_count,
                                               info.max_smem_optin,
                                               reinterpret_cast<cudaStream_t>(stream)),

@@ -319,8 +319,8 @@ struct NormBackward {
 // True when a row fits the registers of a CTA (vec: the rows are aligned).
 bool rmsnorm_grad_held_ok(int64_t cols, bool f32, bool vec);
 size_t rmsnorm_grad_workspace(int64_t rows, int64_t cols, bool f32, bool held, int sm_count);
-// phase: every matrix starts at a multiple of 8 elements and their row strides agree
-// modulo 8.
+// phase: every matrix starts at a multiple of 16 bytes and their row strides agree modulo
+// 16 bytes.
 cudaError_t launch_rmsnorm_backward(const NormBackward &a, bool f32, bool vec, bool phase, bool held,
                                     int sm_count, int smem_max, cudaStream_t s);
 

@@ -323,4 +323,84 @@ __device__ __forceinline__ void drop8_phase(float (&v)[8], const Mask &m, uint32
   for (int j = 0; j < 8; ++j) v[j] = bits >> j & 1u ? v[j] * m.factor : 0.0f;
 }
 
+// ---- 16-byte units ------------------------------------------------------------------
+// A lane's 16 bytes of a row: E = 8 elements of bf16, 4 of fp32.
+template <bool F32>
+struct Unit {
+  static constexpr int E = F32 ? 4 : 8;
+  uint32_t w[4];
+  __device__ __forceinline__ uint64_t pair(int k) const {  // elements 2 k and 2 k + 1
+    if constexpr (F32) return pack_u32x2(w[2 * k], w[2 * k + 1]);
+    else return pack_f32x2(bf16_lo(w[k]), bf16_hi(w[k]));
+  }
+  __device__ __forceinline__ void set(const float (&v)[E]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (F32) w[i] = __float_as_uint(v[i]);
+      else w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    }
+  }
+  // elements before `lo` and from `hi` on become 0
+  __device__ __forceinline__ void clip(int lo, int hi) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      if (j >= lo && j < hi) continue;
+      if constexpr (F32) w[j] = 0;
+      else w[j >> 1] &= (j & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+    }
+  }
+  // writes the elements from column `col` of `row` on that are within it; WHOLE: all are
+  // or none
+  template <bool WHOLE>
+  __device__ __forceinline__ void store(char *row, int col, int cols) const {
+    constexpr int ES = 16 / E;
+    if (col >= cols) return;
+    char *p = row + static_cast<int64_t>(col) * ES;
+    if (WHOLE || (col >= 0 && col + E <= cols)) {
+      st_stream_u4(p, make_uint4(w[0], w[1], w[2], w[3]));
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      if (col + j < 0 || col + j >= cols) continue;
+      if constexpr (F32) st_stream_f32(reinterpret_cast<float *>(p) + j, __uint_as_float(w[j]));
+      else st_stream_u16(p + 2 * j, static_cast<uint16_t>((j & 1) ? w[j >> 1] >> 16 : w[j >> 1]));
+    }
+  }
+};
+
+// Which of a row's elements E k .. E k + E - 1 stay, bit by bit.
+template <int E>
+__device__ __forceinline__ uint32_t kept_group(const Mask &m, uint32_t row, int k) {
+  if constexpr (E == 8) return kept_bits(m, row, static_cast<uint32_t>(k));
+  return kept_bits(m, row, static_cast<uint32_t>(k >> 1)) >> (4 * (k & 1)) & 15u;
+}
+
+// Dropout of a lane's unit of aligned rows, group k of its row.
+template <int E>
+__device__ __forceinline__ void drop_unit(float (&v)[E], const Mask &m, uint32_t row, int k) {
+  if constexpr (E == 8) {
+    drop8<true>(v, m, row, k >> 5, k & 31);
+  } else {
+    const uint32_t bits = kept_group<E>(m, row, k);
+#pragma unroll
+    for (int j = 0; j < E; ++j) v[j] = bits >> j & 1u ? v[j] * m.factor : 0.0f;
+  }
+}
+
+// The same for rows in phase, the lanes of a warp holding groups k after one another: a
+// lane's first `phase` elements belong to the group before its own, lane 0's to the one
+// with the kept bits `before`, which become those of lane 31's.
+template <int E>
+__device__ __forceinline__ void drop_unit_phase(float (&v)[E], const Mask &m, uint32_t row, int k,
+                                                int lane, int phase, uint32_t &before) {
+  const uint32_t own = kept_group<E>(m, row, k);
+  uint32_t prev = __shfl_up_sync(0xffffffffu, own, 1);
+  if (lane == 0) prev = before;
+  before = __shfl_sync(0xffffffffu, own, 31);
+  const uint32_t bits = (prev | own << E) >> (E - phase);
+#pragma unroll
+  for (int j = 0; j < E; ++j) v[j] = bits >> j & 1u ? v[j] * m.factor : 0.0f;
+}
+
 }  // namespace fr

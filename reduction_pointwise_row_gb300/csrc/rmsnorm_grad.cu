@@ -162,8 +162,8 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
-// bf16 rows in phase (every matrix's row starts at the same element of an 8-element unit;
-// base addresses at its first): the rows' units come through a ring of `stages` stages of
+// Rows in phase (every matrix's row starts at the same element of a 16-byte unit; base
+// addresses at its first): the rows' units come through a ring of `stages` stages of
 // RP rows in shared memory by asynchronous 16-byte copies.  A thread reads only what it
 // copied, so the ring needs no barrier, and the copies of the next rows are in flight
 // while a row is reduced and written.  blockDim = (32 W, R), R groups of RP rows at a time,
@@ -171,7 +171,7 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
 // u = dy gamma, the gradient is dh + rstd dy gamma - (rstd^2 mean) h: paired fp32
 // arithmetic, two fused steps a pair.
 //
-// EXACT: aligned rows of 256 NU W columns (or short ones).  Otherwise a row may start
+// EXACT: aligned rows of 32 NU W units (or short ones).  Otherwise a row may start
 // within a unit and end within one: a CTA takes rows that start at one such place (phase),
 // so that its threads' columns stay the same.  The first and last unit of such a row
 // hold elements of its neighbours (or nothing, which the copy leaves out past the matrix's
@@ -181,9 +181,10 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
 template <bool EXACT, int NU>
 constexpr int kRingWarps = EXACT || NU <= 2 ? 16 : 12;
 
-template <bool EXACT, int NU, int RP>
+template <bool F32, bool EXACT, int NU, int RP>
 __global__ void __launch_bounds__(kRingWarps<EXACT, NU> * 32, 1)
 rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
+  constexpr int E = Unit<F32>::E, ES = 16 / E, kUnits = 32 * E;  // columns of a warp's unit
   pdl_enter();
   __shared__ float red[2][16][RP][16];  // [round & 1][row group][row][warp]
   extern __shared__ __align__(16) unsigned char ring[];
@@ -200,11 +201,11 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
   const uint32_t begin = cls + classes * per * R * RP * (blockIdx.x / classes);
   uint32_t row = begin + classes * (threadIdx.y * per + sub);
   const int rounds = begin < rows ? static_cast<int>((rows - begin - 1) / hop + 1) : 0;
-  const int phase = EXACT ? 0 : static_cast<int>((cls * a.ld_h) & 7);
+  const int phase = EXACT ? 0 : static_cast<int>((cls * a.ld_h) & (E - 1));
   // a lane's first unit, and columns from one to the next (inexact rows: a warp's chunks
   // follow one another, as their mask goes on from each to the next)
   const int chunk0 = EXACT ? warp : warp * NU, chunk_step = EXACT ? W : 1;
-  const int col0 = chunk0 * kChunk + at * 8 - phase, unit_cols = chunk_step * kChunk;
+  const int col0 = chunk0 * kUnits + at * E - phase, unit_cols = chunk_step * kUnits;
 
   const int row_bytes = NU * T * 16, input_bytes = RP * row_bytes;
   const int stage_bytes = (up ? 3 : 2) * input_bytes;
@@ -212,15 +213,15 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
   const uint32_t base = smem_addr(ring) + tid * 16, end = base + stages * stage_bytes;
   uint32_t into = base;
   const auto copy_row = [&](const void *m, int64_t ld, uint32_t r, uint32_t dst) {
-    const char *src = static_cast<const char *>(m) + (r * ld + col0) * 2;
+    const char *src = static_cast<const char *>(m) + (r * ld + col0) * ES;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       const int left = cols - (col0 + i * unit_cols);
-      if (EXACT || left >= 8) {
-        if (EXACT && lg < 5 && at * 8 >= cols) continue;
-        cp_async_16(dst + i * (T * 16), src + i * 2 * unit_cols);
+      if (EXACT || left >= E) {
+        if (EXACT && lg < 5 && at * E >= cols) continue;
+        cp_async_16(dst + i * (T * 16), src + i * ES * unit_cols);
       } else if (left > 0) {
-        cp_async_16_part(dst + i * (T * 16), src + i * 2 * unit_cols, 2 * left);
+        cp_async_16_part(dst + i * (T * 16), src + i * ES * unit_cols, ES * left);
       }
     }
   };
@@ -242,24 +243,23 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
   // a lane's unit i of row p of input n of the stage at `slot`
   const auto unit = [&](int n, int p, int i) {
     const uint4 u = lds_u4(slot + n * input_bytes + p * row_bytes + i * (T * 16));
-    Lane8<false> v;
+    Unit<F32> v;
     v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
     if constexpr (!EXACT) {
       const int col = col0 + i * unit_cols;
-      if (col < 0 || col + 8 > cols) v.clip(-col, cols - col);
-    } else if (lg < 5 && at * 8 >= cols) {
-      v.zero();
+      if (col < 0 || col + E > cols) v.clip(-col, cols - col);
+    } else if (lg < 5 && at * E >= cols) {
+      v.w[0] = v.w[1] = v.w[2] = v.w[3] = 0;
     }
     return v;
   };
-  const auto pair = [](uint32_t w) { return pack_f32x2(bf16_lo(w), bf16_hi(w)); };
 
   for (int k = 0; k < stages - 1; ++k) issue();
-  uint64_t g[NU][4], acc[NU][4];
+  uint64_t g[NU][E / 2], acc[NU][E / 2];
 #pragma unroll
   for (int i = 0; i < NU; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < E / 2; ++j) {
       const int col = col0 + i * unit_cols + 2 * j;
       g[i][j] = pack_f32x2(col >= 0 && col < cols ? ld_keep_f32(a.gamma + col) : 0.0f,
                            col >= -1 && col + 1 < cols ? ld_keep_f32(a.gamma + col + 1) : 0.0f);
@@ -288,10 +288,10 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
       if (row + p * next < rows) {
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
-          const Lane8<false> dy = unit(0, p, i), h = unit(1, p, i);
+          const Unit<F32> dy = unit(0, p, i), h = unit(1, p, i);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            s = fma_f32x2(mul_f32x2(pair(dy.w[j]), g[i][j]), pair(h.w[j]), s);
+          for (int j = 0; j < E / 2; ++j)
+            s = fma_f32x2(mul_f32x2(dy.pair(j), g[i][j]), h.pair(j), s);
         }
       }
       dot[p] = f32x2_lo(s) + f32x2_hi(s);
@@ -332,37 +332,37 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
       const float b = -(dot[p] * over * rstd[p]) * rstd[p] * rstd[p];
       const uint64_t rstd2 = pack_f32x2(rstd[p], rstd[p]), b2 = pack_f32x2(b, b);
       uint32_t before = 0;
-      if (!EXACT && drop) before = kept_before(mask, r, chunk0);
-      char *const out_x = row_of<false>(a.dx, r, a.ld_dx), *const out_r = row_of<false>(a.dres, r, a.ld_dres);
+      if (!EXACT && drop && chunk0 > 0) before = kept_group<E>(mask, r, chunk0 * 32 - 1);
+      char *const out_x = row_of<F32>(a.dx, r, a.ld_dx), *const out_r = row_of<F32>(a.dres, r, a.ld_dres);
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         const int c = chunk0 + i * chunk_step, col = col0 + i * unit_cols;
-        if (!EXACT && c * kChunk - phase >= cols) continue;
-        const Lane8<false> dy = unit(0, p, i), h = unit(1, p, i);
-        Lane8<false> dh{};
+        if (!EXACT && c * kUnits - phase >= cols) continue;
+        const Unit<F32> dy = unit(0, p, i), h = unit(1, p, i);
+        Unit<F32> dh{};
         if (up) dh = unit(2, p, i);
-        float d[8];
+        float d[E];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint64_t x = mul_f32x2(pair(dy.w[j]), rstd2), hj = pair(h.w[j]);
+        for (int j = 0; j < E / 2; ++j) {
+          const uint64_t x = mul_f32x2(dy.pair(j), rstd2), hj = h.pair(j);
           acc[i][j] = fma_f32x2(x, hj, acc[i][j]);
-          const uint64_t v = fma_f32x2(hj, b2, up ? fma_f32x2(x, g[i][j], pair(dh.w[j]))
+          const uint64_t v = fma_f32x2(hj, b2, up ? fma_f32x2(x, g[i][j], dh.pair(j))
                                                   : mul_f32x2(x, g[i][j]));
           d[2 * j] = f32x2_lo(v);
           d[2 * j + 1] = f32x2_hi(v);
         }
-        Lane8<false> out;
+        Unit<F32> out;
         const int bound = EXACT && lg == 5 ? INT32_MAX : cols;
         if (drop) {
           if (a.dres != nullptr) {
             out.set(d);
-            store_unit<false, !EXACT>(out_r, col, bound, out);
+            out.template store<EXACT>(out_r, col, bound);
           }
-          if constexpr (!EXACT) drop8_phase(d, mask, r, c, lane, phase, before);
-          else drop8<true>(d, mask, r, c, at);
+          if constexpr (!EXACT) drop_unit_phase<E>(d, mask, r, c * 32 + lane, lane, phase, before);
+          else drop_unit<E>(d, mask, r, c * 32 + at);
         }
         out.set(d);
-        store_unit<false, !EXACT>(out_x, col, bound, out);
+        out.template store<EXACT>(out_x, col, bound);
       }
     }
     row += hop;
@@ -379,9 +379,9 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
     if (static_cast<int>(threadIdx.y) != y) continue;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      float v[8];
+      float v[E];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < E; ++j) {
         v[j] = j & 1 ? f32x2_hi(acc[i][j >> 1]) : f32x2_lo(acc[i][j >> 1]);
         for (int o = 16; o >= 1 << lg; o >>= 1) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
       }
@@ -389,7 +389,7 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
       if constexpr (EXACT) {  // 16-byte pieces: a float an access cost 3 us at 8192 columns
         if (sub != 0 || col >= cols) continue;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < E / 4; ++q) {
           float4 w = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
           float4 *const at_sums = reinterpret_cast<float4 *>(sums + col + 4 * q);
           if (y > 0) w = add4(w, *at_sums);
@@ -398,7 +398,7 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < E; ++j)
           if (col + j >= 0 && col + j < cols) sums[col + j] = y == 0 ? v[j] : sums[col + j] + v[j];
       }
     }
@@ -502,14 +502,16 @@ struct RingShape {
   size_t smem;
 };
 
+template <bool F32>
 RingShape ring_shape(const NormBackward &a, int sm_count, int smem_max) {
+  constexpr int E = Unit<F32>::E, kUnits = 32 * E;
   RingShape g{};
-  const int64_t rem = a.rows == 1 ? 0 : a.ld_h & 7;
-  g.classes = rem == 0 ? 1 : rem & 1 ? 8 : rem & 2 ? 4 : 2;
-  const int chunks = static_cast<int>((a.cols + (g.classes > 1 ? 7 : 0) + kChunk - 1) / kChunk);
+  const int64_t rem = a.rows == 1 ? 0 : a.ld_h & (E - 1);
+  g.classes = rem == 0 ? 1 : rem & 1 ? E : rem & 2 ? E / 2 : 2;
+  const int chunks = static_cast<int>((a.cols + (g.classes > 1 ? E - 1 : 0) + kUnits - 1) / kUnits);
   g.lg = 5;
-  if (g.classes == 1 && a.cols % 8 == 0)
-    while (g.lg > 0 && (8 << g.lg >> 1) >= a.cols) --g.lg;
+  if (g.classes == 1 && a.cols % E == 0)
+    while (g.lg > 0 && (E << g.lg >> 1) >= a.cols) --g.lg;
   // Two rows at a time, one with dropout (with two its generator's code, twice, costs more
   // than they gain: bf16 [16384, 4096] 121 us against 105) or where two do not fit.  Without:
   // [8192, 8192] 66.4 us against 73, 78 with a reduction for each.
@@ -519,13 +521,13 @@ RingShape ring_shape(const NormBackward &a, int sm_count, int smem_max) {
   const auto fit = [&](int units) {
     g.units = units;
     g.W = (chunks + units - 1) / units;
-    g.exact = g.classes == 1 && (g.lg < 5 || a.cols == static_cast<int64_t>(kChunk) * units * g.W);
+    g.exact = g.classes == 1 && (g.lg < 5 || a.cols == static_cast<int64_t>(kUnits) * units * g.W);
     warps = g.exact || units <= 2 ? 16 : 12;
     return warps / g.W * g.W;
   };
   // inexact rows of 9 to 11 warps leave the others idle ([8192, 4097]: 84 us, 64 so)
   if (fit(g.units) < 12 && g.units == 2 && !g.exact) fit(3);
-  if (g.W > warps || (g.units == 4 && !g.exact)) return RingShape{};
+  if (g.W > warps || (!F32 && g.units == 4 && !g.exact)) return RingShape{};
   const int64_t rows = (a.rows + g.classes - 1) / g.classes, ctas = sm_count / g.classes;
   const int64_t per = (32 >> g.lg) * g.rp, groups = (rows + per - 1) / per;
   g.R = static_cast<int>(std::min<int64_t>(std::min(15, warps / g.W), (groups + ctas - 1) / ctas));
@@ -537,24 +539,27 @@ RingShape ring_shape(const NormBackward &a, int sm_count, int smem_max) {
   return g;
 }
 
-template <bool EXACT, int NU, int RP>
+template <bool F32, bool EXACT, int NU, int RP>
 cudaError_t launch_ring_of(const NormBackward &a, const RingShape &g, cudaStream_t s) {
-  const auto kern = rmsnorm_grad_ring<EXACT, NU, RP>;
+  const auto kern = rmsnorm_grad_ring<F32, EXACT, NU, RP>;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kern), g.smem);
   if (e != cudaSuccess) return e;
   return launch_k(kern, dim3(static_cast<unsigned>(g.grid)), dim3(32 * g.W, g.R), g.smem, s, 0, a, g.stages,
                   g.classes, g.lg);
 }
 
+template <bool F32>
 cudaError_t launch_ring(const NormBackward &a, const RingShape &g, cudaStream_t s) {
   if (g.exact) {
-    if (g.units == 1) return g.rp == 1 ? launch_ring_of<true, 1, 1>(a, g, s) : launch_ring_of<true, 1, 2>(a, g, s);
-    if (g.units == 2) return g.rp == 1 ? launch_ring_of<true, 2, 1>(a, g, s) : launch_ring_of<true, 2, 2>(a, g, s);
-    return launch_ring_of<true, 4, 1>(a, g, s);
+    if (g.units == 1) return g.rp == 1 ? launch_ring_of<F32, true, 1, 1>(a, g, s) : launch_ring_of<F32, true, 1, 2>(a, g, s);
+    if (g.units == 2) return g.rp == 1 ? launch_ring_of<F32, true, 2, 1>(a, g, s) : launch_ring_of<F32, true, 2, 2>(a, g, s);
+    return launch_ring_of<F32, true, 4, 1>(a, g, s);
   }
-  if (g.units == 1) return g.rp == 1 ? launch_ring_of<false, 1, 1>(a, g, s) : launch_ring_of<false, 1, 2>(a, g, s);
-  if (g.units == 2) return g.rp == 1 ? launch_ring_of<false, 2, 1>(a, g, s) : launch_ring_of<false, 2, 2>(a, g, s);
-  return g.rp == 1 ? launch_ring_of<false, 3, 1>(a, g, s) : launch_ring_of<false, 3, 2>(a, g, s);
+  if (g.units == 1) return g.rp == 1 ? launch_ring_of<F32, false, 1, 1>(a, g, s) : launch_ring_of<F32, false, 1, 2>(a, g, s);
+  if (g.units == 2) return g.rp == 1 ? launch_ring_of<F32, false, 2, 1>(a, g, s) : launch_ring_of<F32, false, 2, 2>(a, g, s);
+  if constexpr (F32)
+    if (g.units == 4) return launch_ring_of<F32, false, 4, 1>(a, g, s);
+  return g.rp == 1 ? launch_ring_of<F32, false, 3, 1>(a, g, s) : launch_ring_of<F32, false, 3, 2>(a, g, s);
 }
 
 // Shapes of the other launches, which the workspace follows.
@@ -566,7 +571,7 @@ struct GradShape {
 GradShape held_shape(int64_t rows, int64_t cols, bool f32, int sm_count) {
   const int chunks = static_cast<int>((cols + kChunk - 1) / kChunk);
   GradShape g{};
-  g.units = !f32 && chunks > 32 ? 4 : chunks <= 2 ? 1 : 2;
+  g.units = chunks > 32 ? 4 : chunks <= 2 ? 1 : 2;
   g.W = (chunks + g.units - 1) / g.units;
   g.R = g.W >= 8 ? 1 : 8 / g.W;
   const int64_t per = g.W * g.R >= 16 ? 1 : 2;
@@ -591,16 +596,16 @@ cudaError_t launch_grad(const NormBackward &a, bool held, bool phase, int sm_cou
   const float *partial = static_cast<const float *>(a.workspace);
   int64_t P;
   RingShape rs{};
-  if (!F32 && held && phase) rs = ring_shape(a, sm_count, smem_max);
+  if (held && phase) rs = ring_shape<F32>(a, sm_count, smem_max);
   if (rs.W > 0) {
-    e = launch_ring(a, rs, s);
+    e = launch_ring<F32>(a, rs, s);
     P = rs.grid;
   } else if (held) {
     const GradShape g = held_shape(a.rows, a.cols, F32, sm_count);
     const dim3 grid(static_cast<unsigned>(g.grid)), block(32 * g.W, g.R);
     const size_t smem = g.R > 1 ? a.cols * 4 : 0;
-    if constexpr (!F32 && VEC) {  // shorter ones take the ring
-      e = launch_k(rmsnorm_grad_held<false, true, 4>, grid, block, smem, s, 0, a);
+    if constexpr (VEC) {  // shorter ones take the ring
+      e = launch_k(rmsnorm_grad_held<F32, true, F32 ? 2 : 4>, grid, block, smem, s, 0, a);
     } else {
       e = g.units == 1 ? launch_k(rmsnorm_grad_held<F32, VEC, 1>, grid, block, smem, s, 0, a)
                        : launch_k(rmsnorm_grad_held<F32, VEC, 2>, grid, block, smem, s, 0, a);
