@@ -611,3 +611,121 @@ def test_numpy_and_torch_agree_on_the_bits():
     m, _ = ref.keep(rows, cols, 0.5, n, 1)  # the offset wraps past the largest int64
     got = fr.fr_dropout(torch.ones(rows, cols, device="cuda"), 0.5, torch.from_numpy(n).cuda(), 1)
     assert torch.equal(got.cpu() != 0, m)
+
+
+# Row lengths of each launch of the backward pass's ring: one to four units a lane, exact
+# ones (whole units of every lane) and others, one to sixteen warps a row; strides of each
+# class of phases; fewer rows than classes and than row groups, and several rounds.
+RINGS = {"bf16": [(900, 8, 0), (1900, 72, 0), (700, 128, 8), (1300, 256, 0), (650, 264, 0),
+                  (640, 768, 0), (641, 769, 0), (500, 1024, 0), (310, 1030, 2), (311, 1500, 4),
+                  (400, 2048, 0), (333, 2051, 1), (330, 4098, 6), (500, 4100, 0), (320, 4352, 0),
+                  (5, 4097, 0), (9, 515, 0), (317, 5120, 0), (312, 5121, 7), (306, 8186, 6),
+                  (308, 8192, 0), (155, 9216, 0), (160, 16384, 0), (153, 10000, 0)],
+         "f32": [(900, 4, 0), (1000, 60, 0), (700, 130, 2), (640, 512, 0), (620, 516, 0),
+                 (610, 517, 0), (400, 1024, 4), (333, 2050, 0), (310, 2049, 0), (320, 2176, 0),
+                 (308, 4096, 0), (3, 4097, 0), (307, 4098, 0), (160, 5000, 0), (155, 6143, 0),
+                 (156, 8192, 0), (153, 7001, 1)]}
+
+
+@pytest.mark.parametrize("dtype,rows,cols,extra", [(d, *s) for d in RINGS for s in RINGS[d]])
+def test_backward_of_many_rows(dtype, rows, cols, extra):
+    x, dy, up = (values(rows, cols, dtype, 130 + i, s) for i, s in enumerate((2.0, 0.1, 0.1)))
+    gamma, n = vector(cols, 13), rng_of(cols)
+    rstd = ref.norm(x, gamma, EPS)[1].float()
+    layout = (0, extra)
+    for dh, p in ((None, 0.0), (up, 0.0), (up, 0.2), (None, 0.3)):
+        dx, dr = out(x, layout), out(x, layout)
+        kw = dict(p=p, rng=n.cuda(), site=5, dresidual=dr.t) if p else {}
+        got = fr.fr_rmsnorm_backward(put(dy, layout), put(x, layout), gamma.cuda(), rstd.cuda(), dx=dx.t,
+                                     dh=None if dh is None else put(dh, layout), **kw)
+        check_backward(x, gamma, dh, p, n, 5, got, dy, rstd, f"p {p} dh {dh is not None}")
+        assert dx.intact() and (not p or dr.intact())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols,extra", [(700, 255, 0), (700, 300, 1), (600, 511, 5), (2000, 200, 56),
+                                             (500, 769, 2), (400, 2045, 3), (310, 4098, 6), (306, 8191, 0),
+                                             (160, 16377, 0), (160, 16383, 4), (3000, 8, 0), (4100, 40, 0)])
+def test_forward_of_many_rows(dtype, rows, cols, extra):
+    """Rows in phase of every class, and the many short rows that lanes share."""
+    x, r = values(rows, cols, dtype, 140), values(rows, cols, dtype, 141, 3.0)
+    gamma, n = vector(cols, 14), rng_of(cols + 9)
+    layout = (0, extra)
+    for i, (res, p) in enumerate(((None, 0.0), (r, 0.0), (r, 0.2), (None, 0.5))):
+        kw = {}
+        y = out(x, layout)
+        if p or res is not None:
+            h = out(x, layout)
+            kw = dict(h=h.t, p=p, rng=n.cuda(), site=6, residual=None if res is None else put(res, layout))
+        got = fr.fr_rmsnorm(put(x, layout), gamma.cuda(), EPS, out=y.t, **kw)
+        check_norm(x, res, p, n, 6, got, gamma, f"p {p} residual {res is not None}")
+        assert y.intact() and (not kw or h.intact())
+        q = out(x, layout, torch.float8_e4m3fn)
+        scale = ("row", "group", torch.tensor([0.02]))[i % 3]
+        s = scale if isinstance(scale, str) else "given"
+        got = fr.fr_rmsnorm_quant(put(x, layout), gamma.cuda(), EPS, out=q.t,
+                                  scale=scale if s != "given" else scale.cuda(), **kw)
+        check_norm(x, res, p, n, 6, got, gamma, f"{s} p {p}", s, scale if s == "given" else None)
+        assert q.intact()
+        if p:
+            d = out(x, layout)
+            fr.fr_dropout(put(x, layout), p, n.cuda(), 6, out=d.t,
+                          residual=None if res is None else put(res, layout))
+            assert torch.equal(d.t, h.t) and d.intact()
+
+
+def test_neighbours_of_a_row_do_not_reach_it():
+    """A unit at a row's edge holds elements of the rows beside it (or of the gap): whatever
+    they are, the row's results are its own."""
+    rows, cols, ld = 64, 1021, 1029
+    x, dy = values(rows, cols, "bf16", 150), values(rows, cols, "bf16", 151)
+    gamma, n = vector(cols, 15), rng_of(15)
+    for bad in (math.nan, math.inf):
+        def placed(v):
+            buf = torch.full((rows, ld), bad, dtype=v.dtype, device="cuda")
+            buf[1::2, :cols] = v[1::2].cuda()  # every other row is bad too
+            return buf[:, :cols]
+
+        odd = slice(1, None, 2)
+        xb, dyb = placed(x), placed(dy)
+        a = fr.fr_rmsnorm(xb, gamma.cuda(), EPS, residual=xb, p=0.3, rng=n.cuda())
+        want = ref.dropout(x, 0.3, n, 0, x)
+        ref.assert_near(a["h"][odd], want[odd], ref.dropout_bound(x, 0.3, x, want, x.dtype)[odd], "h")
+        h = a["h"].cpu()[odd]
+        y, rstd = ref.norm(h, gamma, EPS)
+        ref.assert_near(a["rstd"][odd], rstd, ref.rstd_bound(cols) * rstd, "rstd")
+        ref.assert_near(a["y"][odd], y, ref.norm_bound(cols, y, x.dtype), "y")
+        rs = ref.norm(x, gamma, EPS)[1].float()
+        b = fr.fr_rmsnorm_backward(dyb, xb, gamma.cuda(), rs.cuda(), dh=dyb)
+        d, _ = ref.backward(dy, x, gamma, rs, dy)
+        bound = ref.backward_bound(dy, x, gamma, rs, dy, d, x.dtype)
+        ref.assert_near(b["dx"][odd], d[odd], bound[odd], "dx")
+
+
+def test_more_rows_than_a_round_of_every_cta():
+    """The row counts at which a CTA's rounds, row groups and pairs of rows end."""
+    cols = 2048
+    gamma = vector(cols, 16)
+    for rows in (151, 152, 153, 303, 304, 305, 607, 608, 609, 1215, 1217):
+        x, dy = values(rows, cols, "bf16", 160), values(rows, cols, "bf16", 161)
+        rstd = ref.norm(x, gamma, EPS)[1].float()
+        for p in (0.0, 0.1):
+            n = rng_of(rows)
+            got = fr.fr_rmsnorm_backward(dy.cuda(), x.cuda(), gamma.cuda(), rstd.cuda(), p=p, rng=n.cuda())
+            check_backward(x, gamma, None, p, n, 0, got, dy, rstd, f"{rows} rows p {p}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols,layout", [(20000, 64, (0, 0)), (12000, 63, (0, 0)), (6000, 500, (0, 4)),
+                                              (6000, 505, (0, 0)), (10000, 7, (0, 2)), (6000, 300, (1, 0)),
+                                              (700, 4096, (0, 0)), (650, 4101, (0, 0)), (600, 4100, (1, 1))])
+def test_dropout_of_many_rows(rows, cols, layout, dtype):
+    x, r = values(rows, cols, dtype, 170), values(rows, cols, dtype, 171)
+    n = rng_of(cols + 17)
+    for res in (None, r):
+        o = out(x, layout)
+        fr.fr_dropout(put(x, layout), 0.4, n.cuda(), 2, out=o.t,
+                      residual=None if res is None else put(res, layout))
+        want = ref.dropout(x, 0.4, n, 2, res)
+        ref.assert_near(o.t, want, ref.dropout_bound(x, 0.4, res, want, DTYPES[dtype]))
+        assert o.intact()
