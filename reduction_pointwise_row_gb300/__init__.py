@@ -705,8 +705,8 @@ def fr_xent_backward(logits, target, dloss, ignore_index: int = -100, want_loss:
 def _device_of(x) -> int:
     """x's device, which has to be the current one (the library launches there)."""
     dev = x.get_device()
-    if _current_device is None:
-        _stream()  # resolves the lookup
+    if _current_raw_stream is None:
+        _stream()  # resolves the lookups; this one is published last
     if dev != _current_device():
         _on_current_device(x)
     return dev

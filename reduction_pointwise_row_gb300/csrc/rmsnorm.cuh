@@ -217,14 +217,20 @@ __device__ __forceinline__ void drop8(float (&v)[8], const Mask &m, uint32_t row
 // chunk c holds the columns from 256 c + 8 l - phase on, one aligned unit; the first and
 // the last unit of a row lie partly outside it.
 
+// Elements from the start of row `row` to the end of its matrix (or more than a row has).
+__device__ __forceinline__ int elements_left(int64_t rows, int64_t row, int64_t ld, int cols) {
+  const int64_t n = (rows - 1 - row) * ld;
+  return n >= 8 ? INT32_MAX : static_cast<int>(n) + cols;
+}
+
 // The unit from column `col` on of the bf16 row at `row`, as it lies in memory: elements
 // outside the row are its neighbours', to be clipped.  A matrix's first row has no head
-// (its base is aligned); what lies past its last one is not read.
-__device__ __forceinline__ Lane8<false> load_unit(const char *row, int col, int cols, bool last) {
+// (its base is aligned); what lies past the matrix's end, `left` elements on, is not read.
+__device__ __forceinline__ Lane8<false> load_unit(const char *row, int col, int cols, int left) {
   Lane8<false> v;
   v.zero();
   const char *p = row + static_cast<int64_t>(col) * 2;
-  if (col < cols && (!last || col + 8 <= cols)) {
+  if (col < cols && col <= left - 8) {
     const uint4 u = ld_once_u4(p);
     v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
   } else if (col < cols) {

@@ -200,3 +200,41 @@ def test_groups():
     v = torch.arange(300.0).expand(2, 300)
     s = ref.scales(v, 128)
     assert s.shape == (2, 3) and np.allclose(s[0] * 448, [127, 255, 299])
+
+
+def test_a_second_thread_finds_both_lookups(monkeypatch):
+    """The stream's lookup is published after the device's: a call that finds the device's
+    alone resolves both."""
+    monkeypatch.setattr(fr, "_current_device", lambda: 0)
+    monkeypatch.setattr(fr, "_current_raw_stream", None)
+
+    class Tensor:
+        def get_device(self):
+            return 0
+
+    try:
+        fr._device_of(Tensor())
+    except (RuntimeError, AssertionError):
+        pass  # no device here
+    assert fr._current_raw_stream is not None
+
+
+def elements_left(rows, row, ld, cols):
+    """As the kernels bound an aligned unit's load at the end of its matrix."""
+    n = (rows - 1 - row) * ld
+    return 2**31 - 1 if n >= 8 else n + cols
+
+
+def test_units_of_rows_in_phase_stay_within_their_matrix():
+    """A whole 16-byte unit is loaded only where all of it lies between the matrix's first
+    and last element, also for rows shorter than a unit."""
+    for rows in (1, 2, 3, 5, 9, 20):
+        for cols in (1, 2, 3, 7, 8, 9, 15, 257):
+            for ld in (cols, cols + 1, cols + 5):
+                total = (rows - 1) * ld + cols
+                for row in range(rows):
+                    phase = row * ld & 7
+                    for unit in range((cols + phase + 7) // 8):
+                        col = unit * 8 - phase
+                        if col < cols and col <= elements_left(rows, row, ld, cols) - 8:
+                            assert 0 <= row * ld + col and row * ld + col + 8 <= total

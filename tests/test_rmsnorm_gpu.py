@@ -729,3 +729,47 @@ def test_dropout_of_many_rows(rows, cols, layout, dtype):
         want = ref.dropout(x, 0.4, n, 2, res)
         ref.assert_near(o.t, want, ref.dropout_bound(x, 0.4, res, want, DTYPES[dtype]))
         assert o.intact()
+
+
+def test_auto_takes_a_form_that_holds_the_rows():
+    """Long rows, aligned and not: the workspace that AUTO asks for serves either form."""
+    for rows, cols in ((2, 8200), (3, 16384), (2, 16383), (1, 16392)):
+        x, dy = values(rows, cols, "bf16", 180), values(rows, cols, "bf16", 181)
+        gamma = vector(cols, 18)
+        rstd = ref.norm(x, gamma, EPS)[1].float()
+        for layout in LAYOUTS:
+            got = fr.fr_rmsnorm(put(x, layout), gamma.cuda(), EPS)
+            check_norm(x, None, 0.0, None, 0, got, gamma, f"{cols} {layout}")
+            back = fr.fr_rmsnorm_backward(put(dy, layout), put(x, layout), gamma.cuda(), rstd.cuda())
+            check_backward(x, gamma, None, 0.0, None, 0, back, dy, rstd, f"{cols} {layout}")
+
+
+FIRST_CALLS = """
+import sys; sys.path.insert(0, sys.argv[1])
+import torch, reduction_pointwise_row_gb300 as fr
+x = torch.randn(200, 4096, device="cuda").bfloat16(); r = torch.randn_like(x)
+g = torch.ones(4096, device="cuda"); n = torch.tensor([3, 4], device="cuda")
+fr.fr_workspace_size("rmsnorm_backward", 200, 4096, "bf16")
+torch.cuda.synchronize()
+def step():
+    a = fr.fr_rmsnorm(x, g, residual=r, p=0.1, rng=n)
+    b = fr.fr_rmsnorm_backward(x, a["h"], g, a["rstd"], dh=r, p=0.1, rng=n)
+    q = fr.fr_rmsnorm_quant(x, g, scale="group")
+    return [*a.values(), *b.values(), *q.values(), fr.fr_dropout(x, 0.2, n)]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    outs = step()
+graph.replay(); torch.cuda.synchronize()
+for o, e in zip(outs, step()):
+    assert torch.equal(o.view(torch.uint8), e.view(torch.uint8))
+print("same")
+"""
+
+
+def test_first_calls_within_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS, root], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
