@@ -747,10 +747,14 @@ def _rng_ptr(p: float, rng, site: int, dev: int):
 
 
 def _matrix_out(x, rows: int, cols: int, ld: int):
-    """A new compact matrix of x's shape and dtype."""
-    if ld == cols and x.is_contiguous():
-        return _TORCH.empty_like(x)
-    return _TORCH.empty((rows, cols), dtype=x.dtype, device=x.device)
+    """(matrix, row stride): a new one of x's shape and dtype whose rows share x's offset
+    within 8 elements (a compact matrix when x is one)."""
+    if ld == cols:
+        if x.is_contiguous():
+            return _TORCH.empty_like(x), cols
+        return _TORCH.empty((rows, cols), dtype=x.dtype, device=x.device), cols
+    ldo = cols + (ld - cols) % 8
+    return _TORCH.empty_strided((rows, cols), (ldo, 1), dtype=x.dtype, device=x.device), ldo
 
 
 def _with_stream(call, stream, *args):
@@ -773,7 +777,7 @@ def fr_dropout(x, p: float, rng, site: int = 0, residual=None, out=None, stream=
     p_rng = _rng_ptr(p, rng, site, dev)
     ldr = 0 if residual is None else _like(residual, x, ld, dev, "residual")
     if out is None:
-        out, ldo = _matrix_out(x, rows, cols, ld), cols
+        out, ldo = _matrix_out(x, rows, cols, ld)
     else:
         ldo = _like(out, x, ld, dev, "out")
     status = lib().fr_dropout(x.data_ptr(), None if residual is None else residual.data_ptr(),
@@ -807,13 +811,13 @@ def fr_rmsnorm(x, gamma, eps: float = 1e-5, residual=None, p: float = 0.0, rng=N
         ldr = _like(residual, x, ld, dev, "residual")
         p_res = residual.data_ptr()
     if out is None:
-        out = _matrix_out(x, rows, cols, ld)
+        out, ldy = _matrix_out(x, rows, cols, ld)
     else:
         ldy = _like(out, x, ld, dev, "out")
     res = {"y": out}
     if p_res is not None or p_rng is not None:
         if h is None:
-            h, ldh = _matrix_out(x, rows, cols, ld), cols
+            h, ldh = _matrix_out(x, rows, cols, ld)
         else:
             ldh = _like(h, x, ld, dev, "h")
         p_h = h.data_ptr()
@@ -876,7 +880,8 @@ def fr_rmsnorm_quant(x, gamma, eps: float = 1e-5, scale="row", residual=None, p:
         ldr = _like(residual, x, ld, dev, "residual")
         p_res = residual.data_ptr()
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=x.device)
+        ldy = cols + (ld - cols) % 8
+        out = torch.empty_strided((rows, cols), (ldy, 1), dtype=torch.float8_e4m3fn, device=x.device)
     else:
         if not out.is_cuda or out.dtype is not torch.float8_e4m3fn or out.shape != x.shape or \
                 (out.stride(1) != 1 and cols != 1):
@@ -910,7 +915,7 @@ def fr_rmsnorm_quant(x, gamma, eps: float = 1e-5, scale="row", residual=None, p:
         p_scale = scale.data_ptr()
     if p_res is not None or p_rng is not None:
         if h is None:
-            h, ldh = _matrix_out(x, rows, cols, ld), cols
+            h, ldh = _matrix_out(x, rows, cols, ld)
         else:
             ldh = _like(h, x, ld, dev, "h")
         p_h = h.data_ptr()
@@ -965,7 +970,7 @@ def fr_rmsnorm_backward(dy, h, gamma, rstd, dh=None, p: float = 0.0, rng=None, s
         if workspace.get_device() != dev:
             _on_current_device(workspace)
     if dx is None:
-        dx = _matrix_out(dy, rows, cols, ld)
+        dx, lddx = _matrix_out(dy, rows, cols, ld)
     else:
         lddx = _like(dx, dy, ld, dev, "dx")
     res = {"dx": dx}
@@ -975,7 +980,7 @@ def fr_rmsnorm_backward(dy, h, gamma, rstd, dh=None, p: float = 0.0, rng=None, s
         if dresidual is not None:
             lddr = _like(dresidual, dy, ld, dev, "dresidual")
         elif want_dresidual:
-            dresidual, lddr = _matrix_out(dy, rows, cols, ld), cols
+            dresidual, lddr = _matrix_out(dy, rows, cols, ld)
         if dresidual is not None:
             p_dr = dresidual.data_ptr()
             res["dresidual"] = dresidual

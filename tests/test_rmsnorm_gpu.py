@@ -773,3 +773,20 @@ def test_first_calls_within_a_capture():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS, root], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("cols,ld", [(1000, 1000), (1000, 1003), (1001, 1008), (1001, 1001), (64, 80), (7, 12)])
+def test_outputs_share_the_phase_of_the_inputs(cols, ld):
+    """New matrices lie as the inputs do within 8 elements; their values do not depend on it."""
+    rows, n = 50, rng_of(6).cuda()
+    x = values(rows, cols, "bf16", 190)
+    v = put(x, (0, ld - cols))
+    gamma = vector(cols, 19)
+    a = fr.fr_rmsnorm(v, gamma.cuda(), EPS, residual=v, p=0.2, rng=n)
+    q = fr.fr_rmsnorm_quant(v, gamma.cuda(), EPS)
+    b = fr.fr_rmsnorm_backward(v, v, gamma.cuda(), a["rstd"], p=0.2, rng=n)
+    for m in (a["y"], a["h"], q["y"], b["dx"], b["dresidual"], fr.fr_dropout(v, 0.2, n)):
+        assert m.shape == (rows, cols) and (m.stride(0) - ld) % 8 == 0 and m.stride(0) < cols + 8
+        assert m.is_contiguous() == ((ld - cols) % 8 == 0)
+    check_norm(x, x, 0.2, n.cpu(), 0, a, gamma, "y")
+    check_norm(x, None, 0.0, None, 0, q, gamma, "y8", "row")
