@@ -60,4 +60,16 @@ def algorithmic_bytes(op: str, rows: int, cols: int, **kw) -> int:
         return 2 * logits + rows * (12 * top + 4) + loss
     if op == "xent_backward":         # targets and dloss in
         return 2 * logits + rows * (8 + 4) + loss
+    # a residual block's row operators (kw: dtype, residual given, dropout): every matrix once
+    n = rows * cols
+    es = 4 if kw.get("dtype", "bf16") == "f32" else 2
+    res, drop = int(kw.get("residual", False)), int(kw.get("drop", False))
+    if op == "dropout":               # x and the residual in, y out
+        return n * es * (2 + res)
+    if op == "rmsnorm":               # the same, the sum's rounding and rstd out, gamma in
+        return n * es * (2 + res + (res or drop)) + 4 * (cols + rows)
+    if op == "rmsnorm_quant":         # y in 8 bits; kw scales: fp32 scales written or read
+        return n * (es * (1 + res + (res or drop)) + 1) + 4 * (cols + kw.get("scales", rows))
+    if op == "rmsnorm_backward":      # dy, h and dh (residual) in, the gradients out
+        return n * es * (3 + res + drop) + 4 * (2 * cols + rows)
     raise ValueError(op)

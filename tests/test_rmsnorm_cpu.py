@@ -238,3 +238,16 @@ def test_units_of_rows_in_phase_stay_within_their_matrix():
                         col = unit * 8 - phase
                         if col < cols and col <= elements_left(rows, row, ld, cols) - 8:
                             assert 0 <= row * ld + col and row * ld + col + 8 <= total
+
+
+def test_algorithmic_bytes():
+    from reduction_pointwise_row_gb300 import traffic
+    n = 16384 * 4096
+    assert traffic.algorithmic_bytes("dropout", 16384, 4096) == 4 * n
+    assert traffic.algorithmic_bytes("rmsnorm", 16384, 4096, residual=True, drop=True) == \
+        8 * n + 4 * (16384 + 4096)
+    assert traffic.algorithmic_bytes("rmsnorm", 16384, 4096, dtype="f32") == 8 * n + 4 * (16384 + 4096)
+    assert traffic.algorithmic_bytes("rmsnorm_quant", 16384, 4096, residual=True) == \
+        7 * n + 4 * (16384 + 4096)
+    assert traffic.algorithmic_bytes("rmsnorm_backward", 16384, 4096, residual=True, drop=True) == \
+        10 * n + 4 * (2 * 4096 + 16384)
