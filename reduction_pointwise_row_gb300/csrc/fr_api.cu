@@ -1083,7 +1083,7 @@ fr_status run_rmsnorm(fr::NormForward &a, fr_dtype dtype, bool quant, float p, c
   fr::DevInfo info;
   if (fr_status st = device_ok(&info)) return st;
   const fr_form f = form == FR_FORM_AUTO ? pick_rmsnorm(a.cols) : form;
-  const bool vec = a.cols % 8 == 0 && aligned(a.gamma, 16) && rows_of_8(x, a.rows) &&
+  const bool vec = a.cols % 8 == 0 && aligned(a.gamma, 32) && rows_of_8(x, a.rows) &&
                    rows_of_8(res, a.rows) && rows_of_8(h, a.rows) && rows_of_8(y, a.rows);
   const bool phase = aligned(a.gamma, 16) && rows_in_phase({x, res, h, y}, a.rows, 8);
   return launched(fr::launch_rmsnorm(a, dtype == FR_F32, vec, phase, quant, f == FR_FORM_PERSISTENT,
@@ -1166,7 +1166,7 @@ fr_status fr_rmsnorm_backward(const void *dy, const void *h, const float *gamma,
                                     {a.drop.rng, 16, 8, false}}))
     return st;
   if (form < FR_FORM_AUTO || form > FR_FORM_LOOPED) return FR_ERR_UNSUPPORTED_FORM;
-  const bool vec = cols % 8 == 0 && aligned(gamma, 16) && rows_of_8(mdy, rows) &&
+  const bool vec = cols % 8 == 0 && aligned(gamma, 32) && rows_of_8(mdy, rows) &&
                    rows_of_8(mh, rows) && rows_of_8(mdh, rows) && rows_of_8(mdx, rows) &&
                    rows_of_8(mdr, rows);
   if (form == FR_FORM_PERSISTENT && !fr::rmsnorm_grad_held_ok(cols, f32, vec))

@@ -122,9 +122,9 @@ __device__ __forceinline__ void load_cols8(float (&g)[8], const float *p, int c,
   if constexpr (VEC) {
     const int col = c * kChunk + lane * 8;
     if (col < cols) {
-      const float4 a = ld_keep_f4(p + col), b = ld_keep_f4(p + col + 4);
-      g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
-      g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
+      const V8 u = ld_keep_v8(p + col);  // (two 16-byte loads would each touch every sector)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = __uint_as_float(u.w[j]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) g[j] = 0.0f;
