@@ -1085,7 +1085,7 @@ fr_status run_rmsnorm(fr::NormForward &a, fr_dtype dtype, bool quant, float p, c
   const fr_form f = form == FR_FORM_AUTO ? pick_rmsnorm(a.cols) : form;
   const bool vec = a.cols % 8 == 0 && aligned(a.gamma, 32) && rows_of_8(x, a.rows) &&
                    rows_of_8(res, a.rows) && rows_of_8(h, a.rows) && rows_of_8(y, a.rows);
-  const bool phase = aligned(a.gamma, 16) && rows_in_phase({x, res, h, y}, a.rows, 8);
+  const bool phase = aligned(a.gamma, 32) && rows_in_phase({x, res, h, y}, a.rows, 8);
   return launched(fr::launch_rmsnorm(a, dtype == FR_F32, vec, phase, quant, f == FR_FORM_PERSISTENT,
                                      info.sm_count, reinterpret_cast<cudaStream_t>(stream)),
                   f);

@@ -299,7 +299,7 @@ struct NormForward {
 bool rmsnorm_held_ok(int64_t cols);
 // quant: y in e4m3.  vec: every matrix's rows are aligned to 8 elements (and cols a
 // multiple of 8), gamma to 32 bytes.  phase: every matrix starts at a multiple of 8
-// elements and their row strides agree modulo 8, gamma at 16 bytes.
+// elements and their row strides agree modulo 8, gamma as before.
 cudaError_t launch_rmsnorm(const NormForward &a, bool f32, bool vec, bool phase, bool quant, bool held,
                            int sm_count, cudaStream_t s);
 // y = residual + dropout(x): x, residual, h (as y), rows, cols, lds and drop of `a`.

@@ -242,28 +242,28 @@ __device__ __forceinline__ Lane8<false> load_unit(const char *row, int col, int 
   return v;
 }
 
-// The 8 values from column `col` on of a 16-byte aligned vector over the columns, 0
-// outside it: the three aligned 16-byte pieces that hold them, cut at the same place in
+template <int T>
+__device__ __forceinline__ void cut8(float (&g)[8], const V8 &a, const V8 &b) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) g[j] = __uint_as_float(j + T < 8 ? a.w[(j + T) & 7] : b.w[(j + T) & 7]);
+}
+
+// The 8 values from column `col` on of a 32-byte aligned vector over the columns, 0
+// outside it: the two aligned 32-byte pieces that hold them, cut at the same place in
 // every lane (rows start at one phase), instead of 8 scattered values a lane.
 __device__ __forceinline__ void load_cols_unit(float (&g)[8], const float *p, int col, int cols) {
-  const int t = col & 3, first = col - t;
-  if (first >= 0 && first + 12 <= cols) {
-    const float4 a = ld_keep_f4(p + first), b = ld_keep_f4(p + first + 4);
-    float4 c = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (t != 0) c = ld_keep_f4(p + first + 8);
-    const float f[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
-    if (t == 0) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = f[j];
-    } else if (t == 1) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = f[j + 1];
-    } else if (t == 2) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = f[j + 2];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = f[j + 3];
+  const int t = col & 7, first = col - t;
+  if (first >= 0 && first + 16 <= cols) {
+    const V8 a = ld_keep_v8(p + first), b = ld_keep_v8(p + first + 8);
+    switch (t) {
+      case 0: cut8<0>(g, a, b); break;
+      case 1: cut8<1>(g, a, b); break;
+      case 2: cut8<2>(g, a, b); break;
+      case 3: cut8<3>(g, a, b); break;
+      case 4: cut8<4>(g, a, b); break;
+      case 5: cut8<5>(g, a, b); break;
+      case 6: cut8<6>(g, a, b); break;
+      default: cut8<7>(g, a, b); break;
     }
   } else {
 #pragma unroll
