@@ -486,12 +486,14 @@ fr_status fr_xent_backward(const void *logits, const int64_t *target, const floa
  * around its matrix products.  Shared by the four calls:
  *
  *   matrices     of `dtype` (FR_BF16 or FR_F32), [rows, ld] with any ld >= cols and
- *                any element-aligned address.  Rows of all of a call's matrices that
- *                start at multiples of 8 elements (16 bytes of bf16, 32 of fp32; an
- *                e4m3 output 8), with cols a multiple of 8 and gamma and dgamma
- *                16-byte aligned, take the vector path; others an element an access
- *                (same results up to the order of a row's sums).  rows <= INT32_MAX,
- *                cols < 2^31 (more: FR_ERR_UNSUPPORTED_FORM).
+ *                any element-aligned address.  Fastest: every row of every matrix of
+ *                a call starts at a multiple of 8 elements (16 bytes of bf16, 32 of
+ *                fp32, 8 of e4m3), cols is one too, gamma is 32-byte aligned.  Next, for
+ *                bf16 and the gradient: the bases are aligned so and the strides agree
+ *                modulo 8 elements, whatever cols is (compact matrices of odd rows).
+ *                Other rows are read an element an access.  The results are the same
+ *                up to the order of a row's sums.  rows <= INT32_MAX, cols < 2^31
+ *                (more: FR_ERR_UNSUPPORTED_FORM).
  *   overlap      an output matrix may be the very buffer of an input matrix of its
  *                type with the same ld, or lie in the gaps of its rows (same ld); any
  *                other overlap of an output with an input or another output is
@@ -511,10 +513,10 @@ fr_status fr_xent_backward(const void *logits, const int64_t *target, const floa
  *                whatever it holds; p = 1 drops everything.
  *   gamma        fp32 [cols], as fr_layernorm's.
  * Arithmetic is fp32, each output rounded once (nearest even).  NaN and infinities
- * follow the formulas: a NaN or an infinity in h makes its row's y, and the gradients
- * of that row and dgamma, NaN (an infinity: zeros where the other elements are
- * finite).  A row whose squares add up past fp32 (elements of about 1e19) has rstd 0.
- * Results are the same from run to run.
+ * follow the formulas: a NaN in h makes its row's y and dx NaN, and dgamma; an infinity
+ * there makes rstd 0, its own y NaN and the row's others 0.  A row whose squares add up
+ * past fp32 (elements of about 1e19) has rstd 0 and y 0 (in 8 bits with a scale a row NaN
+ * where h gamma is past fp32 as well).  Results are the same from run to run.
  */
 
 /*
@@ -532,11 +534,12 @@ fr_status fr_dropout(const void *x, const void *residual, void *y, int64_t rows,
  *   y = h rstd gamma
  * With neither a residual nor dropout h is x: pass h NULL.  Otherwise h is required.
  *
- *   eps         finite, >= 0 (with 0, a row of zeros gives NaN)
+ *   eps         finite, >= 0 (with 0, a row of zeros, or one whose squares all vanish in
+ *               fp32, gives NaN or infinities)
  *   rstd        fp32 [rows] device output; may be NULL
- * Forms: persistent (the row in registers, at most 16384 columns; 1 to 32 warps a
- * row) and looped (a CTA goes over its row twice).  AUTO takes the persistent one as
- * far as it reaches.
+ * Forms: persistent (the row in registers, at most 16384 columns; up to 32 warps a
+ * row, or several rows a warp) and looped (a CTA goes over its row twice).  AUTO takes
+ * the persistent one as far as it reaches.
  */
 fr_status fr_rmsnorm(const void *x, const void *residual, const float *gamma, void *h, void *y,
                      float *rstd, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr,
@@ -577,8 +580,9 @@ fr_status fr_rmsnorm_quant(const void *x, const void *residual, const float *gam
  *   workspace   device scratch of fr_workspace_size(FR_OP_RMSNORM_BACKWARD, ...) bytes,
  *               16-byte aligned (partial sums of dgamma, row sums of the looped form;
  *               contents on entry ignored).  One call at a time may use it.
- * Forms: persistent (the row in registers, at most 16384 columns of bf16, 8192 of
- * fp32) and looped (two passes over the rows; any length).
+ * Forms: persistent (the rows read once, a CTA's share of dgamma in registers; at most
+ * 16384 columns of aligned bf16, 8192 otherwise) and looped (two passes over the rows;
+ * any length).
  */
 fr_status fr_rmsnorm_backward(const void *dy, const void *h, const float *gamma,
                               const float *rstd, const void *dh, void *dx, void *dresidual,
