@@ -908,8 +908,8 @@ def fr_rmsnorm_quant(x, gamma, eps: float = 1e-5, scale="row", residual=None, p:
     else:
         mode = 2
         _need(scale_out is None, "scale_out with a given scale")
-        _need(scale.is_cuda and scale.dtype is torch.float32 and scale.numel() == 1,
-              "scale must be a CUDA tensor of one fp32 value")
+        _need(isinstance(scale, torch.Tensor) and scale.is_cuda and scale.dtype is torch.float32 and
+              scale.numel() == 1, 'scale must be "row", "group" or a CUDA tensor of one fp32 value')
         if scale.get_device() != dev:
             _on_current_device(scale)
         p_scale = scale.data_ptr()

@@ -726,8 +726,9 @@ cudaError_t launch_rmsnorm(const NormForward &a, bool f32, bool vec, bool phase,
 cudaError_t launch_dropout(const NormForward &a, bool f32, bool vec, bool phase, int sm_count,
                            cudaStream_t s) {
   if (f32) return vec ? launch_drop<true, kAligned>(a, sm_count, s) : launch_drop<true, kScattered>(a, sm_count, s);
+  const bool units = phase && a.cols <= (INT64_C(1) << 30);  // 32-bit columns, up to 7 past the row
   return vec     ? launch_drop<false, kAligned>(a, sm_count, s)
-         : phase ? launch_drop<false, kPhase>(a, sm_count, s)
+         : units ? launch_drop<false, kPhase>(a, sm_count, s)
                  : launch_drop<false, kScattered>(a, sm_count, s);
 }
 

@@ -528,7 +528,7 @@ RingShape ring_shape(const NormBackward &a, int sm_count, int smem_max) {
   // inexact rows of 9 to 11 warps leave the others idle ([8192, 4097]: 84 us, 64 so)
   if (fit(g.units) < 12 && g.units == 2 && !g.exact) fit(3);
   if (g.W > warps || (!F32 && g.units == 4 && !g.exact)) return RingShape{};
-  const int64_t rows = (a.rows + g.classes - 1) / g.classes, ctas = sm_count / g.classes;
+  const int64_t rows = (a.rows + g.classes - 1) / g.classes, ctas = std::max(1, sm_count / g.classes);
   const int64_t per = (32 >> g.lg) * g.rp, groups = (rows + per - 1) / per;
   g.R = static_cast<int>(std::min<int64_t>(std::min(15, warps / g.W), (groups + ctas - 1) / ctas));
   g.grid = std::min<int64_t>((groups + g.R - 1) / g.R, ctas) * g.classes;
