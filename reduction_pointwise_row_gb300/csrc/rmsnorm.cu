@@ -520,8 +520,8 @@ enum { kScattered, kAligned, kPhase };  // how a lane's elements lie: element by
                                         // in an aligned unit, in a unit of a row in phase
 template <bool F32, int HOW, int NU, bool SHORT, bool RES>
 __global__ void __launch_bounds__(256, HOW == kAligned && RES ? 3 : 4) dropout_chunks(NormForward a, unsigned runs, int lg) {
-  constexpr bool VEC = HOW == kAligned;
   pdl_enter();
+  constexpr bool VEC = HOW == kAligned;
   const int lane = threadIdx.x & 31, at = lane & ((1 << lg) - 1), W = blockDim.x >> 5;
   const int cols = static_cast<int>(a.cols);
   const unsigned group = SHORT ? blockIdx.x : blockIdx.x / runs;

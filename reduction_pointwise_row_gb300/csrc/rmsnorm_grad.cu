@@ -184,8 +184,8 @@ constexpr int kRingWarps = EXACT || NU <= 2 ? 16 : 12;
 template <bool F32, bool EXACT, int NU, int RP>
 __global__ void __launch_bounds__(kRingWarps<EXACT, NU> * 32, 1)
 rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
-  constexpr int E = Unit<F32>::E, ES = 16 / E, kUnits = 32 * E;  // columns of a warp's unit
   pdl_enter();
+  constexpr int E = Unit<F32>::E, ES = 16 / E, kUnits = 32 * E;  // columns of a warp's unit
   __shared__ float red[2][16][RP][16];  // [round & 1][row group][row][warp]
   extern __shared__ __align__(16) unsigned char ring[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5, R = blockDim.y;
