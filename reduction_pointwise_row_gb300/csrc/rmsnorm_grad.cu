@@ -637,7 +637,9 @@ bool rmsnorm_grad_held_ok(int64_t cols, bool f32, bool vec) {
 }
 
 size_t rmsnorm_grad_workspace(int64_t rows, int64_t cols, bool f32, bool held, int sm_count) {
-  if (held) return static_cast<size_t>(std::min<int64_t>(std::max<int64_t>(rows, 8), 2 * sm_count) * cols * 4);
+  // a share a CTA: at most two an SM, and at most a CTA a row, or in the ring a row of the
+  // longest of 8 classes for each of them
+  if (held) return static_cast<size_t>(std::min<int64_t>((rows + 7) / 8 * 8, std::max(8, 2 * sm_count)) * cols * 4);
   return static_cast<size_t>(dots_bytes(rows) + looped_shape(rows, cols, sm_count).grid * cols * 4);
 }
 

@@ -790,3 +790,42 @@ def test_outputs_share_the_phase_of_the_inputs(cols, ld):
         assert m.is_contiguous() == ((ld - cols) % 8 == 0)
     check_norm(x, x, 0.2, n.cpu(), 0, a, gamma, "y")
     check_norm(x, None, 0.0, None, 0, q, gamma, "y8", "row")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cols", [8, 150, 151, 154, 156, 500, 1001, 4097])
+def test_the_workspace_holds_every_cta_s_share(cols, dtype):
+    """Nothing is written past the bytes that fr_workspace_size gives, whatever the rows'
+    number leaves of the classes of phases."""
+    gamma, n = vector(cols, 21).cuda(), rng_of(21).cuda()
+    for rows in [*range(1, 42), 151, 152, 153, 303, 305]:
+        x, dy = values(rows, cols, dtype, 210).cuda(), values(rows, cols, dtype, 211).cuda()
+        rstd = torch.ones(rows, device="cuda")
+        nws = fr.fr_workspace_size("rmsnorm_backward", rows, cols, dtype)
+        ws = torch.full((nws + 64 * 1024,), GUARD, dtype=torch.uint8, device="cuda")
+        for p in (0.0, 0.5):
+            fr.fr_rmsnorm_backward(dy, x, gamma, rstd, p=p, rng=n, workspace=ws[:nws])
+            assert (ws[nws:] == GUARD).all(), rows
+
+
+def test_vectors_end_where_they_end():
+    """rstd, scales and dgamma are written to their last element and no further."""
+    def guarded(shape):
+        n = int(np.prod(shape))
+        raw = torch.full((n + 64,), -7.0, device="cuda")
+        return raw, raw[:n].view(shape)
+
+    for dtype in DTYPES:
+        for rows, cols in ((1, 1), (3, 129), (17, 128), (33, 1001), (300, 64), (5, 300), (9, 4097), (2, 17000)):
+            x = values(rows, cols, dtype, 220)
+            gamma = vector(cols, 22)
+            groups = -(-cols // 128)
+            for mode, shape in (("row", (rows,)), ("group", (rows, groups))):
+                (r0, rstd), (s0, scale), (d0, dgamma) = (guarded(s) for s in ((rows,), shape, (cols,)))
+                q = fr.fr_rmsnorm_quant(x.cuda(), gamma.cuda(), EPS, scale=mode, scale_out=scale, rstd=rstd)
+                check_norm(x, None, 0.0, None, 0, q, gamma, f"{rows}x{cols} {mode}", mode)
+                fr.fr_rmsnorm_backward(x.cuda(), x.cuda(), gamma.cuda(), rstd, dgamma=dgamma)
+                want = ref.backward(x, x, gamma, rstd.cpu())[1]
+                ref.assert_near(dgamma, want, ref.dgamma_bound(x, x, rstd.cpu()), "dgamma")
+                for raw, v in ((r0, rstd), (s0, scale), (d0, dgamma)):
+                    assert (raw[v.numel():] == -7.0).all()
