@@ -281,8 +281,8 @@ fr_form pick_rmsnorm(int64_t cols) {
   return fr::rmsnorm_held_ok(cols) ? FR_FORM_PERSISTENT : FR_FORM_LOOPED;
 }
 
-fr_form pick_rmsnorm_backward(int64_t cols, bool f32, bool vec) {
-  return fr::rmsnorm_grad_held_ok(cols, f32, vec) ? FR_FORM_PERSISTENT : FR_FORM_LOOPED;
+fr_form pick_rmsnorm_backward(int64_t cols, bool f32, bool whole) {
+  return fr::rmsnorm_grad_held_ok(cols, f32, whole) ? FR_FORM_PERSISTENT : FR_FORM_LOOPED;
 }
 
 }  // namespace
@@ -362,8 +362,8 @@ size_t fr_workspace_size(fr_op op, int64_t rows, int64_t cols, fr_dtype dtype, f
       const bool f32 = dtype == FR_F32;
       if ((!f32 && dtype != FR_BF16) || rows > INT32_MAX || cols > INT32_MAX) return 0;
       // AUTO may take either form, by the rows' alignment
-      const size_t held = fr::rmsnorm_grad_workspace(rows, cols, f32, true, info.sm_count);
-      const size_t looped = fr::rmsnorm_grad_workspace(rows, cols, f32, false, info.sm_count);
+      const size_t held = fr::rmsnorm_grad_workspace(rows, cols, true, info.sm_count);
+      const size_t looped = fr::rmsnorm_grad_workspace(rows, cols, false, info.sm_count);
       const bool h = form == FR_FORM_PERSISTENT ||
                      (form == FR_FORM_AUTO && fr::rmsnorm_grad_held_ok(cols, f32, cols % 8 == 0));
       const bool l = form == FR_FORM_LOOPED ||
@@ -1169,18 +1169,20 @@ fr_status fr_rmsnorm_backward(const void *dy, const void *h, const float *gamma,
   const bool vec = cols % 8 == 0 && aligned(gamma, 32) && rows_of_8(mdy, rows) &&
                    rows_of_8(mh, rows) && rows_of_8(mdh, rows) && rows_of_8(mdx, rows) &&
                    rows_of_8(mdr, rows);
-  if (form == FR_FORM_PERSISTENT && !fr::rmsnorm_grad_held_ok(cols, f32, vec))
+  const int unit = 16 / es;
+  const bool phase = rows_in_phase({mdy, mh, mdh, mdx, mdr}, rows, unit);
+  const bool whole = phase && cols % unit == 0 && (rows == 1 || ld_h % unit == 0);
+  if (form == FR_FORM_PERSISTENT && !fr::rmsnorm_grad_held_ok(cols, f32, whole))
     return FR_ERR_UNSUPPORTED_FORM;
   fr::DevInfo info;
   if (fr_status st = device_ok(&info)) return st;
-  const fr_form f = form == FR_FORM_AUTO ? pick_rmsnorm_backward(cols, f32, vec) : form;
+  const fr_form f = form == FR_FORM_AUTO ? pick_rmsnorm_backward(cols, f32, whole) : form;
   const bool held = f == FR_FORM_PERSISTENT;
   if (!held || dgamma) {
-    const size_t need = fr::rmsnorm_grad_workspace(rows, cols, f32, held, info.sm_count);
+    const size_t need = fr::rmsnorm_grad_workspace(rows, cols, held, info.sm_count);
     if (!workspace || workspace_bytes < need) return FR_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned(workspace, 16)) return FR_ERR_MISALIGNED;
   }
-  const bool phase = rows_in_phase({mdy, mh, mdh, mdx, mdr}, rows, 16 / es);
   return launched(fr::launch_rmsnorm_backward(a, f32, vec, phase, held, info.sm_count,
                                               info.max_smem_optin,
                                               reinterpret_cast<cudaStream_t>(stream)),

@@ -316,9 +316,10 @@ struct NormBackward {
   DropSpec drop;
   void *workspace;
 };
-// True when a row fits the registers of a CTA (vec: the rows are aligned).
-bool rmsnorm_grad_held_ok(int64_t cols, bool f32, bool vec);
-size_t rmsnorm_grad_workspace(int64_t rows, int64_t cols, bool f32, bool held, int sm_count);
+// True when the persistent form takes a row of this length (whole: every row of every
+// matrix is 16-byte units from its start to its end).
+bool rmsnorm_grad_held_ok(int64_t cols, bool f32, bool whole);
+size_t rmsnorm_grad_workspace(int64_t rows, int64_t cols, bool held, int sm_count);
 // phase: every matrix starts at a multiple of 16 bytes and their row strides agree modulo
 // 16 bytes.
 cudaError_t launch_rmsnorm_backward(const NormBackward &a, bool f32, bool vec, bool phase, bool held,

@@ -69,9 +69,11 @@ __device__ __forceinline__ void store_cols8(float *p, int c, int lane, int cols,
   }
 }
 
-// Persistent form: blockDim = (32 W, R), R rows at a time, W warps a row, NU chunks a
-// warp; a CTA takes every gridDim.x-th group of R rows.
-template <bool F32, bool VEC, int NU>
+// Rows that the ring below does not take (out of phase, or with edges and long): element
+// accesses.  blockDim = (32 W, R), R rows at a time, W warps a row, NU chunks a warp; a CTA
+// takes every gridDim.x-th group of R rows.  dh is loaded when its turn comes: there are no
+// registers for it before.
+template <bool F32, int NU>
 __global__ void __launch_bounds__(512) rmsnorm_grad_held(NormBackward a) {
   pdl_enter();
   __shared__ float red[2][16];
@@ -93,25 +95,19 @@ __global__ void __launch_bounds__(512) rmsnorm_grad_held(NormBackward a) {
     const int64_t row = base + threadIdx.y;
     const bool live = row < a.rows;
     const char *dhr = row_of<F32>(a.dh, row, a.ld_dh);
-    // dh is loaded ahead where there are registers for it
-    constexpr bool EARLY = VEC && NU <= 2;
-    Lane8<F32> dy[NU], h[NU], dh[EARLY ? NU : 1];
+    Lane8<F32> dy[NU], h[NU];
     float rstd = 0.0f, dot = 0.0f;
     if (live) {
       const char *dyr = row_of<F32>(a.dy, row, a.ld_dy), *hr = row_of<F32>(a.h, row, a.ld_h);
 #pragma unroll
-      for (int i = 0; i < NU; ++i) dy[i] = load8<F32, VEC>(dyr, i * W + warp, lane, cols);
+      for (int i = 0; i < NU; ++i) dy[i] = load8<F32, false>(dyr, i * W + warp, lane, cols);
 #pragma unroll
-      for (int i = 0; i < NU; ++i) h[i] = load8<F32, VEC>(hr, i * W + warp, lane, cols);
-      if (EARLY && a.dh != nullptr) {
-#pragma unroll
-        for (int i = 0; i < NU; ++i) dh[i] = load8<F32, VEC>(dhr, i * W + warp, lane, cols);
-      }
+      for (int i = 0; i < NU; ++i) h[i] = load8<F32, false>(hr, i * W + warp, lane, cols);
       rstd = ld_keep_f32(a.rstd + row);
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         float g[8];
-        load_cols8<VEC>(g, a.gamma, i * W + warp, lane, cols);
+        load_cols8<false>(g, a.gamma, i * W + warp, lane, cols);
         dot += chunk_dot<F32>(dy[i], h[i], g);
       }
     }
@@ -128,17 +124,17 @@ __global__ void __launch_bounds__(512) rmsnorm_grad_held(NormBackward a) {
       const int c = i * W + warp;
       if (c * kChunk >= cols) continue;
       float g[8];
-      load_cols8<VEC>(g, a.gamma, c, lane, cols);
-      if (!EARLY && a.dh != nullptr) dh[0] = load8<F32, VEC>(dhr, c, lane, cols);
-      chunk_grad<F32, VEC>(a, mask, row, c, lane, dy[i], h[i], dh[EARLY ? i : 0], g, rstd, mean,
-                           acc[i]);
+      load_cols8<false>(g, a.gamma, c, lane, cols);
+      Lane8<F32> dh{};
+      if (a.dh != nullptr) dh = load8<F32, false>(dhr, c, lane, cols);
+      chunk_grad<F32, false>(a, mask, row, c, lane, dy[i], h[i], dh, g, rstd, mean, acc[i]);
     }
   }
   if (a.dgamma == nullptr) return;
   float *part = static_cast<float *>(a.workspace) + static_cast<int64_t>(blockIdx.x) * cols;
   if (R == 1) {
 #pragma unroll
-    for (int i = 0; i < NU; ++i) store_cols8<VEC>(part, i * W + warp, lane, cols, acc[i]);
+    for (int i = 0; i < NU; ++i) store_cols8<false>(part, i * W + warp, lane, cols, acc[i]);
     return;
   }
   for (int y = 0; y < R; ++y) {
@@ -148,7 +144,7 @@ __global__ void __launch_bounds__(512) rmsnorm_grad_held(NormBackward a) {
     for (int i = 0; i < NU; ++i) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int col = lane_col<VEC>(i * W + warp, lane, j);
+        const int col = lane_col<false>(i * W + warp, lane, j);
         if (col < cols) sums[col] = y == 0 ? acc[i][j] : sums[col] + acc[i][j];
       }
     }
@@ -171,20 +167,25 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
 // u = dy gamma, the gradient is dh + rstd dy gamma - (rstd^2 mean) h: paired fp32
 // arithmetic, two fused steps a pair.
 //
-// EXACT: aligned rows of 32 NU W units (or short ones).  Otherwise a row may start
-// within a unit and end within one: a CTA takes rows that start at one such place (phase),
-// so that its threads' columns stay the same.  The first and last unit of such a row
-// hold elements of its neighbours (or nothing, which the copy leaves out past the matrix's
-// end); they count as 0 and are not written.
-// Warps of a CTA, at most: 128 registers a thread, or 170 where NU units of inexact rows
-// need them.
-template <bool EXACT, int NU>
-constexpr int kRingWarps = EXACT || NU <= 2 ? 16 : 12;
+// kExact: aligned rows of 32 NU W units.  kWhole: aligned rows of whole units, fewer than
+// that (or short ones): no element of a unit is masked, which bf16 [4096, 11008] takes
+// 72.8 us with, 149 element by element, and fp32 [4096, 5000] 55.5, 61.8 as rows with edges.  kEdges: a row may start within a unit and end within one: a CTA
+// takes rows that start at one such place (phase), so that its threads' columns stay the
+// same.  The first and last unit of such a row hold elements of its neighbours (or
+// nothing, which the copy leaves out past the matrix's end); they count as 0 and are not
+// written.
+enum Rows { kExact, kWhole, kEdges };
 
-template <bool F32, bool EXACT, int NU, int RP>
-__global__ void __launch_bounds__(kRingWarps<EXACT, NU> * 32, 1)
+// Warps of a CTA, at most: 128 registers a thread, or 170 where NU units of rows with edges
+// need them.
+template <Rows HOW, int NU>
+constexpr int kRingWarps = HOW != kEdges || NU <= 2 ? 16 : 12;
+
+template <bool F32, Rows HOW, int NU, int RP>
+__global__ void __launch_bounds__(kRingWarps<HOW, NU> * 32, 1)
 rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
   pdl_enter();
+  constexpr bool EDGES = HOW == kEdges;
   constexpr int E = Unit<F32>::E, ES = 16 / E, kUnits = 32 * E;  // columns of a warp's unit
   __shared__ float red[2][16][RP][16];  // [round & 1][row group][row][warp]
   extern __shared__ __align__(16) unsigned char ring[];
@@ -201,10 +202,10 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
   const uint32_t begin = cls + classes * per * R * RP * (blockIdx.x / classes);
   uint32_t row = begin + classes * (threadIdx.y * per + sub);
   const int rounds = begin < rows ? static_cast<int>((rows - begin - 1) / hop + 1) : 0;
-  const int phase = EXACT ? 0 : static_cast<int>((cls * a.ld_h) & (E - 1));
-  // a lane's first unit, and columns from one to the next (inexact rows: a warp's chunks
+  const int phase = !EDGES ? 0 : static_cast<int>((cls * a.ld_h) & (E - 1));
+  // a lane's first unit, and columns from one to the next (rows with edges: a warp's chunks
   // follow one another, as their mask goes on from each to the next)
-  const int chunk0 = EXACT ? warp : warp * NU, chunk_step = EXACT ? W : 1;
+  const int chunk0 = EDGES ? warp * NU : warp, chunk_step = EDGES ? 1 : W;
   const int col0 = chunk0 * kUnits + at * E - phase, unit_cols = chunk_step * kUnits;
 
   const int row_bytes = NU * T * 16, input_bytes = RP * row_bytes;
@@ -217,10 +218,9 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       const int left = cols - (col0 + i * unit_cols);
-      if (EXACT || left >= E) {
-        if (EXACT && lg < 5 && at * E >= cols) continue;
+      if (HOW == kExact || (HOW == kWhole ? left > 0 : left >= E)) {
         cp_async_16(dst + i * (T * 16), src + i * ES * unit_cols);
-      } else if (left > 0) {
+      } else if (EDGES && left > 0) {
         cp_async_16_part(dst + i * (T * 16), src + i * ES * unit_cols, ES * left);
       }
     }
@@ -245,10 +245,10 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
     const uint4 u = lds_u4(slot + n * input_bytes + p * row_bytes + i * (T * 16));
     Unit<F32> v;
     v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
-    if constexpr (!EXACT) {
-      const int col = col0 + i * unit_cols;
+    const int col = col0 + i * unit_cols;
+    if constexpr (EDGES) {
       if (col < 0 || col + E > cols) v.clip(-col, cols - col);
-    } else if (lg < 5 && at * E >= cols) {
+    } else if (HOW == kWhole && col >= cols) {
       v.w[0] = v.w[1] = v.w[2] = v.w[3] = 0;
     }
     return v;
@@ -332,12 +332,12 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
       const float b = -(dot[p] * over * rstd[p]) * rstd[p] * rstd[p];
       const uint64_t rstd2 = pack_f32x2(rstd[p], rstd[p]), b2 = pack_f32x2(b, b);
       uint32_t before = 0;
-      if (!EXACT && drop && chunk0 > 0) before = kept_group<E>(mask, r, chunk0 * 32 - 1);
+      if (EDGES && drop && chunk0 > 0) before = kept_group<E>(mask, r, chunk0 * 32 - 1);
       char *const out_x = row_of<F32>(a.dx, r, a.ld_dx), *const out_r = row_of<F32>(a.dres, r, a.ld_dres);
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         const int c = chunk0 + i * chunk_step, col = col0 + i * unit_cols;
-        if (!EXACT && c * kUnits - phase >= cols) continue;
+        if (HOW != kExact && c * kUnits - phase >= cols) continue;
         const Unit<F32> dy = unit(0, p, i), h = unit(1, p, i);
         Unit<F32> dh{};
         if (up) dh = unit(2, p, i);
@@ -352,17 +352,17 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
           d[2 * j + 1] = f32x2_hi(v);
         }
         Unit<F32> out;
-        const int bound = EXACT && lg == 5 ? INT32_MAX : cols;
+        const int bound = HOW == kExact ? INT32_MAX : cols;
         if (drop) {
           if (a.dres != nullptr) {
             out.set(d);
-            out.template store<EXACT>(out_r, col, bound);
+            out.template store<!EDGES>(out_r, col, bound);
           }
-          if constexpr (!EXACT) drop_unit_phase<E>(d, mask, r, c * 32 + lane, lane, phase, before);
+          if constexpr (EDGES) drop_unit_phase<E>(d, mask, r, c * 32 + lane, lane, phase, before);
           else drop_unit<E>(d, mask, r, c * 32 + at);
         }
         out.set(d);
-        out.template store<EXACT>(out_x, col, bound);
+        out.template store<!EDGES>(out_x, col, bound);
       }
     }
     row += hop;
@@ -386,7 +386,7 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
         for (int o = 16; o >= 1 << lg; o >>= 1) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
       }
       const int col = col0 + i * unit_cols;
-      if constexpr (EXACT) {  // 16-byte pieces: a float an access cost 3 us at 8192 columns
+      if constexpr (!EDGES) {  // 16-byte pieces: a float an access cost 3 us at 8192 columns
         if (sub != 0 || col >= cols) continue;
 #pragma unroll
         for (int q = 0; q < E / 4; ++q) {
@@ -403,7 +403,7 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
       }
     }
   }
-  if constexpr (!EXACT) {
+  if constexpr (EDGES) {
     __syncthreads();
     for (int col = tid; col < cols; col += T) part[col] = sums[col];
   }
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_join(const float *partial, 
 // The ring's launch; W = 0: the row does not fit.
 struct RingShape {
   int units, W, R, rp, lg, stages, classes;
-  bool exact;
+  Rows how;
   int64_t grid;
   size_t smem;
 };
@@ -509,25 +509,26 @@ RingShape ring_shape(const NormBackward &a, int sm_count, int smem_max) {
   const int64_t rem = a.rows == 1 ? 0 : a.ld_h & (E - 1);
   g.classes = rem == 0 ? 1 : rem & 1 ? E : rem & 2 ? E / 2 : 2;
   const int chunks = static_cast<int>((a.cols + (g.classes > 1 ? E - 1 : 0) + kUnits - 1) / kUnits);
+  const bool whole = g.classes == 1 && a.cols % E == 0;
   g.lg = 5;
-  if (g.classes == 1 && a.cols % E == 0)
+  if (whole)
     while (g.lg > 0 && (E << g.lg >> 1) >= a.cols) --g.lg;
   // Two rows at a time, one with dropout (with two its generator's code, twice, costs more
   // than they gain: bf16 [16384, 4096] 121 us against 105) or where two do not fit.  Without:
-  // [8192, 8192] 66.4 us against 73, 78 with a reduction for each.
+  // [8192, 8192] 64.2 us against 73.
   g.rp = a.drop.rng != nullptr || chunks > 32 ? 1 : 2;
   g.units = chunks <= 4 ? 1 : chunks <= 32 ? 2 : 4;
   int warps = 16;
   const auto fit = [&](int units) {
     g.units = units;
     g.W = (chunks + units - 1) / units;
-    g.exact = g.classes == 1 && (g.lg < 5 || a.cols == static_cast<int64_t>(kUnits) * units * g.W);
-    warps = g.exact || units <= 2 ? 16 : 12;
+    g.how = !whole ? kEdges : a.cols == static_cast<int64_t>(kUnits) * units * g.W ? kExact : kWhole;
+    warps = whole || units <= 2 ? 16 : 12;
     return warps / g.W * g.W;
   };
-  // inexact rows of 9 to 11 warps leave the others idle ([8192, 4097]: 84 us, 64 so)
-  if (fit(g.units) < 12 && g.units == 2 && !g.exact) fit(3);
-  if (g.W > warps || (!F32 && g.units == 4 && !g.exact)) return RingShape{};
+  // rows with edges of 9 to 11 warps leave the others idle ([8192, 4097]: 84 us, 64 so)
+  if (fit(g.units) < 12 && g.units == 2 && !whole) fit(3);
+  if (g.W > warps || (!F32 && g.units == 4 && !whole)) return RingShape{};
   const int64_t rows = (a.rows + g.classes - 1) / g.classes, ctas = std::max(1, sm_count / g.classes);
   const int64_t per = (32 >> g.lg) * g.rp, groups = (rows + per - 1) / per;
   g.R = static_cast<int>(std::min<int64_t>(std::min(15, warps / g.W), (groups + ctas - 1) / ctas));
@@ -539,27 +540,30 @@ RingShape ring_shape(const NormBackward &a, int sm_count, int smem_max) {
   return g;
 }
 
-template <bool F32, bool EXACT, int NU, int RP>
+template <bool F32, Rows HOW, int NU, int RP>
 cudaError_t launch_ring_of(const NormBackward &a, const RingShape &g, cudaStream_t s) {
-  const auto kern = rmsnorm_grad_ring<F32, EXACT, NU, RP>;
+  const auto kern = rmsnorm_grad_ring<F32, HOW, NU, RP>;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kern), g.smem);
   if (e != cudaSuccess) return e;
   return launch_k(kern, dim3(static_cast<unsigned>(g.grid)), dim3(32 * g.W, g.R), g.smem, s, 0, a, g.stages,
                   g.classes, g.lg);
 }
 
+template <bool F32, Rows HOW>
+cudaError_t launch_ring_how(const NormBackward &a, const RingShape &g, cudaStream_t s) {
+  if (g.units == 1) return g.rp == 1 ? launch_ring_of<F32, HOW, 1, 1>(a, g, s) : launch_ring_of<F32, HOW, 1, 2>(a, g, s);
+  if (g.units == 2) return g.rp == 1 ? launch_ring_of<F32, HOW, 2, 1>(a, g, s) : launch_ring_of<F32, HOW, 2, 2>(a, g, s);
+  if constexpr (HOW == kEdges)
+    if (g.units == 3) return g.rp == 1 ? launch_ring_of<F32, HOW, 3, 1>(a, g, s) : launch_ring_of<F32, HOW, 3, 2>(a, g, s);
+  if constexpr (HOW != kEdges || F32) return launch_ring_of<F32, HOW, 4, 1>(a, g, s);
+  return cudaErrorInvalidValue;  // ring_shape gives no such shape
+}
+
 template <bool F32>
 cudaError_t launch_ring(const NormBackward &a, const RingShape &g, cudaStream_t s) {
-  if (g.exact) {
-    if (g.units == 1) return g.rp == 1 ? launch_ring_of<F32, true, 1, 1>(a, g, s) : launch_ring_of<F32, true, 1, 2>(a, g, s);
-    if (g.units == 2) return g.rp == 1 ? launch_ring_of<F32, true, 2, 1>(a, g, s) : launch_ring_of<F32, true, 2, 2>(a, g, s);
-    return launch_ring_of<F32, true, 4, 1>(a, g, s);
-  }
-  if (g.units == 1) return g.rp == 1 ? launch_ring_of<F32, false, 1, 1>(a, g, s) : launch_ring_of<F32, false, 1, 2>(a, g, s);
-  if (g.units == 2) return g.rp == 1 ? launch_ring_of<F32, false, 2, 1>(a, g, s) : launch_ring_of<F32, false, 2, 2>(a, g, s);
-  if constexpr (F32)
-    if (g.units == 4) return launch_ring_of<F32, false, 4, 1>(a, g, s);
-  return g.rp == 1 ? launch_ring_of<F32, false, 3, 1>(a, g, s) : launch_ring_of<F32, false, 3, 2>(a, g, s);
+  return g.how == kExact   ? launch_ring_how<F32, kExact>(a, g, s)
+         : g.how == kWhole ? launch_ring_how<F32, kWhole>(a, g, s)
+                           : launch_ring_how<F32, kEdges>(a, g, s);
 }
 
 // Shapes of the other launches, which the workspace follows.
@@ -568,10 +572,10 @@ struct GradShape {
   int64_t grid;     // CTAs, or the looped form's runs of rows
 };
 
-GradShape held_shape(int64_t rows, int64_t cols, bool f32, int sm_count) {
+GradShape held_shape(int64_t rows, int64_t cols, int sm_count) {
   const int chunks = static_cast<int>((cols + kChunk - 1) / kChunk);
   GradShape g{};
-  g.units = chunks > 32 ? 4 : chunks <= 2 ? 1 : 2;
+  g.units = chunks <= 2 ? 1 : 2;
   g.W = (chunks + g.units - 1) / g.units;
   g.R = g.W >= 8 ? 1 : 8 / g.W;
   const int64_t per = g.W * g.R >= 16 ? 1 : 2;
@@ -601,15 +605,11 @@ cudaError_t launch_grad(const NormBackward &a, bool held, bool phase, int sm_cou
     e = launch_ring<F32>(a, rs, s);
     P = rs.grid;
   } else if (held) {
-    const GradShape g = held_shape(a.rows, a.cols, F32, sm_count);
+    const GradShape g = held_shape(a.rows, a.cols, sm_count);
     const dim3 grid(static_cast<unsigned>(g.grid)), block(32 * g.W, g.R);
     const size_t smem = g.R > 1 ? a.cols * 4 : 0;
-    if constexpr (VEC) {  // shorter ones take the ring
-      e = launch_k(rmsnorm_grad_held<F32, true, F32 ? 2 : 4>, grid, block, smem, s, 0, a);
-    } else {
-      e = g.units == 1 ? launch_k(rmsnorm_grad_held<F32, VEC, 1>, grid, block, smem, s, 0, a)
-                       : launch_k(rmsnorm_grad_held<F32, VEC, 2>, grid, block, smem, s, 0, a);
-    }
+    e = g.units == 1 ? launch_k(rmsnorm_grad_held<F32, 1>, grid, block, smem, s, 0, a)
+                     : launch_k(rmsnorm_grad_held<F32, 2>, grid, block, smem, s, 0, a);
     P = g.grid;
   } else {
     float *dots = static_cast<float *>(a.workspace);
@@ -632,11 +632,11 @@ cudaError_t launch_grad(const NormBackward &a, bool held, bool phase, int sm_cou
 
 }  // namespace
 
-bool rmsnorm_grad_held_ok(int64_t cols, bool f32, bool vec) {
-  return cols <= kChunk * 16 * (!f32 && vec ? 4 : 2);
+bool rmsnorm_grad_held_ok(int64_t cols, bool f32, bool whole) {
+  return cols <= kChunk * 16 * (!f32 && whole ? 4 : 2);
 }
 
-size_t rmsnorm_grad_workspace(int64_t rows, int64_t cols, bool f32, bool held, int sm_count) {
+size_t rmsnorm_grad_workspace(int64_t rows, int64_t cols, bool held, int sm_count) {
   // a share a CTA: at most two an SM, and at most a CTA a row, or in the ring a row of the
   // longest of 8 classes for each of them
   if (held) return static_cast<size_t>(std::min<int64_t>((rows + 7) / 8 * 8, std::max(8, 2 * sm_count)) * cols * 4);
