@@ -168,12 +168,12 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
 // arithmetic, two fused steps a pair.
 //
 // kExact: aligned rows of 32 NU W units.  kWhole: aligned rows of whole units, fewer than
-// that (or short ones): no element of a unit is masked, which bf16 [4096, 11008] takes
-// 72.8 us with, 149 element by element, and fp32 [4096, 5000] 55.5, 61.8 as rows with edges.  kEdges: a row may start within a unit and end within one: a CTA
-// takes rows that start at one such place (phase), so that its threads' columns stay the
-// same.  The first and last unit of such a row hold elements of its neighbours (or
-// nothing, which the copy leaves out past the matrix's end); they count as 0 and are not
-// written.
+// that (or short ones), no element of a unit masked: bf16 [4096, 11008] 63.9 us (149 element
+// by element), fp32 [4096, 5000] 54.4 (61.8 as rows with edges).  kEdges: a row may start
+// within a unit and end within one: a CTA takes rows that start at one such place (phase),
+// so that its threads' columns stay the same.  The first and last unit of such a row hold
+// elements of its neighbours (or nothing, which the copy leaves out past the matrix's end);
+// they count as 0 and are not written.
 enum Rows { kExact, kWhole, kEdges };
 
 // Warps of a CTA, at most: 128 registers a thread, or 170 where NU units of rows with edges
@@ -517,7 +517,9 @@ RingShape ring_shape(const NormBackward &a, int sm_count, int smem_max) {
   // than they gain: bf16 [16384, 4096] 121 us against 105) or where two do not fit.  Without:
   // [8192, 8192] 64.2 us against 73.
   g.rp = a.drop.rng != nullptr || chunks > 32 ? 1 : 2;
-  g.units = chunks <= 4 ? 1 : chunks <= 32 ? 2 : 4;
+  // Aligned rows of 33 to 48 chunks: three units a lane and up to 16 warps, not four and up
+  // to 12 ([4096, 11008] 63.9 us, 72.8 with four).
+  g.units = chunks <= 4 ? 1 : chunks <= 32 ? 2 : whole && chunks <= 48 ? 3 : 4;
   int warps = 16;
   const auto fit = [&](int units) {
     g.units = units;
@@ -526,8 +528,10 @@ RingShape ring_shape(const NormBackward &a, int sm_count, int smem_max) {
     warps = whole || units <= 2 ? 16 : 12;
     return warps / g.W * g.W;
   };
-  // rows with edges of 9 to 11 warps leave the others idle ([8192, 4097]: 84 us, 64 so)
-  if (fit(g.units) < 12 && g.units == 2 && !whole) fit(3);
+  // Rows of 9 to 11 warps leave the others idle: three units a lane instead.  [8192, 4097] 84 us,
+  // 64 so; one aligned row a round (dropout, [8192, 5120]) 77.4, 74.2 so.  Two of them
+  // a round do not gain: [6000, 5120] 42.0, 45.9 so.
+  if (fit(g.units) < 12 && g.units == 2 && (!whole || g.rp == 1)) fit(3);
   if (g.W > warps || (!F32 && g.units == 4 && !whole)) return RingShape{};
   const int64_t rows = (a.rows + g.classes - 1) / g.classes, ctas = std::max(1, sm_count / g.classes);
   const int64_t per = (32 >> g.lg) * g.rp, groups = (rows + per - 1) / per;
@@ -554,7 +558,8 @@ cudaError_t launch_ring_how(const NormBackward &a, const RingShape &g, cudaStrea
   if (g.units == 1) return g.rp == 1 ? launch_ring_of<F32, HOW, 1, 1>(a, g, s) : launch_ring_of<F32, HOW, 1, 2>(a, g, s);
   if (g.units == 2) return g.rp == 1 ? launch_ring_of<F32, HOW, 2, 1>(a, g, s) : launch_ring_of<F32, HOW, 2, 2>(a, g, s);
   if constexpr (HOW == kEdges)
-    if (g.units == 3) return g.rp == 1 ? launch_ring_of<F32, HOW, 3, 1>(a, g, s) : launch_ring_of<F32, HOW, 3, 2>(a, g, s);
+    if (g.units == 3 && g.rp == 2) return launch_ring_of<F32, HOW, 3, 2>(a, g, s);
+  if (g.units == 3) return launch_ring_of<F32, HOW, 3, 1>(a, g, s);
   if constexpr (HOW != kEdges || F32) return launch_ring_of<F32, HOW, 4, 1>(a, g, s);
   return cudaErrorInvalidValue;  // ring_shape gives no such shape
 }

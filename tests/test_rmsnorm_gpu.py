@@ -620,11 +620,13 @@ RINGS = {"bf16": [(900, 8, 0), (1900, 72, 0), (700, 128, 8), (1300, 256, 0), (65
                   (640, 768, 0), (641, 769, 0), (500, 1024, 0), (310, 1030, 2), (311, 1500, 4),
                   (400, 2048, 0), (333, 2051, 1), (330, 4098, 6), (500, 4100, 0), (320, 4352, 0),
                   (5, 4097, 0), (9, 515, 0), (317, 5120, 0), (312, 5121, 7), (306, 8186, 6),
-                  (308, 8192, 0), (155, 9216, 0), (160, 16384, 0), (153, 10000, 0)],
+                  (308, 8192, 0), (155, 9216, 0), (160, 16384, 0), (153, 10000, 0),
+                  (310, 5376, 0), (160, 8200, 0), (155, 11008, 0), (154, 12288, 0), (157, 13824, 8)],
          "f32": [(900, 4, 0), (1000, 60, 0), (700, 130, 2), (640, 512, 0), (620, 516, 0),
                  (610, 517, 0), (400, 1024, 4), (333, 2050, 0), (310, 2049, 0), (320, 2176, 0),
                  (308, 4096, 0), (3, 4097, 0), (307, 4098, 0), (160, 5000, 0), (155, 6143, 0),
-                 (156, 8192, 0), (153, 7001, 1)]}
+                 (156, 8192, 0), (153, 7001, 1), (153, 4104, 8),
+                 (155, 6144, 0), (154, 6600, 0)]}
 
 
 @pytest.mark.parametrize("dtype,rows,cols,extra", [(d, *s) for d in RINGS for s in RINGS[d]])
