@@ -177,9 +177,10 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
 enum Rows { kExact, kWhole, kEdges };
 
 // Warps of a CTA, at most: 128 registers a thread, or 170 where NU units of rows with edges
-// need them.
+// need them, or 80 where one aligned unit takes no more ([65536, 1024] 79.0 us, 81.3 with 16
+// warps; [32768, 768] 27.9, 29.8).
 template <Rows HOW, int NU>
-constexpr int kRingWarps = HOW != kEdges || NU <= 2 ? 16 : 12;
+constexpr int kRingWarps = HOW != kEdges && NU == 1 ? 24 : HOW != kEdges || NU <= 2 ? 16 : 12;
 
 template <bool F32, Rows HOW, int NU, int RP>
 __global__ void __launch_bounds__(kRingWarps<HOW, NU> * 32, 1)
@@ -370,42 +371,48 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
     if (slot == end) slot = base;
   }
   if (a.dgamma == nullptr) return;
-  // a warp's rows, then the row groups one after the other, in the ring's memory
+  // a warp's rows, then the row groups in their order, in the ring's memory (a group's
+  // columns are at most half of its units there).  [262144, 128] 34.7 us, 42.3 with the
+  // groups one after the other.
   float *part = static_cast<float *>(a.workspace) + static_cast<int64_t>(blockIdx.x) * cols;
-  float *sums = reinterpret_cast<float *>(ring);
+  float *const sums = reinterpret_cast<float *>(ring), *const mine = sums + threadIdx.y * cols;
+  for (int o = 16; o >= 1 << lg; o >>= 1)
+#pragma unroll
+    for (int j = 0; j < E / 2; ++j)  // short rows: NU = 1
+      acc[0][j] = add_f32x2(acc[0][j], __shfl_xor_sync(0xffffffffu, acc[0][j], o));
   cp_async_wait<0>();
-  for (int y = 0; y < R; ++y) {
-    __syncthreads();
-    if (static_cast<int>(threadIdx.y) != y) continue;
+  __syncthreads();
+  // 16-byte pieces where columns allow: a float an access cost 3 us at 8192 columns
 #pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      float v[E];
+  for (int i = 0; i < NU; ++i) {
+    const int col = col0 + i * unit_cols;
+    if constexpr (!EDGES) {
+      if (sub != 0 || col >= cols) continue;
+      float *const to = (R == 1 ? part : mine) + col;
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        v[j] = j & 1 ? f32x2_hi(acc[i][j >> 1]) : f32x2_lo(acc[i][j >> 1]);
-        for (int o = 16; o >= 1 << lg; o >>= 1) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
-      }
-      const int col = col0 + i * unit_cols;
-      if constexpr (!EDGES) {  // 16-byte pieces: a float an access cost 3 us at 8192 columns
-        if (sub != 0 || col >= cols) continue;
+      for (int q = 0; q < E / 4; ++q)
+        reinterpret_cast<float4 *>(to)[q] =
+            make_float4(f32x2_lo(acc[i][2 * q]), f32x2_hi(acc[i][2 * q]), f32x2_lo(acc[i][2 * q + 1]),
+                        f32x2_hi(acc[i][2 * q + 1]));
+    } else {
 #pragma unroll
-        for (int q = 0; q < E / 4; ++q) {
-          float4 w = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-          float4 *const at_sums = reinterpret_cast<float4 *>(sums + col + 4 * q);
-          if (y > 0) w = add4(w, *at_sums);
-          if (y + 1 < R) *at_sums = w;
-          else *reinterpret_cast<float4 *>(part + col + 4 * q) = w;
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-          if (col + j >= 0 && col + j < cols) sums[col + j] = y == 0 ? v[j] : sums[col + j] + v[j];
-      }
+      for (int j = 0; j < E; ++j)
+        if (col + j >= 0 && col + j < cols) mine[col + j] = j & 1 ? f32x2_hi(acc[i][j >> 1]) : f32x2_lo(acc[i][j >> 1]);
     }
   }
-  if constexpr (EDGES) {
-    __syncthreads();
-    for (int col = tid; col < cols; col += T) part[col] = sums[col];
+  if (!EDGES && R == 1) return;
+  __syncthreads();
+  constexpr int kStep = EDGES ? 1 : 4;
+  for (int col = tid * kStep; col < cols; col += T * kStep) {
+    if constexpr (EDGES) {
+      float v = sums[col];
+      for (int y = 1; y < R; ++y) v += sums[y * cols + col];
+      part[col] = v;
+    } else {
+      float4 v = *reinterpret_cast<const float4 *>(sums + col);
+      for (int y = 1; y < R; ++y) v = add4(v, *reinterpret_cast<const float4 *>(sums + y * cols + col));
+      *reinterpret_cast<float4 *>(part + col) = v;
+    }
   }
 }
 
@@ -525,7 +532,7 @@ RingShape ring_shape(const NormBackward &a, int sm_count, int smem_max) {
     g.units = units;
     g.W = (chunks + units - 1) / units;
     g.how = !whole ? kEdges : a.cols == static_cast<int64_t>(kUnits) * units * g.W ? kExact : kWhole;
-    warps = whole || units <= 2 ? 16 : 12;
+    warps = whole && units == 1 ? 24 : whole || units <= 2 ? 16 : 12;
     return warps / g.W * g.W;
   };
   // Rows of 9 to 11 warps leave the others idle: three units a lane instead.  [8192, 4097] 84 us,
@@ -535,7 +542,7 @@ RingShape ring_shape(const NormBackward &a, int sm_count, int smem_max) {
   if (g.W > warps || (!F32 && g.units == 4 && !whole)) return RingShape{};
   const int64_t rows = (a.rows + g.classes - 1) / g.classes, ctas = std::max(1, sm_count / g.classes);
   const int64_t per = (32 >> g.lg) * g.rp, groups = (rows + per - 1) / per;
-  g.R = static_cast<int>(std::min<int64_t>(std::min(15, warps / g.W), (groups + ctas - 1) / ctas));
+  g.R = static_cast<int>(std::min<int64_t>(g.W > 1 ? std::min(15, warps / g.W) : warps, (groups + ctas - 1) / ctas));
   g.grid = std::min<int64_t>((groups + g.R - 1) / g.R, ctas) * g.classes;
   const size_t stage = static_cast<size_t>(a.dh ? 3 : 2) * g.units * 32 * g.W * g.R * 16 * g.rp;
   g.stages = static_cast<int>(std::min<size_t>(g.rp == 2 ? 2 : 3, (smem_max - 5120) / stage));
