@@ -98,6 +98,13 @@ __device__ __forceinline__ void store_unit_e4m3(char *row, int col, int cols, co
       asm volatile("st.global.cs.u8 [%0], %1;" ::"l"(row + col + j), "r"(w[j >> 2] >> (8 * (j & 3))) : "memory");
 }
 
+// The largest magnitude of three (NaN if one is).
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ float warp_max(float v) {
   float m;
   asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
@@ -436,7 +443,10 @@ rmsnorm_phase(NormForward a) {
 }
 
 // Rows of at most a chunk, aligned: 1 << lg lanes hold a row, a warp U times 32 >> lg
-// rows at a time, with one reading of gamma; no barrier.
+// rows at a time, with one reading of gamma; no barrier.  Instructions bound it (e4m3 out,
+// [524288, 128]: 43.2 us, a copy 30): the rows' steps of a reduction stand side by side, and
+// the root and the reciprocals are the approximate ones, off by 2 units in the last place and
+// by 1 (exact reciprocals 45.3), which is less than a sum of 256 columns may be off by.
 template <bool F32, int U, bool SUM, bool QUANT>
 __global__ void __launch_bounds__(256) rmsnorm_short(NormForward a, int lg) {
   pdl_enter();
@@ -444,11 +454,17 @@ __global__ void __launch_bounds__(256) rmsnorm_short(NormForward a, int lg) {
   const int cols = static_cast<int>(a.cols);
   const int64_t first =
       (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * (U * per) + sub;
+  const auto at_row = [&](const void *m, int64_t ld, int es) {
+    return static_cast<char *>(const_cast<void *>(m)) + first * ld * es;
+  };
+  constexpr int ES = F32 ? 4 : 2;
+  const char *const xr = at_row(a.x, a.ldx, ES);
+  const int64_t xs = per * a.ldx * ES;
   Lane8<F32> h[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t row = first + u * per;
-    if (row < a.rows) h[u] = load8<F32, true>(row_of<F32>(a.x, row, a.ldx), 0, at, cols);
+    if (row < a.rows) h[u] = load8<F32, true>(xr + u * xs, 0, at, cols);
     else h[u].zero();
   }
   if constexpr (SUM) {
@@ -473,42 +489,69 @@ __global__ void __launch_bounds__(256) rmsnorm_short(NormForward a, int lg) {
   float g[8];
   load_cols8<true>(g, a.gamma, 0, at, cols);
   const float over = 1.0f / static_cast<float>(cols);
+  float ss[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t row = first + u * per;
-    const bool live = row < a.rows;
-    float v[8];
     const uint64_t squares = squares8(h[u], 0);
-    float ss = f32x2_lo(squares) + f32x2_hi(squares);
-    for (int o = 1 << lg >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    // (an exact root and reciprocal are a large part of a short row's work; the
-    // approximate ones, off by 2 units in the last place, cost less than its few additions)
-    const float rstd = rsqrtf(fmaf(ss, over, a.eps));
-    normed8(v, h[u], rstd, g);
-    if (live && a.rstd != nullptr && at == 0) a.rstd[row] = rstd;
-    if constexpr (QUANT) {
-      char *yr = static_cast<char *>(a.y) + row * a.ldy;
-      float s;
-      if (a.scale_mode == FR_SCALE_GIVEN) {
-        s = ld_keep_f32(a.scale);
-      } else {  // groups of 128 columns are 16 lanes
-        float m = 0.0f;
+    ss[u] = f32x2_lo(squares) + f32x2_hi(squares);
+  }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[j]));
-        const bool row_scale = a.scale_mode == FR_SCALE_ROW;
-        const int lanes = !row_scale && lg > 4 ? 16 : 1 << lg;
-        for (int o = lanes >> 1; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-        s = scale_for(m);
-        const int group = row_scale ? 0 : at >> 4;
-        if (live && (at & (lanes - 1)) == 0 && group * kGroup < cols)
-          a.scale[row * a.scale_row + (row_scale ? 0 : group * a.scale_col)] = s;
-      }
-      const float inv[2] = {1.0f / s, 1.0f / s};
-      if (live) store8_e4m3<true>(yr, 0, at, cols, v, inv);
-    } else if (live) {
+  for (int k = 4; k >= 0; --k)
+    if (k < lg)
+#pragma unroll
+      for (int u = 0; u < U; ++u) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], 1 << k);
+  if constexpr (!QUANT) {
+    char *const yr = at_row(a.y, a.ldy, ES);
+    const int64_t ys = per * a.ldy * ES;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = first + u * per;
+      if (row >= a.rows) break;
+      const float rstd = rsqrtf(fmaf(ss[u], over, a.eps));
+      float v[8];
+      normed8(v, h[u], rstd, g);
+      if (a.rstd != nullptr && at == 0) a.rstd[row] = rstd;
       Lane8<F32> y;
       y.set(v);
-      store8<F32, true>(row_of<F32>(a.y, row, a.ldy), 0, at, cols, y);
+      store8<F32, true>(yr + u * ys, 0, at, cols, y);
+    }
+  } else {
+    float v[U][8], s[U];
+    const bool row_scale = a.scale_mode == FR_SCALE_ROW;
+    const int lanes_lg = !row_scale && lg > 4 ? 4 : lg;  // groups of 128 columns are 16 lanes
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      ss[u] = rsqrtf(fmaf(ss[u], over, a.eps));
+      normed8(v[u], h[u], ss[u], g);
+      s[u] = max_nan(max_abs(max_abs(v[u][0], v[u][1], v[u][2]), v[u][3], v[u][4]),
+                     max_abs(v[u][5], v[u][6], v[u][7]));
+    }
+    if (a.scale_mode == FR_SCALE_GIVEN) {
+      const float given = ld_keep_f32(a.scale);
+#pragma unroll
+      for (int u = 0; u < U; ++u) s[u] = given;
+    } else {
+#pragma unroll
+      for (int k = 4; k >= 0; --k)
+        if (k < lanes_lg)
+#pragma unroll
+          for (int u = 0; u < U; ++u) s[u] = max_nan(s[u], __shfl_xor_sync(0xffffffffu, s[u], 1 << k));
+    }
+    const int group = row_scale ? 0 : at >> 4;
+    const bool writes = a.scale_mode != FR_SCALE_GIVEN && (at & ((1 << lanes_lg) - 1)) == 0 && group * kGroup < cols;
+    char *const yr = at_row(a.y, a.ldy, 1);
+    const int64_t ys = per * a.ldy;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = first + u * per;
+      if (row >= a.rows) break;
+      if (a.rstd != nullptr && at == 0) a.rstd[row] = ss[u];
+      if (a.scale_mode != FR_SCALE_GIVEN) s[u] = scale_for(s[u]);
+      if (writes) a.scale[row * a.scale_row + (row_scale ? 0 : group * a.scale_col)] = s[u];
+      float k;
+      asm("rcp.approx.f32 %0, %1;" : "=f"(k) : "f"(s[u]));
+      const float inv[2] = {k, k};
+      store8_e4m3<true>(yr + u * ys, 0, at, cols, v[u], inv);
     }
   }
 }
@@ -596,17 +639,27 @@ __global__ void __launch_bounds__(256, HOW == kAligned && RES ? 3 : 4) dropout_c
 
 constexpr int kHeldChunks = 64;  // of a row, at most: 32 warps with 2 each
 
-template <bool F32, bool SUM, bool QUANT>
-cudaError_t launch_short(const NormForward &a, cudaStream_t s) {
-  int lg = 5;
-  while (lg > 0 && (8 << lg >> 1) >= a.cols) --lg;
-  // two rows a lane: loads in flight (us with 1, 2, 4, 8: bf16 [524288, 128] 57.6, 47.2,
-  // 48.8, 51.6; 64 columns and a residual 43.4, 40.4, 41.3, 49.2; e4m3 out 72.4, 66.4,
-  // 63.8, 70.3; fp32 64 columns 40.1, 40.5, 40.9, 43.5)
-  constexpr int U = 2;
+template <bool F32, int U, bool SUM, bool QUANT>
+cudaError_t launch_short_of(const NormForward &a, int lg, cudaStream_t s) {
   const int64_t per = 8 * U * static_cast<int64_t>(32 >> lg);
   return launch_k(rmsnorm_short<F32, U, SUM, QUANT>, dim3(static_cast<unsigned>((a.rows + per - 1) / per)),
                   dim3(256), 0, s, 0, a, lg);
+}
+
+// Rows a lane: one while more would leave fewer than two CTAs an SM (us with 1, 2, 4: bf16
+// [2048, 128] 1.4, 1.6, 1.7; [8192, 128] 2.0, 2.5, 2.7; e4m3 out [16384, 128] 2.9, 3.0, 3.6),
+// else four, which share the fixed work (bf16 [32768, 128] 3.3, 3.4, 3.0; [524288, 128]
+// 44.8, 41.6, 40.3; e4m3 out 62.0, 50.0, 43.2, with eight 53.1; bf16 with a residual to e4m3,
+// [262144, 128], 43.8, 37.8, 37.2), or two where a residual's sum leaves less room (bf16 with
+// dropout 43.5, 41.1, 42.0; fp32 to e4m3 64.4, 64.5, 66.2).
+template <bool F32, bool SUM, bool QUANT>
+cudaError_t launch_short(const NormForward &a, int sm_count, cudaStream_t s) {
+  int lg = 5;
+  while (lg > 0 && (8 << lg >> 1) >= a.cols) --lg;
+  constexpr int MANY = SUM && !(QUANT && !F32) ? 2 : 4;
+  if (a.rows < 2 * 8 * MANY * static_cast<int64_t>(32 >> lg) * sm_count)
+    return launch_short_of<F32, 1, SUM, QUANT>(a, lg, s);
+  return launch_short_of<F32, MANY, SUM, QUANT>(a, lg, s);
 }
 
 // How many chunks a warp holds: few warps a row make the row's reduction cheap and the
@@ -662,7 +715,7 @@ cudaError_t launch_form(const NormForward &a, bool phase, bool held, int sm_coun
   const bool sum = a.h != nullptr;
   if constexpr (VEC)
     if (a.cols <= kChunk)
-      return sum ? launch_short<F32, true, QUANT>(a, s) : launch_short<F32, false, QUANT>(a, s);
+      return sum ? launch_short<F32, true, QUANT>(a, sm_count, s) : launch_short<F32, false, QUANT>(a, sm_count, s);
   if constexpr (!F32 && !VEC)
     if (phase && !(QUANT && a.scale_mode == FR_SCALE_GROUP) && a.cols + 7 <= kChunk * kHeldChunks)
       return sum ? launch_phase<QUANT, true>(a, sm_count, s) : launch_phase<QUANT, false>(a, sm_count, s);

@@ -676,6 +676,25 @@ def test_forward_of_many_rows(dtype, rows, cols, extra):
             assert torch.equal(d.t, h.t) and d.intact()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", [(39011, 64), (19999, 128), (9737, 136), (9801, 256), (38920, 24),
+                                       (16384, 128), (4865, 256)])
+def test_more_short_rows_than_a_warp_takes_at_once(rows, cols, dtype):
+    """The lanes of a warp share rows, several each; with every scale and with none."""
+    x, r = values(rows, cols, dtype, 150), values(rows, cols, dtype, 151, 3.0)
+    gamma, n = vector(cols, 15), rng_of(cols + 10)
+    for res, p in ((None, 0.0), (r, 0.0), (r, 0.2)):
+        kw = dict(p=p, rng=n.cuda(), site=7, residual=None if res is None else res.cuda())
+        what = f"p {p} residual {res is not None}"
+        got = fr.fr_rmsnorm(x.cuda(), gamma.cuda(), EPS, **kw)
+        check_norm(x, res, p, n, 7, got, gamma, what)
+        for quant in ("row", "group", "given"):
+            given = torch.tensor([0.01])
+            got = fr.fr_rmsnorm_quant(x.cuda(), gamma.cuda(), EPS, want_rstd=True,
+                                      scale=given.cuda() if quant == "given" else quant, **kw)
+            check_norm(x, res, p, n, 7, got, gamma, f"{what} {quant}", quant, given)
+
+
 def test_neighbours_of_a_row_do_not_reach_it():
     """A unit at a row's edge holds elements of the rows beside it (or of the gap): whatever
     they are, the row's results are its own."""
