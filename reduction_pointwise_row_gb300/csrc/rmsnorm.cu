@@ -377,14 +377,14 @@ rmsnorm_phase(NormForward a) {
     const char *xr = row_of<false>(a.x, row, a.ldx);
     const int x_left = elements_left(a.rows, row, a.ldx, cols);
 #pragma unroll
-    for (int i = 0; i < NU; ++i) h[i] = load_unit(xr, col0 + i * kChunk, cols, x_left);
+    for (int i = 0; i < NU; ++i) h[i] = load_unit<false>(xr, col0 + i * kChunk, cols, x_left);
     if constexpr (SUM) {
       Lane8<false> res[NU];
       const char *rr = row_of<false>(a.residual, row, a.ldr);
       if (a.residual != nullptr) {
         const int r_left = elements_left(a.rows, row, a.ldr, cols);
 #pragma unroll
-        for (int i = 0; i < NU; ++i) res[i] = load_unit(rr, col0 + i * kChunk, cols, r_left);
+        for (int i = 0; i < NU; ++i) res[i] = load_unit<false>(rr, col0 + i * kChunk, cols, r_left);
       }
       Mask mask{};
       uint32_t before = 0;
@@ -556,15 +556,13 @@ __global__ void __launch_bounds__(256) rmsnorm_short(NormForward a, int lg) {
   }
 }
 
-// Dropout alone.  A warp has NU chunks of a row, one after the other (a CTA's 8 warps a run
-// of 8 NU of them, or R = 8 / W rows), or for short rows (SHORT, not in phase) the same chunk
-// of NU rows; 1 << lg lanes hold an aligned row of at most a chunk (32 of others).
-enum { kScattered, kAligned, kPhase };  // how a lane's elements lie: element by element,
-                                        // in an aligned unit, in a unit of a row in phase
-template <bool F32, int HOW, int NU, bool SHORT, bool RES>
-__global__ void __launch_bounds__(256, HOW == kAligned && RES ? 3 : 4) dropout_chunks(NormForward a, unsigned runs, int lg) {
+// Dropout alone, of aligned rows or element by element.  A warp has NU chunks of a row, one
+// after the other (a CTA's 8 warps a run of 8 NU of them, or R = 8 / W rows), or for short
+// rows (SHORT) the same chunk of NU rows; 1 << lg lanes hold an aligned row of at most a
+// chunk (32 of others).
+template <bool F32, bool VEC, int NU, bool SHORT, bool RES>
+__global__ void __launch_bounds__(256, VEC && RES ? 3 : 4) dropout_chunks(NormForward a, unsigned runs, int lg) {
   pdl_enter();
-  constexpr bool VEC = HOW == kAligned;
   const int lane = threadIdx.x & 31, at = lane & ((1 << lg) - 1), W = blockDim.x >> 5;
   const int cols = static_cast<int>(a.cols);
   const unsigned group = SHORT ? blockIdx.x : blockIdx.x / runs;
@@ -574,9 +572,8 @@ __global__ void __launch_bounds__(256, HOW == kAligned && RES ? 3 : 4) dropout_c
                        (lane >> lg);
   const auto row_at = [&](int i) { return SHORT ? row0 + (static_cast<int64_t>(i * blockDim.y) << (5 - lg)) : row0; };
   const auto chunk_at = [&](int i) { return SHORT ? first : first + i; };
-  const auto phase_at = [&](int i) { return HOW == kPhase ? static_cast<int>(row_at(i) * a.ldx & 7) : 0; };
   const auto has = [&](int i) {  // a warp's lanes agree but for short aligned rows
-    return row_at(i) < a.rows && chunk_at(i) <= (cols - 1 + phase_at(i)) / kChunk;
+    return row_at(i) < a.rows && chunk_at(i) <= (cols - 1) / kChunk;
   };
   Mask mask{};
   if (a.drop.rng != nullptr) mask = mask_of(a.drop);
@@ -586,22 +583,14 @@ __global__ void __launch_bounds__(256, HOW == kAligned && RES ? 3 : 4) dropout_c
     if (!has(i)) continue;
     const int64_t row = row_at(i);
     const char *xr = row_of<F32>(a.x, row, a.ldx), *rr = row_of<F32>(a.residual, row, a.ldr);
-    if constexpr (HOW == kPhase) {
-      const int col = chunk_at(i) * kChunk + lane * 8 - phase_at(i);
-      x[i] = load_unit(xr, col, cols, elements_left(a.rows, row, a.ldx, cols));
-      if constexpr (RES) res[i] = load_unit(rr, col, cols, elements_left(a.rows, row, a.ldr, cols));
-    } else {
-      x[i] = load8<F32, VEC>(xr, chunk_at(i), at, cols);
-      if constexpr (RES) res[i] = load8<F32, VEC>(rr, chunk_at(i), at, cols);
-    }
+    x[i] = load8<F32, VEC>(xr, chunk_at(i), at, cols);
+    if constexpr (RES) res[i] = load8<F32, VEC>(rr, chunk_at(i), at, cols);
   }
   // The generator's work is done while the loads are on their way: bf16 [16384, 4096] 43.7
   // us, 47.2 with each chunk's done when its turn comes.
   uint4 words[NU];
-  uint32_t before = 0;
-  if (a.drop.rng != nullptr) {
-    if (HOW == kPhase) before = kept_before(mask, static_cast<uint32_t>(row0), first);
-    if constexpr (HOW == kAligned) {
+  if constexpr (VEC) {
+    if (a.drop.rng != nullptr) {
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         words[i] = block_of(mask, static_cast<uint32_t>(row_at(i)), chunk_at(i), at);
@@ -619,21 +608,90 @@ __global__ void __launch_bounds__(256, HOW == kAligned && RES ? 3 : 4) dropout_c
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = x[i].at(j);
     if (a.drop.rng != nullptr) {
-      if constexpr (HOW == kPhase) {
-        drop8_phase(v, mask, static_cast<uint32_t>(row), c, lane, phase_at(i), before);
-      } else if constexpr (VEC) {
-        drop8_by<true>(v, mask, words[i], at);
-      } else {
-        drop8<false>(v, mask, static_cast<uint32_t>(row), c, lane);
-      }
+      if constexpr (VEC) drop8_by<true>(v, mask, words[i], at);
+      else drop8<false>(v, mask, static_cast<uint32_t>(row), c, lane);
     }
     if constexpr (RES) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += res[i].at(j);
     }
     x[i].set(v);
-    if constexpr (HOW == kPhase) store_unit<false, true>(yr, c * kChunk + lane * 8 - phase_at(i), cols, x[i]);
-    else store8<F32, VEC>(yr, c, at, cols, x[i]);
+    store8<F32, VEC>(yr, c, at, cols, x[i]);
+  }
+}
+
+// Dropout of rows in phase.  The units of all rows, `units` a row, follow one another over
+// the lanes, so that no length leaves lanes idle: a warp has NU spans of 31 units, one after
+// the other.  A unit's elements lie in two blocks of the mask, its own and the one before,
+// which the lane before has drawn; lane 0 only draws the block before its span.  bf16
+// [1000000, 63] 77 us (a warp a row 309), [16384, 4097] 61.7 (element by element 87.5; the
+// mask's bits, packed and moved, bound it: a copy takes 39.6), fp32 [500000, 63] 47.2 (129.6).
+template <bool F32, int NU, bool RES>
+__global__ void __launch_bounds__(256, 4) dropout_units(NormForward a, int units) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31, cols = static_cast<int>(a.cols);
+  const int64_t begin = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * (NU * 31);
+  int64_t row0;
+  int at0;  // of the unit of lane 1 in the first span
+  if (begin <= UINT32_MAX) {
+    row0 = static_cast<uint32_t>(begin) / static_cast<uint32_t>(units);
+    at0 = static_cast<int>(static_cast<uint32_t>(begin) - static_cast<uint32_t>(row0) * static_cast<uint32_t>(units));
+  } else {
+    row0 = begin / units;
+    at0 = static_cast<int>(begin - row0 * units);
+  }
+  // n / units for n < units + 31 NU
+  const uint32_t over = units > 1 && units < 31 * NU ? 0xFFFFFFFFu / units + 1 : 0;
+  const auto rows_on = [&](int n) {
+    if (units >= 31 * NU) return n >= units ? 1 : 0;
+    return units == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), over));
+  };
+  Mask mask{};
+  if (a.drop.rng != nullptr) mask = mask_of(a.drop);
+  Lane8<F32> x[NU], res[RES ? NU : 1];
+  int64_t row[NU];
+  int col[NU];  // cols: nothing of the row
+  uint32_t own[NU];
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const int n = at0 + 31 * i + lane - 1, on = n < 0 ? 0 : rows_on(n), at = n - on * units;
+    row[i] = row0 + on;
+    const int phase = static_cast<int>(static_cast<uint32_t>(row[i]) * static_cast<uint32_t>(a.ldx)) & 7;
+    col[i] = lane == 0 || row[i] >= a.rows ? cols : at * 8 - phase;
+    x[i].zero();
+    if (col[i] < cols) {
+      x[i] = load_unit<F32>(row_of<F32>(a.x, row[i], a.ldx), col[i], cols, elements_left(a.rows, row[i], a.ldx, cols));
+      if constexpr (RES)
+        res[i] = load_unit<F32>(row_of<F32>(a.residual, row[i], a.ldr), col[i], cols,
+                                elements_left(a.rows, row[i], a.ldr, cols));
+    }
+    own[i] = static_cast<uint32_t>(at);
+  }
+  if (a.drop.rng != nullptr) {  // while the loads are on their way
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int phase = static_cast<int>(static_cast<uint32_t>(row[i]) * static_cast<uint32_t>(a.ldx)) & 7;
+      const uint32_t bits = kept_bits(mask, static_cast<uint32_t>(row[i]), own[i]);
+      own[i] = (__shfl_up_sync(0xffffffffu, bits, 1) | bits << 8) >> (8 - phase);
+      asm volatile("" : "+r"(own[i]));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    if (col[i] >= cols) continue;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = x[i].at(j);
+    if (a.drop.rng != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = own[i] >> j & 1u ? v[j] * mask.factor : 0.0f;
+    }
+    if constexpr (RES) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += res[i].at(j);
+    }
+    x[i].set(v);
+    store_unit<F32, true>(row_of<F32>(a.h, row[i], a.ldh), col[i], cols, x[i]);
   }
 }
 
@@ -730,37 +788,53 @@ cudaError_t launch_norm(const NormForward &a, bool phase, bool quant, bool held,
                : launch_form<F32, VEC, false>(a, phase, held, sm_count, s);
 }
 
-template <bool F32, int HOW, bool RES>
-cudaError_t launch_drop_of(const NormForward &a, int sm_count, cudaStream_t s) {
-  const int64_t chunks = (a.cols + (HOW == kPhase ? 7 : 0) + kChunk - 1) / kChunk;
+template <bool F32, bool VEC, bool RES>
+cudaError_t launch_drop_chunks(const NormForward &a, int sm_count, cudaStream_t s) {
+  const int64_t chunks = (a.cols + kChunk - 1) / kChunk;
   int lg = 5;
-  if (HOW == kAligned)
+  if (VEC)
     while (lg > 0 && (8 << lg >> 1) >= a.cols) --lg;
   // several chunks a warp: their loads are in flight together (us with 1, 2, 4: bf16
   // [16384, 4096] 57.0, 49.8, 47.0); few in all, or fp32 (39.8, 40.1, 40.3 at [8192, 4096]): one
-  int units = !F32 && a.rows * chunks >= 64 * static_cast<int64_t>(sm_count) ? 4 : 1;
-  const bool rows4 = HOW != kPhase && units == 4 && chunks <= 2;
-  if (HOW == kPhase && units == 4 && chunks <= 2) units = 2;
+  const int units = !F32 && a.rows * chunks >= 64 * static_cast<int64_t>(sm_count) ? 4 : 1;
+  const bool rows4 = units == 4 && chunks <= 2;
   const int W = static_cast<int>(rows4 ? chunks : std::min<int64_t>(8, (chunks + units - 1) / units)), R = 8 / W;
   const int64_t runs = (chunks + W * units - 1) / (W * units);
   const int64_t per = (static_cast<int64_t>(R) << (5 - lg)) * (rows4 ? units : 1);
   const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per * runs)), block(32 * W, R);
   const unsigned n = static_cast<unsigned>(runs);
   if constexpr (!F32) {
-    if constexpr (HOW == kPhase) {
-      if (units == 2) return launch_k(dropout_chunks<F32, HOW, 2, false, RES>, grid, block, 0, s, 0, a, n, lg);
-    } else {
-      if (rows4) return launch_k(dropout_chunks<F32, HOW, 4, true, RES>, grid, block, 0, s, 0, a, n, lg);
-    }
-    if (units == 4) return launch_k(dropout_chunks<F32, HOW, 4, false, RES>, grid, block, 0, s, 0, a, n, lg);
+    if (rows4) return launch_k(dropout_chunks<F32, VEC, 4, true, RES>, grid, block, 0, s, 0, a, n, lg);
+    if (units == 4) return launch_k(dropout_chunks<F32, VEC, 4, false, RES>, grid, block, 0, s, 0, a, n, lg);
   }
-  return launch_k(dropout_chunks<F32, HOW, 1, false, RES>, grid, block, 0, s, 0, a, n, lg);
+  return launch_k(dropout_chunks<F32, VEC, 1, false, RES>, grid, block, 0, s, 0, a, n, lg);
 }
 
-template <bool F32, int HOW>
-cudaError_t launch_drop(const NormForward &a, int sm_count, cudaStream_t s) {
-  return a.residual != nullptr ? launch_drop_of<F32, HOW, true>(a, sm_count, s)
-                               : launch_drop_of<F32, HOW, false>(a, sm_count, s);
+template <bool F32, int NU, bool RES>
+cudaError_t launch_drop_units_of(const NormForward &a, int64_t units, cudaStream_t s) {
+  const int64_t per = 8 * NU * 31;
+  return launch_k(dropout_units<F32, NU, RES>, dim3(static_cast<unsigned>((a.rows * units + per - 1) / per)), dim3(256),
+                  0, s, 0, a, static_cast<int>(units));
+}
+
+template <bool F32, bool RES>
+cudaError_t launch_drop_units(const NormForward &a, int sm_count, cudaStream_t s) {
+  // the furthest into a unit that a row starts
+  const int64_t ld = a.ldx, most = a.rows == 1 || ld % 8 == 0 ? 0 : ld % 4 == 0 ? 4 : ld % 2 == 0 ? 6 : 7;
+  const int64_t units = (a.cols - 1 + most) / 8 + 1;
+  // spans a warp, us with 1, 2, 4: fp32 [8192, 4097] 40.4, 47.5, -; bf16 with a residual [16384,
+  // 4097] -, 72.6, 68.9; few in all: one
+  if constexpr (!F32)
+    if (a.rows * units >= 64 * 31 * static_cast<int64_t>(sm_count)) return launch_drop_units_of<F32, 4, RES>(a, units, s);
+  return launch_drop_units_of<F32, 1, RES>(a, units, s);
+}
+
+template <bool F32, bool RES>
+cudaError_t launch_drop(const NormForward &a, bool vec, bool phase, int sm_count, cudaStream_t s) {
+  if (vec) return launch_drop_chunks<F32, true, RES>(a, sm_count, s);
+  if (phase && a.cols <= (INT64_C(1) << 30))  // 32-bit columns, up to 7 past the row
+    return launch_drop_units<F32, RES>(a, sm_count, s);
+  return launch_drop_chunks<F32, false, RES>(a, sm_count, s);
 }
 
 }  // namespace
@@ -778,11 +852,9 @@ cudaError_t launch_rmsnorm(const NormForward &a, bool f32, bool vec, bool phase,
 
 cudaError_t launch_dropout(const NormForward &a, bool f32, bool vec, bool phase, int sm_count,
                            cudaStream_t s) {
-  if (f32) return vec ? launch_drop<true, kAligned>(a, sm_count, s) : launch_drop<true, kScattered>(a, sm_count, s);
-  const bool units = phase && a.cols <= (INT64_C(1) << 30);  // 32-bit columns, up to 7 past the row
-  return vec     ? launch_drop<false, kAligned>(a, sm_count, s)
-         : units ? launch_drop<false, kPhase>(a, sm_count, s)
-                 : launch_drop<false, kScattered>(a, sm_count, s);
+  if (a.residual != nullptr)
+    return f32 ? launch_drop<true, true>(a, vec, phase, sm_count, s) : launch_drop<false, true>(a, vec, phase, sm_count, s);
+  return f32 ? launch_drop<true, false>(a, vec, phase, sm_count, s) : launch_drop<false, false>(a, vec, phase, sm_count, s);
 }
 
 }  // namespace fr

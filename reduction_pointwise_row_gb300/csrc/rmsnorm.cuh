@@ -223,21 +223,31 @@ __device__ __forceinline__ int elements_left(int64_t rows, int64_t row, int64_t 
   return n >= 8 ? INT32_MAX : static_cast<int>(n) + cols;
 }
 
-// The unit from column `col` on of the bf16 row at `row`, as it lies in memory: elements
+// The unit from column `col` on of the row at `row`, as it lies in memory: elements
 // outside the row are its neighbours', to be clipped.  A matrix's first row has no head
 // (its base is aligned); what lies past the matrix's end, `left` elements on, is not read.
-__device__ __forceinline__ Lane8<false> load_unit(const char *row, int col, int cols, int left) {
-  Lane8<false> v;
+template <bool F32>
+__device__ __forceinline__ Lane8<F32> load_unit(const char *row, int col, int cols, int left) {
+  constexpr int ES = F32 ? 4 : 2;
+  Lane8<F32> v;
   v.zero();
-  const char *p = row + static_cast<int64_t>(col) * 2;
+  const char *p = row + static_cast<int64_t>(col) * ES;
   if (col < cols && col <= left - 8) {
-    const uint4 u = ld_once_u4(p);
-    v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
+    if constexpr (F32) {
+      const V8 u = ld_stream_v8(p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v.w[i] = u.w[i];
+    } else {
+      const uint4 u = ld_once_u4(p);
+      v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
+    }
   } else if (col < cols) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (col + j < cols)
-        v.w[j >> 1] |= static_cast<uint32_t>(ld_stream_u16(p + 2 * j)) << (16 * (j & 1));
+    for (int j = 0; j < 8; ++j) {
+      if (col + j >= cols) continue;
+      if constexpr (F32) v.w[j] = __float_as_uint(ld_stream_f32(reinterpret_cast<const float *>(p) + j));
+      else v.w[j >> 1] |= static_cast<uint32_t>(ld_stream_u16(p + 2 * j)) << (16 * (j & 1));
+    }
   }
   return v;
 }

@@ -739,7 +739,9 @@ def test_more_rows_than_a_round_of_every_cta():
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("rows,cols,layout", [(20000, 64, (0, 0)), (12000, 63, (0, 0)), (6000, 500, (0, 4)),
                                               (6000, 505, (0, 0)), (10000, 7, (0, 2)), (6000, 300, (1, 0)),
-                                              (700, 4096, (0, 0)), (650, 4101, (0, 0)), (600, 4100, (1, 1))])
+                                              (700, 4096, (0, 0)), (650, 4101, (0, 0)), (600, 4100, (1, 1)),
+                                              (310001, 1, (0, 0)), (160000, 9, (0, 0)), (76001, 20, (0, 4)),
+                                              (40001, 63, (0, 0)), (20001, 121, (0, 5)), (2501, 987, (0, 2))])
 def test_dropout_of_many_rows(rows, cols, layout, dtype):
     x, r = values(rows, cols, dtype, 170), values(rows, cols, dtype, 171)
     n = rng_of(cols + 17)
