@@ -196,11 +196,12 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
   const int cols = static_cast<int>(a.cols);
   const uint32_t rows = static_cast<uint32_t>(a.rows);
   const bool up = a.dh != nullptr, drop = RP == 1 && a.drop.rng != nullptr;
-  // rows cls, cls + classes, ...: of these, runs of per R RP, every step-th run
+  // rows cls, cls + classes, ...: of these, runs of per R, every step-th run, RP of them a round
+  // (runs of RP adjacent ones leave some CTAs RP rows more than others: [4096, 8192] 46.1 us, 45.7 so)
   const uint32_t cls = blockIdx.x % classes;
-  const uint32_t next = classes * per * R;  // from a group's row to its next of the same stage
-  const uint32_t hop = next * RP * (gridDim.x / classes);
-  const uint32_t begin = cls + classes * per * R * RP * (blockIdx.x / classes);
+  const uint32_t next = classes * per * R * (gridDim.x / classes);  // from a group's row to its next
+  const uint32_t hop = next * RP;
+  const uint32_t begin = cls + classes * per * R * (blockIdx.x / classes);
   uint32_t row = begin + classes * (threadIdx.y * per + sub);
   const int rounds = begin < rows ? static_cast<int>((rows - begin - 1) / hop + 1) : 0;
   const int phase = !EDGES ? 0 : static_cast<int>((cls * a.ld_h) & (E - 1));

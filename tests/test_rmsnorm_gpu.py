@@ -754,6 +754,24 @@ def test_dropout_of_many_rows(rows, cols, layout, dtype):
         assert o.intact()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", [(5, 63), (9001, 505), (310001, 1), (33, 4097), (101, 17)])
+def test_dropout_of_odd_rows_bit_for_bit(rows, cols, dtype):
+    """Nothing dropped, everything dropped, in place, and out of phase: the same elements."""
+    x, r = values(rows, cols, dtype, 180).cuda(), values(rows, cols, dtype, 181).cuda()
+    n = rng_of(cols + 18).cuda()
+    assert torch.equal(fr.fr_dropout(x, 0.0, None), x)
+    assert torch.equal(fr.fr_dropout(x, 0.0, None, residual=r), (x.float() + r.float()).to(x.dtype))
+    assert torch.equal(fr.fr_dropout(torch.full_like(x, float("nan")), 1.0, n, residual=r), r)
+    want = fr.fr_dropout(x, 0.3, n, 2, residual=r)
+    a, b = x.clone(), r.clone()
+    assert torch.equal(fr.fr_dropout(a, 0.3, n, 2, residual=r, out=a), want)
+    assert torch.equal(fr.fr_dropout(x, 0.3, n, 2, residual=b, out=b), want)
+    v = torch.zeros(rows, cols + 9, device="cuda", dtype=x.dtype)[:, 1:1 + cols]
+    v.copy_(x)
+    assert torch.equal(fr.fr_dropout(v, 0.3, n, 2, residual=r), want)
+
+
 def test_auto_takes_a_form_that_holds_the_rows():
     """Long rows, aligned and not: the workspace that AUTO asks for serves either form."""
     for rows, cols in ((2, 8200), (3, 16384), (2, 16383), (1, 16392)):
