@@ -725,10 +725,13 @@ cudaError_t launch_short(const NormForward &a, int sm_count, cudaStream_t s) {
 // Measured (us with 1, 2, 3, 4, 6, 8): bf16 with residual, [16384, 4096] with dropout 90,
 // 84.8, -, 78.7, 80, -; [32768, 768] without, 3 chunks, -, 27, 14.7, 15.4, 16.2, -; [8192,
 // 16384] without -, 146, 143, 94.7, -, 80.1; fp32 [8192, 4096] with 83, 78.6, 79.1, -, -, -.
+// e4m3 out with 4, 8: [8192, 8192] 44.1, 39.1; [32768, 2048] 42.0, 36.2.  Fewer rows than
+// about a wave and a half of CTAs: 4 ([512, 4096] to e4m3 4.0, 5.8; bf16 [200, 16384] 3.8, 4.7).
 template <bool F32, bool VEC, bool QUANT, bool SUM>
 cudaError_t launch_held(const NormForward &a, int sm_count, cudaStream_t s) {
   const int chunks = static_cast<int>((a.cols + kChunk - 1) / kChunk);
-  int units = F32 ? 2 : !VEC ? (QUANT ? 2 : 3) : SUM || chunks <= 32 ? 4 : 8;
+  const bool many = a.rows * chunks >= 384 * static_cast<int64_t>(sm_count);
+  int units = F32 ? 2 : !VEC ? (QUANT ? 2 : 3) : SUM || chunks <= (QUANT ? 7 : 40) || !many ? 4 : 8;
   if (units == 3 && chunks > 3 * kHeldThreads<3> / 32) units = 2;
   if (chunks < units) units = chunks;
   if (a.rows < sm_count && chunks <= 32) units = 1;  // few rows: latency
