@@ -695,6 +695,21 @@ def test_more_short_rows_than_a_warp_takes_at_once(rows, cols, dtype):
             check_norm(x, res, p, n, 7, got, gamma, f"{what} {quant}", quant, given)
 
 
+@pytest.mark.parametrize("rows,cols", [(7301, 2048), (6700, 2296), (1830, 8192), (1771, 8200), (920, 16384), (1400, 10512)])
+def test_more_chunks_than_the_gpu_holds(rows, cols):
+    """A warp takes eight chunks of a row (4 with a residual) when there are enough of them."""
+    x, r = values(rows, cols, "bf16", 190), values(rows, cols, "bf16", 191, 3.0)
+    gamma = vector(cols, 19)
+    got = fr.fr_rmsnorm(x.cuda(), gamma.cuda(), EPS)
+    check_norm(x, None, 0.0, None, 0, got, gamma, "norm")
+    for i, quant in enumerate(("row", "group", "given")):
+        given, res = torch.tensor([0.008]), r if i == rows % 3 else None
+        got = fr.fr_rmsnorm_quant(x.cuda(), gamma.cuda(), EPS, want_rstd=True,
+                                  scale=given.cuda() if quant == "given" else quant,
+                                  residual=None if res is None else res.cuda())
+        check_norm(x, res, 0.0, None, 0, got, gamma, quant, quant, given)
+
+
 def test_neighbours_of_a_row_do_not_reach_it():
     """A unit at a row's edge holds elements of the rows beside it (or of the gap): whatever
     they are, the row's results are its own."""
