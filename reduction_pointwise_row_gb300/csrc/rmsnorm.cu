@@ -212,13 +212,16 @@ template <int NU>
 constexpr int kHeldThreads = NU <= 2 ? 1024 : NU <= 4 ? 512 : 256;
 
 // Persistent form: blockDim = (32 W, R), R rows a CTA, W warps a row, NU chunks a warp.
-template <bool F32, bool VEC, int NU, bool SUM, bool QUANT>
+// EXACT: rows of NU W whole chunks, without a comparison an access (to e4m3 without a residual,
+// which instructions bound, bf16 [8192, 8192] 35.9 us, 39.1 with; given scale [2048, 10240] 12.3,
+// 13.8; bf16 out and a residual's sum within 1 %).
+template <bool F32, bool VEC, int NU, bool SUM, bool QUANT, bool EXACT>
 __global__ void __launch_bounds__(kHeldThreads<NU>, 1024 / kHeldThreads<NU>)
 rmsnorm_held(NormForward a) {
   pdl_enter();
   __shared__ float red[2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
-  const int cols = static_cast<int>(a.cols);
+  const int cols = EXACT ? INT32_MAX : static_cast<int>(a.cols);
   const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const bool live = row < a.rows;
   const bool with_max = QUANT && a.scale_mode == FR_SCALE_ROW;
@@ -264,7 +267,7 @@ rmsnorm_held(NormForward a) {
   if constexpr (NU < 8) ss = f32x2_lo(squares) + f32x2_hi(squares);
   row_reduce(ss, most, with_max, W, red);
   if (!live) return;
-  const float rstd = 1.0f / sqrtf(ss / static_cast<float>(cols) + a.eps);
+  const float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
   if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
   float inv[2] = {1.0f, 1.0f};
   if (QUANT && a.scale_mode != FR_SCALE_GROUP) {
@@ -725,29 +728,46 @@ cudaError_t launch_short(const NormForward &a, int sm_count, cudaStream_t s) {
 // Measured (us with 1, 2, 3, 4, 6, 8): bf16 with residual, [16384, 4096] with dropout 90,
 // 84.8, -, 78.7, 80, -; [32768, 768] without, 3 chunks, -, 27, 14.7, 15.4, 16.2, -; [8192,
 // 16384] without -, 146, 143, 94.7, -, 80.1; fp32 [8192, 4096] with 83, 78.6, 79.1, -, -, -.
-// e4m3 out with 4, 8: [8192, 8192] 44.1, 39.1; [32768, 2048] 42.0, 36.2.  Fewer rows than
+// e4m3 out with 4, 8: [8192, 8192] 44.1, 39.1; [32768, 2048] 42.0, 36.2; or 7, 6 or 5 if they
+// divide the row ([12000, 5120] 34.4, 38.7 with 8; [22000, 2560] 31.5, 39.2).  Fewer rows than
 // about a wave and a half of CTAs: 4 ([512, 4096] to e4m3 4.0, 5.8; bf16 [200, 16384] 3.8, 4.7).
 template <bool F32, bool VEC, bool QUANT, bool SUM>
 cudaError_t launch_held(const NormForward &a, int sm_count, cudaStream_t s) {
   const int chunks = static_cast<int>((a.cols + kChunk - 1) / kChunk);
   const bool many = a.rows * chunks >= 384 * static_cast<int64_t>(sm_count);
   int units = F32 ? 2 : !VEC ? (QUANT ? 2 : 3) : SUM || chunks <= (QUANT ? 7 : 40) || !many ? 4 : 8;
+  if (QUANT && units == 8 && a.cols % kChunk == 0)
+    for (int u = 8; u >= 5; --u)
+      if (chunks % u == 0 && chunks / u <= 8) {
+        units = u;
+        break;
+      }
   if (units == 3 && chunks > 3 * kHeldThreads<3> / 32) units = 2;
   if (chunks < units) units = chunks;
   if (a.rows < sm_count && chunks <= 32) units = 1;  // few rows: latency
   const int W = (chunks + units - 1) / units, R = W >= 4 ? 1 : 4 / W;
   const dim3 grid(static_cast<unsigned>((a.rows + R - 1) / R)), block(32 * W, R);
-  if (units == 1) return launch_k(rmsnorm_held<F32, VEC, 1, SUM, QUANT>, grid, block, 0, s, 0, a);
+  if (units == 1) return launch_k(rmsnorm_held<F32, VEC, 1, SUM, QUANT, false>, grid, block, 0, s, 0, a);
   if constexpr (!F32) {
     if constexpr (VEC || !QUANT)
-      if (units == 3) return launch_k(rmsnorm_held<F32, VEC, 3, SUM, QUANT>, grid, block, 0, s, 0, a);
+      if (units == 3) return launch_k(rmsnorm_held<F32, VEC, 3, SUM, QUANT, false>, grid, block, 0, s, 0, a);
     if constexpr (VEC) {
-      if (units == 4) return launch_k(rmsnorm_held<F32, VEC, 4, SUM, QUANT>, grid, block, 0, s, 0, a);
+      const bool exact = a.cols == static_cast<int64_t>(kChunk) * units * W;
+      if (units == 4)
+        return exact ? launch_k(rmsnorm_held<F32, VEC, 4, SUM, QUANT, true>, grid, block, 0, s, 0, a)
+                     : launch_k(rmsnorm_held<F32, VEC, 4, SUM, QUANT, false>, grid, block, 0, s, 0, a);
+      if constexpr (!SUM && QUANT) {
+        if (units == 7 && exact) return launch_k(rmsnorm_held<F32, VEC, 7, SUM, QUANT, true>, grid, block, 0, s, 0, a);
+        if (units == 6 && exact) return launch_k(rmsnorm_held<F32, VEC, 6, SUM, QUANT, true>, grid, block, 0, s, 0, a);
+        if (units == 5 && exact) return launch_k(rmsnorm_held<F32, VEC, 5, SUM, QUANT, true>, grid, block, 0, s, 0, a);
+      }
       if constexpr (!SUM)
-        if (units == 8) return launch_k(rmsnorm_held<F32, VEC, 8, SUM, QUANT>, grid, block, 0, s, 0, a);
+        if (units == 8)
+          return exact ? launch_k(rmsnorm_held<F32, VEC, 8, SUM, QUANT, true>, grid, block, 0, s, 0, a)
+                       : launch_k(rmsnorm_held<F32, VEC, 8, SUM, QUANT, false>, grid, block, 0, s, 0, a);
     }
   }
-  return launch_k(rmsnorm_held<F32, VEC, 2, SUM, QUANT>, grid, block, 0, s, 0, a);
+  return launch_k(rmsnorm_held<F32, VEC, 2, SUM, QUANT, false>, grid, block, 0, s, 0, a);
 }
 
 // Chunks a warp holds (us with 1, 2, 3, 4: [16384, 4097] with residual 134, 108, 89.1, 87.7;

@@ -695,7 +695,8 @@ def test_more_short_rows_than_a_warp_takes_at_once(rows, cols, dtype):
             check_norm(x, res, p, n, 7, got, gamma, f"{what} {quant}", quant, given)
 
 
-@pytest.mark.parametrize("rows,cols", [(7301, 2048), (6700, 2296), (1830, 8192), (1771, 8200), (920, 16384), (1400, 10512)])
+@pytest.mark.parametrize("rows,cols", [(7301, 2048), (6700, 2296), (1830, 8192), (1771, 8200), (920, 16384), (1400, 10512),
+                                       (2950, 5120), (4200, 3584), (3300, 4608), (3250, 4600), (1100, 13824)])
 def test_more_chunks_than_the_gpu_holds(rows, cols):
     """A warp takes eight chunks of a row (4 with a residual) when there are enough of them."""
     x, r = values(rows, cols, "bf16", 190), values(rows, cols, "bf16", 191, 3.0)
