@@ -788,6 +788,18 @@ def test_dropout_of_odd_rows_bit_for_bit(rows, cols, dtype):
     assert torch.equal(fr.fr_dropout(v, 0.3, n, 2, residual=r), want)
 
 
+@pytest.mark.parametrize("dtype,cols", [("bf16", 11008), ("bf16", 1000), ("bf16", 5120), ("f32", 5000), ("f32", 128)])
+def test_gamma_at_any_address(dtype, cols):
+    """A vector needs no more than its type's alignment; the gradient does not depend on it."""
+    x, dy = values(310, cols, dtype, 200).cuda(), values(310, cols, dtype, 201, 0.1).cuda()
+    gamma = vector(cols, 20).cuda()
+    moved = torch.zeros(cols + 1, device="cuda")[1:]
+    moved.copy_(gamma)
+    rstd = fr.fr_rmsnorm(x, gamma, EPS)["rstd"]
+    a, b = (fr.fr_rmsnorm_backward(dy, x, g, rstd) for g in (gamma, moved))
+    assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dgamma"], b["dgamma"])
+
+
 def test_auto_takes_a_form_that_holds_the_rows():
     """Long rows, aligned and not: the workspace that AUTO asks for serves either form."""
     for rows, cols in ((2, 8200), (3, 16384), (2, 16383), (1, 16392)):
