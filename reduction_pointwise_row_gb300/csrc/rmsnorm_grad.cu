@@ -163,9 +163,9 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
 // RP rows in shared memory by asynchronous 16-byte copies.  A thread reads only what it
 // copied, so the ring needs no barrier, and the copies of the next rows are in flight
 // while a row is reduced and written.  blockDim = (32 W, R), R groups of RP rows at a time,
-// NU units a lane; short rows (1 << lg < 32 lanes a row, W = NU = 1) several a warp.  With
-// u = dy gamma, the gradient is dh + rstd dy gamma - (rstd^2 mean) h: paired fp32
-// arithmetic, two fused steps a pair.
+// NU units a lane; short rows (1 << lg < 32 lanes a row, W = NU = 1) several a warp.  Paired
+// fp32 arithmetic; n is formed before it meets mean(u n) or dy, as rstd^2 mean(u n) and rstd dy
+// may be past fp32, or below its normal values, where the gradients are not.
 //
 // kExact: aligned rows of 32 NU W units.  kWhole: aligned rows of whole units, fewer than
 // that (or short ones), no element of a unit masked: bf16 [4096, 11008] 63.9 us (149 element
@@ -330,8 +330,8 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
     for (int p = 0; p < RP; ++p) {
       const uint32_t r = row + p * next;
       if (r >= rows) break;
-      const float b = -(dot[p] * over * rstd[p]) * rstd[p] * rstd[p];
-      const uint64_t rstd2 = pack_f32x2(rstd[p], rstd[p]), b2 = pack_f32x2(b, b);
+      const float less = -(dot[p] * over * rstd[p]);
+      const uint64_t rstd2 = pack_f32x2(rstd[p], rstd[p]), less2 = pack_f32x2(less, less);
       uint32_t before = 0;
       if (EDGES && drop && chunk0 > 0) before = kept_group<E>(mask, r, chunk0 * 32 - 1);
       char *const out_x = row_of<F32>(a.dx, r, a.ld_dx), *const out_r = row_of<F32>(a.dres, r, a.ld_dres);
@@ -345,10 +345,10 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
         float d[E];
 #pragma unroll
         for (int j = 0; j < E / 2; ++j) {
-          const uint64_t x = mul_f32x2(dy.pair(j), rstd2), hj = h.pair(j);
-          acc[i][j] = fma_f32x2(x, hj, acc[i][j]);
-          const uint64_t v = fma_f32x2(hj, b2, up ? fma_f32x2(x, g[i][j], dh.pair(j))
-                                                  : mul_f32x2(x, g[i][j]));
+          const uint64_t n = mul_f32x2(h.pair(j), rstd2);
+          acc[i][j] = fma_f32x2(dy.pair(j), n, acc[i][j]);
+          const uint64_t t = fma_f32x2(n, less2, mul_f32x2(dy.pair(j), g[i][j]));
+          const uint64_t v = up ? fma_f32x2(t, rstd2, dh.pair(j)) : mul_f32x2(t, rstd2);
           d[2 * j] = f32x2_lo(v);
           d[2 * j + 1] = f32x2_hi(v);
         }

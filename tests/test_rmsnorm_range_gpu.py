@@ -1,0 +1,51 @@
+"""The norm's calls far from ordinary magnitudes: where a product of two factors of a formula
+leaves fp32 and the formula's value does not."""
+import pytest
+import torch
+
+import reduction_pointwise_row_gb300 as fr
+import rmsnorm_ref as ref
+from test_rmsnorm_gpu import check_backward, put, values, vector
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = ("bf16", "f32")
+# (cols, offset of the first element, form): the backward pass's launches -- rows of whole
+# units that fill the warps and that do not, rows that start within a unit, element
+# accesses, two passes
+LAUNCHES = [(512, 0, "persistent"), (4096, 0, "persistent"), (1000, 0, "persistent"),
+            (40, 0, "persistent"), (1003, 0, "persistent"), (1000, 1, "persistent"),
+            (4096, 0, "looped"), (1003, 0, "looped")]
+
+
+def scaled(rows, cols, dtype, seed, size):
+    """Normal values of magnitude `size`, rounded to the type."""
+    return values(rows, cols, "f32", seed).mul_(size).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+
+
+def backward(dtype, cols, at, form, size, up):
+    h, dy = scaled(21, cols, dtype, 1, size), scaled(21, cols, dtype, 2, up)
+    gamma = vector(cols, 30)
+    rstd = ref.norm(h, gamma, 0.0)[1].float()
+    got = fr.fr_rmsnorm_backward(put(dy, (at, 0)), put(h, (at, 0)), gamma.cuda(), rstd.cuda(), form=form)
+    return h, dy, gamma, rstd, got
+
+
+@pytest.mark.parametrize("cols,at,form", LAUNCHES)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("size,up", [(1e-18, 1e3), (1e16, 1e-8)])
+def test_the_gradient_needs_no_square_of_rstd(size, up, dtype, cols, at, form):
+    """eps 0, rstd of 1e18 and 1e-16: rstd^2 mean(u n) is past fp32 or below its normal values
+    where the gradient is neither."""
+    h, dy, gamma, rstd, got = backward(dtype, cols, at, form, size, up)
+    check_backward(h, gamma, None, 0.0, None, 0, got, dy, rstd, f"{size} {up}")
+
+
+@pytest.mark.parametrize("cols,at,form", LAUNCHES)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("size,up", [(1e-18, 1e22), (1e16, 1e-25)])
+def test_dgamma_needs_no_product_of_dy_and_rstd(size, up, dtype, cols, at, form):
+    """dy rstd is 1e40, or 1e-41 (as dx is, which is not looked at); dy (h rstd) is about dy."""
+    h, dy, gamma, rstd, got = backward(dtype, cols, at, form, size, up)
+    want = ref.backward(dy, h, gamma, rstd)[1]
+    ref.assert_near(got["dgamma"], want, ref.dgamma_bound(dy, h, rstd), f"{size} {up}")
