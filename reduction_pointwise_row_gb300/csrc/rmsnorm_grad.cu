@@ -50,12 +50,13 @@ __device__ __forceinline__ void chunk_grad(const NormBackward &a, const Mask &ma
   store8<F32, VEC>(row_of<F32>(a.dx, row, a.ld_dx), c, lane, cols, out);
 }
 
+// The sum of u n over a lane's elements.
 template <bool F32>
 __device__ __forceinline__ float chunk_dot(const Lane8<F32> &dy, const Lane8<F32> &h,
-                                           const float (&g)[8]) {
+                                           const float (&g)[8], float rstd) {
   float s = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) s = fmaf(dy.at(j) * g[j], h.at(j), s);
+  for (int j = 0; j < 8; ++j) s = fmaf(dy.at(j) * g[j], h.at(j) * rstd, s);
   return s;
 }
 
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(512) rmsnorm_grad_held(NormBackward a) {
       for (int i = 0; i < NU; ++i) {
         float g[8];
         load_cols8<false>(g, a.gamma, i * W + warp, lane, cols);
-        dot += chunk_dot<F32>(dy[i], h[i], g);
+        dot += chunk_dot<F32>(dy[i], h[i], g, rstd);
       }
     }
     dot = warp_sum(dot);
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(512) rmsnorm_grad_held(NormBackward a) {
       dot = warp_sum(lane < W ? red[turn][threadIdx.y * W + lane] : 0.0f);
     }
     if (!live) continue;
-    const float mean = dot * over * rstd;
+    const float mean = dot * over;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       const int c = i * W + warp;
@@ -287,12 +288,13 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
       if (r < rows) scale[p] = ld_keep_f32(a.rstd + r);
       uint64_t s = 0;
       if (row + p * next < rows) {
+        const uint64_t rstd2 = pack_f32x2(rstd[p], rstd[p]);
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
           const Unit<F32> dy = unit(0, p, i), h = unit(1, p, i);
 #pragma unroll
           for (int j = 0; j < E / 2; ++j)
-            s = fma_f32x2(mul_f32x2(dy.pair(j), g[i][j]), h.pair(j), s);
+            s = fma_f32x2(mul_f32x2(dy.pair(j), g[i][j]), mul_f32x2(h.pair(j), rstd2), s);
         }
       }
       dot[p] = f32x2_lo(s) + f32x2_hi(s);
@@ -330,7 +332,7 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
     for (int p = 0; p < RP; ++p) {
       const uint32_t r = row + p * next;
       if (r >= rows) break;
-      const float less = -(dot[p] * over * rstd[p]);
+      const float less = -dot[p] * over;
       const uint64_t rstd2 = pack_f32x2(rstd[p], rstd[p]), less2 = pack_f32x2(less, less);
       uint32_t before = 0;
       if (EDGES && drop && chunk0 > 0) before = kept_group<E>(mask, r, chunk0 * 32 - 1);
@@ -416,7 +418,7 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
   }
 }
 
-// Looped form, first kernel: sum(u h) of each row, a CTA a row.
+// Looped form, first kernel: sum(u n) of each row, a CTA a row.
 constexpr int kLoopThreads = 512;
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(kLoopThreads) rmsnorm_grad_dots(NormBackward a, float *dots) {
@@ -429,13 +431,14 @@ __global__ void __launch_bounds__(kLoopThreads) rmsnorm_grad_dots(NormBackward a
   int turn = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
     const char *dyr = row_of<F32>(a.dy, row, a.ld_dy), *hr = row_of<F32>(a.h, row, a.ld_h);
+    const float rstd = ld_keep_f32(a.rstd + row);
     float dot = 0.0f;
     for (int c = warp; c < chunks; c += W) {
       const Lane8<F32> dy = load8<F32, VEC, true>(dyr, c, lane, cols);
       const Lane8<F32> h = load8<F32, VEC, true>(hr, c, lane, cols);
       float g[8];
       load_cols8<VEC>(g, a.gamma, c, lane, cols);
-      dot += chunk_dot<F32>(dy, h, g);
+      dot += chunk_dot<F32>(dy, h, g, rstd);
     }
     dot = warp_sum(dot);
     if (lane == 0) red[turn][warp] = dot;
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(256) rmsnorm_grad_cols(NormBackward a, const f
     Lane8<F32> dh{};
     if (a.dh != nullptr) dh = load8<F32, VEC>(row_of<F32>(a.dh, row, a.ld_dh), c, lane, cols);
     const float rstd = ld_keep_f32(a.rstd + row);
-    const float mean = ld_keep_f32(dots + row) * over * rstd;
+    const float mean = ld_keep_f32(dots + row) * over;
     chunk_grad<F32, VEC>(a, mask, row, c, lane, dy, h, dh, g, rstd, mean, acc);
   }
   if (a.dgamma != nullptr)

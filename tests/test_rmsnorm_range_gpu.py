@@ -43,6 +43,15 @@ def test_the_gradient_needs_no_square_of_rstd(size, up, dtype, cols, at, form):
 
 @pytest.mark.parametrize("cols,at,form", LAUNCHES)
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("size,up", [(1e16, 1e24), (1e-16, 1e-26)])
+def test_the_gradient_needs_no_product_of_dy_and_h(size, up, dtype, cols, at, form):
+    """dy h is 1e40, or 1e-42 with few bits left; dy gamma, h rstd and their product are not."""
+    h, dy, gamma, rstd, got = backward(dtype, cols, at, form, size, up)
+    check_backward(h, gamma, None, 0.0, None, 0, got, dy, rstd, f"{size} {up}")
+
+
+@pytest.mark.parametrize("cols,at,form", LAUNCHES)
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("size,up", [(1e-18, 1e22), (1e16, 1e-25)])
 def test_dgamma_needs_no_product_of_dy_and_rstd(size, up, dtype, cols, at, form):
     """dy rstd is 1e40, or 1e-41 (as dx is, which is not looked at); dy (h rstd) is about dy."""
