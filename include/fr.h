@@ -553,8 +553,9 @@ fr_status fr_rmsnorm(const void *x, const void *residual, const float *gamma, vo
  *   y           e4m3 bytes [rows, ldy]
  *   mode        FR_SCALE_ROW: scale = max |v| / 448 over the row, written; FR_SCALE_GROUP:
  *               over each 128 columns (the last group may be shorter), written;
- *               FR_SCALE_GIVEN: *scale is read (finite, > 0).  A written scale is
- *               at least 2^-126, so zeros stay zeros, and NaN where its values hold one.
+ *               FR_SCALE_GIVEN: *scale is read (finite, at least 2^-126; less counts as
+ *               2^-126).  A written scale is at least 2^-126 too, so zeros stay zeros, and
+ *               NaN where its values hold one.
  *   scale       fp32 device memory; row r's at [r * scale_row_stride], group g's at
  *               [r * scale_row_stride + g * scale_col_stride].  One of the two strides
  *               is 1 and the other at least the groups (rows) it passes; of

@@ -861,7 +861,8 @@ def fr_rmsnorm_quant(x, gamma, eps: float = 1e-5, scale="row", residual=None, p:
     """fr_rmsnorm with y in 8 bits (torch.float8_e4m3fn), y * scale being the norm.
 
     ``scale``: "row" (one scale a row, max |y| / 448), "group" (one per 128 columns of
-    a row) or a CUDA tensor of one fp32 value, which is used as it is.  Returns a
+    a row) or a CUDA tensor of one fp32 value, which is used as it is (below 2^-126 as
+    2^-126).  Returns a
     dict: ``y``; ``scale`` ([rows], or [rows, groups], where it is not given); ``h``
     and ``rstd`` as fr_rmsnorm.  ``scale_out`` takes the scales in a tensor of the
     caller's, groups in either order ([rows, groups] with one stride of 1)."""

@@ -117,6 +117,11 @@ __device__ __forceinline__ float scale_for(float most) {
   return max_nan(most * (1.0f / kE4m3Max), 1.17549435e-38f);
 }
 
+// The scale that the caller gives: no smaller than a written one, for the same reasons.
+__device__ __forceinline__ float scale_given(const float *scale) {
+  return max_nan(ld_keep_f32(scale), 1.17549435e-38f);
+}
+
 // A chunk of y in 8 bits with a scale per 128 columns: two scales a chunk.  Aligned
 // rows: the halves of the warp hold one group each; others: a lane's first and last
 // four elements belong to one each.
@@ -271,7 +276,7 @@ rmsnorm_held(NormForward a) {
   if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
   float inv[2] = {1.0f, 1.0f};
   if (QUANT && a.scale_mode != FR_SCALE_GROUP) {
-    const float s = with_max ? scale_for(most * rstd) : ld_keep_f32(a.scale);
+    const float s = with_max ? scale_for(most * rstd) : scale_given(a.scale);
     if (with_max && threadIdx.x == 0) a.scale[row * a.scale_row] = s;
     inv[0] = inv[1] = 1.0f / s;
   }
@@ -334,7 +339,7 @@ __global__ void __launch_bounds__(kLoopThreads) rmsnorm_looped(NormForward a) {
     if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
     float inv[2] = {1.0f, 1.0f};
     if (QUANT && a.scale_mode != FR_SCALE_GROUP) {
-      const float s = a.scale_mode == FR_SCALE_ROW ? scale_for(most * rstd) : ld_keep_f32(a.scale);
+      const float s = a.scale_mode == FR_SCALE_ROW ? scale_for(most * rstd) : scale_given(a.scale);
       if (a.scale_mode == FR_SCALE_ROW && threadIdx.x == 0) a.scale[row * a.scale_row] = s;
       inv[0] = inv[1] = 1.0f / s;
     }
@@ -423,7 +428,7 @@ rmsnorm_phase(NormForward a) {
   if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
   float inv[2] = {1.0f, 1.0f};
   if (QUANT) {
-    const float s = with_max ? scale_for(most * rstd) : ld_keep_f32(a.scale);
+    const float s = with_max ? scale_for(most * rstd) : scale_given(a.scale);
     if (with_max && threadIdx.x == 0) a.scale[row * a.scale_row] = s;
     inv[0] = inv[1] = 1.0f / s;
   }
@@ -530,7 +535,7 @@ __global__ void __launch_bounds__(256) rmsnorm_short(NormForward a, int lg) {
                      max_abs(v[u][5], v[u][6], v[u][7]));
     }
     if (a.scale_mode == FR_SCALE_GIVEN) {
-      const float given = ld_keep_f32(a.scale);
+      const float given = scale_given(a.scale);
 #pragma unroll
       for (int u = 0; u < U; ++u) s[u] = given;
     } else {

@@ -1,5 +1,7 @@
 """The norm's calls far from ordinary magnitudes: where a product of two factors of a formula
 leaves fp32 and the formula's value does not."""
+import math
+
 import pytest
 import torch
 
@@ -58,3 +60,22 @@ def test_dgamma_needs_no_product_of_dy_and_rstd(size, up, dtype, cols, at, form)
     h, dy, gamma, rstd, got = backward(dtype, cols, at, form, size, up)
     want = ref.backward(dy, h, gamma, rstd)[1]
     ref.assert_near(got["dgamma"], want, ref.dgamma_bound(dy, h, rstd), f"{size} {up}")
+
+
+@pytest.mark.parametrize("cols,at,form", [(1000, 0, "persistent"), (1003, 0, "persistent"), (96, 0, "persistent"),
+                                          (16384, 0, "persistent"), (1000, 1, "persistent"), (1003, 0, "looped")])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("scale", [2.0**-126, 2.0**-127, 2.0**-129, 2.0**-149])
+def test_the_smallest_given_scales(scale, dtype, cols, at, form):
+    """Zeros stay zeros, NaN NaN, and the rest, far past 448 scales, the largest value."""
+    x = scaled(7, cols, dtype, 6, 1.0)
+    x[1] = 0.0
+    x[2, 1::2] = 0.0
+    x[3, 0] = math.nan
+    given = torch.tensor([scale]).cuda()
+    assert float(given) == scale
+    y = fr.fr_rmsnorm_quant(put(x, (at, 0)), vector(cols, 33).abs().cuda(), 1e-5, scale=given,
+                            form=form)["y"].float().cpu()
+    want = torch.where(x == 0, 0.0, torch.copysign(torch.tensor(448.0), x.float()))
+    want[3] = math.nan
+    assert torch.equal(y[torch.arange(7) != 3], want[torch.arange(7) != 3]) and y[3].isnan().all()
