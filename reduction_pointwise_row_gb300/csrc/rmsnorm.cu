@@ -260,8 +260,14 @@ rmsnorm_held(NormForward a) {
       if constexpr (NU < 8) {
         squares = squares8(h[i], squares);  // 0 past the row
       } else {  // (a register fewer: 64 suffice)
+        // runs of 4: of a lane's 64 squares, added one by one, the last ones lose bits
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(h[i].at(j), h[i].at(j), ss);
+        for (int j = 0; j < 8; j += 4) {
+          float part = h[i].at(j) * h[i].at(j);
+#pragma unroll
+          for (int k = 1; k < 4; ++k) part = fmaf(h[i].at(j + k), h[i].at(j + k), part);
+          ss += part;
+        }
       }
       if (with_max) {
 #pragma unroll

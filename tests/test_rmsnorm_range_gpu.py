@@ -79,3 +79,20 @@ def test_the_smallest_given_scales(scale, dtype, cols, at, form):
     want = torch.where(x == 0, 0.0, torch.copysign(torch.tensor(448.0), x.float()))
     want[3] = math.nan
     assert torch.equal(y[torch.arange(7) != 3], want[torch.arange(7) != 3]) and y[3].isnan().all()
+
+
+@pytest.mark.parametrize("rows,cols", [(1000, 16384), (1200, 14336), (1500, 10496), (7400, 2048), (1900, 8192)])
+def test_a_lane_adds_its_squares_in_short_runs(rows, cols):
+    """A lane's first square is 1 and its others 2^-24, half a step of the sum: added to it one
+    by one they would all be lost.  A lane has at most 64 squares here, of 8 chunks; added up
+    in runs of 4 a term goes through 4 + 16 + 10 additions at most, of whose roundings half
+    (and 4 more) reach rstd."""
+    x = torch.full((rows, cols), 2.0**-12, dtype=torch.bfloat16)
+    warps = -(-cols // 2048)  # of 8 chunks each, every warps-th one
+    x[:, :256 * warps:8] = 1.0
+    gamma = torch.ones(cols)
+    want = ref.norm(x[:1], gamma, 0.0)[1].expand(rows)
+    bound = ((4 + 16 + 10 + 1) / 2 + 4) * ref.U * want
+    ref.assert_near(fr.fr_rmsnorm(x.cuda(), gamma.cuda(), 0.0)["rstd"], want, bound, "norm")
+    got = fr.fr_rmsnorm_quant(x.cuda(), gamma.cuda(), 0.0, want_rstd=True)
+    ref.assert_near(got["rstd"], want, bound, "8 bits")
