@@ -515,8 +515,8 @@ fr_status fr_xent_backward(const void *logits, const int64_t *target, const floa
  * Arithmetic is fp32, each output rounded once (nearest even).  NaN and infinities
  * follow the formulas: a NaN in h makes its row's y and dx NaN, and dgamma; an infinity
  * there makes rstd 0, its own y NaN and the row's others 0.  A row whose squares add up
- * past fp32 (elements of about 1e19) has rstd 0 and y 0 (in 8 bits with a scale a row NaN
- * where h gamma is past fp32 as well).  Results are the same from run to run.
+ * past fp32 (elements of about 1e19) has rstd 0 and y 0.  Results are the same from run to
+ * run.
  */
 
 /*

@@ -194,6 +194,44 @@ __device__ __forceinline__ char *row_of(void *p, int64_t row, int64_t ld) {
   return static_cast<char *>(p) + row * ld * (F32 ? 4 : 2);
 }
 
+// The largest h rstd gamma of a thread's share of a row of h, read again by its row group, an
+// element an access.  It is seldom called, and apart: of what is still held, within the
+// kernel, 8 bits took up to 3 % more time, from fp32 13 % (registers).
+template <bool F32>
+__device__ __noinline__ float most_again(const void *h, const float *gamma, uint32_t cols, float rstd) {
+  __syncwarp();  // h as the row group has stored it
+  float most = 0.0f;
+#pragma unroll 1
+  for (uint32_t c = threadIdx.x; c < cols; c += blockDim.x) {
+    float v;
+    if constexpr (F32) v = ld_keep_f32(static_cast<const float *>(h) + c);
+    else v = bf16_lo(ld_stream_u16(static_cast<const char *>(h) + static_cast<size_t>(c) * 2));
+    most = max_nan(most, fabsf(v * rstd * ld_keep_f32(gamma + c)));
+  }
+  return most;
+}
+
+// The largest magnitude of a row's h rstd gamma.  While the row is read the largest h gamma is
+// found, `most`; times rstd it is that, unless the product of two is infinite, or short of bits
+// that count beside the smallest scale, though the product of three is neither.  `red` is one
+// pass's own.
+template <bool F32>
+__device__ __forceinline__ float row_most(const NormForward &a, int64_t row, float most, float rstd,
+                                          int W, float (&red)[32]) {
+  if (most < __int_as_float(0x7f800000) && (most >= 1.17549435e-38f || rstd <= 4096.0f)) return most * rstd;
+  const void *h = a.h != nullptr ? row_of<F32>(static_cast<const void *>(a.h), row, a.ldh)
+                                 : row_of<F32>(a.x, row, a.ldx);
+  most = warp_max(most_again<F32>(h, a.gamma, static_cast<uint32_t>(a.cols), rstd));
+  if (W == 1) return most;
+  const int lane = threadIdx.x & 31, first = threadIdx.y * W;
+  if (lane == 0) red[first + (threadIdx.x >> 5)] = most;
+  // (two row groups at most; a computed barrier would take all 16, and fewer CTAs fit an SM:
+  // [8192, 8192] 47.6 us, 36.3 so)
+  if (threadIdx.y == 0) asm volatile("bar.sync 1, %0;" ::"r"(32 * W) : "memory");
+  else asm volatile("bar.sync 2, %0;" ::"r"(32 * W) : "memory");
+  return warp_max(lane < W ? red[first + lane] : 0.0f);
+}
+
 // The sum of a row's squares (and its largest magnitude) over the W warps that hold
 // it: every thread gets them.  `red` is one pass's own.
 __device__ __forceinline__ void row_reduce(float &ss, float &most, bool with_max, int W,
@@ -217,11 +255,13 @@ template <int NU>
 constexpr int kHeldThreads = NU <= 2 ? 1024 : NU <= 4 ? 512 : 256;
 
 // Persistent form: blockDim = (32 W, R), R rows a CTA, W warps a row, NU chunks a warp.
+// T: threads of a CTA at most (8 bits from fp32 rows of up to 4096 columns: 256, of which an SM
+// holds five within 48 registers; [8192, 4096] 30.9 us, with 56 registers and four of them 35.0).
 // EXACT: rows of NU W whole chunks, without a comparison an access (to e4m3 without a residual,
 // which instructions bound, bf16 [8192, 8192] 35.9 us, 39.1 with; given scale [2048, 10240] 12.3,
 // 13.8; bf16 out and a residual's sum within 1 %).
-template <bool F32, bool VEC, int NU, bool SUM, bool QUANT, bool EXACT>
-__global__ void __launch_bounds__(kHeldThreads<NU>, 1024 / kHeldThreads<NU>)
+template <bool F32, bool VEC, int NU, bool SUM, bool QUANT, bool EXACT, int T = kHeldThreads<NU>>
+__global__ void __launch_bounds__(T, NU == 2 && T == 256 ? 5 : 1024 / T)
 rmsnorm_held(NormForward a) {
   pdl_enter();
   __shared__ float red[2][32];
@@ -282,7 +322,8 @@ rmsnorm_held(NormForward a) {
   if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
   float inv[2] = {1.0f, 1.0f};
   if (QUANT && a.scale_mode != FR_SCALE_GROUP) {
-    const float s = with_max ? scale_for(most * rstd) : scale_given(a.scale);
+    __shared__ float again[32];
+    const float s = with_max ? scale_for(row_most<F32>(a, row, most, rstd, W, again)) : scale_given(a.scale);
     if (with_max && threadIdx.x == 0) a.scale[row * a.scale_row] = s;
     inv[0] = inv[1] = 1.0f / s;
   }
@@ -345,7 +386,9 @@ __global__ void __launch_bounds__(kLoopThreads) rmsnorm_looped(NormForward a) {
     if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
     float inv[2] = {1.0f, 1.0f};
     if (QUANT && a.scale_mode != FR_SCALE_GROUP) {
-      const float s = a.scale_mode == FR_SCALE_ROW ? scale_for(most * rstd) : scale_given(a.scale);
+      __shared__ float again[32];
+      const float s = a.scale_mode == FR_SCALE_ROW ? scale_for(row_most<F32>(a, row, most, rstd, W, again))
+                                                   : scale_given(a.scale);
       if (a.scale_mode == FR_SCALE_ROW && threadIdx.x == 0) a.scale[row * a.scale_row] = s;
       inv[0] = inv[1] = 1.0f / s;
     }
@@ -434,7 +477,8 @@ rmsnorm_phase(NormForward a) {
   if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
   float inv[2] = {1.0f, 1.0f};
   if (QUANT) {
-    const float s = with_max ? scale_for(most * rstd) : scale_given(a.scale);
+    __shared__ float again[32];
+    const float s = with_max ? scale_for(row_most<false>(a, row, most, rstd, W, again)) : scale_given(a.scale);
     if (with_max && threadIdx.x == 0) a.scale[row * a.scale_row] = s;
     inv[0] = inv[1] = 1.0f / s;
   }
@@ -778,6 +822,8 @@ cudaError_t launch_held(const NormForward &a, int sm_count, cudaStream_t s) {
                        : launch_k(rmsnorm_held<F32, VEC, 8, SUM, QUANT, false>, grid, block, 0, s, 0, a);
     }
   }
+  if constexpr (F32 && VEC && QUANT && !SUM)
+    if (W <= 8) return launch_k(rmsnorm_held<F32, VEC, 2, SUM, QUANT, false, 256>, grid, block, 0, s, 0, a);
   return launch_k(rmsnorm_held<F32, VEC, 2, SUM, QUANT, false>, grid, block, 0, s, 0, a);
 }
 

@@ -62,6 +62,43 @@ def test_dgamma_needs_no_product_of_dy_and_rstd(size, up, dtype, cols, at, form)
     ref.assert_near(got["dgamma"], want, ref.dgamma_bound(dy, h, rstd), f"{size} {up}")
 
 
+# rows held by 1-8 chunks a warp, rows in phase, element accesses, short rows, two passes
+FORWARD = [(9, 1000, 0, "persistent"), (9, 1003, 0, "persistent"), (9, 1000, 1, "persistent"),
+           (9, 96, 0, "persistent"), (9, 500, 0, "persistent"), (200, 512, 0, "persistent"),
+           (9, 16384, 0, "persistent"), (1000, 16384, 0, "persistent"), (1300, 10240, 0, "persistent"),
+           (9, 4096, 0, "looped"), (9, 1003, 0, "looped")]
+
+
+@pytest.mark.parametrize("rows,cols,at,form", FORWARD)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("size,weight,eps", [(1e10, 1e30, 1e-5), (1e-18, 1e-25, 0.0)])
+def test_a_row_s_scale_needs_no_product_of_h_and_gamma(size, weight, eps, dtype, rows, cols, at, form):
+    """h gamma is 1e40, or 1e-43 with few bits left; h rstd gamma is about gamma."""
+    h, gamma = scaled(rows, cols, dtype, 3, size), vector(cols, 31) * weight
+    h[1] = 0.0
+    h[2] = scaled(1, cols, dtype, 4, 1.0)[0]
+    h[3, cols // 2] = math.nan
+    got = fr.fr_rmsnorm_quant(put(h, (at, 0)), gamma.cuda(), eps, form=form, want_rstd=True)
+    y, _ = ref.norm(h, gamma, eps)
+    s = got["scale"].cpu().double()[:, None]
+    ref.assert_near(s, ref.scales(y, cols), (ref.rstd_bound(cols) + 4 * ref.U) * ref.scales(y, cols), "scale")
+    ref.assert_near(got["y"].float().cpu().double() * s, y, ref.quant_bound(cols, y, s), "y8")
+
+
+@pytest.mark.parametrize("cols,at,form", [(1000, 0, "persistent"), (1003, 0, "persistent"), (96, 0, "persistent"),
+                                          (16384, 0, "persistent"), (1000, 1, "persistent"), (1003, 0, "looped")])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_squares_past_fp32_leave_a_row_of_zeros_in_8_bits_too(dtype, cols, at, form):
+    big = torch.finfo(torch.bfloat16).max
+    h = scaled(5, cols, dtype, 5, 1.0)
+    h[1] = big
+    gamma = vector(cols, 32).abs() + 2.0  # big gamma is past fp32
+    for scale in ("row", "group"):
+        got = fr.fr_rmsnorm_quant(put(h, (at, 0)), gamma.cuda(), 1e-5, scale=scale, form=form)
+        assert (got["y"][1].float() == 0).all() and (got["scale"][1] == 2.0**-126).all()
+        assert not got["y"].float().isnan().any() and got["scale"].isfinite().all()
+
+
 @pytest.mark.parametrize("cols,at,form", [(1000, 0, "persistent"), (1003, 0, "persistent"), (96, 0, "persistent"),
                                           (16384, 0, "persistent"), (1000, 1, "persistent"), (1003, 0, "looped")])
 @pytest.mark.parametrize("dtype", DTYPES)
