@@ -734,7 +734,7 @@ def _rng_ptr(p: float, rng, site: int, dev: int):
     """The address of a call's {seed, offset}; None without dropout."""
     if not -2**63 <= site < 2**63:
         raise ValueError("site must fit 64 bits")
-    if p == 0.0:
+    if 0.0 <= p <= 2.0**-150:  # the library takes p in fp32: 0 there
         return None
     if not 0.0 < p <= 1.0:
         raise ValueError("p must be 0 to 1")

@@ -118,6 +118,19 @@ def test_the_smallest_given_scales(scale, dtype, cols, at, form):
     assert torch.equal(y[torch.arange(7) != 3], want[torch.arange(7) != 3]) and y[3].isnan().all()
 
 
+def test_a_probability_that_rounds_to_none():
+    """The calls take p in fp32: what rounds to 0 there drops nothing, as 0 does."""
+    x, g = values(4, 64, "bf16", 7).cuda(), vector(64, 34).cuda()
+    n = torch.tensor([1, 2], device="cuda")
+    for p in (1e-50, 2.0**-151):
+        assert torch.equal(fr.fr_dropout(x, p, n), x)
+        assert list(fr.fr_rmsnorm(x, g, p=p, rng=n)) == ["y", "rstd"]
+        rstd = fr.fr_rmsnorm(x, g)["rstd"]
+        assert list(fr.fr_rmsnorm_backward(x, x, g, rstd, p=p, rng=n)) == ["dx", "dgamma"]
+    got = fr.fr_rmsnorm(x, g, p=2.0**-149, rng=n)  # the smallest that does not: one of 65536
+    assert "h" in got
+
+
 @pytest.mark.parametrize("rows,cols", [(1000, 16384), (1200, 14336), (1500, 10496), (7400, 2048), (1900, 8192)])
 def test_a_lane_adds_its_squares_in_short_runs(rows, cols):
     """A lane's first square is 1 and its others 2^-24, half a step of the sum: added to it one
