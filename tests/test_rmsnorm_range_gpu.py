@@ -7,7 +7,7 @@ import torch
 
 import reduction_pointwise_row_gb300 as fr
 import rmsnorm_ref as ref
-from test_rmsnorm_gpu import check_backward, put, values, vector
+from test_rmsnorm_gpu import check_backward, check_norm, put, values, vector
 
 pytestmark = pytest.mark.gpu
 
@@ -146,3 +146,19 @@ def test_a_lane_adds_its_squares_in_short_runs(rows, cols):
     ref.assert_near(fr.fr_rmsnorm(x.cuda(), gamma.cuda(), 0.0)["rstd"], want, bound, "norm")
     got = fr.fr_rmsnorm_quant(x.cuda(), gamma.cuda(), 0.0, want_rstd=True)
     ref.assert_near(got["rstd"], want, bound, "8 bits")
+
+
+@pytest.mark.parametrize("off", [1, 2, 4])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", [(5, 96), (33, 1000), (7, 1003), (3, 4096), (200, 768), (2, 16392)])
+def test_gamma_at_any_address_in_the_forward_calls(rows, cols, dtype, off):
+    x, r = values(rows, cols, dtype, 8), values(rows, cols, dtype, 9)
+    gamma, n = vector(cols, 35), torch.tensor([3, 4])
+    moved = torch.full((cols + 16,), math.nan, device="cuda")[off:off + cols]
+    moved.copy_(gamma)
+    for res, p in ((None, 0.0), (r, 0.2)):
+        kw = dict(residual=None if res is None else res.cuda(), p=p, rng=n.cuda())
+        check_norm(x, res, p, n, 0, fr.fr_rmsnorm(x.cuda(), moved, **kw), gamma, f"p {p}")
+        for scale in ("row", "group"):
+            got = fr.fr_rmsnorm_quant(x.cuda(), moved, scale=scale, **kw)
+            check_norm(x, res, p, n, 0, got, gamma, f"p {p} {scale}", scale)
