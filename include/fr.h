@@ -502,7 +502,10 @@ fr_status fr_xent_backward(const void *logits, const int64_t *target, const floa
  *   dropout      p in [0, 1]; 0: none, rng and site are not looked at.  Else rng is
  *                device memory of two int64, {seed, offset}, read by the kernels (a
  *                captured graph replays with what it holds then), and site, added to
- *                the offset, tells apart the places of a model that share it.  Element
+ *                the offset, tells apart the places of a model that share it.  The two
+ *                are one number to the generator: from one step to the next a program
+ *                advances the offset by at least the number of its sites (0, 1, ...), or a
+ *                place draws the mask that another drew a step before.  Element
  *                (r, c) is dropped where half c % 8 (16 bits, the low half of each
  *                word first) of the Philox4x32 block of 7 rounds with counter (c / 8,
  *                r, offset + site low, high) and key (seed low, high) is below t =

@@ -768,7 +768,9 @@ def fr_dropout(x, p: float, rng, site: int = 0, residual=None, out=None, stream=
     """residual + dropout(x) (residual None: dropout(x)) of bf16 or fp32 rows.  The
     mask is drawn from ``rng``, an int64 CUDA tensor {seed, offset}, ``site`` and the
     element's row and column, and never stored: the gradient of x is fr_dropout of
-    y's gradient with the same rng, site and p.  ``out`` may be x or residual."""
+    y's gradient with the same rng, site and p.  offset + site is one number: advance the
+    offset between steps by at least the number of sites, or one place's mask is
+    another's of the step before.  ``out`` may be x or residual."""
     if stream is not None:
         return _with_stream(fr_dropout, stream, x, p, rng, site, residual, out)
     _TORCH or _torch()
