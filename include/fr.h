@@ -488,12 +488,16 @@ fr_status fr_xent_backward(const void *logits, const int64_t *target, const floa
  *   matrices     of `dtype` (FR_BF16 or FR_F32), [rows, ld] with any ld >= cols and
  *                any element-aligned address.  Fastest: every row of every matrix of
  *                a call starts at a multiple of 8 elements (16 bytes of bf16, 32 of
- *                fp32, 8 of e4m3), cols is one too, gamma is 32-byte aligned.  Next, for
- *                bf16 and the gradient: the bases are aligned so and the strides agree
- *                modulo 8 elements, whatever cols is (compact matrices of odd rows).
- *                Other rows are read an element an access.  The results are the same
- *                up to the order of a row's sums.  rows <= INT32_MAX, cols < 2^31
- *                (more: FR_ERR_UNSUPPORTED_FORM).
+ *                fp32, 8 of e4m3; in the gradient 16 bytes of either), cols is one too,
+ *                and in the norm's forward calls gamma is 32-byte aligned.  Next: the
+ *                bases are aligned so and the strides agree modulo as much, whatever
+ *                cols is (compact matrices of odd rows), in fr_dropout up to 2^30 columns,
+ *                in the norm of bf16 up to 16377 (in 8 bits not with scales in groups), in
+ *                the gradient up to 8185 (fp32 6141).  Other rows are read an element an
+ *                access.  The results are the same up to the order of a row's sums and,
+ *                in the norm of aligned rows of at most 256 columns, an approximate
+ *                reciprocal root (2 units in the last place) and, in 8 bits, reciprocal (1).
+ *                rows <= INT32_MAX, cols < 2^31 (more: FR_ERR_UNSUPPORTED_FORM).
  *   overlap      an output matrix may be the very buffer of an input matrix of its
  *                type with the same ld, or lie in the gaps of its rows (same ld); any
  *                other overlap of an output with an input or another output is
@@ -517,9 +521,9 @@ fr_status fr_xent_backward(const void *logits, const int64_t *target, const floa
  *   gamma        fp32 [cols], as fr_layernorm's.
  * Arithmetic is fp32, each output rounded once (nearest even).  NaN and infinities
  * follow the formulas: a NaN in h makes its row's y and dx NaN, and dgamma; an infinity
- * there makes rstd 0, its own y NaN and the row's others 0.  A row whose squares add up
- * past fp32 (elements of about 1e19) has rstd 0 and y 0.  Results are the same from run to
- * run.
+ * there makes rstd 0, its own y NaN and the row's others 0, its row's dx NaN and its column's
+ * dgamma.  A row whose squares add up past fp32 (elements of about 1e19) has rstd 0 and y 0;
+ * squares below 2^-126 have fewer bits.  Results are the same from run to run.
  */
 
 /*
@@ -550,8 +554,10 @@ fr_status fr_rmsnorm(const void *x, const void *residual, const float *gamma, vo
                      int64_t site, fr_dtype dtype, fr_form form, fr_stream_t stream);
 
 /*
- * fr_rmsnorm with y in 8 bits: y8 = e4m3(v / scale) of v = h rstd gamma in fp32, to
- * nearest even, saturating at 448 (NaN stays NaN).
+ * fr_rmsnorm with y in 8 bits: y8 = e4m3(v (1 / scale)) of v = h rstd gamma in fp32, to
+ * nearest even, saturating at 448 (NaN stays NaN).  The reciprocal and the product are
+ * rounded to fp32, so a value within 2^-23 of halfway between two of e4m3 may go to the other
+ * than v / scale does.
  *
  *   y           e4m3 bytes [rows, ldy]
  *   mode        FR_SCALE_ROW: scale = max |v| / 448 over the row, written; FR_SCALE_GROUP:

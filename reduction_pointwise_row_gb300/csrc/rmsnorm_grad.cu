@@ -169,8 +169,8 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
 // may be past fp32, or below its normal values, where the gradients are not.
 //
 // kExact: aligned rows of 32 NU W units.  kWhole: aligned rows of whole units, fewer than
-// that (or short ones), no element of a unit masked: bf16 [4096, 11008] 63.9 us (149 element
-// by element), fp32 [4096, 5000] 54.4 (61.8 as rows with edges).  kEdges: a row may start
+// that (or short ones), no element of a unit masked: bf16 [4096, 11008] 65.7 us (149 element
+// by element), fp32 [4096, 5000] 53.5 (61.8 as rows with edges).  kEdges: a row may start
 // within a unit and end within one: a CTA takes rows that start at one such place (phase),
 // so that its threads' columns stay the same.  The first and last unit of such a row hold
 // elements of its neighbours (or nothing, which the copy leaves out past the matrix's end);
@@ -178,8 +178,8 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
 enum Rows { kExact, kWhole, kEdges };
 
 // Warps of a CTA, at most: 128 registers a thread, or 170 where NU units of rows with edges
-// need them, or 80 where one aligned unit takes no more ([65536, 1024] 79.0 us, 81.3 with 16
-// warps; [32768, 768] 27.9, 29.8).
+// need them, or 80 where one aligned unit takes no more ([65536, 1024] 78.5 us, 81.3 with 16
+// warps; [32768, 768] 27.7, 29.7).
 template <Rows HOW, int NU>
 constexpr int kRingWarps = HOW != kEdges && NU == 1 ? 24 : HOW != kEdges || NU <= 2 ? 16 : 12;
 
@@ -374,7 +374,7 @@ rmsnorm_grad_ring(NormBackward a, int stages, int classes, int lg) {
   }
   if (a.dgamma == nullptr) return;
   // a warp's rows, then the row groups in their order, in the ring's memory (a group's
-  // columns are at most half of its units there).  [262144, 128] 34.7 us, 42.3 with the
+  // columns are at most half of its units there).  [262144, 128] 35.0 us, 42.3 with the
   // groups one after the other.
   float *part = static_cast<float *>(a.workspace) + static_cast<int64_t>(blockIdx.x) * cols;
   float *const sums = reinterpret_cast<float *>(ring), *const mine = sums + threadIdx.y * cols;
@@ -525,10 +525,10 @@ RingShape ring_shape(const NormBackward &a, int sm_count, int smem_max) {
     while (g.lg > 0 && (E << g.lg >> 1) >= a.cols) --g.lg;
   // Two rows at a time, one with dropout (with two its generator's code, twice, costs more
   // than they gain: bf16 [16384, 4096] 121 us against 105) or where two do not fit.  Without:
-  // [8192, 8192] 64.2 us against 73.
+  // [8192, 8192] 64.2 us against 77.7.
   g.rp = a.drop.rng != nullptr || chunks > 32 ? 1 : 2;
   // Aligned rows of 33 to 48 chunks: three units a lane and up to 16 warps, not four and up
-  // to 12 ([4096, 11008] 63.9 us, 72.8 with four).
+  // to 12 ([4096, 11008] 65.7 us, 73.2 with four).
   g.units = chunks <= 4 ? 1 : chunks <= 32 ? 2 : whole && chunks <= 48 ? 3 : 4;
   int warps = 16;
   const auto fit = [&](int units) {
@@ -538,9 +538,9 @@ RingShape ring_shape(const NormBackward &a, int sm_count, int smem_max) {
     warps = whole && units == 1 ? 24 : whole || units <= 2 ? 16 : 12;
     return warps / g.W * g.W;
   };
-  // Rows of 9 to 11 warps leave the others idle: three units a lane instead.  [8192, 4097] 84 us,
-  // 64 so; one aligned row a round (dropout, [8192, 5120]) 77.4, 74.2 so.  Two of them
-  // a round do not gain: [6000, 5120] 42.0, 45.9 so.
+  // Rows of 9 to 11 warps leave the others idle: three units a lane instead.  [8192, 4097] 88 us,
+  // 62 so; one aligned row a round (dropout, [8192, 5120]) 79.4, 77.7 so.  Two of them
+  // a round do not gain: [6000, 5120] 42.2, 47.6 so.
   if (fit(g.units) < 12 && g.units == 2 && (!whole || g.rp == 1)) fit(3);
   if (g.W > warps || (!F32 && g.units == 4 && !whole)) return RingShape{};
   const int64_t rows = (a.rows + g.classes - 1) / g.classes, ctas = std::max(1, sm_count / g.classes);
