@@ -584,6 +584,8 @@ fr_status fr_rmsnorm_quant(const void *x, const void *residual, const float *gam
  *   dx        = dresidual, or with p > 0 dropout's gradient of it (before its rounding)
  *   dgamma    = sum over the rows of dy n
  *
+ * A row whose sum(u n) is past fp32 (u of about 1e35) has a gradient of infinities and NaN.
+ *
  *   h, rstd     of the forward pass (h: x where it had neither residual nor dropout)
  *   dresidual   with p > 0 only; may be NULL
  *   dgamma      fp32 [cols], may be NULL; the sum over the rows in a fixed order

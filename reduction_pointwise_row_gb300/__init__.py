@@ -770,7 +770,8 @@ def fr_dropout(x, p: float, rng, site: int = 0, residual=None, out=None, stream=
     element's row and column, and never stored: the gradient of x is fr_dropout of
     y's gradient with the same rng, site and p.  offset + site is one number: advance the
     offset between steps by at least the number of sites, or one place's mask is
-    another's of the step before.  ``out`` may be x or residual."""
+    another's of the step before.  ``out`` may be x or residual; a new matrix's rows lie as
+    x's do within 8 elements (compact where x is)."""
     if stream is not None:
         return _with_stream(fr_dropout, stream, x, p, rng, site, residual, out)
     _TORCH or _torch()
