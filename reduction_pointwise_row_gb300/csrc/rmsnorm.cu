@@ -47,8 +47,8 @@ __device__ __forceinline__ uint16_t pack_e4m3x2(float lo, float hi) {
 }
 
 // 8 values to e4m3, the first four times inv[0], the others times inv[1]: reciprocals of
-// the scales.  Divided by them, [8192, 8192] took 56.6 us (36.2 so), and as many of its
-// values, those near halfway of two of e4m3, lay on the other side in 64 bits.
+// the scales.  Divided by the scales, [8192, 8192] took 56.6 us (36.2 so), and no fewer values
+// differed from 64 bits' (those near halfway between two of e4m3: some 10 of 21 million).
 __device__ __forceinline__ void e4m3_8(uint32_t (&w)[2], const float (&v)[8], const float (&inv)[2]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
